@@ -338,6 +338,111 @@ mgs_status mgs_delta_scan_fwd(const float *q, const float *k, const float *v, co
                               const float *S0, float *o, float *S_T, int64_t B, int64_t T, int64_t H,
                               int D, void *workspace, size_t workspace_bytes, mgs_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of language models built on these recurrences.  Their tensors are
+ * fp32 or bf16 (the dtype argument); sums, states and statistics are fp32.
+ * ------------------------------------------------------------------------ */
+
+/* Element types. */
+enum { MGS_F32 = 0, MGS_BF16 = 1 };
+
+/* Sizes, types and strides of linear attention.  H value heads, Hk query/key
+ * heads: Hk divides H, value head h reads query/key head h / (H / Hk).  Strides
+ * are in elements, in the order batch, step, head; the D elements of a head are
+ * contiguous.  q, k, v and grad_o start at multiples of 16 bytes and their
+ * strides are multiples of 16 bytes (else MGS_ERR_UNSUPPORTED); a stride may be
+ * 0.  Outputs are dense [B][T][heads][D]. */
+typedef struct mgs_attention_shape {
+    int64_t B, T, H, Hk;
+    int32_t D;            /* 64 or 128, of keys and values alike           */
+    int32_t dtype;        /* of q, k, v, o and their gradients             */
+    int32_t fixed_decay;  /* nonzero: g is [H], one decay a head; dg too   */
+    float scale;          /* factor of o, usually D^-1/2                   */
+    int64_t q_stride[3], k_stride[3], v_stride[3];
+    int64_t g_stride[3];  /* fp32 g, any multiple of 4 bytes; ignored when fixed_decay */
+    int64_t do_stride[3]; /* grad_o's: backward only                       */
+} mgs_attention_shape;
+
+/* Bytes of workspace of the forward (backward = 0) or the backward; 0 also for
+ * invalid shapes. */
+size_t mgs_linear_attention_workspace_size(const mgs_attention_shape *shape, int backward);
+
+/* Linear attention with a decay for each head, forward: per (batch, head), the
+ * state S a D x D matrix with the key index first,
+ *     S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,
+ * S_0 = S0 (zeros when NULL).  g is the logarithm of the decay: g <= 0 in use,
+ * and -infinity starts the state anew at that step.
+ * In: q, k [B][T][Hk][D], v [B][T][H][D], g [B][T][H] or [H] (fp32),
+ *     S0 [B][H][D][D] fp32 (nullable).
+ * Out: o [B][T][H][D]; S_T [B][H][D][D] fp32 (nullable). */
+mgs_status mgs_linear_attention_fwd(const mgs_attention_shape *shape, const void *q, const void *k, const void *v,
+                                    const float *g, const float *S0, void *o, float *S_T, void *workspace,
+                                    size_t workspace_bytes, mgs_stream_t stream);
+
+/* Its backward.  With R_t = dL/dS_t = e^{g_{t+1}} R_{t+1} + scale q_t do_t^T,
+ * R_T = grad_S_T + scale q_T do_T^T:
+ *     dq_t = scale S_t do_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,
+ *     dg_t = <R_t, e^{g_t} S_{t-1}>,  dS0 = e^{g_1} R_1,
+ * dq and dk summed over the value heads that share a query/key head, dg over
+ * batch and steps when the decay is fixed.  The forward's outputs are not
+ * needed.  All of q, k, v, g, S0 as in the forward; grad_S_T nullable.
+ * Out: dq, dk [B][T][Hk][D], dv [B][T][H][D], dg fp32 as g (dense), dS0
+ *     [B][H][D][D] fp32 (nullable). */
+mgs_status mgs_linear_attention_bwd(const mgs_attention_shape *shape, const void *q, const void *k, const void *v,
+                                    const float *g, const float *S0, const void *grad_o, const float *grad_S_T,
+                                    void *dq, void *dk, void *dv, float *dg, float *dS0, void *workspace,
+                                    size_t workspace_bytes, mgs_stream_t stream);
+
+/* One token of each of B sequences (shape->T = 1), their states in a cache
+ * S [n_slots][H][D][D] fp32 that is updated in place: sequence b uses slot
+ * slots[b] (b itself when slots is NULL, which needs n_slots >= B).  A slot
+ * outside 0..n_slots-1 marks an empty row: its output is zero and no state is
+ * touched.  No two sequences of a call may name one slot. */
+mgs_status mgs_linear_attention_step(const mgs_attention_shape *shape, const void *q, const void *k, const void *v,
+                                     const float *g, float *S, const int32_t *slots, int64_t n_slots, void *o,
+                                     mgs_stream_t stream);
+
+/* RMS norm with the residual's addition, per row of N elements:
+ *     r = x + residual (rounded to the type),  rstd = 1 / sqrt(mean(r^2) + eps),
+ *     y = r rstd weight.
+ * residual and r are both given or both NULL (then r is x).  Out: r, y
+ * [rows][N], rstd [rows] fp32 (nullable: only the backward needs it).  Tensors
+ * are dense; 16-byte aligned tensors with N a multiple of 16 bytes run the
+ * vector kernel, others a slower one. */
+mgs_status mgs_rms_norm_fwd(const void *x, const void *residual, const void *weight, float eps, void *r, void *y,
+                            float *rstd, int64_t rows, int64_t N, int dtype, mgs_stream_t stream);
+
+/* The same with y in 8 bits (e4m3): per row (group = 0) or per 128 columns of a
+ * row (group = 128, N a multiple of 128),
+ *     scale = max|y| / 448,  q = y / scale rounded to e4m3,
+ * with q = 0 where scale = 0.  Out: q [rows][N] bytes, scales [rows] or
+ * [rows][N / 128] fp32. */
+mgs_status mgs_rms_norm_fp8_fwd(const void *x, const void *residual, const void *weight, float eps, void *r, void *q,
+                                float *scales, int64_t rows, int64_t N, int group, int dtype, mgs_stream_t stream);
+
+size_t mgs_rms_norm_bwd_workspace_size(int64_t rows, int64_t N);
+
+/* Backward of mgs_rms_norm_fwd, with hat = r rstd:
+ *     dx = rstd (weight dy - hat mean(weight dy hat)) + grad_r,
+ *     dweight = sum over rows of dy hat;
+ * dx is the gradient of x and of residual alike.  grad_r (the gradient that
+ * arrives at r by the residual stream) is nullable. */
+mgs_status mgs_rms_norm_bwd(const void *r, const void *weight, const float *rstd, const void *grad_y,
+                            const void *grad_r, void *dx, void *dweight, int64_t rows, int64_t N, int dtype,
+                            void *workspace, size_t workspace_bytes, mgs_stream_t stream);
+
+size_t mgs_clip_grad_norm_workspace_size(int64_t count);
+
+/* The global norm of `count` tensors, and their scaling by it:
+ *     norm = sqrt(sum of all squares),  out = grad min(1, max_norm / (norm + 1e-6)).
+ * grads, outs, numels and dtypes are HOST arrays; outs[i] == grads[i] clips in
+ * place.  norm is one fp32 on the device; nothing is copied to the host and the
+ * call waits for nothing.  A NaN or infinite element makes the norm so, and
+ * NaN elements of the outputs with it.  Squares are summed in fp32. */
+mgs_status mgs_clip_grad_norm(const void *const *grads, void *const *outs, const int64_t *numels,
+                              const int32_t *dtypes, int64_t count, float max_norm, float *norm, void *workspace,
+                              size_t workspace_bytes, mgs_stream_t stream);
+
 /* Synchronises `stream`, then reads and clears the current device's error
  * word.  Returns MGS_ERR_TIMEOUT if a kernel's bounded wait gave up since the
  * last check, MGS_ERR_CUDA if the synchronisation failed, else MGS_OK. */

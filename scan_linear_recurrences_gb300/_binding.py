@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -39,6 +40,9 @@ MGS_OP_GIVENS_MATRIX_SCAN_BWD = 12
 MGS_OP_DELTA_SCAN_FWD = 13
 MGS_OP_MATRIX_AFFINE_SCAN_BWD_RECOMPUTE = 14
 
+MGS_F32 = 0
+MGS_BF16 = 1
+
 
 class MGSError(RuntimeError):
     """A libmgscan entry point returned a status other than MGS_OK."""
@@ -55,6 +59,7 @@ _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 _sz = ctypes.c_size_t
+_flt = ctypes.c_float
 _SIGNATURES = {
     "mgs_workspace_size": (_sz, [_int, _i64, _i64, _i64, _int]),
     "mgs_matrix_affine_scan_fwd": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp, _sz, _vp]),
@@ -74,6 +79,17 @@ _SIGNATURES = {
     "mgs_givens_matrix_scan_fwd": (_int, [_vp, _vp, _i64, _i64, _i64, _int, _vp, _sz, _vp]),
     "mgs_givens_matrix_scan_bwd": (_int, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp, _sz, _vp]),
     "mgs_delta_scan_fwd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp, _sz, _vp]),
+    "mgs_linear_attention_workspace_size": (_sz, [_vp, _int]),
+    "mgs_linear_attention_fwd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "mgs_linear_attention_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                                        _vp]),
+    "mgs_linear_attention_step": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp]),
+    "mgs_rms_norm_fwd": (_int, [_vp, _vp, _vp, _flt, _vp, _vp, _vp, _i64, _i64, _int, _vp]),
+    "mgs_rms_norm_fp8_fwd": (_int, [_vp, _vp, _vp, _flt, _vp, _vp, _vp, _i64, _i64, _int, _int, _vp]),
+    "mgs_rms_norm_bwd_workspace_size": (_sz, [_i64, _i64]),
+    "mgs_rms_norm_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _vp, _sz, _vp]),
+    "mgs_clip_grad_norm_workspace_size": (_sz, [_i64]),
+    "mgs_clip_grad_norm": (_int, [_vp, _vp, _vp, _vp, _i64, _flt, _vp, _vp, _sz, _vp]),
     "mgs_check": (_int, [_vp]),
     "mgs_set_wait_timeout_ns": (None, [ctypes.c_uint64]),
     "mgs_debug_wait_flag": (_int, [_vp, _vp]),
@@ -219,6 +235,70 @@ def mgs_givens_matrix_scan_bwd(theta, P, grad_P, d_theta, B, T, H, k, workspace=
 def mgs_delta_scan_fwd(q, k, v, beta, S0, o, S_T, B, T, H, D, workspace=None, workspace_bytes=0, stream=None):
     return _call("mgs_delta_scan_fwd", _ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(S0), _ptr(o), _ptr(S_T),
                  B, T, H, D, _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+_ATTENTION_SHAPE = struct.Struct("<4q3if15q")
+_NO_STRIDES = (0, 0, 0)
+
+
+def mgs_attention_shape(B, T, H, Hk, D, dtype, fixed_decay, scale, q_stride, k_stride, v_stride,
+                        g_stride=_NO_STRIDES, do_stride=_NO_STRIDES):
+    """The C struct of that name, as bytes.  Strides: (batch, step, head) in elements."""
+    return _ATTENTION_SHAPE.pack(B, T, H, Hk, D, dtype, fixed_decay, scale, *q_stride, *k_stride, *v_stride,
+                                 *g_stride, *do_stride)
+
+
+def mgs_linear_attention_workspace_size(shape, backward):
+    return int(lib().mgs_linear_attention_workspace_size(shape, int(backward)))
+
+
+def mgs_linear_attention_fwd(shape, q, k, v, g, S0, o, S_T, workspace=None, workspace_bytes=0, stream=None):
+    return _call("mgs_linear_attention_fwd", shape, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(o), _ptr(S_T),
+                 _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def mgs_linear_attention_bwd(shape, q, k, v, g, S0, grad_o, grad_S_T, dq, dk, dv, dg, dS0, workspace=None,
+                             workspace_bytes=0, stream=None):
+    return _call("mgs_linear_attention_bwd", shape, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(grad_o),
+                 _ptr(grad_S_T), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dS0), _ptr(workspace), workspace_bytes,
+                 _stream(stream))
+
+
+def mgs_linear_attention_step(shape, q, k, v, g, S, slots, n_slots, o, stream=None):
+    return _call("mgs_linear_attention_step", shape, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S), _ptr(slots),
+                 n_slots, _ptr(o), _stream(stream))
+
+
+def mgs_rms_norm_fwd(x, residual, weight, eps, r, y, rstd, rows, N, dtype, stream=None):
+    return _call("mgs_rms_norm_fwd", _ptr(x), _ptr(residual), _ptr(weight), eps, _ptr(r), _ptr(y), _ptr(rstd), rows,
+                 N, dtype, _stream(stream))
+
+
+def mgs_rms_norm_fp8_fwd(x, residual, weight, eps, r, q, scales, rows, N, group, dtype, stream=None):
+    return _call("mgs_rms_norm_fp8_fwd", _ptr(x), _ptr(residual), _ptr(weight), eps, _ptr(r), _ptr(q), _ptr(scales),
+                 rows, N, group, dtype, _stream(stream))
+
+
+def mgs_rms_norm_bwd_workspace_size(rows, N):
+    return int(lib().mgs_rms_norm_bwd_workspace_size(rows, N))
+
+
+def mgs_rms_norm_bwd(r, weight, rstd, grad_y, grad_r, dx, dweight, rows, N, dtype, workspace=None, workspace_bytes=0,
+                     stream=None):
+    return _call("mgs_rms_norm_bwd", _ptr(r), _ptr(weight), _ptr(rstd), _ptr(grad_y), _ptr(grad_r), _ptr(dx),
+                 _ptr(dweight), rows, N, dtype, _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def mgs_clip_grad_norm_workspace_size(count):
+    return int(lib().mgs_clip_grad_norm_workspace_size(count))
+
+
+def mgs_clip_grad_norm(grads, outs, numels, dtypes, max_norm, norm, workspace=None, workspace_bytes=0, stream=None):
+    """grads, outs: lists of device addresses; numels, dtypes: lists of ints."""
+    n = len(grads)
+    return _call("mgs_clip_grad_norm", struct.pack(f"{n}Q", *grads), struct.pack(f"{n}Q", *outs),
+                 struct.pack(f"{n}q", *numels), struct.pack(f"{n}i", *dtypes), n, max_norm, _ptr(norm),
+                 _ptr(workspace), workspace_bytes, _stream(stream))
 
 
 def mgs_check(stream=None):

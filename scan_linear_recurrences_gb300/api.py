@@ -228,6 +228,215 @@ def linear_scan_bwd(a, h0, h, grad_h, need_dh0=True, stream=None):
     return da, db, dh0
 
 
+# ---------------------------------------------------------------- linear attention with a decay
+_DTYPES = {torch.float32: _b.MGS_F32, torch.bfloat16: _b.MGS_BF16}
+
+
+def _check_typed(t, name, shape, dtype, dense=True, device=None):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor (the library runs only on the GPU)")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if dtype is None:
+        if t.dtype not in _DTYPES:
+            raise ValueError(f"{name} must be float32 or bfloat16")
+    elif t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}".replace("torch.", ""))
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _head_strides(t, name):
+    """(batch, step, head) strides of [B,T,h,D] whose heads are contiguous."""
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return st[:-1]
+
+
+def _attention_shape(q, k, v, g, scale, grad_o=None):
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a [B,T,Hk,D] tensor")
+    if not isinstance(v, torch.Tensor) or v.dim() != 4:
+        raise ValueError("v must be a [B,T,H,D] tensor")
+    (B, T, Hk, D), H, dev = q.shape, v.shape[2], q.device
+    _check_typed(q, "q", None, None, dense=False)
+    _check_typed(k, "k", q.shape, q.dtype, dense=False, device=dev)
+    _check_typed(v, "v", (B, T, H, D), q.dtype, dense=False, device=dev)
+    if Hk == 0 or H % Hk:
+        raise ValueError(f"{Hk} query/key heads do not divide {H} value heads")
+    if D not in (64, 128):
+        raise ValueError(f"heads of {D}: 64 and 128 are supported")
+    fixed = isinstance(g, torch.Tensor) and g.dim() == 1
+    _check_typed(g, "g", (H,) if fixed else (B, T, H), torch.float32, dense=fixed, device=dev)
+    if grad_o is not None:
+        _check_typed(grad_o, "grad_o", v.shape, q.dtype, dense=False, device=dev)
+    return _b.mgs_attention_shape(
+        B, T, H, Hk, D, _DTYPES[q.dtype], fixed, D ** -0.5 if scale is None else scale, _head_strides(q, "q"),
+        _head_strides(k, "k"), _head_strides(v, "v"), (0, 0, 1) if fixed else g.stride(),
+        _head_strides(grad_o, "grad_o") if grad_o is not None else (0, 0, 0)), (B, T, H, Hk, D)
+
+
+def _scratch(n, device, stream):
+    """n bytes of workspace that stay reserved until `stream` is done with them."""
+    if not n:
+        return None
+    t = torch.empty(n, dtype=torch.uint8, device=device)
+    if stream is not None:
+        t.record_stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
+    return t
+
+
+def linear_attention_fwd(q, k, v, g, S0=None, scale=None, want_state=False, stream=None):
+    """Linear attention with a decay for each head:
+    S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t (scale: D^-1/2 unless given).
+
+    q, k [B,T,Hk,D], v [B,T,H,D] (fp32 or bf16, D 64 or 128, Hk dividing H: value head h reads query/key
+    head h // (H // Hk); any strides of 16 bytes whose heads are contiguous), g [B,T,H] or [H] fp32 (the
+    decay's logarithm; -inf starts the state anew), S0 [B,H,D,D] fp32 or None.
+    Returns o [B,T,H,D] (and the final state when want_state)."""
+    shape, (B, T, H, Hk, D) = _attention_shape(q, k, v, g, scale)
+    if S0 is not None:
+        _check_typed(S0, "S0", (B, H, D, D), torch.float32, device=q.device)
+    o = torch.empty((B, T, H, D), dtype=q.dtype, device=q.device)
+    ST = torch.empty((B, H, D, D), dtype=torch.float32, device=q.device) if want_state else None
+    n = _b.mgs_linear_attention_workspace_size(shape, 0)
+    _b.mgs_linear_attention_fwd(shape, q, k, v, g, S0, o, ST, _scratch(n, q.device, stream), n, stream)
+    return (o, ST) if want_state else o
+
+
+def linear_attention_bwd(q, k, v, g, grad_o, S0=None, grad_ST=None, scale=None, stream=None):
+    """Gradients of linear_attention_fwd for L = <grad_o, o> + <grad_ST, S_T>: returns (dq, dk, dv, dg, dS0),
+    dS0 None without S0.  dg is [B,T,H], or [H] for a g of one decay a head."""
+    shape, (B, T, H, Hk, D) = _attention_shape(q, k, v, g, scale, grad_o)
+    for t, name in ((S0, "S0"), (grad_ST, "grad_ST")):
+        if t is not None:
+            _check_typed(t, name, (B, H, D, D), torch.float32, device=q.device)
+    dq = torch.empty((B, T, Hk, D), dtype=q.dtype, device=q.device)
+    dk = torch.empty_like(dq)
+    dv = torch.empty((B, T, H, D), dtype=q.dtype, device=q.device)
+    dg = torch.empty(g.shape, dtype=torch.float32, device=q.device)
+    dS0 = torch.empty_like(S0) if S0 is not None else None
+    n = _b.mgs_linear_attention_workspace_size(shape, 1)
+    _b.mgs_linear_attention_bwd(shape, q, k, v, g, S0, grad_o, grad_ST, dq, dk, dv, dg, dS0, _scratch(n, q.device, stream), n,
+                                stream)
+    return dq, dk, dv, dg, dS0
+
+
+def linear_attention_step(q, k, v, g, S, slots=None, scale=None, out=None, stream=None):
+    """One token of each of B sequences: q, k [B,Hk,D], v [B,H,D], g [B,H] or [H] fp32, the cache of states
+    S [N,H,D,D] fp32, updated in place.  slots [B] int32: each sequence's place in the cache (None: b itself);
+    a place outside 0..N-1 marks an empty row, whose output is 0.  Returns o [B,H,D]."""
+    (B, Hk, D), H, dev = q.shape, v.shape[1], q.device
+    dt = q.dtype
+    _check_typed(q, "q", None, None, dense=False)
+    _check_typed(k, "k", q.shape, dt, dense=False, device=dev)
+    _check_typed(v, "v", (B, H, D), dt, dense=False, device=dev)
+    if Hk == 0 or H % Hk:
+        raise ValueError(f"{Hk} query/key heads do not divide {H} value heads")
+    if D not in (64, 128):
+        raise ValueError(f"heads of {D}: 64 and 128 are supported")
+    fixed = g.dim() == 1
+    _check_typed(g, "g", (H,) if fixed else (B, H), torch.float32, dense=fixed, device=dev)
+    _check_typed(S, "S", (S.shape[0], H, D, D), torch.float32, device=dev)
+    if slots is not None:
+        _check_typed(slots, "slots", (B,), torch.int32, device=dev)
+    elif S.shape[0] < B:
+        raise ValueError(f"{B} sequences without slots need a cache of as many states, not {S.shape[0]}")
+    if out is None:
+        out = torch.empty((B, H, D), dtype=dt, device=dev)
+    else:
+        _check_typed(out, "out", (B, H, D), dt, device=dev)
+    (qb, qh), (kb, kh), (vb, vh) = _head_strides(q, "q"), _head_strides(k, "k"), _head_strides(v, "v")
+    gs = g.stride()
+    shape = _b.mgs_attention_shape(B, 1, H, Hk, D, _DTYPES[dt], fixed, D ** -0.5 if scale is None else scale,
+                                   (qb, 0, qh), (kb, 0, kh), (vb, 0, vh), (0, 0, 1) if fixed else (gs[0], 0, gs[1]))
+    _b.mgs_linear_attention_step(shape, q, k, v, g, S, slots, S.shape[0], out, stream)
+    return out
+
+
+# ---------------------------------------------------------------- RMS norm with the residual's addition
+def _norm_args(x, weight, residual):
+    _check_typed(x, "x", None, None)
+    if x.dim() == 0:
+        raise ValueError("x must have a last dimension")
+    N = x.shape[-1]
+    _check_typed(weight, "weight", (N,), x.dtype, device=x.device)
+    if residual is not None:
+        _check_typed(residual, "residual", x.shape, x.dtype, device=x.device)
+    return x.numel() // N if N else 0, N, _DTYPES[x.dtype]
+
+
+def rms_norm_fwd(x, weight, residual=None, eps=1e-6, stream=None):
+    """r = x + residual (x itself without one), y = r weight / sqrt(mean(r^2) + eps) over the last dimension.
+    x, residual [..., N], weight [N], all fp32 or all bf16.  Returns (y, r, rstd), rstd fp32 for the backward."""
+    rows, N, dt = _norm_args(x, weight, residual)
+    y = torch.empty_like(x)
+    r = torch.empty_like(x) if residual is not None else None
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    _b.mgs_rms_norm_fwd(x, residual, weight, eps, r, y, rstd, rows, N, dt, stream)
+    return y, (r if r is not None else x), rstd
+
+
+def rms_norm_fp8_fwd(x, weight, residual=None, eps=1e-6, group=0, stream=None):
+    """The same with y in 8 bits (float8_e4m3fn) and fp32 scales: y = q * scale, a scale for each row (group 0) or
+    each 128 columns of a row (group 128).  Returns (q, scales, r)."""
+    rows, N, dt = _norm_args(x, weight, residual)
+    if group not in (0, 128) or (group and N % group):
+        raise ValueError("group must be 0, or 128 with a last dimension that it divides")
+    q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    r = torch.empty_like(x) if residual is not None else None
+    scales = torch.empty((*x.shape[:-1], N // group if group else 1), dtype=torch.float32, device=x.device)
+    _b.mgs_rms_norm_fp8_fwd(x, residual, weight, eps, r, q, scales, rows, N, group, dt, stream)
+    return q, scales, (r if r is not None else x)
+
+
+def rms_norm_bwd(r, weight, rstd, grad_y, grad_r=None, stream=None):
+    """Gradients of rms_norm_fwd: (dx, dweight); dx is that of x and of residual alike, grad_r (or None) what
+    arrives at r itself."""
+    rows, N, dt = _norm_args(r, weight, None)
+    _check_typed(rstd, "rstd", r.shape[:-1], torch.float32, device=r.device)
+    _check_typed(grad_y, "grad_y", r.shape, r.dtype, device=r.device)
+    if grad_r is not None:
+        _check_typed(grad_r, "grad_r", r.shape, r.dtype, device=r.device)
+    dx, dw = torch.empty_like(r), torch.empty_like(weight)
+    n = _b.mgs_rms_norm_bwd_workspace_size(rows, N)
+    _b.mgs_rms_norm_bwd(r, weight, rstd, grad_y, grad_r, dx, dw, rows, N, dt, _scratch(n, r.device, stream), n, stream)
+    return dx, dw
+
+
+# ---------------------------------------------------------------- clipping by the global norm
+def clip_grad_norm(grads, max_norm, out=None, stream=None):
+    """The norm over all of grads (fp32 and bf16 tensors, contiguous) as one fp32 on the device, and the tensors
+    scaled by min(1, max_norm / (norm + 1e-6)): in place, or into `out` (tensors of the same shapes and types)."""
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError(f"{len(outs)} outputs for {len(grads)} tensors")
+    if not grads:
+        raise ValueError("no tensors")
+    dev = grads[0].device
+    for t in grads:
+        if t.device != dev or t.dtype not in _DTYPES or not t.is_contiguous():
+            _check_typed(t, "each of grads", None, None, device=dev)
+    if dev.type != "cuda":
+        raise ValueError("each of grads must be a CUDA tensor (the library runs only on the GPU)")
+    if out is not None:
+        for t, u in zip(grads, outs):
+            if u.device != dev or u.dtype != t.dtype or u.shape != t.shape or not u.is_contiguous():
+                _check_typed(u, "each of out", t.shape, t.dtype, device=dev)
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    n = _b.mgs_clip_grad_norm_workspace_size(len(grads))
+    at = [t.data_ptr() for t in grads]
+    _b.mgs_clip_grad_norm(at, at if out is None else [u.data_ptr() for u in outs], [t.numel() for t in grads],
+                          [_DTYPES[t.dtype] for t in grads], max_norm, norm, _scratch(n, dev, stream), n, stream)
+    return norm
+
+
 # ---------------------------------------------------------------- autograd wrappers
 class MatrixAffineScan(torch.autograd.Function):
     """h = matrix_affine_scan(A, b, h0) with the library's fused backward;
@@ -342,6 +551,44 @@ class GivensMatrixScan(torch.autograd.Function):
         return givens_matrix_scan_bwd(theta, P, grad_P.contiguous())
 
 
+class LinearAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, g, S0=None, scale=None):
+        S0 = S0.contiguous() if S0 is not None else None
+        o, ST = linear_attention_fwd(q, k, v, g, S0, scale, want_state=True)
+        ctx.save_for_backward(q, k, v, g, S0)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        return o, ST
+
+    @staticmethod
+    def backward(ctx, grad_o, grad_ST):
+        q, k, v, g, S0 = ctx.saved_tensors
+        if grad_o is None:
+            grad_o = torch.zeros(v.shape, dtype=v.dtype, device=v.device)
+        if grad_ST is not None:
+            grad_ST = grad_ST.contiguous()
+        dq, dk, dv, dg, dS0 = linear_attention_bwd(q, k, v, g, _aligned(grad_o), S0, grad_ST, ctx.scale)
+        return dq, dk, dv, dg, dS0, None
+
+
+class RMSNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, residual=None, eps=1e-6):
+        y, r, rstd = rms_norm_fwd(x.contiguous(), weight, residual.contiguous() if residual is not None else None, eps)
+        ctx.save_for_backward(r, weight, rstd)
+        ctx.has_residual = residual is not None
+        ctx.set_materialize_grads(False)
+        return (y, r) if ctx.has_residual else y
+
+    @staticmethod
+    def backward(ctx, grad_y, grad_r=None):
+        r, weight, rstd = ctx.saved_tensors
+        grad_y = torch.zeros_like(r) if grad_y is None else grad_y.contiguous()
+        dx, dw = rms_norm_bwd(r, weight, rstd, grad_y, grad_r.contiguous() if grad_r is not None else None)
+        return dx, dw, dx if ctx.has_residual else None, None
+
+
 def givens_affine_scan(theta, a, b, h0=None):
     """GivensMinGRU's angle-fused recurrence h_t = G(theta_t) diag(a_t) h_{t-1} + b_t (a may be None)."""
     return GivensAffineScan.apply(theta, a, b, h0)
@@ -367,3 +614,20 @@ def matrix_scan(A):
 def parallel_scan_log(log_coeffs, log_values, log_h0=None, recompute=False):
     """recompute=True keeps no copy of h for backward; backward rebuilds it."""
     return ParallelScanLog.apply(log_coeffs, log_values, log_h0, recompute)
+
+
+def _aligned(t):
+    """t itself where its strides are ones the attention kernels take, else a dense copy."""
+    es = t.element_size()
+    ok = t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and all(s * es % 16 == 0 for s in t.stride()[:-1])
+    return t if ok else t.contiguous()
+
+
+def linear_attention(q, k, v, g, S0=None, scale=None):
+    """Linear attention with a decay for each head, with gradients: (o, S_T); see linear_attention_fwd."""
+    return LinearAttention.apply(_aligned(q), _aligned(k), _aligned(v), g, S0, scale)
+
+
+def rms_norm(x, weight, residual=None, eps=1e-6):
+    """RMS norm over the last dimension, with gradients: y, or (y, r) with r = x + residual."""
+    return RMSNorm.apply(x, weight, residual, eps)

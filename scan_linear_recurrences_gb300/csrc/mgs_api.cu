@@ -12,6 +12,7 @@
 
 #include "../../include/mgscan.h"
 #include "mgs_launch.h"
+#include "mgs_lm.h"
 
 #define MGS_VERSION_INT 100  // 0.1.0
 
@@ -663,3 +664,289 @@ extern "C" mgs_status mgs_debug_wait_flag(const int *flag, mgs_stream_t stream) 
     debug_wait_flag_kernel<<<1, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(flag, ctl);
     return from_cuda(cudaGetLastError());
 }
+
+// ---------------------------------------------------------------- language-model operators
+namespace {
+
+// Byte ranges of arguments, for the overlap checks of operators whose
+// arguments differ in type.
+struct Bytes {
+    const void *p;
+    int64_t n;
+};
+bool apart(std::initializer_list<Bytes> outs, std::initializer_list<Bytes> ins) {
+    auto hit = [](const Bytes &a, const Bytes &b) {
+        if (a.p == nullptr || b.p == nullptr || a.n == 0 || b.n == 0) return false;
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+        return x < y + uintptr_t(b.n) && y < x + uintptr_t(a.n);
+    };
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        for (auto &i : ins)
+            if (hit(*o, i)) return false;
+        for (auto o2 = o + 1; o2 != outs.end(); ++o2)
+            if (hit(*o, *o2)) return false;
+    }
+    return true;
+}
+
+int esize(int dtype) { return dtype == MGS_F32 ? 4 : dtype == MGS_BF16 ? 2 : 0; }
+
+struct AttnSizes {
+    int64_t qk, v, q_span, k_span, v_span, do_span;  // bytes: dense [B,T,Hk,D], [B,T,H,D]; spans of the strided inputs
+    int64_t g, state;                                // bytes
+};
+
+// Bytes from the first to the last element of [B][T][h][D] with these
+// strides; false when a stride is negative, no multiple of 16 bytes, or too large.
+bool span_of(const int64_t (&st)[3], int64_t B, int64_t T, int64_t h, int64_t inner, int es, int mult, int64_t *out) {
+    int64_t n = inner - 1, x;
+    const int64_t dims[3] = {B, T, h};
+    for (int i = 0; i < 3; ++i) {
+        if (st[i] < 0 || (dims[i] > 1 && (st[i] * es) % mult != 0)) return false;
+        if (!mul_ok(dims[i] - 1, st[i], &x) || x > INT64_MAX / 64 - n) return false;
+        n += x;
+    }
+    *out = (n + 1) * es;
+    return true;
+}
+
+mgs_status attn_sizes(const mgs_attention_shape *sh, bool with_do, AttnSizes *z) {
+    if (sh == nullptr || sh->B < 0 || sh->T < 0 || sh->H < 0 || sh->Hk < 0) return MGS_ERR_INVALID_ARG;
+    const int es = esize(sh->dtype);
+    if (es == 0 || (sh->D != 64 && sh->D != 128)) return MGS_ERR_UNSUPPORTED;
+    if (sh->H > 0 && (sh->Hk == 0 || sh->H % sh->Hk != 0)) return MGS_ERR_INVALID_ARG;
+    int64_t bt, n, ns;
+    if (!mul_ok(sh->B, sh->T, &bt) || !mul_ok(bt, sh->H, &n) || !mul_ok(n, int64_t(sh->D) * 8, &n) ||
+        !mul_ok(sh->B, sh->H, &ns) || !mul_ok(ns, int64_t(sh->D) * sh->D * 4, &ns))
+        return MGS_ERR_INVALID_ARG;
+    if (n > INT64_MAX / 64 || ns > INT64_MAX / 64) return MGS_ERR_INVALID_ARG;
+    // 32-bit grid and tensor-map coordinates
+    if (sh->T > INT32_MAX / 2 || sh->B * sh->H > 65535 * 16 || (sh->T / 128 + 1) * sh->B * sh->H > INT32_MAX / 4)
+        return MGS_ERR_UNSUPPORTED;
+    z->qk = bt * sh->Hk * sh->D * es;
+    z->v = bt * sh->H * sh->D * es;
+    z->state = ns;
+    z->q_span = z->k_span = z->v_span = z->do_span = z->g = 0;
+    if (bt == 0 || sh->H == 0) return MGS_OK;
+    if (!span_of(sh->q_stride, sh->B, sh->T, sh->Hk, sh->D, es, 16, &z->q_span) ||
+        !span_of(sh->k_stride, sh->B, sh->T, sh->Hk, sh->D, es, 16, &z->k_span) ||
+        !span_of(sh->v_stride, sh->B, sh->T, sh->H, sh->D, es, 16, &z->v_span) ||
+        (with_do && !span_of(sh->do_stride, sh->B, sh->T, sh->H, sh->D, es, 16, &z->do_span)))
+        return MGS_ERR_UNSUPPORTED;
+    if (sh->fixed_decay)
+        z->g = sh->H * 4;
+    else if (!span_of(sh->g_stride, sh->B, sh->T, sh->H, 1, 4, 4, &z->g))
+        return MGS_ERR_UNSUPPORTED;
+    return MGS_OK;
+}
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+extern "C" {
+
+size_t mgs_linear_attention_workspace_size(const mgs_attention_shape *shape, int backward) {
+    AttnSizes z;
+    if (attn_sizes(shape, false, &z) != MGS_OK || z.v == 0) return 0;
+    return mgs::attn_workspace_bytes(*shape, backward != 0);
+}
+
+mgs_status mgs_linear_attention_fwd(const mgs_attention_shape *shape, const void *q, const void *k, const void *v,
+                                    const float *g, const float *S0, void *o, float *S_T, void *workspace,
+                                    size_t workspace_bytes, mgs_stream_t stream) {
+    AttnSizes z;
+    mgs_status st = attn_sizes(shape, false, &z);
+    if (st != MGS_OK) return st;
+    if (z.state == 0) return MGS_OK;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (z.v == 0) {  // T = 0: the final state is the initial one
+        if (S_T == nullptr) return MGS_OK;
+        if ((st = check_ptrs({S_T}, {S0})) != MGS_OK) return st;
+        if (!apart({{S_T, z.state}}, {{S0, z.state}})) return MGS_ERR_INVALID_ARG;
+        return from_cuda(S0 ? cudaMemcpyAsync(S_T, S0, size_t(z.state), cudaMemcpyDeviceToDevice, cs)
+                            : cudaMemsetAsync(S_T, 0, size_t(z.state), cs));
+    }
+    if ((st = check_ptrs({q, k, v, o}, {S0, S_T})) != MGS_OK) return st;
+    if (g == nullptr) return MGS_ERR_INVALID_ARG;
+    if (!aligned4(g)) return MGS_ERR_UNSUPPORTED;
+    const size_t need = mgs::attn_workspace_bytes(*shape, false);
+    if ((st = check_ws(need, workspace, workspace_bytes)) != MGS_OK) return st;
+    if (!apart({{o, z.v}, {S_T, z.state}, {workspace, int64_t(need)}},
+               {{q, z.q_span}, {k, z.k_span}, {v, z.v_span}, {g, z.g}, {S0, z.state}}))
+        return MGS_ERR_INVALID_ARG;
+    mgs::DevCtl ctl;
+    if ((st = current_ctl(&ctl)) != MGS_OK) return st;
+    return from_cuda(mgs::launch_attn_fwd(*shape, q, k, v, g, S0, o, S_T, workspace, ctl, cs));
+}
+
+mgs_status mgs_linear_attention_bwd(const mgs_attention_shape *shape, const void *q, const void *k, const void *v,
+                                    const float *g, const float *S0, const void *grad_o, const float *grad_S_T,
+                                    void *dq, void *dk, void *dv, float *dg, float *dS0, void *workspace,
+                                    size_t workspace_bytes, mgs_stream_t stream) {
+    AttnSizes z;
+    mgs_status st = attn_sizes(shape, true, &z);
+    if (st != MGS_OK) return st;
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (z.v == 0) {  // T = 0: dS0 is the final state's gradient; a fixed decay has none
+        if (shape->fixed_decay && dg != nullptr && shape->H > 0) {
+            if (!aligned4(dg)) return MGS_ERR_UNSUPPORTED;
+            if (cudaMemsetAsync(dg, 0, size_t(shape->H) * 4, cs) != cudaSuccess) return MGS_ERR_CUDA;
+        }
+        if (z.state == 0 || dS0 == nullptr) return MGS_OK;
+        if ((st = check_ptrs({dS0}, {grad_S_T})) != MGS_OK) return st;
+        if (!apart({{dS0, z.state}}, {{grad_S_T, z.state}})) return MGS_ERR_INVALID_ARG;
+        return from_cuda(grad_S_T
+                             ? cudaMemcpyAsync(dS0, grad_S_T, size_t(z.state), cudaMemcpyDeviceToDevice, cs)
+                             : cudaMemsetAsync(dS0, 0, size_t(z.state), cs));
+    }
+    if ((st = check_ptrs({q, k, v, grad_o, dq, dk, dv}, {S0, grad_S_T, dS0})) != MGS_OK) return st;
+    if (g == nullptr || dg == nullptr) return MGS_ERR_INVALID_ARG;
+    if (!aligned4(g) || !aligned4(dg)) return MGS_ERR_UNSUPPORTED;
+    const size_t need = mgs::attn_workspace_bytes(*shape, true);
+    if ((st = check_ws(need, workspace, workspace_bytes)) != MGS_OK) return st;
+    const int64_t ndg = (shape->fixed_decay ? shape->H : shape->B * shape->T * shape->H) * 4;
+    if (!apart({{dq, z.qk}, {dk, z.qk}, {dv, z.v}, {dg, ndg}, {dS0, z.state}, {workspace, int64_t(need)}},
+               {{q, z.q_span}, {k, z.k_span}, {v, z.v_span}, {g, z.g}, {S0, z.state}, {grad_o, z.do_span},
+                {grad_S_T, z.state}}))
+        return MGS_ERR_INVALID_ARG;
+    mgs::DevCtl ctl;
+    if ((st = current_ctl(&ctl)) != MGS_OK) return st;
+    return from_cuda(mgs::launch_attn_bwd(*shape, q, k, v, g, S0, grad_o, grad_S_T, dq, dk, dv, dg, dS0, workspace,
+                                          ctl, cs));
+}
+
+mgs_status mgs_linear_attention_step(const mgs_attention_shape *shape, const void *q, const void *k, const void *v,
+                                     const float *g, float *S, const int32_t *slots, int64_t n_slots, void *o,
+                                     mgs_stream_t stream) {
+    AttnSizes z;
+    if (shape == nullptr || shape->T != 1 || n_slots < 0) return MGS_ERR_INVALID_ARG;
+    mgs_status st = attn_sizes(shape, false, &z);
+    if (st != MGS_OK) return st;
+    if (z.state == 0) return MGS_OK;
+    if ((st = check_ptrs({q, k, v, o, S}, {})) != MGS_OK) return st;
+    if (g == nullptr || (slots == nullptr && n_slots < shape->B)) return MGS_ERR_INVALID_ARG;
+    if (!aligned4(g) || !aligned4(slots)) return MGS_ERR_UNSUPPORTED;
+    int64_t ns;
+    if (!mul_ok(n_slots, shape->H * shape->D * int64_t(shape->D) * 4, &ns)) return MGS_ERR_INVALID_ARG;
+    if (!apart({{o, z.v}, {S, ns}},
+               {{q, z.q_span}, {k, z.k_span}, {v, z.v_span}, {g, z.g}, {slots, slots ? shape->B * 4 : 0}}))
+        return MGS_ERR_INVALID_ARG;
+    return from_cuda(mgs::launch_attn_step(*shape, q, k, v, g, S, slots, n_slots, o,
+                                           reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// rows x N elements of the type, as bytes
+static mgs_status norm_sizes(int dtype, int64_t rows, int64_t N, int64_t *bytes) {
+    if (rows < 0 || N < 0) return MGS_ERR_INVALID_ARG;
+    if (esize(dtype) == 0 || N > INT32_MAX / 2) return MGS_ERR_UNSUPPORTED;
+    if (!mul_ok(rows, N, bytes) || *bytes > INT64_MAX / 64) return MGS_ERR_INVALID_ARG;
+    if (rows > INT32_MAX) return MGS_ERR_UNSUPPORTED;
+    *bytes *= esize(dtype);
+    return MGS_OK;
+}
+static mgs_status typed_ptrs(int es, std::initializer_list<const void *> required,
+                             std::initializer_list<const void *> optional) {
+    for (const void *p : required) {
+        if (p == nullptr) return MGS_ERR_INVALID_ARG;
+        if (reinterpret_cast<uintptr_t>(p) % unsigned(es)) return MGS_ERR_UNSUPPORTED;
+    }
+    for (const void *p : optional)
+        if (reinterpret_cast<uintptr_t>(p) % unsigned(es)) return MGS_ERR_UNSUPPORTED;
+    return MGS_OK;
+}
+
+mgs_status mgs_rms_norm_fwd(const void *x, const void *residual, const void *weight, float eps, void *r, void *y,
+                            float *rstd, int64_t rows, int64_t N, int dtype, mgs_stream_t stream) {
+    int64_t n;
+    mgs_status st = norm_sizes(dtype, rows, N, &n);
+    if (st != MGS_OK) return st;
+    if (n == 0) return MGS_OK;
+    const int es = esize(dtype);
+    if ((st = typed_ptrs(es, {x, weight, y}, {residual, r})) != MGS_OK) return st;
+    if ((residual == nullptr) != (r == nullptr)) return MGS_ERR_INVALID_ARG;
+    if (!aligned4(rstd)) return MGS_ERR_UNSUPPORTED;
+    if (!apart({{r, n}, {y, n}, {rstd, rows * 4}}, {{x, n}, {residual, n}, {weight, N * es}}))
+        return MGS_ERR_INVALID_ARG;
+    return from_cuda(mgs::launch_rms_norm_fwd(dtype, x, residual, weight, eps, r, y, rstd, rows, N,
+                                              reinterpret_cast<cudaStream_t>(stream)));
+}
+
+mgs_status mgs_rms_norm_fp8_fwd(const void *x, const void *residual, const void *weight, float eps, void *r, void *q,
+                                float *scales, int64_t rows, int64_t N, int group, int dtype, mgs_stream_t stream) {
+    int64_t n;
+    mgs_status st = norm_sizes(dtype, rows, N, &n);
+    if (st != MGS_OK) return st;
+    if (group != 0 && (group != 128 || N % 128 != 0)) return MGS_ERR_UNSUPPORTED;
+    if (n == 0) return MGS_OK;
+    const int es = esize(dtype);
+    if ((st = typed_ptrs(es, {x, weight, q}, {residual, r})) != MGS_OK) return st;
+    if (scales == nullptr || (residual == nullptr) != (r == nullptr)) return MGS_ERR_INVALID_ARG;
+    if (!aligned4(scales)) return MGS_ERR_UNSUPPORTED;
+    const int64_t nsc = rows * (group ? N / group : 1) * 4;
+    if (!apart({{r, n}, {q, n / es}, {scales, nsc}}, {{x, n}, {residual, n}, {weight, N * es}}))
+        return MGS_ERR_INVALID_ARG;
+    return from_cuda(mgs::launch_rms_norm_fp8(dtype, x, residual, weight, eps, r, q, scales, rows, N, group,
+                                              reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t mgs_rms_norm_bwd_workspace_size(int64_t rows, int64_t N) {
+    int64_t n;
+    if (norm_sizes(MGS_F32, rows, N, &n) != MGS_OK || n == 0) return 0;
+    return mgs::rms_norm_bwd_workspace_bytes(rows, N);
+}
+
+mgs_status mgs_rms_norm_bwd(const void *r, const void *weight, const float *rstd, const void *grad_y,
+                            const void *grad_r, void *dx, void *dweight, int64_t rows, int64_t N, int dtype,
+                            void *workspace, size_t workspace_bytes, mgs_stream_t stream) {
+    int64_t n;
+    mgs_status st = norm_sizes(dtype, rows, N, &n);
+    if (st != MGS_OK) return st;
+    const int es = esize(dtype);
+    cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    if (n == 0) {  // no rows: the weight's gradient is zero
+        if (N == 0) return MGS_OK;
+        if ((st = typed_ptrs(es, {dweight}, {})) != MGS_OK) return st;
+        return from_cuda(cudaMemsetAsync(dweight, 0, size_t(N) * es, cs));
+    }
+    if ((st = typed_ptrs(es, {r, weight, grad_y, dx, dweight}, {grad_r})) != MGS_OK) return st;
+    if (rstd == nullptr) return MGS_ERR_INVALID_ARG;
+    if (!aligned4(rstd)) return MGS_ERR_UNSUPPORTED;
+    const size_t need = mgs::rms_norm_bwd_workspace_bytes(rows, N);
+    if ((st = check_ws(need, workspace, workspace_bytes)) != MGS_OK) return st;
+    if (!apart({{dx, n}, {dweight, N * es}, {workspace, int64_t(need)}},
+               {{r, n}, {weight, N * es}, {rstd, rows * 4}, {grad_y, n}, {grad_r, n}}))
+        return MGS_ERR_INVALID_ARG;
+    return from_cuda(mgs::launch_rms_norm_bwd(dtype, r, weight, rstd, grad_y, grad_r, dx, dweight, rows, N, workspace,
+                                              cs));
+}
+
+size_t mgs_clip_grad_norm_workspace_size(int64_t count) { return count < 0 ? 0 : mgs::clip_workspace_bytes(count); }
+
+mgs_status mgs_clip_grad_norm(const void *const *grads, void *const *outs, const int64_t *numels,
+                              const int32_t *dtypes, int64_t count, float max_norm, float *norm, void *workspace,
+                              size_t workspace_bytes, mgs_stream_t stream) {
+    if (count < 0 || norm == nullptr || !(max_norm >= 0.f)) return MGS_ERR_INVALID_ARG;
+    if (!aligned4(norm)) return MGS_ERR_UNSUPPORTED;
+    if (count > 0 && (grads == nullptr || outs == nullptr || numels == nullptr || dtypes == nullptr))
+        return MGS_ERR_INVALID_ARG;
+    const size_t need = mgs::clip_workspace_bytes(count);
+    for (int64_t i = 0; i < count; ++i) {
+        const int es = esize(dtypes[i]);
+        if (es == 0) return MGS_ERR_UNSUPPORTED;
+        if (numels[i] < 0 || numels[i] > INT64_MAX / 64) return MGS_ERR_INVALID_ARG;
+        if (numels[i] == 0) continue;
+        mgs_status st = typed_ptrs(es, {grads[i], outs[i]}, {});
+        if (st != MGS_OK) return st;
+        const Bytes in{grads[i], numels[i] * es}, out{outs[i], numels[i] * es};
+        // in place, or wholly apart; nothing of it in the norm or the workspace
+        if (grads[i] != outs[i] && !apart({out}, {in})) return MGS_ERR_INVALID_ARG;
+        if (!apart({{norm, 4}, {workspace, int64_t(need)}}, {in, out})) return MGS_ERR_INVALID_ARG;
+    }
+    const mgs_status st = check_ws(need, workspace, workspace_bytes);
+    if (st != MGS_OK) return st;
+    return from_cuda(mgs::launch_clip(grads, outs, numels, dtypes, count, max_norm, norm, workspace,
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,589 @@
+// Linear attention with a decay for each head.  Per (batch, head), state S
+// (D x D, key index first):
+//   S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t.
+// With R_t = dL/dS_t = e^{g_{t+1}} R_{t+1} + scale q_t do_t^T the gradients are
+//   dq_t = scale S_t do_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,
+// each of which is the same map of other tensors (F(q, k, v) for the map):
+//   dq = F(do, v, k) on S^T;  dk = F(v, do, q) and dv = F(k, q, do) in reverse
+// time.  One walking kernel therefore serves attention and its three
+// gradients (AttnWalk).  The decay's gradient dg_t = <R_t, e^{g_t} S_{t-1}>
+// obeys dg_t = dg_{t+1} + <q_t, dq_t> - <k_t, dk_t>; summing that over a long
+// sequence in fp32 would lose digits, so the walks leave S and R every
+// kAttnSpan steps and the sum restarts there from <R, S>.
+//
+// Few (batch, head) lanes and a long sequence: time is cut into segments; a
+// state-only walk gives each segment's own state, a short scan joins them, and
+// the full walk then starts every segment from its state.
+#include "mgs_lm.h"
+#include "mgs_num.cuh"
+
+namespace mgs {
+namespace {
+
+constexpr int TS = 16;  // time steps staged in shared memory at once
+
+// The recurrence itself, in fp32 (SIMT).  A block owns one lane's (segment
+// of) time with the whole D x D state in registers: a thread holds 32 key
+// rows of one column, P = D / 32 neighbouring threads share a column.  Per
+// step and thread 32 x 3 fp32 operations: bound by the fp32 pipes.
+template <typename TI, int D, bool STATE_ONLY>
+__global__ void __launch_bounds__(D *D / 32) attn_rec_kernel(const __grid_constant__ AttnSet set) {
+    constexpr int P = D / 32, NT = D * D / 32, V4 = TS * D / 4, NL = V4 / NT;
+    static_assert(NL >= 1 && V4 % NT == 0, "whole vectors a thread");
+    __shared__ __align__(16) float sq[TS * D], sk[TS * D], sv[TS * D];
+    __shared__ float sa[TS], sg[TS];
+    const AttnWalk &w = set.w[blockIdx.y];
+    const int nseg = set.nseg;
+    const int64_t lane = blockIdx.x / nseg;
+    const int seg = int(blockIdx.x % nseg);
+    const int b = int(lane / set.H), h = int(lane % set.H);
+    if (STATE_ONLY && seg == (w.rev ? 0 : nseg - 1)) return;  // nothing starts from this segment's state
+    const int64_t t0 = seg * set.seg_len, t1 = min64(set.T, t0 + set.seg_len);
+    const int tid = threadIdx.x, part = tid % P, col = tid / P;
+    const TI *q = static_cast<const TI *>(w.q) + b * w.qs[0] + (h / w.qdiv) * w.qs[2];
+    const TI *k = static_cast<const TI *>(w.k) + b * w.ks[0] + (h / w.kdiv) * w.ks[2];
+    const TI *v = static_cast<const TI *>(w.v) + b * w.vs[0] + (h / w.vdiv) * w.vs[2];
+    const float *g = set.g + b * set.gs[0] + h * set.gs[2];
+
+    // row of state element i of this thread
+    auto row = [&](int i) { return 4 * (part + P * (i >> 2)) + (i & 3); };
+    float s[32];
+    {
+        const float *in = nullptr;
+        bool tr = false;
+        if (!STATE_ONLY) {
+            if (nseg > 1)
+                in = w.seg_in + (lane * nseg + seg) * D * D, tr = w.seg_t;
+            else if (w.s_in)
+                in = w.s_in + lane * D * D, tr = w.s_in_t;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i] = in == nullptr ? 0.f : tr ? in[col * D + row(i)] : in[row(i) * D + col];
+    }
+    auto put_state = [&](float *to, bool tr) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) to[tr ? col * D + row(i) : row(i) * D + col] = s[i];
+    };
+
+    float rq[NL][4], rk[NL][4], rv[NL][4], rg = 0.f;
+    auto fetch = [&](int64_t base, int n) {
+#pragma unroll
+        for (int l = 0; l < NL; ++l) {
+            const int e = tid + l * NT, u = e / (D / 4), c = 4 * (e % (D / 4));
+            if (u < n) {
+                if (!STATE_ONLY) load4(q + (base + u) * w.qs[1] + c, rq[l]);
+                load4(k + (base + u) * w.ks[1] + c, rk[l]);
+                load4(v + (base + u) * w.vs[1] + c, rv[l]);
+            }
+        }
+        if (tid < n) rg = g[(base + tid) * set.gs[1]];
+    };
+    auto stage = [&](int n) {
+#pragma unroll
+        for (int l = 0; l < NL; ++l) {
+            const int e = tid + l * NT;
+            if (e / (D / 4) < n) {
+                if (!STATE_ONLY) store4(sq + 4 * e, rq[l]);
+                store4(sk + 4 * e, rk[l]);
+                store4(sv + 4 * e, rv[l]);
+            }
+        }
+        if (tid < n) sa[tid] = expf(rg), sg[tid] = rg;
+    };
+
+    double total = 0.0;  // thread 0, state-only: the segment's sum of g
+    // tiles are [base, base + n) with base a multiple of TS, walked up or down
+    int64_t base = w.rev ? (t1 - 1) / TS * TS : t0;
+    int n = int(min64(TS, t1 - base));
+    if (t0 < t1) fetch(base, n);
+    while (base >= t0 && base < t1) {
+        stage(n);
+        __syncthreads();
+        const int64_t nbase = w.rev ? base - TS : base + TS;
+        const int nn = int(min64(TS, t1 - nbase));
+        if (nbase >= t0 && nbase < t1) fetch(nbase, nn);
+        const int64_t end = base + n;
+        if (!STATE_ONLY && w.ckpt && w.rev && (end % kAttnSpan == 0 || end == set.T))
+            put_state(w.ckpt + (lane * set.spans + (end - 1) / kAttnSpan) * D * D, false);
+        if (STATE_ONLY && tid == 0)
+            for (int u = 0; u < n; ++u) total += double(sg[u]);
+        float prev = 1.f;  // reverse: the decay of step t + 1, applied as step t is added
+        for (int i = 0; i < n; ++i) {
+            const int u = w.rev ? n - 1 - i : i;
+            const float a = w.rev ? prev : sa[u];
+            prev = sa[u];
+            const float vc = sv[u * D + col] * w.kv_scale;
+            const float4 *k4 = reinterpret_cast<const float4 *>(sk + u * D) + part;
+            const float4 *q4 = reinterpret_cast<const float4 *>(sq + u * D) + part;
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float4 kk = k4[c * P];
+                s[4 * c + 0] = fmaf(kk.x, vc, a * s[4 * c + 0]);
+                s[4 * c + 1] = fmaf(kk.y, vc, a * s[4 * c + 1]);
+                s[4 * c + 2] = fmaf(kk.z, vc, a * s[4 * c + 2]);
+                s[4 * c + 3] = fmaf(kk.w, vc, a * s[4 * c + 3]);
+                if (!STATE_ONLY) {
+                    const float4 qq = q4[c * P];
+                    acc[0] = fmaf(qq.x, s[4 * c + 0], acc[0]);
+                    acc[1] = fmaf(qq.y, s[4 * c + 1], acc[1]);
+                    acc[2] = fmaf(qq.z, s[4 * c + 2], acc[2]);
+                    acc[3] = fmaf(qq.w, s[4 * c + 3], acc[3]);
+                }
+            }
+            if (!STATE_ONLY) {
+                float o = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+#pragma unroll
+                for (int m = 1; m < P; m <<= 1) o += __shfl_xor_sync(0xffffffffu, o, m);
+                // the column's own v of this step was read above by all P threads of the column
+                __syncwarp();
+                if (part == 0) sv[u * D + col] = o * w.o_scale;
+            }
+        }
+        if (w.rev) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] *= prev;
+        }
+        __syncthreads();
+        if (!STATE_ONLY) {
+            // the tile's outputs (left in sv) to memory, and their products with x
+#pragma unroll
+            for (int l = 0; l < NL; ++l) {
+                const int e = tid + l * NT, u = e / (D / 4), c = 4 * (e % (D / 4));
+                float o[4] = {0.f, 0.f, 0.f, 0.f}, dot = 0.f;
+                if (u < n) {
+                    load4(sv + 4 * e, o);
+                    const int64_t at = b * w.os[0] + (base + u) * w.os[1] + h * w.os[2] + c;
+                    if (w.out_f32)
+                        store4(static_cast<float *>(w.out) + at, o);
+                    else
+                        store4(static_cast<TI *>(w.out) + at, o);
+                    if (w.row_dot) {
+                        float x[4];
+                        load4(static_cast<const TI *>(w.x) + b * w.xs[0] + (base + u) * w.xs[1] +
+                                  (h / w.xdiv) * w.xs[2] + c,
+                              x);
+                        dot = (o[0] * x[0] + o[1] * x[1]) + (o[2] * x[2] + o[3] * x[3]);
+                    }
+                }
+                if (w.row_dot) {
+#pragma unroll
+                    for (int m = 1; m < D / 4; m <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
+                    if (u < n && c == 0) w.row_dot[(b * set.T + base + u) * set.H + h] = dot;
+                }
+            }
+            if (w.ckpt && !w.rev && (end % kAttnSpan == 0 || end == set.T))
+                put_state(w.ckpt + (lane * set.spans + (end - 1) / kAttnSpan) * D * D, false);
+            __syncthreads();
+        }
+        base = nbase;
+        n = nn;
+    }
+    if (STATE_ONLY) {
+        float *to = w.seg_out + (lane * nseg + seg) * D * D;
+        put_state(to, w.seg_t);
+        if (tid == 0) w.seg_out[int64_t(set.B) * set.H * nseg * D * D + lane * nseg + seg] = float(total);
+    } else if (w.s_out && seg == (w.rev ? 0 : nseg - 1)) {
+        put_state(w.s_out + lane * D * D, false);
+    }
+}
+
+// Joins the segments' own states into the state at each segment's start (in
+// place): elementwise over the D x D entries, one thread a run of 4.
+template <int D>
+__global__ void attn_join_kernel(const __grid_constant__ AttnSet set) {
+    const AttnWalk &w = set.w[blockIdx.z];
+    const int64_t lane = blockIdx.y;
+    const int e = 4 * int(blockIdx.x * blockDim.x + threadIdx.x);
+    const int nseg = set.nseg;
+    float *st = w.seg_out + lane * nseg * D * D + e;
+    const float *total = w.seg_out + int64_t(set.B) * set.H * nseg * D * D + lane * nseg;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (w.s_in) {
+        const float *in = w.s_in + lane * D * D;
+        if (bool(w.s_in_t) == bool(w.seg_t)) {
+            load4(in + e, s);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] = in[((e + i) % D) * D + (e + i) / D];
+        }
+    }
+    for (int i = 0; i < nseg; ++i) {
+        const int seg = w.rev ? nseg - 1 - i : i;
+        float *p = st + int64_t(seg) * D * D;
+        float own[4];
+        if (i + 1 < nseg) load4(p, own);
+        store4(p, s);
+        if (i + 1 < nseg) {
+            const float a = expf(total[seg]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[c] = fmaf(a, s[c], own[c]);
+        }
+    }
+}
+
+__device__ __forceinline__ float block_sum(float x, float *red) {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+    __syncthreads();
+    float t = 0.f;
+    for (int i = 0; i < int(blockDim.x) / 32; ++i) t += red[i];
+    return t;
+}
+
+// dg over one span: dg_t = <R_e, S_e> + sum_{t <= s < e} (<q_s, dq_s> - <k_s, dk_s>),
+// e the span's end.  With a decay of one number a head, the span's sum of dg
+// goes to part[lane][span] instead.
+__global__ void __launch_bounds__(256)
+    attn_dg_kernel(const float *__restrict__ u, const float *__restrict__ w, const float *__restrict__ ckS,
+                   const float *__restrict__ ckR, float *__restrict__ dg, float *__restrict__ part, int64_t T,
+                   int64_t H, int spans, int DD) {
+    __shared__ float red[8], scan[8];
+    const int64_t lane = blockIdx.x / spans;
+    const int span = int(blockIdx.x % spans), tid = threadIdx.x;
+    const int64_t b = lane / H, h = lane % H;
+    const int64_t t0 = span * kAttnSpan;
+    const int n = int(min64(kAttnSpan, T - t0));
+    float tail = 0.f;
+    if (ckS) {
+        const float *a = ckS + (lane * spans + span) * DD, *c = ckR + (lane * spans + span) * DD;
+        float acc = 0.f;
+        for (int e = 4 * tid; e < DD; e += 1024) {
+            float x[4], y[4];
+            load4(a + e, x);
+            load4(c + e, y);
+            acc += (x[0] * y[0] + x[1] * y[1]) + (x[2] * y[2] + x[3] * y[3]);
+        }
+        tail = block_sum(acc, red);
+    }
+    // suffix sums: thread i holds steps 4 i .. 4 i + 3
+    float d[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = 4 * tid + i;
+        const int64_t at = (b * T + t0 + t) * H + h;
+        d[i] = t < n ? u[at] - w[at] : 0.f;
+    }
+    d[2] += d[3], d[1] += d[2], d[0] += d[1];
+    float suf = d[0];
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const float o = __shfl_down_sync(0xffffffffu, suf, m);
+        if ((tid & 31) + m < 32) suf += o;
+    }
+    __syncthreads();
+    if ((tid & 31) == 0) scan[tid >> 5] = suf;
+    __syncthreads();
+    const float next = __shfl_down_sync(0xffffffffu, suf, 1);
+    float after = tail + ((tid & 31) != 31 ? next : 0.f);
+    for (int i = (tid >> 5) + 1; i < 8; ++i) after += scan[i];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = 4 * tid + i;
+        if (t >= n) continue;
+        const float x = d[i] + after;
+        sum += x;
+        if (dg) dg[(b * T + t0 + t) * H + h] = x;
+    }
+    if (part) {
+        sum = block_sum(sum, red);
+        if (tid == 0) part[lane * spans + span] = sum;
+    }
+}
+
+// dg[h] = sum over batch and spans, in a fixed order
+__global__ void __launch_bounds__(256)
+    attn_dg_fixed_kernel(const float *__restrict__ part, float *__restrict__ dg, int64_t B, int64_t H, int spans) {
+    __shared__ float red[8];
+    const int64_t h = blockIdx.x;
+    float acc = 0.f;
+    for (int64_t i = threadIdx.x; i < B * spans; i += blockDim.x)
+        acc += part[((i / spans) * H + h) * spans + i % spans];
+    acc = block_sum(acc, red);
+    if (threadIdx.x == 0) dg[h] = acc;
+}
+
+// out[row][hk][D] = sum of the group's heads of in[row][H][D]
+template <typename TO>
+__global__ void attn_group_sum_kernel(const float *__restrict__ in, TO *__restrict__ out, int64_t n4, int D4,
+                                      int64_t Hk, int group) {
+    for (int64_t e = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; e < n4; e += int64_t(gridDim.x) * blockDim.x) {
+        const int64_t rh = e / D4;
+        const int c = int(e - rh * D4);
+        float s[4] = {0.f, 0.f, 0.f, 0.f}, x[4];
+        for (int i = 0; i < group; ++i) {
+            load4(in + 4 * ((rh * group + i) * D4 + c), x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[j] += x[j];
+        }
+        store4(out + 4 * e, s);
+    }
+}
+
+// One token.  A block holds 32 columns of one head's state: 8 threads across
+// (float4), 32 groups of D / 32 rows; the rows' products with q are summed in
+// shared memory.  Bound by the state's bytes, read and written once.
+template <typename TI, int D>
+__global__ void __launch_bounds__(256)
+    attn_step_kernel(const TI *__restrict__ q, const TI *__restrict__ k, const TI *__restrict__ v,
+                     const float *__restrict__ g, float *__restrict__ S, const int32_t *__restrict__ slots,
+                     TI *__restrict__ o, mgs_attention_shape sh, int64_t nslots) {
+    constexpr int R = D / 32;
+    __shared__ float red[32][33];
+    const int64_t lane = blockIdx.x / (D / 32);
+    const int c0 = 32 * int(blockIdx.x % (D / 32));
+    const int64_t b = lane / sh.H, h = lane % sh.H, hk = h / (sh.H / sh.Hk);
+    const int tid = threadIdx.x, cx = 4 * (tid & 7), rg = tid >> 3;
+    TI *out = o + (b * sh.H + h) * D + c0;
+    const int64_t slot = slots ? slots[b] : b;
+    if (slot < 0 || slot >= nslots) {
+        if (tid < 32) out[tid] = from_f<TI>(0.f);
+        return;
+    }
+    float *st = S + (slot * sh.H + h) * D * D + c0 + cx;
+    float4 x[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) x[r] = *reinterpret_cast<const float4 *>(st + (rg + 32 * r) * D);
+    const float a = expf(sh.fixed_decay ? g[h] : g[b * sh.g_stride[0] + h * sh.g_stride[2]]);
+    float vv[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
+    load4(v + b * sh.v_stride[0] + h * sh.v_stride[2] + c0 + cx, vv);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const float kk = to_f(k[b * sh.k_stride[0] + hk * sh.k_stride[2] + rg + 32 * r]);
+        const float qq = to_f(q[b * sh.q_stride[0] + hk * sh.q_stride[2] + rg + 32 * r]);
+        x[r].x = fmaf(kk, vv[0], a * x[r].x);
+        x[r].y = fmaf(kk, vv[1], a * x[r].y);
+        x[r].z = fmaf(kk, vv[2], a * x[r].z);
+        x[r].w = fmaf(kk, vv[3], a * x[r].w);
+        *reinterpret_cast<float4 *>(st + (rg + 32 * r) * D) = x[r];
+        acc[0] = fmaf(qq, x[r].x, acc[0]);
+        acc[1] = fmaf(qq, x[r].y, acc[1]);
+        acc[2] = fmaf(qq, x[r].z, acc[2]);
+        acc[3] = fmaf(qq, x[r].w, acc[3]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[rg][cx + i] = acc[i];
+    __syncthreads();
+    // 8 threads a column, 4 rows each
+    const int c = tid >> 3, r0 = tid & 7;
+    float s = (red[r0][c] + red[r0 + 8][c]) + (red[r0 + 16][c] + red[r0 + 24][c]);
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    s += __shfl_xor_sync(0xffffffffu, s, 4);
+    if (r0 == 0) out[c] = from_f<TI>(s * sh.scale);
+}
+
+// ---------------------------------------------------------------- host side
+// Segments of the time axis: enough (lane, walk, segment) blocks to fill the
+// GPU's 152 SMs, each of whole chunks.  The state-only walk costs about half
+// of a full one, so time is cut only where it at least doubles the blocks.
+int64_t segments(int64_t lanes_walks, int64_t T, int64_t want) {
+    const int64_t chunks = (T + kAttnChunk - 1) / kAttnChunk;
+    int64_t n = lanes_walks > 0 ? want / lanes_walks : 1;
+    if (n < 3) n = 1;
+    return n > chunks ? chunks : n;
+}
+
+struct Plan {
+    int64_t lanes, chunks, seg_len;
+    int nseg, spans;
+};
+Plan plan_of(const mgs_attention_shape &sh, int walks) {
+    Plan p;
+    p.lanes = sh.B * sh.H;
+    p.chunks = (sh.T + kAttnChunk - 1) / kAttnChunk;
+    const int64_t want = 152 * (sh.D == 64 ? 4 : 1);
+    int64_t n = segments(p.lanes * walks, sh.T, want);
+    if (n < 1) n = 1;
+    p.seg_len = (p.chunks + n - 1) / n * kAttnChunk;
+    if (p.seg_len < kAttnChunk) p.seg_len = kAttnChunk;
+    p.nseg = int((sh.T + p.seg_len - 1) / p.seg_len);
+    if (p.nseg < 1) p.nseg = 1;
+    p.spans = int((sh.T + kAttnSpan - 1) / kAttnSpan);
+    return p;
+}
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+size_t seg_bytes(const Plan &p, int D) {  // one walk's segment states and their sums of g
+    return p.nseg > 1 ? up256(size_t(p.lanes) * p.nseg * (size_t(D) * D + 1) * 4) : 0;
+}
+
+// Hands out consecutive 256-byte aligned parts of the workspace.
+struct Carve {
+    char *p;
+    template <typename T>
+    T *take(size_t bytes) {
+        T *r = reinterpret_cast<T *>(p);
+        p += up256(bytes);
+        return r;
+    }
+};
+
+void copy3(int64_t (&to)[3], const int64_t (&from)[3]) {
+    for (int i = 0; i < 3; ++i) to[i] = from[i];
+}
+void dense(int64_t (&st)[3], int64_t T, int64_t H, int64_t D) { st[0] = T * H * D, st[1] = H * D, st[2] = D; }
+
+AttnSet set_of(const mgs_attention_shape &sh, const Plan &p, const float *g, const DevCtl &ctl) {
+    AttnSet s = {};
+    s.g = g;
+    if (sh.fixed_decay)
+        s.gs[0] = 0, s.gs[1] = 0, s.gs[2] = 1;
+    else
+        copy3(s.gs, sh.g_stride);
+    s.B = sh.B, s.T = sh.T, s.H = sh.H;
+    s.seg_len = p.seg_len, s.nseg = p.nseg, s.spans = p.spans;
+    s.ctl = ctl;
+    for (auto &w : s.w) w.qdiv = w.kdiv = w.vdiv = w.xdiv = 1, w.o_scale = w.kv_scale = 1.f;
+    return s;
+}
+
+cudaError_t run_walks(AttnSet &set, int walks, const mgs_attention_shape &sh, Carve &ws, cudaStream_t s) {
+    cudaError_t e;
+    if (set.nseg > 1) {
+        const Plan p = plan_of(sh, walks);
+        for (int i = 0; i < walks; ++i) set.w[i].seg_in = set.w[i].seg_out = ws.take<float>(seg_bytes(p, sh.D));
+        if ((e = launch_attn_rec(set, walks, sh.D, sh.dtype, true, s)) != cudaSuccess) return e;
+        const dim3 grid(unsigned(sh.D * sh.D / 1024), unsigned(sh.B * sh.H), unsigned(walks));
+        if (sh.D == 64)
+            attn_join_kernel<64><<<grid, 256, 0, s>>>(set);
+        else
+            attn_join_kernel<128><<<grid, 256, 0, s>>>(set);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    }
+    return launch_attn_rec(set, walks, sh.D, sh.dtype, false, s);
+}
+
+}  // namespace
+
+template <typename TI, int D>
+static void rec_go(const AttnSet &set, int nwalks, bool state_only, cudaStream_t s) {
+    const dim3 grid(unsigned(set.B * set.H * set.nseg), unsigned(nwalks));
+    if (state_only)
+        attn_rec_kernel<TI, D, true><<<grid, D * D / 32, 0, s>>>(set);
+    else
+        attn_rec_kernel<TI, D, false><<<grid, D * D / 32, 0, s>>>(set);
+}
+
+cudaError_t launch_attn_rec(const AttnSet &set, int nwalks, int D, int dtype, bool state_only, cudaStream_t s) {
+    if (dtype == MGS_BF16)
+        D == 64 ? rec_go<bf16, 64>(set, nwalks, state_only, s) : rec_go<bf16, 128>(set, nwalks, state_only, s);
+    else
+        D == 64 ? rec_go<float, 64>(set, nwalks, state_only, s) : rec_go<float, 128>(set, nwalks, state_only, s);
+    return cudaGetLastError();
+}
+
+size_t attn_workspace_bytes(const mgs_attention_shape &sh, bool backward) {
+    const Plan p = plan_of(sh, backward ? 3 : 1);
+    size_t n = seg_bytes(p, sh.D) * (backward ? 3 : 1);
+    if (backward) {
+        const size_t rows = size_t(sh.B) * sh.T * sh.H;
+        n += 2 * up256(rows * 4);                                                     // row products
+        n += 2 * up256(size_t(p.lanes) * p.spans * sh.D * sh.D * 4);                  // S and R at span ends
+        n += up256(size_t(p.lanes) * p.spans * 4);                                    // spans' sums of dg
+        if (sh.Hk != sh.H) n += 2 * up256(rows * sh.D * 4);                           // dq, dk of each value head
+    }
+    return n;
+}
+
+cudaError_t launch_attn_fwd(const mgs_attention_shape &sh, const void *q, const void *k, const void *v,
+                            const float *g, const float *S0, void *o, float *ST, void *ws, const DevCtl &ctl,
+                            cudaStream_t s) {
+    const Plan p = plan_of(sh, 1);
+    Carve carve{static_cast<char *>(ws)};
+    AttnSet set = set_of(sh, p, g, ctl);
+    AttnWalk &w = set.w[0];
+    w.q = q, w.k = k, w.v = v, w.out = o;
+    copy3(w.qs, sh.q_stride), copy3(w.ks, sh.k_stride), copy3(w.vs, sh.v_stride);
+    dense(w.os, sh.T, sh.H, sh.D);
+    w.qdiv = w.kdiv = int(sh.H / sh.Hk);
+    w.s_in = S0, w.s_out = ST;
+    w.o_scale = sh.scale;
+    return run_walks(set, 1, sh, carve, s);
+}
+
+cudaError_t launch_attn_bwd(const mgs_attention_shape &sh, const void *q, const void *k, const void *v,
+                            const float *g, const float *S0, const void *go, const float *gST, void *dq, void *dk,
+                            void *dv, float *dg, float *dS0, void *ws, const DevCtl &ctl, cudaStream_t s) {
+    const Plan p = plan_of(sh, 3);
+    const int group = int(sh.H / sh.Hk);
+    const size_t rows = size_t(sh.B) * sh.T * sh.H;
+    Carve carve{static_cast<char *>(ws)};
+    float *u = carve.take<float>(rows * 4), *wd = carve.take<float>(rows * 4);
+    const size_t ck = size_t(p.lanes) * p.spans * sh.D * sh.D * 4;
+    float *ckS = carve.take<float>(ck), *ckR = carve.take<float>(ck);
+    float *part = carve.take<float>(size_t(p.lanes) * p.spans * 4);
+    float *dqf = nullptr, *dkf = nullptr;
+    if (group > 1) dqf = carve.take<float>(rows * sh.D * 4), dkf = carve.take<float>(rows * sh.D * 4);
+    const bool ends = p.spans > 1 || gST != nullptr;  // else R is zero at the only span's end
+
+    AttnSet set = set_of(sh, p, g, ctl);
+    AttnWalk &a = set.w[0], &r = set.w[1], &c = set.w[2];
+    // dq = scale S do: the walk of (do, v, k) on S^T
+    a.q = go, a.k = v, a.v = k, a.x = q;
+    copy3(a.qs, sh.do_stride), copy3(a.ks, sh.v_stride), copy3(a.vs, sh.k_stride), copy3(a.xs, sh.q_stride);
+    a.vdiv = a.xdiv = group;
+    a.s_in = S0, a.s_in_t = 1, a.o_scale = sh.scale;
+    a.row_dot = u, a.ckpt = ends ? ckS : nullptr;
+    // dk = R v: the reverse walk of (v, do, q) on R^T
+    r.q = v, r.k = go, r.v = q, r.x = k;
+    copy3(r.qs, sh.v_stride), copy3(r.ks, sh.do_stride), copy3(r.vs, sh.q_stride), copy3(r.xs, sh.k_stride);
+    r.vdiv = r.xdiv = group;
+    r.s_in = gST, r.s_in_t = 1, r.kv_scale = sh.scale, r.rev = 1;
+    r.row_dot = wd, r.ckpt = ends ? ckR : nullptr;
+    // dv = R^T k: the reverse walk of (k, q, do) on R
+    c.q = k, c.k = q, c.v = go, c.out = dv;
+    copy3(c.qs, sh.k_stride), copy3(c.ks, sh.q_stride), copy3(c.vs, sh.do_stride);
+    c.qdiv = c.kdiv = group;
+    c.s_in = gST, c.s_out = dS0, c.kv_scale = sh.scale, c.rev = 1;
+    dense(c.os, sh.T, sh.H, sh.D);
+    // shared query/key heads: each value head's gradient in fp32, summed after
+    dense(a.os, sh.T, sh.H, sh.D), dense(r.os, sh.T, sh.H, sh.D);
+    a.out = group > 1 ? static_cast<void *>(dqf) : dq, a.out_f32 = group > 1;
+    r.out = group > 1 ? static_cast<void *>(dkf) : dk, r.out_f32 = group > 1;
+    cudaError_t e = run_walks(set, 3, sh, carve, s);
+    if (e != cudaSuccess) return e;
+    attn_dg_kernel<<<unsigned(p.lanes * p.spans), 256, 0, s>>>(u, wd, ends ? ckS : nullptr, ckR,
+                                                              sh.fixed_decay ? nullptr : dg,
+                                                              sh.fixed_decay ? part : nullptr, sh.T, sh.H, p.spans,
+                                                              sh.D * sh.D);
+    if (sh.fixed_decay) attn_dg_fixed_kernel<<<unsigned(sh.H), 256, 0, s>>>(part, dg, sh.B, sh.H, p.spans);
+    if (group > 1) {
+        const int64_t n4 = int64_t(rows) / group * sh.D / 4;
+        const unsigned grid = unsigned(min64((n4 + 255) / 256, 152 * 8));
+        for (int i = 0; i < 2; ++i) {
+            const float *in = i ? dkf : dqf;
+            void *out = i ? dk : dq;
+            if (sh.dtype == MGS_BF16)
+                attn_group_sum_kernel<<<grid, 256, 0, s>>>(in, static_cast<bf16 *>(out), n4, sh.D / 4, sh.Hk, group);
+            else
+                attn_group_sum_kernel<<<grid, 256, 0, s>>>(in, static_cast<float *>(out), n4, sh.D / 4, sh.Hk, group);
+        }
+    }
+    return cudaGetLastError();
+}
+
+template <typename TI, int D>
+static void step_go(const mgs_attention_shape &sh, const void *q, const void *k, const void *v, const float *g,
+                    float *S, const int32_t *slots, int64_t nslots, void *o, cudaStream_t s) {
+    attn_step_kernel<TI, D><<<unsigned(sh.B * sh.H * (D / 32)), 256, 0, s>>>(
+        static_cast<const TI *>(q), static_cast<const TI *>(k), static_cast<const TI *>(v), g, S, slots,
+        static_cast<TI *>(o), sh, nslots);
+}
+
+cudaError_t launch_attn_step(const mgs_attention_shape &sh, const void *q, const void *k, const void *v,
+                             const float *g, float *S, const int32_t *slots, int64_t nslots, void *o,
+                             cudaStream_t s) {
+    if (sh.dtype == MGS_BF16)
+        sh.D == 64 ? step_go<bf16, 64>(sh, q, k, v, g, S, slots, nslots, o, s)
+                   : step_go<bf16, 128>(sh, q, k, v, g, S, slots, nslots, o, s);
+    else
+        sh.D == 64 ? step_go<float, 64>(sh, q, k, v, g, S, slots, nslots, o, s)
+                   : step_go<float, 128>(sh, q, k, v, g, S, slots, nslots, o, s);
+    return cudaGetLastError();
+}
+
+}  // namespace mgs
