@@ -258,6 +258,13 @@ def _head_strides(t, name):
     return st[:-1]
 
 
+def _apart(t):
+    """t, or a dense copy of a broadcast t: the tensor-core kernels load through tensor maps, which have no
+    zero strides, and the copy costs less than the kernel without them."""
+    return t.contiguous() if t.numel() and t.dtype == torch.bfloat16 and \
+        any(s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)) else t
+
+
 def _attention_shape(q, k, v, g, scale, grad_o=None):
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a [B,T,Hk,D] tensor")
@@ -299,6 +306,7 @@ def linear_attention_fwd(q, k, v, g, S0=None, scale=None, want_state=False, stre
     head h // (H // Hk); any strides of 16 bytes whose heads are contiguous), g [B,T,H] or [H] fp32 (the
     decay's logarithm; -inf starts the state anew), S0 [B,H,D,D] fp32 or None.
     Returns o [B,T,H,D] (and the final state when want_state)."""
+    q, k, v = _apart(q), _apart(k), _apart(v)
     shape, (B, T, H, Hk, D) = _attention_shape(q, k, v, g, scale)
     if S0 is not None:
         _check_typed(S0, "S0", (B, H, D, D), torch.float32, device=q.device)
@@ -312,6 +320,7 @@ def linear_attention_fwd(q, k, v, g, S0=None, scale=None, want_state=False, stre
 def linear_attention_bwd(q, k, v, g, grad_o, S0=None, grad_ST=None, scale=None, stream=None):
     """Gradients of linear_attention_fwd for L = <grad_o, o> + <grad_ST, S_T>: returns (dq, dk, dv, dg, dS0),
     dS0 None without S0.  dg is [B,T,H], or [H] for a g of one decay a head."""
+    q, k, v, grad_o = _apart(q), _apart(k), _apart(v), _apart(grad_o)
     shape, (B, T, H, Hk, D) = _attention_shape(q, k, v, g, scale, grad_o)
     for t, name in ((S0, "S0"), (grad_ST, "grad_ST")):
         if t is not None:

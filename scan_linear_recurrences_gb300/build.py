@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmgscan.so")
 SOURCES = ["mgs_api.cu", "mgs_mas.cu", "mgs_ms.cu", "mgs_psl.cu", "mgs_givens.cu", "mgs_delta.cu", "mgs_linear.cu",
-           "mgs_attn.cu", "mgs_norm.cu", "mgs_clip.cu"]
+           "mgs_attn.cu", "mgs_attn_mma.cu", "mgs_norm.cu", "mgs_clip.cu"]
 HEADERS = ["mgs_device.cuh", "mgs_launch.h", "mgs_tiles.cuh", "mgs_chunk.cuh", "mgs_ffsincos.cuh", "mgs_umma.cuh", "mgs_cluster.cuh",
            "mgs_lm.h", "mgs_num.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -136,8 +136,7 @@ mgs_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MGS_OK : MGS_ERR
 
 namespace mgs {
 
-cudaError_t make_tmap(CUtensorMap *map, const float *base, int rank, const uint64_t *dims,
-                      const uint64_t *byte_strides, const uint32_t *box, bool swizzle128) {
+static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static std::once_flag once;
     static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
     std::call_once(once, [] {
@@ -148,6 +147,12 @@ cudaError_t make_tmap(CUtensorMap *map, const float *base, int rank, const uint6
             q == cudaDriverEntryPointSuccess)
             encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     });
+    return encode;
+}
+
+cudaError_t make_tmap(CUtensorMap *map, const float *base, int rank, const uint64_t *dims,
+                      const uint64_t *byte_strides, const uint32_t *box, bool swizzle128) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (encode == nullptr) return cudaErrorNotSupported;
     cuuint64_t gdim[3], gstr[2];
     cuuint32_t bdim[3], estr[3] = {1, 1, 1};
@@ -160,6 +165,20 @@ cudaError_t make_tmap(CUtensorMap *map, const float *base, int rank, const uint6
                         gstr, bdim, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_tmap_bf16_4d(CUtensorMap *map, const void *base, const uint64_t *dims, const uint64_t *byte_strides,
+                              const uint32_t *box) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (encode == nullptr) return cudaErrorNotSupported;
+    cuuint64_t gdim[4], gstr[3];
+    cuuint32_t bdim[4], estr[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 4; ++i) gdim[i] = dims[i], bdim[i] = box[i];
+    for (int i = 0; i < 3; ++i) gstr[i] = byte_strides[i];
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), gdim, gstr, bdim, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 

@@ -25,13 +25,14 @@ constexpr int TS = 16;  // time steps staged in shared memory at once
 // The recurrence itself, in fp32 (SIMT).  A block owns one lane's (segment
 // of) time with the whole D x D state in registers: a thread holds 32 key
 // rows of one column, P = D / 32 neighbouring threads share a column.  Per
-// step and thread 32 x 3 fp32 operations: bound by the fp32 pipes.
+// step and thread 32 x 4 fp32 operations: bound by the fp32 pipes.
 template <typename TI, int D, bool STATE_ONLY>
 __global__ void __launch_bounds__(D *D / 32) attn_rec_kernel(const __grid_constant__ AttnSet set) {
     constexpr int P = D / 32, NT = D * D / 32, V4 = TS * D / 4, NL = V4 / NT;
     static_assert(NL >= 1 && V4 % NT == 0, "whole vectors a thread");
     __shared__ __align__(16) float sq[TS * D], sk[TS * D], sv[TS * D];
-    __shared__ float sa[TS], sg[TS];
+    __shared__ float2 sa[TS];  // e^g in two parts: its rounding would be that of every step of a fixed decay
+    __shared__ float sg[TS];
     const AttnWalk &w = set.w[blockIdx.y];
     const int nseg = set.nseg;
     const int64_t lane = blockIdx.x / nseg;
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(D *D / 32) attn_rec_kernel(const __grid_consta
                 store4(sv + 4 * e, rv[l]);
             }
         }
-        if (tid < n) sa[tid] = expf(rg), sg[tid] = rg;
+        if (tid < n) exp_two(rg, sa[tid].x, sa[tid].y), sg[tid] = rg;
     };
 
     double total = 0.0;  // thread 0, state-only: the segment's sum of g
@@ -107,10 +108,10 @@ __global__ void __launch_bounds__(D *D / 32) attn_rec_kernel(const __grid_consta
             put_state(w.ckpt + (lane * set.spans + (end - 1) / kAttnSpan) * D * D, false);
         if (STATE_ONLY && tid == 0)
             for (int u = 0; u < n; ++u) total += double(sg[u]);
-        float prev = 1.f;  // reverse: the decay of step t + 1, applied as step t is added
+        float2 prev = make_float2(1.f, 0.f);  // reverse: the decay of step t + 1, applied as step t is added
         for (int i = 0; i < n; ++i) {
             const int u = w.rev ? n - 1 - i : i;
-            const float a = w.rev ? prev : sa[u];
+            const float2 a = w.rev ? prev : sa[u];
             prev = sa[u];
             const float vc = sv[u * D + col] * w.kv_scale;
             const float4 *k4 = reinterpret_cast<const float4 *>(sk + u * D) + part;
@@ -119,10 +120,10 @@ __global__ void __launch_bounds__(D *D / 32) attn_rec_kernel(const __grid_consta
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 const float4 kk = k4[c * P];
-                s[4 * c + 0] = fmaf(kk.x, vc, a * s[4 * c + 0]);
-                s[4 * c + 1] = fmaf(kk.y, vc, a * s[4 * c + 1]);
-                s[4 * c + 2] = fmaf(kk.z, vc, a * s[4 * c + 2]);
-                s[4 * c + 3] = fmaf(kk.w, vc, a * s[4 * c + 3]);
+                s[4 * c + 0] = fmaf(a.x, s[4 * c + 0], fmaf(a.y, s[4 * c + 0], kk.x * vc));
+                s[4 * c + 1] = fmaf(a.x, s[4 * c + 1], fmaf(a.y, s[4 * c + 1], kk.y * vc));
+                s[4 * c + 2] = fmaf(a.x, s[4 * c + 2], fmaf(a.y, s[4 * c + 2], kk.z * vc));
+                s[4 * c + 3] = fmaf(a.x, s[4 * c + 3], fmaf(a.y, s[4 * c + 3], kk.w * vc));
                 if (!STATE_ONLY) {
                     const float4 qq = q4[c * P];
                     acc[0] = fmaf(qq.x, s[4 * c + 0], acc[0]);
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(D *D / 32) attn_rec_kernel(const __grid_consta
         }
         if (w.rev) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] *= prev;
+            for (int i = 0; i < 32; ++i) s[i] = fmaf(prev.x, s[i], prev.y * s[i]);
         }
         __syncthreads();
         if (!STATE_ONLY) {
@@ -237,7 +238,7 @@ __device__ __forceinline__ float block_sum(float x, float *red) {
 // e the span's end.  With a decay of one number a head, the span's sum of dg
 // goes to part[lane][span] instead.
 __global__ void __launch_bounds__(256)
-    attn_dg_kernel(const float *__restrict__ u, const float *__restrict__ w, const float *__restrict__ ckS,
+    attn_dg_kernel(const float *__restrict__ u, const float *__restrict__ w, int parts, const float *__restrict__ ckS,
                    const float *__restrict__ ckR, float *__restrict__ dg, float *__restrict__ part, int64_t T,
                    int64_t H, int spans, int DD) {
     __shared__ float red[8], scan[8];
@@ -258,13 +259,16 @@ __global__ void __launch_bounds__(256)
         }
         tail = block_sum(acc, red);
     }
+    const int64_t all = int64_t(gridDim.x) / spans * T;
     // suffix sums: thread i holds steps 4 i .. 4 i + 3
     float d[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int t = 4 * tid + i;
         const int64_t at = (b * T + t0 + t) * H + h;
-        d[i] = t < n ? u[at] - w[at] : 0.f;
+        d[i] = 0.f;
+        if (t < n)
+            for (int p = 0; p < parts; ++p) d[i] += u[at + p * all] - w[at + p * all];
     }
     d[2] += d[3], d[1] += d[2], d[0] += d[1];
     float suf = d[0];
@@ -377,27 +381,38 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------- host side
-// Segments of the time axis: enough (lane, walk, segment) blocks to fill the
-// GPU's 152 SMs, each of whole chunks.  The state-only walk costs about half
-// of a full one, so time is cut only where it at least doubles the blocks.
-int64_t segments(int64_t lanes_walks, int64_t T, int64_t want) {
-    const int64_t chunks = (T + kAttnChunk - 1) / kAttnChunk;
-    int64_t n = lanes_walks > 0 ? want / lanes_walks : 1;
-    if (n < 3) n = 1;
-    return n > chunks ? chunks : n;
+// The tensor-core walk takes bf16 tensors whose steps, heads and batch rows lie
+// apart in memory (a TMA tensor map has no zero strides).
+bool mma_takes(const mgs_attention_shape &sh, bool backward) {
+    if (sh.dtype != MGS_BF16) return false;
+    auto apart = [&](const int64_t (&st)[3], int64_t heads) {
+        return (sh.B == 1 || st[0] > 0) && (sh.T == 1 || st[1] > 0) && (heads == 1 || st[2] > 0);
+    };
+    return apart(sh.q_stride, sh.Hk) && apart(sh.k_stride, sh.Hk) && apart(sh.v_stride, sh.H) &&
+           (!backward || apart(sh.do_stride, sh.H));
 }
 
 struct Plan {
     int64_t lanes, chunks, seg_len;
-    int nseg, spans;
+    int nseg, spans, parts;
+    bool mma;
 };
 Plan plan_of(const mgs_attention_shape &sh, int walks) {
     Plan p;
+    p.mma = mma_takes(sh, walks == 3);
+    p.parts = p.mma && sh.D == 128 ? 2 : 1;
     p.lanes = sh.B * sh.H;
     p.chunks = (sh.T + kAttnChunk - 1) / kAttnChunk;
-    const int64_t want = 152 * (sh.D == 64 ? 4 : 1);
-    int64_t n = segments(p.lanes * walks, sh.T, want);
-    if (n < 1) n = 1;
+    // Segments of the time axis: as many as fill the 152 SMs with blocks (one
+    // block to an SM for the tensor-core walk; the SIMT one wants more warps),
+    // where the lanes alone leave at least half of them idle: the state-only
+    // walk costs about half of a full one.  None shorter than four chunks,
+    // below which its two more launches cost what it gains.
+    const int64_t units = p.mma && sh.D == 64 ? sh.B * ((sh.H + 1) / 2) : p.lanes;
+    const int64_t want = 152 * (p.mma || sh.D == 128 ? 1 : 4);
+    int64_t n = units * walks > 0 ? want / (units * walks) : 1;
+    if (n > p.chunks / 4) n = p.chunks / 4;
+    if (n < 2) n = 1;
     p.seg_len = (p.chunks + n - 1) / n * kAttnChunk;
     if (p.seg_len < kAttnChunk) p.seg_len = kAttnChunk;
     p.nseg = int((sh.T + p.seg_len - 1) / p.seg_len);
@@ -441,12 +456,17 @@ AttnSet set_of(const mgs_attention_shape &sh, const Plan &p, const float *g, con
     return s;
 }
 
-cudaError_t run_walks(AttnSet &set, int walks, const mgs_attention_shape &sh, Carve &ws, cudaStream_t s) {
+cudaError_t run_walks(AttnSet &set, int walks, const mgs_attention_shape &sh, const Plan &p, Carve &ws,
+                      cudaStream_t s) {
     cudaError_t e;
+    // the gradients' walks feed the decay's, whose sums want every digit of fp32
+    auto walk = [&](bool state_only) {
+        return p.mma ? launch_attn_mma(set, walks, sh.D, walks == 1 || state_only ? 1 : 3, state_only, s)
+                     : launch_attn_rec(set, walks, sh.D, sh.dtype, state_only, s);
+    };
     if (set.nseg > 1) {
-        const Plan p = plan_of(sh, walks);
         for (int i = 0; i < walks; ++i) set.w[i].seg_in = set.w[i].seg_out = ws.take<float>(seg_bytes(p, sh.D));
-        if ((e = launch_attn_rec(set, walks, sh.D, sh.dtype, true, s)) != cudaSuccess) return e;
+        if ((e = walk(true)) != cudaSuccess) return e;
         const dim3 grid(unsigned(sh.D * sh.D / 1024), unsigned(sh.B * sh.H), unsigned(walks));
         if (sh.D == 64)
             attn_join_kernel<64><<<grid, 256, 0, s>>>(set);
@@ -454,7 +474,7 @@ cudaError_t run_walks(AttnSet &set, int walks, const mgs_attention_shape &sh, Ca
             attn_join_kernel<128><<<grid, 256, 0, s>>>(set);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    return launch_attn_rec(set, walks, sh.D, sh.dtype, false, s);
+    return walk(false);
 }
 
 }  // namespace
@@ -481,7 +501,7 @@ size_t attn_workspace_bytes(const mgs_attention_shape &sh, bool backward) {
     size_t n = seg_bytes(p, sh.D) * (backward ? 3 : 1);
     if (backward) {
         const size_t rows = size_t(sh.B) * sh.T * sh.H;
-        n += 2 * up256(rows * 4);                                                     // row products
+        n += 2 * up256(rows * 4 * p.parts);                                                     // row products
         n += 2 * up256(size_t(p.lanes) * p.spans * sh.D * sh.D * 4);                  // S and R at span ends
         n += up256(size_t(p.lanes) * p.spans * 4);                                    // spans' sums of dg
         if (sh.Hk != sh.H) n += 2 * up256(rows * sh.D * 4);                           // dq, dk of each value head
@@ -502,7 +522,7 @@ cudaError_t launch_attn_fwd(const mgs_attention_shape &sh, const void *q, const 
     w.qdiv = w.kdiv = int(sh.H / sh.Hk);
     w.s_in = S0, w.s_out = ST;
     w.o_scale = sh.scale;
-    return run_walks(set, 1, sh, carve, s);
+    return run_walks(set, 1, sh, p, carve, s);
 }
 
 cudaError_t launch_attn_bwd(const mgs_attention_shape &sh, const void *q, const void *k, const void *v,
@@ -512,7 +532,7 @@ cudaError_t launch_attn_bwd(const mgs_attention_shape &sh, const void *q, const 
     const int group = int(sh.H / sh.Hk);
     const size_t rows = size_t(sh.B) * sh.T * sh.H;
     Carve carve{static_cast<char *>(ws)};
-    float *u = carve.take<float>(rows * 4), *wd = carve.take<float>(rows * 4);
+    float *u = carve.take<float>(rows * 4 * p.parts), *wd = carve.take<float>(rows * 4 * p.parts);
     const size_t ck = size_t(p.lanes) * p.spans * sh.D * sh.D * 4;
     float *ckS = carve.take<float>(ck), *ckR = carve.take<float>(ck);
     float *part = carve.take<float>(size_t(p.lanes) * p.spans * 4);
@@ -544,9 +564,9 @@ cudaError_t launch_attn_bwd(const mgs_attention_shape &sh, const void *q, const 
     dense(a.os, sh.T, sh.H, sh.D), dense(r.os, sh.T, sh.H, sh.D);
     a.out = group > 1 ? static_cast<void *>(dqf) : dq, a.out_f32 = group > 1;
     r.out = group > 1 ? static_cast<void *>(dkf) : dk, r.out_f32 = group > 1;
-    cudaError_t e = run_walks(set, 3, sh, carve, s);
+    cudaError_t e = run_walks(set, 3, sh, p, carve, s);
     if (e != cudaSuccess) return e;
-    attn_dg_kernel<<<unsigned(p.lanes * p.spans), 256, 0, s>>>(u, wd, ends ? ckS : nullptr, ckR,
+    attn_dg_kernel<<<unsigned(p.lanes * p.spans), 256, 0, s>>>(u, wd, p.parts, ends ? ckS : nullptr, ckR,
                                                               sh.fixed_decay ? nullptr : dg,
                                                               sh.fixed_decay ? part : nullptr, sh.T, sh.H, p.spans,
                                                               sh.D * sh.D);

@@ -31,7 +31,7 @@ struct AttnWalk {
     const float *s_in;            // state at the walk's start, [B H][D][D] (null: zeros)
     int s_in_t;                   // ... stored transposed
     float *s_out;                 // state at the walk's end, [B H][D][D] (null: not wanted)
-    float *row_dot;               // [B][T][H]: <out_t, x_t> before rounding (null: not wanted)
+    float *row_dot;               // [parts][B][T][H]: <out_t, x_t> before rounding, in parts to be added
     float *ckpt;                  // [B H][spans][D][D]: the state at each span's end (null: not wanted)
     const float *seg_in;          // [B H][nseg][D][D]: the state at each segment's start (nseg > 1)
     float *seg_out;               // [B H][nseg][D][D]: state-only pass: each segment's own state
@@ -52,6 +52,9 @@ struct AttnSet {
 
 // SIMT walk: the recurrence itself in fp32, any supported type and size
 cudaError_t launch_attn_rec(const AttnSet &set, int nwalks, int D, int dtype, bool state_only, cudaStream_t s);
+
+// tensor-core walk, bf16; terms: bf16 terms of the computed operands of the output
+cudaError_t launch_attn_mma(const AttnSet &set, int nwalks, int D, int terms, bool state_only, cudaStream_t s);
 
 size_t attn_workspace_bytes(const mgs_attention_shape &sh, bool backward);
 cudaError_t launch_attn_fwd(const mgs_attention_shape &sh, const void *q, const void *k, const void *v,

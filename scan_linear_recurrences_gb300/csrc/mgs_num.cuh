@@ -59,4 +59,32 @@ __device__ __forceinline__ uint4 pack(const float (&v)[8]) {
     return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
+// e^x as a sum of two fp32 (relative error about 1e-8), for factors that are
+// multiplied together hundreds of times: x = n log 2 + y with |y| <= log(2) / 2,
+// e^y = 1 + y + (Taylor's series from y^2 / 2), y and the sum in two parts.
+__device__ __forceinline__ void exp_two(float x, float &hi, float &lo) {
+    if (!(x > -100.f && x < 80.f)) {  // zero, overflow, NaN: nothing to refine
+        hi = expf(x), lo = 0.f;
+        return;
+    }
+    const float LN2_HI = 0.693145751953125f, LN2_LO = 1.42860682030941723e-6f;  // log 2: 16 bits, and the rest
+    const float n = rintf(x * 1.44269504f);
+    const float a = fmaf(-n, LN2_HI, x);  // exact
+    const float b = -n * LN2_LO;
+    const float y = a + b, yl = b - (y - a);
+    float p = 1.f / 40320.f;
+    p = fmaf(p, y, 1.f / 5040.f);
+    p = fmaf(p, y, 1.f / 720.f);
+    p = fmaf(p, y, 1.f / 120.f);
+    p = fmaf(p, y, 1.f / 24.f);
+    p = fmaf(p, y, 1.f / 6.f);
+    p = fmaf(p, y, 0.5f);
+    const float q = fmaf(p * y, y, yl + yl * y);
+    const float s = 1.f + y, t = (1.f - s) + y;
+    const float r = t + q;
+    const float h = s + r, l = r - (h - s);
+    const float e = ldexpf(1.f, int(n));
+    hi = h * e, lo = l * e;
+}
+
 }  // namespace mgs

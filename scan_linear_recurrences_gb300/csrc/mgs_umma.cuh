@@ -248,6 +248,65 @@ __device__ __forceinline__ void tmem_st32x2(uint32_t ca, const float (&a)[32], u
 #undef MGS_R32
 }
 
+// ---- bf16 operands (kind::f16), f32 accumulation ----
+// Instruction descriptor: as above with A / B format 1 = bf16.  An operand may
+// be MN-major (its M or N index contiguous in shared memory).
+__host__ __device__ constexpr uint32_t umma_idesc_bf16(int M, int N, bool b_mn_major) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(b_mn_major) << 16) | (uint32_t(N >> 3) << 17) |
+           (uint32_t(M >> 4) << 24);
+}
+// 128-byte-swizzled panels of 64 bf16 columns: a K-major operand steps K = 16
+// by 32 bytes within the rows (rows 128 bytes, groups of 8 rows 1024 bytes
+// apart); an MN-major one by 16 rows (2048 bytes), its next 64 columns being
+// the next panel, `panel` bytes on.
+__device__ __forceinline__ uint64_t umma_desc_k(uint32_t saddr) { return umma_desc_sw128(saddr, 16u, 1024u); }
+__device__ __forceinline__ uint64_t umma_desc_mn(uint32_t saddr, uint32_t panel) {
+    return umma_desc_sw128(saddr, panel, 1024u);
+}
+__device__ __forceinline__ void umma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(uint32_t(accumulate))
+        : "memory");
+}
+// A from TMEM: row m in lane m, two k to a column (the even one in the low half)
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(uint32_t(accumulate))
+        : "memory");
+}
+
+// Stores of 8 / 16 / 32 columns without a wait; tmem_wait_st() waits for all of
+// the thread's stores.
+__device__ __forceinline__ void tmem_put8(uint32_t taddr, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_put16(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_put32(uint32_t taddr, const float (&r)[32]) {
+    uint32_t u[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(r[i]);
+    tmem_put16(taddr, u);
+    tmem_put16(taddr + 16, u + 16);
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // TMEM address of lane `lane0`, column `col` relative to an allocation base.
 __device__ __forceinline__ uint32_t tmem_at(uint32_t base, int lane0, int col) {
     return base + (uint32_t(lane0) << 16) + uint32_t(col);

@@ -99,6 +99,26 @@ def test_attention_strided_inputs(D, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+def test_attention_zero_strides_through_the_c_entry(dtype):
+    # keys broadcast over the steps: no tensor map has a zero stride, so the
+    # entry point takes the kernel that needs none
+    d = _lm.attn_inputs(2, 60, 2, 2, 64, dtype, False, seed=12)
+    d["k"] = d["k"][:, :1].expand(2, 60, 2, 64)
+    c = _lm.cuda(d)
+    k = c["k"][:, :1].contiguous()
+    dense = (60 * 128, 128, 64)
+    shape = b.mgs_attention_shape(2, 60, 2, 2, 64, b.MGS_F32 if dtype == F32 else b.MGS_BF16, 0, 0.125, dense,
+                                  (128, 0, 64), dense, (120, 2, 1))
+    n = b.mgs_linear_attention_workspace_size(shape, 0)
+    ws = torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
+    o = torch.empty(2, 60, 2, 64, dtype=dtype, device="cuda")
+    ST = torch.empty(2, 2, 64, 64, device="cuda")
+    b.mgs_linear_attention_fwd(shape, c["q"], k, c["v"], c["g"], None, o, ST, ws, n)
+    b.mgs_check()
+    _compare({"o": o, "S_T": ST}, _lm.attn_ref(d, grads=False), dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 def test_attention_reset_and_strong_decays(dtype):
     # a decay of zero (g = -inf) starts the state anew: the steps before do not
     # reach those after; very strong and vanishing decays in one sequence
