@@ -17,7 +17,7 @@
 // Heads of 64 go two to a block: panel p of a tile (64 columns) is head p; the
 // state's product is formed for both at once and its two diagonal blocks used.
 //
-// Roles of the 18 warps (warp w reaches TMEM lanes 32 (w % 4) ..):
+// Roles of the 20 warps (warp w reaches TMEM lanes 32 (w % 4) ..):
 //   0..7   rows i of the chunk: P from A, the scaling of Q S, the output; warps
 //          0..3 take columns 0..63, 4..7 columns 64..127
 //   8..15  rows of the state (key index): the weighted keys, the state itself
@@ -25,27 +25,39 @@
 //          steps' groups and the state's columns
 //   16     one thread issues the products
 //   17     one thread loads tiles by TMA; the warp sums g
+//   18, 19 fill the last warpgroup
 #include "mgs_launch.h"
 #include "mgs_lm.h"
 #include "mgs_num.cuh"
 #include "mgs_tiles.cuh"
 #include "mgs_umma.cuh"
 
-#include <cudaTypedefs.h>
+#include <atomic>
 
 namespace mgs {
 namespace {
 
 constexpr int C = 128;
 constexpr int kTile = 32768, kPanel = 16384;   // a tile: two panels of 128 rows x 64 bf16
-constexpr int kThreads = 18 * 32;
+constexpr int kThreads = 20 * 32;              // five warpgroups
+// Registers a thread: the kernel is launched with kRegs for each; the last
+// warpgroup gives up what the four others take (104 x 4 + 64 = 96 x 5).
+constexpr int kRegs = 96, kRegsWork = 104, kRegsLast = 64;
+static_assert(4 * kRegsWork + kRegsLast <= 5 * kRegs, "within the registers of the launch");
 constexpr int GT = 16;                         // steps of a group of weighted keys: one K = 16 product
 constexpr int NG = C / GT;
 
-// TMEM columns: A 0..127; P after it where it is one term, over it where it is three
-constexpr uint32_t kA = 0, kO = 192, kKV = 320, kW = 448;
-template <int TERMS>
-constexpr uint32_t kP = TERMS == 1 ? 128 : 0;
+// TMEM columns (all 512):
+//   A 0..127 and P behind it (one term) or over it (three: A is read whole before);
+//   the state's product 192..319; the weighted keys of a chunk, three terms of 64
+//   columns, 320..511.  O has no columns of its own: with one term and one head
+//   it takes A's place once P is made of it, else the place of the state's
+//   product once that is in registers.
+template <int D, int TERMS>
+struct Tmem {
+    static constexpr bool over_a = D == 128 && TERMS == 1;
+    static constexpr uint32_t A = 0, P = TERMS == 1 ? 128 : 0, KV = 192, O = over_a ? 0 : 192, W = 320;
+};
 
 template <int D, int TERMS>
 struct Smem {
@@ -55,7 +67,8 @@ struct Smem {
     static constexpr int k = TERMS * sterm, q = k + NK * kTile, v = q + NQ * kTile, arr = v + NV * kTile;
     // per head: G (high and low parts), the column factors and the state weights of the 128 steps
     static constexpr int bars = arr + NH * 4 * C * 4;
-    static constexpr size_t bytes = size_t(bars) + 256;
+    static constexpr int walk = bars + 256;                         // the block's AttnWalk
+    static constexpr size_t bytes = size_t(walk) + sizeof(AttnWalk);
     static_assert(bytes <= 232448, "shared memory of an SM");
 };
 
@@ -75,13 +88,40 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
-// Waits for a phase; false once the wait gives up or another role has.
-__device__ __noinline__ bool slow_wait(uint64_t *bar, uint32_t parity, volatile int *abort_word, DevCtl ctl) {
-    const uint64_t t0 = global_ns();
-    while (true) {
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// 16 lanes x 8 columns: thread t holds, of lanes t / 4 and t / 4 + 8, column
+// t % 4 in r[0], r[1] and column 4 + t % 4 in r[2], r[3]
+__device__ __forceinline__ void tmem_put_16x8(uint32_t taddr, const uint32_t (&r)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+}
+
+// One thread of a converged warp, of which the compiler knows that it is one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.b32 %0, 1, 0, P;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Waits for a phase; false once the wait gives up or another role has.  The
+// clock is read every 64th try only: the read itself takes long.
+__device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity, volatile int *abort_word, DevCtl ctl) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 63u) != 0) continue;
         if (*abort_word != 0) return false;
-        if (global_ns() - t0 > ctl.timeout_ns) {
+        const uint64_t t = global_ns();
+        if (t0 == 0) {
+            t0 = t;
+        } else if (t - t0 > ctl.timeout_ns) {
             record_error(ctl, ERR_MBAR_TIMEOUT);
             *abort_word = 1;
             return false;
@@ -89,15 +129,14 @@ __device__ __noinline__ bool slow_wait(uint64_t *bar, uint32_t parity, volatile 
     }
 }
 
-// x0, x1 as a sum of TERMS bf16 pairs (packed: x0 in the low half)
+// x as a sum of TERMS bf16 pairs (packed: x.x in the low half)
 template <int TERMS>
-__device__ __forceinline__ void split(float x0, float x1, uint32_t (&t)[TERMS]) {
-    t[0] = pack_bf16(x0, x1);
+__device__ __forceinline__ void split(float2 x, uint32_t (&t)[TERMS]) {
+    t[0] = pack_bf16(x.x, x.y);
 #pragma unroll
     for (int i = 1; i < TERMS; ++i) {
-        x0 -= bf_lo(t[i - 1]);
-        x1 -= bf_hi(t[i - 1]);
-        t[i] = pack_bf16(x0, x1);
+        x = __ffma2_rn(make_float2(bf_lo(t[i - 1]), bf_hi(t[i - 1])), make_float2(-1.f, -1.f), x);
+        t[i] = pack_bf16(x.x, x.y);
     }
 }
 
@@ -110,15 +149,31 @@ __device__ __forceinline__ void add2(float &h, float &l, float a, float b) {
     l = lo - (h - s);
 }
 
+// 16 columns of P as TERMS packed terms, 64 TMEM columns apart
+template <int TERMS>
+__device__ __forceinline__ void put_terms(uint32_t at, const float (&x)[16]) {
+    uint32_t pk[TERMS][8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        uint32_t s[TERMS];
+        split<TERMS>(make_float2(x[2 * u], x[2 * u + 1]), s);
+#pragma unroll
+        for (int m = 0; m < TERMS; ++m) pk[m][u] = s[m];
+    }
+#pragma unroll
+    for (int m = 0; m < TERMS; ++m) tmem_put8(at + 64 * m, pk[m]);
+}
+
 template <int D, int TERMS>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_mma_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnSet set, int state_only) {
     using L = Smem<D, TERMS>;
+    using M = Tmem<D, TERMS>;
     constexpr int NH = L::NH, SC = D == 64 ? 32 : 64;  // state columns of a thread
     extern __shared__ __align__(1024) unsigned char sm[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);
     uint64_t *k_full = bars, *k_empty = bars + 2, *q_full = bars + 4, *q_empty = bars + 6, *v_full = bars + 8,
-             *v_empty = bars + 10, *w_full = bars + 12, *w_empty = bars + 14;
+             *v_empty = bars + 10, *w_full = bars + 12, *o_ready = bars + 14;
     uint64_t *a_done = bars + 16, *p_ready = bars + 17, *qs_done = bars + 18, *o_done = bars + 19, *o_free = bars + 20,
              *s_ready = bars + 21, *kv_done = bars + 22, *kv_free = bars + 23, *g_full = bars + 24, *g_empty = bars + 25,
              *a_read = bars + 28, *drained = bars + 29;
@@ -126,26 +181,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_word = reinterpret_cast<volatile int *>(slot + 1);
     float *total = reinterpret_cast<float *>(slot + 2);  // [NH]: the chunk's decay
 
-    const AttnWalk &w = set.w[blockIdx.y];
+    // the walk's description from shared memory: parameters indexed by blockIdx
+    // would be read through the global path
+    const AttnWalk &w = *reinterpret_cast<const AttnWalk *>(sm + L::walk);
+    const bool rev = set.w[blockIdx.y].rev != 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nseg = set.nseg, units = int((set.H + NH - 1) / NH);
     const int unit = int(blockIdx.x) / nseg, seg = int(blockIdx.x) - unit * nseg;
     const int b = unit / units, h0 = (unit - b * units) * NH;
-    if (state_only && seg == (w.rev ? 0 : nseg - 1)) return;  // nothing starts from this segment's state
+    if (state_only && seg == (rev ? 0 : nseg - 1)) return;  // nothing starts from this segment's state
     const int H = int(set.H), T = int(set.T);
     const int c0 = int(seg * (set.seg_len / C)), c1 = min(c0 + int(set.seg_len / C), (T + C - 1) / C);
     const int n = c1 - c0;
-    const bool rev = w.rev != 0;
     const DevCtl ctl = set.ctl;
 
+    static_assert(sizeof(AttnWalk) % 4 == 0 && sizeof(AttnWalk) <= 4 * kThreads, "a word a thread");
+    if (tid < int(sizeof(AttnWalk) / 4))
+        reinterpret_cast<uint32_t *>(sm + L::walk)[tid] = reinterpret_cast<const uint32_t *>(&set.w[blockIdx.y])[tid];
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&k_full[i], 1), mbar_init(&q_full[i], 1), mbar_init(&v_full[i], 1);
-            mbar_init(&k_empty[i], state_only ? 8 : 9);  // the readers of weighted keys, and Q K^T
+            mbar_init(&k_empty[i], 8);  // the rows' warps, who stage the output in it at the end
             mbar_init(&q_empty[i], 1), mbar_init(&v_empty[i], 1);
-            mbar_init(&w_full[i], 4), mbar_init(&w_empty[i], 1);
+            mbar_init(&w_full[i], 8);
         }
-        mbar_init(a_done, 1), mbar_init(p_ready, 8), mbar_init(qs_done, 1), mbar_init(o_done, 1), mbar_init(o_free, 8);
+        mbar_init(a_done, 1), mbar_init(p_ready, 8), mbar_init(o_ready, 8), mbar_init(qs_done, 1), mbar_init(o_done, 1), mbar_init(o_free, 8);
         mbar_init(s_ready, 8), mbar_init(kv_done, 1), mbar_init(kv_free, 8);
         mbar_init(g_full, 1), mbar_init(g_empty, state_only ? 8 : 16);
         mbar_init(a_read, 8), mbar_init(drained, 1);
@@ -162,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tm = *slot;
     const uint32_t tq = tm + (uint32_t(32 * (warp & 3)) << 16);
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-        return mbar_try_wait(bar, parity & 1u) || slow_wait(bar, parity & 1u, abort_word, ctl);
+        return bounded_wait(bar, parity & 1u, abort_word, ctl);
     };
     // the same by a whole warp, whose lanes go on together
     auto wwait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
@@ -171,181 +231,206 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool ok0 = *abort_word == 0;
     if (!ok0 && tid == 0) record_error(ctl, ERR_MBAR_TIMEOUT);
 
+    if (warp < 16) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsWork));
     if (!ok0) {
         // nothing was started
     } else if (warp < 8) {
         // ------------------------------------------------ rows of the chunk
-        if (!state_only) {
-            const int hh = warp >> 2, i = 32 * (warp & 3) + lane, wb = warp & 3;
-            bool ok = true;
-            for (int it = 0; it < n && ok; ++it) {
-                const int c = chunk_of(it);
-                const int64_t t = int64_t(c) * C + i;
-                if (!(ok = wwait(g_full, it))) break;
-                // weight of row i of Q S, for the head of this thread's output columns
-                const float *Go = Gh + (NH == 2 ? hh * 4 * C : 0);
-                const float ri = rev ? ex2_approx((Go[C - 1] - Go[i]) + (Go[2 * C - 1] - Go[C + i]))
-                                     : ex2_approx(Go[i] + Go[C + i]);
-                for (int hp = 0; hp < NH; ++hp) {
-                    const float *G = Gh + hp * 4 * C;
-                    const float gi = G[i], gl = G[C + i];
-                    const int ev = it * NH + hp;
-                    if (!(ok = wwait(a_done, ev))) break;
-                    tc_fence_after();
-                    // the product with the first head's P has read it
-                    if (hp > 0 && !(ok = wwait(o_done, ev - 1))) break;
-                    // two blocks of 32 columns j
-                    float x[TERMS == 1 ? 1 : 2][32];
-                    auto block_load = [&](int bl, float (&v)[32]) {
-                        const int jb = 2 * hh + bl;
-                        if (rev ? jb < wb : jb > wb) return;  // wholly masked
-                        tmem_ld32(tq + kA + 32 * jb, v);
-                        const float *cf = G + 2 * C + 32 * jb;
-                        if (jb == wb) {
+        const int hh = warp >> 2, wb = warp & 3, i = 32 * wb + lane;
+        const float sgn = rev ? -1.f : 1.f, kvs = w.kv_scale, os = w.o_scale;
+        const int isgn = rev ? -1 : 1;
+        // the output's head, and the weights of its rows of Q S
+        const int h = NH == 2 ? h0 + hh : h0, col = NH == 2 ? 0 : 64 * hh;
+        const float *Go = Gh + (NH == 2 ? hh * 4 * C : 0);
+        const int lrow = lane >> 3, lch = lane & 7;  // whole lines: 4 rows of 8 pieces of 16 bytes at a time
+        bool ok = true;
+#pragma unroll 1
+        for (int it = 0; it < (state_only ? 0 : n) && ok; ++it) {
+            const int c = chunk_of(it);
+            if (!(ok = wwait(g_full, it))) break;
+            const float ri = rev ? ex2_approx((Go[C - 1] - Go[i]) + (Go[2 * C - 1] - Go[C + i]))
+                                 : ex2_approx(Go[i] + Go[C + i]);
+#pragma unroll 1
+            for (int hp = 0; hp < NH; ++hp) {
+                const float *G = Gh + hp * 4 * C;
+                const float gi = G[i], gl = G[C + i];
+                const int ev = it * NH + hp;
+                if (!(ok = wwait(a_done, ev))) break;
+                tc_fence_after();
+                // the product with the first head's P has read it
+                if (hp > 0 && !(ok = wwait(o_done, ev - 1))) break;
+                // P from A, 16 columns j at a time.  Off the diagonal's block of 32 the
+                // exponent splits at the block's edge between i and j, into a factor of the
+                // row and one of the column, neither above 1; a block past it is zero.
+                auto piece = [&](int j0, float (&v)[16]) {
+                    const int jb = j0 >> 5;
+                    if (isgn * (jb - wb) > 0) {
 #pragma unroll
-                            for (int u = 0; u < 32; u += 4) {
-                                const float4 a = *reinterpret_cast<const float4 *>(G + 32 * jb + u);
-                                const float4 l = *reinterpret_cast<const float4 *>(G + C + 32 * jb + u);
-                                const float ah[4] = {a.x, a.y, a.z, a.w}, al[4] = {l.x, l.y, l.z, l.w};
+                        for (int u = 0; u < 16; ++u) v[u] = 0.f;
+                        return;
+                    }
+                    tmem_ld16(tq + M::A + j0, v);
+                    if (jb == wb) {
 #pragma unroll
-                                for (int m = 0; m < 4; ++m) {
-                                    const float e = (gi - ah[m]) + (gl - al[m]);
-                                    const float f = ex2_approx(rev ? -e : e) * w.kv_scale;
-                                    const bool in = rev ? u + m >= lane : u + m <= lane;
-                                    v[u + m] = in ? v[u + m] * f : 0.f;
-                                }
+                        for (int u = 0; u < 16; u += 4) {
+                            const float4 ah = *reinterpret_cast<const float4 *>(G + j0 + u);
+                            const float4 al = *reinterpret_cast<const float4 *>(G + C + j0 + u);
+                            const float e[4] = {(gi - ah.x) + (gl - al.x), (gi - ah.y) + (gl - al.y),
+                                                (gi - ah.z) + (gl - al.z), (gi - ah.w) + (gl - al.w)};
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) {
+                                // the mask as bits: a choice would become a branch for each element
+                                const float y = v[u + m] * (ex2_approx(sgn * e[m]) * kvs);
+                                const int past = isgn * (j0 + u + m - i);  // > 0: masked
+                                v[u + m] = __uint_as_float(__float_as_uint(y) & uint32_t((past - 1) >> 31));
                             }
-                        } else {
-                            // off the diagonal the exponent splits at the block's edge between i
-                            // and j, into a factor of the row and one of the column, neither above 1
-                            const int ref = rev ? 32 * jb : 32 * jb + 31;
-                            const float e = (gi - G[ref]) + (gl - G[C + ref]);
-                            const float f = ex2_approx(rev ? -e : e) * w.kv_scale;
-#pragma unroll
-                            for (int u = 0; u < 32; u += 4) {
-                                const float4 a = *reinterpret_cast<const float4 *>(cf + u);
-                                v[u] *= f * a.x, v[u + 1] *= f * a.y, v[u + 2] *= f * a.z, v[u + 3] *= f * a.w;
-                            }
-                        }
-                    };
-                    if constexpr (TERMS == 1) {
-#pragma unroll
-                        for (int bl = 0; bl < 2; ++bl) {
-                            uint32_t pk[16];
-                            const int jb = 2 * hh + bl;
-                            if (rev ? jb < wb : jb > wb) {
-#pragma unroll
-                                for (int u = 0; u < 16; ++u) pk[u] = 0u;
-                            } else {
-                                block_load(bl, x[0]);
-#pragma unroll
-                                for (int u = 0; u < 16; ++u) pk[u] = pack_bf16(x[0][2 * u], x[0][2 * u + 1]);
-                            }
-                            tmem_put16(tq + kP<TERMS> + 16 * jb, pk);
                         }
                     } else {
-                        // P's terms take A's place: all of A is read before any is written
-                        block_load(0, x[0]);
-                        block_load(1, x[1]);
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mb_arrive(a_read);
-                        if (!(ok = wwait(a_read, ev))) break;
-                        tc_fence_after();
+                        const int ref = 32 * jb + (rev ? 0 : 31);
+                        const float f = ex2_approx(sgn * ((gi - G[ref]) + (gl - G[C + ref]))) * kvs;
 #pragma unroll
-                        for (int bl = 0; bl < 2; ++bl) {
-                            const int jb = 2 * hh + bl;
-                            const bool none = rev ? jb < wb : jb > wb;
-#pragma unroll
-                            for (int half = 0; half < 2; ++half) {
-                                uint32_t pk[TERMS][8];
-#pragma unroll
-                                for (int u = 0; u < 8; ++u) {
-                                    uint32_t s[TERMS];
-                                    split<TERMS>(x[bl][16 * half + 2 * u], x[bl][16 * half + 2 * u + 1], s);
-#pragma unroll
-                                    for (int m = 0; m < TERMS; ++m) pk[m][u] = none ? 0u : s[m];
-                                }
-#pragma unroll
-                                for (int m = 0; m < TERMS; ++m)
-                                    tmem_put8(tq + kP<TERMS> + 64 * m + 16 * jb + 8 * half, pk[m]);
-                            }
+                        for (int u = 0; u < 16; u += 4) {
+                            const float4 a = *reinterpret_cast<const float4 *>(G + 2 * C + j0 + u);
+                            const float2 ff = make_float2(f, f);
+                            const float2 y = __fmul2_rn(make_float2(v[u], v[u + 1]), __fmul2_rn(ff, make_float2(a.x, a.y)));
+                            const float2 z =
+                                __fmul2_rn(make_float2(v[u + 2], v[u + 3]), __fmul2_rn(ff, make_float2(a.z, a.w)));
+                            v[u] = y.x, v[u + 1] = y.y, v[u + 2] = z.x, v[u + 3] = z.y;
                         }
                     }
-                    tmem_wait_st();
-                    if (hp == 0) {
-                        // O = Q S scaled by rows, in place; P V is added to it
-                        if (!(ok = wwait(qs_done, it))) break;
-                        tc_fence_after();
+                };
+                if constexpr (TERMS == 1) {
+#pragma unroll 1
+                    for (int j0 = 64 * hh; j0 < 64 * hh + 64; j0 += 16) {
+                        float v[16];
+                        piece(j0, v);
+                        uint32_t pk[8];
 #pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            float o[32];
-                            tmem_ld32(tq + kO + 64 * hh + 32 * p, o);
-#pragma unroll
-                            for (int u = 0; u < 32; ++u) o[u] *= ri;
-                            tmem_put32(tq + kO + 64 * hh + 32 * p, o);
-                        }
-                        tmem_wait_st();
+                        for (int u = 0; u < 8; ++u) pk[u] = pack_bf16(v[2 * u], v[2 * u + 1]);
+                        tmem_put8(tq + M::P + j0 / 2, pk);
                     }
+                } else {
+                    // P's terms take A's place: all of A is read before any is written
+                    float v[4][16];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) piece(64 * hh + 16 * q, v[q]);
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mb_arrive(p_ready);
-                }
-                if (!ok) break;
-                if (lane == 0) mb_arrive(g_empty);
-                // the output: row i, columns 64 hh ..
-                const int h = NH == 2 ? h0 + hh : h0, col = NH == 2 ? 0 : 64 * hh;
-                const bool live = t < T && h < H;
-                uint4 xv[8];
-                if (w.row_dot && live) {
-                    const bf16 *px = static_cast<const bf16 *>(w.x) + b * w.xs[0] + t * w.xs[1] +
-                                     (h / w.xdiv) * w.xs[2] + col;
+                    if (lane == 0) mb_arrive(a_read);
+                    if (!(ok = wwait(a_read, ev))) break;
+                    tc_fence_after();
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) xv[u] = reinterpret_cast<const uint4 *>(px)[u];
+                    for (int q = 0; q < 4; ++q) put_terms<TERMS>(tq + M::P + 32 * hh + 8 * q, v[q]);
                 }
-                if (!(ok = wwait(o_done, it * NH + NH - 1))) break;
-                tc_fence_after();
-                const int64_t at = b * w.os[0] + t * w.os[1] + h * w.os[2] + col;
-                float dot = 0.f;
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mb_arrive(p_ready);
+                if (hp == 0) {
+                    // O = Q S scaled by rows, in place; P V is added to it
+                    if (!(ok = wwait(qs_done, it))) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int j0 = 64 * hh; j0 < 64 * hh + 64; j0 += 16) {
+                        float o[16];
+                        tmem_ld16(tq + M::O + j0, o);
+                        uint32_t y[16];
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    float o[32];
+                        for (int u = 0; u < 16; ++u) y[u] = __float_as_uint(o[u] * ri);
+                        tmem_put16(tq + M::O + j0, y);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
                     __syncwarp();
-                    tmem_ld32(tq + kO + 64 * hh + 32 * p, o);
-                    if (p == 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mb_arrive(o_free);
+                    if (lane == 0) mb_arrive(o_ready);
+                }
+            }
+            if (!ok) break;
+            if (lane == 0) mb_arrive(g_empty);
+            // The output: row i, columns 64 hh .. of the tile.  A thread's row would make
+            // 32 short pieces of every store: the warp's 32 rows go through shared memory
+            // (its part of the chunk's keys, which nobody reads any more: swizzled rows of
+            // 128 bytes) and out in whole lines.  The same way in for x.
+            const int64_t tw = int64_t(c) * C + 32 * wb;  // the warp's first row
+            unsigned char *stage = sm + L::k + (it % L::NK) * kTile + hh * kPanel + 32 * wb * 128;
+            unsigned char *mine = stage + lane * 128;
+            const int live = h < H ? min(32, T - int(tw)) : 0;  // rows that exist (may be negative)
+            auto line = [&](int u) {
+                return reinterpret_cast<uint4 *>(stage + (4 * u + lrow) * 128 + ((lch ^ ((4 * u + lrow) & 7)) << 4));
+            };
+            auto own = [&](int u) { return reinterpret_cast<uint4 *>(mine + ((u ^ (lane & 7)) << 4)); };
+            uint4 xv[8];
+            if (w.row_dot) {
+                const bf16 *px = static_cast<const bf16 *>(w.x) + b * w.xs[0] + tw * w.xs[1] + (h / w.xdiv) * w.xs[2] +
+                                 col + 8 * lch;
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    xv[u] = 4 * u + lrow < live ? *reinterpret_cast<const uint4 *>(px + (4 * u + lrow) * w.xs[1])
+                                                : make_uint4(0u, 0u, 0u, 0u);
+            }
+            if (!(ok = wwait(o_done, it * NH + NH - 1))) break;
+            tc_fence_after();
+            if (w.row_dot) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) *line(u) = xv[u];
+                __syncwarp();
+            }
+            float dot = 0.f;
+#pragma unroll 1
+            for (int p = 0; p < 4; ++p) {  // 16 columns at a time
+                float o[16];
+                tmem_ld16(tq + M::O + 64 * hh + 16 * p, o);
+                if (p == 3) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mb_arrive(o_free);
+                }
+#pragma unroll
+                for (int u = 0; u < 16; ++u) o[u] *= os;
+                if (w.row_dot) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float xx[8];
+                        unpack(*own(2 * p + u), xx);
+#pragma unroll
+                        for (int m = 0; m < 8; ++m) dot = fmaf(o[8 * u + m], xx[m], dot);
                     }
-#pragma unroll
-                    for (int u = 0; u < 32; ++u) o[u] *= w.o_scale;
-                    if (live && w.row_dot) {
-#pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            float xx[8];
-                            unpack(xv[4 * p + u], xx);
-#pragma unroll
-                            for (int m = 0; m < 8; ++m) dot = fmaf(o[8 * u + m], xx[m], dot);
-                        }
-                    }
-                    if (live && w.out_f32) {
-                        float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(w.out) + at + 32 * p);
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) to[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-                    } else if (live) {
-                        uint4 *to = reinterpret_cast<uint4 *>(static_cast<bf16 *>(w.out) + at + 32 * p);
+                }
+                if (w.out_f32) {
+                    // (heads that share keys: each one's gradient in fp32, to be summed) a row's piece at a time
+                    if (lane < live) {
+                        float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(w.out) + b * w.os[0] +
+                                                                (tw + lane) * w.os[1] + h * w.os[2] + col + 16 * p);
 #pragma unroll
                         for (int u = 0; u < 4; ++u)
-                            to[u] = make_uint4(pack_bf16(o[8 * u], o[8 * u + 1]), pack_bf16(o[8 * u + 2], o[8 * u + 3]),
-                                               pack_bf16(o[8 * u + 4], o[8 * u + 5]), pack_bf16(o[8 * u + 6], o[8 * u + 7]));
+                            to[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
                     }
+                    __syncwarp();
+                } else {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        *own(2 * p + u) =
+                            make_uint4(pack_bf16(o[8 * u], o[8 * u + 1]), pack_bf16(o[8 * u + 2], o[8 * u + 3]),
+                                       pack_bf16(o[8 * u + 4], o[8 * u + 5]), pack_bf16(o[8 * u + 6], o[8 * u + 7]));
                 }
-                // heads of 128: each half of the columns leaves its own product
-                if (w.row_dot && live)
-                    w.row_dot[(NH == 2 ? 0 : hh * set.B * set.T * set.H) + (b * set.T + t) * set.H + h] = dot;
             }
+            if (!w.out_f32) {
+                __syncwarp();
+                bf16 *to = static_cast<bf16 *>(w.out) + b * w.os[0] + (tw + lrow) * w.os[1] + h * w.os[2] + col + 8 * lch;
+                const int64_t step = 4 * w.os[1];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (4 * u + lrow < live) *reinterpret_cast<uint4 *>(to + u * step) = *line(u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mb_arrive(&k_empty[it % L::NK]);
+            // heads of 128: each half of the columns leaves its own product
+            if (w.row_dot && lane < live)
+                w.row_dot[(NH == 2 ? 0 : hh * set.B * set.T * set.H) + (b * set.T + tw + lane) * set.H + h] = dot;
         }
-    } else if (warp < 16) {
+    } else {
         // ------------------------------------------------ rows of the state
         const int grp = (warp - 8) >> 2, dk = 32 * (warp & 3) + lane;
         const int hp = NH == 2 ? dk >> 6 : 0, h = h0 + hp;
@@ -358,35 +443,97 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool tr = false;
             if (!state_only && live) {
                 if (nseg > 1)
-                    in = w.seg_in + (ln * nseg + seg) * D * D, tr = w.seg_t;
+                    in = w.seg_in + (ln * nseg + seg) * D * D;
                 else if (w.s_in)
                     in = w.s_in + ln * D * D, tr = w.s_in_t;
             }
+            if (in == nullptr) {
 #pragma unroll
-            for (int u = 0; u < SC; ++u)
-                s[u] = in == nullptr ? 0.f : tr ? in[(col + u) * D + row] : in[row * D + col + u];
-        }
-        auto put_state = [&](float *to, bool tr) {
-            if (!live) return;
-            if (tr) {
+                for (int u = 0; u < SC; ++u) s[u] = 0.f;
+            } else if (tr) {
 #pragma unroll
-                for (int u = 0; u < SC; ++u) to[(col + u) * D + row] = s[u];
+                for (int u = 0; u < SC; ++u) s[u] = in[(col + u) * D + row];
             } else {
 #pragma unroll
-                for (int u = 0; u < SC; u += 4)
-                    *reinterpret_cast<float4 *>(to + row * D + col + u) = make_float4(s[u], s[u + 1], s[u + 2], s[u + 3]);
+                for (int u = 0; u < SC; u += 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(in + row * D + col + u);
+                    s[u] = x.x, s[u + 1] = x.y, s[u + 2] = x.z, s[u + 3] = x.w;
+                }
             }
-        };
-        auto checkpoint = [&](int c) {
-            if (w.ckpt && ((c + 1) % (kAttnSpan / C) == 0 || (c + 1) * C >= T))
-                put_state(w.ckpt + (ln * set.spans + c / (kAttnSpan / C)) * D * D, false);
-        };
-        // element (j, dk) of the keys' tile
-        const uint32_t koff = uint32_t(dk >> 6) * kPanel + (dk & 7) * 2, kch = (dk & 63) >> 3;
+        }
+        // The keys' tile is read transposed: ldmatrix gives thread t of a warp the
+        // steps 2 (t % 4), + 1 of key row t / 4 (of 8 x 8 blocks), which is the
+        // place of that pair in TMEM's 16-lane shape of 128 bits.  Address of this
+        // thread's row of the four blocks (16 key rows x 16 steps):
+        const int lr = ((lane >> 4) << 3) + (lane & 7);        // step within the group
+        const int lc = ((32 * (warp & 3)) & 63) / 8 + ((lane >> 3) & 1);
+        const uint32_t kbase = smem_addr(sm + L::k) + uint32_t((32 * (warp & 3)) >> 6) * kPanel + lr * 128;
+        const uint32_t kx0 = uint32_t((lc ^ (lr & 7)) << 4), kx1 = uint32_t(((lc + 2) ^ (lr & 7)) << 4);
         bool ok = true;
-        for (int it = 0; it < n && ok; ++it) {
-            const int c = chunk_of(it);
-            if (rev) checkpoint(c);
+#pragma unroll 1
+        for (int it = 0; ok; ++it) {
+            // States that are kept: at a span's end (in reverse that is the state before the
+            // chunk is walked), and at the walk's end.
+            const int ce = rev ? chunk_of(it) : chunk_of(it - 1);
+            const bool mark = !state_only && w.ckpt != nullptr && (rev ? it < n : it > 0) &&
+                              ((ce + 1) % (kAttnSpan / C) == 0 || (ce + 1) * C >= T);
+            if (live && (mark || it == n)) {
+#pragma unroll 1
+                for (int k = 0; k < 2; ++k) {
+                    float *to = nullptr;
+                    if (k == 0) {
+                        if (mark) to = w.ckpt + (ln * set.spans + ce / (kAttnSpan / C)) * D * D;
+                    } else if (it == n) {
+                        if (state_only)
+                            to = w.seg_out + (ln * nseg + seg) * D * D;
+                        else if (w.s_out && seg == (rev ? 0 : nseg - 1))
+                            to = w.s_out + ln * D * D;
+                    }
+                    if (to == nullptr) continue;
+#pragma unroll
+                    for (int u = 0; u < SC; u += 4)
+                        *reinterpret_cast<float4 *>(to + row * D + col + u) =
+                            make_float4(s[u], s[u + 1], s[u + 2], s[u + 3]);
+                }
+            }
+            __syncwarp();
+            if (it == n) break;
+            if (!(ok = wwait(&k_full[it % L::NK], it / L::NK) && wwait(g_full, it))) break;
+            const uint32_t kt = kbase + (it % L::NK) * kTile;
+            const float *wt = Gh + hp * 4 * C + 3 * C + 2 * (lane & 3);
+            const float decay = total[hp];
+            // the chunk's weighted keys, half of it at a time, the groups of 16 steps shared
+            // between the two warpgroups
+#pragma unroll 1
+            for (int i = 0; i < NG / 2; ++i) {
+                const int gi = (i >> 1) * (NG / 2) + grp * (NG / 4) + (i & 1);
+                const float2 w0 = *reinterpret_cast<const float2 *>(wt + gi * GT);
+                const float2 w1 = *reinterpret_cast<const float2 *>(wt + gi * GT + 8);
+#pragma unroll 1
+                for (int x = 0; x < 2; ++x) {  // key rows 0..15 and 16..31 of the warp
+                    uint32_t r[4], t[3][4];
+                    ldmatrix_x4_trans(kt + gi * (GT * 128) + (x ? kx1 : kx0), r);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        uint32_t a[3];
+                        split<3>(__fmul2_rn(make_float2(bf_lo(r[m]), bf_hi(r[m])), m < 2 ? w0 : w1), a);
+                        t[0][m] = a[0], t[1][m] = a[1], t[2][m] = a[2];
+                    }
+#pragma unroll
+                    for (int m = 0; m < 3; ++m)
+                        tmem_put_16x8(tq + (uint32_t(16 * x) << 16) + M::W + 64 * m + 8 * gi, t[m]);
+                }
+                if (i & 1) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mb_arrive(&w_full[i >> 1]);
+                }
+            }
+            if (lane == 0) {
+                mb_arrive(g_empty);
+                if (state_only) mb_arrive(&k_empty[it % L::NK]);
+            }
             if (!state_only) {
                 // the state as the operand of Q S (its reader of the chunk before is done)
                 if (it > 0 && !(ok = wwait(qs_done, it - 1))) break;
@@ -395,10 +542,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int u = 0; u < SC; u += 8) {
                     uint32_t t0[TERMS], t1[TERMS], t2[TERMS], t3[TERMS];
-                    split<TERMS>(s[u], s[u + 1], t0);
-                    split<TERMS>(s[u + 2], s[u + 3], t1);
-                    split<TERMS>(s[u + 4], s[u + 5], t2);
-                    split<TERMS>(s[u + 6], s[u + 7], t3);
+                    split<TERMS>(make_float2(s[u], s[u + 1]), t0);
+                    split<TERMS>(make_float2(s[u + 2], s[u + 3]), t1);
+                    split<TERMS>(make_float2(s[u + 4], s[u + 5]), t2);
+                    split<TERMS>(make_float2(s[u + 6], s[u + 7]), t3);
 #pragma unroll
                     for (int m = 0; m < TERMS; ++m)
                         *reinterpret_cast<uint4 *>(base + m * L::sterm + (((ch0 + u / 8) ^ (dk & 7)) << 4)) =
@@ -408,135 +555,126 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mb_arrive(s_ready);
             }
-            if (!(ok = wwait(&k_full[it % L::NK], it / L::NK) && wwait(g_full, it))) break;
-            const unsigned char *kt = sm + L::k + (it % L::NK) * kTile + koff;
-            const float *wt = Gh + hp * 4 * C + 3 * C;
-            const float decay = total[hp];
-            for (int i = 0; i < NG / 2 && ok; ++i) {
-                const int gi = 2 * i + grp, use = it * (NG / 2) + i;
-                uint32_t t[3][GT / 2];
-#pragma unroll
-                for (int u = 0; u < GT; u += 4) {
-                    const float4 ww = *reinterpret_cast<const float4 *>(wt + gi * GT + u);
-                    float x[4];
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const int j = gi * GT + u + m;
-                        x[m] = __uint_as_float(
-                            uint32_t(*reinterpret_cast<const uint16_t *>(kt + j * 128 + ((kch ^ (j & 7)) << 4))) << 16);
-                    }
-                    uint32_t a[3], d[3];
-                    split<3>(x[0] * ww.x, x[1] * ww.y, a);
-                    split<3>(x[2] * ww.z, x[3] * ww.w, d);
-#pragma unroll
-                    for (int m = 0; m < 3; ++m) t[m][u / 2] = a[m], t[m][u / 2 + 1] = d[m];
-                }
-                if (use > 0 && !(ok = wwait(&w_empty[grp], use - 1))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int m = 0; m < 3; ++m) tmem_put8(tq + kW + 24 * grp + 8 * m, t[m]);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mb_arrive(&w_full[grp]);
-            }
-            if (!ok) break;
-            if (lane == 0) mb_arrive(&k_empty[it % L::NK]), mb_arrive(g_empty);
             if (!(ok = wwait(kv_done, it))) break;
             tc_fence_after();
 #pragma unroll
             for (int u = 0; u < SC; u += 32) {
                 float x[32];
-                tmem_ld32(tq + kKV + (NH == 2 ? 64 * hp : 0) + col + u, x);
+                tmem_ld32(tq + M::KV + (NH == 2 ? 64 * hp : 0) + col + u, x);
 #pragma unroll
-                for (int m = 0; m < 32; ++m) s[u + m] = fmaf(decay, s[u + m], x[m]);
+                for (int m = 0; m < 32; m += 2) {
+                    const float2 y = __ffma2_rn(make_float2(decay, decay), make_float2(s[u + m], s[u + m + 1]),
+                                                make_float2(x[m], x[m + 1]));
+                    s[u + m] = y.x, s[u + m + 1] = y.y;
+                }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mb_arrive(kv_free);
-            if (!rev) checkpoint(c);
         }
-        if (ok) {
-            if (state_only)
-                put_state(w.seg_out + (ln * nseg + seg) * D * D, w.seg_t);
-            else if (w.s_out && seg == (rev ? 0 : nseg - 1))
-                put_state(w.s_out + ln * D * D, false);
-        }
+    }
+    } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLast));
+    if (!ok0) {
+        // nothing was started
     } else if (warp == 16) {
         // ------------------------------------------------ the products
-        if (lane == 0) {
+        if (elect_one()) {
             constexpr uint32_t id_k = umma_idesc_bf16(128, 128, false), id_mn = umma_idesc_bf16(128, 128, true);
             constexpr uint32_t id_o = umma_idesc_bf16(128, D, true);
-            const uint32_t sS = smem_addr(sm), sK = smem_addr(sm + L::k), sQ = smem_addr(sm + L::q),
-                           sV = smem_addr(sm + L::v);
+            // Descriptors hold addresses in units of 16 bytes: what is issued is one of these
+            // plus a constant, since a longer sum between two products costs more time than a
+            // product takes (64 cycles at N = 128).
+            const uint64_t dK = umma_desc_k(smem_addr(sm + L::k)), dQ = umma_desc_k(smem_addr(sm + L::q));
+            const uint64_t dV = umma_desc_mn(smem_addr(sm + L::v), kPanel), dS = umma_desc_mn(smem_addr(sm), kPanel);
+            constexpr int KS = D / 16;
+            // K-major step ks of head hp: 32 bytes on in the rows, the next panel after four
+            auto koff = [](int ks) { return uint64_t(((ks >> 2) * kPanel + (ks & 3) * 32) >> 4); };
             auto qk = [&](int it, int hp) {
-                const uint32_t q = sQ + (it % L::NQ) * kTile, k = sK + (it % L::NK) * kTile;
+                const uint64_t q = dQ + uint64_t(((it % L::NQ) * kTile + hp * kPanel) >> 4);
+                const uint64_t k = dK + uint64_t(((it % L::NK) * kTile + hp * kPanel) >> 4);
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = uint32_t(NH == 2 ? hp : ks >> 2) * kPanel + uint32_t(ks & 3) * 32;
-                    umma_bf16_ss(tm + kA, umma_desc_k(q + off), umma_desc_k(k + off), id_k, ks > 0);
-                }
+                for (int ks = 0; ks < KS; ++ks) umma_bf16_ss(tm + M::A, q + koff(ks), k + koff(ks), id_k, ks > 0);
                 umma_commit(a_done);
-                if (hp == NH - 1) umma_commit(&k_empty[it % L::NK]);
             };
             auto qs = [&](int it) {
-                const uint32_t q = sQ + (it % L::NQ) * kTile;
-                for (int hp = 0; hp < NH; ++hp)
+#pragma unroll 1
+                for (int hp = 0; hp < NH; ++hp) {
+                    const uint64_t q = dQ + uint64_t(((it % L::NQ) * kTile + hp * kPanel) >> 4);
+#pragma unroll 1
+                    for (int m = 0; m < TERMS; ++m) {
+                        const uint64_t st = dS + uint64_t((m * L::sterm + hp * 8192) >> 4);
 #pragma unroll
-                    for (int m = 0; m < TERMS; ++m)
-#pragma unroll
-                        for (int ks = 0; ks < D / 16; ++ks) {
-                            const uint32_t off = uint32_t(NH == 2 ? hp : ks >> 2) * kPanel + uint32_t(ks & 3) * 32;
-                            umma_bf16_ss(tm + kO + 64 * hp, umma_desc_k(q + off),
-                                         umma_desc_mn(sS + m * L::sterm + hp * 8192 + ks * 2048, kPanel), id_o,
-                                         m + ks > 0);
-                        }
+                        for (int ks = 0; ks < KS; ++ks)
+                            umma_bf16_ss(tm + M::O + 64 * hp, q + koff(ks), st + uint64_t(ks * 128), id_o, m + ks > 0);
+                    }
+                }
                 umma_commit(qs_done);
+            };
+            auto kv = [&](int it, int half) {
+                const uint64_t v = dV + uint64_t(((it % L::NV) * kTile + half * (NG / 2) * 2048) >> 4);
+                const uint32_t a = tm + M::W + half * (NG / 2) * 8;
+#pragma unroll
+                for (int i = 0; i < NG / 2; ++i)
+#pragma unroll
+                    for (int m = 0; m < 3; ++m)
+                        umma_bf16_ts(tm + M::KV, a + 64 * m + 8 * i, v + uint64_t(i * 128), id_mn, half + i + m > 0);
+            };
+            auto pv = [&](int it, int hp) {
+                const uint64_t v = dV + uint64_t(((it % L::NV) * kTile + hp * kPanel) >> 4);
+#pragma unroll 1
+                for (int m = 0; m < TERMS; ++m)
+#pragma unroll
+                    for (int ks = 0; ks < C / 16; ++ks)
+                        umma_bf16_ts(tm + M::O + 64 * hp, tm + M::P + 64 * m + 8 * ks, v + uint64_t(ks * 128), id_o, true);
+                umma_commit(o_done);
             };
             bool ok = true;
             for (int it = 0; it < n && ok; ++it) {
                 if (!state_only) {
                     if (!(ok = wait(&k_full[it % L::NK], it / L::NK) && wait(&q_full[it % L::NQ], it / L::NQ))) break;
+                    if (it > 0 && !(ok = wait(o_free, it - 1))) break;
+                    tc_fence_after();
                     qk(it, 0);
-                    if (!(ok = wait(s_ready, it) && (it == 0 || wait(o_free, it - 1)))) break;
+                }
+                // the first half of the state's product while P is made of A
+                if (!(ok = wait(&v_full[it % L::NV], it / L::NV) && (it == 0 || wait(kv_free, it - 1)) &&
+                           wait(&w_full[0], it)))
+                    break;
+                tc_fence_after();
+                kv(it, 0);
+                if (M::over_a && !state_only) {
+                    if (!(ok = wait(p_ready, it) && wait(s_ready, it))) break;
                     tc_fence_after();
                     qs(it);
-                    if (NH == 1) umma_commit(&q_empty[it % L::NQ]);
+                    umma_commit(&q_empty[it % L::NQ]);
                 }
-                if (!(ok = wait(&v_full[it % L::NV], it / L::NV) && (it == 0 || wait(kv_free, it - 1)))) break;
-                const uint32_t v = sV + (it % L::NV) * kTile;
-                for (int gi = 0; gi < NG && ok; ++gi) {
-                    const int buf = gi & 1;
-                    if (!(ok = wait(&w_full[buf], it * (NG / 2) + (gi >> 1)))) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int m = 0; m < 3; ++m)
-                        umma_bf16_ts(tm + kKV, tm + kW + 24 * buf + 8 * m, umma_desc_mn(v + gi * 2048, kPanel), id_mn,
-                                     gi + m > 0);
-                    umma_commit(&w_empty[buf]);
-                }
-                if (!ok) break;
+                if (!(ok = wait(&w_full[1], it))) break;
+                tc_fence_after();
+                kv(it, 1);
                 umma_commit(kv_done);
-                if (state_only) {
-                    umma_commit(&v_empty[it % L::NV]);
-                    continue;
-                }
-                for (int hp = 0; hp < NH && ok; ++hp) {
-                    if (hp > 0) {
-                        qk(it, hp);
-                        umma_commit(&q_empty[it % L::NQ]);
+                if (!state_only) {
+                    if (!M::over_a) {
+                        if (!(ok = wait(kv_free, it) && wait(s_ready, it))) break;
+                        tc_fence_after();
+                        qs(it);
+                        if (NH == 1) umma_commit(&q_empty[it % L::NQ]);
+                        if (!(ok = wait(p_ready, it * NH))) break;
+                        tc_fence_after();
+                        if (NH == 2 && TERMS == 1) qk(it, 1);  // P stands beside A
                     }
-                    if (!(ok = wait(p_ready, it * NH + hp))) break;
+                    if (!(ok = wait(o_ready, it))) break;
                     tc_fence_after();
-#pragma unroll
-                    for (int m = 0; m < TERMS; ++m)
-#pragma unroll
-                        for (int ks = 0; ks < C / 16; ++ks)
-                            umma_bf16_ts(tm + kO + 64 * hp, tm + kP<TERMS> + 64 * m + 8 * ks,
-                                         umma_desc_mn(v + hp * kPanel + ks * 2048, kPanel), id_o, true);
-                    umma_commit(o_done);
+                    pv(it, 0);
+                    if (NH == 2) {
+                        if (TERMS != 1) qk(it, 1);             // ... or over it: after the product with P
+                        umma_commit(&q_empty[it % L::NQ]);
+                        if (!(ok = wait(p_ready, it * NH + 1))) break;
+                        tc_fence_after();
+                        pv(it, 1);
+                    }
                 }
-                if (ok) umma_commit(&v_empty[it % L::NV]);
+                umma_commit(&v_empty[it % L::NV]);
             }
             // whatever was issued completes before TMEM and shared memory are released
             if (!ok) {
@@ -548,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncwarp();
-    } else {
+    } else if (warp == 17) {
         // ------------------------------------------------ tiles and decays
         const float L2E = 1.4426950408889634f, L2E_LO = 1.9259629911266175e-8f;
         float *arr = reinterpret_cast<float *>(sm + L::arr);
@@ -664,6 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     }
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == 16) {
@@ -687,8 +826,17 @@ template <int D, int TERMS>
 cudaError_t go(const AttnMaps &maps, const AttnSet &set, int nwalks, bool state_only, cudaStream_t s) {
     using L = Smem<D, TERMS>;
     const void *fn = (const void *)attn_mma_kernel<D, TERMS>;
-    const cudaError_t e = ensure_smem_attr(fn, int(L::bytes));
+    cudaError_t e = ensure_smem_attr(fn, int(L::bytes));
     if (e != cudaSuccess) return e;
+    // the split of the registers counts on this many at launch: with fewer the
+    // warpgroups that ask for more would wait for good
+    static std::atomic<int> regs{0};
+    if (regs.load() == 0) {
+        cudaFuncAttributes a;
+        if ((e = cudaFuncGetAttributes(&a, fn)) != cudaSuccess) return e;
+        regs.store(a.numRegs);
+    }
+    if (regs.load() != kRegs) return cudaErrorInvalidDeviceFunction;
     const dim3 grid(unsigned(set.B * ((set.H + L::NH - 1) / L::NH) * set.nseg), unsigned(nwalks));
     attn_mma_kernel<D, TERMS><<<grid, kThreads, L::bytes, s>>>(maps, set, state_only);
     return cudaGetLastError();

@@ -60,14 +60,16 @@ __device__ __forceinline__ uint4 pack(const float (&v)[8]) {
 }
 
 // e^x as a sum of two fp32 (relative error about 1e-8), for factors that are
-// multiplied together hundreds of times: x = n log 2 + y with |y| <= log(2) / 2,
-// e^y = 1 + y + (Taylor's series from y^2 / 2), y and the sum in two parts.
+// multiplied together hundreds of times: x = n log 2 + y with |y| <= log(2) / 2
+// (log 2 as 11357 / 2^14 and the rest, so that n times the first is exact: Cody
+// and Waite's reduction), e^y = 1 + y + (Taylor's series from y^2 / 2), y and the
+// sum in two parts.
 __device__ __forceinline__ void exp_two(float x, float &hi, float &lo) {
     if (!(x > -100.f && x < 80.f)) {  // zero, overflow, NaN: nothing to refine
         hi = expf(x), lo = 0.f;
         return;
     }
-    const float LN2_HI = 0.693145751953125f, LN2_LO = 1.42860682030941723e-6f;  // log 2: 16 bits, and the rest
+    const float LN2_HI = 11357.f / 16384.f, LN2_LO = -2.9088971304690582e-5f;
     const float n = rintf(x * 1.44269504f);
     const float a = fmaf(-n, LN2_HI, x);  // exact
     const float b = -n * LN2_LO;
