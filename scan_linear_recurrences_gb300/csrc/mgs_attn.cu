@@ -459,10 +459,13 @@ AttnSet set_of(const mgs_attention_shape &sh, const Plan &p, const float *g, con
 cudaError_t run_walks(AttnSet &set, int walks, const mgs_attention_shape &sh, const Plan &p, Carve &ws,
                       cudaStream_t s) {
     cudaError_t e;
-    // the gradients' walks feed the decay's, whose sums want every digit of fp32
+    // Of the gradients' walks the first two feed the decay's, whose sums want every
+    // digit of fp32; dv, and the attention itself, are rounded to the type.
     auto walk = [&](bool state_only) {
-        return p.mma ? launch_attn_mma(set, walks, sh.D, walks == 1 || state_only ? 1 : 3, state_only, s)
-                     : launch_attn_rec(set, walks, sh.D, sh.dtype, state_only, s);
+        if (!p.mma) return launch_attn_rec(set, walks, sh.D, sh.dtype, state_only, s);
+        if (walks == 1 || state_only) return launch_attn_mma(set, 0, walks, sh.D, 1, state_only, s);
+        const cudaError_t e = launch_attn_mma(set, 0, 2, sh.D, 3, false, s);
+        return e != cudaSuccess ? e : launch_attn_mma(set, 2, 1, sh.D, 1, false, s);
     };
     if (set.nseg > 1) {
         for (int i = 0; i < walks; ++i) set.w[i].seg_in = set.w[i].seg_out = ws.take<float>(seg_bytes(p, sh.D));

@@ -24,8 +24,9 @@
 //          in registers, the state as an operand; 8..11 and 12..15 share the
 //          steps' groups and the state's columns
 //   16     one thread issues the products
-//   17     one thread loads tiles by TMA; the warp sums g
-//   18, 19 fill the last warpgroup
+//   17     one thread loads tiles by TMA
+//   18     sums of g
+//   19     fills the last warpgroup
 #include "mgs_launch.h"
 #include "mgs_lm.h"
 #include "mgs_num.cuh"
@@ -41,22 +42,22 @@ constexpr int C = 128;
 constexpr int kTile = 32768, kPanel = 16384;   // a tile: two panels of 128 rows x 64 bf16
 constexpr int kThreads = 20 * 32;              // five warpgroups
 // Registers a thread: the kernel is launched with kRegs for each; the last
-// warpgroup gives up what the four others take (104 x 4 + 64 = 96 x 5).
-constexpr int kRegs = 96, kRegsWork = 104, kRegsLast = 64;
-static_assert(4 * kRegsWork + kRegsLast <= 5 * kRegs, "within the registers of the launch");
+// warpgroup gives up what the two of the rows take more.
+constexpr int kRegs = 96, kRegsRows = 112, kRegsLast = 64;
+static_assert(2 * kRegsRows + 2 * kRegs + kRegsLast <= 5 * kRegs, "within the registers of the launch");
 constexpr int GT = 16;                         // steps of a group of weighted keys: one K = 16 product
 constexpr int NG = C / GT;
 
 // TMEM columns (all 512):
 //   A 0..127 and P behind it (one term) or over it (three: A is read whole before);
-//   the state's product 192..319; the weighted keys of a chunk, three terms of 64
-//   columns, 320..511.  O has no columns of its own: with one term and one head
-//   it takes A's place once P is made of it, else the place of the state's
-//   product once that is in registers.
+//   X 192..319: Q S, then (once the rows have it in registers) the state's product;
+//   the weighted keys of a chunk, three terms of 64 columns, 320..511.
+// P V goes where it finds room: with one term and one head in A's place (P has been
+// made of it), else in X, once the state's product is in registers.
 template <int D, int TERMS>
 struct Tmem {
     static constexpr bool over_a = D == 128 && TERMS == 1;
-    static constexpr uint32_t A = 0, P = TERMS == 1 ? 128 : 0, KV = 192, O = over_a ? 0 : 192, W = 320;
+    static constexpr uint32_t A = 0, P = TERMS == 1 ? 128 : 0, X = 192, O = over_a ? 0 : 192, W = 320;
 };
 
 template <int D, int TERMS>
@@ -73,7 +74,7 @@ struct Smem {
 };
 
 struct AttnMaps {
-    CUtensorMap q[3], k[3], v[3];
+    CUtensorMap q[3], k[3], v[3], o[3];  // loads: 64 columns x 128 steps; stores: x 32 steps
 };
 
 __device__ __forceinline__ void mb_arrive(uint64_t *bar) {
@@ -94,6 +95,13 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4
                  : "r"(addr)
                  : "memory");
 }
+// Tiled store shared -> global, a bulk group of the issuing thread; coordinates not negative
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, int x, int y, int z, int w, const void *src) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(src))
+                 : "memory");
+}
 // 16 lanes x 8 columns: thread t holds, of lanes t / 4 and t / 4 + 8, column
 // t % 4 in r[0], r[1] and column 4 + t % 4 in r[2], r[3]
 __device__ __forceinline__ void tmem_put_16x8(uint32_t taddr, const uint32_t (&r)[4]) {
@@ -109,24 +117,42 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// Waits for a phase; false once the wait gives up or another role has.  The
-// clock is read every 64th try only: the read itself takes long.
-__device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity, volatile int *abort_word, DevCtl ctl) {
-    uint64_t t0 = 0;
+// Up to `tries` tries at a phase, in the fewest instructions: the waiting warps'
+// tries take issue slots from the working ones.
+__device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, uint32_t tries) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, %3;\n\t"
+        "AGAIN:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra DONE;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "@q bra AGAIN;\n\t"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(tries)
+        : "memory");
+    return ok != 0;
+}
+
+// Waits for a phase; false once the wait gives up or another role has.
+__device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity, volatile int *abort_word,
+                                             const DevCtl &ctl) {
+    const uint32_t at = smem_addr(bar);
+    if (mbar_poll(at, parity, 1024)) return true;
+    const uint64_t t0 = global_ns();
 #pragma unroll 1
-    for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 63u) != 0) continue;
-        if (*abort_word != 0) return false;
-        const uint64_t t = global_ns();
-        if (t0 == 0) {
-            t0 = t;
-        } else if (t - t0 > ctl.timeout_ns) {
+    while (*abort_word == 0) {
+        if (mbar_poll(at, parity, 1024)) return true;
+        if (global_ns() - t0 > ctl.timeout_ns) {
             record_error(ctl, ERR_MBAR_TIMEOUT);
             *abort_word = 1;
-            return false;
         }
     }
+    return false;
 }
 
 // x as a sum of TERMS bf16 pairs (packed: x.x in the low half)
@@ -149,21 +175,6 @@ __device__ __forceinline__ void add2(float &h, float &l, float a, float b) {
     l = lo - (h - s);
 }
 
-// 16 columns of P as TERMS packed terms, 64 TMEM columns apart
-template <int TERMS>
-__device__ __forceinline__ void put_terms(uint32_t at, const float (&x)[16]) {
-    uint32_t pk[TERMS][8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        uint32_t s[TERMS];
-        split<TERMS>(make_float2(x[2 * u], x[2 * u + 1]), s);
-#pragma unroll
-        for (int m = 0; m < TERMS; ++m) pk[m][u] = s[m];
-    }
-#pragma unroll
-    for (int m = 0; m < TERMS; ++m) tmem_put8(at + 64 * m, pk[m]);
-}
-
 template <int D, int TERMS>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_mma_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnSet set, int state_only) {
@@ -184,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the walk's description from shared memory: parameters indexed by blockIdx
     // would be read through the global path
     const AttnWalk &w = *reinterpret_cast<const AttnWalk *>(sm + L::walk);
-    const bool rev = set.w[blockIdx.y].rev != 0;
+    const bool rev = set.w[set.first + blockIdx.y].rev != 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nseg = set.nseg, units = int((set.H + NH - 1) / NH);
     const int unit = int(blockIdx.x) / nseg, seg = int(blockIdx.x) - unit * nseg;
@@ -197,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     static_assert(sizeof(AttnWalk) % 4 == 0 && sizeof(AttnWalk) <= 4 * kThreads, "a word a thread");
     if (tid < int(sizeof(AttnWalk) / 4))
-        reinterpret_cast<uint32_t *>(sm + L::walk)[tid] = reinterpret_cast<const uint32_t *>(&set.w[blockIdx.y])[tid];
+        reinterpret_cast<uint32_t *>(sm + L::walk)[tid] = reinterpret_cast<const uint32_t *>(&set.w[set.first + blockIdx.y])[tid];
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&k_full[i], 1), mbar_init(&q_full[i], 1), mbar_init(&v_full[i], 1);
@@ -227,30 +238,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the same by a whole warp, whose lanes go on together
     auto wwait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
     auto chunk_of = [&](int i) { return rev ? c1 - 1 - i : c0 + i; };
-    const float *Gh = reinterpret_cast<const float *>(sm + L::arr);  // [NH][4][C]: G high, G low, column factor, weight
+    const float *Gh = reinterpret_cast<const float *>(sm + L::arr);  // [NH][4][C]: G (-G in reverse) high and low, column factor, weight
     const bool ok0 = *abort_word == 0;
     if (!ok0 && tid == 0) record_error(ctl, ERR_MBAR_TIMEOUT);
 
-    if (warp < 16) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsWork));
-    if (!ok0) {
-        // nothing was started
-    } else if (warp < 8) {
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRows));
         // ------------------------------------------------ rows of the chunk
         const int hh = warp >> 2, wb = warp & 3, i = 32 * wb + lane;
-        const float sgn = rev ? -1.f : 1.f, kvs = w.kv_scale, os = w.o_scale;
+        const float kvs = w.kv_scale, os = w.o_scale;
         const int isgn = rev ? -1 : 1;
+        const uint32_t in = rev ? ~0u << lane : ~0u >> (31 - lane);  // columns of the diagonal's block that count
         // the output's head, and the weights of its rows of Q S
         const int h = NH == 2 ? h0 + hh : h0, col = NH == 2 ? 0 : 64 * hh;
         const float *Go = Gh + (NH == 2 ? hh * 4 * C : 0);
         const int lrow = lane >> 3, lch = lane & 7;  // whole lines: 4 rows of 8 pieces of 16 bytes at a time
-        bool ok = true;
+        bool ok = ok0;
 #pragma unroll 1
         for (int it = 0; it < (state_only ? 0 : n) && ok; ++it) {
             const int c = chunk_of(it);
             if (!(ok = wwait(g_full, it))) break;
-            const float ri = rev ? ex2_approx((Go[C - 1] - Go[i]) + (Go[2 * C - 1] - Go[C + i]))
-                                 : ex2_approx(Go[i] + Go[C + i]);
+            float o1[64];  // Q S, scaled by rows: the part of the output that comes from the state
+            const float ri = os * ex2_approx(rev ? (Go[i] - Go[C - 1]) + (Go[C + i] - Go[2 * C - 1]) : Go[i] + Go[C + i]);
+            auto from_state = [&]() {
+                if (!wwait(qs_done, it)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    float x[32];
+                    tmem_ld32(tq + M::X + 64 * hh + 32 * p, x);
+#pragma unroll
+                    for (int u = 0; u < 32; u += 2) {
+                        const float2 y = __fmul2_rn(make_float2(x[u], x[u + 1]), make_float2(ri, ri));
+                        o1[32 * p + u] = y.x, o1[32 * p + u + 1] = y.y;
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mb_arrive(o_ready);
+                return true;
+            };
+            if (!(ok = from_state())) break;
 #pragma unroll 1
             for (int hp = 0; hp < NH; ++hp) {
                 const float *G = Gh + hp * 4 * C;
@@ -275,20 +303,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int u = 0; u < 16; u += 4) {
                             const float4 ah = *reinterpret_cast<const float4 *>(G + j0 + u);
-                            const float4 al = *reinterpret_cast<const float4 *>(G + C + j0 + u);
-                            const float e[4] = {(gi - ah.x) + (gl - al.x), (gi - ah.y) + (gl - al.y),
-                                                (gi - ah.z) + (gl - al.z), (gi - ah.w) + (gl - al.w)};
+                            float e[4] = {gi - ah.x, gi - ah.y, gi - ah.z, gi - ah.w};
+                            if (TERMS > 1) {
+                                const float4 al = *reinterpret_cast<const float4 *>(G + C + j0 + u);
+                                e[0] += gl - al.x, e[1] += gl - al.y, e[2] += gl - al.z, e[3] += gl - al.w;
+                            }
 #pragma unroll
                             for (int m = 0; m < 4; ++m) {
-                                // the mask as bits: a choice would become a branch for each element
-                                const float y = v[u + m] * (ex2_approx(sgn * e[m]) * kvs);
-                                const int past = isgn * (j0 + u + m - i);  // > 0: masked
-                                v[u + m] = __uint_as_float(__float_as_uint(y) & uint32_t((past - 1) >> 31));
+                                // computed whether or not it is masked: no branch for each element
+                                const float y = v[u + m] * (ex2_approx(e[m]) * kvs);
+                                v[u + m] = (in >> ((j0 & 31) + u + m)) & 1u ? y : 0.f;
                             }
                         }
                     } else {
                         const int ref = 32 * jb + (rev ? 0 : 31);
-                        const float f = ex2_approx(sgn * ((gi - G[ref]) + (gl - G[C + ref]))) * kvs;
+                        const float f = ex2_approx((gi - G[ref]) + (gl - G[C + ref])) * kvs;
 #pragma unroll
                         for (int u = 0; u < 16; u += 4) {
                             const float4 a = *reinterpret_cast<const float4 *>(G + 2 * C + j0 + u);
@@ -311,47 +340,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_put8(tq + M::P + j0 / 2, pk);
                     }
                 } else {
-                    // P's terms take A's place: all of A is read before any is written
-                    float v[4][16];
+                    // P's terms take A's place, 32 steps j at a time (half of them this warp's): all
+                    // of those columns of A are read before the first two terms go there; the third
+                    // has columns of its own.
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        float v[16];
+                        piece(32 * q + 16 * hh, v);
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mb_arrive(a_read);
+                        if (!(ok = wwait(a_read, 4 * ev + q))) break;
+                        tc_fence_after();
+                        uint32_t pk[3][8];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) piece(64 * hh + 16 * q, v[q]);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mb_arrive(a_read);
-                    if (!(ok = wwait(a_read, ev))) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) put_terms<TERMS>(tq + M::P + 32 * hh + 8 * q, v[q]);
+                        for (int u = 0; u < 8; ++u) {
+                            uint32_t t[3];
+                            split<3>(make_float2(v[2 * u], v[2 * u + 1]), t);
+                            pk[0][u] = t[0], pk[1][u] = t[1], pk[2][u] = t[2];
+                        }
+                        tmem_put8(tq + M::P + 32 * q + 8 * hh, pk[0]);
+                        tmem_put8(tq + M::P + 32 * q + 16 + 8 * hh, pk[1]);
+                        tmem_put8(tq + M::P + 128 + 16 * q + 8 * hh, pk[2]);
+                    }
+                    if (!ok) break;
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mb_arrive(p_ready);
-                if (hp == 0) {
-                    // O = Q S scaled by rows, in place; P V is added to it
-                    if (!(ok = wwait(qs_done, it))) break;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int j0 = 64 * hh; j0 < 64 * hh + 64; j0 += 16) {
-                        float o[16];
-                        tmem_ld16(tq + M::O + j0, o);
-                        uint32_t y[16];
-#pragma unroll
-                        for (int u = 0; u < 16; ++u) y[u] = __float_as_uint(o[u] * ri);
-                        tmem_put16(tq + M::O + j0, y);
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mb_arrive(o_ready);
-                }
             }
             if (!ok) break;
-            if (lane == 0) mb_arrive(g_empty);
-            // The output: row i, columns 64 hh .. of the tile.  A thread's row would make
-            // 32 short pieces of every store: the warp's 32 rows go through shared memory
-            // (its part of the chunk's keys, which nobody reads any more: swizzled rows of
-            // 128 bytes) and out in whole lines.  The same way in for x.
+            if (lane == 0) {
+                mb_arrive(g_empty);
+                if (it > 0) {  // the chunk before has been stored: its keys' tile is free
+                    bulk_wait_read();
+                    mb_arrive(&k_empty[(it - 1) % L::NK]);
+                }
+            }
+            // The output: row i, columns 64 hh .. of the tile.  The warp's 32 rows are staged in
+            // its part of the chunk's keys, which nobody reads any more (swizzled rows of 128
+            // bytes), and stored by TMA, which drops rows past the end.  x comes in the same
+            // place before: whole lines instead of a thread's row.
             const int64_t tw = int64_t(c) * C + 32 * wb;  // the warp's first row
             unsigned char *stage = sm + L::k + (it % L::NK) * kTile + hh * kPanel + 32 * wb * 128;
             unsigned char *mine = stage + lane * 128;
@@ -360,77 +390,78 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return reinterpret_cast<uint4 *>(stage + (4 * u + lrow) * 128 + ((lch ^ ((4 * u + lrow) & 7)) << 4));
             };
             auto own = [&](int u) { return reinterpret_cast<uint4 *>(mine + ((u ^ (lane & 7)) << 4)); };
-            uint4 xv[8];
-            if (w.row_dot) {
-                const bf16 *px = static_cast<const bf16 *>(w.x) + b * w.xs[0] + tw * w.xs[1] + (h / w.xdiv) * w.xs[2] +
-                                 col + 8 * lch;
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    xv[u] = 4 * u + lrow < live ? *reinterpret_cast<const uint4 *>(px + (4 * u + lrow) * w.xs[1])
-                                                : make_uint4(0u, 0u, 0u, 0u);
+            const bf16 *px = nullptr;
+            if (TERMS > 1 && w.row_dot) {
+                px = static_cast<const bf16 *>(w.x) + b * w.xs[0] + tw * w.xs[1] + (h / w.xdiv) * w.xs[2] + col;
+                if (lane < live) asm volatile("prefetch.global.L2 [%0];" ::"l"(px + lane * w.xs[1]));
             }
             if (!(ok = wwait(o_done, it * NH + NH - 1))) break;
             tc_fence_after();
-            if (w.row_dot) {
 #pragma unroll
-                for (int u = 0; u < 8; ++u) *line(u) = xv[u];
-                __syncwarp();
-            }
-            float dot = 0.f;
-#pragma unroll 1
-            for (int p = 0; p < 4; ++p) {  // 16 columns at a time
-                float o[16];
-                tmem_ld16(tq + M::O + 64 * hh + 16 * p, o);
-                if (p == 3) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mb_arrive(o_free);
-                }
+            for (int p = 0; p < 2; ++p) {
+                float o[32];
+                tmem_ld32(tq + M::O + 64 * hh + 32 * p, o);
 #pragma unroll
-                for (int u = 0; u < 16; ++u) o[u] *= os;
-                if (w.row_dot) {
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        float xx[8];
-                        unpack(*own(2 * p + u), xx);
-#pragma unroll
-                        for (int m = 0; m < 8; ++m) dot = fmaf(o[8 * u + m], xx[m], dot);
-                    }
-                }
-                if (w.out_f32) {
-                    // (heads that share keys: each one's gradient in fp32, to be summed) a row's piece at a time
-                    if (lane < live) {
-                        float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(w.out) + b * w.os[0] +
-                                                                (tw + lane) * w.os[1] + h * w.os[2] + col + 16 * p);
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            to[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-                    }
-                    __syncwarp();
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        *own(2 * p + u) =
-                            make_uint4(pack_bf16(o[8 * u], o[8 * u + 1]), pack_bf16(o[8 * u + 2], o[8 * u + 3]),
-                                       pack_bf16(o[8 * u + 4], o[8 * u + 5]), pack_bf16(o[8 * u + 6], o[8 * u + 7]));
+                for (int u = 0; u < 32; u += 2) {
+                    const float2 y = __ffma2_rn(make_float2(o[u], o[u + 1]), make_float2(os, os),
+                                                make_float2(o1[32 * p + u], o1[32 * p + u + 1]));
+                    o1[32 * p + u] = y.x, o1[32 * p + u + 1] = y.y;
                 }
             }
-            if (!w.out_f32) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mb_arrive(o_free);
+            if (TERMS > 1 && w.row_dot) {
+                {
+                    uint4 xv[8];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        xv[u] = 4 * u + lrow < live
+                                    ? *reinterpret_cast<const uint4 *>(px + (4 * u + lrow) * w.xs[1] + 8 * lch)
+                                    : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) *line(u) = xv[u];
+                }
                 __syncwarp();
-                bf16 *to = static_cast<bf16 *>(w.out) + b * w.os[0] + (tw + lrow) * w.os[1] + h * w.os[2] + col + 8 * lch;
-                const int64_t step = 4 * w.os[1];
+                float2 dot = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    float xx[8];
+                    unpack(*own(u), xx);
+#pragma unroll
+                    for (int m = 0; m < 8; m += 2)
+                        dot = __ffma2_rn(make_float2(o1[8 * u + m], o1[8 * u + m + 1]), make_float2(xx[m], xx[m + 1]), dot);
+                }
+                __syncwarp();
+                // heads of 128: each half of the columns leaves its own product
+                if (lane < live)
+                    w.row_dot[(NH == 2 ? 0 : hh * set.B * set.T * set.H) + (b * set.T + tw + lane) * set.H + h] =
+                        dot.x + dot.y;
+            }
+            if (w.out_f32) {
+                // heads that share keys: each one's gradient in fp32, to be summed
+                if (lane < live) {
+                    float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(w.out) + b * w.os[0] +
+                                                            (tw + lane) * w.os[1] + h * w.os[2] + col);
+#pragma unroll
+                    for (int u = 0; u < 16; ++u)
+                        to[u] = make_float4(o1[4 * u], o1[4 * u + 1], o1[4 * u + 2], o1[4 * u + 3]);
+                }
+            } else {
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
-                    if (4 * u + lrow < live) *reinterpret_cast<uint4 *>(to + u * step) = *line(u);
+                    *own(u) = make_uint4(pack_bf16(o1[8 * u], o1[8 * u + 1]), pack_bf16(o1[8 * u + 2], o1[8 * u + 3]),
+                                         pack_bf16(o1[8 * u + 4], o1[8 * u + 5]), pack_bf16(o1[8 * u + 6], o1[8 * u + 7]));
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mb_arrive(&k_empty[it % L::NK]);
-            // heads of 128: each half of the columns leaves its own product
-            if (w.row_dot && lane < live)
-                w.row_dot[(NH == 2 ? 0 : hh * set.B * set.T * set.H) + (b * set.T + tw + lane) * set.H + h] = dot;
+            if (lane == 0 && !w.out_f32 && live > 0) tma_store_4d(&maps.o[blockIdx.y], col, int(tw), h, b, stage);
+            if (lane == 0) bulk_commit();
         }
-    } else {
+        // the last chunks' tiles have been read before shared memory is released
+        if (lane == 0) bulk_wait_read();
+        __syncwarp();
+    } else if (warp < 16) {
         // ------------------------------------------------ rows of the state
         const int grp = (warp - 8) >> 2, dk = 32 * (warp & 3) + lane;
         const int hp = NH == 2 ? dk >> 6 : 0, h = h0 + hp;
@@ -469,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lc = ((32 * (warp & 3)) & 63) / 8 + ((lane >> 3) & 1);
         const uint32_t kbase = smem_addr(sm + L::k) + uint32_t((32 * (warp & 3)) >> 6) * kPanel + lr * 128;
         const uint32_t kx0 = uint32_t((lc ^ (lr & 7)) << 4), kx1 = uint32_t(((lc + 2) ^ (lr & 7)) << 4);
-        bool ok = true;
+        bool ok = ok0;
 #pragma unroll 1
         for (int it = 0; ok; ++it) {
             // States that are kept: at a span's end (in reverse that is the state before the
@@ -498,42 +529,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (it == n) break;
-            if (!(ok = wwait(&k_full[it % L::NK], it / L::NK) && wwait(g_full, it))) break;
-            const uint32_t kt = kbase + (it % L::NK) * kTile;
-            const float *wt = Gh + hp * 4 * C + 3 * C + 2 * (lane & 3);
-            const float decay = total[hp];
-            // the chunk's weighted keys, half of it at a time, the groups of 16 steps shared
-            // between the two warpgroups
-#pragma unroll 1
-            for (int i = 0; i < NG / 2; ++i) {
-                const int gi = (i >> 1) * (NG / 2) + grp * (NG / 4) + (i & 1);
-                const float2 w0 = *reinterpret_cast<const float2 *>(wt + gi * GT);
-                const float2 w1 = *reinterpret_cast<const float2 *>(wt + gi * GT + 8);
-#pragma unroll 1
-                for (int x = 0; x < 2; ++x) {  // key rows 0..15 and 16..31 of the warp
-                    uint32_t r[4], t[3][4];
-                    ldmatrix_x4_trans(kt + gi * (GT * 128) + (x ? kx1 : kx0), r);
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        uint32_t a[3];
-                        split<3>(__fmul2_rn(make_float2(bf_lo(r[m]), bf_hi(r[m])), m < 2 ? w0 : w1), a);
-                        t[0][m] = a[0], t[1][m] = a[1], t[2][m] = a[2];
-                    }
-#pragma unroll
-                    for (int m = 0; m < 3; ++m)
-                        tmem_put_16x8(tq + (uint32_t(16 * x) << 16) + M::W + 64 * m + 8 * gi, t[m]);
-                }
-                if (i & 1) {
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mb_arrive(&w_full[i >> 1]);
-                }
-            }
-            if (lane == 0) {
-                mb_arrive(g_empty);
-                if (state_only) mb_arrive(&k_empty[it % L::NK]);
-            }
             if (!state_only) {
                 // the state as the operand of Q S (its reader of the chunk before is done)
                 if (it > 0 && !(ok = wwait(qs_done, it - 1))) break;
@@ -555,14 +550,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mb_arrive(s_ready);
             }
+            if (!(ok = wwait(&k_full[it % L::NK], it / L::NK) && wwait(g_full, it))) break;
+            const uint32_t kt = kbase + (it % L::NK) * kTile;
+            const float *wt = Gh + hp * 4 * C + 3 * C + 2 * (lane & 3);
+            const float decay = total[hp];
+            // the chunk's weighted keys, half of it at a time, the groups of 16 steps shared
+            // between the two warpgroups
+#pragma unroll 1
+            for (int i = 0; i < NG / 2; ++i) {
+                const int gi = (i >> 1) * (NG / 2) + grp * (NG / 4) + (i & 1);
+                uint32_t r[2][4];  // key rows 0..15 and 16..31 of the warp
+                ldmatrix_x4_trans(kt + gi * (GT * 128) + kx0, r[0]);
+                ldmatrix_x4_trans(kt + gi * (GT * 128) + kx1, r[1]);
+                const float2 w0 = *reinterpret_cast<const float2 *>(wt + gi * GT);
+                const float2 w1 = *reinterpret_cast<const float2 *>(wt + gi * GT + 8);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t t[3][4];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        uint32_t a[3];
+                        split<3>(__fmul2_rn(make_float2(bf_lo(r[x][m]), bf_hi(r[x][m])), m < 2 ? w0 : w1), a);
+                        t[0][m] = a[0], t[1][m] = a[1], t[2][m] = a[2];
+                    }
+#pragma unroll
+                    for (int m = 0; m < 3; ++m)
+                        tmem_put_16x8(tq + (uint32_t(16 * x) << 16) + M::W + 64 * m + 8 * gi, t[m]);
+                }
+                if (i & 1) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mb_arrive(&w_full[i >> 1]);
+                }
+            }
+            if (lane == 0) {
+                mb_arrive(g_empty);
+                if (state_only) mb_arrive(&k_empty[it % L::NK]);
+            }
             if (!(ok = wwait(kv_done, it))) break;
             tc_fence_after();
 #pragma unroll
-            for (int u = 0; u < SC; u += 32) {
-                float x[32];
-                tmem_ld32(tq + M::KV + (NH == 2 ? 64 * hp : 0) + col + u, x);
+            for (int u = 0; u < SC; u += 16) {
+                float x[16];
+                tmem_ld16(tq + M::X + (NH == 2 ? 64 * hp : 0) + col + u, x);
 #pragma unroll
-                for (int m = 0; m < 32; m += 2) {
+                for (int m = 0; m < 16; m += 2) {
                     const float2 y = __ffma2_rn(make_float2(decay, decay), make_float2(s[u + m], s[u + m + 1]),
                                                 make_float2(x[m], x[m + 1]));
                     s[u + m] = y.x, s[u + m + 1] = y.y;
@@ -572,7 +605,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mb_arrive(kv_free);
         }
-    }
     } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLast));
     if (!ok0) {
@@ -606,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t st = dS + uint64_t((m * L::sterm + hp * 8192) >> 4);
 #pragma unroll
                         for (int ks = 0; ks < KS; ++ks)
-                            umma_bf16_ss(tm + M::O + 64 * hp, q + koff(ks), st + uint64_t(ks * 128), id_o, m + ks > 0);
+                            umma_bf16_ss(tm + M::X + 64 * hp, q + koff(ks), st + uint64_t(ks * 128), id_o, m + ks > 0);
                     }
                 }
                 umma_commit(qs_done);
@@ -618,56 +650,55 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < NG / 2; ++i)
 #pragma unroll
                     for (int m = 0; m < 3; ++m)
-                        umma_bf16_ts(tm + M::KV, a + 64 * m + 8 * i, v + uint64_t(i * 128), id_mn, half + i + m > 0);
+                        umma_bf16_ts(tm + M::X, a + 64 * m + 8 * i, v + uint64_t(i * 128), id_mn, half + i + m > 0);
             };
             auto pv = [&](int it, int hp) {
                 const uint64_t v = dV + uint64_t(((it % L::NV) * kTile + hp * kPanel) >> 4);
 #pragma unroll 1
-                for (int m = 0; m < TERMS; ++m)
+                for (int m = 0; m < TERMS; ++m) {
+                    // one term lies in a row of columns; of three, 32 steps' first and second terms
+                    // lie side by side, their third ones behind all of those
+                    const uint32_t p = tm + M::P + (TERMS == 1 ? 0 : m == 2 ? 128 : 16 * m);
+                    const uint32_t step = TERMS == 1 || m == 2 ? 16 : 32;
 #pragma unroll
                     for (int ks = 0; ks < C / 16; ++ks)
-                        umma_bf16_ts(tm + M::O + 64 * hp, tm + M::P + 64 * m + 8 * ks, v + uint64_t(ks * 128), id_o, true);
+                        umma_bf16_ts(tm + M::O + 64 * hp, p + (ks >> 1) * step + 8 * (ks & 1), v + uint64_t(ks * 128), id_o,
+                                     m + ks > 0);
+                }
                 umma_commit(o_done);
             };
             bool ok = true;
             for (int it = 0; it < n && ok; ++it) {
                 if (!state_only) {
-                    if (!(ok = wait(&k_full[it % L::NK], it / L::NK) && wait(&q_full[it % L::NQ], it / L::NQ))) break;
-                    if (it > 0 && !(ok = wait(o_free, it - 1))) break;
-                    tc_fence_after();
-                    qk(it, 0);
-                }
-                // the first half of the state's product while P is made of A
-                if (!(ok = wait(&v_full[it % L::NV], it / L::NV) && (it == 0 || wait(kv_free, it - 1)) &&
-                           wait(&w_full[0], it)))
-                    break;
-                tc_fence_after();
-                kv(it, 0);
-                if (M::over_a && !state_only) {
-                    if (!(ok = wait(p_ready, it) && wait(s_ready, it))) break;
+                    // Q S first: its place is wanted by the state's product, its result by nobody soon
+                    if (!(ok = wait(&q_full[it % L::NQ], it / L::NQ) && wait(s_ready, it))) break;
+                    if (it > 0 && !(ok = M::over_a ? wait(kv_free, it - 1) : wait(o_free, it - 1))) break;
                     tc_fence_after();
                     qs(it);
-                    umma_commit(&q_empty[it % L::NQ]);
+                    if (!(ok = wait(&k_full[it % L::NK], it / L::NK))) break;
+                    if (M::over_a && it > 0 && !(ok = wait(o_free, it - 1))) break;
+                    tc_fence_after();
+                    qk(it, 0);
+                    if (NH == 1) umma_commit(&q_empty[it % L::NQ]);
+                    if (!(ok = wait(o_ready, it))) break;  // Q S is in the rows' registers
+                } else if (it > 0 && !(ok = wait(kv_free, it - 1))) {
+                    break;
                 }
+                if (!(ok = wait(&v_full[it % L::NV], it / L::NV) && wait(&w_full[0], it))) break;
+                tc_fence_after();
+                kv(it, 0);
                 if (!(ok = wait(&w_full[1], it))) break;
                 tc_fence_after();
                 kv(it, 1);
                 umma_commit(kv_done);
                 if (!state_only) {
-                    if (!M::over_a) {
-                        if (!(ok = wait(kv_free, it) && wait(s_ready, it))) break;
-                        tc_fence_after();
-                        qs(it);
-                        if (NH == 1) umma_commit(&q_empty[it % L::NQ]);
-                        if (!(ok = wait(p_ready, it * NH))) break;
-                        tc_fence_after();
-                        if (NH == 2 && TERMS == 1) qk(it, 1);  // P stands beside A
-                    }
-                    if (!(ok = wait(o_ready, it))) break;
+                    if (!M::over_a && !(ok = wait(kv_free, it))) break;
+                    if (!(ok = wait(p_ready, it * NH))) break;
                     tc_fence_after();
+                    if (NH == 2 && TERMS == 1) qk(it, 1);  // P stands beside A
                     pv(it, 0);
                     if (NH == 2) {
-                        if (TERMS != 1) qk(it, 1);             // ... or over it: after the product with P
+                        if (TERMS != 1) qk(it, 1);         // ... or over it: after the product with P
                         umma_commit(&q_empty[it % L::NQ]);
                         if (!(ok = wait(p_ready, it * NH + 1))) break;
                         tc_fence_after();
@@ -687,9 +718,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
     } else if (warp == 17) {
-        // ------------------------------------------------ tiles and decays
-        const float L2E = 1.4426950408889634f, L2E_LO = 1.9259629911266175e-8f;
+        // ------------------------------------------------ tiles
+        if (lane == 0) {
+            const CUtensorMap *mq = &maps.q[blockIdx.y], *mk = &maps.k[blockIdx.y], *mv = &maps.v[blockIdx.y];
+            // the next tile of a ring, once its slot is free
+            auto fill = [&](int it, int depth, uint64_t *full, uint64_t *empty, int off, const CUtensorMap *m, int div) {
+                const int sl = it % depth;
+                if (it >= depth && !wait(&empty[sl], it / depth - 1)) return false;
+                unsigned char *dst = sm + off + sl * kTile;
+                mbar_arrive_expect_tx(&full[sl], kTile);
+                for (int p = 0; p < 2; ++p)
+                    tma_load_4d(dst + p * kPanel, m, NH == 2 ? 0 : 64 * p, chunk_of(it) * C,
+                                (NH == 2 ? h0 + p : h0) / div, b, &full[sl]);
+                return true;
+            };
+            // a block starts with the state as an operand and Q, ends with V
+            int lk = 0, lq = 0, lv = 0;  // tiles loaded
+            for (int it = 0; it < n; ++it) {
+                if (!state_only) {
+                    if (!fill(it, L::NQ, q_full, q_empty, L::q, mq, w.qdiv)) break;
+                    ++lq;
+                }
+                if (!fill(it, L::NK, k_full, k_empty, L::k, mk, w.kdiv)) break;
+                ++lk;
+                if (!fill(it, L::NV, v_full, v_empty, L::v, mv, w.vdiv)) break;
+                ++lv;
+            }
+            // every load in flight lands before the block's shared memory is released
+            bool done = true;
+            for (int i = max(0, lk - L::NK); i < lk; ++i)
+                done = mbar_wait_bounded(&k_full[i % L::NK], (i / L::NK) & 1, ctl.timeout_ns) && done;
+            for (int i = max(0, lq - L::NQ); i < lq; ++i)
+                done = mbar_wait_bounded(&q_full[i % L::NQ], (i / L::NQ) & 1, ctl.timeout_ns) && done;
+            for (int i = max(0, lv - L::NV); i < lv; ++i)
+                done = mbar_wait_bounded(&v_full[i % L::NV], (i / L::NV) & 1, ctl.timeout_ns) && done;
+            if (!done) record_error(ctl, ERR_DRAIN_TIMEOUT);
+        }
+        __syncwarp();
+    } else if (warp == 18) {
+        // ------------------------------------------------ decays
+        const float L2E = 1.4426950408889634f, L2E_LO = 1.9259629911266175e-8f;  // log2(e) in two parts
         float *arr = reinterpret_cast<float *>(sm + L::arr);
+        const float kvs = w.kv_scale;
         float gv[NH][4];
         auto fetch_g = [&](int c) {
 #pragma unroll
@@ -700,36 +770,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     gv[hp][u] = t < T && h0 + hp < H ? set.g[b * set.gs[0] + t * set.gs[1] + (h0 + hp) * set.gs[2]] : 0.f;
                 }
         };
-        if (n > 0) fetch_g(chunk_of(0));
-        const CUtensorMap *mq = &maps.q[blockIdx.y], *mk = &maps.k[blockIdx.y], *mv = &maps.v[blockIdx.y];
-        auto load = [&](unsigned char *dst, const CUtensorMap *m, int div, int c, uint64_t *full) {
-            mbar_arrive_expect_tx(full, kTile);
-#pragma unroll
-            for (int p = 0; p < 2; ++p)
-                tma_load_4d(dst + p * kPanel, m, NH == 2 ? 0 : 64 * p, c * C, (NH == 2 ? h0 + p : h0) / div, b, full);
-        };
-        // the next tile of a ring, once its slot is free
-        auto fill = [&](int &l, int depth, uint64_t *full, uint64_t *empty, int off, const CUtensorMap *m, int div, int c) {
-            const int sl = l % depth;
-            if (l >= depth && !wait(&empty[sl], l / depth - 1)) return false;
-            load(sm + off + sl * kTile, m, div, c, &full[sl]);
-            ++l;
-            return true;
-        };
         bool ok = true;
-        int lk = 0, lq = 0, lv = 0;  // tiles loaded
+        if (n > 0) fetch_g(chunk_of(0));
+#pragma unroll 1
         for (int it = 0; it < n && ok; ++it) {
-            const int c = chunk_of(it);
-            // this warp runs about a chunk ahead: keys and queries, the sums of g once the
-            // chunk before has used its own, then the values, whose tile is needed last
-            if (lane == 0) {
-                ok = fill(lk, L::NK, k_full, k_empty, L::k, mk, w.kdiv, c);
-                if (!state_only) ok = ok && fill(lq, L::NQ, q_full, q_empty, L::q, mq, w.qdiv, c);
-            }
-            ok = __shfl_sync(0xffffffffu, int(ok), 0);
-            if (!ok) break;
             // sums of g over the chunk, in units of log 2, as pairs of fp32
-            float ph[NH][4], pl[NH][4];
+            float ph[NH][4], pl[NH][4], cf[NH][4], wt[NH][4], last[NH];
 #pragma unroll
             for (int hp = 0; hp < NH; ++hp) {
                 float h = 0.f, l = 0.f;
@@ -746,61 +792,50 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int m = 1; m < 32; m <<= 1) {
                     const float oh = __shfl_up_sync(0xffffffffu, eh, m), ol = __shfl_up_sync(0xffffffffu, el, m);
-                    if (lane >= m) add2(eh, el, oh, ol);
+                    float th = eh, tl = el;
+                    add2(th, tl, oh, ol);
+                    eh = lane >= m ? th : eh, el = lane >= m ? tl : el;
                 }
                 eh = __shfl_up_sync(0xffffffffu, eh, 1), el = __shfl_up_sync(0xffffffffu, el, 1);
                 if (lane == 0) eh = el = 0.f;
 #pragma unroll
                 for (int u = 0; u < 4; ++u) add2(ph[hp][u], pl[hp][u], eh, el);
-            }
-            if (it + 1 < n) fetch_g(chunk_of(it + 1));
-            if (it > 0 && !(ok = wwait(g_empty, it - 1))) break;
-#pragma unroll
-            for (int hp = 0; hp < NH; ++hp) {
-                float *G = arr + hp * 4 * C;
                 const float lh = __shfl_sync(0xffffffffu, ph[hp][3], 31), ll = __shfl_sync(0xffffffffu, pl[hp][3], 31);
                 // the edge of the 32-step block that column factors refer to
                 const int src = (lane & 24) + (rev ? 0 : 7);
                 const float rh = __shfl_sync(0xffffffffu, rev ? ph[hp][0] : ph[hp][3], src);
                 const float rl = __shfl_sync(0xffffffffu, rev ? pl[hp][0] : pl[hp][3], src);
-                float cf[4], wt[4];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const float h = ph[hp][u], l = pl[hp][u];
-                    cf[u] = exp2f(rev ? (h - rh) + (l - rl) : (rh - h) + (rl - l));
-                    wt[u] = exp2f(rev ? h + l : (lh - h) + (ll - l)) * w.kv_scale;
+                    cf[hp][u] = exp2f(rev ? (h - rh) + (l - rl) : (rh - h) + (rl - l));
+                    wt[hp][u] = exp2f(rev ? h + l : (lh - h) + (ll - l)) * kvs;
+                    // the sign with which the rows' exponents come out as differences row - column
+                    if (rev) ph[hp][u] = -h, pl[hp][u] = -l;
                 }
-                store4(G + 4 * lane, ph[hp]);
-                store4(G + C + 4 * lane, pl[hp]);
-                store4(G + 2 * C + 4 * lane, cf);
-                store4(G + 3 * C + 4 * lane, wt);
-                if (lane == 31) total[hp] = exp2f(lh + ll);
-                if (state_only && lane == 31 && h0 + hp < H) {
+                last[hp] = lh + ll;
+            }
+            if (it + 1 < n) fetch_g(chunk_of(it + 1));
+            // the chunk before has used its own
+            if (it > 0 && !(ok = wwait(g_empty, it - 1))) break;
+#pragma unroll
+            for (int hp = 0; hp < NH; ++hp) {
+                float *G = arr + hp * 4 * C + 4 * lane;
+                store4(G, ph[hp]);
+                store4(G + C, pl[hp]);
+                store4(G + 2 * C, cf[hp]);
+                store4(G + 3 * C, wt[hp]);
+                if (lane == 0) total[hp] = exp2f(last[hp]);
+                if (state_only && lane == 0 && h0 + hp < H) {
                     // the segment's sum of g beside its state, for the scan that joins the segments
                     float *sum = w.seg_out + set.B * set.H * nseg * D * D + (int64_t(b) * H + h0 + hp) * nseg + seg;
-                    const float g = (lh + ll) * 0.6931471805599453f;
+                    const float g = last[hp] * 0.6931471805599453f;
                     *sum = it == 0 ? g : *sum + g;
                 }
             }
             __syncwarp();
-            if (lane == 0) {
-                mb_arrive(g_full);
-                ok = fill(lv, L::NV, v_full, v_empty, L::v, mv, w.vdiv, c);
-            }
-            ok = __shfl_sync(0xffffffffu, int(ok), 0);
+            if (lane == 0) mb_arrive(g_full);
         }
-        // every load in flight lands before the block's shared memory is released
-        if (lane == 0) {
-            bool done = true;
-            for (int i = max(0, lk - L::NK); i < lk; ++i)
-                done = mbar_wait_bounded(&k_full[i % L::NK], (i / L::NK) & 1, ctl.timeout_ns) && done;
-            for (int i = max(0, lq - L::NQ); i < lq; ++i)
-                done = mbar_wait_bounded(&q_full[i % L::NQ], (i / L::NQ) & 1, ctl.timeout_ns) && done;
-            for (int i = max(0, lv - L::NV); i < lv; ++i)
-                done = mbar_wait_bounded(&v_full[i % L::NV], (i / L::NV) & 1, ctl.timeout_ns) && done;
-            if (!done) record_error(ctl, ERR_DRAIN_TIMEOUT);
-        }
-        __syncwarp();
     }
     }
     tc_fence_before();
@@ -811,14 +846,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// [B][T][heads][D] bf16 with any strides: boxes of 64 columns x 128 steps of one head
+// [B][T][heads][D] bf16 with any strides: boxes of 64 columns x `steps` steps of one head
 cudaError_t tile_map(CUtensorMap *m, const void *base, const int64_t (&st)[3], int64_t B, int64_t T, int64_t heads,
-                     int D) {
+                     int D, uint32_t steps = C) {
     const uint64_t dims[4] = {uint64_t(D), uint64_t(T), uint64_t(heads), uint64_t(B)};
     // a dimension of one element is never stepped over: any legal stride does
     const uint64_t str[3] = {uint64_t(T > 1 ? st[1] : D) * 2, uint64_t(heads > 1 ? st[2] : D) * 2,
                              uint64_t(B > 1 ? st[0] : D) * 2};
-    const uint32_t box[4] = {64, C, 1, 1};
+    const uint32_t box[4] = {64, steps, 1, 1};
     return make_tmap_bf16_4d(m, base, dims, str, box);
 }
 
@@ -844,14 +879,20 @@ cudaError_t go(const AttnMaps &maps, const AttnSet &set, int nwalks, bool state_
 
 }  // namespace
 
-cudaError_t launch_attn_mma(const AttnSet &set, int nwalks, int D, int terms, bool state_only, cudaStream_t s) {
+cudaError_t launch_attn_mma(const AttnSet &all, int first, int nwalks, int D, int terms, bool state_only,
+                            cudaStream_t s) {
     AttnMaps maps;
+    AttnSet set = all;
+    set.first = first;
     cudaError_t e;
     for (int i = 0; i < nwalks; ++i) {
-        const AttnWalk &w = set.w[i];
+        const AttnWalk &w = set.w[first + i];
         if ((e = tile_map(&maps.q[i], w.q, w.qs, set.B, set.T, set.H / w.qdiv, D)) != cudaSuccess) return e;
         if ((e = tile_map(&maps.k[i], w.k, w.ks, set.B, set.T, set.H / w.kdiv, D)) != cudaSuccess) return e;
         if ((e = tile_map(&maps.v[i], w.v, w.vs, set.B, set.T, set.H / w.vdiv, D)) != cudaSuccess) return e;
+        if (!state_only && !w.out_f32 &&
+            (e = tile_map(&maps.o[i], w.out, w.os, set.B, set.T, set.H, D, 32)) != cudaSuccess)
+            return e;
     }
     if (D == 64)
         return terms == 1 ? go<64, 1>(maps, set, nwalks, state_only, s) : go<64, 3>(maps, set, nwalks, state_only, s);

@@ -45,6 +45,7 @@ struct AttnSet {
     const float *g;
     int64_t gs[3];
     int64_t B, T, H;
+    int first;                    // the launch's first walk
     int64_t seg_len;              // steps of a segment (a multiple of kAttnChunk)
     int nseg, spans;
     DevCtl ctl;
@@ -54,7 +55,8 @@ struct AttnSet {
 cudaError_t launch_attn_rec(const AttnSet &set, int nwalks, int D, int dtype, bool state_only, cudaStream_t s);
 
 // tensor-core walk, bf16; terms: bf16 terms of the computed operands of the output
-cudaError_t launch_attn_mma(const AttnSet &set, int nwalks, int D, int terms, bool state_only, cudaStream_t s);
+cudaError_t launch_attn_mma(const AttnSet &set, int first, int nwalks, int D, int terms, bool state_only,
+                            cudaStream_t s);
 
 size_t attn_workspace_bytes(const mgs_attention_shape &sh, bool backward);
 cudaError_t launch_attn_fwd(const mgs_attention_shape &sh, const void *q, const void *k, const void *v,
