@@ -452,6 +452,7 @@ AttnSet set_of(const mgs_attention_shape &sh, const Plan &p, const float *g, con
     s.B = sh.B, s.T = sh.T, s.H = sh.H;
     s.seg_len = p.seg_len, s.nseg = p.nseg, s.spans = p.spans;
     s.ctl = ctl;
+    s.tries = uint32_t(min64(int64_t(ctl.timeout_ns / 40) + 1000, 0x7fffffff));
     for (auto &w : s.w) w.qdiv = w.kdiv = w.vdiv = w.xdiv = 1, w.o_scale = w.kv_scale = 1.f;
     return s;
 }

@@ -118,7 +118,9 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // Up to `tries` tries at a phase, in the fewest instructions: the waiting warps'
-// tries take issue slots from the working ones.
+// tries take issue slots, and their code room in the instruction cache, from
+// the working ones.  A try takes about 40 ns (84 cycles measured), so the limit
+// counts tries instead of reading the clock.
 __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, uint32_t tries) {
     uint32_t ok;
     asm volatile(
@@ -136,23 +138,6 @@ __device__ __forceinline__ bool mbar_poll(uint32_t bar, uint32_t parity, uint32_
         : "r"(bar), "r"(parity), "r"(tries)
         : "memory");
     return ok != 0;
-}
-
-// Waits for a phase; false once the wait gives up or another role has.
-__device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity, volatile int *abort_word,
-                                             const DevCtl &ctl) {
-    const uint32_t at = smem_addr(bar);
-    if (mbar_poll(at, parity, 1024)) return true;
-    const uint64_t t0 = global_ns();
-#pragma unroll 1
-    while (*abort_word == 0) {
-        if (mbar_poll(at, parity, 1024)) return true;
-        if (global_ns() - t0 > ctl.timeout_ns) {
-            record_error(ctl, ERR_MBAR_TIMEOUT);
-            *abort_word = 1;
-        }
-    }
-    return false;
 }
 
 // x as a sum of TERMS bf16 pairs (packed: x.x in the low half)
@@ -189,7 +174,6 @@ __global__ void __launch_bounds__(kThreads, 1)
              *s_ready = bars + 21, *kv_done = bars + 22, *kv_free = bars + 23, *g_full = bars + 24, *g_empty = bars + 25,
              *a_read = bars + 28, *drained = bars + 29;
     uint32_t *slot = reinterpret_cast<uint32_t *>(bars + 26);
-    volatile int *abort_word = reinterpret_cast<volatile int *>(slot + 1);
     float *total = reinterpret_cast<float *>(slot + 2);  // [NH]: the chunk's decay
 
     // the walk's description from shared memory: parameters indexed by blockIdx
@@ -221,7 +205,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(g_full, 1), mbar_init(g_empty, state_only ? 8 : 16);
         mbar_init(a_read, 8), mbar_init(drained, 1);
         fence_barrier_init();
-        *abort_word = (smem_addr(sm) & 1023u) != 0;  // the swizzled tiles need it (never seen otherwise)
     }
     if (warp == 16) {
         tmem_alloc(slot, 512);
@@ -232,14 +215,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tm = *slot;
     const uint32_t tq = tm + (uint32_t(32 * (warp & 3)) << 16);
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-        return bounded_wait(bar, parity & 1u, abort_word, ctl);
-    };
+    // a role whose wait gives up ends; the others' waits then give up too
+    // A role whose wait gives up says so and ends; the others' waits then give up too.
+    const uint32_t tries = set.tries;
+    auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_poll(smem_addr(bar), parity & 1u, tries); };
     // the same by a whole warp, whose lanes go on together
     auto wwait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
     auto chunk_of = [&](int i) { return rev ? c1 - 1 - i : c0 + i; };
     const float *Gh = reinterpret_cast<const float *>(sm + L::arr);  // [NH][4][C]: G (-G in reverse) high and low, column factor, weight
-    const bool ok0 = *abort_word == 0;
+    // the swizzled tiles need it (and have never been found elsewhere)
+    const bool ok0 = (smem_addr(sm) & 1023u) == 0;
     if (!ok0 && tid == 0) record_error(ctl, ERR_MBAR_TIMEOUT);
 
     if (warp < 8) {
@@ -458,6 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0 && !w.out_f32 && live > 0) tma_store_4d(&maps.o[blockIdx.y], col, int(tw), h, b, stage);
             if (lane == 0) bulk_commit();
         }
+        if (!ok && lane == 0) record_error(ctl, ERR_MBAR_TIMEOUT);
         // the last chunks' tiles have been read before shared memory is released
         if (lane == 0) bulk_wait_read();
         __syncwarp();
@@ -605,6 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mb_arrive(kv_free);
         }
+        if (!ok && lane == 0) record_error(ctl, ERR_MBAR_TIMEOUT);
     } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLast));
     if (!ok0) {
@@ -615,8 +602,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t id_k = umma_idesc_bf16(128, 128, false), id_mn = umma_idesc_bf16(128, 128, true);
             constexpr uint32_t id_o = umma_idesc_bf16(128, D, true);
             // Descriptors hold addresses in units of 16 bytes: what is issued is one of these
-            // plus a constant, since a longer sum between two products costs more time than a
-            // product takes (64 cycles at N = 128).
+            // plus a short sum, since longer ones between two products cost more time than a
+            // product takes (64 cycles at N = 128); rolled loops, whose code stays at hand.
             const uint64_t dK = umma_desc_k(smem_addr(sm + L::k)), dQ = umma_desc_k(smem_addr(sm + L::q));
             const uint64_t dV = umma_desc_mn(smem_addr(sm + L::v), kPanel), dS = umma_desc_mn(smem_addr(sm), kPanel);
             constexpr int KS = D / 16;
@@ -625,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto qk = [&](int it, int hp) {
                 const uint64_t q = dQ + uint64_t(((it % L::NQ) * kTile + hp * kPanel) >> 4);
                 const uint64_t k = dK + uint64_t(((it % L::NK) * kTile + hp * kPanel) >> 4);
-#pragma unroll
+#pragma unroll 1
                 for (int ks = 0; ks < KS; ++ks) umma_bf16_ss(tm + M::A, q + koff(ks), k + koff(ks), id_k, ks > 0);
                 umma_commit(a_done);
             };
@@ -636,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int m = 0; m < TERMS; ++m) {
                         const uint64_t st = dS + uint64_t((m * L::sterm + hp * 8192) >> 4);
-#pragma unroll
+#pragma unroll 1
                         for (int ks = 0; ks < KS; ++ks)
                             umma_bf16_ss(tm + M::X + 64 * hp, q + koff(ks), st + uint64_t(ks * 128), id_o, m + ks > 0);
                     }
@@ -646,9 +633,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto kv = [&](int it, int half) {
                 const uint64_t v = dV + uint64_t(((it % L::NV) * kTile + half * (NG / 2) * 2048) >> 4);
                 const uint32_t a = tm + M::W + half * (NG / 2) * 8;
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < NG / 2; ++i)
-#pragma unroll
+#pragma unroll 1
                     for (int m = 0; m < 3; ++m)
                         umma_bf16_ts(tm + M::X, a + 64 * m + 8 * i, v + uint64_t(i * 128), id_mn, half + i + m > 0);
             };
@@ -660,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // lie side by side, their third ones behind all of those
                     const uint32_t p = tm + M::P + (TERMS == 1 ? 0 : m == 2 ? 128 : 16 * m);
                     const uint32_t step = TERMS == 1 || m == 2 ? 16 : 32;
-#pragma unroll
+#pragma unroll 1
                     for (int ks = 0; ks < C / 16; ++ks)
                         umma_bf16_ts(tm + M::O + 64 * hp, p + (ks >> 1) * step + 8 * (ks & 1), v + uint64_t(ks * 128), id_o,
                                      m + ks > 0);
@@ -668,6 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma_commit(o_done);
             };
             bool ok = true;
+#pragma unroll 1
             for (int it = 0; it < n && ok; ++it) {
                 if (!state_only) {
                     // Q S first: its place is wanted by the state's product, its result by nobody soon
@@ -710,10 +698,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // whatever was issued completes before TMEM and shared memory are released
             if (!ok) {
                 umma_commit(drained);
-                if (!mbar_wait_bounded(drained, 0, ctl.timeout_ns)) record_error(ctl, ERR_DRAIN_TIMEOUT);
+                record_error(ctl, wait(drained, 0) ? ERR_MBAR_TIMEOUT : ERR_MBAR_TIMEOUT | ERR_DRAIN_TIMEOUT);
             } else if (n > 0) {
-                const bool done = mbar_wait_bounded(&v_empty[(n - 1) % L::NV], ((n - 1) / L::NV) & 1, ctl.timeout_ns);
-                if (!done) record_error(ctl, ERR_DRAIN_TIMEOUT);
+                if (!wait(&v_empty[(n - 1) % L::NV], (n - 1) / L::NV)) record_error(ctl, ERR_DRAIN_TIMEOUT);
             }
         }
         __syncwarp();
@@ -727,6 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (it >= depth && !wait(&empty[sl], it / depth - 1)) return false;
                 unsigned char *dst = sm + off + sl * kTile;
                 mbar_arrive_expect_tx(&full[sl], kTile);
+#pragma unroll 1
                 for (int p = 0; p < 2; ++p)
                     tma_load_4d(dst + p * kPanel, m, NH == 2 ? 0 : 64 * p, chunk_of(it) * C,
                                 (NH == 2 ? h0 + p : h0) / div, b, &full[sl]);
@@ -734,6 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // a block starts with the state as an operand and Q, ends with V
             int lk = 0, lq = 0, lv = 0;  // tiles loaded
+#pragma unroll 1
             for (int it = 0; it < n; ++it) {
                 if (!state_only) {
                     if (!fill(it, L::NQ, q_full, q_empty, L::q, mq, w.qdiv)) break;
@@ -746,13 +735,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // every load in flight lands before the block's shared memory is released
             bool done = true;
-            for (int i = max(0, lk - L::NK); i < lk; ++i)
-                done = mbar_wait_bounded(&k_full[i % L::NK], (i / L::NK) & 1, ctl.timeout_ns) && done;
-            for (int i = max(0, lq - L::NQ); i < lq; ++i)
-                done = mbar_wait_bounded(&q_full[i % L::NQ], (i / L::NQ) & 1, ctl.timeout_ns) && done;
-            for (int i = max(0, lv - L::NV); i < lv; ++i)
-                done = mbar_wait_bounded(&v_full[i % L::NV], (i / L::NV) & 1, ctl.timeout_ns) && done;
-            if (!done) record_error(ctl, ERR_DRAIN_TIMEOUT);
+            auto landed = [&](int l, int depth, uint64_t *full) {
+#pragma unroll 1
+                for (int i = max(0, l - depth); i < l; ++i) done = wait(&full[i % depth], i / depth) && done;
+            };
+            landed(lk, L::NK, k_full), landed(lq, L::NQ, q_full), landed(lv, L::NV, v_full);
+            if (lv < n || !done) record_error(ctl, lv < n ? ERR_MBAR_TIMEOUT : ERR_DRAIN_TIMEOUT);
         }
         __syncwarp();
     } else if (warp == 18) {
@@ -789,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ph[hp][u] = h, pl[hp][u] = l;
                 }
                 float eh = h, el = l;  // inclusive sums over the lanes, then exclusive
-#pragma unroll
+#pragma unroll 1
                 for (int m = 1; m < 32; m <<= 1) {
                     const float oh = __shfl_up_sync(0xffffffffu, eh, m), ol = __shfl_up_sync(0xffffffffu, el, m);
                     float th = eh, tl = el;
@@ -808,8 +796,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     const float h = ph[hp][u], l = pl[hp][u];
-                    cf[hp][u] = exp2f(rev ? (h - rh) + (l - rl) : (rh - h) + (rl - l));
-                    wt[hp][u] = exp2f(rev ? h + l : (lh - h) + (ll - l)) * kvs;
+                    cf[hp][u] = ex2_approx(rev ? (h - rh) + (l - rl) : (rh - h) + (rl - l));
+                    wt[hp][u] = ex2_approx(rev ? h + l : (lh - h) + (ll - l)) * kvs;
                     // the sign with which the rows' exponents come out as differences row - column
                     if (rev) ph[hp][u] = -h, pl[hp][u] = -l;
                 }
@@ -825,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 store4(G + C, pl[hp]);
                 store4(G + 2 * C, cf[hp]);
                 store4(G + 3 * C, wt[hp]);
-                if (lane == 0) total[hp] = exp2f(last[hp]);
+                if (lane == 0) total[hp] = ex2_approx(last[hp]);
                 if (state_only && lane == 0 && h0 + hp < H) {
                     // the segment's sum of g beside its state, for the scan that joins the segments
                     float *sum = w.seg_out + set.B * set.H * nseg * D * D + (int64_t(b) * H + h0 + hp) * nseg + seg;
@@ -836,6 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mb_arrive(g_full);
         }
+        if (!ok && lane == 0) record_error(ctl, ERR_MBAR_TIMEOUT);
     }
     }
     tc_fence_before();

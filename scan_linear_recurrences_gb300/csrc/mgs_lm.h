@@ -48,6 +48,7 @@ struct AttnSet {
     int first;                    // the launch's first walk
     int64_t seg_len;              // steps of a segment (a multiple of kAttnChunk)
     int nseg, spans;
+    uint32_t tries;               // a barrier wait's limit: tries of about 40 ns
     DevCtl ctl;
 };
 
