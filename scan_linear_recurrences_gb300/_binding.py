@@ -101,6 +101,8 @@ _SIGNATURES = {
 def lib():
     """The loaded CUDA library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -132,7 +134,7 @@ def _ptr(x):
 def _stream(s):
     if s is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -233,21 +233,27 @@ _DTYPES = {torch.float32: _b.MGS_F32, torch.bfloat16: _b.MGS_BF16}
 
 
 def _check_typed(t, name, shape, dtype, dense=True, device=None):
+    """One CUDA tensor of this shape, type and device (None: any; a None dtype: fp32 or bf16)."""
+    try:
+        if (t.is_cuda and (dtype is t.dtype or dtype is None and t.dtype in _DTYPES)
+                and (shape is None or t.shape == shape) and (not dense or t.is_contiguous())
+                and (device is None or t.device == device)):
+            return
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device.type != "cuda":
         raise ValueError(f"{name} must be a CUDA tensor (the library runs only on the GPU)")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if dtype is None:
-        if t.dtype not in _DTYPES:
-            raise ValueError(f"{name} must be float32 or bfloat16")
-    elif t.dtype != dtype:
+    if dtype is None and t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be float32 or bfloat16")
+    if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}".replace("torch.", ""))
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dense and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _head_strides(t, name):
@@ -429,20 +435,24 @@ def clip_grad_norm(grads, max_norm, out=None, stream=None):
     if not grads:
         raise ValueError("no tensors")
     dev = grads[0].device
-    for t in grads:
-        if t.device != dev or t.dtype not in _DTYPES or not t.is_contiguous():
-            _check_typed(t, "each of grads", None, None, device=dev)
     if dev.type != "cuda":
         raise ValueError("each of grads must be a CUDA tensor (the library runs only on the GPU)")
-    if out is not None:
+    index = grads[0].get_device()
+    codes = [_DTYPES.get(t.dtype) for t in grads]
+    contiguous = torch.Tensor.is_contiguous
+    if None in codes or any(t.get_device() != index for t in grads) or not all(map(contiguous, grads)):
+        for t in grads:
+            _check_typed(t, "each of grads", None, None, device=dev)
+    if out is not None and ([u.shape for u in outs] != [t.shape for t in grads]
+                            or [_DTYPES.get(u.dtype) for u in outs] != codes
+                            or any(u.get_device() != index for u in outs) or not all(map(contiguous, outs))):
         for t, u in zip(grads, outs):
-            if u.device != dev or u.dtype != t.dtype or u.shape != t.shape or not u.is_contiguous():
-                _check_typed(u, "each of out", t.shape, t.dtype, device=dev)
+            _check_typed(u, "each of out", t.shape, t.dtype, device=dev)
     norm = torch.empty((), dtype=torch.float32, device=dev)
     n = _b.mgs_clip_grad_norm_workspace_size(len(grads))
     at = [t.data_ptr() for t in grads]
-    _b.mgs_clip_grad_norm(at, at if out is None else [u.data_ptr() for u in outs], [t.numel() for t in grads],
-                          [_DTYPES[t.dtype] for t in grads], max_norm, norm, _scratch(n, dev, stream), n, stream)
+    _b.mgs_clip_grad_norm(at, at if out is None else [u.data_ptr() for u in outs], [t.numel() for t in grads], codes,
+                          max_norm, norm, _scratch(n, dev, stream), n, stream)
     return norm
 
 

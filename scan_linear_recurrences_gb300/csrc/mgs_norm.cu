@@ -16,19 +16,26 @@ namespace {
 
 constexpr float kFp8Max = 448.f;
 
-// Sums (SUM) or maxima over the `TPR` threads of a row: TPR <= 32 within a
-// warp, else the whole block.
-template <bool SUM>
-__device__ __forceinline__ float comb(float a, float b) { return SUM ? a + b : fmaxf(a, b); }
-template <bool SUM>
-__device__ __forceinline__ float row_reduce(float x, int tpr, float *red) {
-    for (int m = min(tpr, 32) >> 1; m > 0; m >>= 1) x = comb<SUM>(x, __shfl_xor_sync(0xffffffffu, x, m));
-    if (tpr <= 32) return x;
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+// The sum (and with MAX the maximum of another value) over the `tpr` threads of
+// a row: tpr <= 32 within a warp, else the whole block, in one barrier.
+template <bool MAX>
+__device__ __forceinline__ void row_reduce(float &sum, float &top, int tpr, float (*red)[32]) {
+    for (int m = min(tpr, 32) >> 1; m > 0; m >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, m);
+        if (MAX) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+    }
+    if (tpr <= 32) return;
+    if ((threadIdx.x & 31) == 0) {
+        red[0][threadIdx.x >> 5] = sum;
+        if (MAX) red[1][threadIdx.x >> 5] = top;
+    }
     __syncthreads();
-    float t = red[0];
-    for (int i = 1; i < tpr / 32; ++i) t = comb<SUM>(t, red[i]);
-    return t;
+    sum = red[0][0];
+    if (MAX) top = red[1][0];
+    for (int i = 1; i < tpr / 32; ++i) {
+        sum += red[0][i];
+        if (MAX) top = fmaxf(top, red[1][i]);
+    }
 }
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -37,103 +44,128 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return u;
 }
 
-// V consecutive elements as one access (16 bytes), or V = 1: any N, any alignment
-template <typename T, int V>
-__device__ __forceinline__ void get(const T *p, float (&v)[V]) {
-    if constexpr (V == 1)
-        v[0] = to_f(*p);
-    else
-        unpack(*reinterpret_cast<const uint4 *>(p), v);
+// 16 bytes that are read once (past L1), and written once
+__device__ __forceinline__ uint4 load_once(const void *p) {
+    uint4 u;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                 : "l"(p));
+    return u;
 }
-template <typename T, int V>
-__device__ __forceinline__ void put(T *p, const float (&v)[V]) {
-    if constexpr (V == 1)
-        *p = from_f<T>(v[0]);
-    else
-        *reinterpret_cast<uint4 *>(p) = pack(v);
-}
+__device__ __forceinline__ void store_once(void *p, const uint4 &u) { __stcs(reinterpret_cast<uint4 *>(p), u); }
+
 template <int V>
 __device__ __forceinline__ void put8(uint8_t *p, const float (&v)[V]) {
-    if constexpr (V == 1) {
-        *p = uint8_t(e4m3x2(v[0], 0.f));
-    } else {
 #pragma unroll
-        for (int i = 0; i < V; i += 4)
-            *reinterpret_cast<uint32_t *>(p + i) = e4m3x2(v[i], v[i + 1]) | (e4m3x2(v[i + 2], v[i + 3]) << 16);
-    }
+    for (int i = 0; i < V; i += 4)
+        *reinterpret_cast<uint32_t *>(p + i) = e4m3x2(v[i], v[i + 1]) | (e4m3x2(v[i + 2], v[i + 3]) << 16);
 }
 
-// TPR threads a row, blockDim / TPR rows a block, NV pieces of V elements a
-// thread.  FP8: 0 y in the type, 1 a scale a row, 2 a scale for 128 columns.
-template <typename T, int V, int NV, int FP8>
-__global__ void __launch_bounds__(1024)
+// TPR threads a row, blockDim / TPR rows a block at a time, NV pieces of V
+// elements (16 bytes) a thread.  A block walks rows, gridDim steps apart, and
+// has the next row's loads in flight while it reduces and writes the current
+// one's, w in registers (not with 8 pieces: they would not fit).  FP8: 0 y in the type, 1 a scale a row, 2 a scale
+// for 128 columns.
+template <typename T, int NV, int FP8>
+__global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 4 : NV == 2 ? 2 : 1)
     norm_fwd_kernel(const T *__restrict__ x, const T *__restrict__ res, const T *__restrict__ w, float eps,
                     T *__restrict__ ro, T *__restrict__ y, float *__restrict__ rstd_out, uint8_t *__restrict__ q8,
                     float *__restrict__ scales, int64_t rows, int N, int tpr) {
-    __shared__ float red[2][32];
+    constexpr int V = kVec<T>;
+    __shared__ float red[2][2][32];  // in turn: one barrier for a reduction
     const int c = threadIdx.x % tpr;
-    const int64_t row = int64_t(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
-    const bool live = row < rows;
-    float r[NV][V], ww[NV][V], sum = 0.f, top = 0.f;
-    const int64_t at = row * N;
+    const int64_t step = int64_t(gridDim.x) * (blockDim.x / tpr);
+    int64_t row = int64_t(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
+    const float inv_n = 1.f / float(N);
+    uint4 ux[NV], ur[NV], uw[NV];
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    auto fetch = [&](int64_t at) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+        for (int i = 0; i < NV; ++i) {
+            const int e = (c + i * tpr) * V;
+            const bool in = at < rows && e < N;
+            ux[i] = in ? load_once(x + at * N + e) : zero;
+            if (res) ur[i] = in ? load_once(res + at * N + e) : zero;
+        }
+    };
+    fetch(row);
+    constexpr bool PREFETCH = NV < 8;
+    auto weight = [&](int i) {
         const int e = (c + i * tpr) * V;
+        return e < N ? *reinterpret_cast<const uint4 *>(w + e) : zero;
+    };
+    if (PREFETCH) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) r[i][j] = ww[i][j] = 0.f;
-        if (live && e < N) {
-            get<T, V>(x + at + e, r[i]);
-            get<T, V>(w + e, ww[i]);
+        for (int i = 0; i < NV; ++i) uw[i] = weight(i);
+    }
+    // rows of a block end together (their number is the block's, not the row's)
+    const int64_t last = rows + blockDim.x / tpr - 1;
+    int turn = 0;
+    for (; row < last; row += step, turn ^= 1) {
+        const bool live = row < rows;
+        const int64_t at = row * N;
+        float r[NV][V], sum = 0.f, top = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = (c + i * tpr) * V;
+            unpack(ux[i], r[i]);
             if (res) {
                 float a[V];
-                get<T, V>(res + at + e, a);
+                unpack(ur[i], a);
 #pragma unroll
-                for (int j = 0; j < V; ++j) r[i][j] = to_f(from_f<T>(r[i][j] + a[j]));
-                put<T, V>(ro + at + e, r[i]);
+                for (int j = 0; j < V; ++j) r[i][j] += a[j];
+                const uint4 u = pack(r[i]);
+                if (live && e < N) store_once(ro + at + e, u);
+                unpack(u, r[i]);
             }
+            float ww[V];
+            if (FP8 == 1) unpack(PREFETCH ? uw[i] : weight(i), ww);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 sum = fmaf(r[i][j], r[i][j], sum);
-                if (FP8 == 1) top = fmaxf(top, fabsf(r[i][j] * ww[i][j]));
+                if (FP8 == 1) top = fmaxf(top, fabsf(r[i][j] * ww[j]));
             }
         }
-    }
-    sum = row_reduce<true>(sum, tpr, red[0]);
-    const float rstd = rsqrtf(sum / float(N) + eps);
-    if (FP8 == 0 && rstd_out && live && c == 0) rstd_out[row] = rstd;
-    float inv = 0.f;
-    if (FP8 == 1) {
-        top = row_reduce<false>(top, tpr, red[1]) * rstd;
-        const float sc = top * (1.f / kFp8Max);
-        if (live && c == 0) scales[row] = sc;
-        inv = sc > 0.f ? 1.f / sc : 1.f;
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = (c + i * tpr) * V;
-        const bool in = live && e < N;
-#pragma unroll
-        for (int j = 0; j < V; ++j) r[i][j] = r[i][j] * rstd * ww[i][j];
-        if (FP8 == 0) {
-            if (in) put<T, V>(y + at + e, r[i]);
-            continue;
-        }
-        if (FP8 == 2) {
-            // 128 / V neighbouring threads hold a group (V = 1 has its own kernel)
-            float m = 0.f;
-#pragma unroll
-            for (int j = 0; j < V; ++j) m = fmaxf(m, fabsf(r[i][j]));
-#pragma unroll
-            for (int s = 64 / V; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-            const float sc = m * (1.f / kFp8Max);
-            if (in && e % 128 == 0) scales[row * (N / 128) + e / 128] = sc;
+        if (PREFETCH) fetch(row + step);
+        row_reduce<FP8 == 1>(sum, top, tpr, red[turn]);
+        const float rstd = rsqrtf(sum * inv_n + eps);
+        if (FP8 == 0 && rstd_out && live && c == 0) rstd_out[row] = rstd;
+        float inv = 0.f;
+        if (FP8 == 1) {
+            const float sc = top * rstd * (1.f / kFp8Max);
+            if (live && c == 0) scales[row] = sc;
             inv = sc > 0.f ? 1.f / sc : 1.f;
         }
-        if (in) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) r[i][j] *= inv;
-            put8<V>(q8 + at + e, r[i]);
+        for (int i = 0; i < NV; ++i) {
+            const int e = (c + i * tpr) * V;
+            const bool in = live && e < N;
+            float ww[V];
+            unpack(PREFETCH ? uw[i] : weight(i), ww);
+#pragma unroll
+            for (int j = 0; j < V; ++j) r[i][j] = r[i][j] * rstd * ww[j];
+            if (FP8 == 0) {
+                if (in) store_once(y + at + e, pack(r[i]));
+                continue;
+            }
+            if (FP8 == 2) {
+                // 128 / V neighbouring threads hold a group
+                float m = 0.f;
+#pragma unroll
+                for (int j = 0; j < V; ++j) m = fmaxf(m, fabsf(r[i][j]));
+#pragma unroll
+                for (int s = 64 / V; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+                const float sc = m * (1.f / kFp8Max);
+                if (in && e % 128 == 0) scales[row * (N / 128) + e / 128] = sc;
+                inv = sc > 0.f ? 1.f / sc : 1.f;
+            }
+            if (in) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) r[i][j] *= inv;
+                put8<V>(q8 + at + e, r[i]);
+            }
         }
+        if (!PREFETCH) fetch(row + step);
     }
 }
 
@@ -158,12 +190,12 @@ __global__ void __launch_bounds__(256)
             sum = fmaf(a, a, sum);
             if (FP8 == 1) top = fmaxf(top, fabsf(a * to_f(w[e])));
         }
-        sum = row_reduce<true>(sum, 256, red[0]);
+        row_reduce<FP8 == 1>(sum, top, 256, red);
         const float rstd = rsqrtf(sum / float(N) + eps);
         if (FP8 == 0 && rstd_out && threadIdx.x == 0) rstd_out[row] = rstd;
         float inv = 0.f;
         if (FP8 == 1) {
-            const float sc = row_reduce<false>(top, 256, red[1]) * rstd * (1.f / kFp8Max);
+            const float sc = top * rstd * (1.f / kFp8Max);
             if (threadIdx.x == 0) scales[row] = sc;
             inv = sc > 0.f ? 1.f / sc : 1.f;
         }
@@ -197,67 +229,99 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// A block walks rows blockIdx, + gridDim, ..; dw's sums over its rows stay in
-// registers and go to part[block][N] at the end.
-template <typename T, int V, int NV>
-__global__ void __launch_bounds__(1024)
+// A block walks rows, the next row's loads in flight while it works on the
+// current one (PREFETCH; long rows of bf16 have no registers for it).
+// A row stays in registers as it was loaded and is unpacked twice.  dw's sums
+// over a thread's rows stay in registers and go to part[..][N] at the end: a
+// row of it for each row that the grid has in hand at a time.
+template <typename T, int NV>
+__global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1)
     norm_bwd_kernel(const T *__restrict__ r, const T *__restrict__ w, const float *__restrict__ rstd,
                     const T *__restrict__ gy, const T *__restrict__ gr, T *__restrict__ dx, float *__restrict__ part,
-                    int64_t rows, int N) {
-    __shared__ float red[2][32];
-    const int tpr = blockDim.x, c = threadIdx.x;
-    float dw[NV][V], ww[NV][V];
+                    int64_t rows, int N, int tpr) {
+    constexpr int V = kVec<T>;
+    constexpr bool PREFETCH = NV * V <= 16;
+    __shared__ float red[2][2][32];
+    const int c = threadIdx.x % tpr, rpb = blockDim.x / tpr;
+    const int64_t step = int64_t(gridDim.x) * rpb, first = int64_t(blockIdx.x) * rpb + threadIdx.x / tpr;
+    const float inv_n = 1.f / float(N);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    float dw[NV][V], rs_next;
+    uint4 uw[NV], ur[NV], ug[NV], ua[NV];
+    auto fetch = [&](int64_t row) {
+        rs_next = row < rows ? rstd[row] : 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = (c + i * tpr) * V;
+            const bool in = row < rows && e < N;
+            ur[i] = in ? load_once(r + row * N + e) : zero;
+            ug[i] = in ? load_once(gy + row * N + e) : zero;
+            if (gr && PREFETCH) ua[i] = in ? load_once(gr + row * N + e) : zero;
+        }
+    };
+    fetch(first);
+    auto weight = [&](int i) {
+        const int e = (c + i * tpr) * V;
+        return e < N ? *reinterpret_cast<const uint4 *>(w + e) : zero;
+    };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int e = (c + i * tpr) * V;
+        if (PREFETCH) uw[i] = weight(i);
 #pragma unroll
-        for (int j = 0; j < V; ++j) dw[i][j] = ww[i][j] = 0.f;
-        if (e < N) get<T, V>(w + e, ww[i]);
+        for (int j = 0; j < V; ++j) dw[i][j] = 0.f;
     }
+    // rows of a block end together (their number is the block's, not the row's)
+    const int64_t last = rows + rpb - 1;
     int turn = 0;  // two reduction buffers: one barrier a row
-    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
+    for (int64_t row = first; row < last; row += step, turn ^= 1) {
         const int64_t at = row * N;
-        const float rs = rstd[row];
-        float hat[NV][V], g[NV][V], dot = 0.f;
+        const float rs = rs_next;
+        float dot = 0.f, unused = 0.f;
+        uint4 cr[NV], cg[NV], ca[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            cr[i] = ur[i], cg[i] = ug[i], ca[i] = ua[i];
+            float hat[V], g[V], ww[V];
+            unpack(cr[i], hat);
+            unpack(cg[i], g);
+            unpack(PREFETCH ? uw[i] : weight(i), ww);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                hat[j] *= rs;
+                dw[i][j] = fmaf(g[j], hat[j], dw[i][j]);
+                dot = fmaf(g[j] * ww[j], hat[j], dot);
+            }
+        }
+        if (PREFETCH) fetch(row + step);
+        row_reduce<false>(dot, unused, tpr, red[turn]);
+        dot *= inv_n;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int e = (c + i * tpr) * V;
-            if (e < N) {
-                get<T, V>(r + at + e, hat[i]);
-                get<T, V>(gy + at + e, g[i]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < V; ++j) hat[i][j] = g[i][j] = 0.f;
-            }
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                hat[i][j] *= rs;
-                dw[i][j] = fmaf(g[i][j], hat[i][j], dw[i][j]);
-                g[i][j] *= ww[i][j];
-                dot = fmaf(g[i][j], hat[i][j], dot);
-            }
-        }
-        dot = row_reduce<true>(dot, tpr, red[turn]) / float(N);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = (c + i * tpr) * V;
-            if (e >= N) continue;
-            float o[V], a[V];
-            if (gr) get<T, V>(gr + at + e, a);
+            const bool in = row < rows && e < N;
+            float hat[V], g[V], ww[V], a[V];
+            unpack(cr[i], hat);
+            unpack(cg[i], g);
+            unpack(PREFETCH ? uw[i] : weight(i), ww);
+            if (gr) unpack(PREFETCH ? ca[i] : in ? load_once(gr + at + e) : zero, a);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                o[j] = rs * (g[i][j] - hat[i][j] * dot);
-                if (gr) o[j] += a[j];
+                g[j] = rs * (g[j] * ww[j] - hat[j] * rs * dot);
+                if (gr) g[j] += a[j];
             }
-            put<T, V>(dx + at + e, o);
+            if (in) store_once(dx + at + e, pack(g));
         }
+        if (!PREFETCH) fetch(row + step);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int e = (c + i * tpr) * V;
-        if (e < N)
+        if (e < N) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) part[int64_t(blockIdx.x) * N + e + j] = dw[i][j];
+            for (int j = 0; j < V; j += 4)
+                *reinterpret_cast<float4 *>(part + first * N + e + j) =
+                    make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
+        }
     }
 }
 
@@ -267,7 +331,7 @@ __global__ void __launch_bounds__(256)
     norm_bwd_any_kernel(const T *__restrict__ r, const T *__restrict__ w, const float *__restrict__ rstd,
                         const T *__restrict__ gy, const T *__restrict__ gr, T *__restrict__ dx,
                         float *__restrict__ part, int64_t rows, int64_t N) {
-    __shared__ float red[32];
+    __shared__ float red[2][32];
     float *dw = part + int64_t(blockIdx.x) * N;
     for (int64_t e = threadIdx.x; e < N; e += 256) dw[e] = 0.f;
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
@@ -277,7 +341,9 @@ __global__ void __launch_bounds__(256)
         for (int64_t e = threadIdx.x; e < N; e += 256)
             dot = fmaf(to_f(gy[at + e]) * to_f(w[e]), to_f(r[at + e]) * rs, dot);
         __syncthreads();
-        dot = row_reduce<true>(dot, 256, red) / float(N);
+        float unused = 0.f;
+        row_reduce<false>(dot, unused, 256, red);
+        dot /= float(N);
         for (int64_t e = threadIdx.x; e < N; e += 256) {
             const float hat = to_f(r[at + e]) * rs, g = to_f(gy[at + e]);
             dw[e] = fmaf(g, hat, dw[e]);
@@ -288,87 +354,110 @@ __global__ void __launch_bounds__(256)
 }
 
 // dw[n] = sum over blocks of part[block][n], in a fixed order: 32 columns and
-// 8 runs of blocks a thread block
+// 32 runs of blocks a thread block
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
     norm_dw_kernel(const float *__restrict__ part, T *__restrict__ dw, int blocks, int64_t N) {
-    __shared__ float red[8][33];
+    __shared__ float red[32][33];
     const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
     const int64_t n = int64_t(blockIdx.x) * 32 + c;
     float s = 0.f;
-    if (n < N)
-        for (int i = k; i < blocks; i += 8) s += part[int64_t(i) * N + n];
+    if (n < N) {
+#pragma unroll 8
+        for (int i = k; i < blocks; i += 32) s += part[int64_t(i) * N + n];
+    }
     red[k][c] = s;
     __syncthreads();
-    if (k == 0 && n < N) {
-        for (int i = 1; i < 8; ++i) s += red[i][c];
-        dw[n] = from_f<T>(s);
-    }
+    // warp k adds up column k
+    s = red[c][k];
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    const int64_t o = int64_t(blockIdx.x) * 32 + k;
+    if (c == 0 && o < N) dw[o] = from_f<T>(s);
 }
 
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Threads a row and pieces a thread: up to 4 pieces, at least a warp.
+// Threads a row and pieces a thread.  Up to 32 pieces: a power of two of threads,
+// several rows a warp.  Longer: whole warps, two pieces a thread beyond 256, so
+// that there are more loads in flight for the same warps and no more threads
+// than pieces (N = 5120 in bf16, 640 pieces: 320 threads of 2; 256 of 4, of
+// which a third had none, took 96 us for 8191 rows of the fp8 form against 59).
 struct Shape {
     int tpr, nv;
 };
-Shape shape_of(int64_t pieces) {
-    Shape s{32, 1};
-    while (int64_t(s.tpr) * s.nv < pieces) {
-        if (s.tpr < 256)
-            s.tpr *= 2;
-        else if (s.nv < 4)
-            s.nv *= 2;
-        else if (s.tpr < 1024)
-            s.tpr *= 2;
-        else
-            return {0, 0};
+Shape shape_of(int64_t pieces, int64_t most_of_two) {
+    if (pieces <= 32) {
+        int t = 8;
+        while (t < pieces) t *= 2;
+        return {t, 1};
     }
-    return s;
+    const int nv = pieces <= 256 ? 1 : pieces <= most_of_two ? 2 : pieces <= 2048 ? 4 : 8;
+    const int64_t tpr = ((pieces + nv - 1) / nv + 31) / 32 * 32;
+    if (tpr > 512) return {0, 0};
+    return {int(tpr), nv};
+}
+// Rows of a block: a row's threads are within a warp, or the whole block.
+int block_rows(int tpr) { return tpr > 32 ? 1 : 128 / tpr; }
+
+// Blocks an SM, of kernels that leave room for `most` threads there
+int64_t grid_of(int64_t rows, int rpb, int threads, int most) {
+    return min64((rows + rpb - 1) / rpb, 152 * (threads >= most ? 1 : most / threads));
 }
 
 template <typename T, int FP8>
 cudaError_t fwd_go(const T *x, const T *res, const T *w, float eps, T *r, T *y, float *rstd, uint8_t *q8,
                    float *scales, int64_t rows, int64_t N, cudaStream_t s) {
     constexpr int V = kVec<T>;
-    const Shape sh = shape_of((N + V - 1) / V);
+    const Shape sh = shape_of((N + V - 1) / V, 1024);
     const bool vec = N % V == 0 && al16(x) && al16(res) && al16(w) && al16(r) && al16(y) && al16(q8) && sh.tpr > 0;
     if (!vec) {
         const unsigned grid = unsigned(min64(rows, 152 * 8));
         norm_fwd_any_kernel<T, FP8><<<grid, 256, 0, s>>>(x, res, w, eps, r, y, rstd, q8, scales, rows, N);
         return cudaGetLastError();
     }
-    const int rpb = sh.tpr > 32 ? 1 : 4;  // rows of a block: a row's threads are one warp, or the whole block
-    const int64_t grid = (rows + rpb - 1) / rpb;
-    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-#define MGS_GO(NV)                                                                                              \
-    norm_fwd_kernel<T, V, NV, FP8><<<unsigned(grid), unsigned(rpb * sh.tpr), 0, s>>>(x, res, w, eps, r, y, rstd, \
-                                                                                    q8, scales, rows, int(N), sh.tpr)
+    const int rpb = block_rows(sh.tpr);
+    const int64_t grid = grid_of(rows, rpb, rpb * sh.tpr, sh.nv <= 2 ? 1024 : 512);
+#define MGS_GO(NV)                                                                                             \
+    norm_fwd_kernel<T, NV, FP8><<<unsigned(grid), unsigned(rpb * sh.tpr), 0, s>>>(x, res, w, eps, r, y, rstd, q8, \
+                                                                                 scales, rows, int(N), sh.tpr)
     if (sh.nv == 1) MGS_GO(1);
     else if (sh.nv == 2) MGS_GO(2);
-    else MGS_GO(4);
+    else if (sh.nv == 4) MGS_GO(4);
+    else MGS_GO(8);
 #undef MGS_GO
     return cudaGetLastError();
 }
 
-int bwd_blocks(int64_t rows) { return int(min64(rows, 152 * 4)); }
+// The backward's grid: blocks, of how many rows.  Each row in hand has a row of
+// the workspace for its sums of dw.
+constexpr int kBwdBlocks = 152 * 4;
+int64_t bwd_parts(int64_t rows, int64_t N) { return min64(rows + 15, kBwdBlocks * (N <= 256 ? 16 : 1)); }
 
 template <typename T>
 cudaError_t bwd_go(const T *r, const T *w, const float *rstd, const T *gy, const T *gr, T *dx, T *dw, int64_t rows,
                    int64_t N, float *part, cudaStream_t s) {
     constexpr int V = kVec<T>;
-    const Shape sh = shape_of((N + V - 1) / V);
-    const bool vec = N % V == 0 && al16(r) && al16(w) && al16(gy) && al16(gr) && al16(dx) && sh.tpr > 0;
-    const int blocks = bwd_blocks(rows);
-    if (!vec)
-        norm_bwd_any_kernel<T><<<blocks, 256, 0, s>>>(r, w, rstd, gy, gr, dx, part, rows, N);
-    else if (sh.nv == 1)
-        norm_bwd_kernel<T, V, 1><<<blocks, sh.tpr, 0, s>>>(r, w, rstd, gy, gr, dx, part, rows, int(N));
-    else if (sh.nv == 2)
-        norm_bwd_kernel<T, V, 2><<<blocks, sh.tpr, 0, s>>>(r, w, rstd, gy, gr, dx, part, rows, int(N));
-    else
-        norm_bwd_kernel<T, V, 4><<<blocks, sh.tpr, 0, s>>>(r, w, rstd, gy, gr, dx, part, rows, int(N));
-    norm_dw_kernel<T><<<unsigned((N + 31) / 32), 256, 0, s>>>(part, dw, blocks, N);
+    const Shape sh = shape_of((N + V - 1) / V, 640);
+    const bool vec = N % V == 0 && al16(r) && al16(w) && al16(gy) && al16(gr) && al16(dx) && al16(part) &&
+                     sh.tpr > 0 && sh.nv < 8;
+    int parts;
+    if (!vec) {
+        parts = int(min64(rows, kBwdBlocks));
+        norm_bwd_any_kernel<T><<<parts, 256, 0, s>>>(r, w, rstd, gy, gr, dx, part, rows, N);
+    } else {
+        const int rpb = block_rows(sh.tpr), threads = rpb * sh.tpr;
+        const int blocks =
+            int(min64(kBwdBlocks, grid_of(rows, rpb, threads, sh.nv == 1 ? 768 : 512)));
+        parts = blocks * rpb;
+        if (sh.nv == 1)
+            norm_bwd_kernel<T, 1><<<blocks, threads, 0, s>>>(r, w, rstd, gy, gr, dx, part, rows, int(N), sh.tpr);
+        else if (sh.nv == 2)
+            norm_bwd_kernel<T, 2><<<blocks, threads, 0, s>>>(r, w, rstd, gy, gr, dx, part, rows, int(N), sh.tpr);
+        else
+            norm_bwd_kernel<T, 4><<<blocks, threads, 0, s>>>(r, w, rstd, gy, gr, dx, part, rows, int(N), sh.tpr);
+    }
+    norm_dw_kernel<T><<<unsigned((N + 31) / 32), 1024, 0, s>>>(part, dw, parts, N);
     return cudaGetLastError();
 }
 
@@ -399,7 +488,7 @@ cudaError_t launch_rms_norm_fp8(int dtype, const void *x, const void *res, const
                              : fp8_go<float>(x, res, w, eps, r, q8, scales, rows, N, group, s);
 }
 
-size_t rms_norm_bwd_workspace_bytes(int64_t rows, int64_t N) { return size_t(bwd_blocks(rows)) * size_t(N) * 4; }
+size_t rms_norm_bwd_workspace_bytes(int64_t rows, int64_t N) { return size_t(bwd_parts(rows, N)) * size_t(N) * 4; }
 
 cudaError_t launch_rms_norm_bwd(int dtype, const void *r, const void *w, const float *rstd, const void *gy,
                                 const void *gr, void *dx, void *dw, int64_t rows, int64_t N, void *ws,
