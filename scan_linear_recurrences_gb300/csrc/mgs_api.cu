@@ -168,15 +168,16 @@ cudaError_t make_tmap(CUtensorMap *map, const float *base, int rank, const uint6
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t make_tmap_bf16_4d(CUtensorMap *map, const void *base, const uint64_t *dims, const uint64_t *byte_strides,
-                              const uint32_t *box) {
+cudaError_t make_tmap_4d(CUtensorMap *map, const void *base, const uint64_t *dims, const uint64_t *byte_strides,
+                         const uint32_t *box, bool f32) {
     const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (encode == nullptr) return cudaErrorNotSupported;
     cuuint64_t gdim[4], gstr[3];
     cuuint32_t bdim[4], estr[4] = {1, 1, 1, 1};
     for (int i = 0; i < 4; ++i) gdim[i] = dims[i], bdim[i] = box[i];
     for (int i = 0; i < 3; ++i) gstr[i] = byte_strides[i];
-    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), gdim, gstr, bdim, estr,
+    const CUresult r = encode(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                              const_cast<void *>(base), gdim, gstr, bdim, estr,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;

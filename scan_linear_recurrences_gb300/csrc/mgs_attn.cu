@@ -347,6 +347,35 @@ __global__ void attn_group_sum_kernel(const float *__restrict__ in, TO *__restri
     }
 }
 
+// fp32 as three bf16 tensors: x = a + b + c, each the rest rounded (24 bits).
+struct SplitSet {
+    const float *in[4];
+    bf16 *out[4];
+    int64_t st[4][3];
+    int heads[4];
+    int64_t B, T;
+};
+template <int D>
+__global__ void __launch_bounds__(256) attn_split_kernel(const __grid_constant__ SplitSet set) {
+    const int which = blockIdx.y, heads = set.heads[which];
+    const int64_t rows = set.B * set.T * heads, n4 = rows * (D / 4), plane = rows * D;
+    const float *in = set.in[which];
+    bf16 *out = set.out[which];
+    for (int64_t e = int64_t(blockIdx.x) * 256 + threadIdx.x; e < n4; e += int64_t(gridDim.x) * 256) {
+        const int64_t row = e / (D / 4), bt = row / heads, b = bt / set.T;
+        const int c = 4 * int(e - row * (D / 4));
+        const float4 x = *reinterpret_cast<const float4 *>(in + b * set.st[which][0] + (bt - b * set.T) * set.st[which][1] +
+                                                           (row - bt * heads) * set.st[which][2] + c);
+        float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int m = 0; m < 3; ++m) {
+            const uint2 t = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+            *reinterpret_cast<uint2 *>(out + m * plane + 4 * e) = t;
+            v[0] -= bf_lo(t.x), v[1] -= bf_hi(t.x), v[2] -= bf_lo(t.y), v[3] -= bf_hi(t.y);
+        }
+    }
+}
+
 // One token.  A block holds 32 columns of one head's state: 8 threads across
 // (float4), 32 groups of D / 32 rows; the rows' products with q are summed in
 // shared memory.  Bound by the state's bytes, read and written once.
@@ -402,9 +431,10 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------- host side
 // The tensor-core walk takes bf16 tensors whose steps, heads and batch rows lie
-// apart in memory (a TMA tensor map has no zero strides).
+// apart in memory (a TMA tensor map has no zero strides), and fp32 with heads
+// of 64 (three terms of wider ones have no room in shared memory).
 bool mma_takes(const mgs_attention_shape &sh, bool backward) {
-    if (sh.dtype != MGS_BF16) return false;
+    if (sh.dtype != MGS_BF16) return sh.D == 64;
     auto apart = [&](const int64_t (&st)[3], int64_t heads) {
         return (sh.B == 1 || st[0] > 0) && (sh.T == 1 || st[1] > 0) && (heads == 1 || st[2] > 0);
     };
@@ -420,7 +450,7 @@ struct Plan {
 Plan plan_of(const mgs_attention_shape &sh, int walks) {
     Plan p;
     p.mma = mma_takes(sh, walks == 3);
-    p.parts = p.mma && sh.D == 128 ? 2 : 1;
+    p.parts = p.mma && (sh.D == 128 || sh.dtype == MGS_F32) ? 2 : 1;
     p.lanes = sh.B * sh.H;
     p.chunks = (sh.T + kAttnChunk - 1) / kAttnChunk;
     // Segments of the time axis: as many as fill the 152 SMs with blocks (one
@@ -428,7 +458,7 @@ Plan plan_of(const mgs_attention_shape &sh, int walks) {
     // where the lanes alone leave at least half of them idle: the state-only
     // walk costs about half of a full one.  None shorter than four chunks,
     // below which its two more launches cost what it gains.
-    const int64_t units = p.mma && sh.D == 64 ? sh.B * ((sh.H + 1) / 2) : p.lanes;
+    const int64_t units = p.mma && sh.D == 64 && sh.dtype == MGS_BF16 ? sh.B * ((sh.H + 1) / 2) : p.lanes;
     const int64_t want = 152 * (p.mma || sh.D == 128 ? 1 : 4);
     int64_t n = units * walks > 0 ? want / (units * walks) : 1;
     if (n > p.chunks / 4) n = p.chunks / 4;
@@ -442,6 +472,10 @@ Plan plan_of(const mgs_attention_shape &sh, int walks) {
 }
 
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+// fp32 for the tensor cores: a tensor's three terms
+size_t split_bytes(const mgs_attention_shape &sh, const Plan &p, int64_t heads) {
+    return p.mma && sh.dtype == MGS_F32 ? up256(size_t(sh.B) * sh.T * heads * sh.D * 6) : 0;
+}
 size_t seg_bytes(const Plan &p, int D) {  // one walk's segment states and their sums of g
     return p.nseg > 1 ? up256(size_t(p.lanes) * p.nseg * (size_t(D) * D + 1) * 4) : 0;
 }
@@ -477,16 +511,45 @@ AttnSet set_of(const mgs_attention_shape &sh, const Plan &p, const float *g, con
     return s;
 }
 
+// The terms of fp32 tensors, in the workspace; what the walks read of the others stays.
+struct Splitter {
+    const mgs_attention_shape &sh;
+    const Plan &p;
+    Carve &ws;
+    SplitSet set = {};
+    int n = 0;
+    // p, its strides and, for fp32, their replacement
+    const void *take(const void *in, const int64_t (&st)[3], int64_t heads, int64_t (&to)[3]) {
+        copy3(to, st);
+        const size_t bytes = split_bytes(sh, p, heads);
+        if (bytes == 0) return in;
+        set.in[n] = static_cast<const float *>(in);
+        set.out[n] = ws.take<bf16>(bytes);
+        copy3(set.st[n], st);
+        set.heads[n] = int(heads);
+        dense(to, sh.T, heads, sh.D);
+        return set.out[n++];
+    }
+    cudaError_t run(cudaStream_t s) {
+        if (n == 0) return cudaSuccess;
+        set.B = sh.B, set.T = sh.T;
+        const int64_t most = sh.B * sh.T * sh.H * (sh.D / 4);
+        attn_split_kernel<64><<<dim3(unsigned(min64((most + 255) / 256, 152 * 16)), unsigned(n)), 256, 0, s>>>(set);
+        return cudaGetLastError();
+    }
+};
+
 cudaError_t run_walks(AttnSet &set, int walks, const mgs_attention_shape &sh, const Plan &p, Carve &ws,
                       cudaStream_t s) {
     cudaError_t e;
-    // Of the gradients' walks the first two feed the decay's, whose sums want every
+    // (fp32 has three terms everywhere.)  Of the gradients' walks the first two feed the decay's, whose sums want every
     // digit of fp32; dv, and the attention itself, are rounded to the type.
     auto walk = [&](bool state_only) {
         if (!p.mma) return launch_attn_rec(set, walks, sh.D, sh.dtype, state_only, s);
-        if (walks == 1 || state_only) return launch_attn_mma(set, 0, walks, sh.D, 1, state_only, s);
-        const cudaError_t e = launch_attn_mma(set, 0, 2, sh.D, 3, false, s);
-        return e != cudaSuccess ? e : launch_attn_mma(set, 2, 1, sh.D, 1, false, s);
+        if (walks == 1 || state_only || sh.dtype == MGS_F32)
+            return launch_attn_mma(set, 0, walks, sh.D, sh.dtype, 1, state_only, s);
+        const cudaError_t e = launch_attn_mma(set, 0, 2, sh.D, sh.dtype, 3, false, s);
+        return e != cudaSuccess ? e : launch_attn_mma(set, 2, 1, sh.D, sh.dtype, 1, false, s);
     };
     if (set.nseg > 1) {
         for (int i = 0; i < walks; ++i) set.w[i].seg_in = set.w[i].seg_out = ws.take<float>(seg_bytes(p, sh.D));
@@ -523,6 +586,7 @@ cudaError_t launch_attn_rec(const AttnSet &set, int nwalks, int D, int dtype, bo
 size_t attn_workspace_bytes(const mgs_attention_shape &sh, bool backward) {
     const Plan p = plan_of(sh, backward ? 3 : 1);
     size_t n = seg_bytes(p, sh.D) * (backward ? 3 : 1);
+    n += 2 * split_bytes(sh, p, sh.Hk) + split_bytes(sh, p, sh.H) * (backward ? 2 : 1);
     if (backward) {
         const size_t rows = size_t(sh.B) * sh.T * sh.H;
         n += 2 * up256(rows * 4 * p.parts);                                                     // row products
@@ -540,8 +604,11 @@ cudaError_t launch_attn_fwd(const mgs_attention_shape &sh, const void *q, const 
     Carve carve{static_cast<char *>(ws)};
     AttnSet set = set_of(sh, p, g, ctl);
     AttnWalk &w = set.w[0];
-    w.q = q, w.k = k, w.v = v, w.out = o;
-    copy3(w.qs, sh.q_stride), copy3(w.ks, sh.k_stride), copy3(w.vs, sh.v_stride);
+    Splitter split{sh, p, carve};
+    w.q = split.take(q, sh.q_stride, sh.Hk, w.qs), w.k = split.take(k, sh.k_stride, sh.Hk, w.ks);
+    w.v = split.take(v, sh.v_stride, sh.H, w.vs), w.out = o;
+    const cudaError_t e = split.run(s);
+    if (e != cudaSuccess) return e;
     dense(w.os, sh.T, sh.H, sh.D);
     w.qdiv = w.kdiv = int(sh.H / sh.Hk);
     w.s_in = S0, w.s_out = ST;
@@ -566,21 +633,27 @@ cudaError_t launch_attn_bwd(const mgs_attention_shape &sh, const void *q, const 
 
     AttnSet set = set_of(sh, p, g, ctl);
     AttnWalk &a = set.w[0], &r = set.w[1], &c = set.w[2];
+    Splitter split{sh, p, carve};
+    int64_t qs[3], ks[3], vs[3], gs[3];
+    const void *tq = split.take(q, sh.q_stride, sh.Hk, qs), *tk = split.take(k, sh.k_stride, sh.Hk, ks);
+    const void *tv = split.take(v, sh.v_stride, sh.H, vs), *tg = split.take(go, sh.do_stride, sh.H, gs);
+    cudaError_t e = split.run(s);
+    if (e != cudaSuccess) return e;
     // dq = scale S do: the walk of (do, v, k) on S^T
-    a.q = go, a.k = v, a.v = k, a.x = q;
-    copy3(a.qs, sh.do_stride), copy3(a.ks, sh.v_stride), copy3(a.vs, sh.k_stride), copy3(a.xs, sh.q_stride);
+    a.q = tg, a.k = tv, a.v = tk, a.x = q;
+    copy3(a.qs, gs), copy3(a.ks, vs), copy3(a.vs, ks), copy3(a.xs, sh.q_stride);
     a.vdiv = a.xdiv = group;
     a.s_in = S0, a.s_in_t = 1, a.o_scale = sh.scale;
     a.row_dot = u, a.ckpt = ends ? ckS : nullptr;
     // dk = R v: the reverse walk of (v, do, q) on R^T
-    r.q = v, r.k = go, r.v = q, r.x = k;
-    copy3(r.qs, sh.v_stride), copy3(r.ks, sh.do_stride), copy3(r.vs, sh.q_stride), copy3(r.xs, sh.k_stride);
+    r.q = tv, r.k = tg, r.v = tq, r.x = k;
+    copy3(r.qs, vs), copy3(r.ks, gs), copy3(r.vs, qs), copy3(r.xs, sh.k_stride);
     r.vdiv = r.xdiv = group;
     r.s_in = gST, r.s_in_t = 1, r.kv_scale = sh.scale, r.rev = 1;
     r.row_dot = wd, r.ckpt = ends ? ckR : nullptr;
     // dv = R^T k: the reverse walk of (k, q, do) on R
-    c.q = k, c.k = q, c.v = go, c.out = dv;
-    copy3(c.qs, sh.k_stride), copy3(c.ks, sh.q_stride), copy3(c.vs, sh.do_stride);
+    c.q = tk, c.k = tq, c.v = tg, c.out = dv;
+    copy3(c.qs, ks), copy3(c.ks, qs), copy3(c.vs, gs);
     c.qdiv = c.kdiv = group;
     c.s_in = gST, c.s_out = dS0, c.kv_scale = sh.scale, c.rev = 1;
     dense(c.os, sh.T, sh.H, sh.D);
@@ -588,8 +661,7 @@ cudaError_t launch_attn_bwd(const mgs_attention_shape &sh, const void *q, const 
     dense(a.os, sh.T, sh.H, sh.D), dense(r.os, sh.T, sh.H, sh.D);
     a.out = group > 1 ? static_cast<void *>(dqf) : dq, a.out_f32 = group > 1;
     r.out = group > 1 ? static_cast<void *>(dkf) : dk, r.out_f32 = group > 1;
-    cudaError_t e = run_walks(set, 3, sh, p, carve, s);
-    if (e != cudaSuccess) return e;
+    if ((e = run_walks(set, 3, sh, p, carve, s)) != cudaSuccess) return e;
     attn_dg_kernel<<<unsigned(p.lanes * p.spans), 256, 0, s>>>(u, wd, p.parts, ends ? ckS : nullptr, ckR,
                                                               sh.fixed_decay ? nullptr : dg,
                                                               sh.fixed_decay ? part : nullptr, sh.T, sh.H, p.spans,

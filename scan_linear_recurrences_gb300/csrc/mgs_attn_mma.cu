@@ -14,7 +14,10 @@
 // fp32, and stays it), P and S as one where the output is rounded to bf16
 // anyway, as three where <out, x> goes into the decay's gradient (TERMS).
 //
-// Heads of 64 go two to a block: panel p of a tile (64 columns) is head p; the
+// fp32 (heads of 64) comes as three bf16 tensors whose sum it is, so that every
+// operand has three terms and a product six pairs of them.
+//
+// Heads of 64 in bf16 go two to a block: panel p of a tile (64 columns) is head p; the
 // state's product is formed for both at once and its two diagonal blocks used.
 //
 // Roles of the 20 warps (warp w reaches TMEM lanes 32 (w % 4) ..):
@@ -34,12 +37,13 @@
 #include "mgs_umma.cuh"
 
 #include <atomic>
+#include <type_traits>
 
 namespace mgs {
 namespace {
 
 constexpr int C = 128;
-constexpr int kTile = 32768, kPanel = 16384;   // a tile: two panels of 128 rows x 64 bf16
+constexpr int kPanel = 16384;                  // a panel of a tile: 128 rows x 64 bf16
 constexpr int kThreads = 20 * 32;              // five warpgroups
 // Registers a thread: the kernel is launched with kRegs for each; the last
 // warpgroup gives up what the two of the rows take more.
@@ -54,22 +58,25 @@ constexpr int NG = C / GT;
 //   the weighted keys of a chunk, three terms of 64 columns, 320..511.
 // P V goes where it finds room: with one term and one head in A's place (P has been
 // made of it), else in X, once the state's product is in registers.
-template <int D, int TERMS>
+template <int D, int TERMS, int IN>
 struct Tmem {
     static constexpr bool over_a = D == 128 && TERMS == 1;
     static constexpr uint32_t A = 0, P = TERMS == 1 ? 128 : 0, X = 192, O = over_a ? 0 : 192, W = 320;
 };
 
-template <int D, int TERMS>
+template <int D, int TERMS, int IN>
 struct Smem {
-    static constexpr int NH = D == 64 ? 2 : 1;
-    static constexpr int sterm = D == 64 ? kPanel : kTile;          // one term of the state operand
-    static constexpr int NK = 2, NQ = TERMS == 1 ? 2 : 1, NV = TERMS == 1 || D == 64 ? 2 : 1;
-    static constexpr int k = TERMS * sterm, q = k + NK * kTile, v = q + NQ * kTile, arr = v + NV * kTile;
+    static_assert(IN == 1 || (D == 64 && TERMS == 3), "fp32: heads of 64, every operand in three terms");
+    static constexpr int NH = D == 64 && IN == 1 ? 2 : 1;           // heads of a block
+    static constexpr int tile = IN == 1 ? 2 * kPanel : IN * kPanel;  // a tile: halves, heads or terms in its panels
+    static constexpr int sterm = IN == 3 ? kPanel / 2 : D == 64 ? kPanel : 2 * kPanel;  // a term of the state operand
+    static constexpr int NK = 2, NQ = TERMS == 1 ? 2 : 1, NV = IN == 1 && (TERMS == 1 || D == 64) ? 2 : 1;
+    static constexpr int k = TERMS * sterm, q = k + NK * tile, v = q + NQ * tile, arr = v + NV * tile;
     // per head: G (high and low parts), the column factors and the state weights of the 128 steps
     static constexpr int bars = arr + NH * 4 * C * 4;
     static constexpr int walk = bars + 256;                         // the block's AttnWalk
     static constexpr size_t bytes = size_t(walk) + sizeof(AttnWalk);
+    static_assert(k % 1024 == 0, "swizzled tiles");
     static_assert(bytes <= 232448, "shared memory of an SM");
 };
 
@@ -160,19 +167,21 @@ __device__ __forceinline__ void add2(float &h, float &l, float a, float b) {
     l = lo - (h - s);
 }
 
-template <int D, int TERMS>
+template <int D, int TERMS, int IN>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_mma_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnSet set, int state_only) {
-    using L = Smem<D, TERMS>;
-    using M = Tmem<D, TERMS>;
-    constexpr int NH = L::NH, SC = D == 64 ? 32 : 64;  // state columns of a thread
+    using L = Smem<D, TERMS, IN>;
+    using M = Tmem<D, TERMS, IN>;
+    constexpr int NH = L::NH;
+    constexpr int SC = D / 2;               // state columns of a thread
+    constexpr int OC = NH == 2 ? 64 : D / 2;  // output columns of a thread
     extern __shared__ __align__(1024) unsigned char sm[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);
     uint64_t *k_full = bars, *k_empty = bars + 2, *q_full = bars + 4, *q_empty = bars + 6, *v_full = bars + 8,
              *v_empty = bars + 10, *w_full = bars + 12, *o_ready = bars + 14;
     uint64_t *a_done = bars + 16, *p_ready = bars + 17, *qs_done = bars + 18, *o_done = bars + 19, *o_free = bars + 20,
              *s_ready = bars + 21, *kv_done = bars + 22, *kv_free = bars + 23, *g_full = bars + 24, *g_empty = bars + 25,
-             *a_read = bars + 28, *drained = bars + 29;
+             *a_read = bars + 28, *drained = bars + 29, *w_full2 = bars + 30;
     uint32_t *slot = reinterpret_cast<uint32_t *>(bars + 26);
     float *total = reinterpret_cast<float *>(slot + 2);  // [NH]: the chunk's decay
 
@@ -198,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&k_full[i], 1), mbar_init(&q_full[i], 1), mbar_init(&v_full[i], 1);
             mbar_init(&k_empty[i], 8);  // the rows' warps, who stage the output in it at the end
             mbar_init(&q_empty[i], 1), mbar_init(&v_empty[i], 1);
-            mbar_init(&w_full[i], 8);
+            mbar_init(&w_full[i], 8), mbar_init(&w_full2[i], 8);
         }
         mbar_init(a_done, 1), mbar_init(p_ready, 8), mbar_init(o_ready, 8), mbar_init(qs_done, 1), mbar_init(o_done, 1), mbar_init(o_free, 8);
         mbar_init(s_ready, 8), mbar_init(kv_done, 1), mbar_init(kv_free, 8);
@@ -235,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int isgn = rev ? -1 : 1;
         const uint32_t in = rev ? ~0u << lane : ~0u >> (31 - lane);  // columns of the diagonal's block that count
         // the output's head, and the weights of its rows of Q S
-        const int h = NH == 2 ? h0 + hh : h0, col = NH == 2 ? 0 : 64 * hh;
+        const int h = NH == 2 ? h0 + hh : h0, col = NH == 2 ? 0 : OC * hh;
         const float *Go = Gh + (NH == 2 ? hh * 4 * C : 0);
         const int lrow = lane >> 3, lch = lane & 7;  // whole lines: 4 rows of 8 pieces of 16 bytes at a time
         bool ok = ok0;
@@ -243,15 +252,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int it = 0; it < (state_only ? 0 : n) && ok; ++it) {
             const int c = chunk_of(it);
             if (!(ok = wwait(g_full, it))) break;
-            float o1[64];  // Q S, scaled by rows: the part of the output that comes from the state
+            float o1[OC];  // Q S, scaled by rows: the part of the output that comes from the state
             const float ri = os * ex2_approx(rev ? (Go[i] - Go[C - 1]) + (Go[C + i] - Go[2 * C - 1]) : Go[i] + Go[C + i]);
             auto from_state = [&]() {
                 if (!wwait(qs_done, it)) return false;
                 tc_fence_after();
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
+                for (int p = 0; p < OC / 32; ++p) {
                     float x[32];
-                    tmem_ld32(tq + M::X + 64 * hh + 32 * p, x);
+                    tmem_ld32(tq + M::X + OC * hh + 32 * p, x);
 #pragma unroll
                     for (int u = 0; u < 32; u += 2) {
                         const float2 y = __fmul2_rn(make_float2(x[u], x[u + 1]), make_float2(ri, ri));
@@ -368,24 +377,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             // bytes), and stored by TMA, which drops rows past the end.  x comes in the same
             // place before: whole lines instead of a thread's row.
             const int64_t tw = int64_t(c) * C + 32 * wb;  // the warp's first row
-            unsigned char *stage = sm + L::k + (it % L::NK) * kTile + hh * kPanel + 32 * wb * 128;
+            unsigned char *stage = sm + L::k + (it % L::NK) * L::tile + hh * kPanel + 32 * wb * 128;
             unsigned char *mine = stage + lane * 128;
             const int live = h < H ? min(32, T - int(tw)) : 0;  // rows that exist (may be negative)
             auto line = [&](int u) {
                 return reinterpret_cast<uint4 *>(stage + (4 * u + lrow) * 128 + ((lch ^ ((4 * u + lrow) & 7)) << 4));
             };
             auto own = [&](int u) { return reinterpret_cast<uint4 *>(mine + ((u ^ (lane & 7)) << 4)); };
-            const bf16 *px = nullptr;
+            using TI = typename std::conditional<IN == 1, bf16, float>::type;
+            constexpr int V = kVec<TI>;
+            const TI *px = nullptr;
             if (TERMS > 1 && w.row_dot) {
-                px = static_cast<const bf16 *>(w.x) + b * w.xs[0] + tw * w.xs[1] + (h / w.xdiv) * w.xs[2] + col;
+                px = static_cast<const TI *>(w.x) + b * w.xs[0] + tw * w.xs[1] + (h / w.xdiv) * w.xs[2] + col;
                 if (lane < live) asm volatile("prefetch.global.L2 [%0];" ::"l"(px + lane * w.xs[1]));
             }
             if (!(ok = wwait(o_done, it * NH + NH - 1))) break;
             tc_fence_after();
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
+            for (int p = 0; p < OC / 32; ++p) {
                 float o[32];
-                tmem_ld32(tq + M::O + 64 * hh + 32 * p, o);
+                tmem_ld32(tq + M::O + OC * hh + 32 * p, o);
 #pragma unroll
                 for (int u = 0; u < 32; u += 2) {
                     const float2 y = __ffma2_rn(make_float2(o[u], o[u + 1]), make_float2(os, os),
@@ -402,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int u = 0; u < 8; ++u)
                         xv[u] = 4 * u + lrow < live
-                                    ? *reinterpret_cast<const uint4 *>(px + (4 * u + lrow) * w.xs[1] + 8 * lch)
+                                    ? *reinterpret_cast<const uint4 *>(px + (4 * u + lrow) * w.xs[1] + V * lch)
                                     : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                     for (int u = 0; u < 8; ++u) *line(u) = xv[u];
@@ -411,27 +422,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float2 dot = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
-                    float xx[8];
+                    float xx[V];
                     unpack(*own(u), xx);
 #pragma unroll
-                    for (int m = 0; m < 8; m += 2)
-                        dot = __ffma2_rn(make_float2(o1[8 * u + m], o1[8 * u + m + 1]), make_float2(xx[m], xx[m + 1]), dot);
+                    for (int m = 0; m < V; m += 2)
+                        dot = __ffma2_rn(make_float2(o1[V * u + m], o1[V * u + m + 1]), make_float2(xx[m], xx[m + 1]), dot);
                 }
                 __syncwarp();
-                // heads of 128: each half of the columns leaves its own product
+                // one head in the block: each half of the columns leaves its own product
                 if (lane < live)
                     w.row_dot[(NH == 2 ? 0 : hh * set.B * set.T * set.H) + (b * set.T + tw + lane) * set.H + h] =
                         dot.x + dot.y;
             }
-            if (w.out_f32) {
+            if (IN == 1 && w.out_f32) {
                 // heads that share keys: each one's gradient in fp32, to be summed
                 if (lane < live) {
                     float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(w.out) + b * w.os[0] +
                                                             (tw + lane) * w.os[1] + h * w.os[2] + col);
 #pragma unroll
-                    for (int u = 0; u < 16; ++u)
+                    for (int u = 0; u < OC / 4; ++u)
                         to[u] = make_float4(o1[4 * u], o1[4 * u + 1], o1[4 * u + 2], o1[4 * u + 3]);
                 }
+            } else if constexpr (IN == 3) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    *reinterpret_cast<float4 *>(own(u)) =
+                        make_float4(o1[4 * u], o1[4 * u + 1], o1[4 * u + 2], o1[4 * u + 3]);
             } else {
 #pragma unroll
                 for (int u = 0; u < 8; ++u)
@@ -440,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0 && !w.out_f32 && live > 0) tma_store_4d(&maps.o[blockIdx.y], col, int(tw), h, b, stage);
+            if (lane == 0 && (IN == 3 || !w.out_f32) && live > 0) tma_store_4d(&maps.o[blockIdx.y], col, int(tw), h, b, stage);
             if (lane == 0) bulk_commit();
         }
         if (!ok && lane == 0) record_error(ctl, ERR_MBAR_TIMEOUT);
@@ -452,7 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int grp = (warp - 8) >> 2, dk = 32 * (warp & 3) + lane;
         const int hp = NH == 2 ? dk >> 6 : 0, h = h0 + hp;
         const int row = NH == 2 ? dk & 63 : dk, col = SC * grp;  // the head's state: row, first column
-        const bool live = h < H;
+        // fp32: 64 key rows in 128 lanes, of which the upper half stands idle
+        const bool mine = NH * D == 128 || dk < D, live = h < H && mine;
         const int64_t ln = int64_t(b) * H + h;
         float s[SC];
         {
@@ -486,40 +503,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lc = ((32 * (warp & 3)) & 63) / 8 + ((lane >> 3) & 1);
         const uint32_t kbase = smem_addr(sm + L::k) + uint32_t((32 * (warp & 3)) >> 6) * kPanel + lr * 128;
         const uint32_t kx0 = uint32_t((lc ^ (lr & 7)) << 4), kx1 = uint32_t(((lc + 2) ^ (lr & 7)) << 4);
+        auto put_state = [&](float *to) {
+#pragma unroll
+            for (int u = 0; u < SC; u += 4)
+                *reinterpret_cast<float4 *>(to + row * D + col + u) = make_float4(s[u], s[u + 1], s[u + 2], s[u + 3]);
+        };
+        const bool marks = w.ckpt != nullptr;
+        float decay = 0.f, next_decay = 0.f;  // of the chunk whose product is taken, and of the walked one
         bool ok = ok0;
 #pragma unroll 1
         for (int it = 0; ok; ++it) {
             // States that are kept: at a span's end (in reverse that is the state before the
             // chunk is walked), and at the walk's end.
-            const int ce = rev ? chunk_of(it) : chunk_of(it - 1);
-            const bool mark = !state_only && w.ckpt != nullptr && (rev ? it < n : it > 0) &&
-                              ((ce + 1) % (kAttnSpan / C) == 0 || (ce + 1) * C >= T);
-            if (live && (mark || it == n)) {
-#pragma unroll 1
-                for (int k = 0; k < 2; ++k) {
-                    float *to = nullptr;
-                    if (k == 0) {
-                        if (mark) to = w.ckpt + (ln * set.spans + ce / (kAttnSpan / C)) * D * D;
-                    } else if (it == n) {
-                        if (state_only)
-                            to = w.seg_out + (ln * nseg + seg) * D * D;
-                        else if (w.s_out && seg == (rev ? 0 : nseg - 1))
-                            to = w.s_out + ln * D * D;
-                    }
-                    if (to == nullptr) continue;
-#pragma unroll
-                    for (int u = 0; u < SC; u += 4)
-                        *reinterpret_cast<float4 *>(to + row * D + col + u) =
-                            make_float4(s[u], s[u + 1], s[u + 2], s[u + 3]);
+            if (!state_only) {
+                const int ce = rev ? chunk_of(it) : chunk_of(it - 1);
+                if (marks && live && (rev ? it < n : it > 0) &&
+                    ((ce + 1) % (kAttnSpan / C) == 0 || (ce + 1) * C >= T))
+                    put_state(w.ckpt + (ln * set.spans + ce / (kAttnSpan / C)) * D * D);
+                __syncwarp();
+                if (it == n) {
+                    if (live && w.s_out && seg == (rev ? 0 : nseg - 1)) put_state(w.s_out + ln * D * D);
+                    break;
                 }
             }
-            __syncwarp();
-            if (it == n) break;
             if (!state_only) {
                 // the state as the operand of Q S (its reader of the chunk before is done)
                 if (it > 0 && !(ok = wwait(qs_done, it - 1))) break;
-                unsigned char *base = sm + (NH == 2 ? 0 : grp * kPanel) + dk * 128;
-                const int ch0 = NH == 2 ? 4 * grp : 0;
+                unsigned char *base = sm + (D == 64 ? 0 : grp * kPanel) + dk * 128;
+                const int ch0 = D == 64 ? 4 * grp : 0;
+                if (mine)
 #pragma unroll
                 for (int u = 0; u < SC; u += 8) {
                     uint32_t t0[TERMS], t1[TERMS], t2[TERMS], t3[TERMS];
@@ -536,60 +548,89 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mb_arrive(s_ready);
             }
+            if (it < n) {
             if (!(ok = wwait(&k_full[it % L::NK], it / L::NK) && wwait(g_full, it))) break;
-            const uint32_t kt = kbase + (it % L::NK) * kTile;
+            const uint32_t kt = kbase + (it % L::NK) * L::tile;
             const float *wt = Gh + hp * 4 * C + 3 * C + 2 * (lane & 3);
-            const float decay = total[hp];
+            next_decay = total[hp];
+            if (!state_only) decay = next_decay;
+            // the state-only walk has room for two chunks' keys, each with barriers of its own (it
+            // makes the next chunk's before this one's have been asked for)
+            const bool second = state_only && (it & 1);
+            const uint32_t wcol = tq + (second ? M::A : M::W);
             // the chunk's weighted keys, half of it at a time, the groups of 16 steps shared
             // between the two warpgroups
 #pragma unroll 1
             for (int i = 0; i < NG / 2; ++i) {
                 const int gi = (i >> 1) * (NG / 2) + grp * (NG / 4) + (i & 1);
-                uint32_t r[2][4];  // key rows 0..15 and 16..31 of the warp
-                ldmatrix_x4_trans(kt + gi * (GT * 128) + kx0, r[0]);
-                ldmatrix_x4_trans(kt + gi * (GT * 128) + kx1, r[1]);
                 const float2 w0 = *reinterpret_cast<const float2 *>(wt + gi * GT);
                 const float2 w1 = *reinterpret_cast<const float2 *>(wt + gi * GT + 8);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    uint32_t t[3][4];
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        uint32_t a[3];
-                        split<3>(__fmul2_rn(make_float2(bf_lo(r[x][m]), bf_hi(r[x][m])), m < 2 ? w0 : w1), a);
-                        t[0][m] = a[0], t[1][m] = a[1], t[2][m] = a[2];
-                    }
-#pragma unroll
-                    for (int m = 0; m < 3; ++m)
-                        tmem_put_16x8(tq + (uint32_t(16 * x) << 16) + M::W + 64 * m + 8 * gi, t[m]);
+                uint32_t r[2][4];  // key rows 0..15 and 16..31 of the warp
+                if (IN == 1) {
+                    ldmatrix_x4_trans(kt + gi * (GT * 128) + kx0, r[0]);
+                    ldmatrix_x4_trans(kt + gi * (GT * 128) + kx1, r[1]);
                 }
+                if (mine)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t t[3][4], r1[4], r2[4];
+                        if (IN == 3) {  // a key's three terms add up to it
+                            const uint32_t at = kt + gi * (GT * 128) + (x ? kx1 : kx0);
+                            ldmatrix_x4_trans(at, r[x]);
+                            ldmatrix_x4_trans(at + kPanel, r1);
+                            ldmatrix_x4_trans(at + 2 * kPanel, r2);
+                        }
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            uint32_t a[3];
+                            float2 y = make_float2(bf_lo(r[x][m]), bf_hi(r[x][m]));
+                            if (IN == 3)
+                                y = __fadd2_rn(y, __fadd2_rn(make_float2(bf_lo(r1[m]), bf_hi(r1[m])),
+                                                             make_float2(bf_lo(r2[m]), bf_hi(r2[m]))));
+                            split<3>(__fmul2_rn(y, m < 2 ? w0 : w1), a);
+                            t[0][m] = a[0], t[1][m] = a[1], t[2][m] = a[2];
+                        }
+#pragma unroll
+                        for (int m = 0; m < 3; ++m)
+                            tmem_put_16x8(wcol + (uint32_t(16 * x) << 16) + 64 * m + 8 * gi, t[m]);
+                    }
                 if (i & 1) {
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mb_arrive(&w_full[i >> 1]);
+                    if (lane == 0) mb_arrive(&(second ? w_full2 : w_full)[i >> 1]);
                 }
             }
             if (lane == 0) {
                 mb_arrive(g_empty);
                 if (state_only) mb_arrive(&k_empty[it % L::NK]);
             }
-            if (!(ok = wwait(kv_done, it))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int u = 0; u < SC; u += 16) {
-                float x[16];
-                tmem_ld16(tq + M::X + (NH == 2 ? 64 * hp : 0) + col + u, x);
-#pragma unroll
-                for (int m = 0; m < 16; m += 2) {
-                    const float2 y = __ffma2_rn(make_float2(decay, decay), make_float2(s[u + m], s[u + m + 1]),
-                                                make_float2(x[m], x[m + 1]));
-                    s[u + m] = y.x, s[u + m + 1] = y.y;
-                }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mb_arrive(kv_free);
+            // the state-only walk makes the next chunk's keys before it takes this one's product
+            const int j = state_only ? it - 1 : it;
+            if (j >= 0) {
+                if (!(ok = wwait(kv_done, j))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int u = 0; u < SC; u += 16) {
+                    float x[16];
+                    tmem_ld16(tq + M::X + (NH == 2 ? 64 * hp : 0) + col + u, x);
+#pragma unroll
+                    for (int m = 0; m < 16; m += 2) {
+                        const float2 y = __ffma2_rn(make_float2(decay, decay), make_float2(s[u + m], s[u + m + 1]),
+                                                    make_float2(x[m], x[m + 1]));
+                        s[u + m] = y.x, s[u + m + 1] = y.y;
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mb_arrive(kv_free);
+            }
+            decay = next_decay;
+            if (state_only && it == n) {
+                if (live) put_state(w.seg_out + (ln * nseg + seg) * D * D);
+                break;
+            }
         }
         if (!ok && lane == 0) record_error(ctl, ERR_MBAR_TIMEOUT);
     } else {
@@ -599,8 +640,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 16) {
         // ------------------------------------------------ the products
         if (elect_one()) {
-            constexpr uint32_t id_k = umma_idesc_bf16(128, 128, false), id_mn = umma_idesc_bf16(128, 128, true);
+            // N: the steps; the state's columns (of both heads); a head's columns
+            constexpr uint32_t id_k = umma_idesc_bf16(128, 128, false), id_mn = umma_idesc_bf16(128, NH * D, true);
             constexpr uint32_t id_o = umma_idesc_bf16(128, D, true);
+            // Products of two sums of three terms: the pairs down to 2^-16 of the first,
+            // (0,0) (0,1) (0,2) (1,0) (1,1) (2,0); a sum with an exact operand: its terms.
+            auto others = [](int m) { return IN == 1 ? 1 : 3 - m; };
             // Descriptors hold addresses in units of 16 bytes: what is issued is one of these
             // plus a short sum, since longer ones between two products cost more time than a
             // product takes (64 cycles at N = 128); rolled loops, whose code stays at hand.
@@ -610,37 +655,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             // K-major step ks of head hp: 32 bytes on in the rows, the next panel after four
             auto koff = [](int ks) { return uint64_t(((ks >> 2) * kPanel + (ks & 3) * 32) >> 4); };
             auto qk = [&](int it, int hp) {
-                const uint64_t q = dQ + uint64_t(((it % L::NQ) * kTile + hp * kPanel) >> 4);
-                const uint64_t k = dK + uint64_t(((it % L::NK) * kTile + hp * kPanel) >> 4);
+                const uint64_t q = dQ + uint64_t(((it % L::NQ) * L::tile + hp * kPanel) >> 4);
+                const uint64_t k = dK + uint64_t(((it % L::NK) * L::tile + hp * kPanel) >> 4);
 #pragma unroll 1
-                for (int ks = 0; ks < KS; ++ks) umma_bf16_ss(tm + M::A, q + koff(ks), k + koff(ks), id_k, ks > 0);
+                for (int m = 0; m < IN; ++m)
+#pragma unroll 1
+                    for (int o = 0; o < others(m); ++o)
+#pragma unroll 1
+                        for (int ks = 0; ks < KS; ++ks)
+                            umma_bf16_ss(tm + M::A, q + koff(ks) + uint64_t(m * (kPanel >> 4)),
+                                         k + koff(ks) + uint64_t(o * (kPanel >> 4)), id_k, m + o + ks > 0);
                 umma_commit(a_done);
             };
             auto qs = [&](int it) {
 #pragma unroll 1
                 for (int hp = 0; hp < NH; ++hp) {
-                    const uint64_t q = dQ + uint64_t(((it % L::NQ) * kTile + hp * kPanel) >> 4);
+                    const uint64_t q = dQ + uint64_t(((it % L::NQ) * L::tile + hp * kPanel) >> 4);
 #pragma unroll 1
                     for (int m = 0; m < TERMS; ++m) {
                         const uint64_t st = dS + uint64_t((m * L::sterm + hp * 8192) >> 4);
 #pragma unroll 1
-                        for (int ks = 0; ks < KS; ++ks)
-                            umma_bf16_ss(tm + M::X + 64 * hp, q + koff(ks), st + uint64_t(ks * 128), id_o, m + ks > 0);
+                        for (int o = 0; o < others(m); ++o)
+#pragma unroll 1
+                            for (int ks = 0; ks < KS; ++ks)
+                                umma_bf16_ss(tm + M::X + 64 * hp, q + koff(ks) + uint64_t(o * (kPanel >> 4)),
+                                             st + uint64_t(ks * 128), id_o, m + o + ks > 0);
                     }
                 }
                 umma_commit(qs_done);
             };
             auto kv = [&](int it, int half) {
-                const uint64_t v = dV + uint64_t(((it % L::NV) * kTile + half * (NG / 2) * 2048) >> 4);
-                const uint32_t a = tm + M::W + half * (NG / 2) * 8;
+                const uint64_t v = dV + uint64_t(((it % L::NV) * L::tile + half * (NG / 2) * 2048) >> 4);
+                const uint32_t a = tm + (state_only && (it & 1) ? M::A : M::W) + half * (NG / 2) * 8;
 #pragma unroll 1
                 for (int i = 0; i < NG / 2; ++i)
 #pragma unroll 1
                     for (int m = 0; m < 3; ++m)
-                        umma_bf16_ts(tm + M::X, a + 64 * m + 8 * i, v + uint64_t(i * 128), id_mn, half + i + m > 0);
+#pragma unroll 1
+                        for (int o = 0; o < others(m); ++o)
+                            umma_bf16_ts(tm + M::X, a + 64 * m + 8 * i, v + uint64_t(i * 128 + o * (kPanel >> 4)), id_mn,
+                                         half + i + m + o > 0);
             };
             auto pv = [&](int it, int hp) {
-                const uint64_t v = dV + uint64_t(((it % L::NV) * kTile + hp * kPanel) >> 4);
+                const uint64_t v = dV + uint64_t(((it % L::NV) * L::tile + hp * kPanel) >> 4);
 #pragma unroll 1
                 for (int m = 0; m < TERMS; ++m) {
                     // one term lies in a row of columns; of three, 32 steps' first and second terms
@@ -648,9 +705,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t p = tm + M::P + (TERMS == 1 ? 0 : m == 2 ? 128 : 16 * m);
                     const uint32_t step = TERMS == 1 || m == 2 ? 16 : 32;
 #pragma unroll 1
-                    for (int ks = 0; ks < C / 16; ++ks)
-                        umma_bf16_ts(tm + M::O + 64 * hp, p + (ks >> 1) * step + 8 * (ks & 1), v + uint64_t(ks * 128), id_o,
-                                     m + ks > 0);
+                    for (int o = 0; o < others(m); ++o)
+#pragma unroll 1
+                        for (int ks = 0; ks < C / 16; ++ks)
+                            umma_bf16_ts(tm + M::O + 64 * hp, p + (ks >> 1) * step + 8 * (ks & 1),
+                                         v + uint64_t(ks * 128 + o * (kPanel >> 4)), id_o, m + o + ks > 0);
                 }
                 umma_commit(o_done);
             };
@@ -672,10 +731,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else if (it > 0 && !(ok = wait(kv_free, it - 1))) {
                     break;
                 }
-                if (!(ok = wait(&v_full[it % L::NV], it / L::NV) && wait(&w_full[0], it))) break;
+                uint64_t *keys = state_only && (it & 1) ? w_full2 : w_full;
+                const uint32_t turn = state_only ? it >> 1 : it;
+                if (!(ok = wait(&v_full[it % L::NV], it / L::NV) && wait(&keys[0], turn))) break;
                 tc_fence_after();
                 kv(it, 0);
-                if (!(ok = wait(&w_full[1], it))) break;
+                if (!(ok = wait(&keys[1], turn))) break;
                 tc_fence_after();
                 kv(it, 1);
                 umma_commit(kv_done);
@@ -712,12 +773,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto fill = [&](int it, int depth, uint64_t *full, uint64_t *empty, int off, const CUtensorMap *m, int div) {
                 const int sl = it % depth;
                 if (it >= depth && !wait(&empty[sl], it / depth - 1)) return false;
-                unsigned char *dst = sm + off + sl * kTile;
-                mbar_arrive_expect_tx(&full[sl], kTile);
+                unsigned char *dst = sm + off + sl * L::tile;
+                mbar_arrive_expect_tx(&full[sl], L::tile);
 #pragma unroll 1
-                for (int p = 0; p < 2; ++p)
-                    tma_load_4d(dst + p * kPanel, m, NH == 2 ? 0 : 64 * p, chunk_of(it) * C,
-                                (NH == 2 ? h0 + p : h0) / div, b, &full[sl]);
+                for (int p = 0; p < L::tile / kPanel; ++p)  // halves of a head, heads, or terms (a batch apart)
+                    tma_load_4d(dst + p * kPanel, m, NH * IN == 1 ? 64 * p : 0, chunk_of(it) * C,
+                                (NH == 2 ? h0 + p : h0) / div, IN == 3 ? b + p * int(set.B) : b, &full[sl]);
                 return true;
             };
             // a block starts with the state as an operand and Q, ends with V
@@ -835,21 +896,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// [B][T][heads][D] bf16 with any strides: boxes of 64 columns x `steps` steps of one head
+// [B][T][heads][D] with any strides: boxes of 128 bytes x `steps` steps of one head
 cudaError_t tile_map(CUtensorMap *m, const void *base, const int64_t (&st)[3], int64_t B, int64_t T, int64_t heads,
-                     int D, uint32_t steps = C) {
+                     int D, int steps, bool f32) {
+    const int es = f32 ? 4 : 2;
     const uint64_t dims[4] = {uint64_t(D), uint64_t(T), uint64_t(heads), uint64_t(B)};
     // a dimension of one element is never stepped over: any legal stride does
-    const uint64_t str[3] = {uint64_t(T > 1 ? st[1] : D) * 2, uint64_t(heads > 1 ? st[2] : D) * 2,
-                             uint64_t(B > 1 ? st[0] : D) * 2};
-    const uint32_t box[4] = {64, steps, 1, 1};
-    return make_tmap_bf16_4d(m, base, dims, str, box);
+    const uint64_t str[3] = {uint64_t(T > 1 ? st[1] : D) * es, uint64_t(heads > 1 ? st[2] : D) * es,
+                             uint64_t(B > 1 ? st[0] : D) * es};
+    const uint32_t box[4] = {128u / es, uint32_t(steps), 1, 1};
+    return make_tmap_4d(m, base, dims, str, box, f32);
 }
 
-template <int D, int TERMS>
+template <int D, int TERMS, int IN>
 cudaError_t go(const AttnMaps &maps, const AttnSet &set, int nwalks, bool state_only, cudaStream_t s) {
-    using L = Smem<D, TERMS>;
-    const void *fn = (const void *)attn_mma_kernel<D, TERMS>;
+    using L = Smem<D, TERMS, IN>;
+    const void *fn = (const void *)attn_mma_kernel<D, TERMS, IN>;
     cudaError_t e = ensure_smem_attr(fn, int(L::bytes));
     if (e != cudaSuccess) return e;
     // the split of the registers counts on this many at launch: with fewer the
@@ -862,30 +924,35 @@ cudaError_t go(const AttnMaps &maps, const AttnSet &set, int nwalks, bool state_
     }
     if (regs.load() != kRegs) return cudaErrorInvalidDeviceFunction;
     const dim3 grid(unsigned(set.B * ((set.H + L::NH - 1) / L::NH) * set.nseg), unsigned(nwalks));
-    attn_mma_kernel<D, TERMS><<<grid, kThreads, L::bytes, s>>>(maps, set, state_only);
+    attn_mma_kernel<D, TERMS, IN><<<grid, kThreads, L::bytes, s>>>(maps, set, state_only);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_attn_mma(const AttnSet &all, int first, int nwalks, int D, int terms, bool state_only,
+cudaError_t launch_attn_mma(const AttnSet &all, int first, int nwalks, int D, int dtype, int terms, bool state_only,
                             cudaStream_t s) {
     AttnMaps maps;
     AttnSet set = all;
     set.first = first;
+    const bool f32 = dtype == MGS_F32;
+    const int64_t B = set.B * (f32 ? 3 : 1);  // fp32 comes as three bf16 tensors behind one another
     cudaError_t e;
     for (int i = 0; i < nwalks; ++i) {
         const AttnWalk &w = set.w[first + i];
-        if ((e = tile_map(&maps.q[i], w.q, w.qs, set.B, set.T, set.H / w.qdiv, D)) != cudaSuccess) return e;
-        if ((e = tile_map(&maps.k[i], w.k, w.ks, set.B, set.T, set.H / w.kdiv, D)) != cudaSuccess) return e;
-        if ((e = tile_map(&maps.v[i], w.v, w.vs, set.B, set.T, set.H / w.vdiv, D)) != cudaSuccess) return e;
-        if (!state_only && !w.out_f32 &&
-            (e = tile_map(&maps.o[i], w.out, w.os, set.B, set.T, set.H, D, 32)) != cudaSuccess)
+        if ((e = tile_map(&maps.q[i], w.q, w.qs, B, set.T, set.H / w.qdiv, D, C, false)) != cudaSuccess) return e;
+        if ((e = tile_map(&maps.k[i], w.k, w.ks, B, set.T, set.H / w.kdiv, D, C, false)) != cudaSuccess) return e;
+        if ((e = tile_map(&maps.v[i], w.v, w.vs, B, set.T, set.H / w.vdiv, D, C, false)) != cudaSuccess) return e;
+        if (!state_only && (f32 || !w.out_f32) &&
+            (e = tile_map(&maps.o[i], w.out, w.os, set.B, set.T, set.H, D, 32, f32)) != cudaSuccess)
             return e;
     }
+    if (f32) return go<64, 3, 3>(maps, set, nwalks, state_only, s);
     if (D == 64)
-        return terms == 1 ? go<64, 1>(maps, set, nwalks, state_only, s) : go<64, 3>(maps, set, nwalks, state_only, s);
-    return terms == 1 ? go<128, 1>(maps, set, nwalks, state_only, s) : go<128, 3>(maps, set, nwalks, state_only, s);
+        return terms == 1 ? go<64, 1, 1>(maps, set, nwalks, state_only, s)
+                          : go<64, 3, 1>(maps, set, nwalks, state_only, s);
+    return terms == 1 ? go<128, 1, 1>(maps, set, nwalks, state_only, s)
+                      : go<128, 3, 1>(maps, set, nwalks, state_only, s);
 }
 
 }  // namespace mgs

@@ -98,9 +98,9 @@ cudaError_t launch_delta_fwd(const float *q, const float *k, const float *v, con
 cudaError_t make_tmap(CUtensorMap *map, const float *base, int rank, const uint64_t *dims,
                       const uint64_t *byte_strides, const uint32_t *box, bool swizzle128 = false);
 
-// The same for bf16, rank 4 (three strides), 128-byte swizzle.
-cudaError_t make_tmap_bf16_4d(CUtensorMap *map, const void *base, const uint64_t *dims, const uint64_t *byte_strides,
-                              const uint32_t *box);
+// The same for fp32 or bf16, rank 4 (three strides), 128-byte swizzle.
+cudaError_t make_tmap_4d(CUtensorMap *map, const void *base, const uint64_t *dims, const uint64_t *byte_strides,
+                         const uint32_t *box, bool f32);
 
 // Sets the dynamic shared-memory limit of `fn` once per device context.
 cudaError_t ensure_smem_attr(const void *fn, int bytes);
