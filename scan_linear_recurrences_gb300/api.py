@@ -267,11 +267,14 @@ def _head_strides(t, name):
 def _apart(t):
     """t, or a dense copy of a broadcast t: the tensor-core kernels load through tensor maps, which have no
     zero strides, and the copy costs less than the kernel without them."""
-    return t.contiguous() if t.numel() and t.dtype == torch.bfloat16 and \
-        any(s == 0 and n > 1 for s, n in zip(t.stride(), t.shape)) else t
+    st = t.stride()
+    if 0 not in st or t.dtype != torch.bfloat16:
+        return t
+    return t.contiguous() if any(s == 0 and n > 1 for s, n in zip(st, t.shape)) else t
 
 
 def _attention_shape(q, k, v, g, scale, grad_o=None):
+    """The checked arguments as the C struct, (B, T, H, Hk, D), and the tensors to pass."""
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a [B,T,Hk,D] tensor")
     if not isinstance(v, torch.Tensor) or v.dim() != 4:
@@ -288,10 +291,13 @@ def _attention_shape(q, k, v, g, scale, grad_o=None):
     _check_typed(g, "g", (H,) if fixed else (B, T, H), torch.float32, dense=fixed, device=dev)
     if grad_o is not None:
         _check_typed(grad_o, "grad_o", v.shape, q.dtype, dense=False, device=dev)
-    return _b.mgs_attention_shape(
+        grad_o = _apart(grad_o)
+    q, k, v = _apart(q), _apart(k), _apart(v)
+    shape = _b.mgs_attention_shape(
         B, T, H, Hk, D, _DTYPES[q.dtype], fixed, D ** -0.5 if scale is None else scale, _head_strides(q, "q"),
         _head_strides(k, "k"), _head_strides(v, "v"), (0, 0, 1) if fixed else g.stride(),
-        _head_strides(grad_o, "grad_o") if grad_o is not None else (0, 0, 0)), (B, T, H, Hk, D)
+        _head_strides(grad_o, "grad_o") if grad_o is not None else (0, 0, 0))
+    return shape, (B, T, H, Hk, D), (q, k, v, grad_o)
 
 
 def _scratch(n, device, stream):
@@ -312,8 +318,7 @@ def linear_attention_fwd(q, k, v, g, S0=None, scale=None, want_state=False, stre
     head h // (H // Hk); any strides of 16 bytes whose heads are contiguous), g [B,T,H] or [H] fp32 (the
     decay's logarithm; -inf starts the state anew), S0 [B,H,D,D] fp32 or None.
     Returns o [B,T,H,D] (and the final state when want_state)."""
-    q, k, v = _apart(q), _apart(k), _apart(v)
-    shape, (B, T, H, Hk, D) = _attention_shape(q, k, v, g, scale)
+    shape, (B, T, H, Hk, D), (q, k, v, _) = _attention_shape(q, k, v, g, scale)
     if S0 is not None:
         _check_typed(S0, "S0", (B, H, D, D), torch.float32, device=q.device)
     o = torch.empty((B, T, H, D), dtype=q.dtype, device=q.device)
@@ -326,8 +331,7 @@ def linear_attention_fwd(q, k, v, g, S0=None, scale=None, want_state=False, stre
 def linear_attention_bwd(q, k, v, g, grad_o, S0=None, grad_ST=None, scale=None, stream=None):
     """Gradients of linear_attention_fwd for L = <grad_o, o> + <grad_ST, S_T>: returns (dq, dk, dv, dg, dS0),
     dS0 None without S0.  dg is [B,T,H], or [H] for a g of one decay a head."""
-    q, k, v, grad_o = _apart(q), _apart(k), _apart(v), _apart(grad_o)
-    shape, (B, T, H, Hk, D) = _attention_shape(q, k, v, g, scale, grad_o)
+    shape, (B, T, H, Hk, D), (q, k, v, grad_o) = _attention_shape(q, k, v, g, scale, grad_o)
     for t, name in ((S0, "S0"), (grad_ST, "grad_ST")):
         if t is not None:
             _check_typed(t, name, (B, H, D, D), torch.float32, device=q.device)

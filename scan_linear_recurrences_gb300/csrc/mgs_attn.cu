@@ -454,15 +454,16 @@ Plan plan_of(const mgs_attention_shape &sh, int walks) {
     p.lanes = sh.B * sh.H;
     p.chunks = (sh.T + kAttnChunk - 1) / kAttnChunk;
     // Segments of the time axis: as many as fill the 152 SMs with blocks (one
-    // block to an SM for the tensor-core walk; the SIMT one wants more warps),
-    // where the lanes alone leave at least half of them idle: the state-only
-    // walk costs about half of a full one.  None shorter than four chunks,
-    // below which its two more launches cost what it gains.
+    // block to an SM for the tensor-core walk; the SIMT one wants more warps).
     const int64_t units = p.mma && sh.D == 64 && sh.dtype == MGS_BF16 ? sh.B * ((sh.H + 1) / 2) : p.lanes;
     const int64_t want = 152 * (p.mma || sh.D == 128 ? 1 : 4);
     int64_t n = units * walks > 0 ? want / (units * walks) : 1;
-    if (n > p.chunks / 4) n = p.chunks / 4;
-    if (n < 2) n = 1;
+    if (n > p.chunks) n = p.chunks;
+    // They cost a state-only walk (half as long as a full one; nearly as long in
+    // the SIMT kernel, which is cut in three or more only) and two more launches, of about four chunks' time together (13 chunks in 5 segments, 30
+    // blocks each: 44 us against 66 in one).
+    const int64_t len = n > 0 ? (p.chunks + n - 1) / n : p.chunks;
+    if (n < (p.mma ? 2 : 3) || 3 * len + 8 >= 2 * p.chunks) n = 1;
     p.seg_len = (p.chunks + n - 1) / n * kAttnChunk;
     if (p.seg_len < kAttnChunk) p.seg_len = kAttnChunk;
     p.nseg = int((sh.T + p.seg_len - 1) / p.seg_len);

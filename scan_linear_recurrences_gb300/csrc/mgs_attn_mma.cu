@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) unsigned char sm[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);
     uint64_t *k_full = bars, *k_empty = bars + 2, *q_full = bars + 4, *q_empty = bars + 6, *v_full = bars + 8,
-             *v_empty = bars + 10, *w_full = bars + 12, *o_ready = bars + 14;
+             *v_empty = bars + 10, *w_full = bars + 12, *o_ready = bars + 14, *st_sync = bars + 15;
     uint64_t *a_done = bars + 16, *p_ready = bars + 17, *qs_done = bars + 18, *o_done = bars + 19, *o_free = bars + 20,
              *s_ready = bars + 21, *kv_done = bars + 22, *kv_free = bars + 23, *g_full = bars + 24, *g_empty = bars + 25,
              *a_read = bars + 28, *drained = bars + 29, *w_full2 = bars + 30;
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(a_done, 1), mbar_init(p_ready, 8), mbar_init(o_ready, 8), mbar_init(qs_done, 1), mbar_init(o_done, 1), mbar_init(o_free, 8);
         mbar_init(s_ready, 8), mbar_init(kv_done, 1), mbar_init(kv_free, 8);
         mbar_init(g_full, 1), mbar_init(g_empty, state_only ? 8 : 16);
-        mbar_init(a_read, 8), mbar_init(drained, 1);
+        mbar_init(a_read, 8), mbar_init(drained, 1), mbar_init(st_sync, 8);
         fence_barrier_init();
     }
     if (warp == 16) {
@@ -472,6 +472,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool mine = NH * D == 128 || dk < D, live = h < H && mine;
         const int64_t ln = int64_t(b) * H + h;
         float s[SC];
+        // The state goes to and from memory 16 columns at a time through 2 KB of the warp's own
+        // (the state operand's place, which is free whenever this is done): pieces of 64 bytes
+        // of 8 rows instead of 16 bytes of 32.  Row r of the warp has its four 16-byte chunks
+        // at c ^ (r / 2 % 4); thread t moves chunk t % 4 of rows t / 4, + 8, ..
+        float4 *stage = reinterpret_cast<float4 *>(sm + (warp - 8) * 2048);
+        auto at_row = [&](int c) { return stage + lane * 4 + (c ^ ((lane >> 1) & 3)); };
+        auto at_line = [&](int j) { return stage + (8 * j + (lane >> 2)) * 4 + ((lane & 3) ^ ((lane >> 3) & 3)); };
+        const int64_t moved = int64_t(row - lane + (lane >> 2)) * D + col + 4 * (lane & 3);
         {
             const float *in = nullptr;
             bool tr = false;
@@ -489,12 +497,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int u = 0; u < SC; ++u) s[u] = in[(col + u) * D + row];
             } else {
 #pragma unroll
-                for (int u = 0; u < SC; u += 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(in + row * D + col + u);
+                for (int u = 0; u < SC; u += 4) {  // piece u / 16, rows of j = u / 4 % 4
+                    const float4 x = *reinterpret_cast<const float4 *>(in + moved + (u >> 4) * 16 + ((u >> 2) & 3) * 8 * D);
                     s[u] = x.x, s[u + 1] = x.y, s[u + 2] = x.z, s[u + 3] = x.w;
+                }
+#pragma unroll
+                for (int u = 0; u < SC; u += 16) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        *at_line(j) = make_float4(s[u + 4 * j], s[u + 4 * j + 1], s[u + 4 * j + 2], s[u + 4 * j + 3]);
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 x = *at_row(j);
+                        s[u + 4 * j] = x.x, s[u + 4 * j + 1] = x.y, s[u + 4 * j + 2] = x.z, s[u + 4 * j + 3] = x.w;
+                    }
+                    __syncwarp();
                 }
             }
         }
+        // no warp writes its rows of the operand into another's stage before that one is done
+        uint32_t syncs = 0;
+        auto staged = [&]() {
+            __syncwarp();
+            if (lane == 0) mb_arrive(st_sync);
+            return wwait(st_sync, syncs++);
+        };
         // The keys' tile is read transposed: ldmatrix gives thread t of a warp the
         // steps 2 (t % 4), + 1 of key row t / 4 (of 8 x 8 blocks), which is the
         // place of that pair in TMEM's 16-lane shape of 128 bits.  Address of this
@@ -505,22 +533,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t kx0 = uint32_t((lc ^ (lr & 7)) << 4), kx1 = uint32_t(((lc + 2) ^ (lr & 7)) << 4);
         auto put_state = [&](float *to) {
 #pragma unroll
-            for (int u = 0; u < SC; u += 4)
-                *reinterpret_cast<float4 *>(to + row * D + col + u) = make_float4(s[u], s[u + 1], s[u + 2], s[u + 3]);
+            for (int u = 0; u < SC; u += 16) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    *at_row(j) = make_float4(s[u + 4 * j], s[u + 4 * j + 1], s[u + 4 * j + 2], s[u + 4 * j + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<float4 *>(to + moved + u + j * 8 * D) = *at_line(j);
+                __syncwarp();
+            }
         };
         const bool marks = w.ckpt != nullptr;
         float decay = 0.f, next_decay = 0.f;  // of the chunk whose product is taken, and of the walked one
-        bool ok = ok0;
+        bool ok = ok0 && staged();
 #pragma unroll 1
         for (int it = 0; ok; ++it) {
             // States that are kept: at a span's end (in reverse that is the state before the
             // chunk is walked), and at the walk's end.
             if (!state_only) {
                 const int ce = rev ? chunk_of(it) : chunk_of(it - 1);
-                if (marks && live && (rev ? it < n : it > 0) &&
-                    ((ce + 1) % (kAttnSpan / C) == 0 || (ce + 1) * C >= T))
-                    put_state(w.ckpt + (ln * set.spans + ce / (kAttnSpan / C)) * D * D);
-                __syncwarp();
+                if (marks && (rev ? it < n : it > 0) && ((ce + 1) % (kAttnSpan / C) == 0 || (ce + 1) * C >= T)) {
+                    if (live) put_state(w.ckpt + (ln * set.spans + ce / (kAttnSpan / C)) * D * D);
+                    if (!(ok = staged())) break;
+                }
                 if (it == n) {
                     if (live && w.s_out && seg == (rev ? 0 : nseg - 1)) put_state(w.s_out + ln * D * D);
                     break;
