@@ -434,12 +434,13 @@ __global__ void __launch_bounds__(256)
 // apart in memory (a TMA tensor map has no zero strides), and fp32 with heads
 // of 64 (three terms of wider ones have no room in shared memory).
 bool mma_takes(const mgs_attention_shape &sh, bool backward) {
-    if (sh.dtype != MGS_BF16) return sh.D == 64;
     auto apart = [&](const int64_t (&st)[3], int64_t heads) {
         return (sh.B == 1 || st[0] > 0) && (sh.T == 1 || st[1] > 0) && (heads == 1 || st[2] > 0);
     };
-    return apart(sh.q_stride, sh.Hk) && apart(sh.k_stride, sh.Hk) && apart(sh.v_stride, sh.H) &&
-           (!backward || apart(sh.do_stride, sh.H));
+    const bool qk = apart(sh.q_stride, sh.Hk) && apart(sh.k_stride, sh.Hk);
+    // fp32 is read through its terms' tensors, but for the products of q with dq and k with dk
+    if (sh.dtype != MGS_BF16) return sh.D == 64 && (qk || !backward);
+    return qk && apart(sh.v_stride, sh.H) && (!backward || apart(sh.do_stride, sh.H));
 }
 
 struct Plan {

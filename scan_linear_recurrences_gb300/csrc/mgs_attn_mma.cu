@@ -29,7 +29,7 @@
 //   16     one thread issues the products
 //   17     one thread loads tiles by TMA
 //   18     sums of g
-//   19     fills the last warpgroup
+//   19     one thread loads x
 #include "mgs_launch.h"
 #include "mgs_lm.h"
 #include "mgs_num.cuh"
@@ -53,7 +53,7 @@ constexpr int GT = 16;                         // steps of a group of weighted k
 constexpr int NG = C / GT;
 
 // TMEM columns (all 512):
-//   A 0..127 and P behind it (one term) or over it (three: A is read whole before);
+//   A 0..127 and P behind it (one term) or over it and behind it (three);
 //   X 192..319: Q S, then (once the rows have it in registers) the state's product;
 //   the weighted keys of a chunk, three terms of 64 columns, 320..511.
 // P V goes where it finds room: with one term and one head in A's place (P has been
@@ -70,18 +70,20 @@ struct Smem {
     static constexpr int NH = D == 64 && IN == 1 ? 2 : 1;           // heads of a block
     static constexpr int tile = IN == 1 ? 2 * kPanel : IN * kPanel;  // a tile: halves, heads or terms in its panels
     static constexpr int sterm = IN == 3 ? kPanel / 2 : D == 64 ? kPanel : 2 * kPanel;  // a term of the state operand
-    static constexpr int NK = 2, NQ = TERMS == 1 ? 2 : 1, NV = IN == 1 && (TERMS == 1 || D == 64) ? 2 : 1;
-    static constexpr int k = TERMS * sterm, q = k + NK * tile, v = q + NQ * tile, arr = v + NV * tile;
+    static constexpr int NK = TERMS == 1 ? 2 : 1, NQ = NK, NV = IN == 1 && (TERMS == 1 || D == 64) ? 2 : 1;
+    static constexpr int k = TERMS * sterm, q = k + NK * tile, v = q + NQ * tile;
+    // where rows are staged on their way out: with one term the chunk's keys' place, else that of x
+    static constexpr int x = v + NV * tile, arr = x + (TERMS == 1 ? 0 : 2 * kPanel);
     // per head: G (high and low parts), the column factors and the state weights of the 128 steps
     static constexpr int bars = arr + NH * 4 * C * 4;
-    static constexpr int walk = bars + 256;                         // the block's AttnWalk
+    static constexpr int walk = bars + 320;                         // the block's AttnWalk
     static constexpr size_t bytes = size_t(walk) + sizeof(AttnWalk);
     static_assert(k % 1024 == 0, "swizzled tiles");
     static_assert(bytes <= 232448, "shared memory of an SM");
 };
 
 struct AttnMaps {
-    CUtensorMap q[3], k[3], v[3], o[3];  // loads: 64 columns x 128 steps; stores: x 32 steps
+    CUtensorMap q[3], k[3], v[3], x[3], o[3];  // loads: 128 bytes x 128 steps; stores: x 32 steps
 };
 
 __device__ __forceinline__ void mb_arrive(uint64_t *bar) {
@@ -181,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
              *v_empty = bars + 10, *w_full = bars + 12, *o_ready = bars + 14, *st_sync = bars + 15;
     uint64_t *a_done = bars + 16, *p_ready = bars + 17, *qs_done = bars + 18, *o_done = bars + 19, *o_free = bars + 20,
              *s_ready = bars + 21, *kv_done = bars + 22, *kv_free = bars + 23, *g_full = bars + 24, *g_empty = bars + 25,
-             *a_read = bars + 28, *drained = bars + 29, *w_full2 = bars + 30;
+             *x_full = bars + 28, *x_empty = bars + 32, *drained = bars + 29, *w_full2 = bars + 30;
     uint32_t *slot = reinterpret_cast<uint32_t *>(bars + 26);
     float *total = reinterpret_cast<float *>(slot + 2);  // [NH]: the chunk's decay
 
@@ -205,14 +207,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&k_full[i], 1), mbar_init(&q_full[i], 1), mbar_init(&v_full[i], 1);
-            mbar_init(&k_empty[i], 8);  // the rows' warps, who stage the output in it at the end
+            // the rows' warps, who stage the output in it at the end, or its readers: the state's
+            // warps and Q K^T
+            mbar_init(&k_empty[i], TERMS == 1 || state_only ? 8 : 9);
             mbar_init(&q_empty[i], 1), mbar_init(&v_empty[i], 1);
             mbar_init(&w_full[i], 8), mbar_init(&w_full2[i], 8);
         }
         mbar_init(a_done, 1), mbar_init(p_ready, 8), mbar_init(o_ready, 8), mbar_init(qs_done, 1), mbar_init(o_done, 1), mbar_init(o_free, 8);
         mbar_init(s_ready, 8), mbar_init(kv_done, 1), mbar_init(kv_free, 8);
         mbar_init(g_full, 1), mbar_init(g_empty, state_only ? 8 : 16);
-        mbar_init(a_read, 8), mbar_init(drained, 1), mbar_init(st_sync, 8);
+        mbar_init(x_full, 1), mbar_init(x_empty, 8), mbar_init(drained, 1), mbar_init(st_sync, 8);
         fence_barrier_init();
     }
     if (warp == 16) {
@@ -246,7 +250,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the output's head, and the weights of its rows of Q S
         const int h = NH == 2 ? h0 + hh : h0, col = NH == 2 ? 0 : OC * hh;
         const float *Go = Gh + (NH == 2 ? hh * 4 * C : 0);
-        const int lrow = lane >> 3, lch = lane & 7;  // whole lines: 4 rows of 8 pieces of 16 bytes at a time
         bool ok = ok0;
 #pragma unroll 1
         for (int it = 0; it < (state_only ? 0 : n) && ok; ++it) {
@@ -334,18 +337,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_put8(tq + M::P + j0 / 2, pk);
                     }
                 } else {
-                    // P's terms take A's place, 32 steps j at a time (half of them this warp's): all
-                    // of those columns of A are read before the first two terms go there; the third
-                    // has columns of its own.
+                    // The first two terms take the place of the 16 columns of A that this warp
+                    // has just read (nobody else touches them), the third has columns of its own.
 #pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
+                    for (int j0 = 64 * hh; j0 < 64 * hh + 64; j0 += 16) {
                         float v[16];
-                        piece(32 * q + 16 * hh, v);
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mb_arrive(a_read);
-                        if (!(ok = wwait(a_read, 4 * ev + q))) break;
-                        tc_fence_after();
+                        piece(j0, v);
                         uint32_t pk[3][8];
 #pragma unroll
                         for (int u = 0; u < 8; ++u) {
@@ -353,11 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             split<3>(make_float2(v[2 * u], v[2 * u + 1]), t);
                             pk[0][u] = t[0], pk[1][u] = t[1], pk[2][u] = t[2];
                         }
-                        tmem_put8(tq + M::P + 32 * q + 8 * hh, pk[0]);
-                        tmem_put8(tq + M::P + 32 * q + 16 + 8 * hh, pk[1]);
-                        tmem_put8(tq + M::P + 128 + 16 * q + 8 * hh, pk[2]);
+                        tmem_put8(tq + M::P + j0, pk[0]);
+                        tmem_put8(tq + M::P + j0 + 8, pk[1]);
+                        tmem_put8(tq + M::P + 128 + j0 / 2, pk[2]);
                     }
-                    if (!ok) break;
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -367,30 +363,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             if (lane == 0) {
                 mb_arrive(g_empty);
-                if (it > 0) {  // the chunk before has been stored: its keys' tile is free
+                if (it > 0) {  // the chunk before has been stored: its stage is free
                     bulk_wait_read();
-                    mb_arrive(&k_empty[(it - 1) % L::NK]);
+                    mb_arrive(TERMS == 1 ? &k_empty[(it - 1) % L::NK] : x_empty);
                 }
             }
-            // The output: row i, columns 64 hh .. of the tile.  The warp's 32 rows are staged in
-            // its part of the chunk's keys, which nobody reads any more (swizzled rows of 128
-            // bytes), and stored by TMA, which drops rows past the end.  x comes in the same
-            // place before: whole lines instead of a thread's row.
+            // The output: row i, this thread's columns.  The warp's 32 rows are staged (swizzled
+            // rows of 128 bytes) where nobody else reads any more, one term in the chunk's keys,
+            // three in x's tile, and stored by TMA, which drops rows past the end.
             const int64_t tw = int64_t(c) * C + 32 * wb;  // the warp's first row
-            unsigned char *stage = sm + L::k + (it % L::NK) * L::tile + hh * kPanel + 32 * wb * 128;
+            unsigned char *stage = sm + (TERMS == 1 ? L::k + (it % L::NK) * L::tile : L::x) + hh * kPanel + 32 * wb * 128;
             unsigned char *mine = stage + lane * 128;
             const int live = h < H ? min(32, T - int(tw)) : 0;  // rows that exist (may be negative)
-            auto line = [&](int u) {
-                return reinterpret_cast<uint4 *>(stage + (4 * u + lrow) * 128 + ((lch ^ ((4 * u + lrow) & 7)) << 4));
-            };
             auto own = [&](int u) { return reinterpret_cast<uint4 *>(mine + ((u ^ (lane & 7)) << 4)); };
-            using TI = typename std::conditional<IN == 1, bf16, float>::type;
-            constexpr int V = kVec<TI>;
-            const TI *px = nullptr;
-            if (TERMS > 1 && w.row_dot) {
-                px = static_cast<const TI *>(w.x) + b * w.xs[0] + tw * w.xs[1] + (h / w.xdiv) * w.xs[2] + col;
-                if (lane < live) asm volatile("prefetch.global.L2 [%0];" ::"l"(px + lane * w.xs[1]));
-            }
             if (!(ok = wwait(o_done, it * NH + NH - 1))) break;
             tc_fence_after();
 #pragma unroll
@@ -408,17 +393,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mb_arrive(o_free);
             if (TERMS > 1 && w.row_dot) {
-                {
-                    uint4 xv[8];
-#pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        xv[u] = 4 * u + lrow < live
-                                    ? *reinterpret_cast<const uint4 *>(px + (4 * u + lrow) * w.xs[1] + V * lch)
-                                    : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) *line(u) = xv[u];
-                }
-                __syncwarp();
+                constexpr int V = IN == 1 ? 8 : 4;
+                if (!(ok = wwait(x_full, it))) break;
                 float2 dot = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int u = 0; u < 8; ++u) {
@@ -638,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (lane == 0) {
                 mb_arrive(g_empty);
-                if (state_only) mb_arrive(&k_empty[it % L::NK]);
+                if (state_only || TERMS > 1) mb_arrive(&k_empty[it % L::NK]);
             }
             }
             // the state-only walk makes the next chunk's keys before it takes this one's product
@@ -701,6 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             umma_bf16_ss(tm + M::A, q + koff(ks) + uint64_t(m * (kPanel >> 4)),
                                          k + koff(ks) + uint64_t(o * (kPanel >> 4)), id_k, m + o + ks > 0);
                 umma_commit(a_done);
+                if (TERMS > 1 && hp == NH - 1) umma_commit(&k_empty[it % L::NK]);
             };
             auto qs = [&](int it) {
 #pragma unroll 1
@@ -735,16 +712,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t v = dV + uint64_t(((it % L::NV) * L::tile + hp * kPanel) >> 4);
 #pragma unroll 1
                 for (int m = 0; m < TERMS; ++m) {
-                    // one term lies in a row of columns; of three, 32 steps' first and second terms
-                    // lie side by side, their third ones behind all of those
-                    const uint32_t p = tm + M::P + (TERMS == 1 ? 0 : m == 2 ? 128 : 16 * m);
-                    const uint32_t step = TERMS == 1 || m == 2 ? 16 : 32;
+                    // of three terms, 16 steps' first and second ones lie side by side, the third
+                    // ones behind all of those
+                    const uint32_t p = tm + M::P + (TERMS == 1 ? 0 : m == 2 ? 128 : 8 * m);
+                    const uint32_t step = TERMS == 1 || m == 2 ? 8 : 16;
 #pragma unroll 1
                     for (int o = 0; o < others(m); ++o)
 #pragma unroll 1
                         for (int ks = 0; ks < C / 16; ++ks)
-                            umma_bf16_ts(tm + M::O + 64 * hp, p + (ks >> 1) * step + 8 * (ks & 1),
-                                         v + uint64_t(ks * 128 + o * (kPanel >> 4)), id_o, m + o + ks > 0);
+                            umma_bf16_ts(tm + M::O + 64 * hp, p + ks * step, v + uint64_t(ks * 128 + o * (kPanel >> 4)), id_o,
+                                         m + o + ks > 0);
                 }
                 umma_commit(o_done);
             };
@@ -921,6 +898,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mb_arrive(g_full);
         }
         if (!ok && lane == 0) record_error(ctl, ERR_MBAR_TIMEOUT);
+    } else if (TERMS > 1 && !state_only && w.row_dot) {
+        // ------------------------------------------------ x
+        if (lane == 0) {
+            constexpr int XN = IN == 1 ? 64 : 32;  // columns of a panel
+            bool done = true;
+            int it = 0;
+#pragma unroll 1
+            for (; it < n && done; ++it) {
+                if (it > 0 && !(done = wait(x_empty, it - 1))) break;
+                mbar_arrive_expect_tx(x_full, 2 * kPanel);
+#pragma unroll 1
+                for (int p = 0; p < 2; ++p)
+                    tma_load_4d(sm + L::x + p * kPanel, &maps.x[blockIdx.y], NH == 2 ? 0 : XN * p, chunk_of(it) * C,
+                                (NH == 2 ? h0 + p : h0) / w.xdiv, b, x_full);
+            }
+            // the last load lands before the block's shared memory is released
+            if (it > 0) done = wait(x_full, it - 1) && done;
+            if (!done) record_error(ctl, ERR_MBAR_TIMEOUT);
+        }
+        __syncwarp();
     }
     }
     tc_fence_before();
@@ -978,6 +975,9 @@ cudaError_t launch_attn_mma(const AttnSet &all, int first, int nwalks, int D, in
         if ((e = tile_map(&maps.q[i], w.q, w.qs, B, set.T, set.H / w.qdiv, D, C, false)) != cudaSuccess) return e;
         if ((e = tile_map(&maps.k[i], w.k, w.ks, B, set.T, set.H / w.kdiv, D, C, false)) != cudaSuccess) return e;
         if ((e = tile_map(&maps.v[i], w.v, w.vs, B, set.T, set.H / w.vdiv, D, C, false)) != cudaSuccess) return e;
+        if (!state_only && w.row_dot &&
+            (e = tile_map(&maps.x[i], w.x, w.xs, set.B, set.T, set.H / w.xdiv, D, C, f32)) != cudaSuccess)
+            return e;
         if (!state_only && (f32 || !w.out_f32) &&
             (e = tile_map(&maps.o[i], w.out, w.os, set.B, set.T, set.H, D, 32, f32)) != cudaSuccess)
             return e;
