@@ -655,8 +655,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t id_k = umma_idesc_bf16(128, 128, false), id_mn = umma_idesc_bf16(128, NH * D, true);
             constexpr uint32_t id_o = umma_idesc_bf16(128, D, true);
             // Products of two sums of three terms: the pairs down to 2^-16 of the first,
-            // (0,0) (0,1) (0,2) (1,0) (1,1) (2,0); a sum with an exact operand: its terms.
-            auto others = [](int m) { return IN == 1 ? 1 : 3 - m; };
+            // (2,0) (1,1) (1,0) (0,2) (0,1) (0,0); a sum with an exact operand: its terms.  The
+            // smallest first: the sums are cut off, not rounded, at each step, so that the fewest
+            // steps should be made at full size.
+            auto last = [](int m) { return IN == 1 ? 0 : 2 - m; };
+            bool add = false;  // onto what is there
             // Descriptors hold addresses in units of 16 bytes: what is issued is one of these
             // plus a short sum, since longer ones between two products cost more time than a
             // product takes (64 cycles at N = 128); rolled loops, whose code stays at hand.
@@ -668,14 +671,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto qk = [&](int it, int hp) {
                 const uint64_t q = dQ + uint64_t(((it % L::NQ) * L::tile + hp * kPanel) >> 4);
                 const uint64_t k = dK + uint64_t(((it % L::NK) * L::tile + hp * kPanel) >> 4);
+                add = false;
 #pragma unroll 1
-                for (int m = 0; m < IN; ++m)
+                for (int m = IN - 1; m >= 0; --m)
 #pragma unroll 1
-                    for (int o = 0; o < others(m); ++o)
+                    for (int o = last(m); o >= 0; --o)
 #pragma unroll 1
-                        for (int ks = 0; ks < KS; ++ks)
+                        for (int ks = 0; ks < KS; ++ks, add = true)
                             umma_bf16_ss(tm + M::A, q + koff(ks) + uint64_t(m * (kPanel >> 4)),
-                                         k + koff(ks) + uint64_t(o * (kPanel >> 4)), id_k, m + o + ks > 0);
+                                         k + koff(ks) + uint64_t(o * (kPanel >> 4)), id_k, add);
                 umma_commit(a_done);
                 if (TERMS > 1 && hp == NH - 1) umma_commit(&k_empty[it % L::NK]);
             };
@@ -683,15 +687,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int hp = 0; hp < NH; ++hp) {
                     const uint64_t q = dQ + uint64_t(((it % L::NQ) * L::tile + hp * kPanel) >> 4);
+                    add = false;
 #pragma unroll 1
-                    for (int m = 0; m < TERMS; ++m) {
+                    for (int m = TERMS - 1; m >= 0; --m) {
                         const uint64_t st = dS + uint64_t((m * L::sterm + hp * 8192) >> 4);
 #pragma unroll 1
-                        for (int o = 0; o < others(m); ++o)
+                        for (int o = last(m); o >= 0; --o)
 #pragma unroll 1
-                            for (int ks = 0; ks < KS; ++ks)
+                            for (int ks = 0; ks < KS; ++ks, add = true)
                                 umma_bf16_ss(tm + M::X + 64 * hp, q + koff(ks) + uint64_t(o * (kPanel >> 4)),
-                                             st + uint64_t(ks * 128), id_o, m + o + ks > 0);
+                                             st + uint64_t(ks * 128), id_o, add);
                     }
                 }
                 umma_commit(qs_done);
@@ -699,29 +704,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto kv = [&](int it, int half) {
                 const uint64_t v = dV + uint64_t(((it % L::NV) * L::tile + half * (NG / 2) * 2048) >> 4);
                 const uint32_t a = tm + (state_only && (it & 1) ? M::A : M::W) + half * (NG / 2) * 8;
+                add = half > 0;
 #pragma unroll 1
-                for (int i = 0; i < NG / 2; ++i)
+                for (int m = 2; m >= 0; --m)
 #pragma unroll 1
-                    for (int m = 0; m < 3; ++m)
+                    for (int o = last(m); o >= 0; --o)
 #pragma unroll 1
-                        for (int o = 0; o < others(m); ++o)
+                        for (int i = 0; i < NG / 2; ++i, add = true)
                             umma_bf16_ts(tm + M::X, a + 64 * m + 8 * i, v + uint64_t(i * 128 + o * (kPanel >> 4)), id_mn,
-                                         half + i + m + o > 0);
+                                         add);
             };
             auto pv = [&](int it, int hp) {
                 const uint64_t v = dV + uint64_t(((it % L::NV) * L::tile + hp * kPanel) >> 4);
+                add = false;
 #pragma unroll 1
-                for (int m = 0; m < TERMS; ++m) {
+                for (int m = TERMS - 1; m >= 0; --m) {
                     // of three terms, 16 steps' first and second ones lie side by side, the third
                     // ones behind all of those
                     const uint32_t p = tm + M::P + (TERMS == 1 ? 0 : m == 2 ? 128 : 8 * m);
                     const uint32_t step = TERMS == 1 || m == 2 ? 8 : 16;
 #pragma unroll 1
-                    for (int o = 0; o < others(m); ++o)
+                    for (int o = last(m); o >= 0; --o)
 #pragma unroll 1
-                        for (int ks = 0; ks < C / 16; ++ks)
-                            umma_bf16_ts(tm + M::O + 64 * hp, p + ks * step, v + uint64_t(ks * 128 + o * (kPanel >> 4)), id_o,
-                                         m + o + ks > 0);
+                        for (int ks = 0; ks < C / 16; ++ks, add = true)
+                            umma_bf16_ts(tm + M::O + 64 * hp, p + ks * step, v + uint64_t(ks * 128 + o * (kPanel >> 4)),
+                                         id_o, add);
                 }
                 umma_commit(o_done);
             };
