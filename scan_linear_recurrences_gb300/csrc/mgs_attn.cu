@@ -431,15 +431,14 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------- host side
 // The tensor-core walk takes bf16 tensors whose steps, heads and batch rows lie
-// apart in memory (a TMA tensor map has no zero strides), and fp32 with heads
-// of 64 (three terms of wider ones have no room in shared memory).
+// apart in memory (a TMA tensor map has no zero strides), and fp32.
 bool mma_takes(const mgs_attention_shape &sh, bool backward) {
     auto apart = [&](const int64_t (&st)[3], int64_t heads) {
         return (sh.B == 1 || st[0] > 0) && (sh.T == 1 || st[1] > 0) && (heads == 1 || st[2] > 0);
     };
     const bool qk = apart(sh.q_stride, sh.Hk) && apart(sh.k_stride, sh.Hk);
     // fp32 is read through its terms' tensors, but for the products of q with dq and k with dk
-    if (sh.dtype != MGS_BF16) return sh.D == 64 && (qk || !backward);
+    if (sh.dtype != MGS_BF16) return qk || !backward;
     return qk && apart(sh.v_stride, sh.H) && (!backward || apart(sh.do_stride, sh.H));
 }
 
@@ -451,12 +450,14 @@ struct Plan {
 Plan plan_of(const mgs_attention_shape &sh, int walks) {
     Plan p;
     p.mma = mma_takes(sh, walks == 3);
-    p.parts = p.mma && (sh.D == 128 || sh.dtype == MGS_F32) ? 2 : 1;
+    const bool f32 = sh.dtype == MGS_F32;
+    p.parts = !p.mma ? 1 : (sh.D == 128 ? 2 : 1) * (f32 ? 2 : 1);  // of a head's row products, one a warp
     p.lanes = sh.B * sh.H;
     p.chunks = (sh.T + kAttnChunk - 1) / kAttnChunk;
     // Segments of the time axis: as many as fill the 152 SMs with blocks (one
     // block to an SM for the tensor-core walk; the SIMT one wants more warps).
-    const int64_t units = p.mma && sh.D == 64 && sh.dtype == MGS_BF16 ? sh.B * ((sh.H + 1) / 2) : p.lanes;
+    // (two heads of 64 in bf16 share a block; a head of 128 in fp32 takes two)
+    const int64_t units = !p.mma || (sh.D == 128) != f32 ? p.lanes : f32 ? 2 * p.lanes : sh.B * ((sh.H + 1) / 2);
     const int64_t want = 152 * (p.mma || sh.D == 128 ? 1 : 4);
     int64_t n = units * walks > 0 ? want / (units * walks) : 1;
     if (n > p.chunks) n = p.chunks;
@@ -536,7 +537,8 @@ struct Splitter {
         if (n == 0) return cudaSuccess;
         set.B = sh.B, set.T = sh.T;
         const int64_t most = sh.B * sh.T * sh.H * (sh.D / 4);
-        attn_split_kernel<64><<<dim3(unsigned(min64((most + 255) / 256, 152 * 16)), unsigned(n)), 256, 0, s>>>(set);
+        const dim3 grid(unsigned(min64((most + 255) / 256, 152 * 16)), unsigned(n));
+        sh.D == 64 ? attn_split_kernel<64><<<grid, 256, 0, s>>>(set) : attn_split_kernel<128><<<grid, 256, 0, s>>>(set);
         return cudaGetLastError();
     }
 };

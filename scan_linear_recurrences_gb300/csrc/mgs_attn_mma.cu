@@ -14,8 +14,11 @@
 // fp32, and stays it), P and S as one where the output is rounded to bf16
 // anyway, as three where <out, x> goes into the decay's gradient (TERMS).
 //
-// fp32 (heads of 64) comes as three bf16 tensors whose sum it is, so that every
-// operand has three terms and a product six pairs of them.
+// fp32 comes as three bf16 tensors whose sum it is, so that every operand has
+// three terms and a product six pairs of them.  A block then has room for 64
+// columns of a tile: a head of 128 is shared between two blocks, each with half
+// of the state's columns (of the values and of the output), and a block takes
+// q and k one half of their columns after the other, adding up A and Q S.
 //
 // Heads of 64 in bf16 go two to a block: panel p of a tile (64 columns) is head p; the
 // state's product is formed for both at once and its two diagonal blocks used.
@@ -66,10 +69,12 @@ struct Tmem {
 
 template <int D, int TERMS, int IN>
 struct Smem {
-    static_assert(IN == 1 || (D == 64 && TERMS == 3), "fp32: heads of 64, every operand in three terms");
+    static_assert(IN == 1 || TERMS == 3, "fp32: every operand in three terms");
+    static constexpr int VD = IN == 3 ? 64 : D;                     // the state's columns in a block
+    static constexpr int KH = IN == 3 ? D / 64 : 1;                 // passes over the columns of q and k
     static constexpr int NH = D == 64 && IN == 1 ? 2 : 1;           // heads of a block
     static constexpr int tile = IN == 1 ? 2 * kPanel : IN * kPanel;  // a tile: halves, heads or terms in its panels
-    static constexpr int sterm = IN == 3 ? kPanel / 2 : D == 64 ? kPanel : 2 * kPanel;  // a term of the state operand
+    static constexpr int sterm = IN == 3 ? D * 128 : D == 64 ? kPanel : 2 * kPanel;  // a term of the state operand
     static constexpr int NK = TERMS == 1 ? 2 : 1, NQ = NK, NV = IN == 1 && (TERMS == 1 || D == 64) ? 2 : 1;
     static constexpr int k = TERMS * sterm, q = k + NK * tile, v = q + NQ * tile;
     // where rows are staged on their way out: with one term the chunk's keys' place, else that of x
@@ -174,9 +179,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_mma_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnSet set, int state_only) {
     using L = Smem<D, TERMS, IN>;
     using M = Tmem<D, TERMS, IN>;
-    constexpr int NH = L::NH;
-    constexpr int SC = D / 2;               // state columns of a thread
-    constexpr int OC = NH == 2 ? 64 : D / 2;  // output columns of a thread
+    constexpr int NH = L::NH, KH = L::KH, VH = D / L::VD;
+    constexpr int SC = L::VD / 2;               // state columns of a thread
+    constexpr int OC = NH == 2 ? 64 : L::VD / 2;  // output columns of a thread
     extern __shared__ __align__(1024) unsigned char sm[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);
     uint64_t *k_full = bars, *k_empty = bars + 2, *q_full = bars + 4, *q_empty = bars + 6, *v_full = bars + 8,
@@ -192,9 +197,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const AttnWalk &w = *reinterpret_cast<const AttnWalk *>(sm + L::walk);
     const bool rev = set.w[set.first + blockIdx.y].rev != 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int nseg = set.nseg, units = int((set.H + NH - 1) / NH);
+    const int nseg = set.nseg, units = int((set.H + NH - 1) / NH) * VH;
     const int unit = int(blockIdx.x) / nseg, seg = int(blockIdx.x) - unit * nseg;
-    const int b = unit / units, h0 = (unit - b * units) * NH;
+    const int b = unit / units, h0 = (unit - b * units) / VH * NH, v0 = (unit % VH) * L::VD;  // first head and column
     if (state_only && seg == (rev ? 0 : nseg - 1)) return;  // nothing starts from this segment's state
     const int H = int(set.H), T = int(set.T);
     const int c0 = int(seg * (set.seg_len / C)), c1 = min(c0 + int(set.seg_len / C), (T + C - 1) / C);
@@ -228,7 +233,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tm = *slot;
     const uint32_t tq = tm + (uint32_t(32 * (warp & 3)) << 16);
-    // a role whose wait gives up ends; the others' waits then give up too
     // A role whose wait gives up says so and ends; the others' waits then give up too.
     const uint32_t tries = set.tries;
     auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_poll(smem_addr(bar), parity & 1u, tries); };
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int isgn = rev ? -1 : 1;
         const uint32_t in = rev ? ~0u << lane : ~0u >> (31 - lane);  // columns of the diagonal's block that count
         // the output's head, and the weights of its rows of Q S
-        const int h = NH == 2 ? h0 + hh : h0, col = NH == 2 ? 0 : OC * hh;
+        const int h = NH == 2 ? h0 + hh : h0, col = NH == 2 ? 0 : v0 + OC * hh;
         const float *Go = Gh + (NH == 2 ? hh * 4 * C : 0);
         bool ok = ok0;
 #pragma unroll 1
@@ -405,9 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         dot = __ffma2_rn(make_float2(o1[V * u + m], o1[V * u + m + 1]), make_float2(xx[m], xx[m + 1]), dot);
                 }
                 __syncwarp();
-                // one head in the block: each half of the columns leaves its own product
+                // a head in two warps, or in two of each of two blocks: each leaves its own product
                 if (lane < live)
-                    w.row_dot[(NH == 2 ? 0 : hh * set.B * set.T * set.H) + (b * set.T + tw + lane) * set.H + h] =
+                    w.row_dot[(NH == 2 ? 0 : (v0 / OC + hh) * set.B * set.T * set.H) + (b * set.T + tw + lane) * set.H + h] =
                         dot.x + dot.y;
             }
             if (IN == 1 && w.out_f32) {
@@ -444,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int grp = (warp - 8) >> 2, dk = 32 * (warp & 3) + lane;
         const int hp = NH == 2 ? dk >> 6 : 0, h = h0 + hp;
         const int row = NH == 2 ? dk & 63 : dk, col = SC * grp;  // the head's state: row, first column
-        // fp32: 64 key rows in 128 lanes, of which the upper half stands idle
+        // heads of 64 in fp32: 64 key rows in 128 lanes, of which the upper half stands idle
         const bool mine = NH * D == 128 || dk < D, live = h < H && mine;
         const int64_t ln = int64_t(b) * H + h;
         float s[SC];
@@ -455,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float4 *stage = reinterpret_cast<float4 *>(sm + (warp - 8) * 2048);
         auto at_row = [&](int c) { return stage + lane * 4 + (c ^ ((lane >> 1) & 3)); };
         auto at_line = [&](int j) { return stage + (8 * j + (lane >> 2)) * 4 + ((lane & 3) ^ ((lane >> 3) & 3)); };
-        const int64_t moved = int64_t(row - lane + (lane >> 2)) * D + col + 4 * (lane & 3);
+        const int64_t moved = int64_t(row - lane + (lane >> 2)) * D + v0 + col + 4 * (lane & 3);
         {
             const float *in = nullptr;
             bool tr = false;
@@ -470,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int u = 0; u < SC; ++u) s[u] = 0.f;
             } else if (tr) {
 #pragma unroll
-                for (int u = 0; u < SC; ++u) s[u] = in[(col + u) * D + row];
+                for (int u = 0; u < SC; ++u) s[u] = in[(v0 + col + u) * D + row];
             } else {
 #pragma unroll
                 for (int u = 0; u < SC; u += 4) {  // piece u / 16, rows of j = u / 4 % 4
@@ -505,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // thread's row of the four blocks (16 key rows x 16 steps):
         const int lr = ((lane >> 4) << 3) + (lane & 7);        // step within the group
         const int lc = ((32 * (warp & 3)) & 63) / 8 + ((lane >> 3) & 1);
-        const uint32_t kbase = smem_addr(sm + L::k) + uint32_t((32 * (warp & 3)) >> 6) * kPanel + lr * 128;
+        const uint32_t kbase = smem_addr(sm + L::k) + (IN == 1 ? (warp & 2) * (kPanel / 2) : 0) + lr * 128;
         const uint32_t kx0 = uint32_t((lc ^ (lr & 7)) << 4), kx1 = uint32_t(((lc + 2) ^ (lr & 7)) << 4);
         auto put_state = [&](float *to) {
 #pragma unroll
@@ -540,82 +544,90 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!state_only) {
                 // the state as the operand of Q S (its reader of the chunk before is done)
                 if (it > 0 && !(ok = wwait(qs_done, it - 1))) break;
-                unsigned char *base = sm + (D == 64 ? 0 : grp * kPanel) + dk * 128;
-                const int ch0 = D == 64 ? 4 * grp : 0;
-                if (mine)
+                unsigned char *base = sm + (L::VD == 64 ? 0 : grp * kPanel) + dk * 128;
+                const int ch0 = L::VD == 64 ? 4 * grp : 0;
+                if (mine) {
 #pragma unroll
-                for (int u = 0; u < SC; u += 8) {
-                    uint32_t t0[TERMS], t1[TERMS], t2[TERMS], t3[TERMS];
-                    split<TERMS>(make_float2(s[u], s[u + 1]), t0);
-                    split<TERMS>(make_float2(s[u + 2], s[u + 3]), t1);
-                    split<TERMS>(make_float2(s[u + 4], s[u + 5]), t2);
-                    split<TERMS>(make_float2(s[u + 6], s[u + 7]), t3);
+                    for (int u = 0; u < SC; u += 8) {
+                        uint32_t t0[TERMS], t1[TERMS], t2[TERMS], t3[TERMS];
+                        split<TERMS>(make_float2(s[u], s[u + 1]), t0);
+                        split<TERMS>(make_float2(s[u + 2], s[u + 3]), t1);
+                        split<TERMS>(make_float2(s[u + 4], s[u + 5]), t2);
+                        split<TERMS>(make_float2(s[u + 6], s[u + 7]), t3);
 #pragma unroll
-                    for (int m = 0; m < TERMS; ++m)
-                        *reinterpret_cast<uint4 *>(base + m * L::sterm + (((ch0 + u / 8) ^ (dk & 7)) << 4)) =
-                            make_uint4(t0[m], t1[m], t2[m], t3[m]);
+                        for (int m = 0; m < TERMS; ++m)
+                            *reinterpret_cast<uint4 *>(base + m * L::sterm + (((ch0 + u / 8) ^ (dk & 7)) << 4)) =
+                                make_uint4(t0[m], t1[m], t2[m], t3[m]);
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mb_arrive(s_ready);
             }
             if (it < n) {
-            if (!(ok = wwait(&k_full[it % L::NK], it / L::NK) && wwait(g_full, it))) break;
-            const uint32_t kt = kbase + (it % L::NK) * L::tile;
-            const float *wt = Gh + hp * 4 * C + 3 * C + 2 * (lane & 3);
-            next_decay = total[hp];
-            if (!state_only) decay = next_decay;
-            // the state-only walk has room for two chunks' keys, each with barriers of its own (it
-            // makes the next chunk's before this one's have been asked for)
-            const bool second = state_only && (it & 1);
-            const uint32_t wcol = tq + (second ? M::A : M::W);
-            // the chunk's weighted keys, half of it at a time, the groups of 16 steps shared
-            // between the two warpgroups
+                if (!(ok = wwait(g_full, it))) break;
+                const float *wt = Gh + hp * 4 * C + 3 * C + 2 * (lane & 3);
+                next_decay = total[hp];
+                if (!state_only) decay = next_decay;
+                // the state-only walk has room for two chunks' keys, each with barriers of its own (it
+                // makes the next chunk's before this one's have been asked for)
+                const bool second = state_only && (it & 1);
+                const uint32_t wcol = tq + (second ? M::A : M::W);
 #pragma unroll 1
-            for (int i = 0; i < NG / 2; ++i) {
-                const int gi = (i >> 1) * (NG / 2) + grp * (NG / 4) + (i & 1);
-                const float2 w0 = *reinterpret_cast<const float2 *>(wt + gi * GT);
-                const float2 w1 = *reinterpret_cast<const float2 *>(wt + gi * GT + 8);
-                uint32_t r[2][4];  // key rows 0..15 and 16..31 of the warp
-                if (IN == 1) {
-                    ldmatrix_x4_trans(kt + gi * (GT * 128) + kx0, r[0]);
-                    ldmatrix_x4_trans(kt + gi * (GT * 128) + kx1, r[1]);
-                }
-                if (mine)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        uint32_t t[3][4], r1[4], r2[4];
-                        if (IN == 3) {  // a key's three terms add up to it
-                            const uint32_t at = kt + gi * (GT * 128) + (x ? kx1 : kx0);
-                            ldmatrix_x4_trans(at, r[x]);
-                            ldmatrix_x4_trans(at + kPanel, r1);
-                            ldmatrix_x4_trans(at + 2 * kPanel, r2);
+                for (int kh = 0; kh < KH; ++kh) {
+                    const int kt_i = it * KH + kh;
+                    if (!(ok = wwait(&k_full[kt_i % L::NK], kt_i / L::NK))) break;
+                    const uint32_t kt = kbase + (kt_i % L::NK) * L::tile;
+                    // the chunk's weighted keys, half of it at a time, the groups of 16 steps shared
+                    // between the two warpgroups; a pass over half of the keys' columns is for the warps
+                    // of those rows of the state
+#pragma unroll 1
+                    for (int i = KH == 1 || kh == ((warp & 3) >> 1) ? 0 : NG / 2; i < NG / 2; ++i) {
+                        const int gi = (i >> 1) * (NG / 2) + grp * (NG / 4) + (i & 1);
+                        const float2 w0 = *reinterpret_cast<const float2 *>(wt + gi * GT);
+                        const float2 w1 = *reinterpret_cast<const float2 *>(wt + gi * GT + 8);
+                        uint32_t r[2][4];  // key rows 0..15 and 16..31 of the warp
+                        if (IN == 1) {
+                            ldmatrix_x4_trans(kt + gi * (GT * 128) + kx0, r[0]);
+                            ldmatrix_x4_trans(kt + gi * (GT * 128) + kx1, r[1]);
                         }
+                        if (mine) {
 #pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            uint32_t a[3];
-                            float2 y = make_float2(bf_lo(r[x][m]), bf_hi(r[x][m]));
-                            if (IN == 3)
-                                y = __fadd2_rn(y, __fadd2_rn(make_float2(bf_lo(r1[m]), bf_hi(r1[m])),
-                                                             make_float2(bf_lo(r2[m]), bf_hi(r2[m]))));
-                            split<3>(__fmul2_rn(y, m < 2 ? w0 : w1), a);
-                            t[0][m] = a[0], t[1][m] = a[1], t[2][m] = a[2];
+                            for (int x = 0; x < 2; ++x) {
+                                uint32_t t[3][4], r1[4], r2[4];
+                                if (IN == 3) {  // a key's three terms add up to it
+                                    const uint32_t at = kt + gi * (GT * 128) + (x ? kx1 : kx0);
+                                    ldmatrix_x4_trans(at, r[x]);
+                                    ldmatrix_x4_trans(at + kPanel, r1);
+                                    ldmatrix_x4_trans(at + 2 * kPanel, r2);
+                                }
+#pragma unroll
+                                for (int m = 0; m < 4; ++m) {
+                                    uint32_t a[3];
+                                    float2 y = make_float2(bf_lo(r[x][m]), bf_hi(r[x][m]));
+                                    if (IN == 3)
+                                        y = __fadd2_rn(y, __fadd2_rn(make_float2(bf_lo(r1[m]), bf_hi(r1[m])),
+                                                                     make_float2(bf_lo(r2[m]), bf_hi(r2[m]))));
+                                    split<3>(__fmul2_rn(y, m < 2 ? w0 : w1), a);
+                                    t[0][m] = a[0], t[1][m] = a[1], t[2][m] = a[2];
+                                }
+#pragma unroll
+                                for (int m = 0; m < 3; ++m)
+                                    tmem_put_16x8(wcol + (uint32_t(16 * x) << 16) + 64 * m + 8 * gi, t[m]);
+                            }
                         }
-#pragma unroll
-                        for (int m = 0; m < 3; ++m)
-                            tmem_put_16x8(wcol + (uint32_t(16 * x) << 16) + 64 * m + 8 * gi, t[m]);
+                        if (i & 1) {
+                            tmem_wait_st();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mb_arrive(&(second ? w_full2 : w_full)[i >> 1]);
+                        }
                     }
-                if (i & 1) {
-                    tmem_wait_st();
-                    tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mb_arrive(&(second ? w_full2 : w_full)[i >> 1]);
+                    if (lane == 0 && (state_only || TERMS > 1)) mb_arrive(&k_empty[kt_i % L::NK]);
                 }
-            }
-            if (lane == 0) {
-                mb_arrive(g_empty);
-                if (state_only || TERMS > 1) mb_arrive(&k_empty[it % L::NK]);
-            }
+                if (!ok) break;
+                if (lane == 0) mb_arrive(g_empty);
             }
             // the state-only walk makes the next chunk's keys before it takes this one's product
             const int j = state_only ? it - 1 : it;
@@ -652,8 +664,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ the products
         if (elect_one()) {
             // N: the steps; the state's columns (of both heads); a head's columns
-            constexpr uint32_t id_k = umma_idesc_bf16(128, 128, false), id_mn = umma_idesc_bf16(128, NH * D, true);
-            constexpr uint32_t id_o = umma_idesc_bf16(128, D, true);
+            constexpr uint32_t id_k = umma_idesc_bf16(128, 128, false), id_mn = umma_idesc_bf16(128, NH * L::VD, true);
+            constexpr uint32_t id_o = umma_idesc_bf16(128, L::VD, true);
             // Products of two sums of three terms: the pairs down to 2^-16 of the first,
             // (2,0) (1,1) (1,0) (0,2) (0,1) (0,0); a sum with an exact operand: its terms.  The
             // smallest first: the sums are cut off, not rounded, at each step, so that the fewest
@@ -665,13 +677,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             // product takes (64 cycles at N = 128); rolled loops, whose code stays at hand.
             const uint64_t dK = umma_desc_k(smem_addr(sm + L::k)), dQ = umma_desc_k(smem_addr(sm + L::q));
             const uint64_t dV = umma_desc_mn(smem_addr(sm + L::v), kPanel), dS = umma_desc_mn(smem_addr(sm), kPanel);
-            constexpr int KS = D / 16;
+            constexpr int KS = D / 16 / KH;
             // K-major step ks of head hp: 32 bytes on in the rows, the next panel after four
             auto koff = [](int ks) { return uint64_t(((ks >> 2) * kPanel + (ks & 3) * 32) >> 4); };
-            auto qk = [&](int it, int hp) {
-                const uint64_t q = dQ + uint64_t(((it % L::NQ) * L::tile + hp * kPanel) >> 4);
-                const uint64_t k = dK + uint64_t(((it % L::NK) * L::tile + hp * kPanel) >> 4);
-                add = false;
+            auto qk = [&](int it, int hp, int kh) {
+                const int tile_i = it * KH + kh;
+                const uint64_t q = dQ + uint64_t(((tile_i % L::NQ) * L::tile + hp * kPanel) >> 4);
+                const uint64_t k = dK + uint64_t(((tile_i % L::NK) * L::tile + hp * kPanel) >> 4);
+                add = kh > 0;
 #pragma unroll 1
                 for (int m = IN - 1; m >= 0; --m)
 #pragma unroll 1
@@ -680,17 +693,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int ks = 0; ks < KS; ++ks, add = true)
                             umma_bf16_ss(tm + M::A, q + koff(ks) + uint64_t(m * (kPanel >> 4)),
                                          k + koff(ks) + uint64_t(o * (kPanel >> 4)), id_k, add);
-                umma_commit(a_done);
-                if (TERMS > 1 && hp == NH - 1) umma_commit(&k_empty[it % L::NK]);
+                if (kh == KH - 1) umma_commit(a_done);
+                if (TERMS > 1 && hp == NH - 1) umma_commit(&k_empty[tile_i % L::NK]);
             };
-            auto qs = [&](int it) {
+            auto qs = [&](int it, int kh) {
+                const int tile_i = it * KH + kh;
 #pragma unroll 1
                 for (int hp = 0; hp < NH; ++hp) {
-                    const uint64_t q = dQ + uint64_t(((it % L::NQ) * L::tile + hp * kPanel) >> 4);
-                    add = false;
+                    const uint64_t q = dQ + uint64_t(((tile_i % L::NQ) * L::tile + hp * kPanel) >> 4);
+                    add = kh > 0;
 #pragma unroll 1
                     for (int m = TERMS - 1; m >= 0; --m) {
-                        const uint64_t st = dS + uint64_t((m * L::sterm + hp * 8192) >> 4);
+                        const uint64_t st = dS + uint64_t((m * L::sterm + (hp + kh) * 8192) >> 4);
 #pragma unroll 1
                         for (int o = last(m); o >= 0; --o)
 #pragma unroll 1
@@ -699,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              st + uint64_t(ks * 128), id_o, add);
                     }
                 }
-                umma_commit(qs_done);
+                if (kh == KH - 1) umma_commit(qs_done);
             };
             auto kv = [&](int it, int half) {
                 const uint64_t v = dV + uint64_t(((it % L::NV) * L::tile + half * (NG / 2) * 2048) >> 4);
@@ -737,16 +751,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int it = 0; it < n && ok; ++it) {
                 if (!state_only) {
                     // Q S first: its place is wanted by the state's product, its result by nobody soon
-                    if (!(ok = wait(&q_full[it % L::NQ], it / L::NQ) && wait(s_ready, it))) break;
+                    if (!(ok = wait(s_ready, it))) break;
                     if (it > 0 && !(ok = M::over_a ? wait(kv_free, it - 1) : wait(o_free, it - 1))) break;
-                    tc_fence_after();
-                    qs(it);
-                    if (!(ok = wait(&k_full[it % L::NK], it / L::NK))) break;
-                    if (M::over_a && it > 0 && !(ok = wait(o_free, it - 1))) break;
-                    tc_fence_after();
-                    qk(it, 0);
-                    if (NH == 1) umma_commit(&q_empty[it % L::NQ]);
-                    if (!(ok = wait(o_ready, it))) break;  // Q S is in the rows' registers
+#pragma unroll 1
+                    for (int kh = 0; kh < KH && ok; ++kh) {
+                        const int tile_i = it * KH + kh;
+                        if (!(ok = wait(&q_full[tile_i % L::NQ], tile_i / L::NQ))) break;
+                        tc_fence_after();
+                        qs(it, kh);
+                        if (!(ok = wait(&k_full[tile_i % L::NK], tile_i / L::NK))) break;
+                        if (M::over_a && it > 0 && !(ok = wait(o_free, it - 1))) break;
+                        tc_fence_after();
+                        qk(it, 0, kh);
+                        if (NH == 1) umma_commit(&q_empty[tile_i % L::NQ]);
+                    }
+                    if (!ok || !(ok = wait(o_ready, it))) break;  // Q S is in the rows' registers
                 } else if (it > 0 && !(ok = wait(kv_free, it - 1))) {
                     break;
                 }
@@ -763,10 +782,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!M::over_a && !(ok = wait(kv_free, it))) break;
                     if (!(ok = wait(p_ready, it * NH))) break;
                     tc_fence_after();
-                    if (NH == 2 && TERMS == 1) qk(it, 1);  // P stands beside A
+                    if (NH == 2 && TERMS == 1) qk(it, 1, 0);  // P stands beside A
                     pv(it, 0);
                     if (NH == 2) {
-                        if (TERMS != 1) qk(it, 1);         // ... or over it: after the product with P
+                        if (TERMS != 1) qk(it, 1, 0);         // ... or over it: after the product with P
                         umma_commit(&q_empty[it % L::NQ]);
                         if (!(ok = wait(p_ready, it * NH + 1))) break;
                         tc_fence_after();
@@ -789,28 +808,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             const CUtensorMap *mq = &maps.q[blockIdx.y], *mk = &maps.k[blockIdx.y], *mv = &maps.v[blockIdx.y];
             // the next tile of a ring, once its slot is free
-            auto fill = [&](int it, int depth, uint64_t *full, uint64_t *empty, int off, const CUtensorMap *m, int div) {
-                const int sl = it % depth;
-                if (it >= depth && !wait(&empty[sl], it / depth - 1)) return false;
+            auto fill = [&](int i, int c, int depth, uint64_t *full, uint64_t *empty, int off, const CUtensorMap *m, int div,
+                            int col) {
+                const int sl = i % depth;
+                if (i >= depth && !wait(&empty[sl], i / depth - 1)) return false;
                 unsigned char *dst = sm + off + sl * L::tile;
                 mbar_arrive_expect_tx(&full[sl], L::tile);
 #pragma unroll 1
                 for (int p = 0; p < L::tile / kPanel; ++p)  // halves of a head, heads, or terms (a batch apart)
-                    tma_load_4d(dst + p * kPanel, m, NH * IN == 1 ? 64 * p : 0, chunk_of(it) * C,
-                                (NH == 2 ? h0 + p : h0) / div, IN == 3 ? b + p * int(set.B) : b, &full[sl]);
+                    tma_load_4d(dst + p * kPanel, m, NH * IN == 1 ? 64 * p : col, c * C, (NH == 2 ? h0 + p : h0) / div,
+                                IN == 3 ? b + p * int(set.B) : b, &full[sl]);
                 return true;
             };
             // a block starts with the state as an operand and Q, ends with V
             int lk = 0, lq = 0, lv = 0;  // tiles loaded
+            bool ok = true;
 #pragma unroll 1
-            for (int it = 0; it < n; ++it) {
-                if (!state_only) {
-                    if (!fill(it, L::NQ, q_full, q_empty, L::q, mq, w.qdiv)) break;
-                    ++lq;
+            for (int it = 0; it < n && ok; ++it) {
+                const int c = chunk_of(it);
+#pragma unroll 1
+                for (int kh = 0; kh < KH && ok; ++kh) {
+                    if (!state_only) {
+                        if (!(ok = fill(lq, c, L::NQ, q_full, q_empty, L::q, mq, w.qdiv, 64 * kh))) break;
+                        ++lq;
+                    }
+                    if (!(ok = fill(lk, c, L::NK, k_full, k_empty, L::k, mk, w.kdiv, 64 * kh))) break;
+                    ++lk;
                 }
-                if (!fill(it, L::NK, k_full, k_empty, L::k, mk, w.kdiv)) break;
-                ++lk;
-                if (!fill(it, L::NV, v_full, v_empty, L::v, mv, w.vdiv)) break;
+                if (!ok || !(ok = fill(lv, c, L::NV, v_full, v_empty, L::v, mv, w.vdiv, v0))) break;
                 ++lv;
             }
             // every load in flight lands before the block's shared memory is released
@@ -894,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 store4(G + 2 * C, cf[hp]);
                 store4(G + 3 * C, wt[hp]);
                 if (lane == 0) total[hp] = ex2_approx(last[hp]);
-                if (state_only && lane == 0 && h0 + hp < H) {
+                if (state_only && lane == 0 && h0 + hp < H && v0 == 0) {
                     // the segment's sum of g beside its state, for the scan that joins the segments
                     float *sum = w.seg_out + set.B * set.H * nseg * D * D + (int64_t(b) * H + h0 + hp) * nseg + seg;
                     const float g = last[hp] * 0.6931471805599453f;
@@ -917,7 +942,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive_expect_tx(x_full, 2 * kPanel);
 #pragma unroll 1
                 for (int p = 0; p < 2; ++p)
-                    tma_load_4d(sm + L::x + p * kPanel, &maps.x[blockIdx.y], NH == 2 ? 0 : XN * p, chunk_of(it) * C,
+                    tma_load_4d(sm + L::x + p * kPanel, &maps.x[blockIdx.y], NH == 2 ? 0 : v0 + XN * p, chunk_of(it) * C,
                                 (NH == 2 ? h0 + p : h0) / w.xdiv, b, x_full);
             }
             // the last load lands before the block's shared memory is released
@@ -962,7 +987,7 @@ cudaError_t go(const AttnMaps &maps, const AttnSet &set, int nwalks, bool state_
         regs.store(a.numRegs);
     }
     if (regs.load() != kRegs) return cudaErrorInvalidDeviceFunction;
-    const dim3 grid(unsigned(set.B * ((set.H + L::NH - 1) / L::NH) * set.nseg), unsigned(nwalks));
+    const dim3 grid(unsigned(set.B * ((set.H + L::NH - 1) / L::NH) * (D / L::VD) * set.nseg), unsigned(nwalks));
     attn_mma_kernel<D, TERMS, IN><<<grid, kThreads, L::bytes, s>>>(maps, set, state_only);
     return cudaGetLastError();
 }
@@ -989,7 +1014,9 @@ cudaError_t launch_attn_mma(const AttnSet &all, int first, int nwalks, int D, in
             (e = tile_map(&maps.o[i], w.out, w.os, set.B, set.T, set.H, D, 32, f32)) != cudaSuccess)
             return e;
     }
-    if (f32) return go<64, 3, 3>(maps, set, nwalks, state_only, s);
+    if (f32)
+        return D == 64 ? go<64, 3, 3>(maps, set, nwalks, state_only, s)
+                       : go<128, 3, 3>(maps, set, nwalks, state_only, s);
     if (D == 64)
         return terms == 1 ? go<64, 1, 1>(maps, set, nwalks, state_only, s)
                           : go<64, 3, 1>(maps, set, nwalks, state_only, s);

@@ -56,7 +56,7 @@ struct AttnSet {
 cudaError_t launch_attn_rec(const AttnSet &set, int nwalks, int D, int dtype, bool state_only, cudaStream_t s);
 
 // Tensor-core walks `first` .. of the set.  terms: bf16 terms of the computed
-// operands of the output.  fp32 (heads of 64): q, k and v are each three dense
+// operands of the output.  fp32: q, k and v are each three dense
 // bf16 tensors behind one another (attn_split), out and x are fp32.
 cudaError_t launch_attn_mma(const AttnSet &set, int first, int nwalks, int D, int dtype, int terms, bool state_only,
                             cudaStream_t s);
