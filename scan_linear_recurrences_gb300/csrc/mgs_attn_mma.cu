@@ -32,7 +32,7 @@
 //   16     one thread issues the products
 //   17     one thread loads tiles by TMA
 //   18     sums of g
-//   19     one thread loads x
+//   19     loads x; looks for infinities and NaN in v
 #include "mgs_launch.h"
 #include "mgs_lm.h"
 #include "mgs_num.cuh"
@@ -174,6 +174,50 @@ __device__ __forceinline__ void add2(float &h, float &l, float a, float b) {
     l = lo - (h - s);
 }
 
+// A row's part of P V alone: o += o_scale kv_scale sum_j e^(..) (q_t . k_j) v_j over
+// the chunk's steps j on row t's side of the mask.  For chunks with an infinity
+// or NaN among the v_j: the tensor cores multiply the masked entries too, and 0
+// times it would reach the steps that v_j does not.
+template <int D, int IN, int OC>
+__device__ __forceinline__ void row_alone(const AttnWalk &w, const AttnSet &set, int b, int h, int t, int first, int end,
+                                       int col, float *o) {
+    const bf16 *q = static_cast<const bf16 *>(w.q) + b * w.qs[0] + t * w.qs[1] + (h / w.qdiv) * w.qs[2];
+    const bf16 *k = static_cast<const bf16 *>(w.k) + b * w.ks[0] + (h / w.kdiv) * w.ks[2];
+    const bf16 *v = static_cast<const bf16 *>(w.v) + b * w.vs[0] + (h / w.vdiv) * w.vs[2] + col;
+    const float *g = set.g + b * set.gs[0] + h * set.gs[2];
+    auto get = [](const bf16 *p, int64_t term, float (&x)[4]) {
+        load4(p, x);
+#pragma unroll
+        for (int m = 1; m < IN; ++m) {
+            float y[4];
+            load4(p + m * term, y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] += y[i];
+        }
+    };
+    const int64_t qterm = set.B * w.qs[0], kterm = set.B * w.ks[0], vterm = set.B * w.vs[0];
+    float sum = 0.f;  // of g between the row and step j
+#pragma unroll 1
+    for (int j = t; w.rev ? j < end : j >= first; j += w.rev ? 1 : -1) {
+        if (w.rev && j > t) sum += g[j * set.gs[1]];
+        float dot = 0.f, x[4], y[4];
+#pragma unroll 1
+        for (int c = 0; c < D; c += 4) {
+            get(q + c, qterm, x), get(k + j * w.ks[1] + c, kterm, y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dot = fmaf(x[i], y[i], dot);
+        }
+        const float p = dot * (w.o_scale * w.kv_scale * expf(sum));
+#pragma unroll 1
+        for (int c = 0; c < OC; c += 4) {
+            get(v + j * w.vs[1] + c, vterm, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[c + i] = fmaf(p, x[i], o[c + i]);
+        }
+        if (!w.rev) sum += g[j * set.gs[1]];
+    }
+}
+
 template <int D, int TERMS, int IN>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_mma_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnSet set, int state_only) {
@@ -188,8 +232,10 @@ __global__ void __launch_bounds__(kThreads, 1)
              *v_empty = bars + 10, *w_full = bars + 12, *o_ready = bars + 14, *st_sync = bars + 15;
     uint64_t *a_done = bars + 16, *p_ready = bars + 17, *qs_done = bars + 18, *o_done = bars + 19, *o_free = bars + 20,
              *s_ready = bars + 21, *kv_done = bars + 22, *kv_free = bars + 23, *g_full = bars + 24, *g_empty = bars + 25,
-             *x_full = bars + 28, *x_empty = bars + 32, *drained = bars + 29, *w_full2 = bars + 30;
+             *x_full = bars + 28, *x_empty = bars + 32, *drained = bars + 29, *w_full2 = bars + 30,
+             *v_checked = bars + 33;  // ..36
     uint32_t *slot = reinterpret_cast<uint32_t *>(bars + 26);
+    volatile int *v_flag = reinterpret_cast<int *>(bars + 37);  // [4]: the chunk's v has an infinity or NaN
     float *total = reinterpret_cast<float *>(slot + 2);  // [NH]: the chunk's decay
 
     // the walk's description from shared memory: parameters indexed by blockIdx
@@ -215,13 +261,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the rows' warps, who stage the output in it at the end, or its readers: the state's
             // warps and Q K^T
             mbar_init(&k_empty[i], TERMS == 1 || state_only ? 8 : 9);
-            mbar_init(&q_empty[i], 1), mbar_init(&v_empty[i], 1);
+            mbar_init(&q_empty[i], 1), mbar_init(&v_empty[i], state_only ? 1 : 2);
             mbar_init(&w_full[i], 8), mbar_init(&w_full2[i], 8);
         }
         mbar_init(a_done, 1), mbar_init(p_ready, 8), mbar_init(o_ready, 8), mbar_init(qs_done, 1), mbar_init(o_done, 1), mbar_init(o_free, 8);
         mbar_init(s_ready, 8), mbar_init(kv_done, 1), mbar_init(kv_free, 8);
         mbar_init(g_full, 1), mbar_init(g_empty, state_only ? 8 : 16);
         mbar_init(x_full, 1), mbar_init(x_empty, 8), mbar_init(drained, 1), mbar_init(st_sync, 8);
+        for (int i = 0; i < 4; ++i) mbar_init(&v_checked[i], 1);
         fence_barrier_init();
     }
     if (warp == 16) {
@@ -380,17 +427,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             unsigned char *mine = stage + lane * 128;
             const int live = h < H ? min(32, T - int(tw)) : 0;  // rows that exist (may be negative)
             auto own = [&](int u) { return reinterpret_cast<uint4 *>(mine + ((u ^ (lane & 7)) << 4)); };
-            if (!(ok = wwait(o_done, it * NH + NH - 1))) break;
-            tc_fence_after();
+            // (the answer for the fourth chunk from here waits for v's place, and that for the rows' P two
+            // chunks on: it cannot overtake this wait)
+            if (!(ok = wwait(&v_checked[it & 3], it >> 2) && wwait(o_done, it * NH + NH - 1))) break;
+            if (__builtin_expect(v_flag[it & 3] != 0, 0)) {
+                float o[OC];
 #pragma unroll
-            for (int p = 0; p < OC / 32; ++p) {
-                float o[32];
-                tmem_ld32(tq + M::O + OC * hh + 32 * p, o);
+                for (int u = 0; u < OC; ++u) o[u] = o1[u];
+                if (lane < live) row_alone<D, IN, OC>(w, set, b, h, int(tw) + lane, c * C, min(c * C + C, T), col, o);
+                __syncwarp();
 #pragma unroll
-                for (int u = 0; u < 32; u += 2) {
-                    const float2 y = __ffma2_rn(make_float2(o[u], o[u + 1]), make_float2(os, os),
-                                                make_float2(o1[32 * p + u], o1[32 * p + u + 1]));
-                    o1[32 * p + u] = y.x, o1[32 * p + u + 1] = y.y;
+                for (int u = 0; u < OC; ++u) o1[u] = o[u];
+            } else {
+                tc_fence_after();
+#pragma unroll
+                for (int p = 0; p < OC / 32; ++p) {
+                    float o[32];
+                    tmem_ld32(tq + M::O + OC * hh + 32 * p, o);
+#pragma unroll
+                    for (int u = 0; u < 32; u += 2) {
+                        const float2 y = __ffma2_rn(make_float2(o[u], o[u + 1]), make_float2(os, os),
+                                                    make_float2(o1[32 * p + u], o1[32 * p + u + 1]));
+                        o1[32 * p + u] = y.x, o1[32 * p + u + 1] = y.y;
+                    }
                 }
             }
             tc_fence_before();
@@ -930,26 +989,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) mb_arrive(g_full);
         }
         if (!ok && lane == 0) record_error(ctl, ERR_MBAR_TIMEOUT);
-    } else if (TERMS > 1 && !state_only && w.row_dot) {
-        // ------------------------------------------------ x
-        if (lane == 0) {
-            constexpr int XN = IN == 1 ? 64 : 32;  // columns of a panel
-            bool done = true;
-            int it = 0;
+    } else if (!state_only) {
+        // ------------------------------------------------ x, and whether all of v is finite
+        constexpr int XN = IN == 1 ? 64 : 32;  // columns of a panel
+        const bool has_x = TERMS > 1 && w.row_dot != nullptr;
+        bool ok = true;
+        int loads = 0;
 #pragma unroll 1
-            for (; it < n && done; ++it) {
-                if (it > 0 && !(done = wait(x_empty, it - 1))) break;
-                mbar_arrive_expect_tx(x_full, 2 * kPanel);
-#pragma unroll 1
-                for (int p = 0; p < 2; ++p)
-                    tma_load_4d(sm + L::x + p * kPanel, &maps.x[blockIdx.y], NH == 2 ? 0 : v0 + XN * p, chunk_of(it) * C,
-                                (NH == 2 ? h0 + p : h0) / w.xdiv, b, x_full);
+        for (int it = 0; it < n; ++it) {
+            // 0 times an infinity or NaN is NaN, and stays it in a sum (of three terms the first tells)
+            if (!(ok = wwait(&v_full[it % L::NV], it / L::NV))) break;
+            const uint4 *v = reinterpret_cast<const uint4 *>(sm + L::v + (it % L::NV) * L::tile) + lane;
+            __nv_bfloat162 z[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[j] = __nv_bfloat162(bf16(0.f), bf16(0.f));
+            const __nv_bfloat162 zero = z[0];
+#pragma unroll 2
+            for (int i = 0; i < (IN == 1 ? 2 : 1) * kPanel / 512; ++i) {
+                const uint4 x = v[32 * i];
+                z[0] = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&x.x), zero, z[0]);
+                z[1] = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&x.y), zero, z[1]);
+                z[2] = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&x.z), zero, z[2]);
+                z[3] = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&x.w), zero, z[3]);
             }
-            // the last load lands before the block's shared memory is released
-            if (it > 0) done = wait(x_full, it - 1) && done;
-            if (!done) record_error(ctl, ERR_MBAR_TIMEOUT);
+            const __nv_bfloat162 sum = __hadd2(__hadd2(z[0], z[1]), __hadd2(z[2], z[3]));
+            const bool bad = __any_sync(0xffffffffu, !(__low2float(sum) + __high2float(sum) == 0.f));
+            if (lane == 0) {
+                v_flag[it & 3] = bad;
+                mb_arrive(&v_checked[it & 3]);
+                mb_arrive(&v_empty[it % L::NV]);
+            }
+            if (has_x) {
+                if (it > 0 && !(ok = wwait(x_empty, it - 1))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(x_full, 2 * kPanel);
+#pragma unroll 1
+                    for (int p = 0; p < 2; ++p)
+                        tma_load_4d(sm + L::x + p * kPanel, &maps.x[blockIdx.y], NH == 2 ? 0 : v0 + XN * p,
+                                    chunk_of(it) * C, (NH == 2 ? h0 + p : h0) / w.xdiv, b, x_full);
+                }
+                __syncwarp();
+                ++loads;
+            }
         }
-        __syncwarp();
+        // the last load of x lands before the block's shared memory is released
+        if (loads > 0) ok = wwait(x_full, loads - 1) && ok;
+        if (!ok && lane == 0) record_error(ctl, ERR_MBAR_TIMEOUT);
     }
     }
     tc_fence_before();

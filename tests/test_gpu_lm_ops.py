@@ -71,7 +71,7 @@ def test_attention_segments_and_spans(B, T, H, Hk, D, S0, dtype):
     _compare(_run_attn(d), _lm.attn_ref(d), dtype)
 
 
-@pytest.mark.parametrize("D,dtype", [(64, F32), (64, BF16), (128, BF16)])
+@pytest.mark.parametrize("D,dtype", [(64, F32), (64, BF16), (128, BF16), (128, F32)])
 def test_attention_many_lanes(D, dtype):
     # more lanes than SMs: every lane one walk; an odd number of heads
     d = _lm.attn_inputs(53, 140, 3, 3, D, dtype, False, seed=9)
@@ -140,6 +140,65 @@ def test_attention_reset_and_strong_decays(dtype):
     e["k"][:, :200, :], e["v"][:, :200], e["S0"] = 7.0, 3.0, e["S0"] * 5
     more = _run_attn(e, grads=False)
     assert torch.equal(more["o"][:, 200:, 0], got["o"][:, 200:, 0])
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D,H", [(64, 3), (128, 2)])
+def test_attention_values_that_do_not_reach(D, H, dtype, bad):
+    # an infinity or NaN reaches the steps after it (in the gradients' reverse walks: before it), its own head
+    # and, as a value, its own column, and nothing else: not the other steps of the tile that it is in
+    tol = FP32 if dtype == F32 else BF16_TWO
+    d = _lm.attn_inputs(2, 300, H, H, D, dtype, True, seed=31)
+    ref = _lm.attn_ref(d)
+    alone = [h for h in range(H) if h != 1]
+
+    def put(name, t):
+        x = {**d, name: d[name].clone()}
+        x[name][1, t, 1, 7] = bad
+        return _run_attn(x)
+
+    o = put("v", 200)["o"]
+    assert not torch.isfinite(o[1, 200:, 1, 7]).any()
+    check("o, other batch row", o[0], ref["o"][0], tol)
+    check("o, other heads", o[:, :, alone], ref["o"][:, :, alone], tol)
+    check("o, steps before", o[:, :200], ref["o"][:, :200], tol)
+    others = [c for c in range(D) if c != 7]
+    check("o, other columns", o[..., others], ref["o"][..., others], tol)
+    dq = put("k", 200)["dq"]
+    assert not torch.isfinite(dq[1, 200:, 1, 7]).any()
+    check("dq, steps before", dq[:, :200], ref["dq"][:, :200], tol)
+    check("dq, other heads", dq[:, :, alone], ref["dq"][:, :, alone], tol)
+    dk = put("q", 70)["dk"]
+    assert not torch.isfinite(dk[1, :71, 1, 7]).any()
+    check("dk, steps after", dk[:, 71:], ref["dk"][:, 71:], tol)
+    dv = put("grad_o", 130)["dv"]
+    assert not torch.isfinite(dv[1, :131, 1, 7]).any()
+    check("dv, steps after", dv[:, 131:], ref["dv"][:, 131:], tol)
+    check("dv, other batch row", dv[0], ref["dv"][0], tol)
+
+
+@pytest.mark.parametrize("B,T,H,Hk,D,dtype", [(1, 5000, 2, 1, 128, F32), (1, 7001, 1, 1, 64, F32), (1, 9000, 1, 1, 128, BF16),
+                                              (1, 12345, 3, 3, 64, BF16), (2, 3000, 12, 12, 128, F32)])
+def test_attention_many_chunks_a_segment(B, T, H, Hk, D, dtype):
+    # few lanes and a long sequence: segments of several chunks, whose states are found in a pass of its own
+    d = _lm.attn_inputs(B, T, H, Hk, D, dtype, True, seed=T, decay=0.05)
+    _compare(_run_attn(d, grads=False), _lm.attn_ref(d, grads=False), dtype)
+
+
+def test_attention_gradients_of_a_long_sequence():
+    # the gradients' walks in segments and spans, against the gradients of its two halves joined at the
+    # state between them
+    d = _lm.cuda(_lm.attn_inputs(1, 6000, 2, 2, 128, F32, True, seed=3, decay=0.05))
+    whole = api.linear_attention_bwd(d["q"], d["k"], d["v"], d["g"], d["grad_o"], d["S0"], d["grad_ST"])
+    a = {n: d[n][:, :2500].contiguous() for n in ("q", "k", "v", "g", "grad_o")}
+    c = {n: d[n][:, 2500:].contiguous() for n in ("q", "k", "v", "g", "grad_o")}
+    _, S = api.linear_attention_fwd(a["q"], a["k"], a["v"], a["g"], d["S0"], want_state=True)
+    late = api.linear_attention_bwd(c["q"], c["k"], c["v"], c["g"], c["grad_o"], S, d["grad_ST"])
+    early = api.linear_attention_bwd(a["q"], a["k"], a["v"], a["g"], a["grad_o"], d["S0"], late[4])
+    for n, w, x, y in zip(("dq", "dk", "dv", "dg"), whole, early, late):
+        check(n, w, torch.cat([x, y], 1), 2 * FP32)
+    check("dS0", whole[4], early[4], 2 * FP32)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
