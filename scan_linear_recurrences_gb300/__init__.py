@@ -1,6 +1,9 @@
 """GB300-native scan primitives of the minGRU family (matrix_affine_scan,
-matrix_scan, parallel_scan_log), forward and backward, as a C-ABI CUDA
-library (libmgscan, include/mgscan.h) with a thin Python binding.
+matrix_scan, parallel_scan_log), forward and backward, and operators of
+language models built on recurrences (linear attention with a decay for each
+head, the RMS norm with the residual's addition, clipping by the global norm
+of the gradients), as a C-ABI CUDA library (libmgscan, include/mgscan.h) with a
+thin Python binding.
 
 ``_binding`` mirrors the C entry points one to one; ``api`` adds tensor-level
 helpers and autograd wrappers; ``inputs`` draws the seeded synthetic inputs.
