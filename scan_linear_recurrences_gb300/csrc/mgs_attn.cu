@@ -8,8 +8,8 @@
 // time.  One walking kernel therefore serves attention and its three
 // gradients (AttnWalk).  The decay's gradient dg_t = <R_t, e^{g_t} S_{t-1}>
 // obeys dg_t = dg_{t+1} + <q_t, dq_t> - <k_t, dk_t>; summing that over a long
-// sequence in fp32 would lose digits, so the walks leave S and R every
-// kAttnSpan steps and the sum restarts there from <R, S>.
+// sequence in fp32 would lose digits, so the walks leave S and R at the end of
+// every span of steps and the sum restarts there from <R, S>.
 //
 // Few (batch, head) lanes and a long sequence: time is cut into segments; a
 // state-only walk gives each segment's own state, a short scan joins them, and
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(D *D / 32) attn_rec_kernel(const __grid_consta
         bool tr = false;
         if (!STATE_ONLY) {
             if (nseg > 1)
-                in = w.seg_in + (lane * nseg + seg) * D * D, tr = w.seg_t;
+                in = w.seg_in + (lane * nseg + seg) * D * D;
             else if (w.s_in)
                 in = w.s_in + lane * D * D, tr = w.s_in_t;
         }
@@ -104,8 +104,8 @@ __global__ void __launch_bounds__(D *D / 32) attn_rec_kernel(const __grid_consta
         const int nn = int(min64(TS, t1 - nbase));
         if (nbase >= t0 && nbase < t1) fetch(nbase, nn);
         const int64_t end = base + n;
-        if (!STATE_ONLY && w.ckpt && w.rev && (end % kAttnSpan == 0 || end == set.T))
-            put_state(w.ckpt + (lane * set.spans + (end - 1) / kAttnSpan) * D * D, false);
+        if (!STATE_ONLY && w.ckpt && w.rev && (end % set.span == 0 || end == set.T))
+            put_state(w.ckpt + (lane * set.spans + (end - 1) / set.span) * D * D, false);
         if (STATE_ONLY && tid == 0)
             for (int u = 0; u < n; ++u) total += double(sg[u]);
         float2 prev = make_float2(1.f, 0.f);  // reverse: the decay of step t + 1, applied as step t is added
@@ -173,8 +173,8 @@ __global__ void __launch_bounds__(D *D / 32) attn_rec_kernel(const __grid_consta
                     if (u < n && c == 0) w.row_dot[(b * set.T + base + u) * set.H + h] = dot;
                 }
             }
-            if (w.ckpt && !w.rev && (end % kAttnSpan == 0 || end == set.T))
-                put_state(w.ckpt + (lane * set.spans + (end - 1) / kAttnSpan) * D * D, false);
+            if (w.ckpt && !w.rev && (end % set.span == 0 || end == set.T))
+                put_state(w.ckpt + (lane * set.spans + (end - 1) / set.span) * D * D, false);
             __syncthreads();
         }
         base = nbase;
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(D *D / 32) attn_rec_kernel(const __grid_consta
     }
     if (STATE_ONLY) {
         float *to = w.seg_out + (lane * nseg + seg) * D * D;
-        put_state(to, w.seg_t);
+        put_state(to, false);
         if (tid == 0) w.seg_out[int64_t(set.B) * set.H * nseg * D * D + lane * nseg + seg] = float(total);
     } else if (w.s_out && seg == (w.rev ? 0 : nseg - 1)) {
         put_state(w.s_out + lane * D * D, false);
@@ -256,19 +256,20 @@ __global__ void __launch_bounds__(256)
                    const float *__restrict__ ckR, float *__restrict__ dg, float *__restrict__ part, int64_t T,
                    int64_t H, int spans, int DD) {
     __shared__ float red[8], scan[8];
+    const int NT = blockDim.x;  // a thread has four of the span's steps
     const int64_t lane = blockIdx.x / spans;
     const int span = int(blockIdx.x % spans), tid = threadIdx.x;
     const int64_t b = lane / H, h = lane % H;
-    const int64_t t0 = span * kAttnSpan;
-    const int n = int(min64(kAttnSpan, T - t0));
+    const int64_t t0 = int64_t(span) * 4 * NT;
+    const int n = int(min64(4 * NT, T - t0));
     float tail = 0.f;
     if (ckS) {
         const float *a = ckS + (lane * spans + span) * DD, *c = ckR + (lane * spans + span) * DD;
         float acc = 0.f;
-        for (int e0 = 4 * tid; e0 < DD; e0 += 4096) {  // DD is a multiple of 4096: four pieces at a time
+        for (int e0 = 4 * tid; e0 < DD; e0 += 16 * NT) {  // DD is a multiple of 4096: four pieces at a time
             float x[4][4], y[4][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) load4(a + e0 + 1024 * j, x[j]), load4(c + e0 + 1024 * j, y[j]);
+            for (int j = 0; j < 4; ++j) load4(a + e0 + 4 * NT * j, x[j]), load4(c + e0 + 4 * NT * j, y[j]);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 acc += (x[j][0] * y[j][0] + x[j][1] * y[j][1]) + (x[j][2] * y[j][2] + x[j][3] * y[j][3]);
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(256)
     __syncthreads();
     const float next = __shfl_down_sync(0xffffffffu, suf, 1);
     float after = tail + ((tid & 31) != 31 ? next : 0.f);
-    for (int i = (tid >> 5) + 1; i < 8; ++i) after += scan[i];
+    for (int i = (tid >> 5) + 1; i < NT / 32; ++i) after += scan[i];
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -442,9 +443,16 @@ bool mma_takes(const mgs_attention_shape &sh, bool backward) {
     return qk && apart(sh.v_stride, sh.H) && (!backward || apart(sh.do_stride, sh.H));
 }
 
+// Steps over which the decay's gradient is summed between exact restarts.  The
+// error grows with them (one decay a head, 16 x 1024 steps of 8 heads of 64 in
+// fp32: 7e-7 with 1024, 5e-7 with 512, 3e-7 with 256), the states to be kept
+// shrink (the gradients' time 232, 236 and 241 us; heads of 128: 295, 301, 320).
+// bf16 reads half the bytes for as many states: 9e-7 with 1024.
+constexpr int kSpanF32 = 512, kSpanBF16 = 1024;
+
 struct Plan {
     int64_t lanes, chunks, seg_len;
-    int nseg, spans, parts;
+    int nseg, spans, parts, span;
     bool mma;
 };
 Plan plan_of(const mgs_attention_shape &sh, int walks) {
@@ -470,7 +478,8 @@ Plan plan_of(const mgs_attention_shape &sh, int walks) {
     if (p.seg_len < kAttnChunk) p.seg_len = kAttnChunk;
     p.nseg = int((sh.T + p.seg_len - 1) / p.seg_len);
     if (p.nseg < 1) p.nseg = 1;
-    p.spans = int((sh.T + kAttnSpan - 1) / kAttnSpan);
+    p.span = f32 ? kSpanF32 : kSpanBF16;
+    p.spans = int((sh.T + p.span - 1) / p.span);
     return p;
 }
 
@@ -507,7 +516,7 @@ AttnSet set_of(const mgs_attention_shape &sh, const Plan &p, const float *g, con
     else
         copy3(s.gs, sh.g_stride);
     s.B = sh.B, s.T = sh.T, s.H = sh.H;
-    s.seg_len = p.seg_len, s.nseg = p.nseg, s.spans = p.spans;
+    s.seg_len = p.seg_len, s.nseg = p.nseg, s.spans = p.spans, s.span = p.span;
     s.ctl = ctl;
     s.tries = uint32_t(min64(int64_t(ctl.timeout_ns / 40) + 1000, 0x7fffffff));
     for (auto &w : s.w) w.qdiv = w.kdiv = w.vdiv = w.xdiv = 1, w.o_scale = w.kv_scale = 1.f;
@@ -666,7 +675,7 @@ cudaError_t launch_attn_bwd(const mgs_attention_shape &sh, const void *q, const 
     a.out = group > 1 ? static_cast<void *>(dqf) : dq, a.out_f32 = group > 1;
     r.out = group > 1 ? static_cast<void *>(dkf) : dk, r.out_f32 = group > 1;
     if ((e = run_walks(set, 3, sh, p, carve, s)) != cudaSuccess) return e;
-    attn_dg_kernel<<<unsigned(p.lanes * p.spans), 256, 0, s>>>(u, wd, p.parts, ends ? ckS : nullptr, ckR,
+    attn_dg_kernel<<<unsigned(p.lanes * p.spans), unsigned(p.span / 4), 0, s>>>(u, wd, p.parts, ends ? ckS : nullptr, ckR,
                                                               sh.fixed_decay ? nullptr : dg,
                                                               sh.fixed_decay ? part : nullptr, sh.T, sh.H, p.spans,
                                                               sh.D * sh.D);

@@ -218,6 +218,21 @@ __device__ __forceinline__ void row_alone(const AttnWalk &w, const AttnSet &set,
     }
 }
 
+// fp32: a product's second sum onto its first, 16 columns at a time
+template <int N>
+__device__ __forceinline__ void add_second(uint32_t taddr, float (&x)[N]) {
+#pragma unroll
+    for (int p = 0; p < N; p += 16) {
+        float y[16];
+        tmem_ld16(taddr + p, y);
+#pragma unroll
+        for (int u = 0; u < 16; u += 2) {
+            const float2 z = __fadd2_rn(make_float2(x[p + u], x[p + u + 1]), make_float2(y[u], y[u + 1]));
+            x[p + u] = z.x, x[p + u + 1] = z.y;
+        }
+    }
+}
+
 template <int D, int TERMS, int IN>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_mma_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnSet set, int state_only) {
@@ -315,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int p = 0; p < OC / 32; ++p) {
                     float x[32];
                     tmem_ld32(tq + M::X + OC * hh + 32 * p, x);
+                    if (KH == 2) add_second(tq + M::X + 64 + OC * hh, x);
 #pragma unroll
                     for (int u = 0; u < 32; u += 2) {
                         const float2 y = __fmul2_rn(make_float2(x[u], x[u + 1]), make_float2(ri, ri));
@@ -444,6 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int p = 0; p < OC / 32; ++p) {
                     float o[32];
                     tmem_ld32(tq + M::O + OC * hh + 32 * p, o);
+                    if (IN == 3) add_second(tq + M::O + 64 + OC * hh, o);
 #pragma unroll
                     for (int u = 0; u < 32; u += 2) {
                         const float2 y = __ffma2_rn(make_float2(o[u], o[u + 1]), make_float2(os, os),
@@ -583,6 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         const bool marks = w.ckpt != nullptr;
+        const int per_span = set.span / C;
         float decay = 0.f, next_decay = 0.f;  // of the chunk whose product is taken, and of the walked one
         bool ok = ok0 && staged();
 #pragma unroll 1
@@ -591,8 +609,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // chunk is walked), and at the walk's end.
             if (!state_only) {
                 const int ce = rev ? chunk_of(it) : chunk_of(it - 1);
-                if (marks && (rev ? it < n : it > 0) && ((ce + 1) % (kAttnSpan / C) == 0 || (ce + 1) * C >= T)) {
-                    if (live) put_state(w.ckpt + (ln * set.spans + ce / (kAttnSpan / C)) * D * D);
+                if (marks && (rev ? it < n : it > 0) && ((ce + 1) % per_span == 0 || (ce + 1) * C >= T)) {
+                    if (live) put_state(w.ckpt + (ln * set.spans + ce / per_span) * D * D);
                     if (!(ok = staged())) break;
                 }
                 if (it == n) {
@@ -697,6 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int u = 0; u < SC; u += 16) {
                     float x[16];
                     tmem_ld16(tq + M::X + (NH == 2 ? 64 * hp : 0) + col + u, x);
+                    if (IN == 3) add_second(tq + M::X + 64 + col + u, x);
 #pragma unroll
                     for (int m = 0; m < 16; m += 2) {
                         const float2 y = __ffma2_rn(make_float2(decay, decay), make_float2(s[u + m], s[u + m + 1]),
@@ -728,7 +747,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Products of two sums of three terms: the pairs down to 2^-16 of the first,
             // (2,0) (1,1) (1,0) (0,2) (0,1) (0,0); a sum with an exact operand: its terms.  The
             // smallest first: the sums are cut off, not rounded, at each step, so that the fewest
-            // steps should be made at full size.
+            // steps should be made at full size.  For the same reason fp32's products over the 128
+            // steps, and Q S with heads of 128, are two sums, added by who reads them.
             auto last = [](int m) { return IN == 1 ? 0 : 2 - m; };
             bool add = false;  // onto what is there
             // Descriptors hold addresses in units of 16 bytes: what is issued is one of these
@@ -760,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int hp = 0; hp < NH; ++hp) {
                     const uint64_t q = dQ + uint64_t(((tile_i % L::NQ) * L::tile + hp * kPanel) >> 4);
-                    add = kh > 0;
+                    add = false;
 #pragma unroll 1
                     for (int m = TERMS - 1; m >= 0; --m) {
                         const uint64_t st = dS + uint64_t((m * L::sterm + (hp + kh) * 8192) >> 4);
@@ -768,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int o = last(m); o >= 0; --o)
 #pragma unroll 1
                             for (int ks = 0; ks < KS; ++ks, add = true)
-                                umma_bf16_ss(tm + M::X + 64 * hp, q + koff(ks) + uint64_t(o * (kPanel >> 4)),
+                                umma_bf16_ss(tm + M::X + 64 * (hp + kh), q + koff(ks) + uint64_t(o * (kPanel >> 4)),
                                              st + uint64_t(ks * 128), id_o, add);
                     }
                 }
@@ -777,31 +797,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto kv = [&](int it, int half) {
                 const uint64_t v = dV + uint64_t(((it % L::NV) * L::tile + half * (NG / 2) * 2048) >> 4);
                 const uint32_t a = tm + (state_only && (it & 1) ? M::A : M::W) + half * (NG / 2) * 8;
-                add = half > 0;
+                add = IN == 1 && half > 0;
 #pragma unroll 1
                 for (int m = 2; m >= 0; --m)
 #pragma unroll 1
                     for (int o = last(m); o >= 0; --o)
 #pragma unroll 1
                         for (int i = 0; i < NG / 2; ++i, add = true)
-                            umma_bf16_ts(tm + M::X, a + 64 * m + 8 * i, v + uint64_t(i * 128 + o * (kPanel >> 4)), id_mn,
+                            umma_bf16_ts(tm + M::X + (IN == 3 ? 64 * half : 0), a + 64 * m + 8 * i, v + uint64_t(i * 128 + o * (kPanel >> 4)), id_mn,
                                          add);
             };
             auto pv = [&](int it, int hp) {
                 const uint64_t v = dV + uint64_t(((it % L::NV) * L::tile + hp * kPanel) >> 4);
-                add = false;
+                constexpr int KP = IN == 1 ? C / 16 : C / 32;  // steps of a sum
 #pragma unroll 1
-                for (int m = TERMS - 1; m >= 0; --m) {
-                    // of three terms, 16 steps' first and second ones lie side by side, the third
-                    // ones behind all of those
-                    const uint32_t p = tm + M::P + (TERMS == 1 ? 0 : m == 2 ? 128 : 8 * m);
-                    const uint32_t step = TERMS == 1 || m == 2 ? 8 : 16;
+                for (int k0 = 0; k0 < C / 16; k0 += KP) {
+                    add = false;
 #pragma unroll 1
-                    for (int o = last(m); o >= 0; --o)
+                    for (int m = TERMS - 1; m >= 0; --m) {
+                        // of three terms, 16 steps' first and second ones lie side by side, the third
+                        // ones behind all of those
+                        const uint32_t p = tm + M::P + (TERMS == 1 ? 0 : m == 2 ? 128 : 8 * m);
+                        const uint32_t step = TERMS == 1 || m == 2 ? 8 : 16;
 #pragma unroll 1
-                        for (int ks = 0; ks < C / 16; ++ks, add = true)
-                            umma_bf16_ts(tm + M::O + 64 * hp, p + ks * step, v + uint64_t(ks * 128 + o * (kPanel >> 4)),
-                                         id_o, add);
+                        for (int o = last(m); o >= 0; --o)
+#pragma unroll 1
+                            for (int ks = k0; ks < k0 + KP; ++ks, add = true)
+                                umma_bf16_ts(tm + M::O + 64 * hp + (k0 > 0 ? 64 : 0), p + ks * step,
+                                             v + uint64_t(ks * 128 + o * (kPanel >> 4)), id_o, add);
+                    }
                 }
                 umma_commit(o_done);
             };

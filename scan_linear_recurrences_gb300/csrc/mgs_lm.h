@@ -13,7 +13,6 @@
 namespace mgs {
 
 constexpr int64_t kAttnChunk = 128;   // time steps of a chunk; segments are whole chunks
-constexpr int64_t kAttnSpan = 1024;   // steps over which the decay's gradient is summed between exact restarts
 
 // One walk over time of out_t = o_scale * S_t^T q_t with
 //   forward:  S_t = e^{g_t} S_{t-1} + kv_scale * k_t v_t^T,  t = 0..T-1
@@ -35,7 +34,6 @@ struct AttnWalk {
     float *ckpt;                  // [B H][spans][D][D]: the state at each span's end (null: not wanted)
     const float *seg_in;          // [B H][nseg][D][D]: the state at each segment's start (nseg > 1)
     float *seg_out;               // [B H][nseg][D][D]: state-only pass: each segment's own state
-    int seg_t;                    // ... stored transposed
     float o_scale, kv_scale;
     int rev;
 };
@@ -48,6 +46,7 @@ struct AttnSet {
     int first;                    // the launch's first walk
     int64_t seg_len;              // steps of a segment (a multiple of kAttnChunk)
     int nseg, spans;
+    int span;                     // steps between two states that are kept: whole chunks
     uint32_t tries;               // a barrier wait's limit: tries of about 40 ns
     DevCtl ctl;
 };
