@@ -201,6 +201,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     const int64_t lane = blockIdx.y;
     const int e = 4 * int(blockIdx.x * blockDim.x + threadIdx.x);
     const int nseg = set.nseg;
+    griddep_launch();
+    griddep_wait();
     float *st = w.seg_out + lane * nseg * D * D + e;
     const float *total = w.seg_out + int64_t(set.B) * set.H * nseg * D * D + lane * nseg;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
@@ -358,6 +360,7 @@ struct SplitSet {
 };
 template <int D>
 __global__ void __launch_bounds__(256) attn_split_kernel(const __grid_constant__ SplitSet set) {
+    griddep_launch();
     const int which = blockIdx.y, heads = set.heads[which];
     const int64_t rows = set.B * set.T * heads, n4 = rows * (D / 4), plane = rows * D;
     const float *in = set.in[which];
@@ -559,20 +562,18 @@ cudaError_t run_walks(AttnSet &set, int walks, const mgs_attention_shape &sh, co
     // digit of fp32; dv, and the attention itself, are rounded to the type.
     auto walk = [&](bool state_only) {
         if (!p.mma) return launch_attn_rec(set, walks, sh.D, sh.dtype, state_only, s);
-        if (walks == 1 || state_only || sh.dtype == MGS_F32)
-            return launch_attn_mma(set, 0, walks, sh.D, sh.dtype, 1, state_only, s);
-        const cudaError_t e = launch_attn_mma(set, 0, 2, sh.D, sh.dtype, 3, false, s);
-        return e != cudaSuccess ? e : launch_attn_mma(set, 2, 1, sh.D, sh.dtype, 1, false, s);
+        const bool early = !state_only && p.nseg > 1;  // after attn_join
+        if (sh.dtype == MGS_F32) return launch_attn_mma(set, 0, walks, sh.D, sh.dtype, 3, state_only, true, s);
+        if (walks == 1 || state_only) return launch_attn_mma(set, 0, walks, sh.D, sh.dtype, 1, state_only, early, s);
+        const cudaError_t e = launch_attn_mma(set, 0, 2, sh.D, sh.dtype, 3, false, early, s);
+        return e != cudaSuccess ? e : launch_attn_mma(set, 2, 1, sh.D, sh.dtype, 1, false, false, s);
     };
     if (set.nseg > 1) {
         for (int i = 0; i < walks; ++i) set.w[i].seg_in = set.w[i].seg_out = ws.take<float>(seg_bytes(p, sh.D));
         if ((e = walk(true)) != cudaSuccess) return e;
         const dim3 grid(unsigned(sh.D * sh.D / 1024), unsigned(sh.B * sh.H), unsigned(walks));
-        if (sh.D == 64)
-            attn_join_kernel<64><<<grid, 256, 0, s>>>(set);
-        else
-            attn_join_kernel<128><<<grid, 256, 0, s>>>(set);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        auto *join = sh.D == 64 ? attn_join_kernel<64> : attn_join_kernel<128>;
+        if ((e = launch_next(join, grid, 256, 0, s, p.mma, set)) != cudaSuccess) return e;
     }
     return walk(false);
 }

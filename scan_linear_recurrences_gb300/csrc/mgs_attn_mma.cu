@@ -293,6 +293,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    griddep_launch();
+    // what kernels of this call have written: fp32's terms here; bf16's states below, where they are read
+    if (IN == 3) griddep_wait();
     const uint32_t tm = *slot;
     const uint32_t tq = tm + (uint32_t(32 * (warp & 3)) << 16);
     // A role whose wait gives up says so and ends; the others' waits then give up too.
@@ -539,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         {
             const float *in = nullptr;
             bool tr = false;
+            if (IN == 1) griddep_wait();
             if (!state_only && live) {
                 if (nseg > 1)
                     in = w.seg_in + (ln * nseg + seg) * D * D;
@@ -1082,7 +1086,7 @@ cudaError_t tile_map(CUtensorMap *m, const void *base, const int64_t (&st)[3], i
 }
 
 template <int D, int TERMS, int IN>
-cudaError_t go(const AttnMaps &maps, const AttnSet &set, int nwalks, bool state_only, cudaStream_t s) {
+cudaError_t go(const AttnMaps &maps, const AttnSet &set, int nwalks, bool state_only, bool early, cudaStream_t s) {
     using L = Smem<D, TERMS, IN>;
     const void *fn = (const void *)attn_mma_kernel<D, TERMS, IN>;
     cudaError_t e = ensure_smem_attr(fn, int(L::bytes));
@@ -1097,14 +1101,13 @@ cudaError_t go(const AttnMaps &maps, const AttnSet &set, int nwalks, bool state_
     }
     if (regs.load() != kRegs) return cudaErrorInvalidDeviceFunction;
     const dim3 grid(unsigned(set.B * ((set.H + L::NH - 1) / L::NH) * (D / L::VD) * set.nseg), unsigned(nwalks));
-    attn_mma_kernel<D, TERMS, IN><<<grid, kThreads, L::bytes, s>>>(maps, set, state_only);
-    return cudaGetLastError();
+    return launch_next(attn_mma_kernel<D, TERMS, IN>, grid, kThreads, L::bytes, s, early, maps, set, int(state_only));
 }
 
 }  // namespace
 
 cudaError_t launch_attn_mma(const AttnSet &all, int first, int nwalks, int D, int dtype, int terms, bool state_only,
-                            cudaStream_t s) {
+                            bool early, cudaStream_t s) {
     AttnMaps maps;
     AttnSet set = all;
     set.first = first;
@@ -1123,14 +1126,10 @@ cudaError_t launch_attn_mma(const AttnSet &all, int first, int nwalks, int D, in
             (e = tile_map(&maps.o[i], w.out, w.os, set.B, set.T, set.H, D, 32, f32)) != cudaSuccess)
             return e;
     }
-    if (f32)
-        return D == 64 ? go<64, 3, 3>(maps, set, nwalks, state_only, s)
-                       : go<128, 3, 3>(maps, set, nwalks, state_only, s);
-    if (D == 64)
-        return terms == 1 ? go<64, 1, 1>(maps, set, nwalks, state_only, s)
-                          : go<64, 3, 1>(maps, set, nwalks, state_only, s);
-    return terms == 1 ? go<128, 1, 1>(maps, set, nwalks, state_only, s)
-                      : go<128, 3, 1>(maps, set, nwalks, state_only, s);
+    auto *fn = f32 ? (D == 64 ? go<64, 3, 3> : go<128, 3, 3>)
+               : D == 64 ? (terms == 1 ? go<64, 1, 1> : go<64, 3, 1>)
+                         : (terms == 1 ? go<128, 1, 1> : go<128, 3, 1>);
+    return fn(maps, set, nwalks, state_only, early, s);
 }
 
 }  // namespace mgs

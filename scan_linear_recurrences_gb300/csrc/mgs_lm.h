@@ -51,14 +51,33 @@ struct AttnSet {
     DevCtl ctl;
 };
 
+// Kernels of one call that follow one another: the next one's blocks are set up
+// while the last of this one's still run (griddep_launch, called by a block, lets
+// them be launched when all blocks have called it), and wait for what this one
+// writes (griddep_wait: until it has ended).
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_next(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, bool early,
+                        A... args) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = grid, c.blockDim = dim3(threads), c.dynamicSmemBytes = smem, c.stream = s;
+    cudaLaunchAttribute a = {};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &a, c.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
 // SIMT walk: the recurrence itself in fp32, any supported type and size
 cudaError_t launch_attn_rec(const AttnSet &set, int nwalks, int D, int dtype, bool state_only, cudaStream_t s);
 
 // Tensor-core walks `first` .. of the set.  terms: bf16 terms of the computed
 // operands of the output.  fp32: q, k and v are each three dense
 // bf16 tensors behind one another (attn_split), out and x are fp32.
+// early: it follows a kernel of the same call that lets it be launched early.
 cudaError_t launch_attn_mma(const AttnSet &set, int first, int nwalks, int D, int dtype, int terms, bool state_only,
-                            cudaStream_t s);
+                            bool early, cudaStream_t s);
 
 size_t attn_workspace_bytes(const mgs_attention_shape &sh, bool backward);
 cudaError_t launch_attn_fwd(const mgs_attention_shape &sh, const void *q, const void *k, const void *v,
