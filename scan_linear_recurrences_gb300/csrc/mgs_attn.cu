@@ -563,10 +563,10 @@ cudaError_t run_walks(AttnSet &set, int walks, const mgs_attention_shape &sh, co
     auto walk = [&](bool state_only) {
         if (!p.mma) return launch_attn_rec(set, walks, sh.D, sh.dtype, state_only, s);
         const bool early = !state_only && p.nseg > 1;  // after attn_join
-        if (sh.dtype == MGS_F32) return launch_attn_mma(set, 0, walks, sh.D, sh.dtype, 3, state_only, true, s);
-        if (walks == 1 || state_only) return launch_attn_mma(set, 0, walks, sh.D, sh.dtype, 1, state_only, early, s);
-        const cudaError_t e = launch_attn_mma(set, 0, 2, sh.D, sh.dtype, 3, false, early, s);
-        return e != cudaSuccess ? e : launch_attn_mma(set, 2, 1, sh.D, sh.dtype, 1, false, false, s);
+        if (sh.dtype == MGS_F32) return launch_attn_mma(set, 0, walks, sh.D, sh.dtype, 3, state_only, true, false, s);
+        if (walks == 1 || state_only) return launch_attn_mma(set, 0, walks, sh.D, sh.dtype, 1, state_only, early, false, s);
+        const cudaError_t e = launch_attn_mma(set, 0, 2, sh.D, sh.dtype, 3, false, early, false, s);
+        return e != cudaSuccess ? e : launch_attn_mma(set, 2, 1, sh.D, sh.dtype, 1, false, false, true, s);
     };
     if (set.nseg > 1) {
         for (int i = 0; i < walks; ++i) set.w[i].seg_in = set.w[i].seg_out = ws.take<float>(seg_bytes(p, sh.D));

@@ -293,8 +293,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    griddep_launch();
-    // what kernels of this call have written: fp32's terms here; bf16's states below, where they are read
+    // What kernels of this call have written: fp32's terms are waited for here, bf16's states
+    // below, where they are read (a kernel that runs beside this one may count on them too).
+    if (IN == 3 || state_only) griddep_launch();
     if (IN == 3) griddep_wait();
     const uint32_t tm = *slot;
     const uint32_t tq = tm + (uint32_t(32 * (warp & 3)) << 16);
@@ -542,7 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         {
             const float *in = nullptr;
             bool tr = false;
-            if (IN == 1) griddep_wait();
+            if (IN == 1 && !set.beside) griddep_wait();
+            if (IN == 1 && !state_only) griddep_launch();
             if (!state_only && live) {
                 if (nseg > 1)
                     in = w.seg_in + (ln * nseg + seg) * D * D;
@@ -558,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
 #pragma unroll
                 for (int u = 0; u < SC; u += 4) {  // piece u / 16, rows of j = u / 4 % 4
-                    const float4 x = *reinterpret_cast<const float4 *>(in + moved + (u >> 4) * 16 + ((u >> 2) & 3) * 8 * D);
+                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(in + moved + (u >> 4) * 16 + ((u >> 2) & 3) * 8 * D));
                     s[u] = x.x, s[u + 1] = x.y, s[u + 2] = x.z, s[u + 3] = x.w;
                 }
 #pragma unroll
@@ -1071,6 +1073,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tm, 512);
     }
+    // what follows this kernel follows the one beside it too: one block's end is enough for that
+    if (set.beside && blockIdx.x == gridDim.x - 1 && blockIdx.y == 0) griddep_wait();
 }
 
 // [B][T][heads][D] with any strides: boxes of 128 bytes x `steps` steps of one head
@@ -1107,10 +1111,10 @@ cudaError_t go(const AttnMaps &maps, const AttnSet &set, int nwalks, bool state_
 }  // namespace
 
 cudaError_t launch_attn_mma(const AttnSet &all, int first, int nwalks, int D, int dtype, int terms, bool state_only,
-                            bool early, cudaStream_t s) {
+                            bool early, bool beside, cudaStream_t s) {
     AttnMaps maps;
     AttnSet set = all;
-    set.first = first;
+    set.first = first, set.beside = beside;
     const bool f32 = dtype == MGS_F32;
     const int64_t B = set.B * (f32 ? 3 : 1);  // fp32 comes as three bf16 tensors behind one another
     cudaError_t e;
@@ -1129,7 +1133,7 @@ cudaError_t launch_attn_mma(const AttnSet &all, int first, int nwalks, int D, in
     auto *fn = f32 ? (D == 64 ? go<64, 3, 3> : go<128, 3, 3>)
                : D == 64 ? (terms == 1 ? go<64, 1, 1> : go<64, 3, 1>)
                          : (terms == 1 ? go<128, 1, 1> : go<128, 3, 1>);
-    return fn(maps, set, nwalks, state_only, early, s);
+    return fn(maps, set, nwalks, state_only, early || beside, s);
 }
 
 }  // namespace mgs

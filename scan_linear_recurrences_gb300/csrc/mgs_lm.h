@@ -44,6 +44,7 @@ struct AttnSet {
     int64_t gs[3];
     int64_t B, T, H;
     int first;                    // the launch's first walk
+    int beside;                   // launched beside other walks, with whose kernel it shares nothing but its end
     int64_t seg_len;              // steps of a segment (a multiple of kAttnChunk)
     int nseg, spans;
     int span;                     // steps between two states that are kept: whole chunks
@@ -75,9 +76,10 @@ cudaError_t launch_attn_rec(const AttnSet &set, int nwalks, int D, int dtype, bo
 // Tensor-core walks `first` .. of the set.  terms: bf16 terms of the computed
 // operands of the output.  fp32: q, k and v are each three dense
 // bf16 tensors behind one another (attn_split), out and x are fp32.
-// early: it follows a kernel of the same call that lets it be launched early.
+// early: it follows a kernel of the same call that lets it be launched early;
+// beside: that kernel is of other walks, beside which these run.
 cudaError_t launch_attn_mma(const AttnSet &set, int first, int nwalks, int D, int dtype, int terms, bool state_only,
-                            bool early, cudaStream_t s);
+                            bool early, bool beside, cudaStream_t s);
 
 size_t attn_workspace_bytes(const mgs_attention_shape &sh, bool backward);
 cudaError_t launch_attn_fwd(const mgs_attention_shape &sh, const void *q, const void *k, const void *v,
