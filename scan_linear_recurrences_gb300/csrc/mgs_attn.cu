@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(D *D / 32) attn_rec_kernel(const __grid_consta
                 if (w.row_dot) {
 #pragma unroll
                     for (int m = 1; m < D / 4; m <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, m);
-                    if (u < n && c == 0) w.row_dot[(b * set.T + base + u) * set.H + h] = dot;
+                    if (u < n && c == 0) w.row_dot[lane * set.T + base + u] = dot;
                 }
             }
             if (w.ckpt && !w.rev && (end % set.span == 0 || end == set.T))
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int t = 4 * tid + i;
-            const int64_t at = (b * T + t0 + t) * H + h + p * all;
+            const int64_t at = lane * T + t0 + t + p * all;
             x[i] = t < n ? u[at] : 0.f;
             y[i] = t < n ? w[at] : 0.f;
         }

@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 // a head in two warps, or in two of each of two blocks: each leaves its own product
                 if (lane < live)
-                    w.row_dot[(NH == 2 ? 0 : (v0 / OC + hh) * set.B * set.T * set.H) + (b * set.T + tw + lane) * set.H + h] =
+                    w.row_dot[(NH == 2 ? 0 : (v0 / OC + hh) * set.B * set.T * set.H) + (int64_t(b) * set.H + h) * set.T + tw + lane] =
                         dot.x + dot.y;
             }
             if (IN == 1 && w.out_f32) {

@@ -30,7 +30,7 @@ struct AttnWalk {
     const float *s_in;            // state at the walk's start, [B H][D][D] (null: zeros)
     int s_in_t;                   // ... stored transposed
     float *s_out;                 // state at the walk's end, [B H][D][D] (null: not wanted)
-    float *row_dot;               // [parts][B][T][H]: <out_t, x_t> before rounding, in parts to be added
+    float *row_dot;               // [parts][B H][T]: <out_t, x_t> before rounding, in parts to be added
     float *ckpt;                  // [B H][spans][D][D]: the state at each span's end (null: not wanted)
     const float *seg_in;          // [B H][nseg][D][D]: the state at each segment's start (nseg > 1)
     float *seg_out;               // [B H][nseg][D][D]: state-only pass: each segment's own state
