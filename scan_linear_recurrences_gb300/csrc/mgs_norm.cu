@@ -8,6 +8,9 @@
 // (dx is the gradient of x and of res alike).  All sums in fp32.  Bound by
 // memory: each tensor is read or written once, a row stays in registers
 // between the sum and its use.
+#include <cstring>
+#include <type_traits>
+
 #include "mgs_lm.h"
 #include "mgs_num.cuh"
 
@@ -61,12 +64,94 @@ __device__ __forceinline__ void put8(uint8_t *p, const float (&v)[V]) {
         *reinterpret_cast<uint32_t *>(p + i) = e4m3x2(v[i], v[i + 1]) | (e4m3x2(v[i + 2], v[i + 3]) << 16);
 }
 
+// The V elements from column e of a row, as one piece of 16 bytes.  SHIFT: N is no
+// multiple of V, so that rows start anywhere; a row's pieces are then those of
+// the whole tensor that it lies in, the first one starting `s` elements before
+// the row, and what of them is the neighbouring rows' is masked.  s is the same
+// for all of a thread's rows: they are a multiple of V rows apart.
+// (32768 rows of 1001 in bf16, element by element: forward 118 us, backward 208;
+// so: 55 and 73.)
+template <typename T, bool SHIFT>
+struct Window {
+    static constexpr int V = kVec<T>;
+    const int64_t rows;
+    const int N, s;
+    __device__ __forceinline__ Window(int64_t row, int64_t rows_, int N_)
+        : rows(rows_), N(N_), s(SHIFT ? int((row * N_) % V) : 0) {}
+    // the piece's elements lo .. hi - 1 are the row's
+    __device__ __forceinline__ int lo(int e) const { return max(0, s - e); }
+    __device__ __forceinline__ int hi(int e) const { return min(V, N + s - e); }
+    __device__ __forceinline__ uint4 load(const T *p, int64_t row, int e) const {
+        if (row >= rows || e >= N + s) return make_uint4(0u, 0u, 0u, 0u);
+        const T *at = p + row * N + (e - s);
+        if (!SHIFT || (rows - row) * N - (e - s) >= V) return load_once(at);
+        T v[V];  // the tensor ends within the piece
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = j < hi(e) ? at[j] : from_f<T>(0.f);
+        uint4 u;
+        memcpy(&u, v, 16);
+        return u;
+    }
+    __device__ __forceinline__ void mask(int e, float (&v)[V]) const {
+        if (!SHIFT) return;
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = j >= lo(e) && j < hi(e) ? v[j] : 0.f;
+    }
+    __device__ __forceinline__ uint4 weight(const T *w, int e) const {
+        if (!SHIFT) return e < N ? *reinterpret_cast<const uint4 *>(w + e) : make_uint4(0u, 0u, 0u, 0u);
+        T v[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = j >= lo(e) && j < hi(e) ? w[e - s + j] : from_f<T>(0.f);
+        uint4 u;
+        memcpy(&u, v, 16);
+        return u;
+    }
+    __device__ __forceinline__ void store(T *p, int64_t row, int e, const uint4 &u) const {
+        if (row >= rows || e >= N + s) return;
+        T *at = p + row * N + (e - s);
+        if (!SHIFT || (e >= s && N + s - e >= V)) {
+            store_once(at, u);
+            return;
+        }
+        T v[V];
+        memcpy(v, &u, 16);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j >= lo(e) && j < hi(e)) at[j] = v[j];
+    }
+    __device__ __forceinline__ void store8(uint8_t *p, int64_t row, int e, const float (&v)[V]) const {
+        if (row >= rows || e >= N + s) return;
+        uint8_t *at = p + row * N + (e - s);
+        if (!SHIFT || (e >= s && N + s - e >= V)) {
+            put8<V>(at, v);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j >= lo(e) && j < hi(e)) at[j] = uint8_t(e4m3x2(v[j], 0.f));
+    }
+    // fp32 sums of the row's columns, into a row of N of them
+    __device__ __forceinline__ void store_sums(float *p, int e, const float (&v)[V]) const {
+        if (e >= N + s) return;
+        if (!SHIFT) {
+#pragma unroll
+            for (int j = 0; j < V; j += 4)
+                *reinterpret_cast<float4 *>(p + e + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j >= lo(e) && j < hi(e)) p[e - s + j] = v[j];
+    }
+};
+
 // TPR threads a row, blockDim / TPR rows a block at a time, NV pieces of V
 // elements (16 bytes) a thread.  A block walks rows, gridDim steps apart, and
 // has the next row's loads in flight while it reduces and writes the current
-// one's, w in registers (not with 8 pieces: they would not fit).  FP8: 0 y in the type, 1 a scale a row, 2 a scale
-// for 128 columns.
-template <typename T, int NV, int FP8>
+// one's, w in registers (not with 8 pieces: they would not fit).  FP8: 0 y in the
+// type, 1 a scale a row, 2 a scale for 128 columns.  SHIFT: rows of any length
+// (Window).
+template <typename T, int NV, int FP8, bool SHIFT>
 __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 4 : NV == 2 ? 2 : 1)
     norm_fwd_kernel(const T *__restrict__ x, const T *__restrict__ res, const T *__restrict__ w, float eps,
                     T *__restrict__ ro, T *__restrict__ y, float *__restrict__ rstd_out, uint8_t *__restrict__ q8,
@@ -77,23 +162,18 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 4 : NV == 2 ? 2
     const int64_t step = int64_t(gridDim.x) * (blockDim.x / tpr);
     int64_t row = int64_t(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
     const float inv_n = 1.f / float(N);
+    const Window<T, SHIFT> win(row, rows, N);
     uint4 ux[NV], ur[NV], uw[NV];
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
     auto fetch = [&](int64_t at) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int e = (c + i * tpr) * V;
-            const bool in = at < rows && e < N;
-            ux[i] = in ? load_once(x + at * N + e) : zero;
-            if (res) ur[i] = in ? load_once(res + at * N + e) : zero;
+            ux[i] = win.load(x, at, (c + i * tpr) * V);
+            if (res) ur[i] = win.load(res, at, (c + i * tpr) * V);
         }
     };
     fetch(row);
     constexpr bool PREFETCH = NV < 8;
-    auto weight = [&](int i) {
-        const int e = (c + i * tpr) * V;
-        return e < N ? *reinterpret_cast<const uint4 *>(w + e) : zero;
-    };
+    auto weight = [&](int i) { return win.weight(w, (c + i * tpr) * V); };
     if (PREFETCH) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) uw[i] = weight(i);
@@ -103,7 +183,6 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 4 : NV == 2 ? 2
     int turn = 0;
     for (; row < last; row += step, turn ^= 1) {
         const bool live = row < rows;
-        const int64_t at = row * N;
         float r[NV][V], sum = 0.f, top = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -115,9 +194,10 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 4 : NV == 2 ? 2
 #pragma unroll
                 for (int j = 0; j < V; ++j) r[i][j] += a[j];
                 const uint4 u = pack(r[i]);
-                if (live && e < N) store_once(ro + at + e, u);
+                win.store(ro, row, e, u);
                 unpack(u, r[i]);
             }
+            win.mask(e, r[i]);
             float ww[V];
             if (FP8 == 1) unpack(PREFETCH ? uw[i] : weight(i), ww);
 #pragma unroll
@@ -139,13 +219,12 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 4 : NV == 2 ? 2
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int e = (c + i * tpr) * V;
-            const bool in = live && e < N;
             float ww[V];
             unpack(PREFETCH ? uw[i] : weight(i), ww);
 #pragma unroll
             for (int j = 0; j < V; ++j) r[i][j] = r[i][j] * rstd * ww[j];
             if (FP8 == 0) {
-                if (in) store_once(y + at + e, pack(r[i]));
+                win.store(y, row, e, pack(r[i]));
                 continue;
             }
             if (FP8 == 2) {
@@ -156,20 +235,19 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 4 : NV == 2 ? 2
 #pragma unroll
                 for (int s = 64 / V; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
                 const float sc = m * (1.f / kFp8Max);
-                if (in && e % 128 == 0) scales[row * (N / 128) + e / 128] = sc;
+                if (live && e < N && e % 128 == 0) scales[row * (N / 128) + e / 128] = sc;
                 inv = sc > 0.f ? 1.f / sc : 1.f;
             }
-            if (in) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) r[i][j] *= inv;
-                put8<V>(q8 + at + e, r[i]);
-            }
+            for (int j = 0; j < V; ++j) r[i][j] *= inv;
+            win.store8(q8, row, e, r[i]);
         }
         if (!PREFETCH) fetch(row + step);
     }
 }
 
-// Any N and alignment, one block a row, the row read again for each use.
+// Any N and alignment (tensors that do not start at a multiple of 16 bytes, rows too
+// long for the registers), one block a row, the row read again for each use.
 template <typename T, int FP8>
 __global__ void __launch_bounds__(256)
     norm_fwd_any_kernel(const T *__restrict__ x, const T *__restrict__ res, const T *__restrict__ w, float eps, T *ro,
@@ -234,7 +312,7 @@ __global__ void __launch_bounds__(256)
 // A row stays in registers as it was loaded and is unpacked twice.  dw's sums
 // over a thread's rows stay in registers and go to part[..][N] at the end: a
 // row of it for each row that the grid has in hand at a time.
-template <typename T, int NV>
+template <typename T, int NV, bool SHIFT>
 __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1)
     norm_bwd_kernel(const T *__restrict__ r, const T *__restrict__ w, const float *__restrict__ rstd,
                     const T *__restrict__ gy, const T *__restrict__ gr, T *__restrict__ dx, float *__restrict__ part,
@@ -245,7 +323,7 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1)
     const int c = threadIdx.x % tpr, rpb = blockDim.x / tpr;
     const int64_t step = int64_t(gridDim.x) * rpb, first = int64_t(blockIdx.x) * rpb + threadIdx.x / tpr;
     const float inv_n = 1.f / float(N);
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const Window<T, SHIFT> win(first, rows, N);
     float dw[NV][V], rs_next;
     uint4 uw[NV], ur[NV], ug[NV], ua[NV];
     auto fetch = [&](int64_t row) {
@@ -253,17 +331,13 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int e = (c + i * tpr) * V;
-            const bool in = row < rows && e < N;
-            ur[i] = in ? load_once(r + row * N + e) : zero;
-            ug[i] = in ? load_once(gy + row * N + e) : zero;
-            if (gr && PREFETCH) ua[i] = in ? load_once(gr + row * N + e) : zero;
+            ur[i] = win.load(r, row, e);
+            ug[i] = win.load(gy, row, e);
+            if (gr && PREFETCH) ua[i] = win.load(gr, row, e);
         }
     };
     fetch(first);
-    auto weight = [&](int i) {
-        const int e = (c + i * tpr) * V;
-        return e < N ? *reinterpret_cast<const uint4 *>(w + e) : zero;
-    };
+    auto weight = [&](int i) { return win.weight(w, (c + i * tpr) * V); };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         if (PREFETCH) uw[i] = weight(i);
@@ -274,7 +348,6 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1)
     const int64_t last = rows + rpb - 1;
     int turn = 0;  // two reduction buffers: one barrier a row
     for (int64_t row = first; row < last; row += step, turn ^= 1) {
-        const int64_t at = row * N;
         const float rs = rs_next;
         float dot = 0.f, unused = 0.f;
         uint4 cr[NV], cg[NV], ca[NV];
@@ -284,6 +357,7 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1)
             float hat[V], g[V], ww[V];
             unpack(cr[i], hat);
             unpack(cg[i], g);
+            win.mask((c + i * tpr) * V, hat), win.mask((c + i * tpr) * V, g);
             unpack(PREFETCH ? uw[i] : weight(i), ww);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -298,30 +372,23 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int e = (c + i * tpr) * V;
-            const bool in = row < rows && e < N;
             float hat[V], g[V], ww[V], a[V];
             unpack(cr[i], hat);
             unpack(cg[i], g);
             unpack(PREFETCH ? uw[i] : weight(i), ww);
-            if (gr) unpack(PREFETCH ? ca[i] : in ? load_once(gr + at + e) : zero, a);
+            if (gr) unpack(PREFETCH ? ca[i] : win.load(gr, row, e), a);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 g[j] = rs * (g[j] * ww[j] - hat[j] * rs * dot);
                 if (gr) g[j] += a[j];
             }
-            if (in) store_once(dx + at + e, pack(g));
+            win.store(dx, row, e, pack(g));
         }
         if (!PREFETCH) fetch(row + step);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int e = (c + i * tpr) * V;
-        if (e < N) {
-#pragma unroll
-            for (int j = 0; j < V; j += 4)
-                *reinterpret_cast<float4 *>(part + first * N + e + j) =
-                    make_float4(dw[i][j], dw[i][j + 1], dw[i][j + 2], dw[i][j + 3]);
-        }
+        win.store_sums(part + first * N, (c + i * tpr) * V, dw[i]);
     }
 }
 
@@ -386,6 +453,8 @@ bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 struct Shape {
     int tpr, nv;
 };
+template <int N>
+using Int = std::integral_constant<int, N>;
 Shape shape_of(int64_t pieces, int64_t most_of_two) {
     if (pieces <= 32) {
         int t = 8;
@@ -400,7 +469,9 @@ Shape shape_of(int64_t pieces, int64_t most_of_two) {
 // Rows of a block: a row's threads are within a warp, or the whole block.
 int block_rows(int tpr) { return tpr > 32 ? 1 : 128 / tpr; }
 
-// Blocks an SM, of kernels that leave room for `most` threads there
+// Blocks an SM, of kernels that leave room for `most` threads there.  Where a
+// thread has more than one row, the blocks are a multiple of 8 (as 152 is), and
+// with them the rows between two of a thread's: a multiple of a piece's elements.
 int64_t grid_of(int64_t rows, int rpb, int threads, int most) {
     return min64((rows + rpb - 1) / rpb, 152 * (threads >= most ? 1 : most / threads));
 }
@@ -409,8 +480,9 @@ template <typename T, int FP8>
 cudaError_t fwd_go(const T *x, const T *res, const T *w, float eps, T *r, T *y, float *rstd, uint8_t *q8,
                    float *scales, int64_t rows, int64_t N, cudaStream_t s) {
     constexpr int V = kVec<T>;
-    const Shape sh = shape_of((N + V - 1) / V, 1024);
-    const bool vec = N % V == 0 && al16(x) && al16(res) && al16(w) && al16(r) && al16(y) && al16(q8) && sh.tpr > 0;
+    const bool shift = N % V != 0;  // a row may then begin and end within a piece
+    const Shape sh = shape_of(shift ? (N + 2 * V - 2) / V : N / V, 1024);
+    const bool vec = al16(x) && al16(res) && al16(w) && al16(r) && al16(y) && al16(q8) && sh.tpr > 0;
     if (!vec) {
         const unsigned grid = unsigned(min64(rows, 152 * 8));
         norm_fwd_any_kernel<T, FP8><<<grid, 256, 0, s>>>(x, res, w, eps, r, y, rstd, q8, scales, rows, N);
@@ -418,14 +490,17 @@ cudaError_t fwd_go(const T *x, const T *res, const T *w, float eps, T *r, T *y, 
     }
     const int rpb = block_rows(sh.tpr);
     const int64_t grid = grid_of(rows, rpb, rpb * sh.tpr, sh.nv <= 2 ? 1024 : 512);
-#define MGS_GO(NV)                                                                                             \
-    norm_fwd_kernel<T, NV, FP8><<<unsigned(grid), unsigned(rpb * sh.tpr), 0, s>>>(x, res, w, eps, r, y, rstd, q8, \
-                                                                                 scales, rows, int(N), sh.tpr)
-    if (sh.nv == 1) MGS_GO(1);
-    else if (sh.nv == 2) MGS_GO(2);
-    else if (sh.nv == 4) MGS_GO(4);
-    else MGS_GO(8);
-#undef MGS_GO
+    auto go = [&](auto nv) {
+        auto *fn = norm_fwd_kernel<T, nv.value, FP8, false>;
+        if constexpr (FP8 != 2)  // whose rows are whole groups
+            if (shift) fn = norm_fwd_kernel<T, nv.value, FP8, true>;
+        fn<<<unsigned(grid), unsigned(rpb * sh.tpr), 0, s>>>(x, res, w, eps, r, y, rstd, q8, scales, rows, int(N),
+                                                             sh.tpr);
+    };
+    if (sh.nv == 1) go(Int<1>());
+    else if (sh.nv == 2) go(Int<2>());
+    else if (sh.nv == 4) go(Int<4>());
+    else go(Int<8>());
     return cudaGetLastError();
 }
 
@@ -438,8 +513,9 @@ template <typename T>
 cudaError_t bwd_go(const T *r, const T *w, const float *rstd, const T *gy, const T *gr, T *dx, T *dw, int64_t rows,
                    int64_t N, float *part, cudaStream_t s) {
     constexpr int V = kVec<T>;
-    const Shape sh = shape_of((N + V - 1) / V, 640);
-    const bool vec = N % V == 0 && al16(r) && al16(w) && al16(gy) && al16(gr) && al16(dx) && al16(part) &&
+    const bool shift = N % V != 0;
+    const Shape sh = shape_of(shift ? (N + 2 * V - 2) / V : N / V, 640);
+    const bool vec = al16(r) && al16(w) && al16(gy) && al16(gr) && al16(dx) && al16(part) &&
                      sh.tpr > 0 && sh.nv < 8;
     int parts;
     if (!vec) {
@@ -450,12 +526,13 @@ cudaError_t bwd_go(const T *r, const T *w, const float *rstd, const T *gy, const
         const int blocks =
             int(min64(kBwdBlocks, grid_of(rows, rpb, threads, sh.nv == 1 ? 768 : 512)));
         parts = blocks * rpb;
-        if (sh.nv == 1)
-            norm_bwd_kernel<T, 1><<<blocks, threads, 0, s>>>(r, w, rstd, gy, gr, dx, part, rows, int(N), sh.tpr);
-        else if (sh.nv == 2)
-            norm_bwd_kernel<T, 2><<<blocks, threads, 0, s>>>(r, w, rstd, gy, gr, dx, part, rows, int(N), sh.tpr);
-        else
-            norm_bwd_kernel<T, 4><<<blocks, threads, 0, s>>>(r, w, rstd, gy, gr, dx, part, rows, int(N), sh.tpr);
+        auto go = [&](auto nv) {
+            auto *fn = shift ? norm_bwd_kernel<T, nv.value, true> : norm_bwd_kernel<T, nv.value, false>;
+            fn<<<blocks, threads, 0, s>>>(r, w, rstd, gy, gr, dx, part, rows, int(N), sh.tpr);
+        };
+        if (sh.nv == 1) go(Int<1>());
+        else if (sh.nv == 2) go(Int<2>());
+        else go(Int<4>());
     }
     norm_dw_kernel<T><<<unsigned((N + 31) / 32), 1024, 0, s>>>(part, dw, parts, N);
     return cudaGetLastError();

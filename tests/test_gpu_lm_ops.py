@@ -339,6 +339,40 @@ def test_norm(rows, N, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,N", [(20011, 13), (10007, 77), (3001, 1001), (1301, 5003), (1217, 1), (700, 8190)])
+def test_norm_rows_that_start_anywhere(rows, N, dtype):
+    # rows of no whole number of 16-byte pieces, more than the grid has in hand at a time; what lies behind
+    # the tensors stays as it is
+    x, res, w, gy, gr = (t.cuda() for t in _norm_inputs(rows, N, dtype, seed=N))
+    one = FP32 if dtype == F32 else BF16_ONE
+    n, pad, dt = rows * N, 64, b.MGS_F32 if dtype == F32 else b.MGS_BF16
+    r, y, dx = (torch.full((n + pad,), 7.0, dtype=dtype, device="cuda") for _ in range(3))
+    q8 = torch.zeros(n + pad, dtype=torch.uint8, device="cuda")
+    rstd, scales = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    dw = torch.full((N + pad,), 7.0, dtype=dtype, device="cuda")
+    b.mgs_rms_norm_fwd(x, res, w, 1e-6, r, y, rstd, rows, N, dt)
+    size = b.mgs_rms_norm_bwd_workspace_size(rows, N)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    b.mgs_rms_norm_bwd(r, w, rstd, gy, gr, dx, dw, rows, N, dt, ws, size)
+    r2 = torch.full_like(r, 7.0)
+    b.mgs_rms_norm_fp8_fwd(x, res, w, 1e-6, r2, q8, scales, rows, N, 0, dt)
+    b.mgs_check()
+    ref = _lm.norm_ref(x.cpu(), w.cpu(), res.cpu(), 1e-6, dtype, gy.cpu(), gr.cpu())
+    for t in (r, y, dx, r2, dw):
+        assert (t[-pad:] == 7.0).all()
+    assert not q8[-pad:].any()
+    assert torch.equal(r[:n].view(rows, N).double().cpu(), ref["r"]) and torch.equal(r2, r)
+    check_rounded("y", y[:n].view(rows, N), ref["y"], one)
+    check("rstd", rstd, ref["rstd"], FP32)
+    check_rounded("dx", dx[:n].view(rows, N), ref["dx"], one)
+    check_rounded("dw", dw[:N], ref["dw"], one)
+    check("scales", scales, ref["y"].abs().amax(-1) / 448, 1e-6)
+    back = q8[:n].view(torch.float8_e4m3fn).view(rows, N).double().cpu() * scales.double().cpu()[:, None]
+    # a step of e4m3 is at most 2^-3 of the value, or 2^-9 of the scale below 2^-6 of it; half of it is the error
+    assert ((back - ref["y"]).abs() <= ref["y"].abs() * (2 ** -4 + 1e-5) + scales.double().cpu()[:, None] * 2 ** -10 * 1.01).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("rows,N,group", [(1, 128, 128), (5, 77, 0), (3, 1024, 128), (3, 1024, 0), (2, 1021, 0),
                                           (11, 4096, 128), (2, 8320, 128), (1, 40960, 128), (1, 40960, 0), (600, 256, 128)])
 def test_norm_fp8(rows, N, group, dtype):
