@@ -33,6 +33,16 @@
 //   17     one thread loads tiles by TMA
 //   18     sums of g
 //   19     loads x; looks for infinities and NaN in v
+//
+// C = 128 is the products' M; shorter chunks would leave half of the tensor cores
+// idle, longer ones need more TMEM than there is.  What bounds a block is the
+// chain of a chunk: P from A (two thirds of the rows' time), the weighted keys'
+// three terms (all of the state warps'), the products in their order between
+// them.  A chunk takes 3.9 us of an SM (heads of 128 in bf16; the products'
+// issue 1.6), 5.4 with three terms, 5.2 (two heads of 64), 7.5 and 10 (fp32,
+// heads of 64 and 128); a block's start and end about 6 us.  152 lanes of 1024
+// steps, bf16, heads of 128: 40 us, 3.3 TB/s of HBM, tensor pipe 31 % (44 % with
+// three terms; fp32 36 to 41 %).
 #include "mgs_launch.h"
 #include "mgs_lm.h"
 #include "mgs_num.cuh"
