@@ -431,7 +431,7 @@ def rms_norm_bwd(r, weight, rstd, grad_y, grad_r=None, stream=None):
 # ---------------------------------------------------------------- clipping by the global norm
 def clip_grad_norm(grads, max_norm, out=None, stream=None):
     """The norm over all of grads (fp32 and bf16 tensors, contiguous) as one fp32 on the device, and the tensors
-    scaled by min(1, max_norm / (norm + 1e-6)): in place, or into `out` (tensors of the same shapes and types)."""
+    scaled by min(1, max_norm / (norm + 1e-6)): in place, or into `out` (tensors of the same sizes and types)."""
     grads = list(grads)
     outs = grads if out is None else list(out)
     if len(outs) != len(grads):
@@ -441,22 +441,25 @@ def clip_grad_norm(grads, max_norm, out=None, stream=None):
     dev = grads[0].device
     if dev.type != "cuda":
         raise ValueError("each of grads must be a CUDA tensor (the library runs only on the GPU)")
-    index = grads[0].get_device()
-    codes = [_DTYPES.get(t.dtype) for t in grads]
+    # whole lists at a time: there may be hundreds of tensors, and the check of each should cost little
+    here, n = grads[0].get_device(), len(grads)
+    types, sizes = [t.dtype for t in grads], [t.numel() for t in grads]
+    codes = list(map(_DTYPES.get, types))
     contiguous = torch.Tensor.is_contiguous
-    if None in codes or any(t.get_device() != index for t in grads) or not all(map(contiguous, grads)):
+    if None in codes or [t.get_device() for t in grads].count(here) < n or not all(map(contiguous, grads)):
         for t in grads:
             _check_typed(t, "each of grads", None, None, device=dev)
-    if out is not None and ([u.shape for u in outs] != [t.shape for t in grads]
-                            or [_DTYPES.get(u.dtype) for u in outs] != codes
-                            or any(u.get_device() != index for u in outs) or not all(map(contiguous, outs))):
-        for t, u in zip(grads, outs):
-            _check_typed(u, "each of out", t.shape, t.dtype, device=dev)
-    norm = torch.empty((), dtype=torch.float32, device=dev)
-    n = _b.mgs_clip_grad_norm_workspace_size(len(grads))
     at = [t.data_ptr() for t in grads]
-    _b.mgs_clip_grad_norm(at, at if out is None else [u.data_ptr() for u in outs], [t.numel() for t in grads], codes,
-                          max_norm, norm, _scratch(n, dev, stream), n, stream)
+    to = at
+    if out is not None:
+        if ([u.dtype for u in outs] != types or [u.numel() for u in outs] != sizes
+                or [u.get_device() for u in outs].count(here) < n or not all(map(contiguous, outs))):
+            for t, u in zip(grads, outs):
+                _check_typed(u, "each of out", t.shape, t.dtype, device=dev)
+        to = [u.data_ptr() for u in outs]
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    size = _b.mgs_clip_grad_norm_workspace_size(n)
+    _b.mgs_clip_grad_norm(at, to, sizes, codes, max_norm, norm, _scratch(size, dev, stream), size, stream)
     return norm
 
 
