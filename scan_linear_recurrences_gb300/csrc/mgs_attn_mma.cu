@@ -357,6 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return true;
             };
             if (!(ok = from_state())) break;
+            if (lane == 0 && it > 0) {  // the chunk before has been stored: its stage is free
+                bulk_wait_read();
+                mb_arrive(TERMS == 1 ? &k_empty[(it - 1) % L::NK] : x_empty);
+            }
 #pragma unroll 1
             for (int hp = 0; hp < NH; ++hp) {
                 const float *G = Gh + hp * 4 * C;
@@ -442,13 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mb_arrive(p_ready);
             }
             if (!ok) break;
-            if (lane == 0) {
-                mb_arrive(g_empty);
-                if (it > 0) {  // the chunk before has been stored: its stage is free
-                    bulk_wait_read();
-                    mb_arrive(TERMS == 1 ? &k_empty[(it - 1) % L::NK] : x_empty);
-                }
-            }
+            if (lane == 0) mb_arrive(g_empty);
             // The output: row i, this thread's columns.  The warp's 32 rows are staged (swizzled
             // rows of 128 bytes) where nobody else reads any more, one term in the chunk's keys,
             // three in x's tile, and stored by TMA, which drops rows past the end.
@@ -849,19 +847,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int it = 0; it < n && ok; ++it) {
                 if (!state_only) {
-                    // Q S first: its place is wanted by the state's product, its result by nobody soon
-                    if (!(ok = wait(s_ready, it))) break;
-                    if (it > 0 && !(ok = M::over_a ? wait(kv_free, it - 1) : wait(o_free, it - 1))) break;
-#pragma unroll 1
-                    for (int kh = 0; kh < KH && ok; ++kh) {
+                    // Q K^T as soon as its place is free: where P V goes elsewhere, when P has been made
+                    // of the last one (P's products are ahead of it in the queue); else after Q S, whose
+                    // place is wanted by the state's product
+                    auto a_next = [&](int kh) {
                         const int tile_i = it * KH + kh;
-                        if (!(ok = wait(&q_full[tile_i % L::NQ], tile_i / L::NQ))) break;
-                        tc_fence_after();
-                        qs(it, kh);
-                        if (!(ok = wait(&k_full[tile_i % L::NK], tile_i / L::NK))) break;
-                        if (M::over_a && it > 0 && !(ok = wait(o_free, it - 1))) break;
+                        if (!wait(&k_full[tile_i % L::NK], tile_i / L::NK)) return false;
+                        if (M::over_a && it > 0 && !wait(o_free, it - 1)) return false;
                         tc_fence_after();
                         qk(it, 0, kh);
+                        return true;
+                    };
+#pragma unroll 1
+                    for (int kh = 0; kh < KH; ++kh) {
+                        const int tile_i = it * KH + kh;
+                        if (!(ok = wait(&q_full[tile_i % L::NQ], tile_i / L::NQ))) break;
+                        if (!M::over_a && !(ok = a_next(kh))) break;
+                        if (kh == 0 && !(ok = wait(s_ready, it))) break;
+                        if (kh == 0 && it > 0 && !(ok = wait(M::over_a ? kv_free : o_free, it - 1))) break;
+                        tc_fence_after();
+                        qs(it, kh);
+                        if (M::over_a && !(ok = a_next(kh))) break;
                         if (NH == 1) umma_commit(&q_empty[tile_i % L::NQ]);
                     }
                     if (!ok || !(ok = wait(o_ready, it))) break;  // Q S is in the rows' registers
