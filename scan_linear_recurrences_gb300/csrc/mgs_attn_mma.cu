@@ -77,6 +77,19 @@ struct Tmem {
     static constexpr uint32_t A = 0, P = TERMS == 1 ? 128 : 0, X = 192, O = over_a ? 0 : 192, W = 320;
 };
 
+// mbarriers (of a ring: one a slot) and what goes with them
+struct Bars {
+    uint64_t k_full[2], k_empty[2], q_full[2], q_empty[2], v_full[2], v_empty[2];  // tiles
+    uint64_t w_full[2], w_full2[2];                      // weighted keys, by halves of the chunk; of the second buffer
+    uint64_t a_done, qs_done, o_done, kv_done, drained;  // products
+    uint64_t p_ready, o_ready, o_free, s_ready, kv_free, st_sync;
+    uint64_t g_full, g_empty, x_full, x_empty;
+    uint64_t v_checked[4];
+    int v_flag[4];                                       // the chunk's v has an infinity or NaN
+    float total[2];                                      // the chunk's decay, of each head
+    uint32_t slot;                                       // TMEM's address
+};
+
 template <int D, int TERMS, int IN>
 struct Smem {
     static_assert(IN == 1 || TERMS == 3, "fp32: every operand in three terms");
@@ -91,7 +104,7 @@ struct Smem {
     static constexpr int x = v + NV * tile, arr = x + (TERMS == 1 ? 0 : 2 * kPanel);
     // per head: G (high and low parts), the column factors and the state weights of the 128 steps
     static constexpr int bars = arr + NH * 4 * C * 4;
-    static constexpr int walk = bars + 320;                         // the block's AttnWalk
+    static constexpr int walk = bars + (sizeof(Bars) + 15) / 16 * 16;  // the block's AttnWalk
     static constexpr size_t bytes = size_t(walk) + sizeof(AttnWalk);
     static_assert(k % 1024 == 0, "swizzled tiles");
     static_assert(bytes <= 232448, "shared memory of an SM");
@@ -252,16 +265,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int SC = L::VD / 2;               // state columns of a thread
     constexpr int OC = NH == 2 ? 64 : L::VD / 2;  // output columns of a thread
     extern __shared__ __align__(1024) unsigned char sm[];
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bars);
-    uint64_t *k_full = bars, *k_empty = bars + 2, *q_full = bars + 4, *q_empty = bars + 6, *v_full = bars + 8,
-             *v_empty = bars + 10, *w_full = bars + 12, *o_ready = bars + 14, *st_sync = bars + 15;
-    uint64_t *a_done = bars + 16, *p_ready = bars + 17, *qs_done = bars + 18, *o_done = bars + 19, *o_free = bars + 20,
-             *s_ready = bars + 21, *kv_done = bars + 22, *kv_free = bars + 23, *g_full = bars + 24, *g_empty = bars + 25,
-             *x_full = bars + 28, *x_empty = bars + 32, *drained = bars + 29, *w_full2 = bars + 30,
-             *v_checked = bars + 33;  // ..36
-    uint32_t *slot = reinterpret_cast<uint32_t *>(bars + 26);
-    volatile int *v_flag = reinterpret_cast<int *>(bars + 37);  // [4]: the chunk's v has an infinity or NaN
-    float *total = reinterpret_cast<float *>(slot + 2);  // [NH]: the chunk's decay
+    Bars &bars = *reinterpret_cast<Bars *>(sm + L::bars);
+    uint64_t *k_full = bars.k_full, *k_empty = bars.k_empty, *q_full = bars.q_full, *q_empty = bars.q_empty,
+             *v_full = bars.v_full, *v_empty = bars.v_empty, *w_full = bars.w_full, *w_full2 = bars.w_full2,
+             *v_checked = bars.v_checked, *o_ready = &bars.o_ready, *st_sync = &bars.st_sync, *a_done = &bars.a_done,
+             *p_ready = &bars.p_ready, *qs_done = &bars.qs_done, *o_done = &bars.o_done, *o_free = &bars.o_free,
+             *s_ready = &bars.s_ready, *kv_done = &bars.kv_done, *kv_free = &bars.kv_free, *g_full = &bars.g_full,
+             *g_empty = &bars.g_empty, *x_full = &bars.x_full, *x_empty = &bars.x_empty, *drained = &bars.drained;
+    uint32_t *slot = &bars.slot;
+    volatile int *v_flag = bars.v_flag;
+    float *total = bars.total;
 
     // the walk's description from shared memory: parameters indexed by blockIdx
     // would be read through the global path
