@@ -780,7 +780,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool add = false;  // onto what is there
             // Descriptors hold addresses in units of 16 bytes: what is issued is one of these
             // plus a short sum, since longer ones between two products cost more time than a
-            // product takes (64 cycles at N = 128); rolled loops, whose code stays at hand.
+            // product takes (64 cycles at N = 128).  Four steps' code in a row (fp32, B 16, T 1024: 90 us
+            // against 100 in rolled loops); the loops around them are rolled, whose code stays at hand.
             const uint64_t dK = umma_desc_k(smem_addr(sm + L::k)), dQ = umma_desc_k(smem_addr(sm + L::q));
             const uint64_t dV = umma_desc_mn(smem_addr(sm + L::v), kPanel), dS = umma_desc_mn(smem_addr(sm), kPanel);
             constexpr int KS = D / 16 / KH;
@@ -795,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int m = IN - 1; m >= 0; --m)
 #pragma unroll 1
                     for (int o = last(m); o >= 0; --o)
-#pragma unroll 1
+#pragma unroll 4
                         for (int ks = 0; ks < KS; ++ks, add = true)
                             umma_bf16_ss(tm + M::A, q + koff(ks) + uint64_t(m * (kPanel >> 4)),
                                          k + koff(ks) + uint64_t(o * (kPanel >> 4)), id_k, add);
@@ -813,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t st = dS + uint64_t((m * L::sterm + (hp + kh) * 8192) >> 4);
 #pragma unroll 1
                         for (int o = last(m); o >= 0; --o)
-#pragma unroll 1
+#pragma unroll 4
                             for (int ks = 0; ks < KS; ++ks, add = true)
                                 umma_bf16_ss(tm + M::X + 64 * (hp + kh), q + koff(ks) + uint64_t(o * (kPanel >> 4)),
                                              st + uint64_t(ks * 128), id_o, add);
@@ -829,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int m = 2; m >= 0; --m)
 #pragma unroll 1
                     for (int o = last(m); o >= 0; --o)
-#pragma unroll 1
+#pragma unroll 4
                         for (int i = 0; i < NG / 2; ++i, add = true)
                             umma_bf16_ts(tm + M::X + (IN == 3 ? 64 * half : 0), a + 64 * m + 8 * i, v + uint64_t(i * 128 + o * (kPanel >> 4)), id_mn,
                                          add);
@@ -848,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t step = TERMS == 1 || m == 2 ? 8 : 16;
 #pragma unroll 1
                         for (int o = last(m); o >= 0; --o)
-#pragma unroll 1
+#pragma unroll 4
                             for (int ks = k0; ks < k0 + KP; ++ks, add = true)
                                 umma_bf16_ts(tm + M::O + 64 * hp + (k0 > 0 ? 64 : 0), p + ks * step,
                                              v + uint64_t(ks * 128 + o * (kPanel >> 4)), id_o, add);
