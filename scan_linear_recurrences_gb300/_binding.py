@@ -54,6 +54,7 @@ class MGSError(RuntimeError):
 
 _lock = threading.Lock()
 _lib = None
+_torch_c = None
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -132,16 +133,19 @@ def _ptr(x):
 
 
 def _stream(s):
+    global _torch_c
     if s is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        if _torch_c is None:
+            import torch
+            _torch_c = torch._C
+        return _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
     if isinstance(s, int):
         return s
     return s.cuda_stream
 
 
 def _call(name, *args):
-    st = getattr(lib(), name)(*args)
+    st = getattr(_lib or lib(), name)(*args)
     if st != MGS_OK:
         raise MGSError(name, st)
     return st

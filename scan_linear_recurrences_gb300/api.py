@@ -380,6 +380,16 @@ def linear_attention_step(q, k, v, g, S, slots=None, scale=None, out=None, strea
 
 # ---------------------------------------------------------------- RMS norm with the residual's addition
 def _norm_args(x, weight, residual):
+    try:  # the usual case in few steps: a call on one token takes less time on the GPU than its checks
+        dt, shape, here = x.dtype, x.shape, x.get_device()
+        N = shape[-1]
+        if (dt in _DTYPES and here >= 0 and x.is_contiguous() and weight.dtype is dt and weight.shape == (N,)
+                and weight.is_contiguous() and weight.get_device() == here
+                and (residual is None or (residual.dtype is dt and residual.shape == shape
+                                          and residual.is_contiguous() and residual.get_device() == here))):
+            return x.numel() // N if N else 0, N, _DTYPES[dt]
+    except (AttributeError, IndexError):
+        pass
     _check_typed(x, "x", None, None)
     if x.dim() == 0:
         raise ValueError("x must have a last dimension")
