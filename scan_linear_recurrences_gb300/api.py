@@ -6,6 +6,8 @@ are the library's fwd/bwd entry points, for use inside models.
 """
 from __future__ import annotations
 
+import operator
+
 import torch
 
 from . import _binding as _b
@@ -452,21 +454,20 @@ def clip_grad_norm(grads, max_norm, out=None, stream=None):
     if dev.type != "cuda":
         raise ValueError("each of grads must be a CUDA tensor (the library runs only on the GPU)")
     # whole lists at a time: there may be hundreds of tensors, and the check of each should cost little
-    here, n = grads[0].get_device(), len(grads)
-    types, sizes = [t.dtype for t in grads], [t.numel() for t in grads]
+    T, dtype = torch.Tensor, operator.attrgetter("dtype")
+    here, n = [grads[0].get_device()] * len(grads), len(grads)
+    types, sizes = list(map(dtype, grads)), list(map(T.numel, grads))
     codes = list(map(_DTYPES.get, types))
-    contiguous = torch.Tensor.is_contiguous
-    if None in codes or [t.get_device() for t in grads].count(here) < n or not all(map(contiguous, grads)):
+    if None in codes or list(map(T.get_device, grads)) != here or not all(map(T.is_contiguous, grads)):
         for t in grads:
             _check_typed(t, "each of grads", None, None, device=dev)
-    at = [t.data_ptr() for t in grads]
-    to = at
+    to = at = list(map(T.data_ptr, grads))
     if out is not None:
-        if ([u.dtype for u in outs] != types or [u.numel() for u in outs] != sizes
-                or [u.get_device() for u in outs].count(here) < n or not all(map(contiguous, outs))):
+        if (list(map(dtype, outs)) != types or list(map(T.numel, outs)) != sizes
+                or list(map(T.get_device, outs)) != here or not all(map(T.is_contiguous, outs))):
             for t, u in zip(grads, outs):
                 _check_typed(u, "each of out", t.shape, t.dtype, device=dev)
-        to = [u.data_ptr() for u in outs]
+        to = list(map(T.data_ptr, outs))
     norm = torch.empty((), dtype=torch.float32, device=dev)
     size = _b.mgs_clip_grad_norm_workspace_size(n)
     _b.mgs_clip_grad_norm(at, to, sizes, codes, max_norm, norm, _scratch(size, dev, stream), size, stream)
