@@ -39,7 +39,7 @@
 // chain of a chunk: P from A (two thirds of the rows' time), the weighted keys'
 // three terms (all of the state warps'), the products in their order between
 // them.  A chunk takes 3.9 us of an SM (heads of 128 in bf16; the products'
-// issue 1.6), 5.4 with three terms, 5.2 (two heads of 64), 7.5 and 10 (fp32,
+// issue 1.6), 5.4 with three terms, 5.1 (two heads of 64), 6.2 and 9 (fp32,
 // heads of 64 and 128); a block's start and end about 6 us.  152 lanes of 1024
 // steps, bf16, heads of 128: 40 us, 3.3 TB/s of HBM, tensor pipe 31 % (44 % with
 // three terms; fp32 36 to 41 %).
@@ -822,18 +822,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (kh == KH - 1) umma_commit(qs_done);
             };
+            // The state's product, half of the steps as soon as their keys are there; in one sum (IN = 1)
+            // the largest terms come at the end, for both halves.
             auto kv = [&](int it, int half) {
-                const uint64_t v = dV + uint64_t(((it % L::NV) * L::tile + half * (NG / 2) * 2048) >> 4);
-                const uint32_t a = tm + (state_only && (it & 1) ? M::A : M::W) + half * (NG / 2) * 8;
+                const uint64_t v = dV + uint64_t(((it % L::NV) * L::tile) >> 4);
+                const uint32_t a = tm + (state_only && (it & 1) ? M::A : M::W);
+                auto part = [&](int m, int o, int h) {
+                    const uint32_t am = a + 64 * m + h * (NG / 2) * 8;
+                    const uint64_t vo = v + uint64_t(h * (NG / 2) * 128 + o * (kPanel >> 4));
+#pragma unroll 4
+                    for (int i = 0; i < NG / 2; ++i, add = true)
+                        umma_bf16_ts(tm + M::X + (IN == 3 ? 64 * h : 0), am + 8 * i, vo + uint64_t(i * 128), id_mn, add);
+                };
                 add = IN == 1 && half > 0;
 #pragma unroll 1
-                for (int m = 2; m >= 0; --m)
+                for (int m = 2; m >= (IN == 1 ? 1 : 0); --m)
 #pragma unroll 1
-                    for (int o = last(m); o >= 0; --o)
-#pragma unroll 4
-                        for (int i = 0; i < NG / 2; ++i, add = true)
-                            umma_bf16_ts(tm + M::X + (IN == 3 ? 64 * half : 0), a + 64 * m + 8 * i, v + uint64_t(i * 128 + o * (kPanel >> 4)), id_mn,
-                                         add);
+                    for (int o = last(m); o >= 0; --o) part(m, o, half);
+                if (IN == 1 && half == 1)
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) part(0, 0, h);
             };
             auto pv = [&](int it, int hp) {
                 const uint64_t v = dV + uint64_t(((it % L::NV) * L::tile + hp * kPanel) >> 4);
