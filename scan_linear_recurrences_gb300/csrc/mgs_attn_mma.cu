@@ -59,9 +59,18 @@ constexpr int C = 128;
 constexpr int kPanel = 16384;                  // a panel of a tile: 128 rows x 64 bf16
 constexpr int kThreads = 20 * 32;              // five warpgroups
 // Registers a thread: the kernel is launched with kRegs for each; the last
-// warpgroup gives up what the two of the rows take more.
-constexpr int kRegs = 96, kRegsRows = 112, kRegsLast = 64;
-static_assert(2 * kRegsRows + 2 * kRegs + kRegsLast <= 5 * kRegs, "within the registers of the launch");
+// warpgroup gives up what the others take more.  With heads of 128 and three
+// terms the state's warps take some too (dq and dk of 128 lanes of 4096 steps 5
+// us less); with one term that costs the state-only walk more than it gives
+// (1 x 16384 steps, 16 heads: 144 us against 114), with heads of 64 the last
+// warpgroup's sums of g of two heads need the registers (673 us against 725).
+constexpr int kRegs = 96, kRegsRows = 112;
+template <int D, int TERMS, int IN>
+struct Regs {
+    static constexpr bool more = D == 128 && TERMS == 3 && IN == 1;
+    static constexpr int state = more ? 104 : 96, last = more ? 48 : 64;
+    static_assert(2 * kRegsRows + 2 * state + last <= 5 * kRegs, "within the registers of the launch");
+};
 constexpr int GT = 16;                         // steps of a group of weighted keys: one K = 16 product
 constexpr int NG = C / GT;
 
@@ -545,6 +554,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) bulk_wait_read();
         __syncwarp();
     } else if (warp < 16) {
+        if (Regs<D, TERMS, IN>::more)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Regs<D, TERMS, IN>::state));
         // ------------------------------------------------ rows of the state
         const int grp = (warp - 8) >> 2, dk = 32 * (warp & 3) + lane;
         const int hp = NH == 2 ? dk >> 6 : 0, h = h0 + hp;
@@ -762,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok && lane == 0) record_error(ctl, ERR_MBAR_TIMEOUT);
     } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLast));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Regs<D, TERMS, IN>::last));
     if (!ok0) {
         // nothing was started
     } else if (warp == 16) {
