@@ -371,7 +371,11 @@ size_t mgs_linear_attention_workspace_size(const mgs_attention_shape *shape, int
  * state S a D x D matrix with the key index first,
  *     S_t = e^{g_t} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,
  * S_0 = S0 (zeros when NULL).  g is the logarithm of the decay: g <= 0 in use,
- * and -infinity starts the state anew at that step.
+ * and -infinity starts the state anew at that step.  An infinity or NaN reaches
+ * what the formula takes it to: in v the outputs of its own column from its step
+ * on, not those before.  (Chunks of 128 steps with one in v run many times
+ * slower.)  A stride of 0 in bf16, and in the fp32 backward, selects a slower
+ * kernel.
  * In: q, k [B][T][Hk][D], v [B][T][H][D], g [B][T][H] or [H] (fp32),
  *     S0 [B][H][D][D] fp32 (nullable).
  * Out: o [B][T][H][D]; S_T [B][H][D][D] fp32 (nullable). */
@@ -407,8 +411,8 @@ mgs_status mgs_linear_attention_step(const mgs_attention_shape *shape, const voi
  *     y = r rstd weight.
  * residual and r are both given or both NULL (then r is x).  Out: r, y
  * [rows][N], rstd [rows] fp32 (nullable: only the backward needs it).  Tensors
- * are dense; 16-byte aligned tensors with N a multiple of 16 bytes run the
- * vector kernel, others a slower one. */
+ * are dense; tensors that start at multiples of 16 bytes run the vector kernels
+ * (N a multiple of 16 bytes is the fastest), others a slower one. */
 mgs_status mgs_rms_norm_fwd(const void *x, const void *residual, const void *weight, float eps, void *r, void *y,
                             float *rstd, int64_t rows, int64_t N, int dtype, mgs_stream_t stream);
 
