@@ -240,12 +240,17 @@ __device__ __forceinline__ void row_alone(const AttnWalk &w, const AttnSet &set,
             for (int i = 0; i < 4; ++i) dot = fmaf(x[i], y[i], dot);
         }
         const float p = dot * (w.o_scale * w.kv_scale * expf(sum));
+        bool number = false;
 #pragma unroll 1
         for (int c = 0; c < OC; c += 4) {
             get(v + j * w.vs[1] + c, vterm, x);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[c + i] = fmaf(p, x[i], o[c + i]);
+            for (int i = 0; i < 4; ++i) {
+                o[c + i] = fmaf(p, x[i], o[c + i]);
+                number = number || o[c + i] == o[c + i];
+            }
         }
+        if (!number) return;  // NaN throughout, and whatever comes leaves it so
         if (!w.rev) sum += g[j * set.gs[1]];
     }
 }
