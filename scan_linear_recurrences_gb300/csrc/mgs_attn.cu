@@ -261,6 +261,7 @@ __global__ void __launch_bounds__(256)
                    int64_t H, int spans, int DD) {
     __shared__ float red[8], scan[8];
     const int NT = blockDim.x;  // a thread has four of the span's steps
+    griddep_wait();
     const int64_t lane = blockIdx.x / spans;
     const int span = int(blockIdx.x % spans), tid = threadIdx.x;
     const int64_t b = lane / H, h = lane % H;
@@ -684,10 +685,10 @@ cudaError_t launch_attn_bwd(const mgs_attention_shape &sh, const void *q, const 
     a.out = group > 1 ? static_cast<void *>(dqf) : dq, a.out_f32 = group > 1;
     r.out = group > 1 ? static_cast<void *>(dkf) : dk, r.out_f32 = group > 1;
     if ((e = run_walks(set, 3, sh, p, carve, s)) != cudaSuccess) return e;
-    attn_dg_kernel<<<unsigned(p.lanes * p.spans), unsigned(p.span / 4), 0, s>>>(u, wd, p.parts, ends ? ckS : nullptr, ckR,
-                                                              sh.fixed_decay ? nullptr : dg,
-                                                              sh.fixed_decay ? part : nullptr, sh.T, sh.H, p.spans,
-                                                              sh.D * sh.D);
+    if ((e = launch_next(attn_dg_kernel, unsigned(p.lanes * p.spans), unsigned(p.span / 4), 0, s, p.mma, u, wd, p.parts,
+                         ends ? ckS : nullptr, ckR, sh.fixed_decay ? nullptr : dg, sh.fixed_decay ? part : nullptr, sh.T,
+                         sh.H, p.spans, sh.D * sh.D)) != cudaSuccess)
+        return e;
     if (sh.fixed_decay) attn_dg_fixed_kernel<<<unsigned(sh.H), 256, 0, s>>>(part, dg, sh.B, sh.H, p.spans);
     if (group > 1) {
         const int64_t n4 = int64_t(rows) / group * sh.D / 4;

@@ -324,6 +324,7 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1)
     constexpr bool PREFETCH = NV * V <= 16;
     __shared__ float red[2][2][32];
     const int c = threadIdx.x % tpr, rpb = blockDim.x / tpr;
+    griddep_launch();
     const int64_t step = int64_t(gridDim.x) * rpb, first = int64_t(blockIdx.x) * rpb + threadIdx.x / tpr;
     const float inv_n = 1.f / float(N);
     const Window<T, SHIFT> win(first, rows, N);
@@ -431,6 +432,7 @@ __global__ void __launch_bounds__(1024)
     __shared__ float red[32][33];
     const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
     const int64_t n = int64_t(blockIdx.x) * 32 + c;
+    griddep_wait();
     float s = 0.f;
     if (n < N) {
 #pragma unroll 8
@@ -537,8 +539,9 @@ cudaError_t bwd_go(const T *r, const T *w, const float *rstd, const T *gy, const
         else if (sh.nv == 2) go(Int<2>());
         else go(Int<4>());
     }
-    norm_dw_kernel<T><<<unsigned((N + 31) / 32), 1024, 0, s>>>(part, dw, parts, N);
-    return cudaGetLastError();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_next(norm_dw_kernel<T>, unsigned((N + 31) / 32), 1024, 0, s, true, part, dw, parts, N);
 }
 
 }  // namespace
