@@ -7,9 +7,9 @@
 //   dx = rstd (w dy - hat mean(w dy hat)) + dr,   dw = sum over rows of dy hat
 // (dx is the gradient of x and of res alike).  All sums in fp32.  Bound by
 // memory: each tensor is read or written once, a row stays in registers
-// between the sum and its use.  32768 rows of 2048 in bf16: forward 82 us (537
-// MB, 6.5 TB/s), backward 90 us (537 MB, 6.0 TB/s) and 6 for dw's last sums; 8191
-// rows of 5120 to fp8 53 us (294 MB, 5.5 TB/s); one row of 4096 2.6 us.
+// between the sum and its use.  32768 rows of 2048 in bf16: forward 87 us a call
+// (537 MB, 6.2 TB/s), backward 91 (5.9 TB/s) with dw's last sums; 8191 rows of
+// 5120 to fp8 48 us (294 MB, 6.2 TB/s); one row of 4096 2.6 us on the device.
 #include <cstring>
 #include <type_traits>
 
@@ -72,7 +72,7 @@ __device__ __forceinline__ void put8(uint8_t *p, const float (&v)[V]) {
 // the row, and what of them is the neighbouring rows' is masked.  s is the same
 // for all of a thread's rows: they are a multiple of V rows apart.
 // (32768 rows of 1001 in bf16, element by element: forward 118 us, backward 208;
-// so: 55 and 73.)
+// so: 51 and 61.)
 template <typename T, bool SHIFT>
 struct Window {
     static constexpr int V = kVec<T>;
@@ -451,22 +451,46 @@ __global__ void __launch_bounds__(1024)
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Threads a row and pieces a thread.  Up to 32 pieces: a power of two of threads,
-// several rows a warp.  Longer: whole warps, two pieces a thread beyond 256, so
-// that there are more loads in flight for the same warps and no more threads
-// than pieces (N = 5120 in bf16, 640 pieces: 320 threads of 2; 256 of 4, of
-// which a third had none, took 96 us for 8191 rows of the fp8 form against 59).
+// several rows a warp.  Longer: whole warps.
 struct Shape {
     int tpr, nv;
 };
+int64_t warps_of(int64_t pieces, int nv) { return (pieces + 32 * nv - 1) / (32 * nv); }
+Shape shape_of(int64_t pieces, int nv) {
+    if (pieces > 32) return {warps_of(pieces, nv) <= 16 ? int(32 * warps_of(pieces, nv)) : 0, nv};
+    int t = 8;
+    while (t < pieces) t *= 2;
+    return {t, 1};
+}
+// Forward: four pieces a thread past 64, so that fewer warps wait for one another
+// at a row's sum and a warp has more loads in flight (8191 rows of 5120 in bf16 to
+// fp8: 160 threads of 4 48 us, 320 of 2 60; 30000 of 1024, a warp a row, 35,
+// against 42 with 128 threads; 60000 of 512 44, a warp of 2 45); two where a
+// quarter or more of four would lie idle (30000 of 768 in fp32 48 us, else 50).
+Shape fwd_shape(int64_t pieces) {
+    const int64_t w4 = warps_of(pieces, 4), w2 = warps_of(pieces, 2);
+    return shape_of(pieces, pieces <= 64 ? 1 : pieces > 2048 ? 8 : 96 * w4 >= pieces && 2 * w4 > w2 ? 2 : 4);
+}
+// Backward: as many pieces as there are registers for with the next row's loads in
+// flight (32768 rows of 2048 in bf16: 128 threads of 2 91 us, 256 of 1 98)
+Shape bwd_shape(int64_t pieces) {
+    return shape_of(pieces, pieces <= 192 ? 1 : pieces <= 640 ? 2 : pieces <= 2048 ? 4 : 8);
+}
 template <int N>
 using Int = std::integral_constant<int, N>;
-Shape shape_of(int64_t pieces, int64_t most_of_two) {
+Shape shape_of(int64_t pieces, int64_t most_of_one, int64_t most_of_two) {
     if (pieces <= 32) {
         int t = 8;
         while (t < pieces) t *= 2;
         return {t, 1};
     }
-    const int nv = pieces <= 256 ? 1 : pieces <= most_of_two ? 2 : pieces <= 2048 ? 4 : 8;
+    int nv = pieces <= most_of_one ? 1 : pieces <= most_of_two ? 2 : pieces <= 2048 ? 4 : 8;
+    if (most_of_one == 0) {
+        auto slots = [&](int n) { return (pieces + 32 * n - 1) / (32 * n) * 32 * n; };
+        nv = pieces > 2048 ? 8 : slots(2) < slots(4) ? 2 : 4;
+        if (most_of_two == 1 && pieces > 32 && pieces <= 64) nv = 1;
+        if (most_of_two == 2 && pieces > 32 && pieces <= 128) nv = 1;
+    }
     const int64_t tpr = ((pieces + nv - 1) / nv + 31) / 32 * 32;
     if (tpr > 512) return {0, 0};
     return {int(tpr), nv};
@@ -486,7 +510,7 @@ cudaError_t fwd_go(const T *x, const T *res, const T *w, float eps, T *r, T *y, 
                    float *scales, int64_t rows, int64_t N, cudaStream_t s) {
     constexpr int V = kVec<T>;
     const bool shift = N % V != 0;  // a row may then begin and end within a piece
-    const Shape sh = shape_of(shift ? (N + 2 * V - 2) / V : N / V, 1024);
+    const Shape sh = fwd_shape(shift ? (N + 2 * V - 2) / V : N / V);
     const bool vec = al16(x) && al16(res) && al16(w) && al16(r) && al16(y) && al16(q8) && sh.tpr > 0;
     if (!vec) {
         const unsigned grid = unsigned(min64(rows, 152 * 8));
@@ -511,25 +535,30 @@ cudaError_t fwd_go(const T *x, const T *res, const T *w, float eps, T *r, T *y, 
 
 // The backward's grid: blocks, of how many rows.  Each row in hand has a row of
 // the workspace for its sums of dw.
-constexpr int kBwdBlocks = 152 * 4;
-int64_t bwd_parts(int64_t rows, int64_t N) { return min64(rows + 15, kBwdBlocks * (N <= 256 ? 16 : 1)); }
+// Short rows' blocks are small, and so are their sums: more of them (60000 rows of
+// 512 in bf16: 49 us with 12 blocks an SM, 82 with 4).
+int64_t bwd_blocks(int64_t N) {
+    const int64_t n = N > 0 ? 6144 / N : 12;
+    return 152 * (n < 4 ? 4 : n > 12 ? 12 : n);
+}
+int64_t bwd_parts(int64_t rows, int64_t N) { return min64(rows + 15, bwd_blocks(N) * (N <= 256 ? 16 : 1)); }
 
 template <typename T>
 cudaError_t bwd_go(const T *r, const T *w, const float *rstd, const T *gy, const T *gr, T *dx, T *dw, int64_t rows,
                    int64_t N, float *part, cudaStream_t s) {
     constexpr int V = kVec<T>;
     const bool shift = N % V != 0;
-    const Shape sh = shape_of(shift ? (N + 2 * V - 2) / V : N / V, 640);
+    const Shape sh = bwd_shape(shift ? (N + 2 * V - 2) / V : N / V);
     const bool vec = al16(r) && al16(w) && al16(gy) && al16(gr) && al16(dx) && al16(part) &&
                      sh.tpr > 0 && sh.nv < 8;
     int parts;
     if (!vec) {
-        parts = int(min64(rows, kBwdBlocks));
+        parts = int(min64(rows, bwd_blocks(N)));
         norm_bwd_any_kernel<T><<<parts, 256, 0, s>>>(r, w, rstd, gy, gr, dx, part, rows, N);
     } else {
         const int rpb = block_rows(sh.tpr), threads = rpb * sh.tpr;
         const int blocks =
-            int(min64(kBwdBlocks, grid_of(rows, rpb, threads, sh.nv == 1 ? 768 : 512)));
+            int(min64(bwd_blocks(N), grid_of(rows, rpb, threads, sh.nv == 1 ? 768 : 512)));
         parts = blocks * rpb;
         auto go = [&](auto nv) {
             auto *fn = shift ? norm_bwd_kernel<T, nv.value, true> : norm_bwd_kernel<T, nv.value, false>;
