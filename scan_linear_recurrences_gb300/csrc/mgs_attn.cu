@@ -258,15 +258,15 @@ __device__ __forceinline__ float block_sum(float x, float *red) {
 __global__ void __launch_bounds__(256)
     attn_dg_kernel(const float *__restrict__ u, const float *__restrict__ w, int parts, const float *__restrict__ ckS,
                    const float *__restrict__ ckR, float *__restrict__ dg, float *__restrict__ part, int64_t T,
-                   int64_t H, int spans, int DD) {
+                   int64_t H, int spans, int per, int DD) {
     __shared__ float red[8], scan[8];
-    const int NT = blockDim.x;  // a thread has four of the span's steps
+    constexpr int NT = 256;  // threads, each with `per` of the span's steps, at most 4
     griddep_wait();
     const int64_t lane = blockIdx.x / spans;
     const int span = int(blockIdx.x % spans), tid = threadIdx.x;
     const int64_t b = lane / H, h = lane % H;
-    const int64_t t0 = int64_t(span) * 4 * NT;
-    const int n = int(min64(4 * NT, T - t0));
+    const int64_t t0 = int64_t(span) * per * NT;
+    const int n = int(min64(per * NT, T - t0));
     float tail = 0.f;
     if (ckS) {
         const float *a = ckS + (lane * spans + span) * DD, *c = ckR + (lane * spans + span) * DD;
@@ -282,16 +282,16 @@ __global__ void __launch_bounds__(256)
         tail = block_sum(acc, red);
     }
     const int64_t all = int64_t(gridDim.x) / spans * T;  // of one part
-    // suffix sums: thread i holds steps 4 i .. 4 i + 3
+    // suffix sums: thread i holds steps per i .. per i + per - 1
     float d[4] = {0.f, 0.f, 0.f, 0.f};
     for (int p = 0; p < parts; ++p) {
         float x[4], y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int t = 4 * tid + i;
+            const int t = per * tid + i;
             const int64_t at = lane * T + t0 + t + p * all;
-            x[i] = t < n ? u[at] : 0.f;
-            y[i] = t < n ? w[at] : 0.f;
+            x[i] = i < per && t < n ? u[at] : 0.f;
+            y[i] = i < per && t < n ? w[at] : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[i] += x[i] - y[i];
@@ -312,8 +312,8 @@ __global__ void __launch_bounds__(256)
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int t = 4 * tid + i;
-        if (t >= n) continue;
+        const int t = per * tid + i;
+        if (i >= per || t >= n) continue;
         const float x = d[i] + after;
         sum += x;
         if (dg) dg[(b * T + t0 + t) * H + h] = x;
@@ -685,9 +685,9 @@ cudaError_t launch_attn_bwd(const mgs_attention_shape &sh, const void *q, const 
     a.out = group > 1 ? static_cast<void *>(dqf) : dq, a.out_f32 = group > 1;
     r.out = group > 1 ? static_cast<void *>(dkf) : dk, r.out_f32 = group > 1;
     if ((e = run_walks(set, 3, sh, p, carve, s)) != cudaSuccess) return e;
-    if ((e = launch_next(attn_dg_kernel, unsigned(p.lanes * p.spans), unsigned(p.span / 4), 0, s, p.mma, u, wd, p.parts,
+    if ((e = launch_next(attn_dg_kernel, unsigned(p.lanes * p.spans), 256, 0, s, p.mma, u, wd, p.parts,
                          ends ? ckS : nullptr, ckR, sh.fixed_decay ? nullptr : dg, sh.fixed_decay ? part : nullptr, sh.T,
-                         sh.H, p.spans, sh.D * sh.D)) != cudaSuccess)
+                         sh.H, p.spans, p.span / 256, sh.D * sh.D)) != cudaSuccess)
         return e;
     if (sh.fixed_decay) attn_dg_fixed_kernel<<<unsigned(sh.H), 256, 0, s>>>(part, dg, sh.B, sh.H, p.spans);
     if (group > 1) {
