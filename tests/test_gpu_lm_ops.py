@@ -513,3 +513,36 @@ def test_lm_ops_on_a_side_stream_and_repeated():
     b.mgs_check()
     for p, q, s in zip(ref, inside, outside):
         assert torch.equal(p, q) and torch.equal(p, s)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_lm_ops_captured_in_a_graph(dtype):
+    # launches that are set up early keep their order in a graph; replayed on other inputs it gives their outputs
+    d = _lm.cuda(_lm.attn_inputs(1, 2300, 3, 1, 64, dtype, True, seed=41, decay=0.05))
+    x, res, w, gy, _ = (t.cuda() for t in _norm_inputs(300, 512, dtype, seed=5))
+    grads = _grads([70000, 300, 9])
+    names = ("q", "k", "v", "g", "grad_o", "S0", "grad_ST")
+
+    def run():
+        o, ST = api.linear_attention_fwd(d["q"], d["k"], d["v"], d["g"], d["S0"], want_state=True)
+        r = api.linear_attention_bwd(d["q"], d["k"], d["v"], d["g"], d["grad_o"], d["S0"], d["grad_ST"])
+        y, rr, rstd = api.rms_norm_fwd(x, w, res)
+        n = api.rms_norm_bwd(rr, w, rstd, gy)
+        out = [torch.empty_like(t) for t in grads]
+        return [o, ST, *r, y, *n, api.clip_grad_norm(grads, 0.5, out=out), *out]
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    other = _lm.cuda(_lm.attn_inputs(1, 2300, 3, 1, 64, dtype, True, seed=42, decay=0.05))
+    for n in names:
+        d[n].copy_(other[n])
+    x.mul_(2)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, e in zip(got, run()):
+        assert torch.equal(a, e)
+    b.mgs_check()
