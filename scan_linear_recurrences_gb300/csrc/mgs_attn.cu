@@ -27,7 +27,7 @@ constexpr int TS = 16;  // time steps staged in shared memory at once
 // rows of one column, P = D / 32 neighbouring threads share a column.  Per
 // step and thread 32 x 4 fp32 operations: bound by the fp32 pipes (64 lanes of
 // 1024 steps, heads of 128 in fp32: 684 us, where the tensor-core walk takes
-// 122).  For tensors that no tensor map describes.
+// 113).  For tensors that no tensor map describes.
 template <typename TI, int D, bool STATE_ONLY>
 __global__ void __launch_bounds__(D *D / 32) attn_rec_kernel(const __grid_constant__ AttnSet set) {
     constexpr int P = D / 32, NT = D * D / 32, V4 = TS * D / 4, NL = V4 / NT;
