@@ -3,9 +3,14 @@ with torch (device memory is torch's job here), then one libmgscan call.
 
 Also provides ``torch.autograd.Function`` wrappers whose forward and backward
 are the library's fwd/bwd entry points, for use inside models.
+
+``stream``: the kernels' stream (a torch stream or its address; None: the current
+one).  The caller orders it after the work that makes the inputs, and after what
+torch's current stream has been given: outputs are allocated there.
 """
 from __future__ import annotations
 
+import contextlib
 import operator
 
 import torch
@@ -266,16 +271,27 @@ def _head_strides(t, name):
     return st[:-1]
 
 
-def _apart(t):
+def _on(stream, device):
+    """The context in which memory and copies belong to the call's stream (an address, a torch stream, or None: the
+    current one).  What is allocated in it may be dropped when the call returns: it goes back to that stream."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):  # address 0: the default stream, for which torch has no external one
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def _apart(t, stream):
     """t, or a dense copy of a broadcast t: the tensor-core kernels load through tensor maps, which have no
     zero strides, and the copy costs less than the kernel without them."""
     st = t.stride()
-    if 0 not in st or t.dtype != torch.bfloat16:
+    if 0 not in st or t.dtype != torch.bfloat16 or all(s or n <= 1 for s, n in zip(st, t.shape)):
         return t
-    return t.contiguous() if any(s == 0 and n > 1 for s, n in zip(st, t.shape)) else t
+    with _on(stream, t.device):
+        return t.contiguous()
 
 
-def _attention_shape(q, k, v, g, scale, grad_o=None):
+def _attention_shape(q, k, v, g, scale, stream, grad_o=None):
     """The checked arguments as the C struct, (B, T, H, Hk, D), and the tensors to pass."""
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a [B,T,Hk,D] tensor")
@@ -293,8 +309,8 @@ def _attention_shape(q, k, v, g, scale, grad_o=None):
     _check_typed(g, "g", (H,) if fixed else (B, T, H), torch.float32, dense=fixed, device=dev)
     if grad_o is not None:
         _check_typed(grad_o, "grad_o", v.shape, q.dtype, dense=False, device=dev)
-        grad_o = _apart(grad_o)
-    q, k, v = _apart(q), _apart(k), _apart(v)
+        grad_o = _apart(grad_o, stream)
+    q, k, v = _apart(q, stream), _apart(k, stream), _apart(v, stream)
     shape = _b.mgs_attention_shape(
         B, T, H, Hk, D, _DTYPES[q.dtype], fixed, D ** -0.5 if scale is None else scale, _head_strides(q, "q"),
         _head_strides(k, "k"), _head_strides(v, "v"), (0, 0, 1) if fixed else g.stride(),
@@ -306,10 +322,8 @@ def _scratch(n, device, stream):
     """n bytes of workspace that stay reserved until `stream` is done with them."""
     if not n:
         return None
-    t = torch.empty(n, dtype=torch.uint8, device=device)
-    if stream is not None:
-        t.record_stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
-    return t
+    with _on(stream, device):
+        return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def linear_attention_fwd(q, k, v, g, S0=None, scale=None, want_state=False, stream=None):
@@ -320,7 +334,7 @@ def linear_attention_fwd(q, k, v, g, S0=None, scale=None, want_state=False, stre
     head h // (H // Hk); any strides of 16 bytes whose heads are contiguous), g [B,T,H] or [H] fp32 (the
     decay's logarithm; -inf starts the state anew), S0 [B,H,D,D] fp32 or None.
     Returns o [B,T,H,D] (and the final state when want_state)."""
-    shape, (B, T, H, Hk, D), (q, k, v, _) = _attention_shape(q, k, v, g, scale)
+    shape, (B, T, H, Hk, D), (q, k, v, _) = _attention_shape(q, k, v, g, scale, stream)
     if S0 is not None:
         _check_typed(S0, "S0", (B, H, D, D), torch.float32, device=q.device)
     o = torch.empty((B, T, H, D), dtype=q.dtype, device=q.device)
@@ -333,7 +347,7 @@ def linear_attention_fwd(q, k, v, g, S0=None, scale=None, want_state=False, stre
 def linear_attention_bwd(q, k, v, g, grad_o, S0=None, grad_ST=None, scale=None, stream=None):
     """Gradients of linear_attention_fwd for L = <grad_o, o> + <grad_ST, S_T>: returns (dq, dk, dv, dg, dS0),
     dS0 None without S0.  dg is [B,T,H], or [H] for a g of one decay a head."""
-    shape, (B, T, H, Hk, D), (q, k, v, grad_o) = _attention_shape(q, k, v, g, scale, grad_o)
+    shape, (B, T, H, Hk, D), (q, k, v, grad_o) = _attention_shape(q, k, v, g, scale, stream, grad_o)
     for t, name in ((S0, "S0"), (grad_ST, "grad_ST")):
         if t is not None:
             _check_typed(t, name, (B, H, D, D), torch.float32, device=q.device)

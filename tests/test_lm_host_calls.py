@@ -1,0 +1,65 @@
+"""What the tensor-level functions of the language-model operators do around a
+call of the library, without a GPU: the library's entry points are replaced."""
+import contextlib
+
+import pytest
+import torch
+
+from scan_linear_recurrences_gb300 import _binding as b
+from scan_linear_recurrences_gb300 import api
+
+from . import _lm
+
+BF16 = torch.bfloat16
+
+
+class _Calls:
+    """The entry points' calls, and the streams that were torch's current ones when memory was taken or copied."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.copies, self.scratch, self.calls = ["current"], [], [], []
+
+        @contextlib.contextmanager
+        def on(stream):
+            self.current.append(stream)
+            yield
+            self.current.pop()
+
+        dense, empty = torch.Tensor.contiguous, torch.empty
+
+        def contiguous(t):
+            if not t.is_contiguous():
+                self.copies.append(self.current[-1])
+            return dense(t)
+
+        def new(*a, **k):
+            if k.get("dtype") is torch.uint8:
+                self.scratch.append(self.current[-1])
+            return empty(*a, **k)
+
+        monkeypatch.setattr(torch.cuda, "stream", on)
+        monkeypatch.setattr(torch.cuda, "ExternalStream", lambda at, device=None: ("external", at))
+        monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
+        monkeypatch.setattr(torch.Tensor, "contiguous", contiguous)
+        monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
+        monkeypatch.setattr(torch, "empty", new)
+        monkeypatch.setattr(api, "_check_typed", lambda *a, **k: None)
+        monkeypatch.setattr(b, "mgs_linear_attention_workspace_size", lambda shape, backward: 256)
+        for name in ("mgs_linear_attention_fwd", "mgs_linear_attention_bwd"):
+            monkeypatch.setattr(b, name, lambda *a, _name=name: self.calls.append((_name, a)))
+
+
+@pytest.mark.parametrize("stream,name", [(1234, ("external", 1234)), (0, "default"), ("a torch stream", "a torch stream"),
+                                         (None, "current")])
+def test_copies_and_workspace_belong_to_the_named_stream(monkeypatch, stream, name):
+    # a copy on another stream than the kernels' could be read before it is written, and its memory or the
+    # workspace's be handed out again while they run
+    d = _lm.attn_inputs(2, 8, 2, 2, 64, BF16, S0=False)
+    calls = _Calls(monkeypatch)
+    q = d["q"][:, :1].expand(2, 8, 2, 64)
+    go = d["grad_o"][:1, :1].expand(2, 8, 2, 64)
+    api.linear_attention_fwd(q, d["k"], d["v"], d["g"], stream=stream)
+    api.linear_attention_bwd(d["q"], d["k"], d["v"], d["g"], go, stream=stream)
+    assert [n for n, _ in calls.calls] == ["mgs_linear_attention_fwd", "mgs_linear_attention_bwd"]
+    assert calls.copies == [name, name] and calls.scratch == [name, name]
+    assert all(a[-1] is stream for _, a in calls.calls)
