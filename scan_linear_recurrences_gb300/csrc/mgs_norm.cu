@@ -21,27 +21,42 @@ namespace {
 
 constexpr float kFp8Max = 448.f;
 
-// The sum (and with MAX the maximum of another value) over the `tpr` threads of
-// a row: tpr <= 32 within a warp, else the whole block, in one barrier.
-template <bool MAX>
-__device__ __forceinline__ void row_reduce(float &sum, float &top, int tpr, float (*red)[32]) {
-    for (int m = min(tpr, 32) >> 1; m > 0; m >>= 1) {
-        sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        if (MAX) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-    }
-    if (tpr <= 32) return;
-    if ((threadIdx.x & 31) == 0) {
-        red[0][threadIdx.x >> 5] = sum;
-        if (MAX) red[1][threadIdx.x >> 5] = top;
-    }
+// The sum (MAX: the maximum) over the `tpr` threads of a row: tpr <= 32 within a
+// warp, else the whole block, in one barrier.
+template <bool MAX = false>
+__device__ __forceinline__ float row_reduce(float x, int tpr, float *red) {
+    auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+    for (int m = min(tpr, 32) >> 1; m > 0; m >>= 1) x = join(x, __shfl_xor_sync(0xffffffffu, x, m));
+    if (tpr <= 32) return x;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
     __syncthreads();
-    sum = red[0][0];
-    if (MAX) top = red[1][0];
-    for (int i = 1; i < tpr / 32; ++i) {
-        sum += red[0][i];
-        if (MAX) top = fmaxf(top, red[1][i]);
-    }
+    x = red[0];
+    for (int i = 1; i < tpr / 32; ++i) x = join(x, red[i]);
+    return x;
 }
+
+// The scale of values whose largest is `top`, and their quotients by it (by 1
+// where it is zero), as products with the reciprocal: that differs from the
+// quotient's own rounding where e4m3's rounding is a tie, and is as near.  A low
+// scale, whose reciprocal would be infinite, and what it divides are first
+// multiplied by 2^64 (in a branch: another product for every element costs 2 us of 52).
+struct Scale {
+    float scale, inv;
+    bool low;
+    __device__ __forceinline__ explicit Scale(float top) : scale(top * (1.f / kFp8Max)) {
+        low = scale > 0.f && scale < 0x1p-64f;
+        inv = 1.f / (low ? scale * 0x1p64f : scale > 0.f ? scale : 1.f);
+    }
+    template <int V>
+    __device__ __forceinline__ void divide(float (&v)[V]) const {
+        if (__builtin_expect(low, 0)) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] *= 0x1p64f;
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] *= inv;
+    }
+};
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     uint16_t u;
@@ -159,7 +174,7 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 4 : NV == 2 ? 2
                     T *__restrict__ ro, T *__restrict__ y, float *__restrict__ rstd_out, uint8_t *__restrict__ q8,
                     float *__restrict__ scales, int64_t rows, int N, int tpr) {
     constexpr int V = kVec<T>;
-    __shared__ float red[2][2][32];  // in turn: one barrier for a reduction
+    __shared__ float red[2][2][32];  // in turn: one barrier for a reduction (the sum's and the maximum's apart)
     const int c = threadIdx.x % tpr;
     const int64_t step = int64_t(gridDim.x) * (blockDim.x / tpr);
     int64_t row = int64_t(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
@@ -185,7 +200,7 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 4 : NV == 2 ? 2
     int turn = 0;
     for (; row < last; row += step, turn ^= 1) {
         const bool live = row < rows;
-        float r[NV][V], sum = 0.f, top = 0.f;
+        float r[NV][V], sum = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int e = (c + i * tpr) * V;
@@ -200,24 +215,14 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 4 : NV == 2 ? 2
                 unpack(u, r[i]);
             }
             win.mask(e, r[i]);
-            float ww[V];
-            if (FP8 == 1) unpack(PREFETCH ? uw[i] : weight(i), ww);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                sum = fmaf(r[i][j], r[i][j], sum);
-                if (FP8 == 1) top = fmaxf(top, fabsf(r[i][j] * ww[j]));
-            }
+            for (int j = 0; j < V; ++j) sum = fmaf(r[i][j], r[i][j], sum);
         }
         if (PREFETCH) fetch(row + step);
-        row_reduce<FP8 == 1>(sum, top, tpr, red[turn]);
+        sum = row_reduce(sum, tpr, red[turn][0]);
         const float rstd = rsqrtf(sum * inv_n + eps);
         if (FP8 == 0 && rstd_out && live && c == 0) rstd_out[row] = rstd;
-        float inv = 0.f;
-        if (FP8 == 1) {
-            const float sc = top * rstd * (1.f / kFp8Max);
-            if (live && c == 0) scales[row] = sc;
-            inv = sc > 0.f ? 1.f / sc : 1.f;
-        }
+        float top = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int e = (c + i * tpr) * V;
@@ -225,9 +230,10 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 4 : NV == 2 ? 2
             unpack(PREFETCH ? uw[i] : weight(i), ww);
 #pragma unroll
             for (int j = 0; j < V; ++j) r[i][j] = r[i][j] * rstd * ww[j];
-            if (FP8 == 0) {
-                win.store(y, row, e, pack(r[i]));
-                continue;
+            if (FP8 == 0) win.store(y, row, e, pack(r[i]));
+            if (FP8 == 1) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) top = fmaxf(top, fabsf(r[i][j]));
             }
             if (FP8 == 2) {
                 // 128 / V neighbouring threads hold a group
@@ -236,13 +242,20 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 4 : NV == 2 ? 2
                 for (int j = 0; j < V; ++j) m = fmaxf(m, fabsf(r[i][j]));
 #pragma unroll
                 for (int s = 64 / V; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-                const float sc = m * (1.f / kFp8Max);
-                if (live && e < N && e % 128 == 0) scales[row * (N / 128) + e / 128] = sc;
-                inv = sc > 0.f ? 1.f / sc : 1.f;
+                const Scale sc(m);
+                if (live && e < N && e % 128 == 0) scales[row * (N / 128) + e / 128] = sc.scale;
+                sc.divide(r[i]);
+                win.store8(q8, row, e, r[i]);
             }
+        }
+        if (FP8 == 1) {
+            const Scale sc(row_reduce<true>(top, tpr, red[turn][1]));
+            if (live && c == 0) scales[row] = sc.scale;
 #pragma unroll
-            for (int j = 0; j < V; ++j) r[i][j] *= inv;
-            win.store8(q8, row, e, r[i]);
+            for (int i = 0; i < NV; ++i) {
+                sc.divide(r[i]);
+                win.store8(q8, row, (c + i * tpr) * V, r[i]);
+            }
         }
         if (!PREFETCH) fetch(row + step);
     }
@@ -259,7 +272,7 @@ __global__ void __launch_bounds__(256)
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
         const int64_t at = row * N;
         const T *r = res ? ro : x;
-        float sum = 0.f, top = 0.f;
+        float sum = 0.f;
         for (int64_t e = threadIdx.x; e < N; e += 256) {
             float a = to_f(x[at + e]);
             if (res) {
@@ -268,16 +281,15 @@ __global__ void __launch_bounds__(256)
                 a = to_f(t);
             }
             sum = fmaf(a, a, sum);
-            if (FP8 == 1) top = fmaxf(top, fabsf(a * to_f(w[e])));
         }
-        row_reduce<FP8 == 1>(sum, top, 256, red);
-        const float rstd = rsqrtf(sum / float(N) + eps);
+        const float rstd = rsqrtf(row_reduce(sum, 256, red[0]) / float(N) + eps);
         if (FP8 == 0 && rstd_out && threadIdx.x == 0) rstd_out[row] = rstd;
-        float inv = 0.f;
+        Scale sc(0.f);
         if (FP8 == 1) {
-            const float sc = top * rstd * (1.f / kFp8Max);
-            if (threadIdx.x == 0) scales[row] = sc;
-            inv = sc > 0.f ? 1.f / sc : 1.f;
+            float top = 0.f;  // (a thread's elements are the ones that it has written)
+            for (int64_t e = threadIdx.x; e < N; e += 256) top = fmaxf(top, fabsf(to_f(r[at + e]) * rstd * to_f(w[e])));
+            sc = Scale(row_reduce<true>(top, 256, red[1]));
+            if (threadIdx.x == 0) scales[row] = sc.scale;
         }
         if (FP8 == 2) {  // N is a multiple of 128: one warp a group
             for (int64_t g = threadIdx.x / 32; g < N / 128; g += 8) {
@@ -290,19 +302,21 @@ __global__ void __launch_bounds__(256)
                     m = fmaxf(m, fabsf(v[j]));
                 }
                 for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-                const float sc = m * (1.f / kFp8Max), iv = sc > 0.f ? 1.f / sc : 1.f;
-                if ((threadIdx.x & 31) == 0) scales[row * (N / 128) + g] = sc;
+                const Scale of(m);
+                if ((threadIdx.x & 31) == 0) scales[row * (N / 128) + g] = of.scale;
+                of.divide(v);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    q8[at + g * 128 + 32 * j + (threadIdx.x & 31)] = uint8_t(e4m3x2(v[j] * iv, 0.f));
+                for (int j = 0; j < 4; ++j) q8[at + g * 128 + 32 * j + (threadIdx.x & 31)] = uint8_t(e4m3x2(v[j], 0.f));
             }
         } else {
             for (int64_t e = threadIdx.x; e < N; e += 256) {
-                const float v = to_f(r[at + e]) * rstd * to_f(w[e]);
-                if (FP8 == 0)
-                    y[at + e] = from_f<T>(v);
-                else
-                    q8[at + e] = uint8_t(e4m3x2(v * inv, 0.f));
+                float v[1] = {to_f(r[at + e]) * rstd * to_f(w[e])};
+                if (FP8 == 0) {
+                    y[at + e] = from_f<T>(v[0]);
+                } else {
+                    sc.divide(v);
+                    q8[at + e] = uint8_t(e4m3x2(v[0], 0.f));
+                }
             }
         }
         __syncthreads();
@@ -322,7 +336,7 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1)
                     int64_t rows, int N, int tpr) {
     constexpr int V = kVec<T>;
     constexpr bool PREFETCH = NV * V <= 16;
-    __shared__ float red[2][2][32];
+    __shared__ float red[2][32];
     const int c = threadIdx.x % tpr, rpb = blockDim.x / tpr;
     griddep_launch();
     const int64_t step = int64_t(gridDim.x) * rpb, first = int64_t(blockIdx.x) * rpb + threadIdx.x / tpr;
@@ -353,7 +367,7 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1)
     int turn = 0;  // two reduction buffers: one barrier a row
     for (int64_t row = first; row < last; row += step, turn ^= 1) {
         const float rs = rs_next;
-        float dot = 0.f, unused = 0.f;
+        float dot = 0.f;
         uint4 cr[NV], cg[NV], ca[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -371,8 +385,7 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1)
             }
         }
         if (PREFETCH) fetch(row + step);
-        row_reduce<false>(dot, unused, tpr, red[turn]);
-        dot *= inv_n;
+        dot = row_reduce(dot, tpr, red[turn]) * inv_n;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int e = (c + i * tpr) * V;
@@ -402,7 +415,7 @@ __global__ void __launch_bounds__(256)
     norm_bwd_any_kernel(const T *__restrict__ r, const T *__restrict__ w, const float *__restrict__ rstd,
                         const T *__restrict__ gy, const T *__restrict__ gr, T *__restrict__ dx,
                         float *__restrict__ part, int64_t rows, int64_t N) {
-    __shared__ float red[2][32];
+    __shared__ float red[32];
     float *dw = part + int64_t(blockIdx.x) * N;
     for (int64_t e = threadIdx.x; e < N; e += 256) dw[e] = 0.f;
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
@@ -412,9 +425,7 @@ __global__ void __launch_bounds__(256)
         for (int64_t e = threadIdx.x; e < N; e += 256)
             dot = fmaf(to_f(gy[at + e]) * to_f(w[e]), to_f(r[at + e]) * rs, dot);
         __syncthreads();
-        float unused = 0.f;
-        row_reduce<false>(dot, unused, 256, red);
-        dot /= float(N);
+        dot = row_reduce(dot, 256, red) / float(N);
         for (int64_t e = threadIdx.x; e < N; e += 256) {
             const float hat = to_f(r[at + e]) * rs, g = to_f(gy[at + e]);
             dw[e] = fmaf(g, hat, dw[e]);

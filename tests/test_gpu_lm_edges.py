@@ -45,3 +45,36 @@ def test_broadcast_inputs_on_a_named_stream(dtype, address):
     torch.cuda.synchronize()
     for x, y in zip(got[:-1], want[:-1]):
         assert torch.equal(x, y)
+
+
+# ---------------------------------------------------------------- RMS norm in 8 bits
+def _fp8(x, w, group, aligned=True):
+    """q as numbers, the scales with a column for each q, both in 64 bits; x 16 bytes aligned, or not."""
+    buf = torch.zeros(x.numel() + 8, dtype=x.dtype, device="cuda")
+    xc = buf[8 if aligned else 1:][:x.numel()].view(x.shape).copy_(x)
+    q, sc, _ = api.rms_norm_fp8_fwd(xc, w.cuda(), group=group)
+    b.mgs_check()
+    return q.float().double().cpu(), sc.double().cpu().repeat_interleave(group or x.shape[1], 1)
+
+
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("tiny", [1e-37, 1e-40, 1e-44])
+def test_norm_fp8_of_the_smallest_numbers(tiny, dtype, group, aligned):
+    # a group's (or the whole row's) values so small that the scale is subnormal, or zero; zeros among them
+    gen = torch.Generator().manual_seed(61)
+    x = torch.randn(5, 384, generator=gen).to(dtype)
+    x[:, ::7] = 0
+    w = torch.randn(384, generator=gen) + 3
+    w[128 if group else 0:256 if group else 384] *= tiny
+    w = w.to(dtype)
+    q, s = _fp8(x, w, group, aligned)
+    y = _lm.norm_ref(x, w, None, 1e-6, dtype)["y"]
+    want = y.view(5, -1, group or 384).abs().amax(-1).repeat_interleave(group or 384, 1) / 448
+    unit = 2.0 ** -149  # fp32's smallest step; y, the maximum and the scale are each a rounding to it
+    assert ((s - want).abs() <= want * 1e-5 + 2 * unit).all()
+    # half a step of e4m3 (2^-3 of the value, or 2^-9 below 2^-6), and the scale's own error times q
+    err = y.abs() * (2 ** -4 + 1e-5) + s * 2 ** -10 * 1.01 + 448 * 2 * unit
+    assert ((q * s - y).abs() <= err).all()
+    assert not q[:, ::7].any() and not q[s == 0].any() and (s == 0).any() == (tiny == 1e-44)
