@@ -421,7 +421,7 @@ mgs_status mgs_rms_norm_fwd(const void *x, const void *residual, const void *wei
  *     scale = max|y| / 448,  q = y / scale rounded to e4m3,
  * with q = 0 where scale = 0 (fp32 throughout: a maximum below 3e-43 has none).
  * The quotient is a product with 1 / scale: values at a tie of e4m3 may go either
- * way.  Out: q [rows][N] bytes, scales [rows] or
+ * way.  A NaN among the values that share a scale makes it NaN.  Out: q [rows][N] bytes, scales [rows] or
  * [rows][N / 128] fp32. */
 mgs_status mgs_rms_norm_fp8_fwd(const void *x, const void *residual, const void *weight, float eps, void *r, void *q,
                                 float *scales, int64_t rows, int64_t N, int group, int dtype, mgs_stream_t stream);

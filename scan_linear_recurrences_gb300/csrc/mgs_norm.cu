@@ -21,11 +21,19 @@ namespace {
 
 constexpr float kFp8Max = 448.f;
 
+// The larger of two, NaN if either is: a NaN among a row's or group's values has
+// to reach its scale.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+    return m;
+}
+
 // The sum (MAX: the maximum) over the `tpr` threads of a row: tpr <= 32 within a
 // warp, else the whole block, in one barrier.
 template <bool MAX = false>
 __device__ __forceinline__ float row_reduce(float x, int tpr, float *red) {
-    auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+    auto join = [](float a, float b) { return MAX ? max_nan(a, b) : a + b; };
     for (int m = min(tpr, 32) >> 1; m > 0; m >>= 1) x = join(x, __shfl_xor_sync(0xffffffffu, x, m));
     if (tpr <= 32) return x;
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
@@ -233,15 +241,15 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 4 : NV == 2 ? 2
             if (FP8 == 0) win.store(y, row, e, pack(r[i]));
             if (FP8 == 1) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) top = fmaxf(top, fabsf(r[i][j]));
+                for (int j = 0; j < V; ++j) top = max_nan(top, fabsf(r[i][j]));
             }
             if (FP8 == 2) {
                 // 128 / V neighbouring threads hold a group
                 float m = 0.f;
 #pragma unroll
-                for (int j = 0; j < V; ++j) m = fmaxf(m, fabsf(r[i][j]));
+                for (int j = 0; j < V; ++j) m = max_nan(m, fabsf(r[i][j]));
 #pragma unroll
-                for (int s = 64 / V; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+                for (int s = 64 / V; s > 0; s >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, s));
                 const Scale sc(m);
                 if (live && e < N && e % 128 == 0) scales[row * (N / 128) + e / 128] = sc.scale;
                 sc.divide(r[i]);
@@ -287,7 +295,7 @@ __global__ void __launch_bounds__(256)
         Scale sc(0.f);
         if (FP8 == 1) {
             float top = 0.f;  // (a thread's elements are the ones that it has written)
-            for (int64_t e = threadIdx.x; e < N; e += 256) top = fmaxf(top, fabsf(to_f(r[at + e]) * rstd * to_f(w[e])));
+            for (int64_t e = threadIdx.x; e < N; e += 256) top = max_nan(top, fabsf(to_f(r[at + e]) * rstd * to_f(w[e])));
             sc = Scale(row_reduce<true>(top, 256, red[1]));
             if (threadIdx.x == 0) scales[row] = sc.scale;
         }
@@ -299,9 +307,9 @@ __global__ void __launch_bounds__(256)
                     const int64_t e = g * 128 + 32 * j + (threadIdx.x & 31);
                     // written by other threads of this block, before the barrier of the sum
                     v[j] = to_f(r[at + e]) * rstd * to_f(w[e]);
-                    m = fmaxf(m, fabsf(v[j]));
+                    m = max_nan(m, fabsf(v[j]));
                 }
-                for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+                for (int s = 16; s > 0; s >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, s));
                 const Scale of(m);
                 if ((threadIdx.x & 31) == 0) scales[row * (N / 128) + g] = of.scale;
                 of.divide(v);

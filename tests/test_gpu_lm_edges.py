@@ -78,3 +78,29 @@ def test_norm_fp8_of_the_smallest_numbers(tiny, dtype, group, aligned):
     err = y.abs() * (2 ** -4 + 1e-5) + s * 2 ** -10 * 1.01 + 448 * 2 * unit
     assert ((q * s - y).abs() <= err).all()
     assert not q[:, ::7].any() and not q[s == 0].any() and (s == 0).any() == (tiny == 1e-44)
+
+
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_norm_fp8_of_infinities_and_nan(dtype, group, aligned):
+    # as the formula in fp32 has them: a NaN makes its scale NaN (all of a row's: the row's own norm is NaN
+    # or infinite), an infinite weight an infinite scale and zeros beside it
+    gen = torch.Generator().manual_seed(62)
+    x = torch.randn(5, 384, generator=gen).to(dtype)
+    x[1, 5], x[2, 200], x[3, 7] = float("nan"), float("inf"), -float("inf")
+    for column, value in ((None, 1.0), (300, float("nan")), (140, float("inf"))):
+        w = torch.randn(384, generator=gen).to(dtype)
+        if column is not None:
+            w[column] = value
+        q, s = _fp8(x, w, group, aligned)
+        r = x.float()
+        y = r * torch.rsqrt(r.square().mean(-1, keepdim=True) + 1e-6) * w.float()
+        sc = (y.view(5, -1, group or 384).abs().amax(-1) / 448).repeat_interleave(group or 384, 1)
+        z = (y / torch.where(sc > 0, sc, torch.ones_like(sc))).clamp(-448, 448)
+        assert torch.equal(s.isnan(), sc.isnan()) and torch.equal(q.isnan(), z.isnan())
+        assert torch.equal(s.isinf(), sc.isinf())
+        fine = sc.isfinite()
+        assert ((s - sc).abs()[fine] <= 1e-5 * sc[fine]).all()
+        number = ~z.isnan()  # half a step of e4m3, and the rounding of fp32
+        assert ((q - z)[number].abs() <= z[number].abs() * (2 ** -4 + 1e-5) + 2 ** -10 * 1.01).all()
