@@ -15,6 +15,7 @@
 
 #include "mgs_lm.h"
 #include "mgs_num.cuh"
+#include "mgs_rows.h"
 
 namespace mgs {
 namespace {
@@ -184,29 +185,27 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 4 : NV == 2 ? 2
     constexpr int V = kVec<T>;
     __shared__ float red[2][2][32];  // in turn: one barrier for a reduction (the sum's and the maximum's apart)
     const int c = threadIdx.x % tpr;
-    const int64_t step = int64_t(gridDim.x) * (blockDim.x / tpr);
-    int64_t row = int64_t(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
+    RowWalk at(blockIdx.x, gridDim.x, threadIdx.x, blockDim.x, tpr);
     const float inv_n = 1.f / float(N);
-    const Window<T, SHIFT> win(row, rows, N);
+    const Window<T, SHIFT> win(at.row, rows, N);
     uint4 ux[NV], ur[NV], uw[NV];
-    auto fetch = [&](int64_t at) {
+    auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            ux[i] = win.load(x, at, (c + i * tpr) * V);
-            if (res) ur[i] = win.load(res, at, (c + i * tpr) * V);
+            ux[i] = win.load(x, row, (c + i * tpr) * V);
+            if (res) ur[i] = win.load(res, row, (c + i * tpr) * V);
         }
     };
-    fetch(row);
+    fetch(at.row);
     constexpr bool PREFETCH = NV < 8;
     auto weight = [&](int i) { return win.weight(w, (c + i * tpr) * V); };
     if (PREFETCH) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) uw[i] = weight(i);
     }
-    // rows of a block end together (their number is the block's, not the row's)
-    const int64_t last = rows + blockDim.x / tpr - 1;
     int turn = 0;
-    for (; row < last; row += step, turn ^= 1) {
+    for (; at.more(rows); at.next(), turn ^= 1) {
+        const int64_t row = at.row;
         const bool live = row < rows;
         float r[NV][V], sum = 0.f;
 #pragma unroll
@@ -226,7 +225,7 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 4 : NV == 2 ? 2
 #pragma unroll
             for (int j = 0; j < V; ++j) sum = fmaf(r[i][j], r[i][j], sum);
         }
-        if (PREFETCH) fetch(row + step);
+        if (PREFETCH) fetch(row + at.step);
         sum = row_reduce(sum, tpr, red[turn][0]);
         const float rstd = rsqrtf(sum * inv_n + eps);
         if (FP8 == 0 && rstd_out && live && c == 0) rstd_out[row] = rstd;
@@ -265,7 +264,7 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 4 : NV == 2 ? 2
                 win.store8(q8, row, (c + i * tpr) * V, r[i]);
             }
         }
-        if (!PREFETCH) fetch(row + step);
+        if (!PREFETCH) fetch(row + at.step);
     }
 }
 
@@ -345,9 +344,10 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1)
     constexpr int V = kVec<T>;
     constexpr bool PREFETCH = NV * V <= 16;
     __shared__ float red[2][32];
-    const int c = threadIdx.x % tpr, rpb = blockDim.x / tpr;
+    const int c = threadIdx.x % tpr;
     griddep_launch();
-    const int64_t step = int64_t(gridDim.x) * rpb, first = int64_t(blockIdx.x) * rpb + threadIdx.x / tpr;
+    RowWalk at(blockIdx.x, gridDim.x, threadIdx.x, blockDim.x, tpr);
+    const int64_t first = at.row;
     const float inv_n = 1.f / float(N);
     const Window<T, SHIFT> win(first, rows, N);
     float dw[NV][V], rs_next;
@@ -370,10 +370,9 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1)
 #pragma unroll
         for (int j = 0; j < V; ++j) dw[i][j] = 0.f;
     }
-    // rows of a block end together (their number is the block's, not the row's)
-    const int64_t last = rows + rpb - 1;
     int turn = 0;  // two reduction buffers: one barrier a row
-    for (int64_t row = first; row < last; row += step, turn ^= 1) {
+    for (; at.more(rows); at.next(), turn ^= 1) {
+        const int64_t row = at.row;
         const float rs = rs_next;
         float dot = 0.f;
         uint4 cr[NV], cg[NV], ca[NV];
@@ -392,7 +391,7 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1)
                 dot = fmaf(g[j] * ww[j], hat[j], dot);
             }
         }
-        if (PREFETCH) fetch(row + step);
+        if (PREFETCH) fetch(row + at.step);
         dot = row_reduce(dot, tpr, red[turn]) * inv_n;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -409,7 +408,7 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : 512, NV == 1 ? 3 : 1)
             }
             win.store(dx, row, e, pack(g));
         }
-        if (!PREFETCH) fetch(row + step);
+        if (!PREFETCH) fetch(row + at.step);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {

@@ -104,3 +104,24 @@ def test_norm_fp8_of_infinities_and_nan(dtype, group, aligned):
         assert ((s - sc).abs()[fine] <= 1e-5 * sc[fine]).all()
         number = ~z.isnan()  # half a step of e4m3, and the rounding of fp32
         assert ((q - z)[number].abs() <= z[number].abs() * (2 ** -4 + 1e-5) + 2 ** -10 * 1.01).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N", [13, 56, 64, 77, 128])
+@pytest.mark.parametrize("rows", [1, 6, 9, 16, 23, 12345])
+def test_norm_rows_that_do_not_fill_a_block(rows, N, dtype):
+    # several rows a warp, the last block's rows not all there
+    gen = torch.Generator().manual_seed(rows + N)
+    x, res, gy, gr = (torch.randn(rows, N, generator=gen).to(dtype) for _ in range(4))
+    w = torch.randn(N, generator=gen).to(dtype)
+    y, r, rstd = api.rms_norm_fwd(x.cuda(), w.cuda(), res.cuda())
+    dx, dw = api.rms_norm_bwd(r, w.cuda(), rstd, gy.cuda(), gr.cuda())
+    q, sc, _ = api.rms_norm_fp8_fwd(x.cuda(), w.cuda(), res.cuda())
+    b.mgs_check()
+    ref = _lm.norm_ref(x, w, res, 1e-6, dtype, gy, gr)
+    one = _lm.FP32 if dtype == F32 else _lm.BF16_ONE
+    for name, got in (("y", y), ("dx", dx), ("dw", dw)):
+        _lm.check_rounded(name, got, ref[name], one)
+    _lm.check("rstd", rstd, ref["rstd"], _lm.FP32)
+    _lm.check("scales", sc[:, 0], ref["y"].abs().amax(-1) / 448, _lm.FP32)
+    _lm.check("q", q.float() * sc, ref["y"], 2 ** -4)  # each value within half a step of e4m3
