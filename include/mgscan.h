@@ -374,8 +374,8 @@ size_t mgs_linear_attention_workspace_size(const mgs_attention_shape *shape, int
  * and -infinity starts the state anew at that step.  An infinity or NaN reaches
  * what the formula takes it to: in v the outputs of its own column from its step
  * on, not those before.  (Chunks of 128 steps with one in v run many times
- * slower.)  A stride of 0 in bf16, and in the fp32 backward, selects a slower
- * kernel.
+ * slower.)  A stride of 0 in bf16, and of q or k in the fp32 backward, selects a
+ * slower kernel.
  * In: q, k [B][T][Hk][D], v [B][T][H][D], g [B][T][H] or [H] (fp32),
  *     S0 [B][H][D][D] fp32 (nullable).
  * Out: o [B][T][H][D]; S_T [B][H][D][D] fp32 (nullable). */

@@ -285,7 +285,7 @@ def _apart(t, stream):
     """t, or a dense copy of a broadcast t: the tensor-core kernels load through tensor maps, which have no
     zero strides, and the copy costs less than the kernel without them."""
     st = t.stride()
-    if 0 not in st or t.dtype != torch.bfloat16 or all(s or n <= 1 for s, n in zip(st, t.shape)):
+    if 0 not in st or all(s or n <= 1 for s, n in zip(st, t.shape)):
         return t
     with _on(stream, t.device):
         return t.contiguous()
@@ -309,8 +309,11 @@ def _attention_shape(q, k, v, g, scale, stream, grad_o=None):
     _check_typed(g, "g", (H,) if fixed else (B, T, H), torch.float32, dense=fixed, device=dev)
     if grad_o is not None:
         _check_typed(grad_o, "grad_o", v.shape, q.dtype, dense=False, device=dev)
-        grad_o = _apart(grad_o, stream)
-    q, k, v = _apart(q, stream), _apart(k, stream), _apart(v, stream)
+    # (fp32 is read through dense tensors of its terms, but for the gradients' products of q with dq and k with dk)
+    if q.dtype == torch.bfloat16 or grad_o is not None:
+        q, k = _apart(q, stream), _apart(k, stream)
+    if q.dtype == torch.bfloat16:
+        v, grad_o = _apart(v, stream), _apart(grad_o, stream) if grad_o is not None else None
     shape = _b.mgs_attention_shape(
         B, T, H, Hk, D, _DTYPES[q.dtype], fixed, D ** -0.5 if scale is None else scale, _head_strides(q, "q"),
         _head_strides(k, "k"), _head_strides(v, "v"), (0, 0, 1) if fixed else g.stride(),

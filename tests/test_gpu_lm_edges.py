@@ -47,6 +47,65 @@ def test_broadcast_inputs_on_a_named_stream(dtype, address):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("name", ["q", "k"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_broadcast_queries_and_keys_run_as_dense_ones(dtype, name):
+    # the tensor functions copy them where no tensor map describes them: the same kernels, the same bits
+    d = _lm.cuda(_lm.attn_inputs(2, 200, 2, 2, 64, dtype, True, seed=52))
+    d[name] = d[name][:, :1].expand(2, 200, 2, 64)
+    args = lambda x: (x["q"], x["k"], x["v"], x["g"])  # noqa: E731
+    e = {**d, name: d[name].contiguous()}
+    assert torch.equal(api.linear_attention_fwd(*args(d), d["S0"]), api.linear_attention_fwd(*args(e), d["S0"]))
+    for x, y in zip(api.linear_attention_bwd(*args(d), d["grad_o"], d["S0"], d["grad_ST"]),
+                    api.linear_attention_bwd(*args(e), d["grad_o"], d["S0"], d["grad_ST"])):
+        assert torch.equal(x, y)
+
+
+def _through_the_c_entry(d, scale):
+    """Forward and backward with the tensors' own strides, zero ones among them."""
+    c = _lm.cuda({n: t for n, t in d.items() if isinstance(t, torch.Tensor)})
+    for n in ("q", "k", "v", "grad_o"):  # .cuda() keeps no zero strides
+        lead = tuple(slice(0, 1) if st == 0 else slice(None) for st in d[n].stride())
+        c[n] = d[n][lead].contiguous().cuda().expand(d[n].shape)
+    (B, T, Hk, D), H, dtype = d["q"].shape, d["v"].shape[2], d["q"].dtype
+    fixed = d["g"].dim() == 1
+    shape = b.mgs_attention_shape(B, T, H, Hk, D, b.MGS_F32 if dtype == F32 else b.MGS_BF16, fixed, scale,
+                                  *(c[n].stride()[:3] for n in ("q", "k", "v")),
+                                  (0, 0, 1) if fixed else c["g"].stride(), c["grad_o"].stride()[:3])
+    new = lambda *s, dt=dtype: torch.full(s, float("nan"), dtype=dt, device="cuda")  # noqa: E731
+    out = {"o": new(B, T, H, D), "S_T": new(B, H, D, D, dt=F32), "dq": new(B, T, Hk, D), "dk": new(B, T, Hk, D),
+           "dv": new(B, T, H, D), "dg": new(*d["g"].shape, dt=F32), "dS0": new(B, H, D, D, dt=F32)}
+    ws = []
+    for backward in (False, True):
+        n = b.mgs_linear_attention_workspace_size(shape, backward)
+        ws.append((torch.empty(max(n, 1), dtype=torch.uint8, device="cuda"), n))
+    S0, gST = c.get("S0"), c.get("grad_ST")
+    b.mgs_linear_attention_fwd(shape, c["q"], c["k"], c["v"], c["g"], S0, out["o"], out["S_T"], *ws[0])
+    b.mgs_linear_attention_bwd(shape, c["q"], c["k"], c["v"], c["g"], S0, c["grad_o"], gST, out["dq"], out["dk"],
+                               out["dv"], out["dg"], out["dS0"] if S0 is not None else None, *ws[1])
+    b.mgs_check()
+    return out
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,T,H,Hk,S0,fixed,name,dim", [
+    (2, 1, 2, 2, True, False, "q", 0), (2, 17, 2, 1, True, False, "k", 1), (1, 60, 4, 2, False, True, "q", 2),
+    (2, 300, 2, 2, True, False, "k", 0), (3, 333, 3, 3, True, True, "q", 1),  # fp32: two spans of the decay's gradient
+    (1, 1300, 1, 1, True, False, "k", 1), (1, 1500, 2, 1, False, False, "q", 1),  # segments; bf16: two spans
+    (2, 200, 2, 2, True, False, "v", 1), (2, 150, 4, 2, True, False, "grad_o", 0),  # (bf16 alone takes the recurrence)
+])
+def test_recurrence_kernel_through_the_c_entry(B, T, H, Hk, S0, fixed, name, dim, D, dtype):
+    # a stride of zero, which no tensor map has: the walk that is the recurrence itself, in both directions, with
+    # its row products, kept states and segments
+    d = _lm.attn_inputs(B, T, H, Hk, D, dtype, S0, fixed, seed=B + T + D, decay=0.05)
+    d[name] = d[name].narrow(dim, 0, 1).expand(d[name].shape)
+    got, ref = _through_the_c_entry(d, D ** -0.5), _lm.attn_ref(d)
+    tol = _lm.FP32 if dtype == F32 else _lm.BF16_TWO
+    for n, r in ref.items():
+        _lm.check(n, got[n], r, _lm.FP32 if n in ("S_T", "dg", "dS0") else tol)
+
+
 # ---------------------------------------------------------------- RMS norm in 8 bits
 def _fp8(x, w, group, aligned=True):
     """q as numbers, the scales with a column for each q, both in 64 bits; x 16 bytes aligned, or not."""

@@ -63,3 +63,17 @@ def test_copies_and_workspace_belong_to_the_named_stream(monkeypatch, stream, na
     assert [n for n, _ in calls.calls] == ["mgs_linear_attention_fwd", "mgs_linear_attention_bwd"]
     assert calls.copies == [name, name] and calls.scratch == [name, name]
     assert all(a[-1] is stream for _, a in calls.calls)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF16])
+def test_broadcast_queries_and_keys_are_copied_where_it_matters(monkeypatch, dtype):
+    # no tensor map has a zero stride: the library would take its slow kernel (fp32's forward reads q, k and v
+    # through tensors of its own)
+    d = _lm.attn_inputs(2, 8, 2, 2, 64, dtype, S0=False)
+    calls = _Calls(monkeypatch)
+    q, k = (d[n][:, :1].expand(2, 8, 2, 64) for n in ("q", "k"))
+    api.linear_attention_fwd(q, k, d["v"], d["g"])
+    api.linear_attention_bwd(q, k, d["v"], d["g"], d["grad_o"])
+    (_, fwd), (_, bwd) = calls.calls
+    assert all(0 not in t.stride() for t in bwd[1:3])
+    assert all((0 not in t.stride()) == (dtype == BF16) for t in fwd[1:3])
