@@ -442,7 +442,9 @@ size_t mgs_clip_grad_norm_workspace_size(int64_t count);
 /* The global norm of `count` tensors, and their scaling by it:
  *     norm = sqrt(sum of all squares),  out = grad min(1, max_norm / (norm + 1e-6)).
  * grads, outs, numels and dtypes are HOST arrays; outs[i] == grads[i] clips in
- * place.  norm is one fp32 on the device; nothing is copied to the host and the
+ * place.  What is written meets nothing else that is read or written: a tensor
+ * listed twice in place, or an output over another tensor, is
+ * MGS_ERR_INVALID_ARG.  norm is one fp32 on the device; nothing is copied to the host and the
  * call waits for nothing.  A NaN or infinite element makes the norm so, and
  * NaN elements of the outputs with it.  Squares are summed in fp32. */
 mgs_status mgs_clip_grad_norm(const void *const *grads, void *const *outs, const int64_t *numels,

@@ -460,7 +460,8 @@ def rms_norm_bwd(r, weight, rstd, grad_y, grad_r=None, stream=None):
 # ---------------------------------------------------------------- clipping by the global norm
 def clip_grad_norm(grads, max_norm, out=None, stream=None):
     """The norm over all of grads (fp32 and bf16 tensors, contiguous) as one fp32 on the device, and the tensors
-    scaled by min(1, max_norm / (norm + 1e-6)): in place, or into `out` (tensors of the same sizes and types)."""
+    scaled by min(1, max_norm / (norm + 1e-6)): in place, or into `out` (tensors of the same sizes and types).  No
+    tensor is listed twice in place (tied parameters have one gradient), and no output lies over another tensor."""
     grads = list(grads)
     outs = grads if out is None else list(out)
     if len(outs) != len(grads):

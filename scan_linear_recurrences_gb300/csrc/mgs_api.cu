@@ -1,10 +1,13 @@
 // C ABI of libmgscan (declared in include/mgscan.h): argument validation,
 // the per-device error word, and dispatch to the kernel launchers.
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <cstring>
+#include <memory>
 #include <mutex>
 #include <map>
+#include <new>
 #include <set>
 #include <utility>
 
@@ -941,6 +944,32 @@ mgs_status mgs_rms_norm_bwd(const void *r, const void *weight, const float *rstd
                                               cs));
 }
 
+// The byte ranges that a call on many tensors reads (of those that it does not
+// write in place) and writes.
+struct Span {
+    uintptr_t lo, hi;
+};
+static void by_address(Span *s, int64_t n) {
+    auto before = [](const Span &a, const Span &b) { return a.lo < b.lo; };
+    if (!std::is_sorted(s, s + n, before)) std::sort(s, s + n, before);  // gradients mostly lie in their order
+}
+// Whether no written range meets another one, read or written: in the order of
+// their addresses, none of a pair that meets begins behind the other's end.
+static bool written_apart(Span *in, int64_t nin, Span *out, int64_t nout) {
+    by_address(in, nin), by_address(out, nout);
+    uintptr_t read = 0, written = 0;  // the furthest ends so far
+    for (int64_t i = 0, j = 0; i < nin || j < nout;) {
+        if (j == nout || (i < nin && in[i].lo < out[j].lo)) {
+            if (in[i].lo < written) return false;
+            read = std::max(read, in[i++].hi);
+        } else {
+            if (out[j].lo < std::max(read, written)) return false;
+            written = out[j++].hi;
+        }
+    }
+    return true;
+}
+
 size_t mgs_clip_grad_norm_workspace_size(int64_t count) { return count < 0 ? 0 : mgs::clip_workspace_bytes(count); }
 
 mgs_status mgs_clip_grad_norm(const void *const *grads, void *const *outs, const int64_t *numels,
@@ -951,6 +980,12 @@ mgs_status mgs_clip_grad_norm(const void *const *grads, void *const *outs, const
     if (count > 0 && (grads == nullptr || outs == nullptr || numels == nullptr || dtypes == nullptr))
         return MGS_ERR_INVALID_ARG;
     const size_t need = mgs::clip_workspace_bytes(count);
+    if (count > (int64_t(1) << 32)) return MGS_ERR_UNSUPPORTED;
+    Span few[512];
+    std::unique_ptr<Span[]> many(2 * count > 512 ? new (std::nothrow) Span[2 * count] : nullptr);
+    if (2 * count > 512 && many == nullptr) return MGS_ERR_UNSUPPORTED;  // more tensors than the host has memory for
+    Span *const reads = many ? many.get() : few, *const writes = reads + count;
+    int64_t nreads = 0, nwrites = 0;
     for (int64_t i = 0; i < count; ++i) {
         const int es = esize(dtypes[i]);
         if (es == 0) return MGS_ERR_UNSUPPORTED;
@@ -959,10 +994,12 @@ mgs_status mgs_clip_grad_norm(const void *const *grads, void *const *outs, const
         mgs_status st = typed_ptrs(es, {grads[i], outs[i]}, {});
         if (st != MGS_OK) return st;
         const Bytes in{grads[i], numels[i] * es}, out{outs[i], numels[i] * es};
-        // in place, or wholly apart; nothing of it in the norm or the workspace
-        if (grads[i] != outs[i] && !apart({out}, {in})) return MGS_ERR_INVALID_ARG;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(in.p), b = reinterpret_cast<uintptr_t>(out.p);
+        if (a != b) reads[nreads++] = {a, a + uintptr_t(in.n)};
+        writes[nwrites++] = {b, b + uintptr_t(out.n)};
         if (!apart({{norm, 4}, {workspace, int64_t(need)}}, {in, out})) return MGS_ERR_INVALID_ARG;
     }
+    if (!written_apart(reads, nreads, writes, nwrites)) return MGS_ERR_INVALID_ARG;
     const mgs_status st = check_ws(need, workspace, workspace_bytes);
     if (st != MGS_OK) return st;
     return from_cuda(mgs::launch_clip(grads, outs, numels, dtypes, count, max_norm, norm, workspace,
