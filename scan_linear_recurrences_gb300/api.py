@@ -329,6 +329,13 @@ def _scratch(n, device, stream):
         return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def _written(tensors):
+    """Marks tensors that a call has written in place, so that autograd notices where it had saved one of them."""
+    if any(map(torch.Tensor.is_inference, tensors)):
+        tensors = [t for t in tensors if not t.is_inference()]  # which have no versions
+    torch.autograd.graph.increment_version(tensors)
+
+
 def linear_attention_fwd(q, k, v, g, S0=None, scale=None, want_state=False, stream=None):
     """Linear attention with a decay for each head:
     S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t (scale: D^-1/2 unless given).
@@ -394,6 +401,7 @@ def linear_attention_step(q, k, v, g, S, slots=None, scale=None, out=None, strea
     shape = _b.mgs_attention_shape(B, 1, H, Hk, D, _DTYPES[dt], fixed, D ** -0.5 if scale is None else scale,
                                    (qb, 0, qh), (kb, 0, kh), (vb, 0, vh), (0, 0, 1) if fixed else (gs[0], 0, gs[1]))
     _b.mgs_linear_attention_step(shape, q, k, v, g, S, slots, S.shape[0], out, stream)
+    _written((S, out))
     return out
 
 
@@ -489,6 +497,7 @@ def clip_grad_norm(grads, max_norm, out=None, stream=None):
     norm = torch.empty((), dtype=torch.float32, device=dev)
     size = _b.mgs_clip_grad_norm_workspace_size(n)
     _b.mgs_clip_grad_norm(at, to, sizes, codes, max_norm, norm, _scratch(size, dev, stream), size, stream)
+    _written(outs)
     return norm
 
 

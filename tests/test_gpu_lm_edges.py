@@ -106,6 +106,16 @@ def test_recurrence_kernel_through_the_c_entry(B, T, H, Hk, S0, fixed, name, dim
         _lm.check(n, got[n], r, _lm.FP32 if n in ("S_T", "dg", "dS0") else tol)
 
 
+def test_step_on_a_state_that_autograd_has_saved():
+    # the state of a prompt is saved for the gradients; a token that is stepped on it in place would falsify them
+    d = _lm.cuda(_lm.attn_inputs(1, 20, 2, 2, 64, BF16, True, seed=53))
+    q = d["q"].requires_grad_()
+    o, _ = api.linear_attention(q, d["k"], d["v"], d["g"], d["S0"])
+    api.linear_attention_step(d["q"][:, 0].detach(), d["k"][:, 0], d["v"][:, 0], d["g"][:, 0], d["S0"])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        o.sum().backward()
+
+
 # ---------------------------------------------------------------- RMS norm in 8 bits
 def _fp8(x, w, group, aligned=True):
     """q as numbers, the scales with a column for each q, both in 64 bits; x 16 bytes aligned, or not."""

@@ -77,3 +77,39 @@ def test_broadcast_queries_and_keys_are_copied_where_it_matters(monkeypatch, dty
     (_, fwd), (_, bwd) = calls.calls
     assert all(0 not in t.stride() for t in bwd[1:3])
     assert all((0 not in t.stride()) == (dtype == BF16) for t in fwd[1:3])
+
+
+def test_tensors_written_in_place_are_marked_for_autograd(monkeypatch):
+    d = _lm.attn_inputs(2, 1, 2, 2, 64, BF16)
+    _Calls(monkeypatch)
+    monkeypatch.setattr(b, "mgs_linear_attention_step", lambda *a: None)
+    q, k, v, g = (d[n][:, 0] for n in ("q", "k", "v", "g"))
+    S, out = d["S0"], torch.zeros(2, 2, 64, dtype=BF16)
+    before = [t._version for t in (S, out, q)]
+    api.linear_attention_step(q, k, v, g, S, out=out)
+    assert [t._version for t in (S, out, q)] == [before[0] + 1, before[1] + 1, before[2]]
+    with torch.inference_mode():
+        cache = torch.zeros(2, 2, 64, 64)
+    api.linear_attention_step(q, k, v, g, cache)  # an inference tensor has no version
+    # what is differentiated keeps its state: a step on it is noticed
+    S = torch.ones(3, requires_grad=True) * 2
+    loss = (S * S).sum()
+    api._written([S])
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+def test_clipped_tensors_are_marked_for_autograd(monkeypatch):
+    monkeypatch.setattr(b, "mgs_clip_grad_norm_workspace_size", lambda n: 0)
+    monkeypatch.setattr(b, "mgs_clip_grad_norm", lambda *a: None)
+    grads, outs = [torch.zeros(8), torch.zeros(3, dtype=BF16)], [torch.zeros(8), torch.zeros(3, dtype=BF16)]
+
+    class Card:  # the first check asks for the device's type alone
+        type = "cuda"
+    monkeypatch.setattr(torch.Tensor, "device", property(lambda t: Card()))
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: empty(*a, **k))
+    api.clip_grad_norm(grads, 1.0, out=outs)
+    assert [t._version for t in grads + outs] == [0, 0, 1, 1]
+    api.clip_grad_norm(grads, 1.0)
+    assert [t._version for t in grads + outs] == [1, 1, 1, 1]
