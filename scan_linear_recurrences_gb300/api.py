@@ -329,11 +329,15 @@ def _scratch(n, device, stream):
         return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+_increment_version = torch.autograd.graph.increment_version
+
+
 def _written(tensors):
     """Marks tensors that a call has written in place, so that autograd notices where it had saved one of them."""
-    if any(map(torch.Tensor.is_inference, tensors)):
-        tensors = [t for t in tensors if not t.is_inference()]  # which have no versions
-    torch.autograd.graph.increment_version(tensors)
+    try:
+        _increment_version(tensors)
+    except RuntimeError:  # inference tensors have no versions
+        _increment_version([t for t in tensors if not t.is_inference()])
 
 
 def linear_attention_fwd(q, k, v, g, S0=None, scale=None, want_state=False, stream=None):
@@ -392,6 +396,7 @@ def linear_attention_step(q, k, v, g, S, slots=None, scale=None, out=None, strea
         _check_typed(slots, "slots", (B,), torch.int32, device=dev)
     elif S.shape[0] < B:
         raise ValueError(f"{B} sequences without slots need a cache of as many states, not {S.shape[0]}")
+    written = (S,) if out is None else (S, out)
     if out is None:
         out = torch.empty((B, H, D), dtype=dt, device=dev)
     else:
@@ -401,7 +406,7 @@ def linear_attention_step(q, k, v, g, S, slots=None, scale=None, out=None, strea
     shape = _b.mgs_attention_shape(B, 1, H, Hk, D, _DTYPES[dt], fixed, D ** -0.5 if scale is None else scale,
                                    (qb, 0, qh), (kb, 0, kh), (vb, 0, vh), (0, 0, 1) if fixed else (gs[0], 0, gs[1]))
     _b.mgs_linear_attention_step(shape, q, k, v, g, S, slots, S.shape[0], out, stream)
-    _written((S, out))
+    _written(written)
     return out
 
 
