@@ -739,7 +739,7 @@ mgs_status attn_sizes(const mgs_attention_shape *sh, bool with_do, AttnSizes *z)
     if (es == 0 || (sh->D != 64 && sh->D != 128)) return MGS_ERR_UNSUPPORTED;
     if (sh->H > 0 && (sh->Hk == 0 || sh->H % sh->Hk != 0)) return MGS_ERR_INVALID_ARG;
     int64_t bt, n, ns;
-    if (!mul_ok(sh->B, sh->T, &bt) || !mul_ok(bt, sh->H, &n) || !mul_ok(n, int64_t(sh->D) * 8, &n) ||
+    if (!mul_ok(sh->B, sh->T, &bt) || !mul_ok(bt, sh->H > 0 ? sh->H : sh->Hk, &n) || !mul_ok(n, int64_t(sh->D) * 8, &n) ||
         !mul_ok(sh->B, sh->H, &ns) || !mul_ok(ns, int64_t(sh->D) * sh->D * 4, &ns))
         return MGS_ERR_INVALID_ARG;
     if (n > INT64_MAX / 64 || ns > INT64_MAX / 64) return MGS_ERR_INVALID_ARG;
@@ -812,6 +812,12 @@ mgs_status mgs_linear_attention_bwd(const mgs_attention_shape *shape, const void
     if (st != MGS_OK) return st;
     cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     if (z.v == 0) {  // T = 0: dS0 is the final state's gradient; a fixed decay has none
+        if (z.qk > 0) {  // H = 0: no value head reads the queries and keys
+            if ((st = check_ptrs({dq, dk}, {})) != MGS_OK) return st;
+            if (!apart({{dq, z.qk}, {dk, z.qk}}, {})) return MGS_ERR_INVALID_ARG;
+            if (cudaMemsetAsync(dq, 0, size_t(z.qk), cs) != cudaSuccess || cudaMemsetAsync(dk, 0, size_t(z.qk), cs) != cudaSuccess)
+                return MGS_ERR_CUDA;
+        }
         if (shape->fixed_decay && dg != nullptr && shape->H > 0) {
             if (!aligned4(dg)) return MGS_ERR_UNSUPPORTED;
             if (cudaMemsetAsync(dg, 0, size_t(shape->H) * 4, cs) != cudaSuccess) return MGS_ERR_CUDA;

@@ -116,6 +116,26 @@ def test_step_on_a_state_that_autograd_has_saved():
         o.sum().backward()
 
 
+def _filled(monkeypatch):
+    """From here on torch.empty's memory holds sevens: what a call leaves alone shows."""
+    empty = torch.empty
+
+    def full(*a, **k):
+        t = empty(*a, **k)
+        return t.fill_(7) if t.is_cuda else t
+    monkeypatch.setattr(torch, "empty", full)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gradients_without_value_heads(monkeypatch, dtype):
+    q = torch.randn(2, 5, 2, 64, device="cuda", dtype=dtype)
+    v, g = q[:, :, :0], torch.zeros(2, 5, 0, device="cuda")
+    _filled(monkeypatch)
+    dq, dk, dv, dg, _ = api.linear_attention_bwd(q, q, v, g, v)
+    b.mgs_check()
+    assert dq.shape == q.shape and not dq.any() and not dk.any() and dv.numel() == dg.numel() == 0
+
+
 # ---------------------------------------------------------------- RMS norm in 8 bits
 def _fp8(x, w, group, aligned=True):
     """q as numbers, the scales with a column for each q, both in 64 bits; x 16 bytes aligned, or not."""
