@@ -419,7 +419,7 @@ def _norm_args(x, weight, residual):
                 and weight.is_contiguous() and weight.get_device() == here
                 and (residual is None or (residual.dtype is dt and residual.shape == shape
                                           and residual.is_contiguous() and residual.get_device() == here))):
-            return x.numel() // N if N else 0, N, _DTYPES[dt]
+            return x.numel() // N if N else shape[:-1].numel(), N, _DTYPES[dt]
     except (AttributeError, IndexError):
         pass
     _check_typed(x, "x", None, None)
@@ -429,7 +429,7 @@ def _norm_args(x, weight, residual):
     _check_typed(weight, "weight", (N,), x.dtype, device=x.device)
     if residual is not None:
         _check_typed(residual, "residual", x.shape, x.dtype, device=x.device)
-    return x.numel() // N if N else 0, N, _DTYPES[x.dtype]
+    return x.numel() // N if N else x.shape[:-1].numel(), N, _DTYPES[x.dtype]
 
 
 def rms_norm_fwd(x, weight, residual=None, eps=1e-6, stream=None):

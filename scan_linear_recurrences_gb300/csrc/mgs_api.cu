@@ -890,7 +890,11 @@ mgs_status mgs_rms_norm_fwd(const void *x, const void *residual, const void *wei
     int64_t n;
     mgs_status st = norm_sizes(dtype, rows, N, &n);
     if (st != MGS_OK) return st;
-    if (n == 0) return MGS_OK;
+    if (n == 0) {  // rows of nothing: their mean is none
+        if (rows == 0 || rstd == nullptr) return MGS_OK;
+        if (!aligned4(rstd)) return MGS_ERR_UNSUPPORTED;
+        return from_cuda(cudaMemsetAsync(rstd, 0xff, size_t(rows) * 4, reinterpret_cast<cudaStream_t>(stream)));  // NaN
+    }
     const int es = esize(dtype);
     if ((st = typed_ptrs(es, {x, weight, y}, {residual, r})) != MGS_OK) return st;
     if ((residual == nullptr) != (r == nullptr)) return MGS_ERR_INVALID_ARG;
@@ -907,7 +911,12 @@ mgs_status mgs_rms_norm_fp8_fwd(const void *x, const void *residual, const void 
     mgs_status st = norm_sizes(dtype, rows, N, &n);
     if (st != MGS_OK) return st;
     if (group != 0 && (group != 128 || N % 128 != 0)) return MGS_ERR_UNSUPPORTED;
-    if (n == 0) return MGS_OK;
+    if (n == 0) {  // rows of nothing: no value has a magnitude
+        if (rows == 0 || group != 0) return MGS_OK;
+        if (scales == nullptr) return MGS_ERR_INVALID_ARG;
+        if (!aligned4(scales)) return MGS_ERR_UNSUPPORTED;
+        return from_cuda(cudaMemsetAsync(scales, 0, size_t(rows) * 4, reinterpret_cast<cudaStream_t>(stream)));
+    }
     const int es = esize(dtype);
     if ((st = typed_ptrs(es, {x, weight, q}, {residual, r})) != MGS_OK) return st;
     if (scales == nullptr || (residual == nullptr) != (r == nullptr)) return MGS_ERR_INVALID_ARG;

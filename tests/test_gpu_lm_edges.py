@@ -136,6 +136,17 @@ def test_gradients_without_value_heads(monkeypatch, dtype):
     assert dq.shape == q.shape and not dq.any() and not dk.any() and dv.numel() == dg.numel() == 0
 
 
+def test_norm_of_rows_of_nothing(monkeypatch):
+    x, w = torch.empty(3, 0, device="cuda"), torch.empty(0, device="cuda")
+    _filled(monkeypatch)
+    y, r, rstd = api.rms_norm_fwd(x, w)
+    q, sc, _ = api.rms_norm_fp8_fwd(x, w)
+    dx, dw = api.rms_norm_bwd(r, w, rstd, y)
+    b.mgs_check()
+    assert y.shape == q.shape == dx.shape == (3, 0) and dw.shape == (0,)
+    assert rstd.isnan().all() and not sc.any()  # the mean of nothing, the largest of nothing
+
+
 # ---------------------------------------------------------------- RMS norm in 8 bits
 def _fp8(x, w, group, aligned=True):
     """q as numbers, the scales with a column for each q, both in 64 bits; x 16 bytes aligned, or not."""
