@@ -14,6 +14,7 @@ import contextlib
 import operator
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _binding as _b
 
@@ -631,6 +632,7 @@ class LinearAttention(torch.autograd.Function):
         return o, ST
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_o, grad_ST):
         q, k, v, g, S0 = ctx.saved_tensors
         if grad_o is None:
@@ -651,6 +653,7 @@ class RMSNorm(torch.autograd.Function):
         return (y, r) if ctx.has_residual else y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, grad_y, grad_r=None):
         r, weight, rstd = ctx.saved_tensors
         grad_y = torch.zeros_like(r) if grad_y is None else grad_y.contiguous()

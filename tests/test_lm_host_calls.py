@@ -113,3 +113,17 @@ def test_clipped_tensors_are_marked_for_autograd(monkeypatch):
     assert [t._version for t in grads + outs] == [0, 0, 1, 1]
     api.clip_grad_norm(grads, 1.0)
     assert [t._version for t in grads + outs] == [1, 1, 1, 1]
+
+
+def test_second_derivatives_are_refused(monkeypatch):
+    # the gradients come out of the library without a graph of their own: a second differentiation would take
+    # them for constants
+    monkeypatch.setattr(api, "linear_attention_fwd", lambda q, k, v, g, S0, scale, want_state: (v.detach() * 2, v.detach().sum()))
+    monkeypatch.setattr(api, "linear_attention_bwd", lambda q, k, v, g, go, S0, gST, scale: (q * 0, k * 0, go.detach() * 2, None, None))
+    monkeypatch.setattr(api, "rms_norm_fwd", lambda x, w, res, eps: (x.detach() * 2, x.detach(), x.detach()))
+    monkeypatch.setattr(api, "rms_norm_bwd", lambda r, w, rstd, gy, gr: (gy.detach() * r, w * 0))
+    q, w = torch.ones(1, 2, 1, 64, requires_grad=True), torch.ones(64, requires_grad=True)
+    for y in (api.linear_attention(q, q, q, torch.zeros(1, 2, 1))[0], api.rms_norm(q, w)):
+        d, = torch.autograd.grad((y * y).sum(), q, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            ((d * d).sum() + (q * q).sum()).backward()
