@@ -1,6 +1,6 @@
 // Internal launcher interface of the language-model operators (linear
 // attention with a decay for each head, RMS norm with the residual's addition,
-// clipping by the global gradient norm) between mgs_lm_api.cu and the kernels.
+// clipping by the global gradient norm) between mgs_api.cu and the kernels.
 #pragma once
 
 #include <cstddef>

@@ -496,23 +496,6 @@ Shape bwd_shape(int64_t pieces) {
 }
 template <int N>
 using Int = std::integral_constant<int, N>;
-Shape shape_of(int64_t pieces, int64_t most_of_one, int64_t most_of_two) {
-    if (pieces <= 32) {
-        int t = 8;
-        while (t < pieces) t *= 2;
-        return {t, 1};
-    }
-    int nv = pieces <= most_of_one ? 1 : pieces <= most_of_two ? 2 : pieces <= 2048 ? 4 : 8;
-    if (most_of_one == 0) {
-        auto slots = [&](int n) { return (pieces + 32 * n - 1) / (32 * n) * 32 * n; };
-        nv = pieces > 2048 ? 8 : slots(2) < slots(4) ? 2 : 4;
-        if (most_of_two == 1 && pieces > 32 && pieces <= 64) nv = 1;
-        if (most_of_two == 2 && pieces > 32 && pieces <= 128) nv = 1;
-    }
-    const int64_t tpr = ((pieces + nv - 1) / nv + 31) / 32 * 32;
-    if (tpr > 512) return {0, 0};
-    return {int(tpr), nv};
-}
 // Rows of a block: a row's threads are within a warp, or the whole block.
 int block_rows(int tpr) { return tpr > 32 ? 1 : 128 / tpr; }
 
