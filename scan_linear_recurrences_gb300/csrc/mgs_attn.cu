@@ -566,17 +566,17 @@ cudaError_t run_walks(AttnSet &set, int walks, const mgs_attention_shape &sh, co
                       cudaStream_t s) {
     cudaError_t e;
     // fp32 has three terms everywhere.  In bf16 the first two of the gradients'
-    // walks feed the decay's, whose sums want every digit of fp32; dv, and the
-    // attention itself, are rounded to the type.  dv's walk shares no tensor with
+    // walks feed the decay's, whose sums want every digit of fp32; of dv, and of the
+    // attention itself, nothing but the rounding to the type follows: two.  dv's walk shares no tensor with
     // those two and fills the SMs that they leave (5 x 1537 steps, 12 heads of
     // 64: 173 us, one after the other 243).
     auto walk = [&](bool state_only) {
         if (!p.mma) return launch_attn_rec(set, walks, sh.D, sh.dtype, state_only, s);
         const bool early = !state_only && p.nseg > 1;  // after attn_join
         if (sh.dtype == MGS_F32) return launch_attn_mma(set, 0, walks, sh.D, sh.dtype, 3, state_only, true, false, s);
-        if (walks == 1 || state_only) return launch_attn_mma(set, 0, walks, sh.D, sh.dtype, 1, state_only, early, false, s);
+        if (walks == 1 || state_only) return launch_attn_mma(set, 0, walks, sh.D, sh.dtype, 2, state_only, early, false, s);
         const cudaError_t e = launch_attn_mma(set, 0, 2, sh.D, sh.dtype, 3, false, early, false, s);
-        return e != cudaSuccess ? e : launch_attn_mma(set, 2, 1, sh.D, sh.dtype, 1, false, false, true, s);
+        return e != cudaSuccess ? e : launch_attn_mma(set, 2, 1, sh.D, sh.dtype, 2, false, false, true, s);
     };
     if (set.nseg > 1) {
         for (int i = 0; i < walks; ++i) set.w[i].seg_in = set.w[i].seg_out = ws.take<float>(seg_bytes(p, sh.D));

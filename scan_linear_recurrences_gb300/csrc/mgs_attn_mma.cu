@@ -11,8 +11,11 @@
 // The four products are 128 x 128 x 128 (tcgen05.mma, bf16, fp32 sums).  q, k
 // and v are bf16 and enter exactly; what is computed enters as a sum of bf16
 // terms: the weighted keys of the state always as three (24 bits: the state is
-// fp32, and stays it), P and S as one where the output is rounded to bf16
-// anyway, as three where <out, x> goes into the decay's gradient (TERMS).
+// fp32, and stays it); P and S as two (2^-17) where only the output's own rounding
+// to bf16 follows, which is then the only one (with one term the output's error is
+// 2.35e-3 instead of 1.66e-3 of it, for 128 us instead of 147 in the forward of 128
+// lanes of 4096 steps), as three where <out, x> goes into the decay's gradient
+// (TERMS).
 //
 // fp32 comes as three bf16 tensors whose sum it is, so that every operand has
 // three terms and a product six pairs of them.  A block then has room for 64
@@ -38,11 +41,11 @@
 // idle, longer ones need more TMEM than there is.  What bounds a block is the
 // chain of a chunk: P from A (two thirds of the rows' time), the weighted keys'
 // three terms (all of the state warps'), the products in their order between
-// them.  A chunk takes 3.9 us of an SM (heads of 128 in bf16; the products'
-// issue 1.6), 5.4 with three terms, 5.1 (two heads of 64), 6.2 and 9 (fp32,
-// heads of 64 and 128); a block's start and end about 6 us.  152 lanes of 1024
-// steps, bf16, heads of 128: 40 us, 3.3 TB/s of HBM, tensor pipe 31 % (44 % with
-// three terms; fp32 36 to 41 %).
+// them.  A chunk takes 4.3 us of an SM (heads of 128 in bf16), 5.4 with three
+// terms, 6.2 (two heads of 64), 6.2 and 9 (fp32, heads of 64 and 128); a block's
+// start and end about 6 us.  152 lanes of 1024 steps, bf16, heads of 128: 45 us,
+// 3.0 TB/s of HBM, tensor pipe 38 % (44 % with three terms; fp32 43 to 45 %; heads
+// of 64 in bf16 25 %).
 #include "mgs_launch.h"
 #include "mgs_lm.h"
 #include "mgs_num.cuh"
@@ -61,9 +64,9 @@ constexpr int kThreads = 20 * 32;              // five warpgroups
 // Registers a thread: the kernel is launched with kRegs for each; the last
 // warpgroup gives up what the others take more.  With heads of 128 and three
 // terms the state's warps take some too (dq and dk of 128 lanes of 4096 steps 5
-// us less); with one term that costs the state-only walk more than it gives
-// (1 x 16384 steps, 16 heads: 144 us against 114), with heads of 64 the last
-// warpgroup's sums of g of two heads need the registers (673 us against 725).
+// us less); with two terms that costs the state-only walk more than it gives
+// (1 x 16384 steps, 16 heads: 152 us against 124), with heads of 64 the last
+// warpgroup's sums of g of two heads need the registers (717 us against 758).
 constexpr int kRegs = 96, kRegsRows = 112;
 template <int D, int TERMS, int IN>
 struct Regs {
@@ -75,15 +78,12 @@ constexpr int GT = 16;                         // steps of a group of weighted k
 constexpr int NG = C / GT;
 
 // TMEM columns (all 512):
-//   A 0..127 and P behind it (one term) or over it and behind it (three);
-//   X 192..319: Q S, then (once the rows have it in registers) the state's product;
+//   A 0..127, P over it (a third term behind it, to 191);
+//   X 192..319: Q S, then (once the rows have it in registers) the state's product,
+//   then (once that is in registers) P V;
 //   the weighted keys of a chunk, three terms of 64 columns, 320..511.
-// P V goes where it finds room: with one term and one head in A's place (P has been
-// made of it), else in X, once the state's product is in registers.
-template <int D, int TERMS, int IN>
 struct Tmem {
-    static constexpr bool over_a = D == 128 && TERMS == 1;
-    static constexpr uint32_t A = 0, P = TERMS == 1 ? 128 : 0, X = 192, O = over_a ? 0 : 192, W = 320;
+    static constexpr uint32_t A = 0, P = 0, X = 192, O = 192, W = 320;
 };
 
 // mbarriers (of a ring: one a slot) and what goes with them
@@ -101,16 +101,17 @@ struct Bars {
 
 template <int D, int TERMS, int IN>
 struct Smem {
-    static_assert(IN == 1 || TERMS == 3, "fp32: every operand in three terms");
+    static_assert(TERMS == 3 || (TERMS == 2 && IN == 1), "fp32: every operand in three terms");
     static constexpr int VD = IN == 3 ? 64 : D;                     // the state's columns in a block
     static constexpr int KH = IN == 3 ? D / 64 : 1;                 // passes over the columns of q and k
     static constexpr int NH = D == 64 && IN == 1 ? 2 : 1;           // heads of a block
     static constexpr int tile = IN == 1 ? 2 * kPanel : IN * kPanel;  // a tile: halves, heads or terms in its panels
     static constexpr int sterm = IN == 3 ? D * 128 : D == 64 ? kPanel : 2 * kPanel;  // a term of the state operand
-    static constexpr int NK = TERMS == 1 ? 2 : 1, NQ = NK, NV = IN == 1 && (TERMS == 1 || D == 64) ? 2 : 1;
+    static constexpr int NK = TERMS == 2 ? 2 : 1, NQ = 1;  // (a second place for q gains nothing)
+    static constexpr int NV = IN == 1 && (TERMS == 2 || D == 64) ? 2 : 1;
     static constexpr int k = TERMS * sterm, q = k + NK * tile, v = q + NQ * tile;
-    // where rows are staged on their way out: with one term the chunk's keys' place, else that of x
-    static constexpr int x = v + NV * tile, arr = x + (TERMS == 1 ? 0 : 2 * kPanel);
+    // where rows are staged on their way out: with two terms the chunk's keys' place, else that of x
+    static constexpr int x = v + NV * tile, arr = x + (TERMS == 2 ? 0 : 2 * kPanel);
     // per head: G (high and low parts), the column factors and the state weights of the 128 steps
     static constexpr int bars = arr + NH * 4 * C * 4;
     static constexpr int walk = bars + (sizeof(Bars) + 15) / 16 * 16;  // the block's AttnWalk
@@ -274,7 +275,7 @@ template <int D, int TERMS, int IN>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_mma_kernel(const __grid_constant__ AttnMaps maps, const __grid_constant__ AttnSet set, int state_only) {
     using L = Smem<D, TERMS, IN>;
-    using M = Tmem<D, TERMS, IN>;
+    using M = Tmem;
     constexpr int NH = L::NH, KH = L::KH, VH = D / L::VD;
     constexpr int SC = L::VD / 2;               // state columns of a thread
     constexpr int OC = NH == 2 ? 64 : L::VD / 2;  // output columns of a thread
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&k_full[i], 1), mbar_init(&q_full[i], 1), mbar_init(&v_full[i], 1);
             // the rows' warps, who stage the output in it at the end, or its readers: the state's
             // warps and Q K^T
-            mbar_init(&k_empty[i], TERMS == 1 || state_only ? 8 : 9);
+            mbar_init(&k_empty[i], TERMS == 2 || state_only ? 8 : 9);
             mbar_init(&q_empty[i], 1), mbar_init(&v_empty[i], state_only ? 1 : 2);
             mbar_init(&w_full[i], 8), mbar_init(&w_full2[i], 8);
         }
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = from_state())) break;
             if (lane == 0 && it > 0) {  // the chunk before has been stored: its stage is free
                 bulk_wait_read();
-                mb_arrive(TERMS == 1 ? &k_empty[(it - 1) % L::NK] : x_empty);
+                mb_arrive(TERMS == 2 ? &k_empty[(it - 1) % L::NK] : x_empty);
             }
 #pragma unroll 1
             for (int hp = 0; hp < NH; ++hp) {
@@ -412,11 +413,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int u = 0; u < 16; u += 4) {
                             const float4 ah = *reinterpret_cast<const float4 *>(G + j0 + u);
-                            float e[4] = {gi - ah.x, gi - ah.y, gi - ah.z, gi - ah.w};
-                            if (TERMS > 1) {
-                                const float4 al = *reinterpret_cast<const float4 *>(G + C + j0 + u);
-                                e[0] += gl - al.x, e[1] += gl - al.y, e[2] += gl - al.z, e[3] += gl - al.w;
-                            }
+                            const float4 al = *reinterpret_cast<const float4 *>(G + C + j0 + u);
+                            const float e[4] = {(gi - ah.x) + (gl - al.x), (gi - ah.y) + (gl - al.y),
+                                                (gi - ah.z) + (gl - al.z), (gi - ah.w) + (gl - al.w)};
 #pragma unroll
                             for (int m = 0; m < 4; ++m) {
                                 // computed whether or not it is masked: no branch for each element
@@ -438,34 +437,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 };
-                if constexpr (TERMS == 1) {
+                // The first two terms take the place of the 16 columns of A that this warp
+                // has just read (nobody else touches them), a third has columns of its own.
 #pragma unroll 1
-                    for (int j0 = 64 * hh; j0 < 64 * hh + 64; j0 += 16) {
-                        float v[16];
-                        piece(j0, v);
-                        uint32_t pk[8];
+                for (int j0 = 64 * hh; j0 < 64 * hh + 64; j0 += 16) {
+                    float v[16];
+                    piece(j0, v);
+                    uint32_t pk[TERMS][8];
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) pk[u] = pack_bf16(v[2 * u], v[2 * u + 1]);
-                        tmem_put8(tq + M::P + j0 / 2, pk);
-                    }
-                } else {
-                    // The first two terms take the place of the 16 columns of A that this warp
-                    // has just read (nobody else touches them), the third has columns of its own.
-#pragma unroll 1
-                    for (int j0 = 64 * hh; j0 < 64 * hh + 64; j0 += 16) {
-                        float v[16];
-                        piece(j0, v);
-                        uint32_t pk[3][8];
+                    for (int u = 0; u < 8; ++u) {
+                        uint32_t t[TERMS];
+                        split<TERMS>(make_float2(v[2 * u], v[2 * u + 1]), t);
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            uint32_t t[3];
-                            split<3>(make_float2(v[2 * u], v[2 * u + 1]), t);
-                            pk[0][u] = t[0], pk[1][u] = t[1], pk[2][u] = t[2];
-                        }
-                        tmem_put8(tq + M::P + j0, pk[0]);
-                        tmem_put8(tq + M::P + j0 + 8, pk[1]);
-                        tmem_put8(tq + M::P + 128 + j0 / 2, pk[2]);
+                        for (int m = 0; m < TERMS; ++m) pk[m][u] = t[m];
                     }
+                    tmem_put8(tq + M::P + j0, pk[0]);
+                    tmem_put8(tq + M::P + j0 + 8, pk[1]);
+                    if (TERMS == 3) tmem_put8(tq + M::P + 128 + j0 / 2, pk[TERMS - 1]);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -475,10 +463,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             if (lane == 0) mb_arrive(g_empty);
             // The output: row i, this thread's columns.  The warp's 32 rows are staged (swizzled
-            // rows of 128 bytes) where nobody else reads any more, one term in the chunk's keys,
+            // rows of 128 bytes) where nobody else reads any more, two terms in the chunk's keys,
             // three in x's tile, and stored by TMA, which drops rows past the end.
             const int64_t tw = int64_t(c) * C + 32 * wb;  // the warp's first row
-            unsigned char *stage = sm + (TERMS == 1 ? L::k + (it % L::NK) * L::tile : L::x) + hh * kPanel + 32 * wb * 128;
+            unsigned char *stage = sm + (TERMS == 2 ? L::k + (it % L::NK) * L::tile : L::x) + hh * kPanel + 32 * wb * 128;
             unsigned char *mine = stage + lane * 128;
             const int live = h < H ? min(32, T - int(tw)) : 0;  // rows that exist (may be negative)
             auto own = [&](int u) { return reinterpret_cast<uint4 *>(mine + ((u ^ (lane & 7)) << 4)); };
@@ -511,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mb_arrive(o_free);
-            if (TERMS > 1 && w.row_dot) {
+            if (TERMS == 3 && w.row_dot) {
                 constexpr int V = IN == 1 ? 8 : 4;
                 if (!(ok = wwait(x_full, it))) break;
                 float2 dot = make_float2(0.f, 0.f);
@@ -744,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     __syncwarp();
-                    if (lane == 0 && (state_only || TERMS > 1)) mb_arrive(&k_empty[kt_i % L::NK]);
+                    if (lane == 0 && (state_only || TERMS == 3)) mb_arrive(&k_empty[kt_i % L::NK]);
                 }
                 if (!ok) break;
                 if (lane == 0) mb_arrive(g_empty);
@@ -817,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             umma_bf16_ss(tm + M::A, q + koff(ks) + uint64_t(m * (kPanel >> 4)),
                                          k + koff(ks) + uint64_t(o * (kPanel >> 4)), id_k, add);
                 if (kh == KH - 1) umma_commit(a_done);
-                if (TERMS > 1 && hp == NH - 1) umma_commit(&k_empty[tile_i % L::NK]);
+                if (TERMS == 3 && hp == NH - 1) umma_commit(&k_empty[tile_i % L::NK]);
             };
             auto qs = [&](int it, int kh) {
                 const int tile_i = it * KH + kh;
@@ -867,10 +855,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     add = false;
 #pragma unroll 1
                     for (int m = TERMS - 1; m >= 0; --m) {
-                        // of three terms, 16 steps' first and second ones lie side by side, the third
-                        // ones behind all of those
-                        const uint32_t p = tm + M::P + (TERMS == 1 ? 0 : m == 2 ? 128 : 8 * m);
-                        const uint32_t step = TERMS == 1 || m == 2 ? 8 : 16;
+                        // 16 steps' first and second terms lie side by side, the third ones behind all
+                        // of those
+                        const uint32_t p = tm + M::P + (m == 2 ? 128 : 8 * m);
+                        const uint32_t step = m == 2 ? 8 : 16;
 #pragma unroll 1
                         for (int o = last(m); o >= 0; --o)
 #pragma unroll 4
@@ -885,27 +873,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int it = 0; it < n && ok; ++it) {
                 if (!state_only) {
-                    // Q K^T as soon as its place is free: where P V goes elsewhere, when P has been made
-                    // of the last one (P's products are ahead of it in the queue); else after Q S, whose
-                    // place is wanted by the state's product
-                    auto a_next = [&](int kh) {
-                        const int tile_i = it * KH + kh;
-                        if (!wait(&k_full[tile_i % L::NK], tile_i / L::NK)) return false;
-                        if (M::over_a && it > 0 && !wait(o_free, it - 1)) return false;
-                        tc_fence_after();
-                        qk(it, 0, kh);
-                        return true;
-                    };
+                    // Q K^T at once: P has been made of the last one, and P's products are ahead of it in the
+                    // queue
 #pragma unroll 1
                     for (int kh = 0; kh < KH; ++kh) {
                         const int tile_i = it * KH + kh;
                         if (!(ok = wait(&q_full[tile_i % L::NQ], tile_i / L::NQ))) break;
-                        if (!M::over_a && !(ok = a_next(kh))) break;
+                        if (!(ok = wait(&k_full[tile_i % L::NK], tile_i / L::NK))) break;
+                        tc_fence_after();
+                        qk(it, 0, kh);
                         if (kh == 0 && !(ok = wait(s_ready, it))) break;
-                        if (kh == 0 && it > 0 && !(ok = wait(M::over_a ? kv_free : o_free, it - 1))) break;
+                        if (kh == 0 && it > 0 && !(ok = wait(o_free, it - 1))) break;
                         tc_fence_after();
                         qs(it, kh);
-                        if (M::over_a && !(ok = a_next(kh))) break;
                         if (NH == 1) umma_commit(&q_empty[tile_i % L::NQ]);
                     }
                     if (!ok || !(ok = wait(o_ready, it))) break;  // Q S is in the rows' registers
@@ -922,13 +902,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 kv(it, 1);
                 umma_commit(kv_done);
                 if (!state_only) {
-                    if (!M::over_a && !(ok = wait(kv_free, it))) break;
+                    if (!(ok = wait(kv_free, it))) break;
                     if (!(ok = wait(p_ready, it * NH))) break;
                     tc_fence_after();
-                    if (NH == 2 && TERMS == 1) qk(it, 1, 0);  // P stands beside A
                     pv(it, 0);
                     if (NH == 2) {
-                        if (TERMS != 1) qk(it, 1, 0);         // ... or over it: after the product with P
+                        qk(it, 1, 0);  // P stands over A: after the product with it
                         umma_commit(&q_empty[it % L::NQ]);
                         if (!(ok = wait(p_ready, it * NH + 1))) break;
                         tc_fence_after();
@@ -1076,7 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (!state_only) {
         // ------------------------------------------------ x, and whether all of v is finite
         constexpr int XN = IN == 1 ? 64 : 32;  // columns of a panel
-        const bool has_x = TERMS > 1 && w.row_dot != nullptr;
+        const bool has_x = TERMS == 3 && w.row_dot != nullptr;
         bool ok = true;
         int loads = 0;
 #pragma unroll 1
@@ -1185,8 +1164,8 @@ cudaError_t launch_attn_mma(const AttnSet &all, int first, int nwalks, int D, in
             return e;
     }
     auto *fn = f32 ? (D == 64 ? go<64, 3, 3> : go<128, 3, 3>)
-               : D == 64 ? (terms == 1 ? go<64, 1, 1> : go<64, 3, 1>)
-                         : (terms == 1 ? go<128, 1, 1> : go<128, 3, 1>);
+               : D == 64 ? (terms == 2 ? go<64, 2, 1> : go<64, 3, 1>)
+                         : (terms == 2 ? go<128, 2, 1> : go<128, 3, 1>);
     return fn(maps, set, nwalks, state_only, early || beside, s);
 }
 

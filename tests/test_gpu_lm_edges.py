@@ -106,6 +106,37 @@ def test_recurrence_kernel_through_the_c_entry(B, T, H, Hk, S0, fixed, name, dim
         _lm.check(n, got[n], r, _lm.FP32 if n in ("S_T", "dg", "dS0") else tol)
 
 
+@pytest.mark.parametrize("B,T,H,Hk,D", [(2, 300, 3, 3, 64), (1, 700, 4, 2, 64), (2, 300, 2, 2, 128), (1, 700, 4, 1, 128),
+                                        (1, 5000, 2, 2, 128), (3, 1, 2, 2, 64), (40, 129, 4, 4, 64), (40, 129, 4, 4, 128)])
+@pytest.mark.parametrize("resets", [False, True])
+def test_bf16_outputs_are_rounded_once(B, T, H, Hk, D, resets):
+    # what is computed of bf16 inputs is held to 2^-17 and better before the output's own rounding, sums of many
+    # strong decays included.  Granted that to 2^-14 of the output, an element differs from the rounded reference
+    # by a step (2^-8) where the reference is as near as that to a tie, one of 64: 2^-11 of the whole
+    d = _lm.attn_inputs(B, T, H, Hk, D, BF16, True, seed=D + T, decay=0.3)
+    if resets:
+        d["g"][:, ::3] = -100.0  # from the sums of g only the differences between near steps count
+    c, grads = _lm.cuda(d), T <= 700 and B < 40
+    ref = _lm.attn_ref(d, grads=grads)
+    got = {"o": api.linear_attention_fwd(c["q"], c["k"], c["v"], c["g"], c["S0"])}
+    if grads:
+        r = api.linear_attention_bwd(c["q"], c["k"], c["v"], c["g"], c["grad_o"], c["S0"], c["grad_ST"])
+        got.update(zip(("dq", "dk", "dv"), r))
+    b.mgs_check()
+    for n, x in got.items():
+        _lm.check(n, x, ref[n], _lm.BF16_ONE)
+        _lm.check_rounded(n, x, ref[n], 2.0 ** -11)
+
+
+def test_prompt_and_tokens_agree_to_one_rounding():
+    d = _lm.cuda(_lm.attn_inputs(3, 150, 4, 2, 128, BF16, False, seed=54))
+    whole = api.linear_attention_fwd(d["q"], d["k"], d["v"], d["g"])
+    _, S = api.linear_attention_fwd(*(d[n][:, :130] for n in ("q", "k", "v", "g")), want_state=True)
+    for t in range(130, 150):
+        o = api.linear_attention_step(*(d[n][:, t] for n in ("q", "k", "v", "g")), S)
+        _lm.check("o", o, whole[:, t], 2.0 ** -11)  # the same value rounded, but where it is near a tie
+
+
 def test_step_on_a_state_that_autograd_has_saved():
     # the state of a prompt is saved for the gradients; a token that is stepped on it in place would falsify them
     d = _lm.cuda(_lm.attn_inputs(1, 20, 2, 2, 64, BF16, True, seed=53))
