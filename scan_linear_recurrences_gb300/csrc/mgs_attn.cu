@@ -455,8 +455,8 @@ bool mma_takes(const mgs_attention_shape &sh, bool backward) {
 // Steps over which the decay's gradient is summed between exact restarts.  The
 // error grows with them (one decay a head, 16 x 1024 steps of 8 heads of 64 in
 // fp32: 7e-7 with 1024, 5e-7 with 512, 3e-7 with 256), the states to be kept
-// shrink (the gradients' time 203 us with 512, 207 with 256; heads of 128: 274
-// and 286).  bf16 reads half the bytes for as many states: 7e-7 with 1024.
+// shrink (the gradients' time 203 us with 512, 206 with 256; heads of 128: 270
+// and 278).  bf16 reads half the bytes for as many states: 7e-7 with 1024.
 constexpr int kSpanF32 = 256, kSpanBF16 = 1024;
 
 struct Plan {
