@@ -378,8 +378,8 @@ size_t mgs_linear_attention_workspace_size(const mgs_attention_shape *shape, int
  * slower kernel.
  * Precision: states, decays and all sums are fp32; running sums of g are pairs of
  * fp32.  bf16: o, dq, dk and dv err by their one rounding (1.66e-3, relative L2),
- * states by 1e-7 to 3e-7, dg by 1e-6 to 2e-6; factors computed on the way are held
- * to 2^-17 or better.  fp32: products of factors of 24 bits down to 2^-16 of the
+ * states by 1e-7 to 3e-7, dg by 3e-7 to 9e-7 (of a fixed decay, a sum that cancels,
+ * up to some 1e-6); factors computed on the way are held to 2^-17 or better.  fp32: products of factors of 24 bits down to 2^-16 of the
  * largest, in sums that the tensor cores cut off: o and the gradients err by 2e-7
  * (heads of 64) to 7e-7 (128), dg by 2e-7 to 8e-7.  fp32 values beyond bf16's
  * largest (3.39e38) count as infinite.
@@ -396,7 +396,7 @@ mgs_status mgs_linear_attention_fwd(const mgs_attention_shape *shape, const void
  *     dg_t = <R_t, e^{g_t} S_{t-1}>,  dS0 = e^{g_1} R_1,
  * dq and dk summed over the value heads that share a query/key head, dg over
  * batch and steps when the decay is fixed.  The forward's outputs are not
- * needed.  dg comes out of sums over up to 1024 steps, so that an infinity or NaN
+ * needed.  dg comes out of sums over up to 512 steps, so that an infinity or NaN
  * reaches that of some steps before it too.  All of q, k, v, g, S0 as in the
  * forward; grad_S_T nullable.
  * Out: dq, dk [B][T][Hk][D], dv [B][T][H][D], dg fp32 as g (dense), dS0

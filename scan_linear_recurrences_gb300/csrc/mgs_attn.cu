@@ -241,34 +241,37 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     }
 }
 
-__device__ __forceinline__ float block_sum(float x, float *red) {
+// The sum over a block of 256 threads, as a pair.
+__device__ __forceinline__ float2 block_sum(float2 x, float2 *red) {
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+    for (int m = 16; m > 0; m >>= 1)
+        add2(x.x, x.y, __shfl_xor_sync(0xffffffffu, x.x, m), __shfl_xor_sync(0xffffffffu, x.y, m));
     __syncthreads();
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
     __syncthreads();
-    float t = 0.f;
-    for (int i = 0; i < int(blockDim.x) / 32; ++i) t += red[i];
+    float2 t = red[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) add2(t.x, t.y, red[i].x, red[i].y);
     return t;
 }
 
 // dg over one span: dg_t = <R_e, S_e> + sum_{t <= s < e} (<q_s, dq_s> - <k_s, dk_s>),
-// e the span's end.  With a decay of one number a head, the span's sum of dg
-// goes to part[lane][span] instead.  Bound by the reads of S and R (128 lanes of 4
-// spans, heads of 128: 76 MB in 17 us).
+// e the span's end.  With a decay of one number a head, the span's sum of dg goes
+// to part[lane][span] instead.  These sums cancel (of a fixed decay's, all but one
+// part in a hundred), so they are of pairs of fp32.  Bound by the reads of S and R.
 __global__ void __launch_bounds__(256)
     attn_dg_kernel(const float *__restrict__ u, const float *__restrict__ w, int parts, const float *__restrict__ ckS,
-                   const float *__restrict__ ckR, float *__restrict__ dg, float *__restrict__ part, int64_t T,
-                   int64_t H, int spans, int per, int DD) {
-    __shared__ float red[8], scan[8];
-    constexpr int NT = 256;  // threads, each with `per` of the span's steps, at most 4
+                   const float *__restrict__ ckR, float *__restrict__ dg, float2 *__restrict__ part, int64_t T,
+                   int64_t H, int spans, int span_steps, int DD) {
+    __shared__ float2 red[8], scan[8];
+    constexpr int NT = 256;  // threads, each with one or two of the span's steps
     griddep_wait();
     const int64_t lane = blockIdx.x / spans;
-    const int span = int(blockIdx.x % spans), tid = threadIdx.x;
+    const int span = int(blockIdx.x % spans), tid = threadIdx.x, per = span_steps > NT ? 2 : 1;
     const int64_t b = lane / H, h = lane % H;
-    const int64_t t0 = int64_t(span) * per * NT;
-    const int n = int(min64(per * NT, T - t0));
-    float tail = 0.f;
+    const int64_t t0 = int64_t(span) * span_steps;
+    const int n = int(min64(span_steps, T - t0));
+    float2 tail = make_float2(0.f, 0.f);
     if (ckS) {
         const float *a = ckS + (lane * spans + span) * DD, *c = ckR + (lane * spans + span) * DD;
         float acc = 0.f;
@@ -280,44 +283,45 @@ __global__ void __launch_bounds__(256)
             for (int j = 0; j < 4; ++j)
                 acc += (x[j][0] * y[j][0] + x[j][1] * y[j][1]) + (x[j][2] * y[j][2] + x[j][3] * y[j][3]);
         }
-        tail = block_sum(acc, red);
+        tail = block_sum(make_float2(acc, 0.f), red);
     }
     const int64_t all = int64_t(gridDim.x) / spans * T;  // of one part
     // suffix sums: thread i holds steps per i .. per i + per - 1
-    float d[4] = {0.f, 0.f, 0.f, 0.f};
+    float2 d[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     for (int p = 0; p < parts; ++p) {
-        float x[4], y[4];
+        float x[2], y[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             const int t = per * tid + i;
             const int64_t at = lane * T + t0 + t + p * all;
             x[i] = i < per && t < n ? u[at] : 0.f;
             y[i] = i < per && t < n ? w[at] : 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] += x[i] - y[i];
+        for (int i = 0; i < 2; ++i) add2(d[i].x, d[i].y, x[i], 0.f), add2(d[i].x, d[i].y, -y[i], 0.f);
     }
-    d[2] += d[3], d[1] += d[2], d[0] += d[1];
-    float suf = d[0];
+    add2(d[0].x, d[0].y, d[1].x, d[1].y);
+    float2 suf = d[0];
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const float o = __shfl_down_sync(0xffffffffu, suf, m);
-        if ((tid & 31) + m < 32) suf += o;
+        const float oh = __shfl_down_sync(0xffffffffu, suf.x, m), ol = __shfl_down_sync(0xffffffffu, suf.y, m);
+        if ((tid & 31) + m < 32) add2(suf.x, suf.y, oh, ol);
     }
     __syncthreads();
     if ((tid & 31) == 0) scan[tid >> 5] = suf;
     __syncthreads();
-    const float next = __shfl_down_sync(0xffffffffu, suf, 1);
-    float after = tail + ((tid & 31) != 31 ? next : 0.f);
-    for (int i = (tid >> 5) + 1; i < NT / 32; ++i) after += scan[i];
-    float sum = 0.f;
+    const float nh = __shfl_down_sync(0xffffffffu, suf.x, 1), nl = __shfl_down_sync(0xffffffffu, suf.y, 1);
+    float2 after = tail, sum = make_float2(0.f, 0.f);
+    if ((tid & 31) != 31) add2(after.x, after.y, nh, nl);
+    for (int i = (tid >> 5) + 1; i < NT / 32; ++i) add2(after.x, after.y, scan[i].x, scan[i].y);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
         const int t = per * tid + i;
         if (i >= per || t >= n) continue;
-        const float x = d[i] + after;
-        sum += x;
-        if (dg) dg[(b * T + t0 + t) * H + h] = x;
+        float2 x = d[i];
+        add2(x.x, x.y, after.x, after.y);
+        add2(sum.x, sum.y, x.x, x.y);
+        if (dg) dg[(b * T + t0 + t) * H + h] = x.x;
     }
     if (part) {
         sum = block_sum(sum, red);
@@ -327,14 +331,16 @@ __global__ void __launch_bounds__(256)
 
 // dg[h] = sum over batch and spans, in a fixed order: a few thousand numbers, 3 us
 __global__ void __launch_bounds__(256)
-    attn_dg_fixed_kernel(const float *__restrict__ part, float *__restrict__ dg, int64_t B, int64_t H, int spans) {
-    __shared__ float red[8];
+    attn_dg_fixed_kernel(const float2 *__restrict__ part, float *__restrict__ dg, int64_t B, int64_t H, int spans) {
+    __shared__ float2 red[8];
     const int64_t h = blockIdx.x;
-    float acc = 0.f;
-    for (int64_t i = threadIdx.x; i < B * spans; i += blockDim.x)
-        acc += part[((i / spans) * H + h) * spans + i % spans];
+    float2 acc = make_float2(0.f, 0.f);
+    for (int64_t i = threadIdx.x; i < B * spans; i += blockDim.x) {
+        const float2 x = part[((i / spans) * H + h) * spans + i % spans];
+        add2(acc.x, acc.y, x.x, x.y);
+    }
     acc = block_sum(acc, red);
-    if (threadIdx.x == 0) dg[h] = acc;
+    if (threadIdx.x == 0) dg[h] = acc.x;
 }
 
 // out[row][hk][D] = sum of the group's heads of in[row][H][D].  Bound by memory.
@@ -452,12 +458,15 @@ bool mma_takes(const mgs_attention_shape &sh, bool backward) {
     return qk && apart(sh.v_stride, sh.H) && (!backward || apart(sh.do_stride, sh.H));
 }
 
-// Steps over which the decay's gradient is summed between exact restarts.  The
-// error grows with them (one decay a head, 16 x 1024 steps of 8 heads of 64 in
-// fp32: 7e-7 with 1024, 5e-7 with 512, 3e-7 with 256), the states to be kept
-// shrink (the gradients' time 203 us with 512, 206 with 256; heads of 128: 270
-// and 278).  bf16 reads half the bytes for as many states: 7e-7 with 1024.
-constexpr int kSpanF32 = 256, kSpanBF16 = 1024;
+// Steps over which the decay's gradient is summed between exact restarts, whole
+// chunks and at most 512.  The error grows with them, the states to be kept shrink
+// (the gradients of 128 lanes of 4096 steps, heads of 128 in bf16: 517 us with 1024,
+// 523 with 512, 556 with 256; dg's error up to 1.6e-6, 9e-7, 6e-7; in fp32, 64 lanes
+// of 1024 steps: 270 with 512, 278 with 256, dg's error 7e-7 with 256).  A decay of
+// one number a head has the sum of a whole batch's, which cancels further: chunk by
+// chunk (8 x 1000 steps, 8 heads of 128 in bf16: 4.4e-6, against 8.8e-6 with 256 and
+// 4.3e-5 with 1024).
+constexpr int kSpanF32 = 256, kSpanBF16 = 512, kSpanFixed = 128;
 
 struct Plan {
     int64_t lanes, chunks, seg_len;
@@ -488,7 +497,7 @@ Plan plan_of(const mgs_attention_shape &sh, int walks) {
     if (p.seg_len < kAttnChunk) p.seg_len = kAttnChunk;
     p.nseg = int((sh.T + p.seg_len - 1) / p.seg_len);
     if (p.nseg < 1) p.nseg = 1;
-    p.span = f32 ? kSpanF32 : kSpanBF16;
+    p.span = sh.fixed_decay ? kSpanFixed : f32 ? kSpanF32 : kSpanBF16;
     p.spans = int((sh.T + p.span - 1) / p.span);
     return p;
 }
@@ -615,7 +624,7 @@ size_t attn_workspace_bytes(const mgs_attention_shape &sh, bool backward) {
         const size_t rows = size_t(sh.B) * sh.T * sh.H;
         n += 2 * up256(rows * 4 * p.parts);                                                     // row products
         n += 2 * up256(size_t(p.lanes) * p.spans * sh.D * sh.D * 4);                  // S and R at span ends
-        n += up256(size_t(p.lanes) * p.spans * 4);                                    // spans' sums of dg
+        n += up256(size_t(p.lanes) * p.spans * 8);                                    // spans' sums of dg
         if (sh.Hk != sh.H) n += 2 * up256(rows * sh.D * 4);                           // dq, dk of each value head
     }
     return n;
@@ -650,7 +659,7 @@ cudaError_t launch_attn_bwd(const mgs_attention_shape &sh, const void *q, const 
     float *u = carve.take<float>(rows * 4 * p.parts), *wd = carve.take<float>(rows * 4 * p.parts);
     const size_t ck = size_t(p.lanes) * p.spans * sh.D * sh.D * 4;
     float *ckS = carve.take<float>(ck), *ckR = carve.take<float>(ck);
-    float *part = carve.take<float>(size_t(p.lanes) * p.spans * 4);
+    float2 *part = carve.take<float2>(size_t(p.lanes) * p.spans * 8);
     float *dqf = nullptr, *dkf = nullptr;
     if (group > 1) dqf = carve.take<float>(rows * sh.D * 4), dkf = carve.take<float>(rows * sh.D * 4);
     const bool ends = p.spans > 1 || gST != nullptr;  // else R is zero at the only span's end
@@ -688,7 +697,7 @@ cudaError_t launch_attn_bwd(const mgs_attention_shape &sh, const void *q, const 
     if ((e = run_walks(set, 3, sh, p, carve, s)) != cudaSuccess) return e;
     if ((e = launch_next(attn_dg_kernel, unsigned(p.lanes * p.spans), 256, 0, s, p.mma, u, wd, p.parts,
                          ends ? ckS : nullptr, ckR, sh.fixed_decay ? nullptr : dg, sh.fixed_decay ? part : nullptr, sh.T,
-                         sh.H, p.spans, p.span / 256, sh.D * sh.D)) != cudaSuccess)
+                         sh.H, p.spans, p.span, sh.D * sh.D)) != cudaSuccess)
         return e;
     if (sh.fixed_decay) attn_dg_fixed_kernel<<<unsigned(sh.H), 256, 0, s>>>(part, dg, sh.B, sh.H, p.spans);
     if (group > 1) {

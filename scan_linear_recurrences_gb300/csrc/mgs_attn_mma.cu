@@ -198,15 +198,6 @@ __device__ __forceinline__ void split(float2 x, uint32_t (&t)[TERMS]) {
     }
 }
 
-// (h, l) += (a, b), both sums of two fp32
-__device__ __forceinline__ void add2(float &h, float &l, float a, float b) {
-    const float s = h + a, t = s - h;
-    const float e = (h - (s - t)) + (a - t);
-    const float lo = l + b + e;
-    h = s + lo;
-    l = lo - (h - s);
-}
-
 // A row's part of P V alone: o += o_scale kv_scale sum_j e^(..) (q_t . k_j) v_j over
 // the chunk's steps j on row t's side of the mask.  For chunks with an infinity
 // or NaN among the v_j: the tensor cores multiply the masked entries too, and 0
@@ -504,12 +495,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(ok = wwait(x_full, it))) break;
                 float2 dot = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
+                for (int u = 0; u < 8; ++u) {  // a sum of short sums: half the rounding of one long one
                     float xx[V];
                     unpack(*own(u), xx);
+                    float2 part = __fmul2_rn(make_float2(o1[V * u], o1[V * u + 1]), make_float2(xx[0], xx[1]));
 #pragma unroll
-                    for (int m = 0; m < V; m += 2)
-                        dot = __ffma2_rn(make_float2(o1[V * u + m], o1[V * u + m + 1]), make_float2(xx[m], xx[m + 1]), dot);
+                    for (int m = 2; m < V; m += 2)
+                        part = __ffma2_rn(make_float2(o1[V * u + m], o1[V * u + m + 1]), make_float2(xx[m], xx[m + 1]), part);
+                    dot = __fadd2_rn(dot, part);
                 }
                 __syncwarp();
                 // a head in two warps, or in two of each of two blocks: each leaves its own product

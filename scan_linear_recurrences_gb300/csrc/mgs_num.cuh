@@ -59,6 +59,15 @@ __device__ __forceinline__ uint4 pack(const float (&v)[8]) {
     return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
 }
 
+// (h, l) += (a, b), both sums of two fp32
+__device__ __forceinline__ void add2(float &h, float &l, float a, float b) {
+    const float s = h + a, t = s - h;
+    const float e = (h - (s - t)) + (a - t);
+    const float lo = l + b + e;
+    h = s + lo;
+    l = lo - (h - s);
+}
+
 // e^x as a sum of two fp32 (relative error about 1e-8), for factors that are
 // multiplied together hundreds of times: x = n log 2 + y with |y| <= log(2) / 2
 // (log 2 as 11357 / 2^14 and the rest, so that n times the first is exact: Cody

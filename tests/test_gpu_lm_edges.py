@@ -137,6 +137,33 @@ def test_prompt_and_tokens_agree_to_one_rounding():
         _lm.check("o", o, whole[:, t], 2.0 ** -11)  # the same value rounded, but where it is near a tie
 
 
+def _dg64(d, scale):
+    """The decay's gradient in 64 bits: dg_t = <R_t, e^{g_t} S_{t-1}> from dg_t - dg_{t+1} = <q_t, dq_t> - <k_t, dk_t>."""
+    q, k, v, go = (d[n].double().cuda() for n in ("q", "k", "v", "grad_o"))
+    (B, T, H, D), a = q.shape, d["g"].double().cuda().exp()[:, None, None]
+    S, x = torch.zeros(B, H, D, D, dtype=torch.float64, device="cuda"), torch.empty(B, T, H, dtype=torch.float64, device="cuda")
+    R = torch.zeros_like(S)
+    for t in range(T):
+        S = a * S + k[:, t, :, :, None] * v[:, t, :, None, :]
+        x[:, t] = scale * ((S @ go[:, t, :, :, None])[..., 0] * q[:, t]).sum(-1)
+    for t in range(T - 1, -1, -1):
+        R = R + scale * q[:, t, :, :, None] * go[:, t, :, None, :]
+        x[:, t] -= ((R @ v[:, t, :, :, None])[..., 0] * k[:, t]).sum(-1)
+        R = a * R
+    return x.flip(1).cumsum(1).flip(1)
+
+
+@pytest.mark.parametrize("seed", range(10))
+@pytest.mark.parametrize("D", [64, 128])
+def test_gradient_of_a_fixed_decay(D, seed):
+    # one number for thousands of steps, whose gradients cancel in it: the more, the faster the decay
+    d = _lm.attn_inputs(8, 1000, 8, 8, D, BF16, False, True, seed=seed, decay=0.5)
+    c = _lm.cuda(d)
+    got = api.linear_attention_bwd(c["q"], c["k"], c["v"], c["g"], c["grad_o"])[3]
+    b.mgs_check()
+    _lm.check("dg", got, _dg64(d, D ** -0.5).sum((0, 1)), _lm.FP32)
+
+
 def test_step_on_a_state_that_autograd_has_saved():
     # the state of a prompt is saved for the gradients; a token that is stepped on it in place would falsify them
     d = _lm.cuda(_lm.attn_inputs(1, 20, 2, 2, 64, BF16, True, seed=53))
