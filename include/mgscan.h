@@ -378,11 +378,12 @@ size_t mgs_linear_attention_workspace_size(const mgs_attention_shape *shape, int
  * slower kernel.
  * Precision: states, decays and all sums are fp32; running sums of g are pairs of
  * fp32.  bf16: o, dq, dk and dv err by their one rounding (1.66e-3, relative L2),
- * states by 1e-7 to 3e-7, dg by 3e-7 to 9e-7 (of a fixed decay, a sum that cancels,
- * up to some 1e-6); factors computed on the way are held to 2^-17 or better.  fp32: products of factors of 24 bits down to 2^-16 of the
- * largest, in sums that the tensor cores cut off: o and the gradients err by 2e-7
- * (heads of 64) to 7e-7 (128), dg by 2e-7 to 8e-7.  fp32 values beyond bf16's
- * largest (3.39e38) count as infinite.
+ * states by 1e-7 to 3e-7, dg by 3e-7 to 9e-7 (of a fixed decay, whose sum cancels,
+ * some 1e-6); factors computed on the way are held to 2^-17 or better.  fp32:
+ * products of factors of 24 bits down to 2^-16 of the largest, in sums that the
+ * tensor cores cut off: o and the gradients err by 2e-7 (heads of 64) to 7e-7
+ * (128), dg by 2e-7 to 8e-7 (of a fixed decay some 1e-6).  fp32 values beyond
+ * bf16's largest (3.39e38) count as infinite.
  * In: q, k [B][T][Hk][D], v [B][T][H][D], g [B][T][H] or [H] (fp32),
  *     S0 [B][H][D][D] fp32 (nullable).
  * Out: o [B][T][H][D]; S_T [B][H][D][D] fp32 (nullable). */
