@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(D *D / 32) attn_rec_kernel(const __grid_consta
         const int nn = int(min64(TS, t1 - nbase));
         if (nbase >= t0 && nbase < t1) fetch(nbase, nn);
         const int64_t end = base + n;
-        if (!STATE_ONLY && w.ckpt && w.rev && (end % set.span == 0 || end == set.T))
+        const bool keep = !STATE_ONLY && w.ckpt && (end % set.span == 0 || end == set.T) && (end - 1) / set.span < set.kept;
+        if (keep && w.rev)
             put_state(w.ckpt + (lane * set.spans + (end - 1) / set.span) * D * D, false);
         if (STATE_ONLY && tid == 0)
             for (int u = 0; u < n; ++u) total += double(sg[u]);
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(D *D / 32) attn_rec_kernel(const __grid_consta
                     if (u < n && c == 0) w.row_dot[lane * set.T + base + u] = dot;
                 }
             }
-            if (w.ckpt && !w.rev && (end % set.span == 0 || end == set.T))
+            if (keep && !w.rev)
                 put_state(w.ckpt + (lane * set.spans + (end - 1) / set.span) * D * D, false);
             __syncthreads();
         }
@@ -262,7 +263,7 @@ __device__ __forceinline__ float2 block_sum(float2 x, float2 *red) {
 __global__ void __launch_bounds__(256)
     attn_dg_kernel(const float *__restrict__ u, const float *__restrict__ w, int parts, const float *__restrict__ ckS,
                    const float *__restrict__ ckR, float *__restrict__ dg, float2 *__restrict__ part, int64_t T,
-                   int64_t H, int spans, int span_steps, int DD) {
+                   int64_t H, int spans, int kept, int span_steps, int DD) {
     __shared__ float2 red[8], scan[8];
     constexpr int NT = 256;  // threads, each with one or two of the span's steps
     griddep_wait();
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(256)
     const int64_t t0 = int64_t(span) * span_steps;
     const int n = int(min64(span_steps, T - t0));
     float2 tail = make_float2(0.f, 0.f);
-    if (ckS) {
+    if (span < kept) {
         const float *a = ckS + (lane * spans + span) * DD, *c = ckR + (lane * spans + span) * DD;
         float acc = 0.f;
         for (int e0 = 4 * tid; e0 < DD; e0 += 16 * NT) {  // DD is a multiple of 4096: four pieces at a time
@@ -662,9 +663,8 @@ cudaError_t launch_attn_bwd(const mgs_attention_shape &sh, const void *q, const 
     float2 *part = carve.take<float2>(size_t(p.lanes) * p.spans * 8);
     float *dqf = nullptr, *dkf = nullptr;
     if (group > 1) dqf = carve.take<float>(rows * sh.D * 4), dkf = carve.take<float>(rows * sh.D * 4);
-    const bool ends = p.spans > 1 || gST != nullptr;  // else R is zero at the only span's end
-
     AttnSet set = set_of(sh, p, g, ctl);
+    set.kept = p.spans - (gST == nullptr ? 1 : 0);  // without a gradient of the last state R is zero there
     AttnWalk &a = set.w[0], &r = set.w[1], &c = set.w[2];
     Splitter split{sh, p, carve};
     int64_t qs[3], ks[3], vs[3], gs[3];
@@ -677,13 +677,13 @@ cudaError_t launch_attn_bwd(const mgs_attention_shape &sh, const void *q, const 
     copy3(a.qs, gs), copy3(a.ks, vs), copy3(a.vs, ks), copy3(a.xs, sh.q_stride);
     a.vdiv = a.xdiv = group;
     a.s_in = S0, a.s_in_t = 1, a.o_scale = sh.scale;
-    a.row_dot = u, a.ckpt = ends ? ckS : nullptr;
+    a.row_dot = u, a.ckpt = set.kept > 0 ? ckS : nullptr;
     // dk = R v: the reverse walk of (v, do, q) on R^T
     r.q = tv, r.k = tg, r.v = tq, r.x = k;
     copy3(r.qs, vs), copy3(r.ks, gs), copy3(r.vs, qs), copy3(r.xs, sh.k_stride);
     r.vdiv = r.xdiv = group;
     r.s_in = gST, r.s_in_t = 1, r.kv_scale = sh.scale, r.rev = 1;
-    r.row_dot = wd, r.ckpt = ends ? ckR : nullptr;
+    r.row_dot = wd, r.ckpt = set.kept > 0 ? ckR : nullptr;
     // dv = R^T k: the reverse walk of (k, q, do) on R
     c.q = tk, c.k = tq, c.v = tg, c.out = dv;
     copy3(c.qs, ks), copy3(c.ks, qs), copy3(c.vs, gs);
@@ -696,8 +696,8 @@ cudaError_t launch_attn_bwd(const mgs_attention_shape &sh, const void *q, const 
     r.out = group > 1 ? static_cast<void *>(dkf) : dk, r.out_f32 = group > 1;
     if ((e = run_walks(set, 3, sh, p, carve, s)) != cudaSuccess) return e;
     if ((e = launch_next(attn_dg_kernel, unsigned(p.lanes * p.spans), 256, 0, s, p.mma, u, wd, p.parts,
-                         ends ? ckS : nullptr, ckR, sh.fixed_decay ? nullptr : dg, sh.fixed_decay ? part : nullptr, sh.T,
-                         sh.H, p.spans, p.span, sh.D * sh.D)) != cudaSuccess)
+                         ckS, ckR, sh.fixed_decay ? nullptr : dg, sh.fixed_decay ? part : nullptr, sh.T, sh.H, p.spans,
+                         set.kept, p.span, sh.D * sh.D)) != cudaSuccess)
         return e;
     if (sh.fixed_decay) attn_dg_fixed_kernel<<<unsigned(sh.H), 256, 0, s>>>(part, dg, sh.B, sh.H, p.spans);
     if (group > 1) {

@@ -633,7 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // chunk is walked), and at the walk's end.
             if (!state_only) {
                 const int ce = rev ? chunk_of(it) : chunk_of(it - 1);
-                if (marks && (rev ? it < n : it > 0) && ((ce + 1) % per_span == 0 || (ce + 1) * C >= T)) {
+                if (marks && (rev ? it < n : it > 0) && ((ce + 1) % per_span == 0 || (ce + 1) * C >= T) &&
+                    ce / per_span < set.kept) {
                     if (live) put_state(w.ckpt + (ln * set.spans + ce / per_span) * D * D);
                     if (!(ok = staged())) break;
                 }

@@ -31,7 +31,7 @@ struct AttnWalk {
     int s_in_t;                   // ... stored transposed
     float *s_out;                 // state at the walk's end, [B H][D][D] (null: not wanted)
     float *row_dot;               // [parts][B H][T]: <out_t, x_t> before rounding, in parts to be added
-    float *ckpt;                  // [B H][spans][D][D]: the state at each span's end (null: not wanted)
+    float *ckpt;                  // [B H][spans][D][D]: the state at the first `kept` spans' ends (null: not wanted)
     const float *seg_in;          // [B H][nseg][D][D]: the state at each segment's start (nseg > 1)
     float *seg_out;               // [B H][nseg][D][D]: state-only pass: each segment's own state
     float o_scale, kv_scale;
@@ -46,7 +46,7 @@ struct AttnSet {
     int first;                    // the launch's first walk
     int beside;                   // launched beside other walks, with whose kernel it shares nothing but its end
     int64_t seg_len;              // steps of a segment (a multiple of kAttnChunk)
-    int nseg, spans;
+    int nseg, spans, kept;
     int span;                     // steps between two states that are kept: whole chunks
     uint32_t tries;               // a barrier wait's limit: tries of about 40 ns
     DevCtl ctl;
