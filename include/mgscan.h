@@ -397,8 +397,10 @@ mgs_status mgs_linear_attention_fwd(const mgs_attention_shape *shape, const void
  *     dg_t = <R_t, e^{g_t} S_{t-1}>,  dS0 = e^{g_1} R_1,
  * dq and dk summed over the value heads that share a query/key head, dg over
  * batch and steps when the decay is fixed.  The forward's outputs are not
- * needed.  dg comes out of sums over up to 512 steps, so that an infinity or NaN
- * reaches that of some steps before it too.  All of q, k, v, g, S0 as in the
+ * needed.  dg comes out of sums of <q_s, dq_s> - <k_s, dk_s> over up to 512 steps:
+ * it errs by 1e-7 of those products rather than of itself, which is much less where
+ * a decay is near zero, and an infinity or NaN reaches that of some steps before
+ * it too.  All of q, k, v, g, S0 as in the
  * forward; grad_S_T nullable.
  * Out: dq, dk [B][T][Hk][D], dv [B][T][H][D], dg fp32 as g (dense), dS0
  *     [B][H][D][D] fp32 (nullable). */
