@@ -32,12 +32,28 @@ def _check(t, name, shape=None):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def workspace(op, B, T, H_or_D, k, device):
-    """A workspace tensor of the size the op needs (None when it needs none)."""
+def _on(stream, device):
+    """The context in which memory and copies belong to the call's stream (an address, a torch stream, or None: the
+    current one).  What is allocated in it may be dropped when the call returns: it goes back to that stream."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):  # address 0: the default stream, for which torch has no external one
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
+
+
+def _scratch(n, device, stream):
+    """n bytes of workspace that stay reserved until `stream` is done with them."""
+    if not n:
+        return None
+    with _on(stream, device):
+        return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def workspace(op, B, T, H_or_D, k, device, stream=None):
+    """A workspace tensor of the size the op needs (None when it needs none), of the stream that it is for."""
     n = _b.mgs_workspace_size(op, B, T, H_or_D, k)
-    if n == 0:
-        return None, 0
-    return torch.empty(n, dtype=torch.uint8, device=device), n
+    return _scratch(n, device, stream), n
 
 
 # ---------------------------------------------------------------- matrix_affine_scan
@@ -48,7 +64,7 @@ def matrix_affine_scan_fwd(A, b, h0=None, out=None, stream=None):
     if h0 is not None:
         _check(h0, "h0", (B, H, k))
     h = out if out is not None else torch.empty_like(b)
-    ws, nws = workspace(_b.MGS_OP_MATRIX_AFFINE_SCAN_FWD, B, T, H, k, b.device)
+    ws, nws = workspace(_b.MGS_OP_MATRIX_AFFINE_SCAN_FWD, B, T, H, k, b.device, stream)
     _b.mgs_matrix_affine_scan_fwd(A, b, h0, h, B, T, H, k, ws, nws, stream)
     return h
 
@@ -62,7 +78,7 @@ def matrix_affine_scan_bwd(A, h0, h, grad_h, need_dh0=True, stream=None):
     dA = torch.empty_like(A)
     db = torch.empty_like(h)
     dh0 = torch.empty((B, H, k), dtype=torch.float32, device=h.device) if need_dh0 else None
-    ws, nws = workspace(_b.MGS_OP_MATRIX_AFFINE_SCAN_BWD, B, T, H, k, h.device)
+    ws, nws = workspace(_b.MGS_OP_MATRIX_AFFINE_SCAN_BWD, B, T, H, k, h.device, stream)
     _b.mgs_matrix_affine_scan_bwd(A, h0, h, grad_h, dA, db, dh0, B, T, H, k, ws, nws, stream)
     return dA, db, dh0
 
@@ -77,7 +93,7 @@ def matrix_affine_scan_bwd_recompute(A, b, h0, grad_h, need_dh0=True, stream=Non
     dA = torch.empty_like(A)
     db = torch.empty_like(b)
     dh0 = torch.empty((B, H, k), dtype=torch.float32, device=b.device) if need_dh0 else None
-    ws, nws = workspace(_b.MGS_OP_MATRIX_AFFINE_SCAN_BWD_RECOMPUTE, B, T, H, k, b.device)
+    ws, nws = workspace(_b.MGS_OP_MATRIX_AFFINE_SCAN_BWD_RECOMPUTE, B, T, H, k, b.device, stream)
     _b.mgs_matrix_affine_scan_bwd_recompute(A, b, h0, grad_h, dA, db, dh0, B, T, H, k, ws, nws, stream)
     return dA, db, dh0
 
@@ -88,7 +104,7 @@ def matrix_scan_fwd(A, out=None, stream=None):
     B, T, H, k, _ = A.shape
     _check(A, "A", (B, T, H, k, k))
     P = out if out is not None else torch.empty_like(A)
-    ws, nws = workspace(_b.MGS_OP_MATRIX_SCAN_FWD, B, T, H, k, A.device)
+    ws, nws = workspace(_b.MGS_OP_MATRIX_SCAN_FWD, B, T, H, k, A.device, stream)
     _b.mgs_matrix_scan_fwd(A, P, B, T, H, k, ws, nws, stream)
     return P
 
@@ -97,7 +113,7 @@ def matrix_scan_bwd(A, P, grad_P, stream=None):
     B, T, H, k, _ = A.shape
     _check(A, "A", (B, T, H, k, k)); _check(P, "P", A.shape); _check(grad_P, "grad_P", A.shape)
     dA = torch.empty_like(A)
-    ws, nws = workspace(_b.MGS_OP_MATRIX_SCAN_BWD, B, T, H, k, A.device)
+    ws, nws = workspace(_b.MGS_OP_MATRIX_SCAN_BWD, B, T, H, k, A.device, stream)
     _b.mgs_matrix_scan_bwd(A, P, grad_P, dA, B, T, H, k, ws, nws, stream)
     return dA
 
@@ -131,7 +147,7 @@ def parallel_scan_log_bwd(log_coeffs, log_values, log_h0, h, grad_h, stream=None
     dlv = torch.empty_like(log_values)
     dl0 = torch.empty_like(log_h0) if log_h0 is not None else None
     ws, nws = (None, 0) if h is not None else \
-        workspace(_b.MGS_OP_PARALLEL_SCAN_LOG_BWD, B, T, D, 0, log_coeffs.device)
+        workspace(_b.MGS_OP_PARALLEL_SCAN_LOG_BWD, B, T, D, 0, log_coeffs.device, stream)
     _b.mgs_parallel_scan_log_bwd(log_coeffs, log_values, log_h0, h, grad_h, dlc, dlv, dl0, B, T, D,
                                  ws, nws, stream)
     return dlc, dlv, dl0
@@ -152,7 +168,7 @@ def givens_affine_scan_fwd(theta, a, b, h0=None, stream=None):
     if h0 is not None:
         _check(h0, "h0", (B, H, k))
     h = torch.empty_like(b)
-    ws, nws = workspace(_b.MGS_OP_GIVENS_AFFINE_SCAN_FWD, B, T, H, k, b.device)
+    ws, nws = workspace(_b.MGS_OP_GIVENS_AFFINE_SCAN_FWD, B, T, H, k, b.device, stream)
     _b.mgs_givens_affine_scan_fwd(theta, a, b, h0, h, B, T, H, k, ws, nws, stream)
     return h
 
@@ -169,7 +185,7 @@ def givens_affine_scan_bwd(theta, a, h0, h, grad_h, need_dh0=True, stream=None):
     da = torch.empty_like(a) if a is not None else None
     db = torch.empty_like(h)
     dh0 = torch.empty((B, H, k), dtype=torch.float32, device=h.device) if need_dh0 else None
-    ws, nws = workspace(_b.MGS_OP_GIVENS_AFFINE_SCAN_BWD, B, T, H, k, h.device)
+    ws, nws = workspace(_b.MGS_OP_GIVENS_AFFINE_SCAN_BWD, B, T, H, k, h.device, stream)
     _b.mgs_givens_affine_scan_bwd(theta, a, h0, h, grad_h, dth, da, db, dh0, B, T, H, k, ws, nws, stream)
     return dth, da, db, dh0
 
@@ -179,7 +195,7 @@ def givens_matrix_scan_fwd(theta, k=GIVENS_K, stream=None):
     B, T, H, n = theta.shape
     _check(theta, "theta", (B, T, H, k * (k - 1) // 2))
     P = torch.empty((B, T, H, k, k), dtype=torch.float32, device=theta.device)
-    ws, nws = workspace(_b.MGS_OP_GIVENS_MATRIX_SCAN_FWD, B, T, H, k, theta.device)
+    ws, nws = workspace(_b.MGS_OP_GIVENS_MATRIX_SCAN_FWD, B, T, H, k, theta.device, stream)
     _b.mgs_givens_matrix_scan_fwd(theta, P, B, T, H, k, ws, nws, stream)
     return P
 
@@ -188,7 +204,7 @@ def givens_matrix_scan_bwd(theta, P, grad_P, stream=None):
     B, T, H, k, _ = P.shape
     _check(theta, "theta", (B, T, H, k * (k - 1) // 2)); _check(P, "P"); _check(grad_P, "grad_P", P.shape)
     dth = torch.empty_like(theta)
-    ws, nws = workspace(_b.MGS_OP_GIVENS_MATRIX_SCAN_BWD, B, T, H, k, theta.device)
+    ws, nws = workspace(_b.MGS_OP_GIVENS_MATRIX_SCAN_BWD, B, T, H, k, theta.device, stream)
     _b.mgs_givens_matrix_scan_bwd(theta, P, grad_P, dth, B, T, H, k, ws, nws, stream)
     return dth
 
@@ -204,7 +220,7 @@ def delta_scan_fwd(q, k, v, beta, S0=None, want_state=False, stream=None):
         _check(S0, "S0", (B, H, D, D))
     o = torch.empty_like(q)
     ST = torch.empty((B, H, D, D), dtype=torch.float32, device=q.device) if want_state else None
-    ws, nws = workspace(_b.MGS_OP_DELTA_SCAN_FWD, B, T, H, D, q.device)
+    ws, nws = workspace(_b.MGS_OP_DELTA_SCAN_FWD, B, T, H, D, q.device, stream)
     _b.mgs_delta_scan_fwd(q, k, v, beta, S0, o, ST, B, T, H, D, ws, nws, stream)
     return (o, ST) if want_state else o
 
@@ -217,7 +233,7 @@ def linear_scan_fwd(a, b, h0=None, stream=None):
     if h0 is not None:
         _check(h0, "h0", (B, D))
     h = torch.empty_like(b)
-    ws, nws = workspace(_b.MGS_OP_LINEAR_SCAN_FWD, B, T, D, 1, b.device)
+    ws, nws = workspace(_b.MGS_OP_LINEAR_SCAN_FWD, B, T, D, 1, b.device, stream)
     _b.mgs_linear_scan_fwd(a, b, h0, h, B, T, D, ws, nws, stream)
     return h
 
@@ -231,7 +247,7 @@ def linear_scan_bwd(a, h0, h, grad_h, need_dh0=True, stream=None):
         _check(h0, "h0", (B, D))
     da, db = torch.empty_like(a), torch.empty_like(a)
     dh0 = torch.empty((B, D), dtype=torch.float32, device=a.device) if need_dh0 else None
-    ws, nws = workspace(_b.MGS_OP_LINEAR_SCAN_BWD, B, T, D, 1, a.device)
+    ws, nws = workspace(_b.MGS_OP_LINEAR_SCAN_BWD, B, T, D, 1, a.device, stream)
     _b.mgs_linear_scan_bwd(a, h0, h, grad_h, da, db, dh0, B, T, D, ws, nws, stream)
     return da, db, dh0
 
@@ -272,16 +288,6 @@ def _head_strides(t, name):
     return st[:-1]
 
 
-def _on(stream, device):
-    """The context in which memory and copies belong to the call's stream (an address, a torch stream, or None: the
-    current one).  What is allocated in it may be dropped when the call returns: it goes back to that stream."""
-    if stream is None:
-        return contextlib.nullcontext()
-    if isinstance(stream, int):  # address 0: the default stream, for which torch has no external one
-        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
-    return torch.cuda.stream(stream)
-
-
 def _apart(t, stream):
     """t, or a dense copy of a broadcast t: the tensor-core kernels load through tensor maps, which have no
     zero strides, and the copy costs less than the kernel without them."""
@@ -320,14 +326,6 @@ def _attention_shape(q, k, v, g, scale, stream, grad_o=None):
         _head_strides(k, "k"), _head_strides(v, "v"), (0, 0, 1) if fixed else g.stride(),
         _head_strides(grad_o, "grad_o") if grad_o is not None else (0, 0, 0))
     return shape, (B, T, H, Hk, D), (q, k, v, grad_o)
-
-
-def _scratch(n, device, stream):
-    """n bytes of workspace that stay reserved until `stream` is done with them."""
-    if not n:
-        return None
-    with _on(stream, device):
-        return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 _increment_version = torch.autograd.graph.increment_version
