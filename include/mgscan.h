@@ -343,8 +343,9 @@ mgs_status mgs_delta_scan_fwd(const float *q, const float *k, const float *v, co
  * fp32 or bf16 (the dtype argument); sums, states and statistics are fp32.
  * ------------------------------------------------------------------------ */
 
-/* Element types. */
+/* Element types; the types of tokens. */
 enum { MGS_F32 = 0, MGS_BF16 = 1 };
+enum { MGS_I32 = 2, MGS_I64 = 3 };
 
 /* Sizes, types and strides of linear attention.  H value heads, Hk query/key
  * heads: Hk divides H, value head h reads query/key head h / (H / Hk).  Strides
@@ -462,6 +463,112 @@ size_t mgs_clip_grad_norm_workspace_size(int64_t count);
 mgs_status mgs_clip_grad_norm(const void *const *grads, void *const *outs, const int64_t *numels,
                               const int32_t *dtypes, int64_t count, float max_norm, float *norm, void *workspace,
                               size_t workspace_bytes, mgs_stream_t stream);
+
+/* Sizes, types and strides of the gated linear recurrence.  Strides are in
+ * elements, in the order batch, step; the D channels of a step are contiguous.
+ * Any stride >= 0; outputs are dense [B][T][D].  The vector kernels want channels
+ * in pairs: an even D, even strides, and tensors that start at multiples of two
+ * elements; others run slower ones. */
+typedef struct mgs_gated_shape {
+    int64_t B, T, D;
+    int32_t dtype;        /* of gate, value, h and their gradients            */
+    int32_t positive;     /* c = g(value) (nonzero), or c = value             */
+    int64_t gate_stride[2], value_stride[2];
+    int64_t gh_stride[2]; /* grad_h's: backward only                          */
+} mgs_gated_shape;
+
+/* The gated linear recurrence (minGRU) from its pre-activations, forward.  Per
+ * channel, with z = sigmoid(gate),
+ *     h_t = (1 - z_t) h_{t-1} + z_t c_t,   c = value, or c = g(value):
+ *     g(v) = v + 1/2 for v >= 0, sigmoid(v) below (minGRU's positive candidate),
+ * h_0 = h0 (zeros when NULL).  The state is fp32 throughout, h is rounded once.  A
+ * gate of -infinity masks the step: the state stays as it is, whatever the value,
+ * and the gradients of both are zero; +infinity starts the state anew from c.
+ * In: gate, value [B][T][D], h0 [B][D] fp32 (nullable).
+ * Out: h [B][T][D]; h_T [B][D] fp32 (nullable), the state after the last step;
+ *     carries [B][ceil(T / MGS_GATED_SPAN)][D] fp32 (nullable: only the backward
+ *     needs them), the state before each MGS_GATED_SPAN steps. */
+enum { MGS_GATED_SPAN = 64 };
+mgs_status mgs_gated_scan_fwd(const mgs_gated_shape *shape, const void *gate, const void *value, const float *h0,
+                              void *h, float *h_T, float *carries, mgs_stream_t stream);
+
+/* Its backward.  With a = 1 - z and L_t = dL/dh_t = grad_h_t + a_{t+1} L_{t+1},
+ * L_T = grad_h_T + grad_h's last:
+ *     d_value = L z c',  d_gate = L (c - h_{t-1}) z a,  d_h0 = a_1 L_1.
+ * h is rebuilt in fp32 from the carries.  In: carries as the forward left them,
+ * grad_h [B][T][D], grad_h_T [B][D] fp32 (nullable).  Out: d_gate, d_value
+ * [B][T][D], d_h0 [B][D] fp32 (nullable). */
+mgs_status mgs_gated_scan_bwd(const mgs_gated_shape *shape, const void *gate, const void *value, const float *carries,
+                              const void *grad_h, const float *grad_h_T, void *d_gate, void *d_value, float *d_h0,
+                              mgs_stream_t stream);
+
+/* One step of each of B sequences (shape->T = 1), their states in a cache
+ * [n_slots][D] fp32 that is updated in place; slots as in
+ * mgs_linear_attention_step.  Out: h [B][D], zero in an empty row. */
+mgs_status mgs_gated_scan_step(const mgs_gated_shape *shape, const void *gate, const void *value, float *state,
+                               const int32_t *slots, int64_t n_slots, void *h, mgs_stream_t stream);
+
+/* Sizes, types and strides of the norm of queries and keys.  Strides are in
+ * elements, in the order batch, step, head (positions: batch, step); the D
+ * elements of a head are contiguous.  Any stride >= 0; tensors that start at
+ * multiples of four elements, with strides that are so too, run the vector
+ * kernels, others slower ones.  Outputs are dense [B][T][heads][D]. */
+typedef struct mgs_qk_norm_shape {
+    int64_t B, T, Hq, Hk;
+    int64_t positions;    /* rows of the table                                */
+    int32_t D;            /* a multiple of 8, up to 256                       */
+    int32_t dtype;        /* of q, k, the weights and their gradients         */
+    int32_t rotary;       /* elements of a head that are turned: a multiple of 8, up to D (0: none) */
+    int32_t interleaved;  /* pairs 2 i and 2 i + 1 (nonzero), or i and i + rotary / 2 */
+    float eps;
+    int64_t q_stride[3], k_stride[3];
+    int64_t gq_stride[3], gk_stride[3]; /* the outputs' gradients': backward only */
+    int64_t pos_stride[2];
+} mgs_qk_norm_shape;
+
+/* RMS norm of queries and keys for each head, and their positions' rotation.  For
+ * each head x of D elements, n = x weight / sqrt(mean(x^2) + eps); then the pairs
+ * (n1, n2) of its `rotary` first elements are turned by their position's angles,
+ *     y1 = n1 cos - n2 sin,  y2 = n2 cos + n1 sin,
+ * whose cosines and sines are a row of the table: rotary / 2 cosines, then as many
+ * sines.  All in fp32, rounded once.
+ * In: q [B][T][Hq][D], k [B][T][Hk][D] (Hk may be 0), q_weight, k_weight [D] (each
+ *     nullable: ones), table [positions][rotary] fp32 (16-byte aligned; NULL with
+ *     rotary = 0), token_positions [B][T] (nullable: 0..T-1 in each sequence,
+ *     which needs positions >= T).  A position outside the table marks an empty
+ *     row: its outputs and gradients are zero.
+ * Out: yq [B][T][Hq][D], yk [B][T][Hk][D]. */
+mgs_status mgs_qk_norm_fwd(const mgs_qk_norm_shape *shape, const void *q, const void *k, const void *q_weight,
+                           const void *k_weight, const float *table, const int32_t *token_positions, void *yq,
+                           void *yk, mgs_stream_t stream);
+
+size_t mgs_qk_norm_bwd_workspace_size(const mgs_qk_norm_shape *shape);
+
+/* Its backward: with dn = grad_y turned back and hat = x / sqrt(mean(x^2) + eps),
+ *     dx = (weight dn - hat mean(weight dn hat)) / sqrt(mean(x^2) + eps),
+ *     dweight = sum over tokens and heads of dn hat (in a fixed order).
+ * Out: dq, dk (dense), dq_weight, dk_weight [D] (each nullable). */
+mgs_status mgs_qk_norm_bwd(const mgs_qk_norm_shape *shape, const void *q, const void *k, const void *q_weight,
+                           const void *k_weight, const void *grad_yq, const void *grad_yk, const float *table,
+                           const int32_t *token_positions, void *dq, void *dk, void *dq_weight, void *dk_weight,
+                           void *workspace, size_t workspace_bytes, mgs_stream_t stream);
+
+/* Embedding: out[n] = scale weight[tokens[n]], rounded once.  tokens [N] of
+ * token_type MGS_I32 or MGS_I64; a token outside 0..V-1 marks an empty row, whose
+ * output is zero.  weight [V][D], out [N][D] dense; tensors whose rows start at
+ * multiples of 16 bytes are the fastest. */
+mgs_status mgs_embedding_fwd(const void *tokens, int token_type, const void *weight, float scale, void *out,
+                             int64_t N, int64_t V, int64_t D, int dtype, mgs_stream_t stream);
+
+size_t mgs_embedding_bwd_workspace_size(int64_t N, int64_t V, int64_t D);
+
+/* Its table's gradient, all rows of it: dweight[v] = scale times the sum of
+ * grad[n] over the n with tokens[n] = v, zero where there is none.  Sums are fp32,
+ * in an order that the tokens alone decide.  Rows of grad are grad_stride (>= 0)
+ * elements apart. */
+mgs_status mgs_embedding_bwd(const void *tokens, int token_type, const void *grad, int64_t grad_stride, float scale,
+                             void *dweight, int64_t N, int64_t V, int64_t D, int dtype, void *workspace,
+                             size_t workspace_bytes, mgs_stream_t stream);
 
 /* Synchronises `stream`, then reads and clears the current device's error
  * word.  Returns MGS_ERR_TIMEOUT if a kernel's bounded wait gave up since the

@@ -42,6 +42,9 @@ MGS_OP_MATRIX_AFFINE_SCAN_BWD_RECOMPUTE = 14
 
 MGS_F32 = 0
 MGS_BF16 = 1
+MGS_I32 = 2
+MGS_I64 = 3
+GATED_SPAN = 64  # MGS_GATED_SPAN in include/mgscan.h
 
 
 class MGSError(RuntimeError):
@@ -91,6 +94,15 @@ _SIGNATURES = {
     "mgs_rms_norm_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _vp, _sz, _vp]),
     "mgs_clip_grad_norm_workspace_size": (_sz, [_i64]),
     "mgs_clip_grad_norm": (_int, [_vp, _vp, _vp, _vp, _i64, _flt, _vp, _vp, _sz, _vp]),
+    "mgs_gated_scan_fwd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "mgs_gated_scan_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "mgs_gated_scan_step": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp]),
+    "mgs_qk_norm_fwd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "mgs_qk_norm_bwd_workspace_size": (_sz, [_vp]),
+    "mgs_qk_norm_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "mgs_embedding_fwd": (_int, [_vp, _int, _vp, _flt, _vp, _i64, _i64, _i64, _int, _vp]),
+    "mgs_embedding_bwd_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "mgs_embedding_bwd": (_int, [_vp, _int, _vp, _i64, _flt, _vp, _i64, _i64, _i64, _int, _vp, _sz, _vp]),
     "mgs_check": (_int, [_vp]),
     "mgs_set_wait_timeout_ns": (None, [ctypes.c_uint64]),
     "mgs_debug_wait_flag": (_int, [_vp, _vp]),
@@ -305,6 +317,70 @@ def mgs_clip_grad_norm(grads, outs, numels, dtypes, max_norm, norm, workspace=No
     return _call("mgs_clip_grad_norm", struct.pack(f"{n}Q", *grads), struct.pack(f"{n}Q", *outs),
                  struct.pack(f"{n}q", *numels), struct.pack(f"{n}i", *dtypes), n, max_norm, _ptr(norm),
                  _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+_GATED_SHAPE = struct.Struct("<3q2i6q")
+
+
+def mgs_gated_shape(B, T, D, dtype, positive, gate_stride, value_stride, gh_stride=(0, 0)):
+    """The C struct of that name, as bytes.  Strides: (batch, step) in elements."""
+    return _GATED_SHAPE.pack(B, T, D, dtype, positive, *gate_stride, *value_stride, *gh_stride)
+
+
+def mgs_gated_scan_fwd(shape, gate, value, h0, h, h_T, carries, stream=None):
+    return _call("mgs_gated_scan_fwd", shape, _ptr(gate), _ptr(value), _ptr(h0), _ptr(h), _ptr(h_T), _ptr(carries),
+                 _stream(stream))
+
+
+def mgs_gated_scan_bwd(shape, gate, value, carries, grad_h, grad_h_T, d_gate, d_value, d_h0, stream=None):
+    return _call("mgs_gated_scan_bwd", shape, _ptr(gate), _ptr(value), _ptr(carries), _ptr(grad_h), _ptr(grad_h_T),
+                 _ptr(d_gate), _ptr(d_value), _ptr(d_h0), _stream(stream))
+
+
+def mgs_gated_scan_step(shape, gate, value, state, slots, n_slots, h, stream=None):
+    return _call("mgs_gated_scan_step", shape, _ptr(gate), _ptr(value), _ptr(state), _ptr(slots), n_slots, _ptr(h),
+                 _stream(stream))
+
+
+_QK_NORM_SHAPE = struct.Struct("<5q4if4x14q")
+
+
+def mgs_qk_norm_shape(B, T, Hq, Hk, positions, D, dtype, rotary, interleaved, eps, q_stride, k_stride,
+                      gq_stride=_NO_STRIDES, gk_stride=_NO_STRIDES, pos_stride=(0, 0)):
+    """The C struct of that name, as bytes.  Strides: (batch, step, head), positions (batch, step), in elements."""
+    return _QK_NORM_SHAPE.pack(B, T, Hq, Hk, positions, D, dtype, rotary, interleaved, eps, *q_stride, *k_stride,
+                               *gq_stride, *gk_stride, *pos_stride)
+
+
+def mgs_qk_norm_fwd(shape, q, k, q_weight, k_weight, table, token_positions, yq, yk, stream=None):
+    return _call("mgs_qk_norm_fwd", shape, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(table),
+                 _ptr(token_positions), _ptr(yq), _ptr(yk), _stream(stream))
+
+
+def mgs_qk_norm_bwd_workspace_size(shape):
+    return int(lib().mgs_qk_norm_bwd_workspace_size(shape))
+
+
+def mgs_qk_norm_bwd(shape, q, k, q_weight, k_weight, grad_yq, grad_yk, table, token_positions, dq, dk, dq_weight,
+                    dk_weight, workspace=None, workspace_bytes=0, stream=None):
+    return _call("mgs_qk_norm_bwd", shape, _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(grad_yq),
+                 _ptr(grad_yk), _ptr(table), _ptr(token_positions), _ptr(dq), _ptr(dk), _ptr(dq_weight),
+                 _ptr(dk_weight), _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def mgs_embedding_fwd(tokens, token_type, weight, scale, out, N, V, D, dtype, stream=None):
+    return _call("mgs_embedding_fwd", _ptr(tokens), token_type, _ptr(weight), scale, _ptr(out), N, V, D, dtype,
+                 _stream(stream))
+
+
+def mgs_embedding_bwd_workspace_size(N, V, D):
+    return int(lib().mgs_embedding_bwd_workspace_size(N, V, D))
+
+
+def mgs_embedding_bwd(tokens, token_type, grad, grad_stride, scale, dweight, N, V, D, dtype, workspace=None,
+                      workspace_bytes=0, stream=None):
+    return _call("mgs_embedding_bwd", _ptr(tokens), token_type, _ptr(grad), grad_stride, scale, _ptr(dweight), N, V, D,
+                 dtype, _ptr(workspace), workspace_bytes, _stream(stream))
 
 
 def mgs_check(stream=None):

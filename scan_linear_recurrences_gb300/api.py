@@ -506,6 +506,229 @@ def clip_grad_norm(grads, max_norm, out=None, stream=None):
     return norm
 
 
+# ---------------------------------------------------------------- gated linear recurrence
+def _there(device):
+    """The context in which calls go to this device (the library launches on the current one)."""
+    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _inner(t, name):
+    """Strides of all but the last dimension, which is contiguous."""
+    st = t.stride()
+    if st[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return st[:-1]
+
+
+def _gated_shape(gate, value, positive, grad_h=None):
+    if not isinstance(gate, torch.Tensor) or gate.dim() != 3:
+        raise ValueError("gate must be a [B,T,D] tensor")
+    _check_typed(gate, "gate", None, None, dense=False)
+    _check_typed(value, "value", gate.shape, gate.dtype, dense=False, device=gate.device)
+    if grad_h is not None:
+        _check_typed(grad_h, "grad_h", gate.shape, gate.dtype, dense=False, device=gate.device)
+    B, T, D = gate.shape
+    return _b.mgs_gated_shape(B, T, D, _DTYPES[gate.dtype], bool(positive), _inner(gate, "gate"), _inner(value, "value"),
+                              _inner(grad_h, "grad_h") if grad_h is not None else (0, 0))
+
+
+def gated_scan_fwd(gate, value, h0=None, positive=True, want_carries=False, stream=None):
+    """The gated linear recurrence (minGRU) from its pre-activations: with z = sigmoid(gate),
+    h_t = (1 - z_t) h_{t-1} + z_t c_t, c = g(value) (positive: v + 1/2 for v >= 0, sigmoid(v) below) or value itself.
+
+    gate, value [B,T,D] (fp32 or bf16, any strides whose channels are contiguous, so halves of one product too),
+    h0 [B,D] fp32 or None.  A gate of -inf masks its step, whatever its value; +inf starts the state anew.  The
+    state is fp32, h is rounded once.  Returns (h [B,T,D], h_T [B,D] fp32), and the carries that gated_scan_bwd
+    takes when want_carries."""
+    shape, (B, T, D), dev = _gated_shape(gate, value, positive), gate.shape, gate.device
+    if h0 is not None:
+        _check_typed(h0, "h0", (B, D), torch.float32, device=dev)
+    h = torch.empty((B, T, D), dtype=gate.dtype, device=dev)
+    hT = torch.empty((B, D), dtype=torch.float32, device=dev)
+    carries = torch.empty((B, -(-T // _b.GATED_SPAN), D), dtype=torch.float32, device=dev) if want_carries else None
+    with _there(dev):
+        _b.mgs_gated_scan_fwd(shape, gate, value, h0, h, hT, carries, stream)
+    return (h, hT, carries) if want_carries else (h, hT)
+
+
+def gated_scan_bwd(gate, value, carries, grad_h, grad_hT=None, positive=True, need_dh0=True, stream=None):
+    """Gradients of gated_scan_fwd for L = <grad_h, h> + <grad_hT, h_T>: (dgate, dvalue, dh0), dh0 None unless
+    needed.  carries: the forward's; h itself is rebuilt from them."""
+    shape, (B, T, D), dev = _gated_shape(gate, value, positive, grad_h), gate.shape, gate.device
+    _check_typed(carries, "carries", (B, -(-T // _b.GATED_SPAN), D), torch.float32, device=dev)
+    if grad_hT is not None:
+        _check_typed(grad_hT, "grad_hT", (B, D), torch.float32, device=dev)
+    dgate = torch.empty((B, T, D), dtype=gate.dtype, device=dev)
+    dvalue = torch.empty_like(dgate)
+    dh0 = torch.empty((B, D), dtype=torch.float32, device=dev) if need_dh0 else None
+    with _there(dev):
+        _b.mgs_gated_scan_bwd(shape, gate, value, carries, grad_h, grad_hT, dgate, dvalue, dh0, stream)
+    return dgate, dvalue, dh0
+
+
+def gated_scan_step(gate, value, state, slots=None, positive=True, out=None, stream=None):
+    """One step of each of B sequences: gate, value [B,D], the cache of states [N,D] fp32, updated in place.
+    slots [B] int32: each sequence's place in the cache (None: b itself); a place outside 0..N-1 marks an empty row,
+    whose output is 0.  Returns h [B,D]."""
+    if not isinstance(gate, torch.Tensor) or gate.dim() != 2:
+        raise ValueError("gate must be a [B,D] tensor")
+    (B, D), dt, dev = gate.shape, gate.dtype, gate.device
+    _check_typed(gate, "gate", None, None, dense=False)
+    _check_typed(value, "value", gate.shape, dt, dense=False, device=dev)
+    if not isinstance(state, torch.Tensor) or state.dim() != 2:
+        raise ValueError("state must be a [N,D] tensor")
+    N = state.shape[0]
+    _check_typed(state, "state", (N, D), torch.float32, device=dev)
+    if slots is not None:
+        _check_typed(slots, "slots", (B,), torch.int32, device=dev)
+    elif N < B:
+        raise ValueError(f"{B} sequences without slots need a cache of as many states, not {N}")
+    written = (state,) if out is None else (state, out)
+    if out is None:
+        out = torch.empty((B, D), dtype=dt, device=dev)
+    else:
+        _check_typed(out, "out", (B, D), dt, device=dev)
+    shape = _b.mgs_gated_shape(B, 1, D, _DTYPES[dt], bool(positive), (*_inner(gate, "gate"), 0),
+                               (*_inner(value, "value"), 0))
+    with _there(dev):
+        _b.mgs_gated_scan_step(shape, gate, value, state, slots, N, out, stream)
+    _written(written)
+    return out
+
+
+# ---------------------------------------------------------------- norm of queries and keys, with the position's rotation
+def rotary_table(positions, rotary, base=10000.0, device="cuda"):
+    """The cosines and sines [positions, rotary] fp32 that qk_norm takes: of p base^(-2 i / rotary) for position p and
+    pair i, computed in 64 bits (an angle of a far position in 32 bits is off by itself times 6e-8)."""
+    if rotary % 2:
+        raise ValueError("rotary must be even")
+    i = torch.arange(rotary // 2, dtype=torch.float64, device=device)
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * base ** (-2 * i / max(rotary, 1))
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def _qk_shape(q, k, q_weight, k_weight, table, positions, eps, interleaved, grad_q=None, grad_k=None):
+    """The checked arguments as the C struct.  One token of each sequence ([B,H,D]) is T = 1."""
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+        raise ValueError("q must be a [B,T,Hq,D] or [B,Hq,D] tensor")
+    dt, dev, D, lead = q.dtype, q.device, q.shape[-1], q.shape[:-2]
+    _check_typed(q, "q", None, None, dense=False)
+    if not isinstance(k, torch.Tensor) or k.dim() != q.dim():
+        raise ValueError("k must have as many dimensions as q")
+    _check_typed(k, "k", (*lead, k.shape[-2], D), dt, dense=False, device=dev)
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _check_typed(w, name, (D,), dt, device=dev)
+    if D % 8 or not 8 <= D <= 256:
+        raise ValueError(f"heads of {D}: multiples of 8 up to 256 are supported")
+    rows, R = 0, 0
+    if table is not None:
+        if not isinstance(table, torch.Tensor) or table.dim() != 2:
+            raise ValueError("table must be a [positions, rotary] tensor")
+        rows, R = table.shape
+        _check_typed(table, "table", None, torch.float32, device=dev)
+        if R % 8 or not 8 <= R <= D:
+            raise ValueError(f"{R} rotated elements of heads of {D}: multiples of 8 up to {D} are supported")
+        if positions is None and rows < (lead[1] if len(lead) == 2 else 1):
+            raise ValueError(f"{lead[1] if len(lead) == 2 else 1} positions need a table of as many rows, not {rows}")
+    if positions is not None:
+        if table is None:
+            raise ValueError("positions without a table")
+        _check_typed(positions, "positions", lead, torch.int32, dense=False, device=dev)
+    for g, like, name in ((grad_q, q, "grad_q"), (grad_k, k, "grad_k")):
+        if g is not None:
+            _check_typed(g, name, like.shape, dt, dense=False, device=dev)
+    one = len(lead) == 1
+
+    def strides(t, name):
+        st = _inner(t, name) if t is not None else (0,) * (len(lead) + 1)
+        return (st[0], 0, st[1]) if one else st
+
+    at = (0, 0) if positions is None else (*positions.stride(), 0) if one else positions.stride()
+    return _b.mgs_qk_norm_shape(lead[0], 1 if one else lead[1], q.shape[-2], k.shape[-2], rows, D, _DTYPES[dt], R,
+                                bool(interleaved), eps, strides(q, "q"), strides(k, "k"), strides(grad_q, "grad_q"),
+                                strides(grad_k, "grad_k"), at)
+
+
+def qk_norm_fwd(q, k, q_weight=None, k_weight=None, table=None, positions=None, eps=1e-6, interleaved=False, stream=None):
+    """RMS norm of queries and keys over each head's D elements, times the weights [D] (None: ones), then the rotation
+    of their positions, in one pass: what linear_attention takes.
+
+    q [B,T,Hq,D], k [B,T,Hk,D], or [B,H,D] for one token of each sequence (fp32 or bf16, D a multiple of 8 up to 256, any
+    strides whose heads are contiguous).  table: rotary_table's, as many elements of a head turned as it has columns
+    (None: none); pairs are elements i and i + rotary / 2, or 2 i and 2 i + 1 (interleaved).  positions [B,T] or [B]
+    int32 (None: 0..T-1); one outside the table marks an empty row, whose outputs and gradients are 0.  Sums and
+    rotations are fp32, outputs are rounded once.  Returns dense (q, k)."""
+    shape = _qk_shape(q, k, q_weight, k_weight, table, positions, eps, interleaved)
+    yq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    yk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    with _there(q.device):
+        _b.mgs_qk_norm_fwd(shape, q, k, q_weight, k_weight, table, positions, yq, yk, stream)
+    return yq, yk
+
+
+def qk_norm_bwd(q, k, q_weight, k_weight, grad_q, grad_k, table=None, positions=None, eps=1e-6, interleaved=False,
+                stream=None):
+    """Gradients of qk_norm_fwd: (dq, dk, dq_weight, dk_weight), those of weights that are None None."""
+    if grad_q is None or grad_k is None:
+        raise ValueError("grad_q and grad_k must be tensors")
+    shape = _qk_shape(q, k, q_weight, k_weight, table, positions, eps, interleaved, grad_q, grad_k)
+    dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    dqw, dkw = (None if w is None else torch.empty_like(w) for w in (q_weight, k_weight))
+    n = _b.mgs_qk_norm_bwd_workspace_size(shape)
+    with _there(q.device):
+        _b.mgs_qk_norm_bwd(shape, q, k, q_weight, k_weight, grad_q, grad_k, table, positions, dq, dk, dqw, dkw,
+                           _scratch(n, q.device, stream), n, stream)
+    return dq, dk, dqw, dkw
+
+
+# ---------------------------------------------------------------- embedding
+_TOKENS = {torch.int32: _b.MGS_I32, torch.int64: _b.MGS_I64}
+
+
+def _check_tokens(tokens, device=None):
+    if not isinstance(tokens, torch.Tensor) or tokens.dtype not in _TOKENS:
+        raise ValueError("tokens must be an int32 or int64 tensor")
+    _check_typed(tokens, "tokens", None, tokens.dtype, device=device)
+
+
+def embedding_fwd(tokens, weight, scale=1.0, stream=None):
+    """scale * weight[tokens]: tokens [...] int32 or int64, weight [V,D] fp32 or bf16.  A token outside 0..V-1 marks an
+    empty row, which is 0.  Returns [..., D]."""
+    _check_typed(weight, "weight", None, None)
+    if weight.dim() != 2:
+        raise ValueError("weight must be a [V,D] tensor")
+    _check_tokens(tokens, weight.device)
+    V, D = weight.shape
+    out = torch.empty((*tokens.shape, D), dtype=weight.dtype, device=weight.device)
+    with _there(weight.device):
+        _b.mgs_embedding_fwd(tokens, _TOKENS[tokens.dtype], weight, scale, out, tokens.numel(), V, D,
+                             _DTYPES[weight.dtype], stream)
+    return out
+
+
+def embedding_bwd(tokens, grad, V, scale=1.0, stream=None):
+    """The gradient [V,D] of embedding_fwd's weight, dense: scale times the sum of grad's rows over each token's places
+    (fp32 sums, in an order that the tokens alone decide).  grad [..., D]: rows a fixed distance apart."""
+    _check_typed(grad, "grad", None, None, dense=False)
+    _check_tokens(tokens, grad.device)
+    if grad.dim() != tokens.dim() + 1 or grad.shape[:-1] != tokens.shape:
+        raise ValueError(f"grad has shape {tuple(grad.shape)}, expected {(*tokens.shape, 'D')}")
+    N, D = tokens.numel(), grad.shape[-1]
+    try:
+        rows = grad if grad.dim() == 2 else grad.view(N, D)
+    except RuntimeError:
+        raise ValueError("grad must have rows a fixed distance apart") from None
+    apart, = _inner(rows, "grad")
+    dW = torch.empty((V, D), dtype=grad.dtype, device=grad.device)
+    n = _b.mgs_embedding_bwd_workspace_size(N, V, D)
+    with _there(grad.device):
+        _b.mgs_embedding_bwd(tokens, _TOKENS[tokens.dtype], rows, apart, scale, dW, N, V, D, _DTYPES[grad.dtype],
+                             _scratch(n, grad.device, stream), n, stream)
+    return dW
+
+
 # ---------------------------------------------------------------- autograd wrappers
 class MatrixAffineScan(torch.autograd.Function):
     """h = matrix_affine_scan(A, b, h0) with the library's fused backward;
@@ -660,6 +883,68 @@ class RMSNorm(torch.autograd.Function):
         return dx, dw, dx if ctx.has_residual else None, None
 
 
+def _dense_inner(t):
+    """t itself where its last dimension is contiguous, else a dense copy."""
+    return t if t.stride(-1) == 1 else t.contiguous()
+
+
+def _zeros_like_rows(t):
+    """Zeros of t's shape, one row of them in memory."""
+    return torch.zeros(t.shape[-1], dtype=t.dtype, device=t.device).expand(t.shape)
+
+
+class GatedScan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, gate, value, h0=None, positive=True):
+        h0 = h0.contiguous() if h0 is not None else None
+        h, hT, carries = gated_scan_fwd(gate, value, h0, positive, want_carries=True)
+        ctx.save_for_backward(gate, value, carries)
+        ctx.positive, ctx.has_h0 = positive, h0 is not None
+        ctx.set_materialize_grads(False)
+        return h, hT
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_h, grad_hT):
+        gate, value, carries = ctx.saved_tensors
+        grad_h = _zeros_like_rows(gate) if grad_h is None else _dense_inner(grad_h)
+        grad_hT = grad_hT.contiguous() if grad_hT is not None else None
+        dgate, dvalue, dh0 = gated_scan_bwd(gate, value, carries, grad_h, grad_hT, ctx.positive, ctx.has_h0)
+        return dgate, dvalue, dh0, None
+
+
+class QKNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, table, positions, eps, interleaved):
+        ctx.save_for_backward(q, k, q_weight, k_weight, table, positions)
+        ctx.eps, ctx.interleaved = eps, interleaved
+        ctx.set_materialize_grads(False)
+        return qk_norm_fwd(q, k, q_weight, k_weight, table, positions, eps, interleaved)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_q, grad_k):
+        q, k, q_weight, k_weight, table, positions = ctx.saved_tensors
+        grad_q, grad_k = (_zeros_like_rows(x) if g is None else _dense_inner(g) for g, x in ((grad_q, q), (grad_k, k)))
+        grads = qk_norm_bwd(q, k, q_weight, k_weight, grad_q, grad_k, table, positions, ctx.eps, ctx.interleaved)
+        return *grads, None, None, None, None
+
+
+class Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, tokens, weight, scale=1.0):
+        tokens = tokens.contiguous()
+        ctx.save_for_backward(tokens)
+        ctx.V, ctx.scale = weight.shape[0], scale
+        return embedding_fwd(tokens, weight, scale)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        tokens, = ctx.saved_tensors
+        return None, embedding_bwd(tokens, grad.contiguous(), ctx.V, ctx.scale), None
+
+
 def givens_affine_scan(theta, a, b, h0=None):
     """GivensMinGRU's angle-fused recurrence h_t = G(theta_t) diag(a_t) h_{t-1} + b_t (a may be None)."""
     return GivensAffineScan.apply(theta, a, b, h0)
@@ -702,3 +987,18 @@ def linear_attention(q, k, v, g, S0=None, scale=None):
 def rms_norm(x, weight, residual=None, eps=1e-6):
     """RMS norm over the last dimension, with gradients: y, or (y, r) with r = x + residual."""
     return RMSNorm.apply(x, weight, residual, eps)
+
+
+def gated_scan(gate, value, h0=None, positive=True):
+    """The gated linear recurrence (minGRU) from its pre-activations, with gradients: (h, h_T); see gated_scan_fwd."""
+    return GatedScan.apply(_dense_inner(gate), _dense_inner(value), h0, positive)
+
+
+def qk_norm(q, k, q_weight=None, k_weight=None, table=None, positions=None, eps=1e-6, interleaved=False):
+    """Norm of queries and keys for each head with their positions' rotation, with gradients: (q, k); see qk_norm_fwd."""
+    return QKNorm.apply(_dense_inner(q), _dense_inner(k), q_weight, k_weight, table, positions, eps, interleaved)
+
+
+def embedding(tokens, weight, scale=1.0):
+    """scale * weight[tokens], with the gradient of weight; see embedding_fwd."""
+    return Embedding.apply(tokens, weight, scale)

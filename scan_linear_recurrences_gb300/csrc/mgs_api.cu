@@ -1021,4 +1021,246 @@ mgs_status mgs_clip_grad_norm(const void *const *grads, void *const *outs, const
                                       reinterpret_cast<cudaStream_t>(stream)));
 }
 
+static cudaStream_t cs_of(mgs_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+
+// ---------------------------------------------------------------- gated linear recurrence
+struct GatedSizes {
+    int64_t n, gate, value, gh, state, carries;  // bytes: dense, spans of the strided inputs, [B,D] and the carries in fp32
+};
+
+static mgs_status gated_sizes(const mgs_gated_shape *sh, bool with_gh, GatedSizes *z) {
+    if (sh == nullptr || sh->B < 0 || sh->T < 0 || sh->D < 0) return MGS_ERR_INVALID_ARG;
+    const int es = esize(sh->dtype);
+    if (es == 0) return MGS_ERR_UNSUPPORTED;
+    int64_t bt, n, bd;
+    if (!mul_ok(sh->B, sh->T, &bt) || !mul_ok(bt, sh->D, &n) || !mul_ok(sh->B, sh->D, &bd) || n > INT64_MAX / 64 ||
+        bd > INT64_MAX / 64)
+        return MGS_ERR_INVALID_ARG;
+    // 32-bit grids and steps
+    if (sh->T > INT32_MAX / 2 || sh->D > INT32_MAX / 2 || sh->B > INT32_MAX || bd > (int64_t(1) << 34))
+        return MGS_ERR_UNSUPPORTED;
+    *z = {n * es, 0, 0, 0, bd * 4, sh->B * ((sh->T + MGS_GATED_SPAN - 1) / MGS_GATED_SPAN) * sh->D * 4};
+    if (n == 0) return MGS_OK;
+    auto span = [&](const int64_t (&st)[2], int64_t *out) {
+        const int64_t s3[3] = {st[0], st[1], 0};
+        return span_of(s3, sh->B, sh->T, 1, sh->D, es, es, out);
+    };
+    if (!span(sh->gate_stride, &z->gate) || !span(sh->value_stride, &z->value) ||
+        (with_gh && !span(sh->gh_stride, &z->gh)))
+        return MGS_ERR_UNSUPPORTED;
+    return MGS_OK;
+}
+// T = 0: one [B,D] in fp32 is another, or zeros
+static mgs_status pass_state(float *out, const float *in, int64_t bytes, cudaStream_t cs) {
+    if (out == nullptr || bytes == 0) return MGS_OK;
+    if (!aligned4(out) || !aligned4(in)) return MGS_ERR_UNSUPPORTED;
+    if (!apart({{out, bytes}}, {{in, bytes}})) return MGS_ERR_INVALID_ARG;
+    return from_cuda(in ? cudaMemcpyAsync(out, in, size_t(bytes), cudaMemcpyDeviceToDevice, cs)
+                        : cudaMemsetAsync(out, 0, size_t(bytes), cs));
+}
+
+mgs_status mgs_gated_scan_fwd(const mgs_gated_shape *shape, const void *gate, const void *value, const float *h0,
+                              void *h, float *h_T, float *carries, mgs_stream_t stream) {
+    GatedSizes z;
+    mgs_status st = gated_sizes(shape, false, &z);
+    if (st != MGS_OK) return st;
+    const cudaStream_t cs = cs_of(stream);
+    if (z.n == 0) return pass_state(h_T, h0, z.state, cs);
+    if ((st = typed_ptrs(esize(shape->dtype), {gate, value, h}, {})) != MGS_OK) return st;
+    if ((st = typed_ptrs(4, {}, {h0, h_T, carries})) != MGS_OK) return st;
+    if (!apart({{h, z.n}, {h_T, z.state}, {carries, z.carries}}, {{gate, z.gate}, {value, z.value}, {h0, z.state}}))
+        return MGS_ERR_INVALID_ARG;
+    return from_cuda(mgs::launch_gated_fwd(*shape, gate, value, h0, h, h_T, carries, cs));
+}
+
+mgs_status mgs_gated_scan_bwd(const mgs_gated_shape *shape, const void *gate, const void *value, const float *carries,
+                              const void *grad_h, const float *grad_h_T, void *d_gate, void *d_value, float *d_h0,
+                              mgs_stream_t stream) {
+    GatedSizes z;
+    mgs_status st = gated_sizes(shape, true, &z);
+    if (st != MGS_OK) return st;
+    const cudaStream_t cs = cs_of(stream);
+    if (z.n == 0) return pass_state(d_h0, grad_h_T, z.state, cs);
+    if ((st = typed_ptrs(esize(shape->dtype), {gate, value, grad_h, d_gate, d_value}, {})) != MGS_OK) return st;
+    if ((st = typed_ptrs(4, {carries}, {grad_h_T, d_h0})) != MGS_OK) return st;
+    if (!apart({{d_gate, z.n}, {d_value, z.n}, {d_h0, z.state}},
+               {{gate, z.gate}, {value, z.value}, {carries, z.carries}, {grad_h, z.gh}, {grad_h_T, z.state}}))
+        return MGS_ERR_INVALID_ARG;
+    return from_cuda(mgs::launch_gated_bwd(*shape, gate, value, carries, grad_h, grad_h_T, d_gate, d_value, d_h0, cs));
+}
+
+mgs_status mgs_gated_scan_step(const mgs_gated_shape *shape, const void *gate, const void *value, float *state,
+                               const int32_t *slots, int64_t n_slots, void *h, mgs_stream_t stream) {
+    GatedSizes z;
+    if (shape == nullptr || shape->T != 1 || n_slots < 0) return MGS_ERR_INVALID_ARG;
+    mgs_status st = gated_sizes(shape, false, &z);
+    if (st != MGS_OK) return st;
+    if (z.n == 0) return MGS_OK;
+    if ((st = typed_ptrs(esize(shape->dtype), {gate, value, h}, {})) != MGS_OK) return st;
+    if ((st = typed_ptrs(4, {state}, {slots})) != MGS_OK) return st;
+    if (slots == nullptr && n_slots < shape->B) return MGS_ERR_INVALID_ARG;
+    int64_t ns;
+    if (!mul_ok(n_slots, shape->D * 4, &ns) || ns > INT64_MAX / 64) return MGS_ERR_INVALID_ARG;
+    if (!apart({{h, z.n}, {state, ns}}, {{gate, z.gate}, {value, z.value}, {slots, slots ? shape->B * 4 : 0}}))
+        return MGS_ERR_INVALID_ARG;
+    return from_cuda(mgs::launch_gated_step(*shape, gate, value, state, slots, n_slots, h, cs_of(stream)));
+}
+
+// ---------------------------------------------------------------- norm of queries and keys
+struct QkSizes {
+    int64_t q, k, q_span, k_span, gq_span, gk_span, table, pos;  // bytes
+};
+
+static mgs_status qk_sizes(const mgs_qk_norm_shape *sh, bool bwd, bool positions, QkSizes *z) {
+    if (sh == nullptr || sh->B < 0 || sh->T < 0 || sh->Hq < 0 || sh->Hk < 0 || sh->positions < 0)
+        return MGS_ERR_INVALID_ARG;
+    const int es = esize(sh->dtype);
+    if (es == 0 || sh->D <= 0 || sh->D > 256 || sh->D % 8 != 0 || sh->rotary < 0 || sh->rotary > sh->D ||
+        sh->rotary % 8 != 0)
+        return MGS_ERR_UNSUPPORTED;
+    int64_t bt, nq, nk;
+    if (!mul_ok(sh->B, sh->T, &bt) || !mul_ok(bt, sh->Hq, &nq) || !mul_ok(bt, sh->Hk, &nk) ||
+        nq > INT64_MAX / (64 * 256 * 4) || nk > INT64_MAX / (64 * 256 * 4) || sh->positions > INT64_MAX / (64 * 256 * 4))
+        return MGS_ERR_INVALID_ARG;
+    // 32-bit grids; positions are 32-bit
+    if (sh->Hq > INT32_MAX / 2 || sh->Hk > INT32_MAX / 2 || bt > (int64_t(1) << 40)) return MGS_ERR_UNSUPPORTED;
+    *z = {nq * sh->D * es, nk * sh->D * es, 0, 0, 0, 0, sh->positions * sh->rotary * 4, 0};
+    if (nq + nk == 0) return MGS_OK;
+    auto span = [&](const int64_t (&st)[3], int64_t H, int64_t *out) {
+        return H == 0 || span_of(st, sh->B, sh->T, H, sh->D, es, es, out);
+    };
+    if (!span(sh->q_stride, sh->Hq, &z->q_span) || !span(sh->k_stride, sh->Hk, &z->k_span) ||
+        (bwd && (!span(sh->gq_stride, sh->Hq, &z->gq_span) || !span(sh->gk_stride, sh->Hk, &z->gk_span))))
+        return MGS_ERR_UNSUPPORTED;
+    if (sh->rotary > 0 && positions) {
+        const int64_t st[3] = {sh->pos_stride[0], sh->pos_stride[1], 0};
+        if (!span_of(st, sh->B, sh->T, 1, 1, 4, 4, &z->pos)) return MGS_ERR_UNSUPPORTED;
+    }
+    return MGS_OK;
+}
+// the arguments that both passes read
+static mgs_status qk_inputs(const mgs_qk_norm_shape *sh, const void *q, const void *k, const void *qw, const void *kw,
+                            const float *table, const int32_t *pos) {
+    const int es = esize(sh->dtype);
+    mgs_status st = typed_ptrs(es, {}, {q, k, qw, kw});
+    if (st != MGS_OK) return st;
+    if ((sh->Hq > 0 && q == nullptr) || (sh->Hk > 0 && k == nullptr)) return MGS_ERR_INVALID_ARG;
+    if ((sh->rotary > 0) != (table != nullptr) || (pos != nullptr && table == nullptr)) return MGS_ERR_INVALID_ARG;
+    if (sh->rotary > 0 && pos == nullptr && sh->positions < sh->T) return MGS_ERR_INVALID_ARG;
+    return aligned16(table) && aligned4(pos) ? MGS_OK : MGS_ERR_UNSUPPORTED;
+}
+
+mgs_status mgs_qk_norm_fwd(const mgs_qk_norm_shape *shape, const void *q, const void *k, const void *q_weight,
+                           const void *k_weight, const float *table, const int32_t *token_positions, void *yq,
+                           void *yk, mgs_stream_t stream) {
+    QkSizes z;
+    mgs_status st = qk_sizes(shape, false, token_positions != nullptr, &z);
+    if (st != MGS_OK) return st;
+    if (z.q + z.k == 0) return MGS_OK;
+    if ((st = qk_inputs(shape, q, k, q_weight, k_weight, table, token_positions)) != MGS_OK) return st;
+    const int es = esize(shape->dtype);
+    if ((st = typed_ptrs(es, {}, {yq, yk})) != MGS_OK) return st;
+    if ((z.q > 0 && yq == nullptr) || (z.k > 0 && yk == nullptr)) return MGS_ERR_INVALID_ARG;
+    const int64_t nw = shape->D * es;
+    if (!apart({{yq, z.q}, {yk, z.k}},
+               {{q, z.q_span}, {k, z.k_span}, {q_weight, nw}, {k_weight, nw}, {table, z.table}, {token_positions, z.pos}}))
+        return MGS_ERR_INVALID_ARG;
+    return from_cuda(mgs::launch_qk_norm_fwd(*shape, q, k, q_weight, k_weight, table, token_positions, yq, yk,
+                                             cs_of(stream)));
+}
+
+size_t mgs_qk_norm_bwd_workspace_size(const mgs_qk_norm_shape *shape) {
+    QkSizes z;
+    if (qk_sizes(shape, true, false, &z) != MGS_OK || z.q + z.k == 0) return 0;
+    return mgs::qk_norm_bwd_workspace_bytes(*shape);
+}
+
+mgs_status mgs_qk_norm_bwd(const mgs_qk_norm_shape *shape, const void *q, const void *k, const void *q_weight,
+                           const void *k_weight, const void *grad_yq, const void *grad_yk, const float *table,
+                           const int32_t *token_positions, void *dq, void *dk, void *dq_weight, void *dk_weight,
+                           void *workspace, size_t workspace_bytes, mgs_stream_t stream) {
+    QkSizes z;
+    mgs_status st = qk_sizes(shape, true, token_positions != nullptr, &z);
+    if (st != MGS_OK) return st;
+    const int es = esize(shape->dtype);
+    const int64_t nw = shape->D * es;
+    if ((st = typed_ptrs(es, {}, {dq_weight, dk_weight})) != MGS_OK) return st;
+    if (z.q + z.k == 0) {  // no heads: the weights' gradients are zero
+        if (!apart({{dq_weight, nw}, {dk_weight, nw}}, {})) return MGS_ERR_INVALID_ARG;
+        for (void *dw : {dq_weight, dk_weight})
+            if (dw != nullptr && cudaMemsetAsync(dw, 0, size_t(nw), cs_of(stream)) != cudaSuccess) return MGS_ERR_CUDA;
+        return MGS_OK;
+    }
+    if ((st = qk_inputs(shape, q, k, q_weight, k_weight, table, token_positions)) != MGS_OK) return st;
+    if ((st = typed_ptrs(es, {}, {grad_yq, grad_yk, dq, dk})) != MGS_OK) return st;
+    if ((z.q > 0 && (grad_yq == nullptr || dq == nullptr)) || (z.k > 0 && (grad_yk == nullptr || dk == nullptr)))
+        return MGS_ERR_INVALID_ARG;
+    const size_t need = mgs::qk_norm_bwd_workspace_bytes(*shape);
+    if ((st = check_ws(need, workspace, workspace_bytes)) != MGS_OK) return st;
+    if (!apart({{dq, z.q}, {dk, z.k}, {dq_weight, nw}, {dk_weight, nw}, {workspace, int64_t(need)}},
+               {{q, z.q_span}, {k, z.k_span}, {q_weight, nw}, {k_weight, nw}, {grad_yq, z.gq_span},
+                {grad_yk, z.gk_span}, {table, z.table}, {token_positions, z.pos}}))
+        return MGS_ERR_INVALID_ARG;
+    return from_cuda(mgs::launch_qk_norm_bwd(*shape, q, k, q_weight, k_weight, grad_yq, grad_yk, table,
+                                             token_positions, dq, dk, dq_weight, dk_weight, workspace, cs_of(stream)));
+}
+
+// ---------------------------------------------------------------- embedding
+static mgs_status embed_sizes(int token_type, int64_t N, int64_t V, int64_t D, int dtype, int64_t *tokens, int64_t *rows,
+                              int64_t *table) {
+    if (N < 0 || V < 0 || D < 0) return MGS_ERR_INVALID_ARG;
+    const int es = esize(dtype);
+    if (es == 0 || (token_type != MGS_I32 && token_type != MGS_I64)) return MGS_ERR_UNSUPPORTED;
+    if (!mul_ok(N, D, rows) || !mul_ok(V, D, table) || *rows > INT64_MAX / 64 || *table > INT64_MAX / 64)
+        return MGS_ERR_INVALID_ARG;
+    // 32-bit places in the sorted order
+    if (N > INT32_MAX / 2 || V > INT32_MAX / 2 || D > INT32_MAX / 2) return MGS_ERR_UNSUPPORTED;
+    *tokens = N * (token_type == MGS_I64 ? 8 : 4), *rows *= es, *table *= es;
+    return MGS_OK;
+}
+static bool aligned_tokens(int token_type, const void *p) {
+    return reinterpret_cast<uintptr_t>(p) % (token_type == MGS_I64 ? 8 : 4) == 0;
+}
+
+mgs_status mgs_embedding_fwd(const void *tokens, int token_type, const void *weight, float scale, void *out,
+                             int64_t N, int64_t V, int64_t D, int dtype, mgs_stream_t stream) {
+    int64_t nt, nr, nw;
+    mgs_status st = embed_sizes(token_type, N, V, D, dtype, &nt, &nr, &nw);
+    if (st != MGS_OK) return st;
+    if (nr == 0) return MGS_OK;
+    if (tokens == nullptr || (weight == nullptr && nw > 0)) return MGS_ERR_INVALID_ARG;
+    if ((st = typed_ptrs(esize(dtype), {out}, {weight})) != MGS_OK) return st;
+    if (!aligned_tokens(token_type, tokens)) return MGS_ERR_UNSUPPORTED;
+    if (!apart({{out, nr}}, {{tokens, nt}, {weight, nw}})) return MGS_ERR_INVALID_ARG;
+    return from_cuda(mgs::launch_embed_fwd(token_type, dtype, tokens, weight, scale, out, N, V, D, cs_of(stream)));
+}
+
+size_t mgs_embedding_bwd_workspace_size(int64_t N, int64_t V, int64_t D) {
+    int64_t nt, nr, nw;
+    if (embed_sizes(MGS_I64, N, V, D, MGS_F32, &nt, &nr, &nw) != MGS_OK || nr == 0 || nw == 0) return 0;
+    return mgs::embed_bwd_workspace_bytes(N, V, D);
+}
+
+mgs_status mgs_embedding_bwd(const void *tokens, int token_type, const void *grad, int64_t grad_stride, float scale,
+                             void *dweight, int64_t N, int64_t V, int64_t D, int dtype, void *workspace,
+                             size_t workspace_bytes, mgs_stream_t stream) {
+    int64_t nt, nr, nw;
+    mgs_status st = embed_sizes(token_type, N, V, D, dtype, &nt, &nr, &nw);
+    if (st != MGS_OK) return st;
+    if (nw == 0) return MGS_OK;
+    const int es = esize(dtype);
+    if ((st = typed_ptrs(es, {dweight}, {grad})) != MGS_OK) return st;
+    if (N == 0) return from_cuda(cudaMemsetAsync(dweight, 0, size_t(nw), cs_of(stream)));
+    if (tokens == nullptr || grad == nullptr) return MGS_ERR_INVALID_ARG;
+    if (!aligned_tokens(token_type, tokens)) return MGS_ERR_UNSUPPORTED;
+    int64_t span;
+    const int64_t gs[3] = {grad_stride, 0, 0};
+    if (!span_of(gs, N, 1, 1, D, es, es, &span)) return MGS_ERR_UNSUPPORTED;
+    const size_t need = mgs::embed_bwd_workspace_bytes(N, V, D);
+    if ((st = check_ws(need, workspace, workspace_bytes)) != MGS_OK) return st;
+    if (!apart({{dweight, nw}, {workspace, int64_t(need)}}, {{tokens, nt}, {grad, span}})) return MGS_ERR_INVALID_ARG;
+    return from_cuda(mgs::launch_embed_bwd(token_type, dtype, tokens, grad, grad_stride, scale, dweight, N, V, D,
+                                           workspace, cs_of(stream)));
+}
+
 }  // extern "C"

@@ -1,6 +1,7 @@
 // Internal launcher interface of the language-model operators (linear
 // attention with a decay for each head, RMS norm with the residual's addition,
-// clipping by the global gradient norm) between mgs_api.cu and the kernels.
+// clipping by the global gradient norm, the gated linear recurrence, the norm of
+// queries and keys, the embedding) between mgs_api.cu and the kernels.
 #pragma once
 
 #include <cstddef>
@@ -104,5 +105,27 @@ cudaError_t launch_rms_norm_bwd(int dtype, const void *r, const void *w, const f
 size_t clip_workspace_bytes(int64_t count);
 cudaError_t launch_clip(const void *const *in, void *const *out, const int64_t *numel, const int32_t *dtypes,
                         int64_t count, float max_norm, float *norm, void *ws, cudaStream_t s);
+
+cudaError_t launch_gated_fwd(const mgs_gated_shape &sh, const void *gate, const void *value, const float *h0, void *h,
+                             float *hT, float *carries, cudaStream_t s);
+cudaError_t launch_gated_bwd(const mgs_gated_shape &sh, const void *gate, const void *value, const float *carries,
+                             const void *gh, const float *ghT, void *dgate, void *dvalue, float *dh0, cudaStream_t s);
+cudaError_t launch_gated_step(const mgs_gated_shape &sh, const void *gate, const void *value, float *state,
+                              const int32_t *slots, int64_t nslots, void *h, cudaStream_t s);
+
+cudaError_t launch_qk_norm_fwd(const mgs_qk_norm_shape &sh, const void *q, const void *k, const void *qw,
+                               const void *kw, const float *table, const int32_t *positions, void *yq, void *yk,
+                               cudaStream_t s);
+size_t qk_norm_bwd_workspace_bytes(const mgs_qk_norm_shape &sh);
+cudaError_t launch_qk_norm_bwd(const mgs_qk_norm_shape &sh, const void *q, const void *k, const void *qw,
+                               const void *kw, const void *gq, const void *gk, const float *table,
+                               const int32_t *positions, void *dq, void *dk, void *dqw, void *dkw, void *ws,
+                               cudaStream_t s);
+
+cudaError_t launch_embed_fwd(int itype, int dtype, const void *tokens, const void *w, float scale, void *out,
+                             int64_t N, int64_t V, int64_t D, cudaStream_t s);
+size_t embed_bwd_workspace_bytes(int64_t N, int64_t V, int64_t D);
+cudaError_t launch_embed_bwd(int itype, int dtype, const void *tokens, const void *grad, int64_t gs, float scale,
+                             void *dw, int64_t N, int64_t V, int64_t D, void *ws, cudaStream_t s);
 
 }  // namespace mgs
