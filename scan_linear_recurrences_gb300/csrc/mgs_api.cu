@@ -1213,8 +1213,8 @@ static mgs_status embed_sizes(int token_type, int64_t N, int64_t V, int64_t D, i
     if (es == 0 || (token_type != MGS_I32 && token_type != MGS_I64)) return MGS_ERR_UNSUPPORTED;
     if (!mul_ok(N, D, rows) || !mul_ok(V, D, table) || *rows > INT64_MAX / 64 || *table > INT64_MAX / 64)
         return MGS_ERR_INVALID_ARG;
-    // 32-bit places in the sorted order
-    if (N > INT32_MAX / 2 || V > INT32_MAX / 2 || D > INT32_MAX / 2) return MGS_ERR_UNSUPPORTED;
+    // 32-bit places in the sorted order, 16-bit grids over the columns
+    if (N > INT32_MAX / 2 || V > INT32_MAX / 2 || D > (1 << 22)) return MGS_ERR_UNSUPPORTED;
     *tokens = N * (token_type == MGS_I64 ? 8 : 4), *rows *= es, *table *= es;
     return MGS_OK;
 }
