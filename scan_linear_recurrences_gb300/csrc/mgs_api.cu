@@ -1070,7 +1070,9 @@ mgs_status mgs_gated_scan_fwd(const mgs_gated_shape *shape, const void *gate, co
     if ((st = typed_ptrs(4, {}, {h0, h_T, carries})) != MGS_OK) return st;
     if (!apart({{h, z.n}, {h_T, z.state}, {carries, z.carries}}, {{gate, z.gate}, {value, z.value}, {h0, z.state}}))
         return MGS_ERR_INVALID_ARG;
-    return from_cuda(mgs::launch_gated_fwd(*shape, gate, value, h0, h, h_T, carries, cs));
+    mgs::DevCtl ctl;
+    if ((st = current_ctl(&ctl)) != MGS_OK) return st;
+    return from_cuda(mgs::launch_gated_fwd(*shape, gate, value, h0, h, h_T, carries, ctl, cs));
 }
 
 mgs_status mgs_gated_scan_bwd(const mgs_gated_shape *shape, const void *gate, const void *value, const float *carries,
@@ -1086,7 +1088,9 @@ mgs_status mgs_gated_scan_bwd(const mgs_gated_shape *shape, const void *gate, co
     if (!apart({{d_gate, z.n}, {d_value, z.n}, {d_h0, z.state}},
                {{gate, z.gate}, {value, z.value}, {carries, z.carries}, {grad_h, z.gh}, {grad_h_T, z.state}}))
         return MGS_ERR_INVALID_ARG;
-    return from_cuda(mgs::launch_gated_bwd(*shape, gate, value, carries, grad_h, grad_h_T, d_gate, d_value, d_h0, cs));
+    mgs::DevCtl ctl;
+    if ((st = current_ctl(&ctl)) != MGS_OK) return st;
+    return from_cuda(mgs::launch_gated_bwd(*shape, gate, value, carries, grad_h, grad_h_T, d_gate, d_value, d_h0, ctl, cs));
 }
 
 mgs_status mgs_gated_scan_step(const mgs_gated_shape *shape, const void *gate, const void *value, float *state,

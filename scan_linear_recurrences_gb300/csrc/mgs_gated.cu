@@ -7,23 +7,25 @@
 //
 // A run of steps acts on the state before it as s -> A s + H (A the product of its
 // a, H its states from zero), and on the gradient behind it as f -> A f + R.  A
-// block owns 64 channels of one sequence, each of its warps kSteps consecutive
-// steps of a tile of kTile, a lane two channels: the inputs are read once and stay
-// in registers, the warps exchange their maps through shared memory, and each runs
-// its steps again from its own state.  With few channels a cluster of blocks takes
-// tiles in turn, the blocks' maps pushed into each other's shared memory: one
-// barrier of the cluster a round.
+// block owns 64 channels of one sequence, each of its warps consecutive steps of a
+// tile of 64, a lane two channels.  A warp copies its part of the next tile to
+// shared memory while it works on this one's, keeps what it computes in registers,
+// exchanges its map with the other warps' and runs its steps again from its own
+// state: the inputs are read once.  With few channels a cluster of blocks takes
+// tiles in turn, their maps pushed into each other's shared memory.
 // The backward rebuilds h within a tile from the state that the forward kept before
 // it (the carries), so that h is not read: five tensors pass, not six.
+#include <type_traits>
+
 #include "mgs_cluster.cuh"
+#include "mgs_launch.h"
 #include "mgs_lm.h"
 #include "mgs_num.cuh"
 
 namespace mgs {
 namespace {
 
-constexpr int kSteps = 8, kWarps = 8, kTile = kSteps * kWarps;
-static_assert(kTile == MGS_GATED_SPAN, "a tile begins at a kept state");
+constexpr int kTile = MGS_GATED_SPAN;  // a tile begins at a kept state
 constexpr int kMaxCluster = 16;
 
 // Two channels in one register pair: sm_100 has fp32 sums and products of pairs
@@ -80,49 +82,55 @@ __device__ __forceinline__ float exp_minus(float x) {
     return fmaf(e * kLn2, low, e);
 }
 
-// z, a = 1 - z and c of one step of two channels; z and a both to their own last
-// digits.  Two sigmoids share one reciprocal, of the product of their denominators
-// (both in 1..2).  Where z is zero in fp32 (a gate of -infinity, or of the type's
-// lowest value) the step is masked: c is zero whatever the value.  A NaN in the
-// value stays out of z and a, with which gradients pass.
-template <typename T, bool POS>
-__device__ __forceinline__ void gates(float2 k, float2 v, f2 &z, f2 &a, f2 &c) {
+// z, a = 1 - z, c and z c' (BWD) of one step of two channels; z and a both to
+// their own last digits.  Two sigmoids share one reciprocal, of the product of their
+// denominators (both in 1..2).  BWD: a NaN in the value stays out of z and a, with
+// which gradients pass (the states behind it are NaN anyway).
+template <typename T, bool POS, bool BWD>
+__device__ __forceinline__ void gates(float2 k, float2 v, f2 &z, f2 &a, f2 &c, f2 &zs) {
     const f2 one = pair(1.f, 1.f);
     const f2 e = pair(exp_minus<T>(k.x), exp_minus<T>(k.y));
     const f2 d = e + one;
-    const float2 dd = both(d);
-    f2 r, fs;
+    f2 r, s, fs;
     if constexpr (POS) {
         const f2 f = pair(exp_minus<T>(v.x), exp_minus<T>(v.y));
-        float2 g = both(f + one);
-        g.x = fminf(g.x, 2.f), g.y = fminf(g.y, 2.f);  // (2 for NaN)
-        const f2 gg = pair(g.x, g.y);
-        const float2 p = both(d * gg);
+        f2 g = f + one;
+        if constexpr (BWD) {
+            const float2 gg = both(g);
+            g = pair(fminf(gg.x, 2.f), fminf(gg.y, 2.f));  // (2 for NaN)
+        }
+        const float2 p = both(d * g);
         const f2 q = pair(rcp_approx(p.x), rcp_approx(p.y));
-        r = q * gg;
-        fs = f * (q * d);
+        r = q * g;
+        s = q * d;
+        fs = f * s;
     } else {
-        r = pair(rcp_approx(dd.x), rcp_approx(dd.y));
+        const float2 p = both(d);
+        r = pair(rcp_approx(p.x), rcp_approx(p.y));
     }
     // the smaller of z and a; the larger is 1 less it, rounded once: 1 where z is nothing beside it, so that a state
     // behind many such steps does not drift
     const f2 low = e * r;
     const float2 lo = both(low), hi = both(fma2(low, pair(-1.f, -1.f), one));
-    const float2 zz = make_float2(k.x >= 0.f ? hi.x : lo.x, k.y >= 0.f ? hi.y : lo.y);
-    z = pair(zz.x, zz.y);
-    a = pair(k.x >= 0.f ? lo.x : hi.x, k.y >= 0.f ? lo.y : hi.y);
-    float2 cc = v;
+    const bool kx = k.x >= 0.f, ky = k.y >= 0.f;
+    z = pair(kx ? hi.x : lo.x, ky ? hi.y : lo.y);
+    a = pair(kx ? lo.x : hi.x, ky ? lo.y : hi.y);
+    c = pair(v.x, v.y);
+    zs = z;
     if constexpr (POS) {
-        const float2 up = both(pair(v.x, v.y) + pair(0.5f, 0.5f)), down = both(fs);
-        // below zero less than 1/2, so that c tells the side (sigmoid of -1e-9 rounds to 1/2)
-        cc.x = v.x < 0.f ? fminf(down.x, 0x1.fffffep-2f) : up.x;
-        cc.y = v.y < 0.f ? fminf(down.y, 0x1.fffffep-2f) : up.y;
+        const bool vx = v.x < 0.f, vy = v.y < 0.f;
+        const float2 up = both(c + pair(0.5f, 0.5f)), down = both(fs);
+        c = pair(vx ? down.x : up.x, vy ? down.y : up.y);
+        if constexpr (BWD) {
+            const float2 slope = both(fs * s);
+            zs = z * pair(vx ? slope.x : 1.f, vy ? slope.y : 1.f);
+        }
     }
-    c = pair(zz.x == 0.f ? 0.f : cc.x, zz.y == 0.f ? 0.f : cc.y);
 }
 
-// Two channels of a step as they lie in memory: neighbours (VEC: one load), or 32
-// apart (any alignment; `ok` has a bit for each).
+// Two channels of a step: neighbours (VEC), or 32 apart (any alignment; `ok` has a
+// bit for each).
+constexpr float kMasked = -88.f;  // z is zero in fp32: the step is masked, whatever its value
 template <typename T, bool VEC>
 struct Two;
 template <bool VEC>
@@ -130,13 +138,19 @@ struct Two<bf16, VEC> {
     uint32_t u;
     __device__ __forceinline__ void load(const bf16 *p, int ok) {
         if (VEC) {
-            u = ok ? __ldcs(reinterpret_cast<const uint32_t *>(p)) : 0u;
+            u = ok ? *reinterpret_cast<const uint32_t *>(p) : 0u;
         } else {
             const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
             u = (ok & 1 ? uint32_t(q[0]) : 0u) | (ok & 2 ? uint32_t(q[32]) << 16 : 0u);
         }
     }
     __device__ __forceinline__ float2 get() const { return make_float2(bf_lo(u), bf_hi(u)); }
+    // the value, zero where its gate masks it
+    __device__ __forceinline__ float2 get_unmasked(const Two &gate) const {
+        const __nv_bfloat162 k = *reinterpret_cast<const __nv_bfloat162 *>(&gate.u);
+        const uint32_t x = u & __hgeu2_mask(k, __float2bfloat162_rn(kMasked));  // (NaN: not masked)
+        return make_float2(bf_lo(x), bf_hi(x));
+    }
     static __device__ __forceinline__ void store(bf16 *p, float2 v, int ok) {
         const uint32_t u = pack_bf16(v.x, v.y);
         if (VEC) {
@@ -151,10 +165,13 @@ template <bool VEC>
 struct Two<float, VEC> {
     float2 u;
     __device__ __forceinline__ void load(const float *p, int ok) {
-        if (VEC) u = ok ? __ldcs(reinterpret_cast<const float2 *>(p)) : make_float2(0.f, 0.f);
+        if (VEC) u = ok ? *reinterpret_cast<const float2 *>(p) : make_float2(0.f, 0.f);
         else u = make_float2(ok & 1 ? p[0] : 0.f, ok & 2 ? p[32] : 0.f);
     }
     __device__ __forceinline__ float2 get() const { return u; }
+    __device__ __forceinline__ float2 get_unmasked(const Two &gate) const {
+        return make_float2(gate.u.x < kMasked ? 0.f : u.x, gate.u.y < kMasked ? 0.f : u.y);
+    }
     static __device__ __forceinline__ void store(float *p, float2 v, int ok) {
         if (VEC) {
             if (ok) __stcs(reinterpret_cast<float2 *>(p), v);
@@ -165,6 +182,56 @@ struct Two<float, VEC> {
     }
 };
 
+// How a warp's steps come to shared memory: copies of 16 bytes (rows that start at
+// such multiples), of 4 bytes, or element by element (bf16 that starts anywhere).
+enum Copy { kCopy16, kCopy4, kCopyAny };
+__device__ __forceinline__ void copy16(void *dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(void *dst, const void *src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(ok ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Rows 0 .. n - 1 of L of 64 channels (zeros behind them and past channel D), `stride`
+// apart, from `src` (the sequence's first row needed, channel d0) to a warp's [L][64].
+template <typename T, int L, Copy HOW>
+__device__ __forceinline__ void copy_rows(T *dst, const T *src, int64_t stride, int n, int64_t left) {
+    const int lane = threadIdx.x & 31;
+    if constexpr (HOW == kCopy16) {
+        constexpr int V = 16 / int(sizeof(T)), PER = 64 / V, ROWS = 32 / PER;  // lanes a row, rows at once
+        const int row = lane / PER, col = lane % PER * V;
+        const bool in = col < left;
+        const T *p = src + row * stride + col;
+#pragma unroll
+        for (int i = 0; i < L / ROWS; ++i) {
+            const bool ok = in && i * ROWS + row < n;
+            copy16(dst + (i * ROWS + row) * 64 + col, ok ? p + i * ROWS * stride : src, ok);
+        }
+    } else if constexpr (HOW == kCopy4) {
+        constexpr int V = 4 / int(sizeof(T));
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+#pragma unroll
+            for (int j = 0; j < 2 / V; ++j) {
+                const int col = lane * V + 32 * j;
+                const bool ok = col < left && i < n;
+                copy4(dst + i * 64 + col, ok ? src + i * stride + col : src, ok);
+            }
+    } else {
+        T x[L][2];
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                x[i][j] = lane + 32 * j < left && i < n ? src[i * stride + lane + 32 * j] : from_f<T>(0.f);
+#pragma unroll
+        for (int i = 0; i < L; ++i) dst[i * 64 + lane] = x[i][0], dst[i * 64 + lane + 32] = x[i][1];
+    }
+}
+
 struct Args {
     const void *gate, *value, *gh;
     void *h, *dgate, *dvalue;
@@ -173,6 +240,7 @@ struct Args {
     float *carries;
     int64_t D, kb, kt, vb, vt, gb, gt;
     int T, tiles, strips, cluster;
+    DevCtl ctl;
 };
 
 // a lane's two channels of the block's 64, and which of them are there
@@ -187,12 +255,6 @@ struct Lane {
     }
 };
 
-__device__ __forceinline__ void push16(void *slot, unsigned rank, float4 v) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dsmem_addr(slot, rank)), "f"(v.x), "f"(v.y),
-                 "f"(v.z), "f"(v.w)
-                 : "memory");
-}
-
 // One map of a lane's two channels
 struct Map {
     f2 A, H;
@@ -203,186 +265,269 @@ struct Map {
     static __device__ __forceinline__ Map unpack(float4 m) { return {pair(m.x, m.y), pair(m.z, m.w)}; }
 };
 
+// 16 bytes into shared memory of the cluster's CTA `rank`, counted by its barrier
+__device__ __forceinline__ void push16(void *slot, uint64_t *bar, unsigned rank, float4 v) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                     dsmem_addr(slot, rank)),
+                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(dsmem_addr(bar, rank))
+                 : "memory");
+}
+
+// The maps of a tile's warps, and of a round's blocks (CL).  Two of each, in turn: a
+// block pushes into a peer's slots of round n + 2 when it has that peer's map of round
+// n + 1, which the peer pushes when all its warps are past round n.
+template <int W, bool CL>
+struct Exchange {
+    float4 maps[2][W][32];
+    float4 slots[CL ? 2 : 1][CL ? kMaxCluster : 1][32];
+    alignas(16) uint64_t bar[2];
+};
+
 // The state that enters this warp's steps: `s` (the state before the round) through
 // the maps before this warp's, and s through all of them for the next round.  REV:
 // the maps act from the last warp, and the last block of the cluster, to the first.
-template <bool CL, bool REV>
-__device__ __forceinline__ f2 enter(const float4 (*maps)[32], float4 (*slots)[32], f2 &s, int warp, int lane,
-                                    int cluster, unsigned rank) {
+template <bool REV, int W, bool CL>
+__device__ __forceinline__ f2 enter(Exchange<W, CL> &ex, int turn, int phase, f2 &s, int warp, int lane, int cluster,
+                                    unsigned rank, const DevCtl &ctl, bool &lost) {
     f2 mine = s;
     if constexpr (!CL) {
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            const int j = REV ? kWarps - 1 - i : i;
+        for (int i = 0; i < W; ++i) {
+            const int j = REV ? W - 1 - i : i;
             if (j == warp) mine = s;
-            const Map m = Map::unpack(maps[j][lane]);
+            const Map m = Map::unpack(ex.maps[turn][j][lane]);
             s = fma2(m.A, s, m.H);
         }
         return mine;
     }
     Map before{pair(1.f, 1.f), pair(0.f, 0.f)}, all = before;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        const int j = REV ? kWarps - 1 - i : i;
+    for (int i = 0; i < W; ++i) {
+        const int j = REV ? W - 1 - i : i;
         if (j == warp) before = all;
-        const Map m = Map::unpack(maps[j][lane]);
+        const Map m = Map::unpack(ex.maps[turn][j][lane]);
         all.H = fma2(m.A, all.H, m.H);
         all.A = m.A * all.A;
     }
-    for (int r = warp; r < cluster; r += kWarps) push16(&slots[rank][lane], unsigned(r), all.pack());
-    cluster_arrive();
-    cluster_wait();
+    for (int r = warp; r < cluster; r += W) push16(&ex.slots[turn][rank][lane], &ex.bar[turn], unsigned(r), all.pack());
+    if (warp == 0 && lane == 0) mbar_arrive_expect_tx(&ex.bar[turn], unsigned(cluster) * 512u);
+    // (after a wait that gave up the rounds go on without waiting, to their end)
+    if (!lost && !mbar_wait_bounded(&ex.bar[turn], unsigned(phase), ctl.timeout_ns)) {
+        lost = true;
+        record_error(ctl, ERR_MBAR_TIMEOUT);
+    }
     for (int i = 0; i < cluster; ++i) {
         const int r = REV ? cluster - 1 - i : i;
         if (r == int(rank)) mine = s;
-        const Map m = Map::unpack(slots[r][lane]);
+        const Map m = Map::unpack(ex.slots[turn][r][lane]);
         s = fma2(m.A, s, m.H);
     }
     return fma2(before.A, mine, before.H);
 }
 
-template <typename T, bool POS, bool VEC, bool CL>
-__global__ void __launch_bounds__(kWarps * 32, 2) gated_fwd_kernel(const __grid_constant__ Args g) {
-    __shared__ float4 maps[2][kWarps][32];
-    __shared__ float4 slots[CL ? 2 : 1][CL ? kMaxCluster : 1][32];
+// all blocks of the cluster have their barriers (before the first push), or are done with each other's memory
+template <bool CL>
+__device__ __forceinline__ void meet(uint64_t *bar, bool init) {
+    if constexpr (CL) {
+        if (init && threadIdx.x == 0) {
+            mbar_init(&bar[0], 1), mbar_init(&bar[1], 1);
+            fence_barrier_init();
+        }
+        __syncthreads();
+        cluster_arrive();
+        cluster_wait();
+    }
+}
+
+constexpr int kFwdWarps = 4, kFwdSteps = kTile / kFwdWarps;
+constexpr int kBwdWarps = 8, kBwdSteps = kTile / kBwdWarps;
+
+template <typename T, bool POS, Copy HOW, bool CL>
+__global__ void __launch_bounds__(kFwdWarps * 32, 4) gated_fwd_kernel(const __grid_constant__ Args g) {
+    constexpr int W = kFwdWarps, L = kFwdSteps;
+    constexpr bool VEC = HOW == kCopy16 || (HOW == kCopy4 && sizeof(T) == 2);
+    using Ex = Exchange<W, CL>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    Ex &ex = *reinterpret_cast<Ex *>(smem);
+    T *ring = reinterpret_cast<T *>(smem + sizeof(Ex));  // [W][2 stages][2 tensors][L][64]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cluster = CL ? g.cluster : 1;
     const unsigned rank = CL ? cluster_rank() : 0;
     const int strip = int(blockIdx.x / cluster % g.strips);
-    const int64_t b = int64_t(blockIdx.x / cluster / g.strips);
+    const int64_t b = int64_t(blockIdx.x / cluster / g.strips), left = g.D - int64_t(strip) * 64;
     const Lane<VEC> at(strip, g.D);
-    const T *gate = (const T *)g.gate + b * g.kb + at.d, *value = (const T *)g.value + b * g.vb + at.d;
+    const T *gate = (const T *)g.gate + b * g.kb + int64_t(strip) * 64,
+            *value = (const T *)g.value + b * g.vb + int64_t(strip) * 64;
     T *h = (T *)g.h + b * g.T * g.D + at.d;
+    T *mine = ring + warp * (2 * 2 * L * 64);
+    auto fetch = [&](int tile, int stage) {
+        const int t0 = tile * kTile + warp * L, n = g.T - t0;
+        T *to = mine + stage * (2 * L * 64);
+        if (tile < g.tiles && n > 0) {
+            copy_rows<T, L, HOW>(to, gate + t0 * g.kt, g.kt, n, left);
+            copy_rows<T, L, HOW>(to + L * 64, value + t0 * g.vt, g.vt, n, left);
+        }
+        copies_close();
+    };
+    fetch(int(rank), 0);
+    meet<CL>(ex.bar, true);
     f2 s = pair(0.f, 0.f);
     if (g.in) {
         Two<float, VEC> x;
         x.load(g.in + b * g.D + at.d, at.ok);
         s = pair(x.u.x, x.u.y);
     }
-    Two<T, VEC> rk[kSteps], rv[kSteps];
-    auto fetch = [&](int tile) {
-        const int t0 = tile * kTile + warp * kSteps;
+    int turn = 0, phase = 0;
+    bool lost = false;
+    for (int first = 0; first < g.tiles; first += cluster) {
+        const int tile = first + int(rank), t0 = tile * kTile + warp * L, n = g.T - t0;
+        __syncwarp();  // the other stage has been read
+        fetch(tile + cluster, turn ^ 1);
+        copies_wait<1>();
+        __syncwarp();
+        const T *from = mine + turn * (2 * L * 64) + (VEC ? 2 * lane : lane);
+        f2 a[L], c[L];
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int ok = t0 + i < g.T ? at.ok : 0;
-            rk[i].load(gate + int64_t(t0 + i) * g.kt, ok);
-            rv[i].load(value + int64_t(t0 + i) * g.vt, ok);
-        }
-    };
-    fetch(int(rank));
-    int turn = 0;
-    for (int first = 0; first < g.tiles; first += cluster, turn ^= 1) {
-        const int tile = first + int(rank), t0 = tile * kTile + warp * kSteps;
-        f2 a[kSteps], c[kSteps];
-        Map m{pair(1.f, 1.f), pair(0.f, 0.f)};
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            f2 z;
-            gates<T, POS>(rk[i].get(), rv[i].get(), z, a[i], c[i]);
+        for (int i = 0; i < L; ++i) {
+            Two<T, VEC> k, v;
+            f2 z, zs;
+            k.load(from + i * 64, 3), v.load(from + (L + i) * 64, 3);
+            gates<T, POS, false>(k.get(), v.get_unmasked(k), z, a[i], c[i], zs);
             c[i] = z * c[i];
-            if (t0 + i >= g.T) a[i] = pair(1.f, 1.f), c[i] = pair(0.f, 0.f);  // no step
+        }
+        if (n < L) {  // no steps
+#pragma unroll
+            for (int i = 0; i < L; ++i)
+                if (i >= n) a[i] = pair(1.f, 1.f), c[i] = pair(0.f, 0.f);
+        }
+        Map m{a[0], c[0]};
+#pragma unroll
+        for (int i = 1; i < L; ++i) {
             m.H = fma2(a[i], m.H, c[i]);
             m.A = m.A * a[i];
         }
-        if (tile + cluster < g.tiles) fetch(tile + cluster);
-        maps[turn][warp][lane] = m.pack();
+        ex.maps[turn][warp][lane] = m.pack();
         __syncthreads();
-        f2 x = enter<CL, false>(maps[turn], slots[CL ? turn : 0], s, warp, lane, cluster, rank);
+        f2 x = enter<false>(ex, turn, phase, s, warp, lane, cluster, rank, g.ctl, lost);
         if (g.carries && warp == 0 && tile < g.tiles)
             Two<float, VEC>::store(g.carries + (b * g.tiles + tile) * g.D + at.d, both(x), at.ok);
+        T *to = h + t0 * g.D;
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
+        for (int i = 0; i < L; ++i) {
             x = fma2(a[i], x, c[i]);
-            Two<T, VEC>::store(h + int64_t(t0 + i) * g.D, both(x), t0 + i < g.T ? at.ok : 0);
+            Two<T, VEC>::store(to + i * g.D, both(x), i < n ? at.ok : 0);
         }
+        phase ^= turn;
+        turn ^= 1;
     }
     if (g.out && rank == 0 && warp == 0) Two<float, VEC>::store(g.out + b * g.D + at.d, both(s), at.ok);
+    meet<CL>(ex.bar, false);
 }
 
-template <typename T, bool POS, bool VEC, bool CL>
-__global__ void __launch_bounds__(kWarps * 32, 2) gated_bwd_kernel(const __grid_constant__ Args g) {
-    __shared__ float4 maps[2][kWarps][32], back[2][kWarps][32];
-    __shared__ float4 slots[CL ? 2 : 1][CL ? kMaxCluster : 1][32];
+template <typename T, bool POS, Copy HOW, bool CL>
+__global__ void __launch_bounds__(kBwdWarps * 32, 2) gated_bwd_kernel(const __grid_constant__ Args g) {
+    constexpr int W = kBwdWarps, L = kBwdSteps;
+    constexpr bool VEC = HOW == kCopy16 || (HOW == kCopy4 && sizeof(T) == 2);
+    using Ex = Exchange<W, CL>;
+    extern __shared__ __align__(16) unsigned char smem[];
+    Ex &ex = *reinterpret_cast<Ex *>(smem);
+    float4(*maps)[W][32] = reinterpret_cast<float4(*)[W][32]>(smem + sizeof(Ex));  // the states' maps [2][W][32]
+    T *ring = reinterpret_cast<T *>(smem + sizeof(Ex) + sizeof(float4) * 2 * W * 32);  // [W][2 stages][3 tensors][L][64]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cluster = CL ? g.cluster : 1;
     const unsigned rank = CL ? cluster_rank() : 0;
     const int strip = int(blockIdx.x / cluster % g.strips);
-    const int64_t b = int64_t(blockIdx.x / cluster / g.strips);
+    const int64_t b = int64_t(blockIdx.x / cluster / g.strips), left = g.D - int64_t(strip) * 64;
     const Lane<VEC> at(strip, g.D);
-    const T *gate = (const T *)g.gate + b * g.kb + at.d, *value = (const T *)g.value + b * g.vb + at.d,
-            *gh = (const T *)g.gh + b * g.gb + at.d;
+    const T *gate = (const T *)g.gate + b * g.kb + int64_t(strip) * 64,
+            *value = (const T *)g.value + b * g.vb + int64_t(strip) * 64,
+            *gh = (const T *)g.gh + b * g.gb + int64_t(strip) * 64;
     T *dgate = (T *)g.dgate + b * g.T * g.D + at.d, *dvalue = (T *)g.dvalue + b * g.T * g.D + at.d;
+    T *mine = ring + warp * (2 * 3 * L * 64);
+    Two<float, VEC> next;  // the state before the next tile
+    auto fetch = [&](int tile, int stage) {
+        const int t0 = tile * kTile + warp * L, n = g.T - t0;
+        T *to = mine + stage * (3 * L * 64);
+        const bool there = tile >= 0 && tile < g.tiles;
+        next.load(g.carries + (b * g.tiles + tile) * g.D + at.d, there ? at.ok : 0);
+        if (there && n > 0) {
+            copy_rows<T, L, HOW>(to, gate + t0 * g.kt, g.kt, n, left);
+            copy_rows<T, L, HOW>(to + L * 64, value + t0 * g.vt, g.vt, n, left);
+            copy_rows<T, L, HOW>(to + 2 * L * 64, gh + t0 * g.gt, g.gt, n, left);
+        }
+        copies_close();
+    };
+    int first = (g.tiles - 1) / cluster * cluster, turn = 0, phase = 0;
+    bool lost = false;
+    fetch(first + int(rank), 0);
+    meet<CL>(ex.bar, true);
     f2 flow = pair(0.f, 0.f);
     if (g.in) {
         Two<float, VEC> x;
         x.load(g.in + b * g.D + at.d, at.ok);
         flow = pair(x.u.x, x.u.y);
     }
-    Two<T, VEC> rk[kSteps], rv[kSteps], rg[kSteps];
-    Two<float, VEC> rc;
-    auto fetch = [&](int tile) {
-        const int t0 = tile * kTile + warp * kSteps;
-        rc.load(g.carries + (b * g.tiles + tile) * g.D + at.d, tile < g.tiles ? at.ok : 0);
+    for (; first >= 0; first -= cluster) {
+        const int tile = first + int(rank), t0 = tile * kTile + warp * L, n = g.T - t0;
+        f2 x = pair(next.u.x, next.u.y);
+        __syncwarp();  // the other stage has been read
+        fetch(tile - cluster, turn ^ 1);
+        copies_wait<1>();
+        __syncwarp();
+        const T *from = mine + turn * (3 * L * 64) + (VEC ? 2 * lane : lane);
+        f2 a[L], z[L], c[L], zs[L];
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const int ok = t0 + i < g.T ? at.ok : 0;
-            rk[i].load(gate + int64_t(t0 + i) * g.kt, ok);
-            rv[i].load(value + int64_t(t0 + i) * g.vt, ok);
-            rg[i].load(gh + int64_t(t0 + i) * g.gt, ok);
+        for (int i = 0; i < L; ++i) {
+            Two<T, VEC> k, v;
+            k.load(from + i * 64, 3), v.load(from + (L + i) * 64, 3);
+            gates<T, POS, true>(k.get(), v.get_unmasked(k), z[i], a[i], c[i], zs[i]);
         }
-    };
-    int first = (g.tiles - 1) / cluster * cluster, turn = 0;
-    fetch(first + int(rank));
-    for (; first >= 0; first -= cluster, turn ^= 1) {
-        const int tile = first + int(rank), t0 = tile * kTile + warp * kSteps;
-        f2 a[kSteps], z[kSteps], c[kSteps];
-        Two<T, VEC> gr[kSteps];
-        Map m{pair(1.f, 1.f), pair(0.f, 0.f)};
+        if (n < L) {  // no steps
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            gates<T, POS>(rk[i].get(), rv[i].get(), z[i], a[i], c[i]);
-            if (t0 + i >= g.T) a[i] = pair(1.f, 1.f), z[i] = c[i] = pair(0.f, 0.f);
+            for (int i = 0; i < L; ++i)
+                if (i >= n) a[i] = pair(1.f, 1.f), z[i] = c[i] = zs[i] = pair(0.f, 0.f);
+        }
+        auto gradient = [&](int i) {
+            Two<T, VEC> y;
+            y.load(from + (2 * L + i) * 64, 3);
+            const float2 u = y.get();
+            return i < n ? pair(u.x, u.y) : pair(0.f, 0.f);
+        };
+        Map m{a[0], z[0] * c[0]}, r{a[0], pair(0.f, 0.f)};
+#pragma unroll
+        for (int i = 1; i < L; ++i) {
             m.H = fma2(a[i], m.H, z[i] * c[i]);
             m.A = m.A * a[i];
-            gr[i] = rg[i];
         }
-        const f2 start = pair(rc.u.x, rc.u.y);
-        if (first > 0) fetch(tile - cluster);
-        Map n{m.A, pair(0.f, 0.f)};
+        r.A = m.A;
 #pragma unroll
-        for (int i = kSteps - 1; i >= 0; --i) {
-            const float2 x = gr[i].get();
-            n.H = a[i] * (pair(x.x, x.y) + n.H);
-        }
+        for (int i = L - 1; i >= 0; --i) r.H = a[i] * (gradient(i) + r.H);
         maps[turn][warp][lane] = m.pack();
-        back[turn][warp][lane] = n.pack();
+        ex.maps[turn][warp][lane] = r.pack();
         __syncthreads();
-        f2 x = start;  // the state before this warp's steps
         for (int j = 0; j < warp; ++j) {
             const Map o = Map::unpack(maps[turn][j][lane]);
             x = fma2(o.A, x, o.H);
         }
-        // z <- z c', c <- (c - h before) z a
 #pragma unroll
-        for (int i = 0; i < kSteps; ++i) {
-            const f2 d = fma2(x, pair(-1.f, -1.f), c[i]), w = z[i] * d;
+        for (int i = 0; i < L; ++i) {  // c <- z a (c - h before)
+            const f2 w = z[i] * fma2(x, pair(-1.f, -1.f), c[i]);
             x = x + w;
-            if constexpr (POS) {
-                const float2 cc = both(c[i]), lo = both(fma2(c[i] * pair(-1.f, -1.f), c[i], c[i]));
-                z[i] = z[i] * pair(cc.x < 0.5f ? lo.x : 1.f, cc.y < 0.5f ? lo.y : 1.f);
-            }
             c[i] = a[i] * w;
         }
-        f2 f = enter<CL, true>(back[turn], slots[CL ? turn : 0], flow, warp, lane, cluster, rank);
+        f2 f = enter<true>(ex, turn, phase, flow, warp, lane, cluster, rank, g.ctl, lost);
+        T *to_k = dgate + t0 * g.D, *to_v = dvalue + t0 * g.D;
 #pragma unroll
-        for (int i = kSteps - 1; i >= 0; --i) {
-            const float2 y = gr[i].get();
-            const f2 lam = pair(y.x, y.y) + f;
-            const int ok = t0 + i < g.T ? at.ok : 0;
-            Two<T, VEC>::store(dvalue + int64_t(t0 + i) * g.D, both(lam * z[i]), ok);
-            Two<T, VEC>::store(dgate + int64_t(t0 + i) * g.D, both(lam * c[i]), ok);
+        for (int i = L - 1; i >= 0; --i) {
+            const f2 lam = gradient(i) + f;
+            const int ok = i < n ? at.ok : 0;
+            Two<T, VEC>::store(to_v + i * g.D, both(lam * zs[i]), ok);
+            Two<T, VEC>::store(to_k + i * g.D, both(lam * c[i]), ok);
             f = a[i] * lam;
         }
+        phase ^= turn;
+        turn ^= 1;
     }
     if (g.out && rank == 0 && warp == 0) Two<float, VEC>::store(g.out + b * g.D + at.d, both(flow), at.ok);
+    meet<CL>(ex.bar, false);
 }
 
 template <typename T, bool POS, bool VEC>
@@ -401,20 +546,29 @@ __global__ void __launch_bounds__(128)
     if (slot >= 0 && slot < nslots) {
         Two<float, VEC> s;
         s.load(state + slot * D + at.d, at.ok);
-        f2 z, a, c;
-        gates<T, POS>(k.get(), v.get(), z, a, c);
+        f2 z, a, c, zs;
+        gates<T, POS, false>(k.get(), v.get_unmasked(k), z, a, c, zs);
         x = both(fma2(a, pair(s.u.x, s.u.y), z * c));
         Two<float, VEC>::store(state + slot * D + at.d, x, at.ok);
     }
     Two<T, VEC>::store(h + b * D + at.d, x, at.ok);
 }
 
-// channels in pairs: every row of every tensor starts at a multiple of two elements
-bool pairs(const Args &g, int es) {
-    auto ok = [&](const void *p, int size) { return reinterpret_cast<uintptr_t>(p) % unsigned(2 * size) == 0; };
-    return ((g.D | g.kb | g.kt | g.vb | g.vt | g.gb | g.gt) & 1) == 0 && ok(g.gate, es) && ok(g.value, es) &&
-           ok(g.gh, es) && ok(g.h, es) && ok(g.dgate, es) && ok(g.dvalue, es) && ok(g.in, 4) && ok(g.out, 4) &&
-           ok(g.carries, 4);
+// The widest copies that every row's start allows; channels in pairs (every output
+// and state too) with 16 bytes, and in bf16 with 4
+Copy copy_of(const Args &g, int es) {
+    const void *in[] = {g.gate, g.value, g.gh}, *out[] = {g.h, g.dgate, g.dvalue}, *f32[] = {g.in, g.out, g.carries};
+    const uint64_t strides = uint64_t(g.kb | g.kt | g.vb | g.vt | g.gb | g.gt);
+    auto rows = [&](unsigned bytes) {
+        bool ok = strides * uint64_t(es) % bytes == 0;
+        for (const void *p : in) ok = ok && reinterpret_cast<uintptr_t>(p) % bytes == 0;
+        return ok;
+    };
+    bool pairs = g.D % 2 == 0;
+    for (const void *p : out) pairs = pairs && reinterpret_cast<uintptr_t>(p) % unsigned(2 * es) == 0;
+    for (const void *p : f32) pairs = pairs && reinterpret_cast<uintptr_t>(p) % 8 == 0;
+    if (pairs && g.D * es % 16 == 0 && rows(16)) return kCopy16;
+    return es == 4 || (pairs && rows(4)) ? kCopy4 : kCopyAny;
 }
 
 // Blocks of a cluster: enough for two blocks an SM, as far as there are tiles
@@ -425,10 +579,14 @@ int cluster_of(int64_t lanes, int tiles) {
 }
 
 template <typename F, typename C>
-cudaError_t run(F *plain, C *clustered, Args &g, int64_t lanes, cudaStream_t s) {
+cudaError_t run(F *plain, C *clustered, Args &g, int64_t lanes, const size_t (&exchange)[2], int warps, size_t ring, cudaStream_t s) {
     g.cluster = cluster_of(lanes, g.tiles);
-    if (g.cluster > 1) return launch_cluster(clustered, lanes * g.cluster, kWarps * 32, 0, g.cluster, s, g);
-    plain<<<unsigned(lanes), kWarps * 32, 0, s>>>(g);
+    const size_t smem = ring + (g.cluster > 1 ? exchange[1] : exchange[0]);
+    const void *fn = g.cluster > 1 ? reinterpret_cast<const void *>(clustered) : reinterpret_cast<const void *>(plain);
+    const cudaError_t e = ensure_smem_attr(fn, int(smem));
+    if (e != cudaSuccess) return e;
+    if (g.cluster > 1) return launch_cluster(clustered, lanes * g.cluster, warps * 32, smem, g.cluster, s, g);
+    plain<<<unsigned(lanes), warps * 32, smem, s>>>(g);
     return cudaGetLastError();
 }
 
@@ -441,21 +599,39 @@ Args args_of(const mgs_gated_shape &sh) {
 template <typename T, bool POS>
 cudaError_t fwd_go(const mgs_gated_shape &sh, Args &g, cudaStream_t s) {
     const int64_t lanes = sh.B * g.strips;
-    return pairs(g, sizeof(T)) ? run(gated_fwd_kernel<T, POS, true, false>, gated_fwd_kernel<T, POS, true, true>, g, lanes, s)
-                               : run(gated_fwd_kernel<T, POS, false, false>, gated_fwd_kernel<T, POS, false, true>, g, lanes, s);
+    auto go = [&](auto how) {
+        return run(gated_fwd_kernel<T, POS, how.value, false>, gated_fwd_kernel<T, POS, how.value, true>, g, lanes,
+                   {sizeof(Exchange<kFwdWarps, false>), sizeof(Exchange<kFwdWarps, true>)}, kFwdWarps, 2 * 2 * kTile * 64 * sizeof(T), s);
+    };
+    const Copy how = copy_of(g, sizeof(T));
+    if (how == kCopy16) return go(std::integral_constant<Copy, kCopy16>());
+    if constexpr (sizeof(T) == 2)
+        if (how == kCopyAny) return go(std::integral_constant<Copy, kCopyAny>());
+    return go(std::integral_constant<Copy, kCopy4>());
 }
 template <typename T, bool POS>
 cudaError_t bwd_go(const mgs_gated_shape &sh, Args &g, cudaStream_t s) {
     const int64_t lanes = sh.B * g.strips;
-    return pairs(g, sizeof(T)) ? run(gated_bwd_kernel<T, POS, true, false>, gated_bwd_kernel<T, POS, true, true>, g, lanes, s)
-                               : run(gated_bwd_kernel<T, POS, false, false>, gated_bwd_kernel<T, POS, false, true>, g, lanes, s);
+    auto go = [&](auto how) {
+        return run(gated_bwd_kernel<T, POS, how.value, false>, gated_bwd_kernel<T, POS, how.value, true>, g, lanes,
+                   {sizeof(Exchange<kBwdWarps, false>), sizeof(Exchange<kBwdWarps, true>)}, kBwdWarps,
+                   2 * 3 * kTile * 64 * sizeof(T) + sizeof(float4) * 2 * kBwdWarps * 32, s);
+    };
+    const Copy how = copy_of(g, sizeof(T));
+    if (how == kCopy16) return go(std::integral_constant<Copy, kCopy16>());
+    if constexpr (sizeof(T) == 2)
+        if (how == kCopyAny) return go(std::integral_constant<Copy, kCopyAny>());
+    return go(std::integral_constant<Copy, kCopy4>());
 }
 template <typename T, bool POS>
 cudaError_t step_go(const mgs_gated_shape &sh, Args &g, float *state, const int32_t *slots, int64_t nslots,
                     cudaStream_t s) {
     g.kt = g.vt = 0;
     g.out = state;
-    auto *fn = pairs(g, sizeof(T)) ? gated_step_kernel<T, POS, true> : gated_step_kernel<T, POS, false>;
+    // in pairs: neighbours in one load each (single elements for fp32 rows that start at 4 bytes alone)
+    const Copy how = copy_of(g, sizeof(T));
+    auto *fn = how == kCopy16 || (how == kCopy4 && sizeof(T) == 2) ? gated_step_kernel<T, POS, true>
+                                                                   : gated_step_kernel<T, POS, false>;
     fn<<<unsigned((sh.B * g.strips + 3) / 4), 128, 0, s>>>((const T *)g.gate, (const T *)g.value, state, slots, nslots,
                                                           (T *)g.h, sh.B, sh.D, g.strips, g.kb, g.vb);
     return cudaGetLastError();
@@ -468,14 +644,17 @@ cudaError_t step_go(const mgs_gated_shape &sh, Args &g, float *state, const int3
                           : (sh.positive ? go<float, true>(__VA_ARGS__) : go<float, false>(__VA_ARGS__)))
 
 cudaError_t launch_gated_fwd(const mgs_gated_shape &sh, const void *gate, const void *value, const float *h0, void *h,
-                             float *hT, float *carries, cudaStream_t s) {
+                             float *hT, float *carries, const DevCtl &ctl, cudaStream_t s) {
     Args g = args_of(sh);
+    g.ctl = ctl;
     g.gate = gate, g.value = value, g.in = h0, g.h = h, g.out = hT, g.carries = carries;
     return MGS_BY_TYPE(fwd_go, sh, g, s);
 }
 cudaError_t launch_gated_bwd(const mgs_gated_shape &sh, const void *gate, const void *value, const float *carries,
-                             const void *gh, const float *ghT, void *dgate, void *dvalue, float *dh0, cudaStream_t s) {
+                             const void *gh, const float *ghT, void *dgate, void *dvalue, float *dh0,
+                             const DevCtl &ctl, cudaStream_t s) {
     Args g = args_of(sh);
+    g.ctl = ctl;
     g.gate = gate, g.value = value, g.carries = const_cast<float *>(carries), g.gh = gh, g.in = ghT;
     g.dgate = dgate, g.dvalue = dvalue, g.out = dh0, g.gb = sh.gh_stride[0], g.gt = sh.gh_stride[1];
     return MGS_BY_TYPE(bwd_go, sh, g, s);

@@ -107,9 +107,10 @@ cudaError_t launch_clip(const void *const *in, void *const *out, const int64_t *
                         int64_t count, float max_norm, float *norm, void *ws, cudaStream_t s);
 
 cudaError_t launch_gated_fwd(const mgs_gated_shape &sh, const void *gate, const void *value, const float *h0, void *h,
-                             float *hT, float *carries, cudaStream_t s);
+                             float *hT, float *carries, const DevCtl &ctl, cudaStream_t s);
 cudaError_t launch_gated_bwd(const mgs_gated_shape &sh, const void *gate, const void *value, const float *carries,
-                             const void *gh, const float *ghT, void *dgate, void *dvalue, float *dh0, cudaStream_t s);
+                             const void *gh, const float *ghT, void *dgate, void *dvalue, float *dh0,
+                             const DevCtl &ctl, cudaStream_t s);
 cudaError_t launch_gated_step(const mgs_gated_shape &sh, const void *gate, const void *value, float *state,
                               const int32_t *slots, int64_t nslots, void *h, cudaStream_t s);
 
