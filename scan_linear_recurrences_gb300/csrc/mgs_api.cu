@@ -1126,8 +1126,8 @@ static mgs_status qk_sizes(const mgs_qk_norm_shape *sh, bool bwd, bool positions
     if (!mul_ok(sh->B, sh->T, &bt) || !mul_ok(bt, sh->Hq, &nq) || !mul_ok(bt, sh->Hk, &nk) ||
         nq > INT64_MAX / (64 * 256 * 4) || nk > INT64_MAX / (64 * 256 * 4) || sh->positions > INT64_MAX / (64 * 256 * 4))
         return MGS_ERR_INVALID_ARG;
-    // 32-bit grids; positions are 32-bit
-    if (sh->Hq > INT32_MAX / 2 || sh->Hk > INT32_MAX / 2 || bt > (int64_t(1) << 40)) return MGS_ERR_UNSUPPORTED;
+    // 32-bit counts of tokens and of a warp's heads
+    if (sh->Hq > (1 << 20) || sh->Hk > (1 << 20) || bt > INT32_MAX / 2) return MGS_ERR_UNSUPPORTED;
     *z = {nq * sh->D * es, nk * sh->D * es, 0, 0, 0, 0, sh->positions * sh->rotary * 4, 0};
     if (nq + nk == 0) return MGS_OK;
     auto span = [&](const int64_t (&st)[3], int64_t H, int64_t *out) {

@@ -28,36 +28,6 @@ namespace {
 constexpr int kTile = MGS_GATED_SPAN;  // a tile begins at a kept state
 constexpr int kMaxCluster = 16;
 
-// Two channels in one register pair: sm_100 has fp32 sums and products of pairs
-struct f2 {
-    unsigned long long v;
-};
-__device__ __forceinline__ f2 pair(float x, float y) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ float2 both(f2 p) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p.v));
-    return r;
-}
-__device__ __forceinline__ f2 operator+(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ f2 operator*(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-
 __device__ __forceinline__ float rcp_approx(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -339,12 +309,15 @@ __device__ __forceinline__ void meet(uint64_t *bar, bool init) {
     }
 }
 
-constexpr int kFwdWarps = 4, kFwdSteps = kTile / kFwdWarps;
-constexpr int kBwdWarps = 8, kBwdSteps = kTile / kBwdWarps;
+// Warps of a block (of 64 / warps steps each).  The forward's maps cost the less the
+// longer a warp's steps; in fp32, with twice the bytes, more warps pay.
+template <typename T>
+constexpr int kFwdWarps = sizeof(T) == 2 ? 4 : 8;
+constexpr int kBwdWarps = 8;
 
 template <typename T, bool POS, Copy HOW, bool CL>
-__global__ void __launch_bounds__(kFwdWarps * 32, 4) gated_fwd_kernel(const __grid_constant__ Args g) {
-    constexpr int W = kFwdWarps, L = kFwdSteps;
+__global__ void __launch_bounds__(kFwdWarps<T> * 32, 512 / (kFwdWarps<T> * 32)) gated_fwd_kernel(const __grid_constant__ Args g) {
+    constexpr int W = kFwdWarps<T>, L = kTile / W;
     constexpr bool VEC = HOW == kCopy16 || (HOW == kCopy4 && sizeof(T) == 2);
     using Ex = Exchange<W, CL>;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -425,7 +398,7 @@ __global__ void __launch_bounds__(kFwdWarps * 32, 4) gated_fwd_kernel(const __gr
 
 template <typename T, bool POS, Copy HOW, bool CL>
 __global__ void __launch_bounds__(kBwdWarps * 32, 2) gated_bwd_kernel(const __grid_constant__ Args g) {
-    constexpr int W = kBwdWarps, L = kBwdSteps;
+    constexpr int W = kBwdWarps, L = kTile / W;
     constexpr bool VEC = HOW == kCopy16 || (HOW == kCopy4 && sizeof(T) == 2);
     using Ex = Exchange<W, CL>;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -571,16 +544,21 @@ Copy copy_of(const Args &g, int es) {
     return es == 4 || (pairs && rows(4)) ? kCopy4 : kCopyAny;
 }
 
-// Blocks of a cluster: enough for two blocks an SM, as far as there are tiles
-int cluster_of(int64_t lanes, int tiles) {
+// Blocks of a cluster, up to `blocks` in all and as far as there are tiles.  Their
+// exchange costs more the more they are, a lack of warps too.  Forward in bf16, four
+// blocks an SM at a time, up to twice as many (training, 8 x 4096 x 2048: 92 us with 4
+// a cluster, 101 with 2, 110 with 8).  Forward in fp32 and backward, two blocks an SM,
+// as many (fp32, 16 x 4096 x 1024: forward 151 us with 1 a cluster, 174 with 2; backward
+// 236 and 316, in bf16 160 and 190).
+int cluster_of(int64_t lanes, int tiles, int blocks) {
     int c = 1;
-    while (c < kMaxCluster && lanes * c < 304 && c < tiles) c *= 2;
+    while (c < kMaxCluster && 2 * c * lanes <= blocks && c < tiles) c *= 2;
     return c;
 }
 
 template <typename F, typename C>
-cudaError_t run(F *plain, C *clustered, Args &g, int64_t lanes, const size_t (&exchange)[2], int warps, size_t ring, cudaStream_t s) {
-    g.cluster = cluster_of(lanes, g.tiles);
+cudaError_t run(F *plain, C *clustered, Args &g, int64_t lanes, const size_t (&exchange)[2], int blocks, int warps, size_t ring, cudaStream_t s) {
+    g.cluster = cluster_of(lanes, g.tiles, blocks);
     const size_t smem = ring + (g.cluster > 1 ? exchange[1] : exchange[0]);
     const void *fn = g.cluster > 1 ? reinterpret_cast<const void *>(clustered) : reinterpret_cast<const void *>(plain);
     const cudaError_t e = ensure_smem_attr(fn, int(smem));
@@ -601,7 +579,8 @@ cudaError_t fwd_go(const mgs_gated_shape &sh, Args &g, cudaStream_t s) {
     const int64_t lanes = sh.B * g.strips;
     auto go = [&](auto how) {
         return run(gated_fwd_kernel<T, POS, how.value, false>, gated_fwd_kernel<T, POS, how.value, true>, g, lanes,
-                   {sizeof(Exchange<kFwdWarps, false>), sizeof(Exchange<kFwdWarps, true>)}, kFwdWarps, 2 * 2 * kTile * 64 * sizeof(T), s);
+                   {sizeof(Exchange<kFwdWarps<T>, false>), sizeof(Exchange<kFwdWarps<T>, true>)},
+                   sizeof(T) == 2 ? 1216 : 304, kFwdWarps<T>, 2 * 2 * kTile * 64 * sizeof(T), s);
     };
     const Copy how = copy_of(g, sizeof(T));
     if (how == kCopy16) return go(std::integral_constant<Copy, kCopy16>());
@@ -614,7 +593,7 @@ cudaError_t bwd_go(const mgs_gated_shape &sh, Args &g, cudaStream_t s) {
     const int64_t lanes = sh.B * g.strips;
     auto go = [&](auto how) {
         return run(gated_bwd_kernel<T, POS, how.value, false>, gated_bwd_kernel<T, POS, how.value, true>, g, lanes,
-                   {sizeof(Exchange<kBwdWarps, false>), sizeof(Exchange<kBwdWarps, true>)}, kBwdWarps,
+                   {sizeof(Exchange<kBwdWarps, false>), sizeof(Exchange<kBwdWarps, true>)}, 304, kBwdWarps,
                    2 * 3 * kTile * 64 * sizeof(T) + sizeof(float4) * 2 * kBwdWarps * 32, s);
     };
     const Copy how = copy_of(g, sizeof(T));
