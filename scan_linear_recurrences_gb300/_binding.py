@@ -139,9 +139,10 @@ def exported_symbols():
 def _ptr(x):
     if x is None:
         return None
-    if isinstance(x, int):
+    try:
+        return x.data_ptr()
+    except AttributeError:  # an address
         return x
-    return x.data_ptr()
 
 
 def _stream(s):

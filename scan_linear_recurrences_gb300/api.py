@@ -507,9 +507,10 @@ def clip_grad_norm(grads, max_norm, out=None, stream=None):
 
 
 # ---------------------------------------------------------------- gated linear recurrence
-def _there(device):
-    """The context in which calls go to this device (the library launches on the current one)."""
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _elsewhere(t):
+    """Whether t is on another GPU than the current one, on which the library would launch."""
+    here = t.get_device()
+    return here >= 0 and here != torch._C._cuda_getDevice()
 
 
 def _inner(t, name):
@@ -521,6 +522,13 @@ def _inner(t, name):
 
 
 def _gated_shape(gate, value, positive, grad_h=None):
+    try:  # the usual case in few steps
+        dt, shape, here, (kb, kt, kd), (vb, vt, vd) = gate.dtype, gate.shape, gate.get_device(), gate.stride(), value.stride()
+        if (dt in _DTYPES and here >= 0 and value.dtype is dt and value.shape == shape and value.get_device() == here
+                and kd == 1 and vd == 1 and grad_h is None):
+            return _b.mgs_gated_shape(*shape, _DTYPES[dt], bool(positive), (kb, kt), (vb, vt))
+    except (AttributeError, ValueError):
+        pass
     if not isinstance(gate, torch.Tensor) or gate.dim() != 3:
         raise ValueError("gate must be a [B,T,D] tensor")
     _check_typed(gate, "gate", None, None, dense=False)
@@ -540,29 +548,35 @@ def gated_scan_fwd(gate, value, h0=None, positive=True, want_carries=False, stre
     h0 [B,D] fp32 or None.  A gate of -inf masks its step, whatever its value; +inf starts the state anew.  The
     state is fp32, h is rounded once.  Returns (h [B,T,D], h_T [B,D] fp32), and the carries that gated_scan_bwd
     takes when want_carries."""
-    shape, (B, T, D), dev = _gated_shape(gate, value, positive), gate.shape, gate.device
+    shape = _gated_shape(gate, value, positive)
+    if _elsewhere(gate):
+        with torch.cuda.device(gate.device):
+            return gated_scan_fwd(gate, value, h0, positive, want_carries, stream)
+    (B, T, D), dev = gate.shape, gate.device
     if h0 is not None:
         _check_typed(h0, "h0", (B, D), torch.float32, device=dev)
     h = torch.empty((B, T, D), dtype=gate.dtype, device=dev)
     hT = torch.empty((B, D), dtype=torch.float32, device=dev)
     carries = torch.empty((B, -(-T // _b.GATED_SPAN), D), dtype=torch.float32, device=dev) if want_carries else None
-    with _there(dev):
-        _b.mgs_gated_scan_fwd(shape, gate, value, h0, h, hT, carries, stream)
+    _b.mgs_gated_scan_fwd(shape, gate, value, h0, h, hT, carries, stream)
     return (h, hT, carries) if want_carries else (h, hT)
 
 
 def gated_scan_bwd(gate, value, carries, grad_h, grad_hT=None, positive=True, need_dh0=True, stream=None):
     """Gradients of gated_scan_fwd for L = <grad_h, h> + <grad_hT, h_T>: (dgate, dvalue, dh0), dh0 None unless
     needed.  carries: the forward's; h itself is rebuilt from them."""
-    shape, (B, T, D), dev = _gated_shape(gate, value, positive, grad_h), gate.shape, gate.device
+    shape = _gated_shape(gate, value, positive, grad_h)
+    if _elsewhere(gate):
+        with torch.cuda.device(gate.device):
+            return gated_scan_bwd(gate, value, carries, grad_h, grad_hT, positive, need_dh0, stream)
+    (B, T, D), dev = gate.shape, gate.device
     _check_typed(carries, "carries", (B, -(-T // _b.GATED_SPAN), D), torch.float32, device=dev)
     if grad_hT is not None:
         _check_typed(grad_hT, "grad_hT", (B, D), torch.float32, device=dev)
     dgate = torch.empty((B, T, D), dtype=gate.dtype, device=dev)
     dvalue = torch.empty_like(dgate)
     dh0 = torch.empty((B, D), dtype=torch.float32, device=dev) if need_dh0 else None
-    with _there(dev):
-        _b.mgs_gated_scan_bwd(shape, gate, value, carries, grad_h, grad_hT, dgate, dvalue, dh0, stream)
+    _b.mgs_gated_scan_bwd(shape, gate, value, carries, grad_h, grad_hT, dgate, dvalue, dh0, stream)
     return dgate, dvalue, dh0
 
 
@@ -570,11 +584,37 @@ def gated_scan_step(gate, value, state, slots=None, positive=True, out=None, str
     """One step of each of B sequences: gate, value [B,D], the cache of states [N,D] fp32, updated in place.
     slots [B] int32: each sequence's place in the cache (None: b itself); a place outside 0..N-1 marks an empty row,
     whose output is 0.  Returns h [B,D]."""
+    try:  # the usual case in few steps: a call on one token takes less time on the GPU than its checks
+        (B, D), dt, here, (kb, kd), (vb, vd), N = gate.shape, gate.dtype, gate.get_device(), gate.stride(), value.stride(), len(state)
+        usual = (dt in _DTYPES and here >= 0 and value.dtype is dt and value.shape == gate.shape and value.get_device() == here
+                 and kd == 1 and vd == 1 and state.dtype is torch.float32 and state.shape == (N, D)
+                 and state.is_contiguous() and state.get_device() == here and out is None
+                 and (N >= B if slots is None else slots.dtype is torch.int32 and slots.shape == (B,)
+                      and slots.is_contiguous() and slots.get_device() == here))
+    except (AttributeError, TypeError, ValueError):
+        usual = False
+    if not usual:
+        B, D, N = _gated_step_check(gate, value, state, slots, out)
+        dt, (kb, _), (vb, _) = gate.dtype, gate.stride(), value.stride()
+    if _elsewhere(gate):
+        with torch.cuda.device(gate.device):
+            return gated_scan_step(gate, value, state, slots, positive, out, stream)
+    written = (state,) if out is None else (state, out)
+    if out is None:
+        out = torch.empty((B, D), dtype=dt, device=gate.device)
+    shape = _b.mgs_gated_shape(B, 1, D, _DTYPES[dt], bool(positive), (kb, 0), (vb, 0))
+    _b.mgs_gated_scan_step(shape, gate, value, state, slots, N, out, stream)
+    _written(written)
+    return out
+
+
+def _gated_step_check(gate, value, state, slots, out):
     if not isinstance(gate, torch.Tensor) or gate.dim() != 2:
         raise ValueError("gate must be a [B,D] tensor")
     (B, D), dt, dev = gate.shape, gate.dtype, gate.device
     _check_typed(gate, "gate", None, None, dense=False)
     _check_typed(value, "value", gate.shape, dt, dense=False, device=dev)
+    _inner(gate, "gate"), _inner(value, "value")
     if not isinstance(state, torch.Tensor) or state.dim() != 2:
         raise ValueError("state must be a [N,D] tensor")
     N = state.shape[0]
@@ -583,17 +623,9 @@ def gated_scan_step(gate, value, state, slots=None, positive=True, out=None, str
         _check_typed(slots, "slots", (B,), torch.int32, device=dev)
     elif N < B:
         raise ValueError(f"{B} sequences without slots need a cache of as many states, not {N}")
-    written = (state,) if out is None else (state, out)
-    if out is None:
-        out = torch.empty((B, D), dtype=dt, device=dev)
-    else:
+    if out is not None:
         _check_typed(out, "out", (B, D), dt, device=dev)
-    shape = _b.mgs_gated_shape(B, 1, D, _DTYPES[dt], bool(positive), (*_inner(gate, "gate"), 0),
-                               (*_inner(value, "value"), 0))
-    with _there(dev):
-        _b.mgs_gated_scan_step(shape, gate, value, state, slots, N, out, stream)
-    _written(written)
-    return out
+    return B, D, N
 
 
 # ---------------------------------------------------------------- norm of queries and keys, with the position's rotation
@@ -609,6 +641,38 @@ def rotary_table(positions, rotary, base=10000.0, device="cuda"):
 
 def _qk_shape(q, k, q_weight, k_weight, table, positions, eps, interleaved, grad_q=None, grad_k=None):
     """The checked arguments as the C struct.  One token of each sequence ([B,H,D]) is T = 1."""
+    try:  # the usual case in few steps
+        qs, ks, dt, here, nd = q.shape, k.shape, q.dtype, q.get_device(), len(q.shape)
+        D, one = qs[-1], nd == 3
+        usual = (dt in _DTYPES and here >= 0 and k.dtype is dt and k.get_device() == here and 3 <= nd <= 4 and len(ks) == nd
+                 and qs[0] == ks[0] and (one or qs[1] == ks[1]) and ks[-1] == D and D % 8 == 0 and 8 <= D <= 256)
+        for w in (q_weight, k_weight):
+            usual = usual and (w is None or w.dtype is dt and w.shape == (D,) and w.get_device() == here and w.is_contiguous())
+        rows, R = 0, 0
+        if table is not None:
+            rows, R = table.shape
+            usual = (usual and table.dtype is torch.float32 and table.is_contiguous() and table.get_device() == here
+                     and R % 8 == 0 and 8 <= R <= D and (positions is not None or rows >= (1 if one else qs[1])))
+        at = (0, 0)
+        if positions is not None:
+            usual = (usual and table is not None and positions.dtype is torch.int32 and positions.shape == qs[:-2]
+                     and positions.get_device() == here)
+            at = (positions.stride(0), 0) if one else positions.stride()
+        none = (0, 0, 0)
+        strides = [none if t is None else t.stride() for t in (q, k, grad_q, grad_k)]
+        for t, like, st in ((q, q, strides[0]), (k, k, strides[1]), (grad_q, q, strides[2]), (grad_k, k, strides[3])):
+            usual = usual and (t is None or st[-1] == 1 and (t is like or t.dtype is dt and t.shape == like.shape
+                                                            and t.get_device() == here))
+    except (AttributeError, IndexError, TypeError, ValueError):
+        usual = False
+    if not usual:
+        return _qk_shape_checked(q, k, q_weight, k_weight, table, positions, eps, interleaved, grad_q, grad_k)
+    strides = [st if st is none else (st[0], 0, st[1]) if one else st[:3] for st in strides]
+    return _b.mgs_qk_norm_shape(qs[0], 1 if one else qs[1], qs[-2], ks[-2], rows, D, _DTYPES[dt], R, bool(interleaved), eps,
+                                *strides, at)
+
+
+def _qk_shape_checked(q, k, q_weight, k_weight, table, positions, eps, interleaved, grad_q, grad_k):
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
         raise ValueError("q must be a [B,T,Hq,D] or [B,Hq,D] tensor")
     dt, dev, D, lead = q.dtype, q.device, q.shape[-1], q.shape[:-2]
@@ -660,10 +724,12 @@ def qk_norm_fwd(q, k, q_weight=None, k_weight=None, table=None, positions=None, 
     int32 (None: 0..T-1); one outside the table marks an empty row, whose outputs and gradients are 0.  Sums and
     rotations are fp32, outputs are rounded once.  Returns dense (q, k)."""
     shape = _qk_shape(q, k, q_weight, k_weight, table, positions, eps, interleaved)
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return qk_norm_fwd(q, k, q_weight, k_weight, table, positions, eps, interleaved, stream)
     yq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     yk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    with _there(q.device):
-        _b.mgs_qk_norm_fwd(shape, q, k, q_weight, k_weight, table, positions, yq, yk, stream)
+    _b.mgs_qk_norm_fwd(shape, q, k, q_weight, k_weight, table, positions, yq, yk, stream)
     return yq, yk
 
 
@@ -673,13 +739,15 @@ def qk_norm_bwd(q, k, q_weight, k_weight, grad_q, grad_k, table=None, positions=
     if grad_q is None or grad_k is None:
         raise ValueError("grad_q and grad_k must be tensors")
     shape = _qk_shape(q, k, q_weight, k_weight, table, positions, eps, interleaved, grad_q, grad_k)
+    if _elsewhere(q):
+        with torch.cuda.device(q.device):
+            return qk_norm_bwd(q, k, q_weight, k_weight, grad_q, grad_k, table, positions, eps, interleaved, stream)
     dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     dk = torch.empty(k.shape, dtype=k.dtype, device=k.device)
     dqw, dkw = (None if w is None else torch.empty_like(w) for w in (q_weight, k_weight))
     n = _b.mgs_qk_norm_bwd_workspace_size(shape)
-    with _there(q.device):
-        _b.mgs_qk_norm_bwd(shape, q, k, q_weight, k_weight, grad_q, grad_k, table, positions, dq, dk, dqw, dkw,
-                           _scratch(n, q.device, stream), n, stream)
+    _b.mgs_qk_norm_bwd(shape, q, k, q_weight, k_weight, grad_q, grad_k, table, positions, dq, dk, dqw, dkw,
+                       _scratch(n, q.device, stream), n, stream)
     return dq, dk, dqw, dkw
 
 
@@ -700,11 +768,13 @@ def embedding_fwd(tokens, weight, scale=1.0, stream=None):
     if weight.dim() != 2:
         raise ValueError("weight must be a [V,D] tensor")
     _check_tokens(tokens, weight.device)
+    if _elsewhere(weight):
+        with torch.cuda.device(weight.device):
+            return embedding_fwd(tokens, weight, scale, stream)
     V, D = weight.shape
     out = torch.empty((*tokens.shape, D), dtype=weight.dtype, device=weight.device)
-    with _there(weight.device):
-        _b.mgs_embedding_fwd(tokens, _TOKENS[tokens.dtype], weight, scale, out, tokens.numel(), V, D,
-                             _DTYPES[weight.dtype], stream)
+    _b.mgs_embedding_fwd(tokens, _TOKENS[tokens.dtype], weight, scale, out, tokens.numel(), V, D, _DTYPES[weight.dtype],
+                         stream)
     return out
 
 
@@ -721,11 +791,13 @@ def embedding_bwd(tokens, grad, V, scale=1.0, stream=None):
     except RuntimeError:
         raise ValueError("grad must have rows a fixed distance apart") from None
     apart, = _inner(rows, "grad")
+    if _elsewhere(grad):
+        with torch.cuda.device(grad.device):
+            return embedding_bwd(tokens, grad, V, scale, stream)
     dW = torch.empty((V, D), dtype=grad.dtype, device=grad.device)
     n = _b.mgs_embedding_bwd_workspace_size(N, V, D)
-    with _there(grad.device):
-        _b.mgs_embedding_bwd(tokens, _TOKENS[tokens.dtype], rows, apart, scale, dW, N, V, D, _DTYPES[grad.dtype],
-                             _scratch(n, grad.device, stream), n, stream)
+    _b.mgs_embedding_bwd(tokens, _TOKENS[tokens.dtype], rows, apart, scale, dW, N, V, D, _DTYPES[grad.dtype],
+                         _scratch(n, grad.device, stream), n, stream)
     return dW
 
 

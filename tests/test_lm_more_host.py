@@ -289,7 +289,6 @@ class _Calls:
         monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
         monkeypatch.setattr(torch, "empty", new)
         monkeypatch.setattr(api, "_check_typed", lambda *a, **k: None)
-        monkeypatch.setattr(api, "_there", lambda device: contextlib.nullcontext())
         for name in ("gated_scan_fwd", "gated_scan_bwd", "gated_scan_step", "qk_norm_fwd", "qk_norm_bwd", "embedding_fwd",
                      "embedding_bwd"):
             monkeypatch.setattr(b, "mgs_" + name, lambda *a, _name=name: self.calls.append((_name, a)))
