@@ -524,9 +524,11 @@ def _inner(t, name):
 def _gated_shape(gate, value, positive, grad_h=None):
     try:  # the usual case in few steps
         dt, shape, here, (kb, kt, kd), (vb, vt, vd) = gate.dtype, gate.shape, gate.get_device(), gate.stride(), value.stride()
+        gb, gt, gd = (0, 0, 1) if grad_h is None else grad_h.stride()
         if (dt in _DTYPES and here >= 0 and value.dtype is dt and value.shape == shape and value.get_device() == here
-                and kd == 1 and vd == 1 and grad_h is None):
-            return _b.mgs_gated_shape(*shape, _DTYPES[dt], bool(positive), (kb, kt), (vb, vt))
+                and kd == 1 and vd == 1 and gd == 1
+                and (grad_h is None or grad_h.dtype is dt and grad_h.shape == shape and grad_h.get_device() == here)):
+            return _b.mgs_gated_shape(*shape, _DTYPES[dt], bool(positive), (kb, kt), (vb, vt), (gb, gt))
     except (AttributeError, ValueError):
         pass
     if not isinstance(gate, torch.Tensor) or gate.dim() != 3:
