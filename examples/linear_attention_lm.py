@@ -1,7 +1,10 @@
 """A small language model on linear attention: trained, then used token by token.
 
-Every layer is  r += attention(norm(r)),  r += mlp(norm(r))  with
+Tokens are looked up by embedding, whose gradient is summed by sorted tokens; every
+layer is  r += attention(norm(r)),  r += mlp(norm(r))  with
   * rms_norm, which adds the residual and normalises in one pass,
+  * qk_norm, which normalises each head of the queries and keys (to unit length to
+    begin with, so that the state stays bounded) and turns half of it by its position,
   * linear_attention with a learned decay for each head and step,
   * clip_grad_norm over all gradients before the optimiser's step,
 and answers with
@@ -28,6 +31,8 @@ FP8_MAX = 448.0
 class Layer(torch.nn.Module):
     def __init__(self, width, heads, kv_heads, D):
         super().__init__()
+        self.q_norm = torch.nn.Parameter(torch.full((D,), D ** -0.5))
+        self.k_norm = torch.nn.Parameter(torch.full((D,), D ** -0.5))
         self.H, self.Hk, self.D = heads, kv_heads, D
         self.norm1 = torch.nn.Parameter(torch.ones(width))
         self.norm2 = torch.nn.Parameter(torch.ones(width))
@@ -40,19 +45,19 @@ class Layer(torch.nn.Module):
             self.gate.weight.mul_(0.1)
             self.gate.bias.copy_(torch.linspace(-2.3, -7.0, heads))
 
-    def project(self, y):
-        """q, k (of unit length, so that the state stays bounded), v as views of one product, and the decay's logarithm."""
+    def project(self, y, norm, table, at=None):
+        """q, k (normed and turned), v as a view of one product, and the decay's logarithm."""
         q, k, v = self.qkv(y).unflatten(-1, (-1, self.D)).split([self.Hk, self.Hk, self.H], -2)
-        g = -F.softplus(self.gate(y).float())
-        return F.normalize(q.float(), dim=-1).to(y.dtype), F.normalize(k.float(), dim=-1).to(y.dtype), v, g
+        q, k = norm(q, k, self.q_norm, self.k_norm, table, at)
+        return q, k, v, -F.softplus(self.gate(y).float())
 
-    def forward(self, x, res):
+    def forward(self, x, res, table):
         """x: what the layer before adds to the residual stream res (None: x is the stream)."""
         if res is None:
             y, res = api.rms_norm(x, self.norm1), x
         else:
             y, res = api.rms_norm(x, self.norm1, res)
-        o, _ = api.linear_attention(*self.project(y), scale=1.0)
+        o, _ = api.linear_attention(*self.project(y, api.qk_norm, table), scale=1.0)
         y, res = api.rms_norm(self.out(o.flatten(-2)), self.norm2, res)
         return self.down(F.gelu(self.up(y))), res
 
@@ -64,13 +69,13 @@ class Layer(torch.nn.Module):
         self.up8 = (w / self.up_scale[:, None]).to(torch.float8_e4m3fn)
 
     @torch.no_grad()
-    def serve(self, x, res, states, slots):
+    def serve(self, x, res, states, slots, table, at):
         """A prompt (x [B,T,width]: the states are left in their slots) or one token of each sequence ([B,width])."""
         if res is None:
             y, res = api.rms_norm_fwd(x, self.norm1)[0], x
         else:
             y, res, _ = api.rms_norm_fwd(x, self.norm1, res)
-        q, k, v, g = self.project(y)
+        q, k, v, g = self.project(y, api.qk_norm_fwd, table, at)
         if x.dim() == 3:
             o, S = api.linear_attention_fwd(q, k, v, g, scale=1.0, want_state=True)
             states[slots.long()] = S
@@ -83,8 +88,9 @@ class Layer(torch.nn.Module):
 
 
 class Model(torch.nn.Module):
-    def __init__(self, vocab=64, width=256, layers=2, heads=4, kv_heads=2, D=64):
+    def __init__(self, vocab=64, width=256, layers=2, heads=4, kv_heads=2, D=64, length=4096):
         super().__init__()
+        self.table = api.rotary_table(length, D // 2)  # stays in fp32, beside the model's parameters
         self.embed = torch.nn.Embedding(vocab, width)
         self.layers = torch.nn.ModuleList(Layer(width, heads, kv_heads, D) for _ in range(layers))
         self.norm = torch.nn.Parameter(torch.ones(width))
@@ -92,22 +98,27 @@ class Model(torch.nn.Module):
         torch.nn.init.normal_(self.embed.weight, std=0.5)
 
     def forward(self, tokens):
-        x, res = self.embed(tokens), None
+        x, res = api.embedding(tokens, self.embed.weight), None
         for layer in self.layers:
-            x, res = layer(x, res)
+            x, res = layer(x, res, self.table)
         return self.head(api.rms_norm(x, self.norm, res)[0])
 
     def cache(self, users):
-        """A state for each layer, user and head."""
+        """A state for each layer, user and head, and how many tokens each user's have seen."""
         L = self.layers[0]
-        return [torch.zeros(users, L.H, L.D, L.D, device=self.norm.device) for _ in self.layers]
+        states = [torch.zeros(users, L.H, L.D, L.D, device=self.norm.device) for _ in self.layers]
+        return [*states, torch.zeros(users, dtype=torch.int32, device=self.norm.device)]
 
     @torch.no_grad()
     def serve(self, tokens, cache, slots):
         """Logits after the prompts [B,T], or after one more token [B], of the users in `slots` (int32 [B])."""
-        x, res = self.embed(tokens), None
-        for layer, states in zip(self.layers, cache):
-            x, res = layer.serve(x, res, states, slots)
+        *states, seen = cache
+        users = slots.long()
+        at = None if tokens.dim() == 2 else seen[users]  # (a prompt begins at the first place)
+        seen[users] = tokens.shape[1] if at is None else at + 1
+        x, res = api.embedding_fwd(tokens.contiguous(), self.embed.weight), None
+        for layer, S in zip(self.layers, states):
+            x, res = layer.serve(x, res, S, slots, self.table, at)
         return self.head(api.rms_norm_fwd(x, self.norm, res)[0])
 
 

@@ -2,7 +2,8 @@
 matrix_scan, parallel_scan_log), forward and backward, and operators of
 language models built on recurrences (linear attention with a decay for each
 head, the RMS norm with the residual's addition, clipping by the global norm
-of the gradients), as a C-ABI CUDA library (libmgscan, include/mgscan.h) with a
+of the gradients, minGRU's gated recurrence, the norm of queries and keys with
+their rotation, the embedding), as a C-ABI CUDA library (libmgscan, include/mgscan.h) with a
 thin Python binding.
 
 ``_binding`` mirrors the C entry points one to one; ``api`` adds tensor-level
