@@ -715,3 +715,95 @@ def test_on_a_named_stream(address):
         for i in range(2):
             for a, w in zip(g[i], want[i]):
                 assert torch.equal(a, w)
+
+
+# ---------------------------------------------------------------- sizes and offsets past 32 bits
+def _far(shape, dtype, apart, gen):
+    """A tensor whose batch rows lie `apart` elements from each other."""
+    buf = torch.empty((shape[0] - 1) * apart + shape[1:].numel(), dtype=dtype, device="cuda")
+    t = buf.as_strided(shape, (apart, *torch.empty(shape[1:]).stride()))
+    return t.copy_(torch.randn(shape, generator=gen, device="cuda"))
+
+
+def test_offsets_past_32_bits():
+    gen = torch.Generator(device="cuda").manual_seed(61)
+    apart = (1 << 31) + 64
+    # rows of inputs 2^31 elements apart
+    gate, value, gh = (_far(torch.Size((2, 70, 64)), BF16, apart, gen) for _ in range(3))
+    near = [x.contiguous() for x in (gate, value, gh)]
+    a, w = api.gated_scan_fwd(gate, value, want_carries=True), api.gated_scan_fwd(*near[:2], want_carries=True)
+    assert all(torch.equal(x, y) for x, y in zip(a, w))
+    for x, y in zip(api.gated_scan_bwd(gate, value, a[2], gh), api.gated_scan_bwd(*near[:2], w[2], near[2])):
+        assert torch.equal(x, y)
+    del gate, value, gh
+    q, gq = (_far(torch.Size((2, 9, 2, 64)), BF16, apart, gen) for _ in range(2))
+    table, c, gc = api.rotary_table(9, 64), q.contiguous(), gq.contiguous()
+    for x, y in zip(api.qk_norm_fwd(q, q, table=table), api.qk_norm_fwd(c, c, table=table)):
+        assert torch.equal(x, y)
+    for x, y in zip(api.qk_norm_bwd(q, q, None, None, gq, gq, table)[:2], api.qk_norm_bwd(c, c, None, None, gc, gc, table)[:2]):
+        assert torch.equal(x, y)
+    del q, gq
+    # a cache and a table of more than 2^31 elements
+    N, D = 530000, 4096
+    state = torch.empty(N, D, device="cuda")
+    slots = torch.tensor([N - 1, 3, N - 2], dtype=torch.int32, device="cuda")
+    state[slots.long()] = torch.randn(3, D, generator=gen, device="cuda")
+    small = state[slots.long()].clone()
+    k, v = torch.randn(3, D, generator=gen, device="cuda"), torch.randn(3, D, generator=gen, device="cuda")
+    assert torch.equal(api.gated_scan_step(k, v, state, slots), api.gated_scan_step(k, v, small))
+    assert torch.equal(state[slots.long()], small)
+    W = state  # (the same memory as a table)
+    tokens = torch.tensor([N - 1, 0, N - 2, N - 1, 3], device="cuda")
+    assert torch.equal(api.embedding_fwd(tokens, W), W[tokens])
+    del W, state
+    g = torch.randn(5, D, generator=gen, device="cuda").to(BF16)
+    dW = api.embedding_bwd(tokens, g, N)
+    assert torch.equal(dW[N - 1], (g[0].float() + g[3].float()).to(BF16)) and torch.equal(dW[N - 2], g[2])
+    assert torch.equal(dW[3], g[4]) and dW.count_nonzero().item() == sum(dW[i].count_nonzero().item() for i in (0, 3, N - 2, N - 1))
+
+
+def test_large_vocabulary():
+    # more rows than the blocks mark at a time
+    V, N = 6_000_000, 5000
+    gen = torch.Generator(device="cuda").manual_seed(62)
+    tokens = torch.randint(0, V, (N,), generator=gen, device="cuda")
+    tokens[:700] = V - 1
+    g = torch.randn(N, 8, generator=gen, device="cuda")
+    dW = api.embedding_bwd(tokens, g, V)
+    ref = torch.zeros(V, 8, dtype=torch.float64, device="cuda").index_add_(0, tokens, g.double())
+    mag = torch.zeros(V, 8, dtype=torch.float64, device="cuda").index_add_(0, tokens, g.double().abs())
+    assert ((dW.double() - ref).abs() <= 703 * U * mag).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_tokens_of_one_width(dtype):
+    # more places than a block keeps in registers, odd rows; and bf16 rows that start anywhere
+    d = m.embed_inputs(70001, 3000, 33, dtype, seed=63)
+    _embed_check(d, 3000, 1.0)
+
+
+@pytest.mark.parametrize("B,T,D", [(70000, 3, 2), (1, 100001, 1), (3, 64, 5000)])
+def test_gated_many_of_one_dimension(B, T, D):
+    # 400 u of the largest covers memories of 100 steps whatever the length; one channel's reference on the GPU
+    d = m.gated_inputs(B, T, D, seed=64, shift=1.0)
+    if T < 1000:
+        _gated_check(_gated_run(_views(d)), m.gated_ref(d))
+        return
+    c = _views(d)
+    got = _gated_run(c)
+    whole = m.gated_ref({**d, "gate": d["gate"][:, -3000:], "value": d["value"][:, -3000:], "grad_h": d["grad_h"][:, -3000:],
+                         "h0": got["h"][:, -3001].cpu()})
+    for n in ("h", "dgate", "dvalue"):  # the end, from the state that the call itself has there
+        m.check_each(n, got[n][:, -3000:], whole[n], 400 * U * whole[n].abs().amax())
+
+
+def test_gradients_of_some_leaves():
+    d = _views(m.gated_inputs(2, 40, 16, seed=65))
+    gate = d["gate"].clone().requires_grad_()
+    h, hT = api.gated_scan(gate, d["value"])
+    hT.sum().backward()
+    ref = m.gated_ref({**{n: (x.cpu() if isinstance(x, torch.Tensor) else x) for n, x in d.items()}, "h0": None,
+                       "grad_h": torch.zeros(2, 40, 16), "grad_hT": torch.ones(2, 16)})
+    m.check_each("dgate", gate.grad, ref["dgate"], 400 * U * ref["dgate"].abs().amax(1, keepdim=True))
+    with torch.no_grad():
+        assert not api.gated_scan(gate, d["value"])[0].requires_grad

@@ -360,3 +360,25 @@ def test_gradients_that_do_not_arrive_are_zeros(monkeypatch):
     shape, *_ = calls.calls[-1][1]
     assert shape == b.mgs_qk_norm_shape(2, 4, 2, 2, 0, 8, b.MGS_F32, 0, 0, 1e-6, (64, 16, 8), (64, 16, 8), (0, 0, 0),
                                         (64, 16, 8))
+
+
+def test_calls_on_another_device_go_there(monkeypatch):
+    # the library launches on the current device: a call on another one's tensors makes that one current
+    calls = _Calls(monkeypatch)
+    there = []
+
+    @contextlib.contextmanager
+    def device(d):
+        there.append(d)
+        yield
+        there.append("back")
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(api, "_elsewhere", lambda t: not there or there[-1] == "back")
+    x, q, t = torch.zeros(2, 4, 8), torch.zeros(2, 4, 2, 16), torch.zeros(2, 4).long()
+    for i, call in enumerate((lambda: api.gated_scan_fwd(x, x), lambda: api.gated_scan_bwd(x, x, x[:, :1], x),
+                              lambda: api.gated_scan_step(x[:, 0], x[:, 0], x[:, 1].clone()), lambda: api.qk_norm_fwd(q, q),
+                              lambda: api.qk_norm_bwd(q, q, None, None, q, q), lambda: api.embedding_fwd(t, x[0]),
+                              lambda: api.embedding_bwd(t, x, 5))):
+        call()
+        assert there[2 * i:] == [torch.device("cpu"), "back"] and len(calls.calls) == i + 1
