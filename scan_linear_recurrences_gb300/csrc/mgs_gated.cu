@@ -165,8 +165,9 @@ __device__ __forceinline__ void copies_close() { asm volatile("cp.async.commit_g
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Rows 0 .. n - 1 of L of 64 channels (zeros behind them and past channel D), `stride`
-// apart, from `src` (the sequence's first row needed, channel d0) to a warp's [L][64].
+// Rows 0 .. n - 1 of L of 64 channels (zeros behind them and past the `left` that are
+// there), `stride` apart, from `src` (any address of the tensor where n <= 0) to a
+// warp's [L][64].
 template <typename T, int L, Copy HOW>
 __device__ __forceinline__ void copy_rows(T *dst, const T *src, int64_t stride, int n, int64_t left) {
     const int lane = threadIdx.x & 31;
@@ -175,6 +176,14 @@ __device__ __forceinline__ void copy_rows(T *dst, const T *src, int64_t stride, 
         const int row = lane / PER, col = lane % PER * V;
         const bool in = col < left;
         const T *p = src + row * stride + col;
+        if (n >= L && left >= 64) {
+#pragma unroll
+            for (int i = 0; i < L / ROWS; ++i) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst + (i * ROWS + row) * 64 + col)), "l"(p) : "memory");
+                p += ROWS * stride;
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < L / ROWS; ++i) {
             const bool ok = in && i * ROWS + row < n;
@@ -249,27 +258,40 @@ __device__ __forceinline__ void push16(void *slot, uint64_t *bar, unsigned rank,
 template <int W, bool CL>
 struct Exchange {
     float4 maps[2][W][32];
-    float4 slots[CL ? 2 : 1][CL ? kMaxCluster : 1][32];
+    float4 slots[2][kMaxCluster][32];
     alignas(16) uint64_t bar[2];
 };
+// Without a cluster: what the last warp leaves to the next tile.  (Two blocks of the
+// backward in fp32 fill an SM's shared memory to the last KB.)
+template <int W>
+struct Exchange<W, false> {
+    float4 maps[2][W][32];
+    unsigned long long pass[2][32];
+};
 
-// The state that enters this warp's steps: `s` (the state before the round) through
-// the maps before this warp's, and s through all of them for the next round.  REV:
-// the maps act from the last warp, and the last block of the cluster, to the first.
-template <bool REV, int W, bool CL>
-__device__ __forceinline__ f2 enter(Exchange<W, CL> &ex, int turn, int phase, f2 &s, int warp, int lane, int cluster,
-                                    unsigned rank, const DevCtl &ctl, bool &lost) {
-    f2 mine = s;
-    if constexpr (!CL) {
+// The state that enters this warp's steps: what the last warp had after its own in the
+// tile before, through the maps of this tile's warps before this one (REV: the maps act
+// from the last warp to the first).
+template <bool REV, int W>
+__device__ __forceinline__ f2 enter(const Exchange<W, false> &ex, int turn, int warp, int lane) {
+    f2 s{ex.pass[turn ^ 1][lane]};
 #pragma unroll
-        for (int i = 0; i < W; ++i) {
-            const int j = REV ? W - 1 - i : i;
-            if (j == warp) mine = s;
+    for (int i = 0; i < W - 1; ++i) {
+        const int j = REV ? W - 1 - i : i;
+        if (REV ? j > warp : j < warp) {
             const Map m = Map::unpack(ex.maps[turn][j][lane]);
             s = fma2(m.A, s, m.H);
         }
-        return mine;
     }
+    return s;
+}
+// In a cluster: `s` (the state before the round, which every block keeps) through the
+// maps of the blocks before this one and of the warps before this one, and s through
+// all of them for the next round.
+template <bool REV, int W>
+__device__ __forceinline__ f2 enter(Exchange<W, true> &ex, int turn, int phase, f2 &s, int warp, int lane, int cluster,
+                                    unsigned rank, const DevCtl &ctl, bool &lost) {
+    f2 mine = s;
     Map before{pair(1.f, 1.f), pair(0.f, 0.f)}, all = before;
 #pragma unroll
     for (int i = 0; i < W; ++i) {
@@ -296,11 +318,11 @@ __device__ __forceinline__ f2 enter(Exchange<W, CL> &ex, int turn, int phase, f2
 }
 
 // all blocks of the cluster have their barriers (before the first push), or are done with each other's memory
-template <bool CL>
-__device__ __forceinline__ void meet(uint64_t *bar, bool init) {
+template <bool CL, typename E>
+__device__ __forceinline__ void meet(E &ex, bool init) {
     if constexpr (CL) {
         if (init && threadIdx.x == 0) {
-            mbar_init(&bar[0], 1), mbar_init(&bar[1], 1);
+            mbar_init(&ex.bar[0], 1), mbar_init(&ex.bar[1], 1);
             fence_barrier_init();
         }
         __syncthreads();
@@ -342,13 +364,15 @@ __global__ void __launch_bounds__(kFwdWarps<T> * 32, 512 / (kFwdWarps<T> * 32)) 
         copies_close();
     };
     fetch(int(rank), 0);
-    meet<CL>(ex.bar, true);
+    meet<CL>(ex, true);
     f2 s = pair(0.f, 0.f);
     if (g.in) {
         Two<float, VEC> x;
         x.load(g.in + b * g.D + at.d, at.ok);
         s = pair(x.u.x, x.u.y);
     }
+    if constexpr (!CL)
+        if (warp == 0) ex.pass[1][lane] = s.v;
     int turn = 0, phase = 0;
     bool lost = false;
     for (int first = 0; first < g.tiles; first += cluster) {
@@ -380,20 +404,32 @@ __global__ void __launch_bounds__(kFwdWarps<T> * 32, 512 / (kFwdWarps<T> * 32)) 
         }
         ex.maps[turn][warp][lane] = m.pack();
         __syncthreads();
-        f2 x = enter<false>(ex, turn, phase, s, warp, lane, cluster, rank, g.ctl, lost);
+        f2 x;
+        if constexpr (CL) x = enter<false>(ex, turn, phase, s, warp, lane, cluster, rank, g.ctl, lost);
+        else x = enter<false>(ex, turn, warp, lane);
         if (g.carries && warp == 0 && tile < g.tiles)
             Two<float, VEC>::store(g.carries + (b * g.tiles + tile) * g.D + at.d, both(x), at.ok);
         T *to = h + t0 * g.D;
+        auto run = [&](auto all) {  // all: every step is there
 #pragma unroll
-        for (int i = 0; i < L; ++i) {
-            x = fma2(a[i], x, c[i]);
-            Two<T, VEC>::store(to + i * g.D, both(x), i < n ? at.ok : 0);
+            for (int i = 0; i < L; ++i) {
+                x = fma2(a[i], x, c[i]);
+                Two<T, VEC>::store(to, both(x), all.value || i < n ? at.ok : 0);
+                to += g.D;
+            }
+        };
+        if (n >= L) run(std::true_type());
+        else run(std::false_type());
+        if constexpr (!CL) {
+            s = x;
+            if (warp == W - 1) ex.pass[turn][lane] = x.v;
         }
         phase ^= turn;
         turn ^= 1;
     }
-    if (g.out && rank == 0 && warp == 0) Two<float, VEC>::store(g.out + b * g.D + at.d, both(s), at.ok);
-    meet<CL>(ex.bar, false);
+    // (steps behind the last one leave the state as it is)
+    if (g.out && rank == 0 && warp == (CL ? 0 : W - 1)) Two<float, VEC>::store(g.out + b * g.D + at.d, both(s), at.ok);
+    meet<CL>(ex, false);
 }
 
 template <typename T, bool POS, Copy HOW, bool CL>
@@ -424,20 +460,22 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) gated_bwd_kernel(const __gr
         if (there && n > 0) {
             copy_rows<T, L, HOW>(to, gate + t0 * g.kt, g.kt, n, left);
             copy_rows<T, L, HOW>(to + L * 64, value + t0 * g.vt, g.vt, n, left);
-            copy_rows<T, L, HOW>(to + 2 * L * 64, gh + t0 * g.gt, g.gt, n, left);
         }
+        if (tile >= 0) copy_rows<T, L, HOW>(to + 2 * L * 64, gh + (n > 0 ? t0 * g.gt : 0), g.gt, n, left);  // (zeros where no step is)
         copies_close();
     };
     int first = (g.tiles - 1) / cluster * cluster, turn = 0, phase = 0;
     bool lost = false;
     fetch(first + int(rank), 0);
-    meet<CL>(ex.bar, true);
+    meet<CL>(ex, true);
     f2 flow = pair(0.f, 0.f);
     if (g.in) {
         Two<float, VEC> x;
         x.load(g.in + b * g.D + at.d, at.ok);
         flow = pair(x.u.x, x.u.y);
     }
+    if constexpr (!CL)
+        if (warp == 0) ex.pass[1][lane] = flow.v;
     for (; first >= 0; first -= cluster) {
         const int tile = first + int(rank), t0 = tile * kTile + warp * L, n = g.T - t0;
         f2 x = pair(next.u.x, next.u.y);
@@ -462,7 +500,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) gated_bwd_kernel(const __gr
             Two<T, VEC> y;
             y.load(from + (2 * L + i) * 64, 3);
             const float2 u = y.get();
-            return i < n ? pair(u.x, u.y) : pair(0.f, 0.f);
+            return pair(u.x, u.y);
         };
         Map m{a[0], z[0] * c[0]}, r{a[0], pair(0.f, 0.f)};
 #pragma unroll
@@ -476,9 +514,12 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) gated_bwd_kernel(const __gr
         maps[turn][warp][lane] = m.pack();
         ex.maps[turn][warp][lane] = r.pack();
         __syncthreads();
-        for (int j = 0; j < warp; ++j) {
-            const Map o = Map::unpack(maps[turn][j][lane]);
-            x = fma2(o.A, x, o.H);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            if (j < warp) {
+                const Map o = Map::unpack(maps[turn][j][lane]);
+                x = fma2(o.A, x, o.H);
+            }
         }
 #pragma unroll
         for (int i = 0; i < L; ++i) {  // c <- z a (c - h before)
@@ -486,21 +527,32 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) gated_bwd_kernel(const __gr
             x = x + w;
             c[i] = a[i] * w;
         }
-        f2 f = enter<true>(ex, turn, phase, flow, warp, lane, cluster, rank, g.ctl, lost);
-        T *to_k = dgate + t0 * g.D, *to_v = dvalue + t0 * g.D;
+        f2 f;
+        if constexpr (CL) f = enter<true>(ex, turn, phase, flow, warp, lane, cluster, rank, g.ctl, lost);
+        else f = enter<true>(ex, turn, warp, lane);
+        T *to_k = dgate + (t0 + L - 1) * g.D, *to_v = dvalue + (t0 + L - 1) * g.D;
+        auto run = [&](auto all) {  // all: every step is there
 #pragma unroll
-        for (int i = L - 1; i >= 0; --i) {
-            const f2 lam = gradient(i) + f;
-            const int ok = i < n ? at.ok : 0;
-            Two<T, VEC>::store(to_v + i * g.D, both(lam * zs[i]), ok);
-            Two<T, VEC>::store(to_k + i * g.D, both(lam * c[i]), ok);
-            f = a[i] * lam;
+            for (int i = L - 1; i >= 0; --i) {
+                const f2 lam = gradient(i) + f;
+                const int ok = all.value || i < n ? at.ok : 0;
+                Two<T, VEC>::store(to_v, both(lam * zs[i]), ok);
+                Two<T, VEC>::store(to_k, both(lam * c[i]), ok);
+                f = a[i] * lam;
+                to_v -= g.D, to_k -= g.D;
+            }
+        };
+        if (n >= L) run(std::true_type());
+        else run(std::false_type());
+        if constexpr (!CL) {
+            flow = f;
+            if (warp == 0) ex.pass[turn][lane] = f.v;
         }
         phase ^= turn;
         turn ^= 1;
     }
     if (g.out && rank == 0 && warp == 0) Two<float, VEC>::store(g.out + b * g.D + at.d, both(flow), at.ok);
-    meet<CL>(ex.bar, false);
+    meet<CL>(ex, false);
 }
 
 template <typename T, bool POS, bool VEC>
@@ -544,21 +596,26 @@ Copy copy_of(const Args &g, int es) {
     return es == 4 || (pairs && rows(4)) ? kCopy4 : kCopyAny;
 }
 
-// Blocks of a cluster, up to `blocks` in all and as far as there are tiles.  Their
-// exchange costs more the more they are, a lack of warps too.  Forward in bf16, four
-// blocks an SM at a time, up to twice as many (training, 8 x 4096 x 2048: 92 us with 4
-// a cluster, 101 with 2, 110 with 8).  Forward in fp32 and backward, two blocks an SM,
-// as many (fp32, 16 x 4096 x 1024: forward 151 us with 1 a cluster, 174 with 2; backward
-// 236 and 316, in bf16 160 and 190).
-int cluster_of(int64_t lanes, int tiles, int blocks) {
+// Blocks of a cluster.  Their exchange costs more the more they are, a lack of warps
+// too: none where the lanes alone keep the SMs busy (`enough` of them), else as many as
+// make up to `blocks`, as far as there are tiles.  2048 steps of 2048 channels in bf16, us:
+//   lanes            32    64    96   128   160   192   256
+//   forward, 1     29.1  29.1  29.3  29.6  43.8  44.3  44.7
+//            4     13.9  18.2  22.3  27.4  37.9  42.5  48.7
+//           16     10.5  20.3  28.8  37.8  49.0  57.6  74.5
+//   backward, 1    40.6  40.8  41.9  43.4  74.2  74.5  74.8
+//             4    17.0  25.9  40.8  51.5  64.0  75.1  88.7
+int cluster_of(int64_t lanes, int tiles, int enough, int blocks) {
     int c = 1;
-    while (c < kMaxCluster && 2 * c * lanes <= blocks && c < tiles) c *= 2;
+    if (lanes >= enough) return c;
+    while (c < kMaxCluster && c < tiles && 2 * c * lanes <= blocks) c *= 2;
     return c;
 }
 
 template <typename F, typename C>
-cudaError_t run(F *plain, C *clustered, Args &g, int64_t lanes, const size_t (&exchange)[2], int blocks, int warps, size_t ring, cudaStream_t s) {
-    g.cluster = cluster_of(lanes, g.tiles, blocks);
+cudaError_t run(F *plain, C *clustered, Args &g, int64_t lanes, const size_t (&exchange)[2], int enough, int blocks,
+                int warps, size_t ring, cudaStream_t s) {
+    g.cluster = cluster_of(lanes, g.tiles, enough, blocks);
     const size_t smem = ring + (g.cluster > 1 ? exchange[1] : exchange[0]);
     const void *fn = g.cluster > 1 ? reinterpret_cast<const void *>(clustered) : reinterpret_cast<const void *>(plain);
     const cudaError_t e = ensure_smem_attr(fn, int(smem));
@@ -580,7 +637,7 @@ cudaError_t fwd_go(const mgs_gated_shape &sh, Args &g, cudaStream_t s) {
     auto go = [&](auto how) {
         return run(gated_fwd_kernel<T, POS, how.value, false>, gated_fwd_kernel<T, POS, how.value, true>, g, lanes,
                    {sizeof(Exchange<kFwdWarps<T>, false>), sizeof(Exchange<kFwdWarps<T>, true>)},
-                   sizeof(T) == 2 ? 1216 : 304, kFwdWarps<T>, 2 * 2 * kTile * 64 * sizeof(T), s);
+                   sizeof(T) == 2 ? 228 : 76, sizeof(T) == 2 ? 640 : 256, kFwdWarps<T>, 2 * 2 * kTile * 64 * sizeof(T), s);
     };
     const Copy how = copy_of(g, sizeof(T));
     if (how == kCopy16) return go(std::integral_constant<Copy, kCopy16>());
@@ -593,7 +650,7 @@ cudaError_t bwd_go(const mgs_gated_shape &sh, Args &g, cudaStream_t s) {
     const int64_t lanes = sh.B * g.strips;
     auto go = [&](auto how) {
         return run(gated_bwd_kernel<T, POS, how.value, false>, gated_bwd_kernel<T, POS, how.value, true>, g, lanes,
-                   {sizeof(Exchange<kBwdWarps, false>), sizeof(Exchange<kBwdWarps, true>)}, 304, kBwdWarps,
+                   {sizeof(Exchange<kBwdWarps, false>), sizeof(Exchange<kBwdWarps, true>)}, 76, 256, kBwdWarps,
                    2 * 3 * kTile * 64 * sizeof(T) + sizeof(float4) * 2 * kBwdWarps * 32, s);
     };
     const Copy how = copy_of(g, sizeof(T));
