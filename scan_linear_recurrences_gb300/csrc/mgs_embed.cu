@@ -16,7 +16,9 @@
 //      to the workspace.  Memory writes alone at 4.9 TB/s, with the sums' reads
 //      beside them at more: the zeros are not written in a kernel of their own;
 //   3. the long runs' parts are joined, a block a run.
-// No atomics on the sums: the order is that of the tokens alone.
+// No atomics on the sums: the order is that of the tokens alone.  32768 tokens of a
+// text, 50000 x 2048 in bf16: forward 26 us, backward 71 (sort 19 beside the zeros, joins
+// 7; with the zeros in a kernel beside the sort alone 96).
 #include "mgs_cluster.cuh"
 #include "mgs_launch.h"
 #include "mgs_lm.h"
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) embed_sum_kernel(const __grid_
 // its eight warps add up a run's parts, each every eighth one.
 constexpr int kJoinChunks = 16, kJoinCols = 128;
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 8)
     embed_join_kernel(const unsigned *__restrict__ keys, const float *__restrict__ part, float scale,
                       T *__restrict__ dw, int N, int V, int64_t D, int chunk) {
     __shared__ float joined[8][kJoinCols];
@@ -436,7 +438,7 @@ __global__ void __launch_bounds__(256)
         }
         // part 0 is c's tail, parts 1.. the heads of the chunks behind it
         float s[4] = {};
-#pragma unroll 8
+#pragma unroll 2
         for (int m = warp; m <= len; m += 8) {
             const float *row = part + (2 * (c + m) + (m == 0)) * D + d0;
 #pragma unroll
