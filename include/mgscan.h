@@ -466,9 +466,9 @@ mgs_status mgs_clip_grad_norm(const void *const *grads, void *const *outs, const
 
 /* Sizes, types and strides of the gated linear recurrence.  Strides are in
  * elements, in the order batch, step; the D channels of a step are contiguous.
- * Any stride >= 0; outputs are dense [B][T][D].  The vector kernels want channels
- * in pairs: an even D, even strides, and tensors that start at multiples of two
- * elements; others run slower ones. */
+ * Any stride >= 0; outputs are dense [B][T][D].  Rows (of every tensor) that start at
+ * multiples of 16 bytes are the fastest; then those at 4 bytes, with channels in
+ * pairs in bf16; bf16 rows that start anywhere run slower. */
 typedef struct mgs_gated_shape {
     int64_t B, T, D;
     int32_t dtype;        /* of gate, value, h and their gradients            */
@@ -482,8 +482,12 @@ typedef struct mgs_gated_shape {
  *     h_t = (1 - z_t) h_{t-1} + z_t c_t,   c = value, or c = g(value):
  *     g(v) = v + 1/2 for v >= 0, sigmoid(v) below (minGRU's positive candidate),
  * h_0 = h0 (zeros when NULL).  The state is fp32 throughout, h is rounded once.  A
- * gate of -infinity masks the step: the state stays as it is, whatever the value,
- * and the gradients of both are zero; +infinity starts the state anew from c.
+ * gate below -88 (-infinity, the type's lowest) masks the step: z is zero, the state
+ * stays as it is, whatever the value, and the gradients of both are zero; +infinity
+ * starts the state anew from c.  An infinity or NaN reaches its own channel from its
+ * step on (a gradient's: up to its step); an infinite state may go on as NaN.
+ * Precision: fp32 outputs and gradients err by 1e-7 to 2e-7 (relative L2, gates to 5 in
+ * magnitude), bf16 ones by their one rounding.
  * In: gate, value [B][T][D], h0 [B][D] fp32 (nullable).
  * Out: h [B][T][D]; h_T [B][D] fp32 (nullable), the state after the last step;
  *     carries [B][ceil(T / MGS_GATED_SPAN)][D] fp32 (nullable: only the backward
@@ -510,9 +514,9 @@ mgs_status mgs_gated_scan_step(const mgs_gated_shape *shape, const void *gate, c
 
 /* Sizes, types and strides of the norm of queries and keys.  Strides are in
  * elements, in the order batch, step, head (positions: batch, step); the D
- * elements of a head are contiguous.  Any stride >= 0; tensors that start at
- * multiples of four elements, with strides that are so too, run the vector
- * kernels, others slower ones.  Outputs are dense [B][T][heads][D]. */
+ * elements of a head are contiguous.  Any stride >= 0; heads that start at
+ * multiples of 16 bytes in all tensors run the fastest kernels.  Outputs are dense
+ * [B][T][heads][D].  B T up to 2^30, Hq and Hk up to 2^20. */
 typedef struct mgs_qk_norm_shape {
     int64_t B, T, Hq, Hk;
     int64_t positions;    /* rows of the table                                */
