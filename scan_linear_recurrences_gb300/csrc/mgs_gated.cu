@@ -16,9 +16,9 @@
 // The backward rebuilds h within a tile from the state that the forward kept before
 // it (the carries), so that h is not read: five tensors pass, not six.
 //
-// Bound by instructions (27 a step and channel forward, 50 backward; MUFU and selects
-// take more than an issue slot each) before memory.  8 x 4096 x 2048 in bf16: forward 86
-// us (4.7 TB/s, with the carries), backward 146 (4.6); 16 x 4096 x 1024 in fp32: 127 (6.3)
+// Bound by instructions (28 a step and channel forward, 50 backward; MUFU and selects
+// take more than an issue slot each) before memory.  8 x 4096 x 2048 in bf16: forward 83
+// us (5.0 TB/s, with the carries), backward 146 (4.6); 16 x 4096 x 1024 in fp32: 127 (6.3)
 // and 230 (5.8); 1 x 16384 x 2048 in bf16, clusters of 16: 61 (3.3).
 #include <type_traits>
 
@@ -336,15 +336,20 @@ __device__ __forceinline__ void meet(E &ex, bool init) {
     }
 }
 
-// Warps of a block (of 64 / warps steps each).  The forward's maps cost the less the
-// longer a warp's steps; in fp32, with twice the bytes, more warps pay.
-template <typename T>
-constexpr int kFwdWarps = sizeof(T) == 2 ? 4 : 8;
+// Warps of a forward's block and steps of its tile.  The maps cost the less the longer a
+// warp's steps: 16 in bf16, by four warps in a cluster (more of them to a round; a prompt
+// of 16384 x 2048 takes 61 us, 64 with eight), by eight without (8 x 4096 x 2048: 83 us,
+// 86 with four); 8 in fp32, where, with twice the bytes, more warps pay.
+template <typename T, bool CL>
+constexpr int kFwdWarps = sizeof(T) == 2 && CL ? 4 : 8;
+template <typename T, bool CL>
+constexpr int kFwdTile = kFwdWarps<T, CL> * (sizeof(T) == 2 ? 16 : 8);
 constexpr int kBwdWarps = 8;
 
 template <typename T, bool POS, Copy HOW, bool CL>
-__global__ void __launch_bounds__(kFwdWarps<T> * 32, 512 / (kFwdWarps<T> * 32)) gated_fwd_kernel(const __grid_constant__ Args g) {
-    constexpr int W = kFwdWarps<T>, L = kTile / W;
+__global__ void __launch_bounds__(kFwdWarps<T, CL> * 32, 512 / (kFwdWarps<T, CL> * 32))
+    gated_fwd_kernel(const __grid_constant__ Args g) {
+    constexpr int W = kFwdWarps<T, CL>, TILE = kFwdTile<T, CL>, L = TILE / W;
     constexpr bool VEC = HOW == kCopy16 || (HOW == kCopy4 && sizeof(T) == 2);
     using Ex = Exchange<W, CL>;
     extern __shared__ __align__(16) unsigned char smem[];
@@ -360,7 +365,7 @@ __global__ void __launch_bounds__(kFwdWarps<T> * 32, 512 / (kFwdWarps<T> * 32)) 
     T *h = (T *)g.h + b * g.T * g.D + at.d;
     T *mine = ring + warp * (2 * 2 * L * 64);
     auto fetch = [&](int tile, int stage) {
-        const int t0 = tile * kTile + warp * L, n = g.T - t0;
+        const int t0 = tile * TILE + warp * L, n = g.T - t0;
         T *to = mine + stage * (2 * L * 64);
         if (tile < g.tiles && n > 0) {
             copy_rows<T, L, HOW>(to, gate + t0 * g.kt, g.kt, n, left);
@@ -381,7 +386,7 @@ __global__ void __launch_bounds__(kFwdWarps<T> * 32, 512 / (kFwdWarps<T> * 32)) 
     int turn = 0, phase = 0;
     bool lost = false;
     for (int first = 0; first < g.tiles; first += cluster) {
-        const int tile = first + int(rank), t0 = tile * kTile + warp * L, n = g.T - t0;
+        const int tile = first + int(rank), t0 = tile * TILE + warp * L, n = g.T - t0;
         __syncwarp();  // the other stage has been read
         fetch(tile + cluster, turn ^ 1);
         copies_wait<1>();
@@ -412,8 +417,8 @@ __global__ void __launch_bounds__(kFwdWarps<T> * 32, 512 / (kFwdWarps<T> * 32)) 
         f2 x;
         if constexpr (CL) x = enter<false>(ex, turn, phase, s, warp, lane, cluster, rank, g.ctl, lost);
         else x = enter<false>(ex, turn, warp, lane);
-        if (g.carries && warp == 0 && tile < g.tiles)
-            Two<float, VEC>::store(g.carries + (b * g.tiles + tile) * g.D + at.d, both(x), at.ok);
+        if (g.carries && warp * L % kTile == 0 && n > 0)
+            Two<float, VEC>::store(g.carries + (b * ((g.T - 1) / kTile + 1) + t0 / kTile) * g.D + at.d, both(x), at.ok);
         T *to = h + t0 * g.D;
         auto run = [&](auto all) {  // all: every step is there
 #pragma unroll
@@ -605,44 +610,63 @@ Copy copy_of(const Args &g, int es) {
 // too: none where the lanes alone keep the SMs busy (`enough` of them), else as many as
 // make up to `blocks`, as far as there are tiles.  2048 steps of 2048 channels in bf16, us:
 //   lanes            32    64    96   128   160   192   256
-//   forward, 1     29.1  29.1  29.3  29.6  43.8  44.3  44.7
+//   forward, 1     24.2  24.3  24.5  24.5  42.3  43.1  43.7
 //            4     13.9  18.2  22.3  27.4  37.9  42.5  48.7
 //           16     10.5  20.3  28.8  37.8  49.0  57.6  74.5
 //   backward, 1    40.6  40.8  41.9  43.4  74.2  74.5  74.8
 //             4    17.0  25.9  40.8  51.5  64.0  75.1  88.7
-int cluster_of(int64_t lanes, int tiles, int enough, int blocks) {
+int cluster_of(int64_t lanes, int64_t steps, int enough, int blocks) {
     int c = 1;
     if (lanes >= enough) return c;
-    while (c < kMaxCluster && c < tiles && 2 * c * lanes <= blocks) c *= 2;
+    while (c < kMaxCluster && c * kTile < steps && 2 * c * lanes <= blocks) c *= 2;
     return c;
+}
+template <typename T>
+int fwd_cluster(int64_t lanes, int64_t steps) {
+    if (sizeof(T) == 4) return cluster_of(lanes, steps, 76, 256);
+    return cluster_of(lanes, steps, lanes <= 152 ? 108 : 228, 640);  // (a lane on most SMs, or two)
+}
+
+// A kernel's form, without a cluster and with one: warps, steps of a tile, bytes of shared memory.
+struct Form {
+    int warps, tile;
+    size_t smem;
+};
+template <typename T, bool CL>
+Form fwd_form() {
+    constexpr int W = kFwdWarps<T, CL>, tile = kFwdTile<T, CL>;
+    return {W, tile, sizeof(Exchange<W, CL>) + 2 * 2 * tile * 64 * sizeof(T)};
+}
+template <typename T, bool CL>
+Form bwd_form() {
+    constexpr int W = kBwdWarps;
+    return {W, kTile, sizeof(Exchange<W, CL>) + sizeof(float4) * 2 * W * 32 + 2 * 3 * kTile * 64 * sizeof(T)};
 }
 
 template <typename F, typename C>
-cudaError_t run(F *plain, C *clustered, Args &g, int64_t lanes, const size_t (&exchange)[2], int enough, int blocks,
-                int warps, size_t ring, cudaStream_t s) {
-    g.cluster = cluster_of(lanes, g.tiles, enough, blocks);
-    const size_t smem = ring + (g.cluster > 1 ? exchange[1] : exchange[0]);
-    const void *fn = g.cluster > 1 ? reinterpret_cast<const void *>(clustered) : reinterpret_cast<const void *>(plain);
-    const cudaError_t e = ensure_smem_attr(fn, int(smem));
+cudaError_t run(F *plain, C *clustered, Args &g, int64_t lanes, int cluster, Form f, cudaStream_t s) {
+    g.cluster = cluster, g.tiles = int((int64_t(g.T) + f.tile - 1) / f.tile);
+    const void *fn = cluster > 1 ? reinterpret_cast<const void *>(clustered) : reinterpret_cast<const void *>(plain);
+    const cudaError_t e = ensure_smem_attr(fn, int(f.smem));
     if (e != cudaSuccess) return e;
-    if (g.cluster > 1) return launch_cluster(clustered, lanes * g.cluster, warps * 32, smem, g.cluster, s, g);
-    plain<<<unsigned(lanes), warps * 32, smem, s>>>(g);
+    if (cluster > 1) return launch_cluster(clustered, lanes * cluster, f.warps * 32, f.smem, cluster, s, g);
+    plain<<<unsigned(lanes), f.warps * 32, f.smem, s>>>(g);
     return cudaGetLastError();
 }
 
 Args args_of(const mgs_gated_shape &sh) {
     Args g = {};
-    g.D = sh.D, g.T = int(sh.T), g.tiles = int((sh.T + kTile - 1) / kTile), g.strips = int((sh.D + 63) / 64);
+    g.D = sh.D, g.T = int(sh.T), g.strips = int((sh.D + 63) / 64);
     g.kb = sh.gate_stride[0], g.kt = sh.gate_stride[1], g.vb = sh.value_stride[0], g.vt = sh.value_stride[1];
     return g;
 }
 template <typename T, bool POS>
 cudaError_t fwd_go(const mgs_gated_shape &sh, Args &g, cudaStream_t s) {
     const int64_t lanes = sh.B * g.strips;
+    const int cluster = fwd_cluster<T>(lanes, sh.T);
     auto go = [&](auto how) {
-        return run(gated_fwd_kernel<T, POS, how.value, false>, gated_fwd_kernel<T, POS, how.value, true>, g, lanes,
-                   {sizeof(Exchange<kFwdWarps<T>, false>), sizeof(Exchange<kFwdWarps<T>, true>)},
-                   sizeof(T) == 2 ? 228 : 76, sizeof(T) == 2 ? 640 : 256, kFwdWarps<T>, 2 * 2 * kTile * 64 * sizeof(T), s);
+        return run(gated_fwd_kernel<T, POS, how.value, false>, gated_fwd_kernel<T, POS, how.value, true>, g, lanes, cluster,
+                   cluster > 1 ? fwd_form<T, true>() : fwd_form<T, false>(), s);
     };
     const Copy how = copy_of(g, sizeof(T));
     if (how == kCopy16) return go(std::integral_constant<Copy, kCopy16>());
@@ -653,10 +677,10 @@ cudaError_t fwd_go(const mgs_gated_shape &sh, Args &g, cudaStream_t s) {
 template <typename T, bool POS>
 cudaError_t bwd_go(const mgs_gated_shape &sh, Args &g, cudaStream_t s) {
     const int64_t lanes = sh.B * g.strips;
+    const int cluster = cluster_of(lanes, sh.T, 76, 256);
     auto go = [&](auto how) {
-        return run(gated_bwd_kernel<T, POS, how.value, false>, gated_bwd_kernel<T, POS, how.value, true>, g, lanes,
-                   {sizeof(Exchange<kBwdWarps, false>), sizeof(Exchange<kBwdWarps, true>)}, 76, 256, kBwdWarps,
-                   2 * 3 * kTile * 64 * sizeof(T) + sizeof(float4) * 2 * kBwdWarps * 32, s);
+        return run(gated_bwd_kernel<T, POS, how.value, false>, gated_bwd_kernel<T, POS, how.value, true>, g, lanes, cluster,
+                   cluster > 1 ? bwd_form<T, true>() : bwd_form<T, false>(), s);
     };
     const Copy how = copy_of(g, sizeof(T));
     if (how == kCopy16) return go(std::integral_constant<Copy, kCopy16>());

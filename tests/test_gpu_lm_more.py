@@ -92,6 +92,15 @@ def test_gated(B, T, D, dtype, positive):
     _gated_check(_gated_run(_views(d)), m.gated_ref(d))
 
 
+@pytest.mark.parametrize("D", [64, 63, 66])
+@pytest.mark.parametrize("T", [1, 64, 65, 127, 129, 192, 335])
+@pytest.mark.parametrize("B", [120, 250])
+def test_gated_many_lanes(B, T, D):
+    # no clusters, and in bf16 a forward whose tiles hold two of the kept states
+    d = m.gated_inputs(B // -(-D // 64), T, D, BF16, h0=T % 2 == 0, seed=B + T + D)
+    _gated_check(_gated_run(_views(d)), m.gated_ref(d))
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_gated_long_memory(dtype):
     # one channel each of a memory of a step, some hundred and some thousand steps, over a long sequence: with gates
