@@ -532,9 +532,9 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) gated_bwd_kernel(const __gr
             }
         }
 #pragma unroll
-        for (int i = 0; i < L; ++i) {  // c <- z a (c - h before)
-            const f2 w = z[i] * fma2(x, pair(-1.f, -1.f), c[i]);
-            x = x + w;
+        for (int i = 0; i < L; ++i) {  // c <- z a (c - h before); x as the forward has it (x + z (c - x) keeps the
+            const f2 w = z[i] * fma2(x, pair(-1.f, -1.f), c[i]);  // rounding of a large x where a is nothing)
+            x = fma2(a[i], x, z[i] * c[i]);
             c[i] = a[i] * w;
         }
         f2 f;

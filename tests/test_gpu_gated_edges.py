@@ -1,0 +1,55 @@
+"""GPU tests of the gated recurrence against 64-bit formulas where a bound of the
+channel's largest value would see nothing: what stands behind a new start, element by
+element; what the formula leaves infinite or NaN; a long chain of tiles in full.
+
+Tolerances as in test_gpu_lm_more.py: 400 u (u = 2^-24) of what a step's own states
+and gradients are, beside one rounding to the output's type.
+"""
+import pytest
+import torch
+
+from scan_linear_recurrences_gb300 import _binding as b
+from scan_linear_recurrences_gb300.build import build
+
+from . import _lm_more as m
+from .test_gpu_lm_more import BF16, F32, U, _gated_check, _gated_run, _views
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    build()
+    b.lib()
+    yield
+    b.mgs_check()
+
+
+# (a tile in part, a cluster over time, enough lanes for none)
+@pytest.mark.parametrize("B,T,D", [(2, 60, 64), (1, 700, 66), (80, 200, 64)])
+@pytest.mark.parametrize("start", [torch.inf, 30.0])
+@pytest.mark.parametrize("size", [1e2, 1e4, 1e8])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_new_start_behind_a_large_state(dtype, size, start, B, T, D):
+    # the first state is large and stays, masked, up to a gate of +inf (or 30: a = 1e-13), at another step of each
+    # channel: what follows knows nothing of it, and errs by its own states and gradients alone
+    d = m.gated_inputs(B, T, D, dtype, positive=False, seed=T + D, shift=0.5, halves=False)
+    d["h0"] = d["h0"].sign() * size
+    at, step = T // 3 + torch.arange(D) % 11, torch.arange(T)[:, None]
+    d["gate"] = torch.where(step < at, -torch.inf, torch.where(step == at, start, d["gate"].float())).to(dtype)
+    got, ref = _gated_run(_views(d)), m.gated_ref(d)
+    behind = (step > at).expand(B, T, D)
+    k, before = d["gate"].double(), torch.cat([d["h0"].double()[:, None], ref["h"][:, :-1]], 1)
+    away = d["value"].double().abs() + before.abs()  # what c - h comes from
+
+    def largest(x, where):  # in each channel
+        return (x.abs() * where).amax(1, keepdim=True)
+
+    since = behind | (step == at)
+    lam = largest(ref["lam"], since)
+    m.check_each("h", got["h"], ref["h"], 400 * U * torch.where(since, largest(ref["h"], since), ref["h"].abs()))
+    m.check_each("dvalue", got["dvalue"], ref["dvalue"], 400 * U * lam * since)
+    slope = torch.sigmoid(k) * torch.sigmoid(-k)  # (0 up to the new start, 1e-13 at one of 30)
+    m.check_each("dgate", got["dgate"], ref["dgate"], 400 * U * lam * torch.where(behind, largest(away, behind), away * slope))
