@@ -60,7 +60,8 @@ __device__ __forceinline__ float exp_minus(float x) {
 // z, a = 1 - z, c and z c' (BWD) of one step of two channels; z and a both to
 // their own last digits.  Two sigmoids share one reciprocal, of the product of their
 // denominators (both in 1..2).  BWD: a NaN in the value stays out of z and a, with
-// which gradients pass (the states behind it are NaN anyway).
+// which gradients pass to the steps before (its own slope and the states behind it are
+// NaN).
 template <typename T, bool POS, bool BWD>
 __device__ __forceinline__ void gates(float2 k, float2 v, f2 &z, f2 &a, f2 &c, f2 &zs) {
     const f2 one = pair(1.f, 1.f);
@@ -93,7 +94,7 @@ __device__ __forceinline__ void gates(float2 k, float2 v, f2 &z, f2 &a, f2 &c, f
     c = pair(v.x, v.y);
     zs = z;
     if constexpr (POS) {
-        const bool vx = v.x < 0.f, vy = v.y < 0.f;
+        const bool vx = !(v.x >= 0.f), vy = !(v.y >= 0.f);  // (a NaN has the slope of NaN)
         const float2 up = both(c + pair(0.5f, 0.5f)), down = both(fs);
         c = pair(vx ? down.x : up.x, vy ? down.y : up.y);
         if constexpr (BWD) {

@@ -53,3 +53,17 @@ def test_new_start_behind_a_large_state(dtype, size, start, B, T, D):
     m.check_each("dvalue", got["dvalue"], ref["dvalue"], 400 * U * lam * since)
     slope = torch.sigmoid(k) * torch.sigmoid(-k)  # (0 up to the new start, 1e-13 at one of 30)
     m.check_each("dgate", got["dgate"], ref["dgate"], 400 * U * lam * torch.where(behind, largest(away, behind), away * slope))
+
+
+@pytest.mark.parametrize("positive", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,T,D", [(2, 300, 32), (1, 2300, 34), (90, 90, 7)])
+@pytest.mark.parametrize("what,x", [("value", torch.inf), ("value", -torch.inf), ("value", torch.nan), ("gate", torch.nan),
+                                    ("grad_h", torch.nan), ("grad_h", torch.inf), ("h0", torch.inf), ("h0", torch.nan)])
+def test_what_the_formula_leaves_infinite_or_nan(what, x, B, T, D, dtype, positive):
+    # is infinite or NaN (an infinity may have become NaN), the rest is finite
+    d = m.gated_inputs(B, T, D, dtype, positive=positive, seed=12, halves=False)
+    d[what][(0, D // 2) if what == "h0" else (0, T * 2 // 3, D // 2)] = x
+    got, ref = _gated_run(_views(d)), m.gated_ref(d)
+    for n in ("h", "h_T", "dgate", "dvalue", "dh0"):
+        assert torch.equal(torch.isfinite(got[n]).cpu(), torch.isfinite(ref[n])), n
