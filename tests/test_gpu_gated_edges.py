@@ -67,3 +67,10 @@ def test_what_the_formula_leaves_infinite_or_nan(what, x, B, T, D, dtype, positi
     got, ref = _gated_run(_views(d)), m.gated_ref(d)
     for n in ("h", "h_T", "dgate", "dvalue", "dh0"):
         assert torch.equal(torch.isfinite(got[n]).cpu(), torch.isfinite(ref[n])), n
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_a_long_chain_of_tiles_in_full(dtype):
+    # all states and gradients of 1563 tiles, and what the whole chain of rounds ends in
+    d = m.gated_inputs(1, 100001, 2, dtype, seed=64, shift=1.0)
+    _gated_check(_gated_run(_views(d)), m.gated_ref(d))
