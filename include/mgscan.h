@@ -591,6 +591,18 @@ void mgs_set_wait_timeout_ns(uint64_t ns);
  * failure detection without faulting or hanging the GPU. */
 mgs_status mgs_debug_wait_flag(const int *flag, mgs_stream_t stream);
 
+/* Diagnostic: launches one cluster of MGS_EXCHANGE_BLOCKS blocks that exchange a
+ * message with each other in each of MGS_EXCHANGE_ROUNDS rounds, by the steps by which
+ * the gated recurrence's blocks do, where block `late_block` (-1: none) comes late_ns (up
+ * to 1e9) late to round `late_round`.  When that is past the limit of a wait, the others
+ * give up, all leave and mgs_check() returns MGS_ERR_TIMEOUT.
+ * Out, both int32 [MGS_EXCHANGE_BLOCKS] on the device: the rounds that each block took
+ * part in, and how many messages of rounds that it saw through were wrong (none; -1:
+ * some had not come when the blocks left). */
+enum { MGS_EXCHANGE_BLOCKS = 8, MGS_EXCHANGE_ROUNDS = 6 };
+mgs_status mgs_debug_exchange(int32_t late_block, int32_t late_round, uint64_t late_ns, int32_t *rounds, int32_t *wrong,
+                              mgs_stream_t stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *mgs_status_string(mgs_status status);
 

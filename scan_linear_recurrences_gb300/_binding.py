@@ -45,6 +45,7 @@ MGS_BF16 = 1
 MGS_I32 = 2
 MGS_I64 = 3
 GATED_SPAN = 64  # MGS_GATED_SPAN in include/mgscan.h
+EXCHANGE_BLOCKS, EXCHANGE_ROUNDS = 8, 6  # MGS_EXCHANGE_BLOCKS, MGS_EXCHANGE_ROUNDS
 
 
 class MGSError(RuntimeError):
@@ -106,6 +107,7 @@ _SIGNATURES = {
     "mgs_check": (_int, [_vp]),
     "mgs_set_wait_timeout_ns": (None, [ctypes.c_uint64]),
     "mgs_debug_wait_flag": (_int, [_vp, _vp]),
+    "mgs_debug_exchange": (_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_uint64, _vp, _vp, _vp]),
     "mgs_status_string": (ctypes.c_char_p, [_int]),
     "mgs_version": (_int, []),
 }
@@ -394,6 +396,10 @@ def mgs_set_wait_timeout_ns(ns: int):
 
 def mgs_debug_wait_flag(flag, stream=None):
     return _call("mgs_debug_wait_flag", _ptr(flag), _stream(stream))
+
+
+def mgs_debug_exchange(late_block, late_round, late_ns, rounds, wrong, stream=None):
+    return _call("mgs_debug_exchange", late_block, late_round, late_ns, _ptr(rounds), _ptr(wrong), _stream(stream))
 
 
 def mgs_status_string(status: int) -> str:

@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libmgscan.so")
 SOURCES = ["mgs_api.cu", "mgs_mas.cu", "mgs_ms.cu", "mgs_psl.cu", "mgs_givens.cu", "mgs_delta.cu", "mgs_linear.cu",
            "mgs_attn.cu", "mgs_attn_mma.cu", "mgs_norm.cu", "mgs_clip.cu", "mgs_gated.cu", "mgs_qknorm.cu", "mgs_embed.cu"]
 HEADERS = ["mgs_device.cuh", "mgs_launch.h", "mgs_tiles.cuh", "mgs_chunk.cuh", "mgs_ffsincos.cuh", "mgs_umma.cuh", "mgs_cluster.cuh",
-           "mgs_lm.h", "mgs_num.cuh", "mgs_rows.h"]
+           "mgs_lm.h", "mgs_num.cuh", "mgs_rows.h", "mgs_rounds.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I", os.path.join(ROOT, "include")]

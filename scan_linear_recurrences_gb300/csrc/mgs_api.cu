@@ -1110,6 +1110,18 @@ mgs_status mgs_gated_scan_step(const mgs_gated_shape *shape, const void *gate, c
     return from_cuda(mgs::launch_gated_step(*shape, gate, value, state, slots, n_slots, h, cs_of(stream)));
 }
 
+mgs_status mgs_debug_exchange(int32_t late_block, int32_t late_round, uint64_t late_ns, int32_t *rounds, int32_t *wrong,
+                              mgs_stream_t stream) {
+    if (rounds == nullptr || wrong == nullptr || late_ns > 1000000000ull) return MGS_ERR_INVALID_ARG;
+    if (!aligned4(rounds) || !aligned4(wrong)) return MGS_ERR_UNSUPPORTED;
+    constexpr int64_t n = MGS_EXCHANGE_BLOCKS * 4;
+    if (!apart({{rounds, n}, {wrong, n}}, {})) return MGS_ERR_INVALID_ARG;
+    mgs::DevCtl ctl;
+    const mgs_status st = current_ctl(&ctl);
+    if (st != MGS_OK) return st;
+    return from_cuda(mgs::launch_exchange_check(late_block, late_round, late_ns, rounds, wrong, ctl, cs_of(stream)));
+}
+
 // ---------------------------------------------------------------- norm of queries and keys
 struct QkSizes {
     int64_t q, k, q_span, k_span, gq_span, gk_span, table, pos;  // bytes

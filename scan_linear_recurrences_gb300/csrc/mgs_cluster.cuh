@@ -33,6 +33,14 @@ __device__ __forceinline__ float ld_dsmem(const float *p, unsigned rank) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(dsmem_addr(p, rank)) : "memory");
     return v;
 }
+__device__ __forceinline__ unsigned ld_dsmem_u32(const unsigned *p, unsigned rank) {
+    unsigned v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(dsmem_addr(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_dsmem_u32(unsigned *p, unsigned rank, unsigned v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(dsmem_addr(p, rank)), "r"(v) : "memory");
+}
 // 16 bytes (p 16-byte aligned)
 __device__ __forceinline__ float4 ld_dsmem4(const float *p, unsigned rank) {
     float4 v;

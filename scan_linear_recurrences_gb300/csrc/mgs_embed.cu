@@ -32,12 +32,6 @@ constexpr int kWindow = 32768;   // rows of dW that a block marks at a time (bit
 constexpr unsigned kNone = 0xffffffffu;
 constexpr unsigned kCluster = 8, kKeep = 4;  // blocks that sort; a warp's batches that it keeps in registers
 
-__device__ __forceinline__ unsigned ld_dsmem_u32(const unsigned *p, unsigned rank) {
-    unsigned v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(dsmem_addr(p, rank)) : "memory");
-    return v;
-}
-
 // The row pieces: 16 bytes (VEC), or single elements, a lane's 32 apart
 template <typename T, bool VEC>
 struct Piece {

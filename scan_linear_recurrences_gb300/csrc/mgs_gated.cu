@@ -26,6 +26,7 @@
 #include "mgs_launch.h"
 #include "mgs_lm.h"
 #include "mgs_num.cuh"
+#include "mgs_rounds.h"
 
 namespace mgs {
 namespace {
@@ -258,14 +259,15 @@ __device__ __forceinline__ void push16(void *slot, uint64_t *bar, unsigned rank,
                  : "memory");
 }
 
-// The maps of a tile's warps, and of a round's blocks (CL).  Two of each, in turn: a
-// block pushes into a peer's slots of round n + 2 when it has that peer's map of round
-// n + 1, which the peer pushes when all its warps are past round n.
+// The maps of a tile's warps, and of a round's blocks (CL): two of each, in turn.
 template <int W, bool CL>
 struct Exchange {
     float4 maps[2][W][32];
     float4 slots[2][kMaxCluster][32];
     alignas(16) uint64_t bar[2];
+    unsigned gave_up[2];  // a wait of that turn has
+    unsigned pushed;      // the rounds in which this block has pushed its map
+    unsigned told;        // some block's wait has given up
 };
 // Without a cluster: what the last warp leaves to the next tile.  (Two blocks of the
 // backward in fp32 fill an SM's shared memory to the last KB.)
@@ -291,50 +293,117 @@ __device__ __forceinline__ f2 enter(const Exchange<W, false> &ex, int turn, int 
     }
     return s;
 }
+// The steps of exchange_round and leave_rounds, by a thread
+template <int W>
+struct Ops {
+    Exchange<W, true> &ex;
+    int warp, lane, cluster;
+    unsigned self;
+    const DevCtl &ctl;
+    float4 map;  // the block's
+    __device__ __forceinline__ bool gave_up(int turn) const { return *const_cast<volatile unsigned *>(&ex.gave_up[turn]) != 0; }
+    __device__ __forceinline__ void give_up(int turn) const {
+        *const_cast<volatile unsigned *>(&ex.gave_up[turn]) = 1;
+        record_error(ctl, ERR_MBAR_TIMEOUT);
+    }
+    __device__ __forceinline__ void push(int turn) const {
+        for (int r = warp; r < cluster; r += W) push16(&ex.slots[turn][self][lane], &ex.bar[turn], unsigned(r), map);
+    }
+    __device__ __forceinline__ void count_and_arm(int turn) const {
+        if (warp != 0 || lane != 0) return;
+        mbar_arrive_expect_tx(&ex.bar[turn], unsigned(cluster) * 512u);
+        atomicAdd(&ex.pushed, 1u);
+    }
+    __device__ __forceinline__ bool wait(int turn, int phase) const {
+        return mbar_wait_bounded(&ex.bar[turn], unsigned(phase), ctl.timeout_ns);
+    }
+    __device__ __forceinline__ void block_barrier() const { __syncthreads(); }
+    __device__ __forceinline__ void cluster_barrier() const { cluster_arrive(), cluster_wait(); }
+    __device__ __forceinline__ void tell_all() const {
+        if (int(threadIdx.x) < cluster) st_dsmem_u32(&ex.told, threadIdx.x, 1u);
+    }
+    __device__ __forceinline__ bool told() const { return *const_cast<volatile unsigned *>(&ex.told) != 0; }
+    __device__ __forceinline__ bool first_warp() const { return warp == 0; }
+    __device__ __forceinline__ unsigned rank() const { return self; }
+    __device__ __forceinline__ int pushed(unsigned r) const { return int(ld_dsmem_u32(&ex.pushed, r)); }
+    __device__ __forceinline__ void stand_in(int r, int turn) const {
+        push16(&ex.slots[turn][r][lane], &ex.bar[turn], self, make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+    __device__ __forceinline__ void arm(int turn, int blocks) const {
+        if (lane == 0) mbar_arrive_expect_tx(&ex.bar[turn], unsigned(blocks) * 512u);
+        __syncwarp();
+    }
+    __device__ __forceinline__ void not_drained() const { record_error(ctl, ERR_DRAIN_TIMEOUT); }
+};
+
 // In a cluster: `s` (the state before the round, which every block keeps) through the
 // maps of the blocks before this one and of the warps before this one, and s through
-// all of them for the next round.
+// all of them for the next round.  (Of no meaning where a wait gave up.)
 template <bool REV, int W>
-__device__ __forceinline__ f2 enter(Exchange<W, true> &ex, int turn, int phase, f2 &s, int warp, int lane, int cluster,
-                                    unsigned rank, const DevCtl &ctl, bool &lost) {
+__device__ __forceinline__ f2 enter(Ops<W> op, int turn, int phase, f2 &s, bool &lost) {
+    const Exchange<W, true> &ex = op.ex;
     f2 mine = s;
     Map before{pair(1.f, 1.f), pair(0.f, 0.f)}, all = before;
 #pragma unroll
     for (int i = 0; i < W; ++i) {
         const int j = REV ? W - 1 - i : i;
-        if (j == warp) before = all;
-        const Map m = Map::unpack(ex.maps[turn][j][lane]);
+        if (j == op.warp) before = all;
+        const Map m = Map::unpack(ex.maps[turn][j][op.lane]);
         all.H = fma2(m.A, all.H, m.H);
         all.A = m.A * all.A;
     }
-    for (int r = warp; r < cluster; r += W) push16(&ex.slots[turn][rank][lane], &ex.bar[turn], unsigned(r), all.pack());
-    if (warp == 0 && lane == 0) mbar_arrive_expect_tx(&ex.bar[turn], unsigned(cluster) * 512u);
-    // (after a wait that gave up the rounds go on without waiting, to their end)
-    if (!lost && !mbar_wait_bounded(&ex.bar[turn], unsigned(phase), ctl.timeout_ns)) {
-        lost = true;
-        record_error(ctl, ERR_MBAR_TIMEOUT);
-    }
-    for (int i = 0; i < cluster; ++i) {
-        const int r = REV ? cluster - 1 - i : i;
-        if (r == int(rank)) mine = s;
-        const Map m = Map::unpack(ex.slots[turn][r][lane]);
+    op.map = all.pack();
+    exchange_round(op, turn, phase, lost);
+    for (int i = 0; i < op.cluster; ++i) {
+        const int r = REV ? op.cluster - 1 - i : i;
+        if (r == int(op.self)) mine = s;
+        const Map m = Map::unpack(ex.slots[turn][r][op.lane]);
         s = fma2(m.A, s, m.H);
     }
     return fma2(before.A, mine, before.H);
 }
 
-// all blocks of the cluster have their barriers (before the first push), or are done with each other's memory
-template <bool CL, typename E>
-__device__ __forceinline__ void meet(E &ex, bool init) {
-    if constexpr (CL) {
-        if (init && threadIdx.x == 0) {
-            mbar_init(&ex.bar[0], 1), mbar_init(&ex.bar[1], 1);
-            fence_barrier_init();
-        }
-        __syncthreads();
-        cluster_arrive();
-        cluster_wait();
+// all blocks of the cluster have their barriers before the first push
+template <int W>
+__device__ __forceinline__ void meet(Exchange<W, true> &ex) {
+    if (threadIdx.x == 0) {
+        mbar_init(&ex.bar[0], 1), mbar_init(&ex.bar[1], 1);
+        ex.gave_up[0] = ex.gave_up[1] = ex.pushed = ex.told = 0u;
+        fence_barrier_init();
     }
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+}
+
+// The exchange by itself, between the blocks of one cluster, one of which may come late to a
+// round: how many rounds each took part in, and how many messages it found wrong in them.
+constexpr int kCheckBlocks = MGS_EXCHANGE_BLOCKS, kCheckRounds = MGS_EXCHANGE_ROUNDS, kCheckWarps = 4;
+__global__ void __launch_bounds__(kCheckWarps * 32)
+    exchange_check_kernel(int late_block, int late_round, uint64_t late_ns, int32_t *rounds, int32_t *wrong, DevCtl ctl) {
+    __shared__ Exchange<kCheckWarps, true> ex;
+    __shared__ int bad;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned rank = cluster_rank();
+    Ops<kCheckWarps> op{ex, warp, lane, kCheckBlocks, rank, ctl, {}};
+    if (threadIdx.x == 0) bad = 0;
+    meet(ex);
+    bool lost = false;
+    for (int n = 0; n < kCheckRounds; ++n) {
+        if (int(rank) == late_block && n == late_round)
+            for (const uint64_t t0 = global_ns(); global_ns() - t0 < late_ns;) __nanosleep(1000);
+        __syncthreads();
+        op.map = make_float4(float(n), float(rank), float(lane), 1.f);
+        exchange_round(op, n & 1, (n >> 1) & 1, lost);
+        for (int r = 0; r < kCheckBlocks && !lost; ++r) {
+            const float4 m = ex.slots[n & 1][r][lane];
+            if (m.x != float(n) || m.y != float(r) || m.z != float(lane) || m.w != 1.f) atomicAdd(&bad, 1);
+        }
+    }
+    leave_rounds(op, kCheckBlocks);
+    if (threadIdx.x != 0) return;
+    rounds[rank] = int32_t(ex.pushed);
+    wrong[rank] = atomicOr(ctl.err, 0u) & ERR_DRAIN_TIMEOUT ? -1 : bad;
 }
 
 // Warps of a forward's block and steps of its tile.  The maps cost the less the longer a
@@ -365,6 +434,9 @@ __global__ void __launch_bounds__(kFwdWarps<T, CL> * 32, 512 / (kFwdWarps<T, CL>
             *value = (const T *)g.value + b * g.vb + int64_t(strip) * 64;
     T *h = (T *)g.h + b * g.T * g.D + at.d;
     T *mine = ring + warp * (2 * 2 * L * 64);
+    auto op = [&] {
+        if constexpr (CL) return Ops<W>{ex, warp, lane, cluster, rank, g.ctl, {}};
+    };
     auto fetch = [&](int tile, int stage) {
         const int t0 = tile * TILE + warp * L, n = g.T - t0;
         T *to = mine + stage * (2 * L * 64);
@@ -375,7 +447,7 @@ __global__ void __launch_bounds__(kFwdWarps<T, CL> * 32, 512 / (kFwdWarps<T, CL>
         copies_close();
     };
     fetch(int(rank), 0);
-    meet<CL>(ex, true);
+    if constexpr (CL) meet(ex);
     f2 s = pair(0.f, 0.f);
     if (g.in) {
         Two<float, VEC> x;
@@ -416,7 +488,7 @@ __global__ void __launch_bounds__(kFwdWarps<T, CL> * 32, 512 / (kFwdWarps<T, CL>
         ex.maps[turn][warp][lane] = m.pack();
         __syncthreads();
         f2 x;
-        if constexpr (CL) x = enter<false>(ex, turn, phase, s, warp, lane, cluster, rank, g.ctl, lost);
+        if constexpr (CL) x = enter<false>(op(), turn, phase, s, lost);
         else x = enter<false>(ex, turn, warp, lane);
         if (g.carries && warp * L % kTile == 0 && n > 0)
             Two<float, VEC>::store(g.carries + (b * ((g.T - 1) / kTile + 1) + t0 / kTile) * g.D + at.d, both(x), at.ok);
@@ -440,7 +512,7 @@ __global__ void __launch_bounds__(kFwdWarps<T, CL> * 32, 512 / (kFwdWarps<T, CL>
     }
     // (steps behind the last one leave the state as it is)
     if (g.out && rank == 0 && warp == (CL ? 0 : W - 1)) Two<float, VEC>::store(g.out + b * g.D + at.d, both(s), at.ok);
-    meet<CL>(ex, false);
+    if constexpr (CL) leave_rounds(op(), cluster);
 }
 
 template <typename T, bool POS, Copy HOW, bool CL>
@@ -462,6 +534,9 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) gated_bwd_kernel(const __gr
             *gh = (const T *)g.gh + b * g.gb + int64_t(strip) * 64;
     T *dgate = (T *)g.dgate + b * g.T * g.D + at.d, *dvalue = (T *)g.dvalue + b * g.T * g.D + at.d;
     T *mine = ring + warp * (2 * 3 * L * 64);
+    auto op = [&] {
+        if constexpr (CL) return Ops<W>{ex, warp, lane, cluster, rank, g.ctl, {}};
+    };
     Two<float, VEC> next;  // the state before the next tile
     auto fetch = [&](int tile, int stage) {
         const int t0 = tile * kTile + warp * L, n = g.T - t0;
@@ -478,7 +553,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) gated_bwd_kernel(const __gr
     int first = (g.tiles - 1) / cluster * cluster, turn = 0, phase = 0;
     bool lost = false;
     fetch(first + int(rank), 0);
-    meet<CL>(ex, true);
+    if constexpr (CL) meet(ex);
     f2 flow = pair(0.f, 0.f);
     if (g.in) {
         Two<float, VEC> x;
@@ -539,7 +614,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) gated_bwd_kernel(const __gr
             c[i] = a[i] * w;
         }
         f2 f;
-        if constexpr (CL) f = enter<true>(ex, turn, phase, flow, warp, lane, cluster, rank, g.ctl, lost);
+        if constexpr (CL) f = enter<true>(op(), turn, phase, flow, lost);
         else f = enter<true>(ex, turn, warp, lane);
         T *to_k = dgate + (t0 + L - 1) * g.D, *to_v = dvalue + (t0 + L - 1) * g.D;
         auto run = [&](auto all) {  // all: every step is there
@@ -563,7 +638,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) gated_bwd_kernel(const __gr
         turn ^= 1;
     }
     if (g.out && rank == 0 && warp == 0) Two<float, VEC>::store(g.out + b * g.D + at.d, both(flow), at.ok);
-    meet<CL>(ex, false);
+    if constexpr (CL) leave_rounds(op(), cluster);
 }
 
 template <typename T, bool POS, bool VEC>
@@ -732,5 +807,11 @@ cudaError_t launch_gated_step(const mgs_gated_shape &sh, const void *gate, const
     return MGS_BY_TYPE(step_go, sh, g, state, slots, nslots, s);
 }
 #undef MGS_BY_TYPE
+
+cudaError_t launch_exchange_check(int late_block, int late_round, uint64_t late_ns, int32_t *rounds, int32_t *wrong,
+                                  const DevCtl &ctl, cudaStream_t s) {
+    return launch_cluster(exchange_check_kernel, kCheckBlocks, kCheckWarps * 32, 0, kCheckBlocks, s, late_block, late_round,
+                          late_ns, rounds, wrong, ctl);
+}
 
 }  // namespace mgs

@@ -113,6 +113,9 @@ cudaError_t launch_gated_bwd(const mgs_gated_shape &sh, const void *gate, const 
                              const DevCtl &ctl, cudaStream_t s);
 cudaError_t launch_gated_step(const mgs_gated_shape &sh, const void *gate, const void *value, float *state,
                               const int32_t *slots, int64_t nslots, void *h, cudaStream_t s);
+// late_ns: how late a block comes to a round (of no effect with a late_block that is none)
+cudaError_t launch_exchange_check(int late_block, int late_round, uint64_t late_ns, int32_t *rounds, int32_t *wrong,
+                                  const DevCtl &ctl, cudaStream_t s);
 
 cudaError_t launch_qk_norm_fwd(const mgs_qk_norm_shape &sh, const void *q, const void *k, const void *qw,
                                const void *kw, const float *table, const int32_t *positions, void *yq, void *yk,

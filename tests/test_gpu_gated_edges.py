@@ -74,3 +74,41 @@ def test_a_long_chain_of_tiles_in_full(dtype):
     # all states and gradients of 1563 tiles, and what the whole chain of rounds ends in
     d = m.gated_inputs(1, 100001, 2, dtype, seed=64, shift=1.0)
     _gated_check(_gated_run(_views(d)), m.gated_ref(d))
+
+
+def _exchange(block, at, ns):
+    rounds, wrong = (torch.full((b.EXCHANGE_BLOCKS,), 99, dtype=torch.int32, device="cuda") for _ in range(2))
+    b.mgs_debug_exchange(block, at, ns, rounds, wrong)
+    return rounds, wrong
+
+
+def test_exchange_of_a_cluster():
+    # a block that comes late, within the limit of the others' waits
+    for block, at in ((-1, 0), (0, 0), (3, 2), (7, b.EXCHANGE_ROUNDS - 1)):
+        rounds, wrong = _exchange(block, at, 2_000_000)
+        b.mgs_check()
+        assert (rounds == b.EXCHANGE_ROUNDS).all() and not wrong.any()
+
+
+@pytest.mark.parametrize("block", [0, 5])
+@pytest.mark.parametrize("at", range(b.EXCHANGE_ROUNDS))
+def test_exchange_whose_waits_give_up(at, block):
+    # past the limit: the others have pushed in that round and take no further part; the late one has their messages of
+    # it and pushes once more.  Nothing is on its way when they leave, and the next call knows nothing of it.
+    d = _views(m.gated_inputs(1, 1000, 64, BF16, seed=7))
+    want = _gated_run(d)
+    b.mgs_check()
+    b.mgs_set_wait_timeout_ns(2_000_000)
+    try:
+        rounds, wrong = _exchange(block, at, 50_000_000)
+        with pytest.raises(b.MGSError) as e:
+            b.mgs_check()
+        assert e.value.status == b.MGS_ERR_TIMEOUT
+        b.mgs_check()  # cleared
+    finally:
+        b.mgs_set_wait_timeout_ns(1_000_000_000)
+    took = [at + 1] * b.EXCHANGE_BLOCKS
+    took[block] = min(at + 2, b.EXCHANGE_ROUNDS)
+    assert rounds.tolist() == took and not wrong.any()
+    for n, x in _gated_run(d).items():
+        assert torch.equal(x, want[n]), n
