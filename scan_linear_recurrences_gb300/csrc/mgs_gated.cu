@@ -265,7 +265,7 @@ struct Exchange {
     float4 maps[2][W][32];
     float4 slots[2][kMaxCluster][32];
     alignas(16) uint64_t bar[2];
-    unsigned gave_up[2];  // a wait of that turn has
+    unsigned gave_up[2];  // up to a round of that turn a wait has
     unsigned pushed;      // the rounds in which this block has pushed its map
     unsigned told;        // some block's wait has given up
 };
@@ -302,8 +302,9 @@ struct Ops {
     const DevCtl &ctl;
     float4 map;  // the block's
     __device__ __forceinline__ bool gave_up(int turn) const { return *const_cast<volatile unsigned *>(&ex.gave_up[turn]) != 0; }
+    __device__ __forceinline__ void stay_out(int turn) const { *const_cast<volatile unsigned *>(&ex.gave_up[turn]) = 1u; }
     __device__ __forceinline__ void give_up(int turn) const {
-        *const_cast<volatile unsigned *>(&ex.gave_up[turn]) = 1;
+        stay_out(turn);
         record_error(ctl, ERR_MBAR_TIMEOUT);
     }
     __device__ __forceinline__ void push(int turn) const {
@@ -340,8 +341,9 @@ struct Ops {
 // maps of the blocks before this one and of the warps before this one, and s through
 // all of them for the next round.  (Of no meaning where a wait gave up.)
 template <bool REV, int W>
-__device__ __forceinline__ f2 enter(Ops<W> op, int turn, int phase, f2 &s, bool &lost) {
+__device__ __forceinline__ f2 enter(Ops<W> op, int round, f2 &s) {
     const Exchange<W, true> &ex = op.ex;
+    const int turn = round & 1;
     f2 mine = s;
     Map before{pair(1.f, 1.f), pair(0.f, 0.f)}, all = before;
 #pragma unroll
@@ -353,7 +355,7 @@ __device__ __forceinline__ f2 enter(Ops<W> op, int turn, int phase, f2 &s, bool 
         all.A = m.A * all.A;
     }
     op.map = all.pack();
-    exchange_round(op, turn, phase, lost);
+    exchange_round(op, round);
     for (int i = 0; i < op.cluster; ++i) {
         const int r = REV ? op.cluster - 1 - i : i;
         if (r == int(op.self)) mine = s;
@@ -388,14 +390,13 @@ __global__ void __launch_bounds__(kCheckWarps * 32)
     Ops<kCheckWarps> op{ex, warp, lane, kCheckBlocks, rank, ctl, {}};
     if (threadIdx.x == 0) bad = 0;
     meet(ex);
-    bool lost = false;
     for (int n = 0; n < kCheckRounds; ++n) {
         if (int(rank) == late_block && n == late_round)
             for (const uint64_t t0 = global_ns(); global_ns() - t0 < late_ns;) __nanosleep(1000);
         __syncthreads();
         op.map = make_float4(float(n), float(rank), float(lane), 1.f);
-        exchange_round(op, n & 1, (n >> 1) & 1, lost);
-        for (int r = 0; r < kCheckBlocks && !lost; ++r) {
+        exchange_round(op, n);
+        for (int r = 0; r < kCheckBlocks && !op.gave_up(n & 1); ++r) {
             const float4 m = ex.slots[n & 1][r][lane];
             if (m.x != float(n) || m.y != float(r) || m.z != float(lane) || m.w != 1.f) atomicAdd(&bad, 1);
         }
@@ -456,10 +457,8 @@ __global__ void __launch_bounds__(kFwdWarps<T, CL> * 32, 512 / (kFwdWarps<T, CL>
     }
     if constexpr (!CL)
         if (warp == 0) ex.pass[1][lane] = s.v;
-    int turn = 0, phase = 0;
-    bool lost = false;
-    for (int first = 0; first < g.tiles; first += cluster) {
-        const int tile = first + int(rank), t0 = tile * TILE + warp * L, n = g.T - t0;
+    for (int first = 0, round = 0; first < g.tiles; first += cluster, ++round) {
+        const int turn = round & 1, tile = first + int(rank), t0 = tile * TILE + warp * L, n = g.T - t0;
         __syncwarp();  // the other stage has been read
         fetch(tile + cluster, turn ^ 1);
         copies_wait<1>();
@@ -488,7 +487,7 @@ __global__ void __launch_bounds__(kFwdWarps<T, CL> * 32, 512 / (kFwdWarps<T, CL>
         ex.maps[turn][warp][lane] = m.pack();
         __syncthreads();
         f2 x;
-        if constexpr (CL) x = enter<false>(op(), turn, phase, s, lost);
+        if constexpr (CL) x = enter<false>(op(), round, s);
         else x = enter<false>(ex, turn, warp, lane);
         if (g.carries && warp * L % kTile == 0 && n > 0)
             Two<float, VEC>::store(g.carries + (b * ((g.T - 1) / kTile + 1) + t0 / kTile) * g.D + at.d, both(x), at.ok);
@@ -507,8 +506,6 @@ __global__ void __launch_bounds__(kFwdWarps<T, CL> * 32, 512 / (kFwdWarps<T, CL>
             s = x;
             if (warp == W - 1) ex.pass[turn][lane] = x.v;
         }
-        phase ^= turn;
-        turn ^= 1;
     }
     // (steps behind the last one leave the state as it is)
     if (g.out && rank == 0 && warp == (CL ? 0 : W - 1)) Two<float, VEC>::store(g.out + b * g.D + at.d, both(s), at.ok);
@@ -550,8 +547,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) gated_bwd_kernel(const __gr
         if (tile >= 0) copy_rows<T, L, HOW>(to + 2 * L * 64, gh + (n > 0 ? t0 * g.gt : 0), g.gt, n, left);  // (zeros where no step is)
         copies_close();
     };
-    int first = (g.tiles - 1) / cluster * cluster, turn = 0, phase = 0;
-    bool lost = false;
+    int first = (g.tiles - 1) / cluster * cluster;
     fetch(first + int(rank), 0);
     if constexpr (CL) meet(ex);
     f2 flow = pair(0.f, 0.f);
@@ -562,7 +558,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) gated_bwd_kernel(const __gr
     }
     if constexpr (!CL)
         if (warp == 0) ex.pass[1][lane] = flow.v;
-    for (; first >= 0; first -= cluster) {
+    for (int round = 0, turn = 0; first >= 0; first -= cluster, ++round, turn ^= 1) {
         const int tile = first + int(rank), t0 = tile * kTile + warp * L, n = g.T - t0;
         f2 x = pair(next.u.x, next.u.y);
         __syncwarp();  // the other stage has been read
@@ -614,7 +610,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) gated_bwd_kernel(const __gr
             c[i] = a[i] * w;
         }
         f2 f;
-        if constexpr (CL) f = enter<true>(op(), turn, phase, flow, lost);
+        if constexpr (CL) f = enter<true>(op(), round, flow);
         else f = enter<true>(ex, turn, warp, lane);
         T *to_k = dgate + (t0 + L - 1) * g.D, *to_v = dvalue + (t0 + L - 1) * g.D;
         auto run = [&](auto all) {  // all: every step is there
@@ -634,8 +630,6 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) gated_bwd_kernel(const __gr
             flow = f;
             if (warp == 0) ex.pass[turn][lane] = f.v;
         }
-        phase ^= turn;
-        turn ^= 1;
     }
     if (g.out && rank == 0 && warp == 0) Two<float, VEC>::store(g.out + b * g.D + at.d, both(flow), at.ok);
     if constexpr (CL) leave_rounds(op(), cluster);

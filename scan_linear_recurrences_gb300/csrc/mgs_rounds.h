@@ -29,17 +29,15 @@
 
 namespace mgs {
 
-// A warp's part of a round, behind a block barrier.  lost: this block takes no part any more
-// (the same in all its warps before the wait).
+// A warp's part of a round, behind a block barrier.  (Whether its block takes part is the same for all its warps: what
+// they read was written before that barrier, and is written for the round after this one in the other turn's place.)
 template <class Ops>
-MGS_ROUNDS_FN void exchange_round(const Ops &op, int turn, int phase, bool &lost) {
-    if (op.gave_up(turn ^ 1)) lost = true;
-    if (lost) return;
+MGS_ROUNDS_FN void exchange_round(const Ops &op, int round) {
+    const int turn = round & 1;
+    if (op.gave_up(turn ^ 1)) return op.stay_out(turn);
     op.push(turn);
     op.count_and_arm(turn);  // (by the first warp)
-    if (op.wait(turn, phase)) return;
-    lost = true;
-    op.give_up(turn);
+    if (!op.wait(turn, (round >> 1) & 1)) op.give_up(turn);
 }
 
 // Behind the last round; all warps

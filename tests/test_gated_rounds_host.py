@@ -80,7 +80,8 @@ struct Ops {
     bool leaving = false;
     Block &me() const { return sim->blocks[block]; }
     bool gave_up(int turn) const { sim->yield(); return me().gave_up[turn]; }
-    void give_up(int turn) const { ++sim->give_ups, me().gave_up[turn] = 1; }
+    void stay_out(int turn) const { me().gave_up[turn] = 1; }
+    void give_up(int turn) const { ++sim->give_ups, stay_out(turn); }
     void push(int turn) const {
         for (int r = warp; r < int(sim->blocks.size()); r += int(sim->warps.size() / sim->blocks.size())) {
             sim->way.push_back({r, block, round});
@@ -133,15 +134,17 @@ struct Ops {
 
 #ifdef PLANTED  // what must be seen: a block that gave up goes on without waiting, and leaves behind a cluster barrier
 template <class O>
-void exchange(O &op, int turn, int phase, bool &lost) {
+void exchange(O &op, int round) {
+    const int turn = round & 1;
     op.push(turn), op.count_and_arm(turn);
-    if (!lost && !op.wait(turn, phase)) lost = true, op.give_up(turn);
+    if (!op.gave_up(turn ^ 1) && op.wait(turn, (round >> 1) & 1)) return;
+    op.give_up(turn);
 }
 template <class O>
 void leave(O &op, int) { op.block_barrier(), op.cluster_barrier(); }
 #else
 template <class O>
-void exchange(O &op, int turn, int phase, bool &lost) { mgs::exchange_round(op, turn, phase, lost); }
+void exchange(O &op, int round) { mgs::exchange_round(op, round); }
 template <class O>
 void leave(O &op, int n) { mgs::leave_rounds(op, n); }
 #endif
@@ -149,13 +152,12 @@ void leave(O &op, int n) { mgs::leave_rounds(op, n); }
 static void play() {
     Warp &w = sim->warps[sim->running];
     Ops op{w.block, w.warp, 0};
-    bool lost = false;
     for (int n = 0; n < sim->rounds; ++n) {
         op.round = n;
         op.block_barrier();
-        exchange(op, n & 1, (n >> 1) & 1, lost);
+        exchange(op, n);
         for (int m : sim->blocks[w.block].slots[n & 1]) {
-            if (!lost && m != n) sim->fail("a message of another round");
+            if (!sim->blocks[w.block].gave_up[n & 1] && m != n) sim->fail("a message of another round");
             sim->yield();
         }
     }
