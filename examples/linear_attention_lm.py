@@ -69,8 +69,8 @@ class Layer(torch.nn.Module):
         self.up8 = (w / self.up_scale[:, None]).to(torch.float8_e4m3fn)
 
     @torch.no_grad()
-    def serve(self, x, res, states, slots, table, at):
-        """A prompt (x [B,T,width]: the states are left in their slots) or one token of each sequence ([B,width])."""
+    def serve(self, x, res, states, slots, place, table, at):
+        """A prompt (x [B,T,width]: the states are left in their places) or one token of each sequence ([B,width])."""
         if res is None:
             y, res = api.rms_norm_fwd(x, self.norm1)[0], x
         else:
@@ -78,9 +78,9 @@ class Layer(torch.nn.Module):
         q, k, v, g = self.project(y, api.qk_norm_fwd, table, at)
         if x.dim() == 3:
             o, S = api.linear_attention_fwd(q, k, v, g, scale=1.0, want_state=True)
-            states[slots.long()] = S
+            states[place] = S
         else:
-            o = api.linear_attention_step(q, k, v, g, states, slots, scale=1.0)
+            o = api.linear_attention_step(q, k, v, g, states[:-1], slots, scale=1.0)
         y8, scale, res = api.rms_norm_fp8_fwd(self.out(o.flatten(-2)), self.norm2, res)
         # the product of 8-bit operands, scaled by rows and columns (here in 32 bits)
         up = (y8.float() @ self.up8.float().T) * scale * self.up_scale
@@ -104,21 +104,25 @@ class Model(torch.nn.Module):
         return self.head(api.rms_norm(x, self.norm, res)[0])
 
     def cache(self, users):
-        """A state for each layer, user and head, and how many tokens each user's have seen."""
+        """A state for each layer, user and head, and how many tokens each user's have seen; behind the users' a spare
+        place, for what empty rows leave."""
         L = self.layers[0]
-        states = [torch.zeros(users, L.H, L.D, L.D, device=self.norm.device) for _ in self.layers]
-        return [*states, torch.zeros(users, dtype=torch.int32, device=self.norm.device)]
+        states = [torch.zeros(users + 1, L.H, L.D, L.D, device=self.norm.device) for _ in self.layers]
+        return [*states, torch.zeros(users + 1, dtype=torch.int32, device=self.norm.device)]
 
     @torch.no_grad()
     def serve(self, tokens, cache, slots):
-        """Logits after the prompts [B,T], or after one more token [B], of the users in `slots` (int32 [B])."""
+        """Logits after the prompts [B,T], or after one more token [B], of the users in `slots` (int32 [B]).  A slot that
+        is no user's, such as -1, marks an empty row of the batch: its logits mean nothing."""
         *states, seen = cache
-        users = slots.long()
-        at = None if tokens.dim() == 2 else seen[users]  # (a prompt begins at the first place)
-        seen[users] = tokens.shape[1] if at is None else at + 1
+        users = len(seen) - 1
+        live = (slots >= 0) & (slots < users)
+        place = torch.where(live, slots, users).long()
+        at = None if tokens.dim() == 2 else seen[place]  # (a prompt begins at the first place)
+        seen[place] = tokens.shape[1] if at is None else at + 1
         x, res = api.embedding_fwd(tokens.contiguous(), self.embed.weight), None
         for layer, S in zip(self.layers, states):
-            x, res = layer.serve(x, res, S, slots, self.table, at)
+            x, res = layer.serve(x, res, S, slots, place, self.table, at)
         return self.head(api.rms_norm_fwd(x, self.norm, res)[0])
 
 
