@@ -90,17 +90,29 @@ class Layer(torch.nn.Module):
 class Model(torch.nn.Module):
     def __init__(self, vocab=64, width=256, layers=2, heads=4, kv_heads=2, D=64, length=4096):
         super().__init__()
-        self.table = api.rotary_table(length, D // 2)  # stays in fp32, beside the model's parameters
+        self.length, self.turned, self.table = length, D // 2, None  # (the table stays in fp32, beside the parameters)
         self.embed = torch.nn.Embedding(vocab, width)
         self.layers = torch.nn.ModuleList(Layer(width, heads, kv_heads, D) for _ in range(layers))
         self.norm = torch.nn.Parameter(torch.ones(width))
         self.head = torch.nn.Linear(width, vocab, bias=False)
         torch.nn.init.normal_(self.embed.weight, std=0.5)
 
+    def places(self, n):
+        """The rotations of the places 0 .. n - 1: of `length` of them, until a longer sequence needs more."""
+        if self.table is None or len(self.table) < n or self.table.device != self.norm.device:
+            self.table = api.rotary_table(max(n, self.length), self.turned, device=self.norm.device)
+        return self.table
+
+    def places_of(self, at):
+        """The rotations of these places, a row each: a sequence goes on for as long as it likes."""
+        i = torch.arange(self.turned // 2, dtype=torch.float64, device=at.device)
+        angle = at.double()[:, None] * 10000.0 ** (-2 * i / self.turned)
+        return torch.cat([angle.cos(), angle.sin()], 1).float()
+
     def forward(self, tokens):
-        x, res = api.embedding(tokens, self.embed.weight), None
+        x, res, table = api.embedding(tokens, self.embed.weight), None, self.places(tokens.shape[1])
         for layer in self.layers:
-            x, res = layer(x, res, self.table)
+            x, res = layer(x, res, table)
         return self.head(api.rms_norm(x, self.norm, res)[0])
 
     def cache(self, users):
@@ -118,11 +130,15 @@ class Model(torch.nn.Module):
         users = len(seen) - 1
         live = (slots >= 0) & (slots < users)
         place = torch.where(live, slots, users).long()
-        at = None if tokens.dim() == 2 else seen[place]  # (a prompt begins at the first place)
-        seen[place] = tokens.shape[1] if at is None else at + 1
+        if tokens.dim() == 2:  # a prompt begins at the first place
+            table, at = self.places(tokens.shape[1]), None
+            seen[place] = tokens.shape[1]
+        else:
+            table, at = self.places_of(seen[place]), torch.arange(len(slots), dtype=torch.int32, device=slots.device)
+            seen[place] += 1
         x, res = api.embedding_fwd(tokens.contiguous(), self.embed.weight), None
         for layer, S in zip(self.layers, states):
-            x, res = layer.serve(x, res, S, slots, place, self.table, at)
+            x, res = layer.serve(x, res, S, slots, place, table, at)
         return self.head(api.rms_norm_fwd(x, self.norm, res)[0])
 
 

@@ -85,3 +85,16 @@ def test_empty_rows_leave_every_user_as_it_was(model):
         a = m.serve(torch.stack([text[2, 0], text[0, t], text[1, 0]]), padded, torch.tensor([-1, 1, 3], dtype=torch.int32))
         b = m.serve(torch.cat([text[1:, t], text[:1, 0]]), padded, torch.tensor([2, 0, -5], dtype=torch.int32))
         _same(a[1], want[0]), _same(b[:2], want[1:])
+
+
+def test_sequences_longer_than_the_model_was_made_for(model):
+    long, short = model(64), model(8)
+    short.load_state_dict(long.state_dict())
+    for layer in short.layers:
+        layer.freeze()
+    text, users = torch.randint(16, (2, 20), generator=torch.Generator().manual_seed(2)), torch.tensor([1, 0], dtype=torch.int32)
+    want = long.serve(text, long.cache(2), users)
+    _same(short.serve(text, short.cache(2), users), want)
+    cache = short.cache(2)
+    got = [short.serve(text[:, :5], cache, users)[:, -1]] + [short.serve(text[:, t], cache, users) for t in range(5, 20)]
+    _same(torch.stack(got, 1), want[:, 4:])
