@@ -958,8 +958,8 @@ class RMSNorm(torch.autograd.Function):
 
 
 def _dense_inner(t):
-    """t itself where its last dimension is contiguous, else a dense copy."""
-    return t if t.stride(-1) == 1 else t.contiguous()
+    """t itself where its last dimension is contiguous (or it is refused further on), else a dense copy."""
+    return t.contiguous() if isinstance(t, torch.Tensor) and t.dim() and t.stride(-1) != 1 else t
 
 
 def _zeros_like_rows(t):
@@ -1007,10 +1007,11 @@ class QKNorm(torch.autograd.Function):
 class Embedding(torch.autograd.Function):
     @staticmethod
     def forward(ctx, tokens, weight, scale=1.0):
-        tokens = tokens.contiguous()
+        tokens = tokens.contiguous() if isinstance(tokens, torch.Tensor) else tokens
+        out = embedding_fwd(tokens, weight, scale)
         ctx.save_for_backward(tokens)
         ctx.V, ctx.scale = weight.shape[0], scale
-        return embedding_fwd(tokens, weight, scale)
+        return out
 
     @staticmethod
     @once_differentiable

@@ -382,3 +382,13 @@ def test_calls_on_another_device_go_there(monkeypatch):
                               lambda: api.embedding_bwd(t, x, 5))):
         call()
         assert there[2 * i:] == [torch.device("cpu"), "back"] and len(calls.calls) == i + 1
+
+
+def test_differentiable_forms_refuse_what_is_no_tensor():
+    # as the plain forms do
+    x, w = torch.zeros(2, 4, 8), torch.zeros(4, 8)
+    for fn in (lambda: api.gated_scan(None, x), lambda: api.gated_scan([1.0], [2.0]), lambda: api.gated_scan(torch.zeros(()), x),
+               lambda: api.qk_norm(None, x), lambda: api.qk_norm(x[None], 3), lambda: api.qk_norm(torch.zeros(()), x),
+               lambda: api.embedding([1, 2], w), lambda: api.embedding(torch.zeros(2).long(), None)):
+        with pytest.raises((TypeError, ValueError), match="must"):
+            fn()
