@@ -392,3 +392,88 @@ def test_differentiable_forms_refuse_what_is_no_tensor():
                lambda: api.embedding([1, 2], w), lambda: api.embedding(torch.zeros(2).long(), None)):
         with pytest.raises((TypeError, ValueError), match="must"):
             fn()
+
+
+# ---------------------------------------------------------------- the short checks beside the full ones
+def _odd(*shape):  # rows of odd starts and distances
+    return torch.zeros(*shape[:-1], shape[-1] + 3)[..., 1:-2]
+
+
+def test_short_checks_make_the_same_call_as_the_full_ones(monkeypatch):
+    calls = _Calls(monkeypatch)
+    monkeypatch.setattr(api, "_elsewhere", lambda t: False)
+    x, h0, q = torch.zeros(2, 70, 2 * 8).split(8, -1), torch.zeros(2, 8), torch.zeros(3, 5, 6, 16).split([4, 2], 2)
+    carries, state, slots = torch.zeros(2, 2, 8), torch.zeros(4, 8), torch.zeros(2, dtype=torch.int32)
+    table, at, w = torch.zeros(9, 8), torch.zeros(1, 5, dtype=torch.int32).expand(3, 5), torch.zeros(16)
+    one, few = [t[:, 1] for t in q], torch.zeros(6, dtype=torch.int32)[::2]
+    made = [
+        lambda: api.gated_scan_fwd(*x, h0, False),
+        lambda: api.gated_scan_fwd(x[0], _odd(2, 70, 8), want_carries=True),
+        lambda: api.gated_scan_fwd(x[0].bfloat16(), x[1].bfloat16()[:, :1].expand(2, 70, 8)),
+        lambda: api.gated_scan_bwd(*x, carries, _odd(2, 70, 8), h0),
+        lambda: api.gated_scan_step(x[0][:, 3], _odd(2, 8), state, slots),
+        lambda: api.gated_scan_step(x[0][:, 3], x[1][:, 3], state, positive=False),
+        lambda: api.qk_norm_fwd(*q, w, None, table, at, eps=0.5, interleaved=True),
+        lambda: api.qk_norm_fwd(*q, None, w, table),
+        lambda: api.qk_norm_fwd(*q),
+        lambda: api.qk_norm_fwd(*one, w, w, table, few),
+        lambda: api.qk_norm_fwd(*one, table=table[:1]),
+        lambda: api.qk_norm_fwd(q[0], q[1][:, :, :0]),
+        lambda: api.qk_norm_bwd(*q, w, None, _odd(3, 5, 4, 16), q[0][:, :, :1].expand(3, 5, 2, 16), table),
+        lambda: api.qk_norm_bwd(*one, None, None, one[0], one[1], table, few),
+    ]
+
+    def shapes():
+        for fn in made:
+            fn()
+        return [args[0] for _, args in calls.calls[-len(made):]]
+
+    full = shapes()
+
+    def refused(*a, **k):
+        raise AssertionError("the full check ran")
+
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    for name in ("_qk_shape_checked", "_gated_step_check"):
+        monkeypatch.setattr(api, name, refused)
+    monkeypatch.setattr(api, "_inner", refused)
+    assert shapes() == full
+
+
+def test_short_checks_pass_on_what_the_full_ones_refuse(monkeypatch):
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True))
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+
+    class Card:
+        type, index = "cuda", 0
+    card = Card()
+    monkeypatch.setattr(torch.Tensor, "device", property(lambda t: card))
+    monkeypatch.setattr(api, "_elsewhere", lambda t: False)
+    x, q, one = torch.zeros(2, 4, 8), torch.zeros(2, 4, 2, 16), torch.zeros(2, 2, 16)
+    state, slots, table, w = torch.zeros(3, 8), torch.zeros(2, dtype=torch.int32), torch.zeros(9, 16), torch.zeros(16)
+    at = torch.zeros(2, 4, dtype=torch.int32)
+    for i, fn in enumerate((
+            lambda: api.gated_scan_fwd(x.half(), x.half()), lambda: api.gated_scan_fwd(x, x.bfloat16()),
+            lambda: api.gated_scan_fwd(x, x[:, :3]), lambda: api.gated_scan_fwd(x.transpose(1, 2), x.transpose(1, 2)),
+            lambda: api.gated_scan_fwd(x, x.transpose(0, 1).transpose(1, 2)), lambda: api.gated_scan_fwd(x[0], x[0]),
+            lambda: api.gated_scan_bwd(x, x, x[:, :1], x[:, :, :4]), lambda: api.gated_scan_bwd(x, x, x[:, :1], x.bfloat16()),
+            lambda: api.gated_scan_step(x, x, state), lambda: api.gated_scan_step(x[:, 0], x[:, 0], state[:1]),
+            lambda: api.gated_scan_step(x[:, 0], x[:, 0], state.double()), lambda: api.gated_scan_step(x[:, 0], x[:, 0], state[:, :4]),
+            lambda: api.gated_scan_step(x[:, 0], x[:, 0], torch.zeros(8, 3).T), lambda: api.gated_scan_step(x[:, 0], x[:, 0], state, slots.long()),
+            lambda: api.gated_scan_step(x[:, 0], x[:, 0], state, slots[:1]), lambda: api.gated_scan_step(x[:, 0], x[:, 0, :4], state),
+            lambda: api.gated_scan_step(x[:, 0], x[:, 0], state, torch.zeros(4, dtype=torch.int32)[::2]),
+            lambda: api.gated_scan_step(x[:, 0].half(), x[:, 0].half(), state),
+            lambda: api.qk_norm_fwd(q[..., :12], q[..., :12]), lambda: api.qk_norm_fwd(q, q[:, :3]), lambda: api.qk_norm_fwd(q, q[:1]),
+            lambda: api.qk_norm_fwd(q, one), lambda: api.qk_norm_fwd(q, q[..., :8]), lambda: api.qk_norm_fwd(q.bfloat16(), q),
+            lambda: api.qk_norm_fwd(q.half(), q.half()), lambda: api.qk_norm_fwd(q.transpose(2, 3), q.transpose(2, 3)),
+            lambda: api.qk_norm_fwd(q, q, w[:8]), lambda: api.qk_norm_fwd(q, q, None, w.bfloat16()),
+            lambda: api.qk_norm_fwd(q, q, torch.zeros(32)[::2]), lambda: api.qk_norm_fwd(q, q, table=torch.zeros(9, 24)),
+            lambda: api.qk_norm_fwd(q, q, table=torch.zeros(9, 12)), lambda: api.qk_norm_fwd(q, q, table=table[:3]),
+            lambda: api.qk_norm_fwd(q, q, table=table.double()), lambda: api.qk_norm_fwd(q, q, table=torch.zeros(16, 9).T),
+            lambda: api.qk_norm_fwd(one, one, table=table[:0]), lambda: api.qk_norm_fwd(q, q, positions=at),
+            lambda: api.qk_norm_fwd(q, q, table=table, positions=at.long()), lambda: api.qk_norm_fwd(q, q, table=table, positions=at[0]),
+            lambda: api.qk_norm_bwd(q, q, None, None, q[:, :2], q), lambda: api.qk_norm_bwd(q, q, None, None, q, q.bfloat16()),
+            lambda: api.qk_norm_bwd(q, q, None, None, q, q.transpose(2, 3)))):
+        with pytest.raises(ValueError):
+            fn()
+            raise AssertionError(f"call {i} went through")
