@@ -89,7 +89,6 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
     return r;
 }
 __device__ __forceinline__ f2 pair(float x) { return pair(x, x); }
-__device__ __forceinline__ f2 neg(f2 a) { return a * pair(-1.f); }
 
 // (h, l) += (a, b), both sums of two fp32
 __device__ __forceinline__ void add2(float &h, float &l, float a, float b) {
