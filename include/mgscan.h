@@ -486,8 +486,11 @@ typedef struct mgs_gated_shape {
  * stays as it is, whatever the value, and the gradients of both are zero; +infinity
  * starts the state anew from c.  An infinity or NaN reaches its own channel from its
  * step on (a gradient's: up to its step); an infinite state may go on as NaN.
- * Precision: fp32 outputs and gradients err by 1e-7 to 2e-7 (relative L2, gates to 5 in
- * magnitude), bf16 ones by their one rounding.
+ * Precision: fp32 outputs and gradients, h_T, the carries and d_h0 of bf16 calls among
+ * them, err by 4e-8 to 2e-7 (relative L2, gates that vary), bf16 ones by their one
+ * rounding.  What a gate's z and a are rounded by adds up where it stays the same: a by
+ * 2^-25 a step (up to T 2^-25 of a state that long remembered; 2e-5 measured for 3000 steps
+ * of -9.1), z in bf16 calls by |gate| 2^-24 of itself (3e-6 for 3000 steps of -5.7).
  * In: gate, value [B][T][D], h0 [B][D] fp32 (nullable).
  * Out: h [B][T][D]; h_T [B][D] fp32 (nullable), the state after the last step;
  *     carries [B][ceil(T / MGS_GATED_SPAN)][D] fp32 (nullable: only the backward

@@ -18,7 +18,11 @@
 //   3. the long runs' parts are joined, a block a run.
 // No atomics on the sums: the order is that of the tokens alone.  32768 tokens of a
 // text, 50000 x 2048 in bf16: forward 26 us, backward 71 (sort 19 beside the zeros, joins
-// 7; with the zeros in a kernel beside the sort alone 96).
+// 7; with the zeros in a kernel beside the sort alone 96).  Past that text the one cluster's
+// sort and every block's reading of all tokens grow with the text: 131072 tokens of 2048 206
+// us backward, 524288 734, of 256 columns 92 and 346; and one token more than 32768, past
+// what the sort keeps in registers, 75 in place of 72 (of 256 columns 46 and 41).  A token
+// that is all of a text is joined by one block for 128 columns: 524288 of 256 975 us.
 #include "mgs_cluster.cuh"
 #include "mgs_launch.h"
 #include "mgs_lm.h"
@@ -470,7 +474,8 @@ cudaError_t fwd_go(const void *tokens, const void *w, float scale, void *out, in
     return fwd_at<I, T, false, 8>(tokens, w, scale, out, N, V, D, s);
 }
 
-// Places a chunk: 32, and fewer where that would leave the GPU without work
+// Places a chunk: 32, and fewer where that would leave the GPU without work (by 512 columns a segment, bf16's;
+// the segments of fp32 and of rows that start anywhere are narrower, so that theirs are cut finer than they need)
 int chunk_of(int64_t N, int64_t D) {
     int c = 32;
     while (c > 4 && (N / c) * ((D + 511) / 512) < 4096) c /= 2;

@@ -12,14 +12,18 @@
 // shared memory while it works on this one's, keeps what it computes in registers,
 // exchanges its map with the other warps' and runs its steps again from its own
 // state: the inputs are read once.  With few channels a cluster of blocks takes
-// tiles in turn, their maps pushed into each other's shared memory.
+// tiles in turn, their maps pushed into each other's shared memory (mgs_rounds.h).
 // The backward rebuilds h within a tile from the state that the forward kept before
 // it (the carries), so that h is not read: five tensors pass, not six.
 //
-// Bound by instructions (28 a step and channel forward, 50 backward; MUFU and selects
-// take more than an issue slot each) before memory.  8 x 4096 x 2048 in bf16: forward 83
-// us (5.0 TB/s, with the carries), backward 146 (4.6); 16 x 4096 x 1024 in fp32: 127 (6.3)
-// and 230 (5.8); 1 x 16384 x 2048 in bf16, clusters of 16: 61 (3.3).
+// fp32 is bound by memory: 16 x 4096 x 1024 forward 127 us (6.3 TB/s), backward 226
+// (5.9).  bf16, with half the bytes and as much to compute, by latency at 16 warps an SM:
+// 8 x 4096 x 2048 forward 83 us (4.9, with the carries), backward 148 (4.5), in which 28
+// and about 50 instructions a step and channel fill two thirds of the issue slots; and by
+// the spread of the blocks, two on some SMs and one on others: 4096 steps take 49 and 87 us
+// with 152 blocks, 83 and 149 with 256, 84 and 151 (5.7 and 5.3 TB/s) with 304.  Few
+// channels are bound by the exchange: 1 x 16384 x 2048 in bf16, clusters of 16, 60 us (3.3),
+// in fp32, clusters of 8, 94 (4.3).
 #include <type_traits>
 
 #include "mgs_cluster.cuh"
@@ -409,7 +413,7 @@ __global__ void __launch_bounds__(kCheckWarps * 32)
 
 // Warps of a forward's block and steps of its tile.  The maps cost the less the longer a
 // warp's steps: 16 in bf16, by four warps in a cluster (more of them to a round; a prompt
-// of 16384 x 2048 takes 61 us, 64 with eight), by eight without (8 x 4096 x 2048: 83 us,
+// of 16384 x 2048 takes 60 us, 81 with eight), by eight without (8 x 4096 x 2048: 83 us,
 // 86 with four); 8 in fp32, where, with twice the bytes, more warps pay.
 template <typename T, bool CL>
 constexpr int kFwdWarps = sizeof(T) == 2 && CL ? 4 : 8;
@@ -678,13 +682,25 @@ Copy copy_of(const Args &g, int es) {
 
 // Blocks of a cluster.  Their exchange costs more the more they are, a lack of warps
 // too: none where the lanes alone keep the SMs busy (`enough` of them), else as many as
-// make up to `blocks`, as far as there are tiles.  2048 steps of 2048 channels in bf16, us:
-//   lanes            32    64    96   128   160   192   256
-//   forward, 1     24.2  24.3  24.5  24.5  42.3  43.1  43.7
-//            4     13.9  18.2  22.3  27.4  37.9  42.5  48.7
-//           16     10.5  20.3  28.8  37.8  49.0  57.6  74.5
-//   backward, 1    40.6  40.8  41.9  43.4  74.2  74.5  74.8
-//             4    17.0  25.9  40.8  51.5  64.0  75.1  88.7
+// make up to `blocks`, as far as there are tiles.  2048 steps, us:
+//   lanes                32    64    96   128   160   192   256
+//   bf16 forward, 1    24.3  24.2  24.6  24.6  42.9  43.3  43.9
+//                 4    13.4  17.5  21.6  26.5  36.7  41.5  47.3
+//                 8    10.8  15.5  23.5  29.0  36.7  42.2  54.2
+//                16    10.5  20.1  29.0  37.8  48.9  58.0  74.9
+//       backward, 1    41.5  41.6  42.7  43.7  75.6  75.8  76.2
+//                 4    16.8  25.7  40.6  51.2  63.9  75.1  88.4
+//                 8    16.2  30.4  44.6  58.6  71.8  82.4   107
+//   fp32 forward, 1    38.6  38.6  39.7  40.6  64.7  65.1  65.9
+//                 4    16.0  23.1  38.8  47.8  60.3  69.6  83.5
+//                 8    14.3  27.6  42.6  55.7  67.2  78.6   101
+//       backward, 1    55.4  56.4  57.0  58.3  98.7  99.7   115
+//                 4    21.0  43.9  65.1  86.1   107   128   167
+//                 8    35.0  63.5  89.0   114   140   165   220
+// The forward in bf16 has two bands, the others one, which misses the fastest form just
+// past a lane an SM (160 lanes: 75.6 in place of 63.9 backward in bf16, 64.7 in place of 60.3
+// forward in fp32), and backward in fp32 at about 32 lanes, where an SM holds one block of
+// a cluster and 256 blocks take two turns (35.0 in place of 21.0).
 int cluster_of(int64_t lanes, int64_t steps, int enough, int blocks) {
     int c = 1;
     if (lanes >= enough) return c;
